@@ -22,15 +22,19 @@ __all__ = ["Dims", "GdnError", "load", "gdn_replay_verify", "gdn_replay_accept",
            "STATUS_DRAIN", "FLAG_TEST_EXPIRE", "FAMILY_TCGEN05", "FAMILY_PERTOKEN", "DTYPE_BF16",
            "DTYPE_F32", "ReplayLayer", "ConvDims", "gdn_conv_verify", "gdn_conv_accept",
            "gdn_gated_rmsnorm_fp8", "ConvLayer", "CONV_ACT_NONE", "CONV_ACT_SILU",
-           "gdn_nonreplay_verify", "gdn_nonreplay_accept", "NonReplayLayer"]
+           "gdn_nonreplay_verify", "gdn_nonreplay_accept", "NonReplayLayer",
+           "PageDims", "AttnDims", "RopeDims", "PagedCache", "AttnLayer", "ROPE_HALF", "ROPE_PAIRS",
+           "STATUS_BAD_PAGE", "STATUS_BAD_POS", "STATUS_BAD_TREE", "STATUS_NO_PAGES"]
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
 STATUS_BAD_ACCEPT, STATUS_NO_ROOM, STATUS_BAD_LEN, STATUS_BAD_SLOT, STATUS_TIMEOUT = 1, 2, 4, 8, 16
 STATUS_DRAIN = 32
+STATUS_BAD_PAGE, STATUS_BAD_POS, STATUS_BAD_TREE, STATUS_NO_PAGES = 64, 128, 256, 512
 FLAG_TEST_EXPIRE = 1
 FAMILY_TCGEN05, FAMILY_PERTOKEN = 1, 2
 FAMILY_NAMES = {FAMILY_TCGEN05: "tcgen05", FAMILY_PERTOKEN: "per-token"}
 CONV_ACT_NONE, CONV_ACT_SILU = 0, 1
+ROPE_HALF, ROPE_PAIRS = 0, 1
 _TORCH_IN = {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32}
 
 
@@ -53,6 +57,36 @@ class ConvDims(ctypes.Structure):
 
     def __repr__(self):
         return "ConvDims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class PageDims(ctypes.Structure):
+    """Mirror of ``gdn_page_cache`` (include/gdnattn.h); the pointers are PagedCache's."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_slot", "max_pages", "n_page", "page", "n_layer", "Hkv", "d", "dtype")] + \
+               [(n, ctypes.c_void_p) for n in
+                ("k", "v", "block_table", "seq_len", "n_owned", "ref", "free_list", "free_count")]
+
+    def __repr__(self):
+        return "PageDims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_[:8]) + ")"
+
+
+class AttnDims(ctypes.Structure):
+    """Mirror of ``gdn_attn_dims``."""
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+    def __repr__(self):
+        return "AttnDims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class RopeDims(ctypes.Structure):
+    """Mirror of ``gdn_rope_dims``; the strides are taken from each call's tensors."""
+    _fields_ = [("rot", ctypes.c_int32), ("style", ctypes.c_int32), ("max_pos", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+    def __repr__(self):
+        return "RopeDims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
 class GdnError(RuntimeError):
@@ -89,6 +123,20 @@ def load(rebuild: bool = False) -> ctypes.CDLL:
         lib.gdn_gated_rmsnorm_fp8.argtypes = [I, I, P, P, I, P, ctypes.c_float, ctypes.c_float, P, P]
         lib.gdn_nonreplay_verify.argtypes = [D] + [P] * 11
         lib.gdn_nonreplay_accept.argtypes = [D] + [P] * 6
+        C, A, R = ctypes.POINTER(PageDims), ctypes.POINTER(AttnDims), ctypes.POINTER(RopeDims)
+        lib.gdn_attn_stage.argtypes = [C, I, A, R] + [P] * 12
+        lib.gdn_tree_build.argtypes = [C, A] + [P] * 7
+        lib.gdn_attn_verify.argtypes = [C, I, A] + [P] * 9
+        lib.gdn_attn_workspace.argtypes = [C, A]
+        lib.gdn_attn_workspace.restype = ctypes.c_int64
+        lib.gdn_attn_accept.argtypes = [C, I, I] + [P] * 6
+        lib.gdn_pages_reserve.argtypes = [C, I, P, I, P, P]
+        lib.gdn_pages_fork.argtypes = [C, I] + [P] * 5
+        lib.gdn_pages_copy.argtypes = [C, I] + [P] * 3
+        lib.gdn_pages_release.argtypes = [C, I] + [P] * 3
+        for f in (lib.gdn_attn_stage, lib.gdn_tree_build, lib.gdn_attn_verify, lib.gdn_attn_accept,
+                  lib.gdn_pages_reserve, lib.gdn_pages_fork, lib.gdn_pages_copy, lib.gdn_pages_release):
+            f.restype = ctypes.c_int
         for f in (lib.gdn_conv_verify, lib.gdn_conv_accept, lib.gdn_gated_rmsnorm_fp8,
                   lib.gdn_nonreplay_verify, lib.gdn_nonreplay_accept):
             f.restype = ctypes.c_int
@@ -390,3 +438,181 @@ def gdn_gated_rmsnorm_fp8(o, z, weight, eps: float, inv_scale: float, q, stream=
                                       _ptr(weight, torch.float32, "weight"), float(eps),
                                       float(inv_scale), _ptr(q, torch.uint8, "q"), _stream(stream))
     _check("gdn_gated_rmsnorm_fp8", rc)
+
+
+# ------------------------------------------ attention layers: paged cache and drafts
+def _raw_stream(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+def _in(t, dtype, n, name):
+    """Address of a dense device tensor of dtype that holds at least n elements."""
+    p = _ptr(t, dtype, name)
+    if t.numel() < n:
+        raise ValueError(f"{name}: needs at least {n} elements, got {t.numel()}")
+    return p
+
+
+def _opt(t, dtype, n, name):
+    return None if t is None else _in(t, dtype, n, name)
+
+
+class PagedCache:
+    """Keys and values of the attention layers in pages, and the pages' bookkeeping
+    (include/gdnattn.h).
+
+    ``init`` is a dict of tensors k, v, block_table, seq_len, n_owned, ref, free_list and
+    free_count with the header's layouts; they are moved to ``device`` once (a tensor that
+    is there already is used as it is).  Without ``init`` every page is free and k and v are
+    zeros.  The tensors are attributes; write into them, do not replace them.  ``status``
+    collects GDN_STATUS_* bits.  The methods enqueue the library calls.
+    """
+
+    _FIELDS = ("k", "v", "block_table", "seq_len", "n_owned", "ref", "free_list", "free_count")
+
+    def __init__(self, dims: PageDims, init: dict | None = None, device="cuda"):
+        t, n = _TORCH_IN.get(dims.dtype), dims
+        if t is None:
+            raise TypeError(f"dtype: expected DTYPE_BF16 or DTYPE_F32, got {dims.dtype}")
+        shape = {"k": (n.n_layer, n.n_page, n.Hkv, n.page, n.d), "block_table": (n.n_slot, n.max_pages),
+                 "seq_len": (n.n_slot,), "n_owned": (n.n_slot,), "ref": (n.n_page,), "free_list": (n.n_page,),
+                 "free_count": (1,)}
+        shape["v"] = shape["k"]
+        if init is None:
+            init = {f: torch.zeros(shape[f], dtype=t if f in "kv" else torch.int32, device=device)
+                    for f in self._FIELDS}
+            init["block_table"].fill_(-1)
+            init["free_list"].copy_(torch.arange(n.n_page - 1, -1, -1, dtype=torch.int32))
+            init["free_count"].fill_(n.n_page)
+        self._t = {}
+        self.d = PageDims(**{f: getattr(dims, f) for f, _ in PageDims._fields_[:8]})
+        for f in self._FIELDS:
+            x = init[f].to(device).contiguous()
+            if tuple(x.shape) != shape[f]:
+                raise ValueError(f"{f}: expected shape {shape[f]}, got {tuple(x.shape)}")
+            setattr(self.d, f, _ptr(x, t if f in "kv" else torch.int32, f) or None)
+            self._t[f] = x
+        self._c = ctypes.byref(self.d)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self._t["k"].device)
+        self._status = self.status.data_ptr()
+        self._lib = load()
+
+    def __getattr__(self, name):
+        if name in PagedCache._FIELDS:
+            return self._t[name]
+        raise AttributeError(name)
+
+    def reserve(self, slots, extra: int, stream=None):
+        """Room for ``extra`` tokens past seq_len in each of ``slots`` (int32)."""
+        n = slots.numel()
+        _check("gdn_pages_reserve", self._lib.gdn_pages_reserve(
+            self._c, n, _in(slots, torch.int32, n, "slots"), extra, self._status, _raw_stream(stream)))
+
+    def fork(self, src, dst, copies, stream=None):
+        """Sequences ``dst`` become copies of ``src`` (int32 slots): full pages shared, the
+        last page's rows copied in every layer.  ``copies`` int32 [n, 2] receives those pages."""
+        n, s = src.numel(), _raw_stream(stream)
+        c = _in(copies, torch.int32, 2 * n, "copies")
+        _check("gdn_pages_fork", self._lib.gdn_pages_fork(
+            self._c, n, _in(src, torch.int32, n, "src"), _in(dst, torch.int32, n, "dst"), c, self._status, s))
+        _check("gdn_pages_copy", self._lib.gdn_pages_copy(self._c, n, c, self._status, s))
+
+    def release(self, slots, stream=None):
+        """The pages of ``slots`` (int32) go back, as far as no other sequence holds them."""
+        n = slots.numel()
+        _check("gdn_pages_release", self._lib.gdn_pages_release(
+            self._c, n, _in(slots, torch.int32, n, "slots"), self._status, _raw_stream(stream)))
+
+    def accept(self, accepted, path=None, state_idx=None, new_len=None, stream=None):
+        """Commit accepted[b] drafted tokens of each sequence: along ``path`` (int32 [B, T]),
+        whose rows move to the front of the draft's in every layer, or, without one, the first
+        accepted[b].  The lengths go to ``new_len`` (seq_len when None)."""
+        i32, B = torch.int32, accepted.numel()
+        T = 64 if path is None else path.shape[-1]
+        _check("gdn_attn_accept", self._lib.gdn_attn_accept(
+            self._c, B, T, _opt(state_idx, i32, B, "state_idx"), _opt(path, i32, B * T, "path"),
+            _in(accepted, i32, B, "accepted"),
+            self.d.seq_len if new_len is None else _in(new_len, i32, self.d.n_slot, "new_len"),
+            self._status, _raw_stream(stream)))
+
+
+class AttnLayer:
+    """One attention layer over a PagedCache: the staging of a draft block and its verify.
+
+    ``rope``, ``q_weight``, ``k_weight`` (fp32 [d]) and ``cos_sin`` (fp32 [max_pos, rot]) serve
+    ``stage`` alone.  state_idx (int32 [B]) maps rows to slots; None is the identity.  The
+    workspace is allocated here unless one is passed (layers that run one after the other may
+    share one: ``other.workspace``); ``status`` is the cache's.
+    """
+
+    def __init__(self, dims: AttnDims, cache: PagedCache, layer: int, rope: RopeDims | None = None,
+                 q_weight=None, k_weight=None, cos_sin=None, state_idx=None, workspace=None):
+        c, f32 = cache.d, torch.float32
+        self.d, self.cache, self.layer, self.status = dims, cache, layer, cache.status
+        self.rope = rope
+        dev = cache.status.device
+        need = cache._lib.gdn_attn_workspace(cache._c, ctypes.byref(dims)) if dims.T <= 64 else 0
+        _check("gdn_attn_workspace", min(need, 0))
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.workspace, self.state_idx = workspace, state_idx
+        self._keep = (q_weight, k_weight, cos_sin)
+        self._ws = _in(workspace, torch.uint8, need, "workspace") or None
+        self._idx = _opt(state_idx, torch.int32, dims.B, "state_idx")
+        if rope is not None:
+            self._w = (_in(q_weight, f32, c.d, "q_weight"), _in(k_weight, f32, c.d, "k_weight"),
+                       _opt(cos_sin, f32, rope.max_pos * rope.rot, "cos_sin"))
+
+    def _block(self, t, heads, name):
+        """Address and token stride of q, k or v: [B, T, heads, d], dense within a token, the
+        tokens evenly spaced."""
+        d, c = self.d, self.cache.d
+        if t.dim() != 4 or t.shape != (d.B, d.T, heads, c.d):
+            raise ValueError(f"{name}: expected shape {(d.B, d.T, heads, c.d)}, got {tuple(t.shape)}")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        if t.dtype != _TORCH_IN[c.dtype]:
+            raise TypeError(f"{name}: expected {_TORCH_IN[c.dtype]}, got {t.dtype}")
+        sb, st, sh, se = t.stride()
+        if se != 1 or (heads > 1 and sh != c.d):
+            raise ValueError(f"{name}: the heads of a token must be dense")
+        if d.T == 1:
+            st = sb if d.B > 1 else max(heads * c.d, st)
+        elif d.B > 1 and sb != d.T * st:
+            raise ValueError(f"{name}: tokens must be evenly spaced over the batch")
+        return t.data_ptr(), st
+
+    def stage(self, q, k, v, q_out, pos=None, draft_len=None, stream=None):
+        """Norm and rotate q [B, T, Hq, d] into ``q_out`` and k [B, T, Hkv, d] into the cache's
+        draft rows, v beside it.  q, k and v may be views of one projection's output."""
+        d, c, i32 = self.d, self.cache.d, torch.int32
+        if self.rope is None:
+            raise ValueError("stage: this layer was made without rope and norm weights")
+        r = RopeDims.from_buffer_copy(self.rope)
+        pq, r.q_stride = self._block(q, d.Hq, "q")
+        pk, r.k_stride = self._block(k, c.Hkv, "k")
+        pv, r.v_stride = self._block(v, c.Hkv, "v")
+        n = d.B * d.T
+        _check("gdn_attn_stage", self.cache._lib.gdn_attn_stage(
+            self.cache._c, self.layer, ctypes.byref(d), ctypes.byref(r), self._idx,
+            _opt(draft_len, i32, d.B, "draft_len"), pq, pk, pv, _opt(pos, i32, n, "pos"), *self._w,
+            _in(q_out, _TORCH_IN[c.dtype], n * d.Hq * c.d, "q_out"), self.cache._status, _raw_stream(stream)))
+
+    def build_tree(self, parent, tree, pos=None, draft_len=None, stream=None):
+        """Ancestor words ``tree`` (int64 [B, T]) and rotation positions ``pos`` (int32 [B, T])
+        of a token tree given by its parents (int32 [B, T])."""
+        d, i32, n = self.d, torch.int32, self.d.B * self.d.T
+        _check("gdn_tree_build", self.cache._lib.gdn_tree_build(
+            self.cache._c, ctypes.byref(d), self._idx, _opt(draft_len, i32, d.B, "draft_len"),
+            _in(parent, i32, n, "parent"), _in(tree, torch.int64, n, "tree"), _opt(pos, i32, n, "pos"),
+            self.cache._status, _raw_stream(stream)))
+
+    def verify(self, q, out, lse=None, tree=None, draft_len=None, stream=None):
+        """Attention of the block's rows q [B, T, Hq, d] over the cache into ``out`` (and
+        ``lse`` fp32 [B, T, Hq]); ``tree`` int64 [B, T] ancestor words, None: a chain."""
+        d, c = self.d, self.cache.d
+        n, t = d.B * d.T, _TORCH_IN[c.dtype]
+        _check("gdn_attn_verify", self.cache._lib.gdn_attn_verify(
+            self.cache._c, self.layer, ctypes.byref(d), self._idx, _opt(draft_len, torch.int32, d.B, "draft_len"),
+            _in(q, t, n * d.Hq * c.d, "q"), _opt(tree, torch.int64, n, "tree"), _in(out, t, n * d.Hq * c.d, "out"),
+            _opt(lse, torch.float32, n * d.Hq, "lse"), self._ws, self.cache._status, _raw_stream(stream)))
