@@ -14,7 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f)
            for f in ("gdn_replay.cu", "gdn_replay_tc.cu", "gdn_layer_ops.cu", "gdn_nonreplay.cu",
-                     "gdn_attn.cu", "gdn_pages.cu")]
+                     "gdn_attn.cu", "gdn_attn_tc.cu", "gdn_pages.cu")]
 HEADERS = [os.path.join(ROOT, "include", "gdnreplay.h"), os.path.join(ROOT, "include", "gdnlayer.h"),
            os.path.join(ROOT, "include", "gdnnonreplay.h"), os.path.join(ROOT, "include", "gdnattn.h"),
            os.path.join(PKG, "csrc", "replay_common.h"), os.path.join(PKG, "csrc", "tc_common.cuh"),

@@ -97,4 +97,8 @@ inline size_t layer_elems(const gdn_page_cache *c) {
     return static_cast<size_t>(c->n_page) * c->Hkv * c->page * c->d;
 }
 
+// The bf16 verify (gdn_attn_tc.cu).
+int64_t attn_tc_workspace(const gdn_page_cache *c, const gdn_attn_dims *d);
+int attn_tc_verify(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a, cudaStream_t s);
+
 }  // namespace gdn

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(128) tree_kernel(const SeqArgs s, const int32_
     }
 }
 
-// ---------------------------------------------------- verify on CUDA cores
+// ------------------------------------------- verify on CUDA cores (fp32 caches)
 constexpr int kRT = 32, kKT = 32;               // rows and keys of a tile
 constexpr int kCoreThreads = 128;
 
@@ -236,13 +236,6 @@ template <int D> struct CorePlan {
     static constexpr int STR = D + 4;           // padded row: lanes of a warp read 8 rows without conflicts
     static constexpr int BYTES = (kRT * STR + kKT * STR + kKT * D + kRT * (kKT + 4)) * 4;
 };
-
-template <typename T> __device__ __forceinline__ float to_f32(T x);
-template <> __device__ __forceinline__ float to_f32<float>(float x) { return x; }
-template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T> __device__ __forceinline__ T from_f32(float x);
-template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // Partial results in the workspace: [unit][split][kRT] rows of D sums, the maximum (in
 // powers of two) and the denominator; unit = (b Hkv + h) row tiles + row tile.
@@ -252,7 +245,7 @@ template <int D> __host__ __device__ constexpr int part_floats() { return D + 2;
 // scores (2 rows x 4 keys a lane), their running maximum and denominator, and their
 // D output columns (D / 32 a lane), so the only barriers are those around the shared
 // key and value tiles.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kCoreThreads) verify_core_kernel(const AttnArgs a, int row_tiles)
 {
     using P = CorePlan<D>;
@@ -276,7 +269,7 @@ __global__ void __launch_bounds__(kCoreThreads) verify_core_kernel(const AttnArg
         float x = 0.f;
         if (r < rows && r / a.G < sq.n) {
             const size_t at = ((static_cast<size_t>(b) * a.s.T + r / a.G) * a.Hq + h * a.G + r % a.G) * D + col;
-            x = to_f32<T>(static_cast<const T *>(a.q)[at]) * a.scale_log2;
+            x = static_cast<const float *>(a.q)[at] * a.scale_log2;
         }
         sQ[(i / D) * P::STR + col] = x;
     }
@@ -308,8 +301,8 @@ __global__ void __launch_bounds__(kCoreThreads) verify_core_kernel(const AttnArg
                 const int id = a.s.table[static_cast<size_t>(sq.slot) * a.s.max_pages + (at >> a.s.page_shift)];
                 if (id >= 0 && id < a.s.n_page) {
                     const size_t row = ((static_cast<size_t>(id) * a.s.Hkv + h) << a.s.page_shift) + (at & (page - 1));
-                    Vec8<T>::unpack(Vec8<T>::load(static_cast<const T *>(a.k) + row * D + c8 * 8), fk);
-                    Vec8<T>::unpack(Vec8<T>::load(static_cast<const T *>(a.v) + row * D + c8 * 8), fv);
+                    Vec8<float>::unpack(Vec8<float>::load(static_cast<const float *>(a.k) + row * D + c8 * 8), fk);
+                    Vec8<float>::unpack(Vec8<float>::load(static_cast<const float *>(a.v) + row * D + c8 * 8), fv);
                 } else if (c8 == 0) {
                     atomicOr(a.s.status, GDN_STATUS_BAD_PAGE);
                 }
@@ -412,7 +405,7 @@ __global__ void __launch_bounds__(kCoreThreads) verify_core_kernel(const AttnArg
             const size_t orow = (static_cast<size_t>(b) * a.s.T + row / a.G) * a.Hq + h * a.G + row % a.G;
             const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
 #pragma unroll
-            for (int i = 0; i < C; ++i) static_cast<T *>(a.out)[orow * D + lane + 32 * i] = from_f32<T>(acc[r][i] * inv);
+            for (int i = 0; i < C; ++i) static_cast<float *>(a.out)[orow * D + lane + 32 * i] = acc[r][i] * inv;
             if (a.lse && lane == 0) a.lse[orow] = (mm + log2f(ll)) * 0.69314718055994531f;
         }
     }
@@ -420,7 +413,7 @@ __global__ void __launch_bounds__(kCoreThreads) verify_core_kernel(const AttnArg
 
 // Joins the splits' partial results of a row (a warp): their common maximum, then the
 // weighted sums in the order of the splits.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) verify_join_kernel(const AttnArgs a, int row_tiles)
 {
     const int rows = a.s.T * a.G, lane = threadIdx.x & 31;
@@ -449,7 +442,7 @@ __global__ void __launch_bounds__(128) verify_join_kernel(const AttnArgs a, int 
     const size_t orow = (static_cast<size_t>(b) * a.s.T + row / a.G) * a.Hq + h * a.G + row % a.G;
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) static_cast<T *>(a.out)[orow * D + lane + 32 * i] = from_f32<T>(acc[i] * inv);
+    for (int i = 0; i < C; ++i) static_cast<float *>(a.out)[orow * D + lane + 32 * i] = acc[i] * inv;
     if (a.lse && lane == 0) a.lse[orow] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
@@ -473,17 +466,17 @@ int core_splits(const gdn_page_cache *c, const gdn_attn_dims *d) {
     return static_cast<int>(want < 1 ? 1 : want > 128 ? 128 : want);
 }
 
-template <typename T, int D>
+template <int D>
 int launch_core(const gdn_page_cache *c, const gdn_attn_dims *d, AttnArgs a, cudaStream_t s) {
     const int rts = core_row_tiles(c, d);
     a.splits = core_splits(c, d);
-    if (cudaFuncSetAttribute(verify_core_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(verify_core_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              CorePlan<D>::BYTES) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    if (launch_pdl(verify_core_kernel<T, D>, dim3(rts * a.splits, c->Hkv, d->B), dim3(kCoreThreads),
+    if (launch_pdl(verify_core_kernel<D>, dim3(rts * a.splits, c->Hkv, d->B), dim3(kCoreThreads),
                    CorePlan<D>::BYTES, s, a, rts) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    if (a.splits > 1 && launch_pdl(verify_join_kernel<T, D>, dim3((d->T * a.G + 3) / 4, c->Hkv, d->B), dim3(128), 0, s,
+    if (a.splits > 1 && launch_pdl(verify_join_kernel<D>, dim3((d->T * a.G + 3) / 4, c->Hkv, d->B), dim3(128), 0, s,
                                    a, rts) != cudaSuccess)
         return GDN_ERR_LAUNCH;
     return GDN_OK;
@@ -636,6 +629,7 @@ int gdn_tree_build(const gdn_page_cache *c, const gdn_attn_dims *d, const int32_
 int64_t gdn_attn_workspace(const gdn_page_cache *c, const gdn_attn_dims *d)
 {
     if (const int rc = check_attn(c, d, 64)) return rc;
+    if (c->dtype == GDN_DTYPE_BF16) return attn_tc_workspace(c, d);
     const int splits = core_splits(c, d);
     if (splits == 1) return 0;
     return static_cast<int64_t>(d->B) * c->Hkv * core_row_tiles(c, d) * splits * kRT * (c->d + 2) * 4;
@@ -658,13 +652,9 @@ int gdn_attn_verify(const gdn_page_cache *c, int32_t layer, const gdn_attn_dims 
     AttnArgs a{seq_args(c, d->B, d->T, state_idx, draft_len, status), q, static_cast<const char *>(c->k) + off,
                static_cast<const char *>(c->v) + off, tree, out, lse, static_cast<float *>(workspace),
                d->scale * 1.4426950408889634f, d->Hq, d->Hq / c->Hkv, 1, d->flags};
-    if (c->dtype == GDN_DTYPE_BF16)
-        return c->d == 64 ? launch_core<__nv_bfloat16, 64>(c, d, a, stream)
-               : c->d == 128 ? launch_core<__nv_bfloat16, 128>(c, d, a, stream)
-                             : launch_core<__nv_bfloat16, 256>(c, d, a, stream);
-    return c->d == 64 ? launch_core<float, 64>(c, d, a, stream)
-           : c->d == 128 ? launch_core<float, 128>(c, d, a, stream)
-                         : launch_core<float, 256>(c, d, a, stream);
+    if (c->dtype == GDN_DTYPE_BF16) return attn_tc_verify(c, d, a, stream);
+    return c->d == 64 ? launch_core<64>(c, d, a, stream)
+           : c->d == 128 ? launch_core<128>(c, d, a, stream) : launch_core<256>(c, d, a, stream);
 }
 
 int gdn_attn_accept(const gdn_page_cache *c, int32_t B, int32_t T, const int32_t *state_idx, const int32_t *path,

@@ -123,8 +123,8 @@ def verify_bounds(A, S, lse, keys, d, bf16):
     """Absolute bounds on the errors of out and lse.  A score is a sum of d exact products
     (bf16) or d fused multiply-adds (fp32) in fp32, scaled and exponentiated with relative
     error 2^-22: |ds| <= (d + 8) 2^-24 S.  The sums over the keys add keys 2^-24.  With bf16
-    inputs the weights are rounded to bf16 (2^-9) before the second product and the output
-    once (2^-9)."""
+    inputs the output is rounded once, a relative 2^-8, which the second product's roundings
+    (2^-16) hardly add to."""
     es = (d + 8) * 2.0 ** -24 * S
     rel = 2 * es + (keys + 16) * 2.0 ** -23
     if bf16:

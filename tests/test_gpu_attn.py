@@ -265,6 +265,21 @@ def test_verify_faults_skip_the_sequence(dtype):
     r.check(skip=(0, 1, 2, 3, 4), status=lib.STATUS_BAD_SLOT | lib.STATUS_BAD_LEN | lib.STATUS_NO_ROOM | lib.STATUS_BAD_PAGE)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_verify_wait_expiry(d):
+    """The tensor-core kernel's wait-expiry exit (taken at the first wait, with nothing in
+    flight): the status word tells, the device stays usable, the next call is right."""
+    lib = _lib()
+    r = VerifyRun([100, 700], [4, 4], 4, 8, 2, d, 16, BF, seed=25)
+    r.attn.d.flags = lib.FLAG_TEST_EXPIRE
+    r.call()
+    assert int(r.cache.status.item()) == lib.STATUS_TIMEOUT
+    r.attn.d.flags = 0
+    r.cache.status.zero_()
+    r.call()
+    r.check()
+
+
 # ------------------------------------------------------------------------ stage
 STAGE = [
     # lens, drafts, T, Hq, Hkv, d, page, rot, pairs, packed
