@@ -34,7 +34,7 @@ __device__ __forceinline__ Seq load_seq(const SeqArgs &s, int b) {
         return q;
     }
     q.len = s.seq_len[q.slot];
-    const int room = s.max_pages << s.page_shift;                 // <= 2^25
+    const int room = s.max_pages << s.page_shift;                 // <= 2^24
     if (q.len < 0 || q.len > room || q.n < 0 || q.n > s.T) q.bad = GDN_STATUS_BAD_LEN;
     else if (q.len + q.n > room) q.bad = GDN_STATUS_NO_ROOM;
     return q;
@@ -71,10 +71,11 @@ inline int elem_size(int dtype) { return dtype == GDN_DTYPE_BF16 ? 2 : 4; }
 inline int check_cache(const gdn_page_cache *c) {
     if (!c) return GDN_ERR_NULL;
     if (c->dtype != GDN_DTYPE_BF16 && c->dtype != GDN_DTYPE_F32) return GDN_ERR_DTYPE;
-    if (c->n_slot < 0 || c->max_pages < 1 || c->n_page < 1 || c->n_layer < 1 || c->Hkv < 1 || c->Hkv > 256)
+    if (c->n_slot < 0 || c->max_pages < 1 || c->n_page < 1 || c->n_layer < 1 || c->Hkv < 1 || c->Hkv > 128)
         return GDN_ERR_DIMS;
     if (page_shift(c->page) < 0 || (c->d != 64 && c->d != 128 && c->d != 256)) return GDN_ERR_DIMS;
-    if (c->max_pages > 1 << 18) return GDN_ERR_DIMS;              // 2^25 tokens; sums over 4096 rows fit 32 bits
+    if (c->max_pages > 1 << 18 || static_cast<long long>(c->max_pages) * c->page > 1 << 24)
+        return GDN_ERR_DIMS;                                      // sums over 4096 rows fit 32 bits
     if (static_cast<long long>(c->n_page) * c->Hkv * c->page > 0x7fffffffLL) return GDN_ERR_DIMS;
     return GDN_OK;
 }

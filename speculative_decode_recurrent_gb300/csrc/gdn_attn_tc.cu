@@ -13,16 +13,18 @@
 // What bounds it: the keys and values are read once for all T x (Hq / Hkv) rows of a key head,
 // so up to about 128 rows the kernel is bound by HBM; above, by the softmax and the MMAs.
 //
-// Work.  A unit is (sequence, key head, tile of 128 rows); its keys come in tiles of 64.  All
-// units' tiles in a row are cut into equal shares, one per resident CTA, so ragged lengths
+// Work.  A unit is (sequence, key head, tile of 128 rows or pair of such tiles); its keys come in
+// tiles of 64.  All units' tiles in a row are cut into equal shares, one per SM, so ragged lengths
 // balance and one long sequence fills the GPU.  A unit that one CTA covers is finished there; the
 // others leave partial results (o, m, l) that a second kernel joins in a fixed order.
 //
-// A CTA: warp 4 loads (TMA, one copy per page and 64-column atom, through the block table), warp
-// 5 issues the MMAs, warps 0-3 own a row per thread: S = Q K^T (M 128, N 64) in two TMEM buffers;
-// the weights' two terms go back over S and are the A operands of O += P V straight from TMEM, with
-// the value rows read MN-major as they lie.  S of the next tile is formed while the softmax of the
-// present one runs.
+// A CTA.  Two warps load (TMA, one copy per page and 64-column atom, through the block table) into a
+// ring of four tiles of keys and values.  Two groups of 256 threads with an MMA warp
+// each work side by side: on a pair of row tiles, both on every tile of keys; on a single one, on
+// every second tile, their results joined at the end (d = 256 has TMEM for one group).  A
+// group forms S = Q K^T (M 128, N 64) in two TMEM buffers; its threads, two per row, each take
+// half of the tile's keys; the weights' two terms go back over S and are the A operands of
+// O += P V straight from TMEM, with the value rows read MN-major as they lie.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -36,31 +38,41 @@ namespace {
 using namespace tc;
 
 constexpr int kKeys = 64, kRows = 128;              // tile of keys, tile of rows
-constexpr int kTcThreads = 192;
-constexpr int kMaxSeqs = 512;                       // sequences of one launch (their table in shared memory)
+constexpr uint32_t kIdleLimit = 1u << 24;           // polls of an MMA warp without work before giving up
+constexpr int kGroupThreads = 256;                  // two per row
+constexpr int kMaxSeqs = 512;                       // most sequences of one launch (their table in shared memory)
 constexpr uint32_t kIdescMnMajorB = 1u << 16;
 
-template <int D> struct TcPlan {
+// D: head dim; NQ: most row tiles of a unit.
+template <int D, int NQ> struct TcPlan {
+    static constexpr int NG = D == 256 ? 1 : 2;                 // groups
     static constexpr int ATOMS = D / 64;                        // 128-byte column atoms of a row
     static constexpr int STAGE = kKeys * D * 2;                 // a tile of keys or of values
-    static constexpr int NST = D == 64 ? 8 : 4;
-    static constexpr int OFF_RING = kRows * D * 2;              // after the queries
-    static constexpr int OFF_SEQ = OFF_RING + NST * STAGE;      // prefix (int64), slot, len, n
-    static constexpr int OFF_BAR = OFF_SEQ + (kMaxSeqs + 1) * 8 + kMaxSeqs * 12 + 8;
-    static constexpr int BYTES = OFF_BAR + 320;
-    static constexpr int CTAS = D == 256 ? 1 : 2;               // per SM
-    static constexpr int COL_O = 2 * kKeys;                     // TMEM: S in [0, 64) and [64, 128), then O
-    static constexpr int TMEM_COLS = D == 256 ? 512 : 256;
-    static_assert(OFF_BAR % 8 == 0, "mbarriers");
-    static_assert(CTAS * (BYTES + 1024) <= 228 * 1024 && BYTES <= 227 * 1024, "shared memory");
+    static constexpr int NST = D == 64 ? 16 : D == 256 ? 4 : 8;
+    static constexpr int ROWS = NG * kGroupThreads;             // row threads
+    static constexpr int LOAD_WARP = ROWS / 32, MMA_WARP = LOAD_WARP + 2;      // two and NG warps
+    static constexpr int THREADS = ROWS + 32 * (2 + NG);
+    static constexpr int QTILE = kRows * D * 2;
+    static constexpr int OFF_RING = NQ * QTILE;                 // after the queries
+    static constexpr int OFF_SEQ = OFF_RING + NST * STAGE;      // prefix, slot, len, n
+    static constexpr int OFF_XCH = OFF_SEQ + (4 * kMaxSeqs + 4) * 4;                      // two words per row thread
+    static constexpr int OFF_BAR = OFF_XCH + ROWS * 8;
+    static constexpr int BYTES = OFF_BAR + 640;
+    static constexpr int TCOLS = 2 * kKeys + D;                 // TMEM of a group: S in [0, 64) and [64, 128), then O
+    static constexpr int TMEM_COLS = 512;
+    static_assert(NG * TCOLS <= TMEM_COLS && NQ <= NG, "tensor memory");
+    // Where the groups take every second tile, a stage always serves the same group (the one of
+    // its tile's parity): a group that had not seen a stage's last round could take its phase for the next.
+    static_assert(NST % 4 == 0, "stages of a tile alternate between the groups");
+    static_assert(OFF_BAR % 16 == 0 && BYTES <= 227 * 1024, "shared memory");
 };
 
 struct TcArgs {
     AttnArgs a;
     int b0, nb;                 // sequences [b0, b0 + nb) of the call
-    int row_tiles, rp;          // row tiles of a unit; rows of a partial result (a multiple of 32)
-    int2 *desc;                 // per unit: first CTA and number of CTAs
-    float *part;                // [2 grid][D + 2][rp]
+    int row_tiles, rp;          // row tiles of a key head; rows of a partial result (a multiple of 32)
+    int2 *desc;                 // per row tile: 2 (first CTA) + its place in the unit, and the last CTA
+    float *part;                // [2 CTAs][NQ][D + 2][rp]
 };
 
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -68,6 +80,15 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, 
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};"
+        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(taddr)
         : "memory");
 }
 // 32 consecutive columns of this thread's TMEM lane; the caller waits.
@@ -94,8 +115,34 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// True in one lane of a converged warp (the same one each time: commits track the issuing thread's MMAs).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(saddr(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
+}
+// Named barriers of the row threads: of all of them (id 1), of a group (2, 3), and of the 64 threads
+// of a group's TMEM lane quarter (4 ..).  No row warp leaves its loops early (an expired wait only
+// stops the waiting), so they always complete.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"(id), "r"(static_cast<uint32_t>(x)) : "memory");
+    return any != 0;
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -120,83 +167,115 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // ------------------------------------------------------------- the work's layout
-// Tiles of one (sequence, key head): the row tiles that hold rows in use take every tile of
-// keys, the others one tile without keys (their rows get zeros).
+// Units of one (sequence, key head): the row tiles that hold rows in use, in pairs where NQ is 2
+// (`pairs`, then `single`), take every tile of keys; each of the others is one tile without keys (its
+// rows get zeros).  Work is counted in row tiles times tiles of keys: a pair's tile counts 2.
 struct Shape {
-    int live, dead, tiles, total;                   // total: keys
-    __device__ Shape(int len, int n, int G, int row_tiles) {
+    int live, dead, pairs, single, tiles, total;    // total: keys
+    __device__ Shape(int len, int n, int G, int row_tiles, int nq) {
         live = (n * G + kRows - 1) / kRows;
         dead = row_tiles - live;
+        pairs = nq == 2 ? live / 2 : 0;
+        single = live - 2 * pairs;
         total = len + n;
         tiles = (total + kKeys - 1) / kKeys;        // >= 1 when live > 0
     }
-    __device__ long long per_head() const { return static_cast<long long>(live) * tiles + dead; }
+    __device__ int per_head() const { return live * tiles + dead; }
 };
 
 struct SeqTable {
-    long long *prefix;                              // [nb + 1] tiles before each sequence
+    int *prefix;                                    // [nb + 1] work before each sequence
     int *slot, *len, *n;                            // [nb]
+    int nb;
+    // The last sequence that starts at or before w, among those with work.
+    __device__ int find(int w) const {
+        int lo = 0, hi = nb - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= w) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
 };
 
 struct Segment {
-    int b, h, rt;                                   // sequence (within the launch), key head, row tile
+    int b, h, rt, nq;                               // sequence (within the launch), key head, first row tile, row tiles
     int slot, len, n, total;                        // total 0: a row tile without rows in use
     int first, count, tiles;                        // tiles [first, first + count) of the unit's `tiles`
-    long long unit_w;                               // the unit's first tile in the launch's order
+    int unit_w;                                     // the unit's place in the launch's work
+};
+
+// The unit that holds work item w, and the tile of it.
+__device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int G, int row_tiles, int nq, Segment &s) {
+    const Shape sh(st.len[b], st.n[b], G, row_tiles, nq);
+    const int in_b = w - st.prefix[b], per = sh.per_head(), tiles = sh.tiles;
+    s.b = b;
+    s.slot = st.slot[b];
+    s.len = st.len[b];
+    s.n = st.n[b];
+    s.h = in_b / per;
+    const int r = in_b - s.h * per, paired = 2 * sh.pairs * tiles, live = sh.live * tiles;
+    int start;
+    s.nq = 1;
+    s.tiles = sh.tiles;
+    s.total = sh.total;
+    if (r < paired) {
+        const int u = sh.pairs == 1 ? 0 : r / (2 * tiles);
+        s.nq = 2;
+        s.rt = 2 * u;
+        start = u * 2 * tiles;
+        s.first = (r - start) / 2;
+    } else if (r < live) {
+        const int u = sh.single == 1 ? 0 : (r - paired) / tiles;
+        s.rt = 2 * sh.pairs + u;
+        start = paired + u * tiles;
+        s.first = r - start;
+    } else {
+        s.rt = sh.live + r - live;
+        start = r;
+        s.first = 0;
+        s.tiles = 1;
+        s.total = 0;
+    }
+    s.unit_w = st.prefix[b] + s.h * per + start;
+}
+
+// W work items cut into N shares: share c starts at c W / N, at a pair's tile rounded down to its
+// first item.
+struct Cut {
+    int W, N, q, r;                                 // W = q N + r
+    __device__ int start(const SeqTable &st, int c, int G, int row_tiles, int nq) const {
+        int w = q * c + r * c / N;                  // r c < N^2
+        if (nq == 2 && c > 0 && c < N) {
+            Segment s;
+            locate(st, st.find(w), w, G, row_tiles, nq, s);
+            w = s.unit_w + s.first * s.nq;
+        }
+        return w;
+    }
 };
 
 // Walks a CTA's share [w, w1) unit by unit.
 struct Cursor {
-    long long w, w1;
-    int b;
-    __device__ bool next(const SeqTable &st, int G, int row_tiles, Segment &s) {
+    int w, w1, b;
+    __device__ bool next(const SeqTable &st, int G, int row_tiles, int nq, Segment &s) {
         if (w >= w1) return false;
         while (st.prefix[b + 1] <= w) ++b;
-        const Shape sh(st.len[b], st.n[b], G, row_tiles);
-        const long long in_b = w - st.prefix[b], per = sh.per_head();
-        s.b = b;
-        s.slot = st.slot[b];
-        s.len = st.len[b];
-        s.n = st.n[b];
-        s.h = static_cast<int>(in_b / per);
-        const long long r = in_b - s.h * per, live_tiles = static_cast<long long>(sh.live) * sh.tiles;
-        if (r < live_tiles) {
-            s.rt = static_cast<int>(r / sh.tiles);
-            s.first = static_cast<int>(r - static_cast<long long>(s.rt) * sh.tiles);
-            s.tiles = sh.tiles;
-            s.total = sh.total;
-        } else {
-            s.rt = sh.live + static_cast<int>(r - live_tiles);
-            s.first = 0;
-            s.tiles = 1;
-            s.total = 0;
-        }
-        s.unit_w = w - s.first;
-        const long long left = w1 - w;
-        s.count = left < s.tiles - s.first ? static_cast<int>(left) : s.tiles - s.first;
-        w += s.count;
+        locate(st, b, w, G, row_tiles, nq, s);
+        s.count = min((w1 - w) >> (s.nq - 1), s.tiles - s.first);
+        w += s.count * s.nq;
         return true;
     }
 };
 
-// Share c of W tiles cut into N: [c W / N, (c + 1) W / N).
-__device__ __forceinline__ long long share(long long W, int N, int c) { return W / N * c + W % N * c / N; }
-__device__ __forceinline__ int owner(long long W, int N, long long w) {
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (share(W, N, mid) <= w) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
 // ------------------------------------------------------------------ the kernel
-template <int D>
-__global__ void __launch_bounds__(kTcThreads, TcPlan<D>::CTAS)
+template <int D, int NQ>
+__global__ void __launch_bounds__(TcPlan<D, NQ>::THREADS, 1)
 verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TcArgs ta)
 {
-    using P = TcPlan<D>;
+    using P = TcPlan<D, NQ>;
+    constexpr int NG = P::NG;
     const AttnArgs &a = ta.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -206,86 +285,89 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     uint8_t *sQ = smem_raw, *ring = smem_raw + P::OFF_RING;
     SeqTable st;
-    st.prefix = reinterpret_cast<long long *>(smem_raw + P::OFF_SEQ);
-    st.slot = reinterpret_cast<int *>(st.prefix + kMaxSeqs + 1);
+    st.prefix = reinterpret_cast<int *>(smem_raw + P::OFF_SEQ);
+    st.slot = st.prefix + kMaxSeqs + 4;
     st.len = st.slot + kMaxSeqs;
     st.n = st.len + kMaxSeqs;
+    st.nb = ta.nb;
+    float *xch = reinterpret_cast<float *>(smem_raw + P::OFF_XCH);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem_raw + P::OFF_BAR);
-    uint64_t *full = bar, *empty = bar + P::NST, *s_full = bar + 2 * P::NST, *p_full = s_full + 2;
-    uint64_t *o_done = p_full + 2, *q_full = o_done + 1, *rows_bar = q_full + 1, *drain = rows_bar + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *full = bar, *empty = bar + P::NST, *q_full = bar + 2 * P::NST;
+    uint64_t *s_full = q_full + 1, *p_full = s_full + 2 * NG, *o_done = p_full + 2 * NG, *drain = o_done + 2 * NG;   // [group][2]; drain [group]
+    unsigned long long *odd = reinterpret_cast<unsigned long long *>(drain + NG);         // [group][2]
+    int *warp_sum = reinterpret_cast<int *>(odd + 2 * NG);                                // [warps]
+    Cut *cut = reinterpret_cast<Cut *>(warp_sum + P::THREADS / 32);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cut + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    unsigned long long *odd = reinterpret_cast<unsigned long long *>(tmem_slot + 2);      // [2]
-    long long *warp_sum = reinterpret_cast<long long *>(odd + 2);                         // [6]
-    static_assert((2 * P::NST + 8) * 8 + 8 + 16 + 48 <= 320, "barrier area");
+    static_assert((2 * P::NST + 1 + 9 * NG + P::THREADS / 32) * 8 + sizeof(Cut) + 8 <= 640, "barrier area");
 
     if (tid == 0) {
-#pragma unroll
         for (int i = 0; i < P::NST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], NG);               // a commit of each group, or two of the only one that reads it
         }
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
-        mbar_init(&p_full[0], 128);
-        mbar_init(&p_full[1], 128);
-        mbar_init(o_done, 1);
-        mbar_init(q_full, 128);
-        mbar_init(rows_bar, 128);
-        mbar_init(drain, 1);
+        mbar_init(q_full, P::ROWS);
+        for (int i = 0; i < 2 * NG; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], kGroupThreads);
+            mbar_init(&o_done[i], 1);
+            odd[i] = 0ull;
+        }
+        for (int i = 0; i < NG; ++i) mbar_init(&drain[i], 1);
         *abort = 0;
-        odd[0] = odd[1] = 0ull;
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc(tmem_slot, P::TMEM_COLS);
+    if (warp == P::LOAD_WARP) {
+        tmem_alloc(tmem_slot, P::TMEM_COLS);
+        if (lane < 2)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tm_v : &tm_k)) : "memory");
+    }
     pdl_wait();
     pdl_release();
-    // ---- the sequences' table: the tiles before each
-    long long before = 0;
-    for (int i0 = 0; i0 < ta.nb; i0 += kTcThreads) {
+    // ---- the sequences' table: the work before each
+    int before = 0;
+    for (int i0 = 0; i0 < ta.nb; i0 += P::THREADS) {
         const int i = i0 + tid;
-        long long mine = 0;
+        int mine = 0;
         if (i < ta.nb) {
             const Seq q = load_seq(a.s, ta.b0 + i);
-            if (!q.bad) mine = Shape(q.len, q.n, a.G, ta.row_tiles).per_head() * a.s.Hkv;
+            if (!q.bad) mine = Shape(q.len, q.n, a.G, ta.row_tiles, NQ).per_head() * a.s.Hkv;
             else if (blockIdx.x == 0) atomicOr(a.s.status, q.bad);
             st.slot[i] = q.slot;
             st.len[i] = q.len;
             st.n[i] = q.n;
         }
-        long long incl = mine;
+        int incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += y;
         }
         if (i0 > 0) __syncthreads();                // the sums of the round before have been read
         if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kTcThreads / 32; ++w) {
+        for (int w = 0; w < P::THREADS / 32; ++w) {
             if (w == warp && i < ta.nb) st.prefix[i] = before + incl - mine;
             before += warp_sum[w];
         }
     }
-    if (tid == 0) st.prefix[ta.nb] = before;
+    if (tid == 0) {
+        st.prefix[ta.nb] = before;
+        const int N = min(NQ == 2 ? (before + 1) / 2 : before, static_cast<int>(gridDim.x));   // every share has a tile
+        cut->W = before;
+        cut->N = N;
+        cut->q = N ? before / N : 0;
+        cut->r = N ? before % N : 0;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const long long W = st.prefix[ta.nb];
-    const int N = W < gridDim.x ? static_cast<int>(W) : gridDim.x;        // every share has a tile
     Cursor cur{0, 0, 0};
-    if (static_cast<int>(blockIdx.x) < N) {
-        cur.w = share(W, N, blockIdx.x);
-        cur.w1 = share(W, N, blockIdx.x + 1);
-        int lo = 0, hi = ta.nb - 1;                 // the last sequence that starts at or before w
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (st.prefix[mid] <= cur.w) lo = mid;
-            else hi = mid - 1;
-        }
-        cur.b = lo;
+    if (static_cast<int>(blockIdx.x) < cut->N) {
+        cur.w = cut->start(st, blockIdx.x, a.G, ta.row_tiles, NQ);
+        cur.w1 = cut->start(st, blockIdx.x + 1, a.G, ta.row_tiles, NQ);
+        cur.b = st.find(cur.w);
     }
     // GDN_FLAG_TEST_EXPIRE: the wait-expiry exit, with nothing issued before it
     if (a.flags & GDN_FLAG_TEST_EXPIRE) {
@@ -295,196 +377,255 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         __syncthreads();
     }
+    auto expire = [&]() {
+        *abort = 1;
+        atomicOr(a.s.status, kStatusTimeout);
+    };
     // A bounded wait: false when it, or another role's, expired.
     auto wait = [&](uint64_t *b, uint32_t parity) {
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
             if (mbar_try_wait(b, parity)) return true;
             if (*abort) return false;
         }
-        *abort = 1;
-        atomicOr(a.s.status, kStatusTimeout);
+        expire();
         return false;
     };
     Segment s;
-    uint32_t pos = 0;                               // warp 4: tiles loaded
-    bool issued = false;                            // warp 5: some MMA
-    if (warp == 4) {
+    uint32_t pos = 0;                               // load warps: tiles loaded (of keys, or of values)
+    bool issued = false;                            // MMA warps: some MMA
+    if (warp >= P::LOAD_WARP && warp < P::MMA_WARP) {
         // ------------------------------------------------------ loads
-        // Tile by tile, keys then values; a lane per (page of the tile, 64-column atom).
-        const int ps = a.s.page_shift < 6 ? a.s.page_shift : 6;            // rows of a copy: 16, 32 or 64
-        const int copies = (kKeys >> ps) * P::ATOMS;
-        const int chunk = lane / P::ATOMS, atom = lane % P::ATOMS;
+        // The first warp loads the tiles of keys, the second those of values: a copy for each page of
+        // the tile and 64-column atom.  Lane c holds the page of place c in the block table's next 32
+        // entries, read 32 entries ahead; the copies are issued by one lane from values that are
+        // the same in every lane (issued lane by lane, each cost 100 cycles).
+        const int kv = warp - P::LOAD_WARP, shift = a.s.page_shift;
+        const int ps = shift < 6 ? shift : 6;                              // rows of a copy: 16, 32 or 64
+        const CUtensorMap *map = kv ? &tm_v : &tm_k;
         bool ok = !*abort;
-        while (ok && cur.next(st, a.G, ta.row_tiles, s)) {
+        while (ok && cur.next(st, a.G, ta.row_tiles, NQ, s)) {
             const int32_t *tab = a.s.table + static_cast<size_t>(s.slot) * a.s.max_pages;
-            for (int i = 0; ok && i < s.count; ++i) {
-                const int j0 = (s.first + i) * kKeys, j = j0 + (chunk << ps);
-                const bool mine = lane < copies && j < s.total;
-                int row = 0;
-                if (mine) {
-                    int id = __ldg(tab + (j >> a.s.page_shift));
-                    if (id < 0 || id >= a.s.n_page) {
-                        atomicOr(a.s.status, GDN_STATUS_BAD_PAGE);
-                        id = 0;
-                    }
-                    row = ((id * a.s.Hkv + s.h) << a.s.page_shift) + (j & ((1 << a.s.page_shift) - 1));
+            const int count = __shfl_sync(0xffffffffu, s.count, 0), first = __shfl_sync(0xffffffffu, s.first, 0);
+            const int total = __shfl_sync(0xffffffffu, s.total, 0), head = __shfl_sync(0xffffffffu, s.h, 0);
+            const int p0 = first * kKeys >> shift;                         // the segment's first block-table entry
+            const int p_end = min((first + count) * kKeys, total);         // tokens
+            auto read_ids = [&](int at) {                                  // entries p0 + at + lane
+                const int p = p0 + at + lane;
+                if (static_cast<long long>(p) << shift >= p_end) return -1;
+                const int id = __ldg(tab + p);
+                if (id >= 0 && id < a.s.n_page) return id;
+                if (kv == 0) atomicOr(a.s.status, GDN_STATUS_BAD_PAGE);
+                return 0;
+            };
+            int ids = read_ids(0), ids_next = read_ids(32), base = 0;
+            for (int i = 0; i < count; ++i, ++pos) {
+                const int j0 = (first + i) * kKeys, at = (j0 >> shift) - p0;
+                if (at - base >= 32) {
+                    base += 32;
+                    ids = ids_next;
+                    ids_next = read_ids(base + 32);
                 }
-                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) << (ps + 7);
+                const uint32_t spos = 2 * pos + kv, stage = spos % P::NST, round = spos / P::NST;
+                if (round > 0) ok = __all_sync(0xffffffffu, wait(&empty[stage], (round - 1) & 1)) != 0;
+                if (!ok) break;
+                int row[kKeys / 16];
+                uint32_t bytes = 0;
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++pos) {
-                    const uint32_t stage = pos % P::NST, round = pos / P::NST;
-                    if (ok && round > 0) ok = wait(&empty[stage], (round - 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(&full[stage], bytes);
-                    __syncwarp();
-                    if (mine)
-                        tma_load_2d(ring + stage * P::STAGE + atom * (kKeys * 128) + (chunk << ps) * 128, kv ? &tm_v : &tm_k,
-                                    atom * 64, row, &full[stage]);
+                for (int c = 0; c < kKeys / 16; ++c) {
+                    const int id = __shfl_sync(0xffffffffu, ids, (at - base + c) & 31);
+                    row[c] = c < (kKeys >> ps) && j0 + (c << ps) < total
+                                 ? ((id * a.s.Hkv + head) << shift) + (j0 & ((1 << shift) - 1) & ~((1 << ps) - 1)) : -1;
+                    bytes += row[c] >= 0 ? (P::ATOMS * 128u) << ps : 0u;
                 }
+                uint8_t *dst = ring + stage * P::STAGE;
+                if (elect_one()) {
+                    mbar_expect_tx(&full[stage], bytes);
+#pragma unroll
+                    for (int c = 0; c < kKeys / 16; ++c)
+                        if (row[c] >= 0) {
+#pragma unroll
+                            for (int x = 0; x < P::ATOMS; ++x)
+                                tma_load_2d(dst + x * (kKeys * 128) + (c << (ps + 7)), map, x * 64, row[c], &full[stage]);
+                        }
+                }
+                __syncwarp();
             }
         }
-    } else if (warp == 5) {
+    } else if (warp >= P::MMA_WARP) {
         // ------------------------------------------------------ MMAs
-        if (lane == 0) {
-            const uint64_t dq = desc_sw128(saddr(sQ));
-            const uint32_t idS = idesc_mn(1, kRows, kKeys), idO = idesc_mn(1, kRows, D) | kIdescMnMajorB;
-            uint32_t g = 0, segs = 0;               // tiles and segments so far
-            bool ok = !*abort;
-            auto scores = [&](uint32_t t) {         // S of tile t into its buffer
-                const uint32_t pos = 2 * t, stage = pos % P::NST;
-                if (!wait(&full[stage], (pos / P::NST) & 1)) return false;
-                tc_fence_after();
-                const uint64_t dk = desc_sw128(saddr(ring + stage * P::STAGE));
+        // The whole warp walks the tiles and one elected lane issues: values that the compiler
+        // can see to be the same in every lane stay in uniform registers, where the MMA takes its
+        // operands from (issued inside a one-lane branch, each MMA cost about 125 cycles).
+        const int group = warp - P::MMA_WARP;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + group * P::TCOLS;
+        const uint64_t dk0 = desc_sw128(saddr(ring)), dv0 = desc_mn_sw128(saddr(ring), kKeys * 128);
+        constexpr uint32_t idS = idesc_mn(1, kRows, kKeys), idO = idesc_mn(1, kRows, D) | kIdescMnMajorB;
+        uint64_t *sf = s_full + 2 * group, *pf = p_full + 2 * group, *od = o_done + 2 * group;
+        uint32_t g = 0, tile0 = 0, segs = 0;        // this group's tiles, the CTA's tiles and segments so far
+        bool ok = !*abort;
+        while (ok && cur.next(st, a.G, ta.row_tiles, NQ, s)) {
+            const bool alternate = NG == 2 && s.nq == 1;
+            const int step = alternate ? 2 : 1, off = alternate ? (group ^ tile0) & 1 : 0;
+            const int count = __shfl_sync(0xffffffffu, (s.count - off + step - 1) / step, 0);
+            const bool twice = __shfl_sync(0xffffffffu, alternate ? 1 : 0, 0) != 0;
+            const uint64_t dq = desc_sw128(saddr(sQ) + (s.nq == 2 ? group * P::QTILE : 0));
+            ok = __all_sync(0xffffffffu, wait(q_full, segs++ & 1)) != 0;
+            int sn = 0, pn = 0;                     // next tile to score, next to multiply with the values
+            uint32_t idle = 0;
+            while (ok && pn < count) {
+                bool did = false;
+                if (sn < count && sn < pn + 2) {
+                    // the buffer held the weights of tile sn - 2: their product must be done
+                    const uint32_t t = g + sn, kpos = 2 * (tile0 + sn * step + off), stage = kpos % P::NST;
+                    const bool ready = mbar_test(&full[stage], (kpos / P::NST) & 1) &&
+                                       (sn < 2 || mbar_test(&od[t & 1], ((t - 2) >> 1) & 1));
+                    if (__all_sync(0xffffffffu, ready)) {
+                        tc_fence_after();
+                        const uint64_t dk = desc_add(dk0, stage * P::STAGE);
+                        if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t at = (k & 3) * 32;
-                    mma_bf16(tmem + (t & 1) * kKeys, desc_add(dq, (k >> 2) * (kRows * 128) + at),
-                             desc_add(dk, (k >> 2) * (kKeys * 128) + at), idS, k > 0);
-                }
-                mma_commit(&s_full[t & 1]);
-                mma_commit(&empty[stage]);
-                issued = true;
-                return true;
-            };
-            while (ok && cur.next(st, a.G, ta.row_tiles, s)) {
-                ok = wait(q_full, segs++ & 1) && scores(g);
-                for (int i = 0; ok && i < s.count; ++i, ++g) {
-                    if (i + 1 < s.count) {
-                        // the other buffer held the weights of tile g - 1: their product is done
-                        if (i > 0) ok = wait(o_done, (g - 1) & 1);
-                        if (ok) ok = scores(g + 1);
-                        if (!ok) break;
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t at = (k & 3) * 32;
+                                mma_bf16(tm + (t & 1) * kKeys, desc_add(dq, (k >> 2) * (kRows * 128) + at),
+                                         desc_add(dk, (k >> 2) * (kKeys * 128) + at), idS, k > 0);
+                            }
+                            mma_commit(&sf[t & 1]);
+                            mma_commit(&empty[stage]);
+                            if (twice) mma_commit(&empty[stage]);
+                        }
+                        issued = did = true;
+                        ++sn;
                     }
-                    const uint32_t pos = 2 * g + 1, stage = pos % P::NST;
-                    ok = wait(&p_full[g & 1], (g >> 1) & 1) && wait(&full[stage], (pos / P::NST) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dv = desc_mn_sw128(saddr(ring + stage * P::STAGE), kKeys * 128);
-#pragma unroll
-                    for (int k = 0; k < kKeys / 8; ++k)           // the weights' first terms, then their second
-                        mma_bf16_ts(tmem + P::COL_O, tmem + (g & 1) * kKeys + k * 8, desc_add(dv, (k & 3) * 2048), idO,
-                                    i > 0 || k > 0);
-                    mma_commit(&empty[stage]);
-                    mma_commit(o_done);
                 }
+                if (pn < sn) {
+                    const uint32_t t = g + pn, vpos = 2 * (tile0 + pn * step + off) + 1, stage = vpos % P::NST;
+                    const bool ready = mbar_test(&pf[t & 1], (t >> 1) & 1) && mbar_test(&full[stage], (vpos / P::NST) & 1);
+                    if (__all_sync(0xffffffffu, ready)) {
+                        tc_fence_after();
+                        const uint64_t dv = desc_add(dv0, stage * P::STAGE);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < kKeys / 8; ++k)   // the weights' first terms, then their second
+                                mma_bf16_ts(tm + 2 * kKeys, tm + (t & 1) * kKeys + k * 8, desc_add(dv, (k & 3) * 2048), idO,
+                                            pn > 0 || k > 0);
+                            mma_commit(&empty[stage]);
+                            if (twice) mma_commit(&empty[stage]);
+                            mma_commit(&od[t & 1]);
+                        }
+                        did = true;
+                        ++pn;
+                    }
+                }
+                idle = did ? 0 : idle + 1;
+                if (*abort || idle > kIdleLimit) {
+                    if (idle > kIdleLimit) expire();
+                    ok = false;
+                }
+                ok = __all_sync(0xffffffffu, ok);
             }
+            g += count;
+            tile0 += s.count;
         }
     } else {
         // ------------------------------------------------------ rows
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        uint32_t g = 0, syncs = 0;
-        bool ok = !*abort;
-        // a bounded wait of a whole warp (the TMEM loads and stores take all lanes), and one for
-        // all 128 rows
-        auto wait_warp = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
-        auto rows_sync = [&]() {
-            mbar_arrive(rows_bar);
-            return wait_warp(rows_bar, syncs++ & 1);
+        // Thread (group, half, row): keys [32 half, 32 half + 32) of the group's tiles, output columns
+        // [D/2 half, + D/2).
+        const int group = NG == 2 ? warp >> 3 : 0, quarter = warp & 3, half = (warp >> 2) & 1;
+        const int r_in = quarter * 32 + lane, gtid = tid & (kGroupThreads - 1), pair_id = 4 + group * 4 + quarter;
+        const uint32_t t_lane = tmem + group * P::TCOLS + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t t_o = t_lane + 2 * kKeys + half * (D / 2);
+        uint64_t *sf = s_full + 2 * group, *pf = p_full + 2 * group, *od = o_done + 2 * group;
+        float *xm = xch, *xl = xch + P::ROWS;       // maxima and sums of the row threads
+        uint32_t g = 0, tile0 = 0;
+        auto wait_rows = [&](uint64_t *b, uint32_t parity) {   // reconverged: TMEM accesses take whole warps
+            wait(b, parity);
+            __syncwarp();
+            tc_fence_after();
         };
-        while (ok && cur.next(st, a.G, ta.row_tiles, s)) {
-            const int r0 = s.rt * kRows, rows = a.s.T * a.G;
+        while (cur.next(st, a.G, ta.row_tiles, NQ, s)) {
+            const bool alternate = NG == 2 && s.nq == 1;
+            const int step = alternate ? 2 : 1, off = alternate ? (group ^ tile0) & 1 : 0;
+            const int rt = s.rt + (s.nq == 2 ? group : 0), r0 = rt * kRows, rows = a.s.T * a.G;
             const int b = ta.b0 + s.b;
+            if (NG == 2) bar_sync(1, P::ROWS);      // both groups have left the queries and the exchange words
             {                                       // the unit's queries, rows not in use zero
                 constexpr int VECS = D / 8;
-#pragma unroll 8
-                for (int i = 0; i < VECS; ++i) {
-                    const int x = i * 128 + tid, r = x / VECS, c = x % VECS;
-                    const int t = (r0 + r) / a.G, qh = (r0 + r) - t * a.G;
+                const int vecs = s.nq * kRows * VECS;
+#pragma unroll 4
+                for (int x = tid; x < vecs; x += P::ROWS) {
+                    const int q = x / (kRows * VECS), r = x / VECS % kRows, c = x % VECS;
+                    const int row = (s.rt + q) * kRows + r, t = row / a.G, qh = row - t * a.G;
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r0 + r < rows && t < s.n)
+                    if (row < rows && t < s.n)
                         v = __ldg(reinterpret_cast<const uint4 *>(
                                       static_cast<const __nv_bfloat16 *>(a.q) +
                                       ((static_cast<size_t>(b) * a.s.T + t) * a.Hq + s.h * a.G + qh) * D) + c);
-                    *reinterpret_cast<uint4 *>(sQ + (c >> 3) * (kRows * 128) + sw128(r, c & 7)) = v;
+                    *reinterpret_cast<uint4 *>(sQ + q * P::QTILE + (c >> 3) * (kRows * 128) + sw128(r, c & 7)) = v;
                 }
                 fence_proxy_async();
                 mbar_arrive(q_full);
             }
-            const int row = r0 + tid, t = row / a.G;
+            const int row = r0 + r_in, t = row / a.G;
             const bool used = row < rows && t < s.n;
             const bool warp_live = __any_sync(0xffffffffu, used);
             const uint64_t bits = used ? row_tree(a, b, t, s.n) : 0ull;
-            float m = -INFINITY, l = 0.f;
-            for (int i = 0; i < s.count; ++i, ++g) {
+            float m = -INFINITY, l = 0.f;           // m: the same in both threads of a row; l: of this thread's keys
+            int mine = 0;                           // tiles of this group
+            for (int i = off; i < s.count; i += step, ++g, ++mine) {
                 const int j0 = (s.first + i) * kKeys;
                 const bool edge = j0 + kKeys > (s.total ? s.len : 0);      // some tokens may be unseen
                 const uint32_t t_s = t_lane + (g & 1) * kKeys;
-                uint64_t seen = ~0ull;
-                if (!(ok = wait_warp(&s_full[g & 1], (g >> 1) & 1))) break;
-                tc_fence_after();
+                wait_rows(&sf[g & 1], (g >> 1) & 1);
                 if (warp_live) {
-                    uint32_t x0[32], x1[32];
-                    tmem_ld32(t_s, x0);
-                    tmem_ld32(t_s + 32, x1);
+                    uint32_t x[32];
+                    tmem_ld32(t_s + 32 * half, x);
                     tmem_wait_ld();
                     if (edge) {
                         const int sh = s.len - j0;                          // draft token 0's place in the tile
-                        seen = sh >= 64 ? ~0ull : sh > 0 ? (1ull << sh) - 1 : 0ull;
-                        seen |= sh >= 64 ? 0ull : sh >= 0 ? bits << sh : sh > -64 ? bits >> -sh : 0ull;
-                        if (!used) seen = 0ull;
+                        uint64_t all = sh >= 64 ? ~0ull : sh > 0 ? (1ull << sh) - 1 : 0ull;
+                        all |= sh >= 64 ? 0ull : sh >= 0 ? bits << sh : sh > -64 ? bits >> -sh : 0ull;
+                        const uint32_t seen = used ? static_cast<uint32_t>(all >> (32 * half)) : 0u;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            if (!((seen >> k) & 1)) x0[k] = 0xff800000u;
-                            if (!((seen >> (k + 32)) & 1)) x1[k] = 0xff800000u;
+                        for (int k = 0; k < 32; ++k)
+                            if (!((seen >> k) & 1)) x[k] = 0xff800000u;
+                    }
+                    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        top[(k >> 1) & 1] = fmaxf(top[(k >> 1) & 1], fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                    const float mt = fmaxf(top[0], top[1]) * a.scale_log2;
+                    // (also: both threads have read their scores, which the weights go over)
+                    if (pair_any(pair_id, mt > m + 8.f)) {
+                        xm[tid] = mt;
+                        bar_sync(pair_id, 64);
+                        const float mp = fmaxf(mt, xm[tid ^ 128]);
+                        bar_sync(pair_id, 64);                              // read before it is written again
+                        float fac = 1.f;
+                        if (mp > m + 8.f) {
+                            fac = ex2(m - mp);                              // 0 when nothing was summed
+                            m = mp;
+                            l *= fac;
                         }
-                    }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        top[k & 3] = fmaxf(top[k & 3], fmaxf(__uint_as_float(x0[k]), __uint_as_float(x1[k])));
-                    }
-                    const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-                    float fac = 1.f;
-                    bool raise = false;
-                    if (mt > m + 8.f || m == -INFINITY) {       // m -inf: nothing summed yet
-                        fac = ex2(m - (mt == -INFINITY ? 0.f : mt));
-                        raise = i > 0 && m != mt;
-                        m = mt;
-                        l *= fac;
-                    }
-                    if (__any_sync(0xffffffffu, raise)) {
-                        if (!(ok = wait_warp(o_done, (g - 1) & 1))) break;
-                        tc_fence_after();
+                        if (mine > 0) {
+                            wait_rows(&od[(g - 1) & 1], ((g - 1) >> 1) & 1);
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(t_lane + P::COL_O + c, o);
-                            tmem_wait_ld();
+                            for (int c = 0; c < D / 2; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(t_o + c, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
-                            tmem_st32(t_lane + P::COL_O + c, o);
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
+                                tmem_st32(t_o + c, o);
+                            }
                         }
-                        tmem_wait_st();
                     }
                     const float ms = m == -INFINITY ? 0.f : m;
                     const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-ms, -ms);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    uint32_t hi[32], lo[32];
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const uint32_t *x = k < 16 ? x0 + 2 * k : x1 + 2 * k - 32;
-                        float2 e = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc, mm);
+                    for (int k = 0; k < 16; ++k) {
+                        float2 e = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc, mm);
                         e = make_float2(ex2(e.x), ex2(e.y));
                         sum[k & 1] = add2(sum[k & 1], e);
                         __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
@@ -495,22 +636,24 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         lo[k] = *reinterpret_cast<const uint32_t *>(&h);
                     }
                     l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-                    tmem_st32(t_s, hi);
-                    tmem_st32(t_s + 32, lo);
+                    tmem_st16(t_s + 16 * half, hi);
+                    tmem_st16(t_s + 32 + 16 * half, lo);
                     tmem_wait_st();
                 }
-                unsigned long long special = 0ull;
+                unsigned long long special = 0ull, *flags = &odd[(alternate ? 2 * group : 0) + (g & 1)];
+                const int who = alternate || NG == 1 ? gtid : tid, whole_id = alternate ? 2 + group : 1;
+                const int whole_n = alternate || NG == 1 ? kGroupThreads : P::ROWS;
                 if (edge) {
                     // Value rows past the last token hold anything: zeros in their place.  The
                     // draft's values may be unseen by some rows, whose zero weights must not meet
                     // an infinity or NaN: those elements are zeroed too, and added below to
-                    // the rows that do see them.
-                    const uint32_t pos = 2 * g + 1, stage = pos % P::NST;
-                    if (!(ok = wait_warp(&full[stage], (pos / P::NST) & 1))) break;
+                    // the rows that do see them.  (All threads that use the tile do this together.)
+                    const uint32_t vpos = 2 * (tile0 + i) + 1, stage = vpos % P::NST;
+                    wait_rows(&full[stage], (vpos / P::NST) & 1);
                     uint8_t *sv = ring + stage * P::STAGE;
-                    const int from = max(0, s.len - j0) * (s.total ? 1 : 0), live = s.total - j0;
-                    for (int x = tid + from * (D / 8); x < kKeys * (D / 8); x += 128) {
-                        const int r = x / (D / 8), c = x % (D / 8);
+                    const int from = s.total ? max(0, s.len - j0) : 0, live = s.total - j0;
+                    for (int y = who + from * (D / 8); y < kKeys * (D / 8); y += whole_n) {
+                        const int r = y / (D / 8), c = y % (D / 8);
                         uint4 *at = reinterpret_cast<uint4 *>(sv + (c >> 3) * (kKeys * 128) + sw128(r, c & 7));
                         if (r >= live) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
@@ -525,28 +668,27 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         }
                         if (bad) {
                             *at = make_uint4(w[0], w[1], w[2], w[3]);
-                            atomicOr(&odd[g & 1], 1ull << r);
+                            atomicOr(flags, 1ull << r);
                         }
                     }
                     fence_proxy_async();
-                    if (!(ok = rows_sync())) break;
-                    special = odd[g & 1];
+                    bar_sync(whole_id, whole_n);
+                    special = *flags;
                 }
-                // The product before is done (it nearly always is: the softmax takes longer), so that a
-                // wait for this tile's cannot mistake that one's phase for its own.
-                if (i > 0 && !(ok = wait_warp(o_done, (g - 1) & 1))) break;
                 tc_fence_before();
-                mbar_arrive(&p_full[g & 1]);
-                if (special) {                      // the same for all 128 rows
-                    if (!(ok = wait_warp(o_done, g & 1))) break;
-                    tc_fence_after();
+                mbar_arrive(&pf[g & 1]);
+                if (special) {                      // the same for all threads that use the tile
+                    wait_rows(&od[g & 1], (g >> 1) & 1);
                     if (warp_live) {
-                        const uint64_t mine = used ? seen & special : 0ull;
+                        const int sh = s.len - j0;
+                        uint64_t view = sh >= 64 ? 0ull : sh >= 0 ? bits << sh : sh > -64 ? bits >> -sh : 0ull;
+                        view = used ? view & special : 0ull;
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
+                        for (int c = 0; c < D / 2; c += 32) {
                             uint32_t o[32];
-                            tmem_ld32(t_lane + P::COL_O + c, o);
+                            tmem_ld32(t_o + c, o);
                             tmem_wait_ld();
+#pragma unroll 1
                             for (int r = 0; r < kKeys; ++r) {
                                 if (!((special >> r) & 1)) continue;
                                 const int j = j0 + r;
@@ -554,169 +696,203 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                                 if (id < 0 || id >= a.s.n_page) id = 0;
                                 const size_t vrow = ((static_cast<size_t>(id) * a.s.Hkv + s.h) << a.s.page_shift) +
                                                     (j & ((1 << a.s.page_shift) - 1));
-                                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + vrow * D + c;
+                                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + vrow * D + half * (D / 2) + c;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
                                     const float y = __bfloat162float(v[k]);
-                                    if (((mine >> r) & 1) && !(fabsf(y) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
+                                    if (((view >> r) & 1) && !(fabsf(y) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
                                 }
                             }
-                            tmem_st32(t_lane + P::COL_O + c, o);
+                            tmem_st32(t_o + c, o);
                         }
                         tmem_wait_st();
                     }
-                    if (!(ok = rows_sync())) break;
-                    if (tid == 0) odd[g & 1] = 0ull;
-                    if (!(ok = rows_sync())) break;
+                    bar_sync(whole_id, whole_n);
+                    if (who == 0) *flags = 0ull;
+                    bar_sync(whole_id, whole_n);
                 }
             }
-            if (!ok) break;
+            tile0 += s.count;
             // ---- the unit's result, or this CTA's part of it
-            if (!(ok = wait_warp(o_done, (g - 1) & 1))) break;
-            tc_fence_after();
+            if (mine > 0) wait_rows(&od[(g - 1) & 1], ((g - 1) >> 1) & 1);
             const bool whole = s.count == s.tiles;
-            const size_t unit = (static_cast<size_t>(b) * a.s.Hkv + s.h) * ta.row_tiles + s.rt;
-            if (tid == 0 && s.first == 0)
-                ta.desc[unit] = make_int2(blockIdx.x, whole ? 1 : owner(W, N, s.unit_w + s.tiles - 1) - static_cast<int>(blockIdx.x) + 1);
-            if (__any_sync(0xffffffffu, row < rows)) {
-                if (whole) {
-                    const float inv = used && (l > 0.f || l != l) ? 1.f / l : 0.f;
-                    const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + s.h * a.G + (row - t * a.G);
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D);
+            const size_t unit = (static_cast<size_t>(b) * a.s.Hkv + s.h) * ta.row_tiles + rt;
+            if (gtid == 0 && (group == 0 || s.nq == 2)) {
+                if (s.first == 0) ta.desc[unit].x = 2 * blockIdx.x + (s.nq == 2 ? group : 0);
+                if (s.first + s.count == s.tiles) ta.desc[unit].y = blockIdx.x;
+            }
+            // the row's threads: two, or four when both groups worked on it (each group's O scaled to
+            // the common maximum)
+            xm[tid] = m;
+            xl[tid] = l;
+            tc_fence_before();
+            bar_sync(alternate ? 1 : 2 + group, alternate ? P::ROWS : kGroupThreads);
+            tc_fence_after();
+            l += xl[tid ^ 128];                     // (commutative: the same in all the row's threads)
+            float f0 = 1.f, f1 = 0.f;               // of this group's O, of the other's
+            const bool both = alternate && s.count > 1;
+            if (both) {
+                const float m1 = xm[tid ^ 256], mn = fmaxf(m, m1), ms = mn == -INFINITY ? 0.f : mn;
+                f0 = ex2(m - ms);
+                f1 = ex2(m1 - ms);
+                const float l0 = l * f0, l1 = (xl[tid ^ 256] + xl[tid ^ 384]) * f1;
+                l = group == 0 ? l0 + l1 : l1 + l0;
+                m = mn;
+            }
+            const bool writer = !alternate || mine > 0;                    // a single tile leaves one group without
+            if (writer && __any_sync(0xffffffffu, row < rows)) {
+                const int cols = both ? D / 4 : D / 2, c0 = both ? (2 * group + half) * (D / 4) : half * (D / 2);
+                const uint32_t o_mine = t_lane + 2 * kKeys + c0;
+                const uint32_t o_other = both ? o_mine + (group == 0 ? P::TCOLS : -P::TCOLS) : o_mine;
+                const float inv = !whole ? 1.f : used && (l > 0.f || l != l) ? 1.f / l : 0.f;
+                f0 *= inv;
+                f1 *= inv;
+                const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + s.h * a.G + (row - t * a.G);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c0);
+                float *slot = ta.part + static_cast<size_t>((2 * blockIdx.x + (s.first == 0 ? 1 : 0)) * NQ + (s.nq == 2 ? group : 0)) *
+                                            (D + 2) * ta.rp + r_in;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(t_lane + P::COL_O + c, o);
-                        tmem_wait_ld();
+                for (int c = 0; c < cols; c += 16) {
+                    float o[16];
+                    tmem_ld16(o_mine + c, o);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t h[4];
+                    for (int k = 0; k < 16; ++k) o[k] *= f0;
+                    if (both) {
+                        float o1[16];
+                        tmem_ld16(o_other + c, o1);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * inv,
-                                                                               __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                                h[e] = inv != 0.f ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
-                            }
-                            if (row < rows) dst[c / 8 + k] = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                        __syncwarp();
-                    }
-                    if (a.lse && row < rows) a.lse[orow] = used ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-                } else {
-                    // column by column, so that a warp's rows are one run of memory
-                    float *dst = ta.part + static_cast<size_t>(2 * blockIdx.x + (s.first == 0 ? 1 : 0)) * (D + 2) * ta.rp + tid;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(t_lane + P::COL_O + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (row < rows) dst[static_cast<size_t>(c + k) * ta.rp] = __uint_as_float(o[k]);
-                        __syncwarp();
+                        for (int k = 0; k < 16; ++k) o[k] = fmaf(o1[k], f1, o[k]);
                     }
                     if (row < rows) {
-                        dst[static_cast<size_t>(D) * ta.rp] = m;
-                        dst[static_cast<size_t>(D + 1) * ta.rp] = l;
+                        if (whole) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * k + 2 * e], o[8 * k + 2 * e + 1]);
+                                    h[e] = inv != 0.f ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
+                                }
+                                dst[c / 8 + k] = make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        } else {                    // column by column: a warp's rows are one run of memory
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) slot[static_cast<size_t>(c0 + c + k) * ta.rp] = o[k];
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (row < rows && c0 == 0) {
+                    if (whole) {
+                        if (a.lse) a.lse[orow] = used ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                    } else {
+                        slot[static_cast<size_t>(D) * ta.rp] = m;
+                        slot[static_cast<size_t>(D + 1) * ta.rp] = l;
                     }
                 }
             }
             tc_fence_before();
+            if (NG == 1) bar_sync(1, P::ROWS);      // the exchange words have been read
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (*abort) {                                   // nothing of this CTA runs on when it ends
-        if (warp == 4) {
-            for (uint32_t k = pos > P::NST ? pos - P::NST : 0; k < pos; ++k)
+        if (warp >= P::LOAD_WARP && warp < P::MMA_WARP) {
+            for (uint32_t t = pos > P::NST / 2 ? pos - P::NST / 2 : 0; t < pos; ++t) {
+                const uint32_t k = 2 * t + warp - P::LOAD_WARP;
                 if (!mbar_wait(&full[k % P::NST], (k / P::NST) & 1) && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
-        } else if (warp == 5 && issued) {
-            mma_commit(drain);
-            if (!mbar_wait(drain, 0)) atomicOr(a.s.status, GDN_STATUS_DRAIN);
+            }
+        } else if (warp >= P::MMA_WARP && issued) {
+            if (elect_one()) mma_commit(&drain[warp - P::MMA_WARP]);
+            if (!mbar_wait(&drain[warp - P::MMA_WARP], 0)) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
         __syncwarp();
         tc_fence_before();
         __syncthreads();
     }
-    if (warp == 5) tmem_dealloc(tmem, P::TMEM_COLS);
+    if (warp == P::LOAD_WARP) tmem_dealloc(tmem, P::TMEM_COLS);
 }
 
 // ------------------------------------------------------------------- the join
-// One CTA per (unit, 8 output columns): a thread per row in each of kGroups groups, which take
-// every kGroups-th part; the groups' sums are joined in shared memory in their order.
-constexpr int kGroups = 4;
+// A task is 32 rows (a lane each) and 8 output columns of a unit; `wide` warps (a power of two,
+// about one for every four parts) take its parts in turn, and the first of them joins their
+// sums in a fixed order.  gridDim.y CTAs share a unit's tasks.
+constexpr int kJoinWarps = 16;
 
-template <int D>
-__global__ void __launch_bounds__(kGroups * kRows) verify_tc_join_kernel(const TcArgs ta, int grid)
+template <int D, int NQ>
+__global__ void __launch_bounds__(kJoinWarps * 32) verify_tc_join_kernel(const TcArgs ta, int grid)
 {
     const AttnArgs &a = ta.a;
     const int rt = blockIdx.x % ta.row_tiles, bh = blockIdx.x / ta.row_tiles;
     const int h = bh % a.s.Hkv, b = ta.b0 + bh / a.s.Hkv;
-    const int r = threadIdx.x % kRows, grp = threadIdx.x / kRows;
-    __shared__ float acc_s[kGroups][8][kRows], m_s[kGroups][kRows], l_s[kGroups][kRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float sums[kJoinWarps][10][32];
     pdl_wait();
     pdl_release();
     const int2 d = ta.desc[(static_cast<size_t>(b) * a.s.Hkv + h) * ta.row_tiles + rt];
-    if (d.y < 2 || d.x < 0 || d.x + d.y > grid) return;           // finished by one CTA
     const Seq sq = load_seq(a.s, b);
-    if (sq.bad) return;
-    const int row = rt * kRows + r, t = row / a.G, rows = a.s.T * a.G;
-    const bool used = row < rows && t < sq.n;
-    auto part = [&](int k) {                                      // part k: the first CTA's second slot, then first slots
-        return ta.part + static_cast<size_t>(2 * (d.x + k) + (k == 0 ? 1 : 0)) * (D + 2) * ta.rp + r;
-    };
-    float m = -INFINITY, l = 0.f, acc[8];
+    const int cta = d.x >> 1, place = d.x & 1, parts = d.y - cta + 1;
+    if (sq.bad || parts < 2 || cta < 0 || place >= NQ || d.y >= grid) return;      // finished by one CTA
+    int wide = 1;
+    while (wide < kJoinWarps && wide * 4 < parts) wide *= 2;
+    const int at_once = kJoinWarps / wide, mine = warp / wide, sub = warp % wide;
+    const int rows = a.s.T * a.G, groups = min(ta.rp, rows - rt * kRows + 31) / 32, tasks = groups * (D / 8);
+    for (int t0 = blockIdx.y * at_once; t0 < tasks; t0 += gridDim.y * at_once) {
+        const int task = t0 + mine, r = task / (D / 8) * 32 + lane, c0 = task % (D / 8) * 8;
+        const int row = rt * kRows + r, t = row / a.G;
+        const bool used = task < tasks && row < rows && t < sq.n;
+        float m = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-    if (used) {
-        const int c0 = blockIdx.y * 8;
-#pragma unroll 2
-        for (int k = grp; k < d.y; k += kGroups) {
-            const float *p = part(k);
-            const float mk = p[static_cast<size_t>(D) * ta.rp], lk = p[static_cast<size_t>(D + 1) * ta.rp];
-            float x[8];
+        for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+        if (used) {
+#pragma unroll 4
+            for (int k = sub; k < parts; k += wide) {                      // part 0: the first CTA's second slot
+                const float *p = ta.part + static_cast<size_t>((2 * (cta + k) + (k == 0 ? 1 : 0)) * NQ + place) * (D + 2) * ta.rp + r;
+                const float mk = p[static_cast<size_t>(D) * ta.rp], lk = p[static_cast<size_t>(D + 1) * ta.rp];
+                float x[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = p[static_cast<size_t>(c0 + c) * ta.rp];
-            const float mn = fmaxf(m, mk), ms = mn == -INFINITY ? 0.f : mn;
-            const float f0 = ex2(m - ms), f1 = ex2(mk - ms);
-            m = mn;
-            l = l * f0 + lk * f1;
+                for (int c = 0; c < 8; ++c) x[c] = p[static_cast<size_t>(c0 + c) * ta.rp];
+                const float mn = fmaxf(m, mk), ms = mn == -INFINITY ? 0.f : mn;
+                const float f0 = ex2(m - ms), f1 = ex2(mk - ms);
+                m = mn;
+                l = l * f0 + lk * f1;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) acc[c] = acc[c] * f0 + x[c] * f1;
+                for (int c = 0; c < 8; ++c) acc[c] = acc[c] * f0 + x[c] * f1;
+            }
         }
+        if (wide > 1) {                                                  // the same in the whole CTA
+            sums[warp][8][lane] = m;
+            sums[warp][9][lane] = l;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sums[warp][c][lane] = acc[c];
+            __syncthreads();
+            if (sub == 0) {
+                for (int w = 1; w < wide; ++w) {
+                    const float mk = sums[warp + w][8][lane], mn = fmaxf(m, mk), ms = mn == -INFINITY ? 0.f : mn;
+                    const float f0 = ex2(m - ms), f1 = ex2(mk - ms);
+                    m = mn;
+                    l = l * f0 + sums[warp + w][9][lane] * f1;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] = acc[c] * f0 + sums[warp + w][c][lane] * f1;
+                }
+            }
+            __syncthreads();
+        }
+        if (sub != 0 || task >= tasks || row >= rows) continue;
+        const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + h * a.G + (row - t * a.G);
+        const bool any = used && (l > 0.f || l != l);
+        const float inv = any ? 1.f / l : 0.f;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+            w[e] = any ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
+        }
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (a.lse && c0 == 0) a.lse[orow] = used ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
-    m_s[grp][r] = m;
-    l_s[grp][r] = l;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc_s[grp][c][r] = acc[c];
-    __syncthreads();
-    if (grp != 0 || row >= rows) return;
-    float mn = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) mn = fmaxf(mn, m_s[k][r]);
-    const float ms = mn == -INFINITY ? 0.f : mn;
-    float lt = 0.f, o[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) o[c] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        const float f = ex2(m_s[k][r] - ms);
-        lt = fmaf(l_s[k][r], f, lt);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) o[c] = fmaf(acc_s[k][c][r], f, o[c]);
-    }
-    const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + h * a.G + (row - t * a.G);
-    const bool any = used && (lt > 0.f || lt != lt);
-    const float inv = any ? 1.f / lt : 0.f;
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
-        w[e] = any ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
-    }
-    reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D)[blockIdx.y] = make_uint4(w[0], w[1], w[2], w[3]);
-    if (a.lse && blockIdx.y == 0) a.lse[orow] = used ? (mn + log2f(lt)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------------- host side
@@ -738,32 +914,47 @@ int tc_rp(const gdn_page_cache *c, const gdn_attn_dims *d) {
     const int rows = d->T * (d->Hq / c->Hkv);
     return rows >= kRows ? kRows : (rows + 31) / 32 * 32;
 }
-// CTAs of a launch over nb sequences: as many as can be resident, but no more than there may be tiles.
+// Row tiles of a unit: pairs where there are any and TMEM has room for two groups.
+int tc_nq(const gdn_page_cache *c, const gdn_attn_dims *d) { return c->d != 256 && tc_row_tiles(c, d) > 1 ? 2 : 1; }
+// Sequences of one launch: its table has kMaxSeqs entries, its work is counted in 32 bits.
+int tc_seqs(const gdn_page_cache *c, const gdn_attn_dims *d) {
+    const long long tiles = (static_cast<long long>(c->max_pages) * c->page + kKeys - 1) / kKeys;   // <= 2^18
+    const long long most = (1ll << 30) / (tiles * c->Hkv * tc_row_tiles(c, d));                     // >= 1
+    const int n = most < kMaxSeqs ? static_cast<int>(most) : kMaxSeqs;
+    return d->B < n ? d->B : n;
+}
+// CTAs of a launch over nb sequences: one per SM, but no more than there may be tiles.
 int tc_grid(const gdn_page_cache *c, const gdn_attn_dims *d, int nb) {
     const long long tiles = (static_cast<long long>(c->max_pages) * c->page + kKeys - 1) / kKeys;
     const long long all = tiles * nb * c->Hkv * tc_row_tiles(c, d);
-    const int resident = sm_count() * (c->d == 256 ? TcPlan<256>::CTAS : TcPlan<128>::CTAS);
-    return static_cast<int>(all < resident ? all : resident);
+    const int sms = sm_count();
+    return static_cast<int>(all < sms ? all : sms);
+}
+// CTAs that share a unit's tasks in the join: two per SM in all, at most one per task.
+int join_ctas(int units, int tasks) {
+    const int want = (2 * sm_count() + units - 1) / units;
+    return want < 1 ? 1 : want > tasks ? tasks : want;
 }
 size_t desc_bytes(const gdn_page_cache *c, const gdn_attn_dims *d) {
     return (static_cast<size_t>(d->B) * c->Hkv * tc_row_tiles(c, d) * sizeof(int2) + 15) & ~static_cast<size_t>(15);
 }
 
-template <int D>
+template <int D, int NQ>
 int launch_tc(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a, cudaStream_t s) {
-    using P = TcPlan<D>;
+    using P = TcPlan<D, NQ>;
     CUtensorMap mk, mv;
     if (!page_map(&mk, a.k, c) || !page_map(&mv, a.v, c)) return GDN_ERR_LAUNCH;
-    if (cudaFuncSetAttribute(verify_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES) != cudaSuccess)
+    if (cudaFuncSetAttribute(verify_tc_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES) != cudaSuccess)
         return GDN_ERR_LAUNCH;
     TcArgs ta{a, 0, 0, tc_row_tiles(c, d), tc_rp(c, d), reinterpret_cast<int2 *>(a.ws),
               reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + desc_bytes(c, d))};
-    for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += kMaxSeqs) {
-        ta.nb = d->B - ta.b0 < kMaxSeqs ? d->B - ta.b0 : kMaxSeqs;
-        const int grid = tc_grid(c, d, ta.nb);
-        if (launch_pdl(verify_tc_kernel<D>, dim3(grid), dim3(kTcThreads), P::BYTES, s, mk, mv, ta) != cudaSuccess ||
-            launch_pdl(verify_tc_join_kernel<D>, dim3(ta.nb * c->Hkv * ta.row_tiles, D / 8), dim3(kGroups * kRows), 0, s,
-                       ta, grid) != cudaSuccess)
+    const int step = tc_seqs(c, d);
+    for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += step) {
+        ta.nb = d->B - ta.b0 < step ? d->B - ta.b0 : step;
+        const int grid = tc_grid(c, d, ta.nb), units = ta.nb * c->Hkv * ta.row_tiles;
+        if (launch_pdl(verify_tc_kernel<D, NQ>, dim3(grid), dim3(P::THREADS), P::BYTES, s, mk, mv, ta) != cudaSuccess ||
+            launch_pdl(verify_tc_join_kernel<D, NQ>, dim3(units, join_ctas(units, ta.rp / 32 * (D / 8))),
+                       dim3(kJoinWarps * 32), 0, s, ta, grid) != cudaSuccess)
             return GDN_ERR_LAUNCH;
     }
     return GDN_OK;
@@ -772,13 +963,15 @@ int launch_tc(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a
 }  // namespace
 
 int64_t attn_tc_workspace(const gdn_page_cache *c, const gdn_attn_dims *d) {
-    const int nb = d->B < kMaxSeqs ? d->B : kMaxSeqs;
     return static_cast<int64_t>(desc_bytes(c, d)) +
-           static_cast<int64_t>(2) * tc_grid(c, d, nb) * (c->d + 2) * tc_rp(c, d) * 4;
+           static_cast<int64_t>(2) * tc_grid(c, d, tc_seqs(c, d)) * tc_nq(c, d) * (c->d + 2) * tc_rp(c, d) * 4;
 }
 
 int attn_tc_verify(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a, cudaStream_t s) {
-    return c->d == 64 ? launch_tc<64>(c, d, a, s) : c->d == 128 ? launch_tc<128>(c, d, a, s) : launch_tc<256>(c, d, a, s);
+    const bool pairs = tc_nq(c, d) == 2;
+    if (c->d == 256) return launch_tc<256, 1>(c, d, a, s);
+    if (c->d == 128) return pairs ? launch_tc<128, 2>(c, d, a, s) : launch_tc<128, 1>(c, d, a, s);
+    return pairs ? launch_tc<64, 2>(c, d, a, s) : launch_tc<64, 1>(c, d, a, s);
 }
 
 }  // namespace gdn

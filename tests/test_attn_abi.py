@@ -44,7 +44,7 @@ def test_struct_sizes_match_the_header():
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(page=48), -2), (dict(page=8), -2), (dict(page=256), -2), (dict(d=96), -2), (dict(Hkv=0), -2), (dict(Hkv=257), -2),
+    (dict(page=48), -2), (dict(page=8), -2), (dict(page=256), -2), (dict(d=96), -2), (dict(Hkv=0), -2), (dict(Hkv=129), -2),
     (dict(n_page=0), -2), (dict(max_pages=0), -2), (dict(max_pages=(1 << 18) + 1), -2), (dict(n_layer=0), -2),
     (dict(n_slot=-1), -2), (dict(n_page=1 << 27), -2), (dict(dtype=2), -3)])
 def test_bad_cache_refused(kw, code):
