@@ -70,7 +70,8 @@ template <int D, int NQ> struct TcPlan {
 struct TcArgs {
     AttnArgs a;
     int b0, nb;                 // sequences [b0, b0 + nb) of the call
-    int row_tiles, rp;          // row tiles of a key head; rows of a partial result (a multiple of 32)
+    int tpt, row_tiles;         // tokens of a row tile (128 / G), row tiles of a key head
+    int rp;                     // rows of a partial result (a multiple of 32)
     int2 *desc;                 // per row tile: 2 (first CTA) + its place in the unit, and the last CTA
     float *part;                // [2 CTAs][NQ][D + 2][rp]
 };
@@ -120,6 +121,12 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t one;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
     return one != 0;
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(saddr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(saddr(bar))
+        : "memory");
 }
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
@@ -172,8 +179,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // rows get zeros).  Work is counted in row tiles times tiles of keys: a pair's tile counts 2.
 struct Shape {
     int live, dead, pairs, single, tiles, total;    // total: keys
-    __device__ Shape(int len, int n, int G, int row_tiles, int nq) {
-        live = (n * G + kRows - 1) / kRows;
+    __device__ Shape(int len, int n, int tpt, int row_tiles, int nq) {
+        live = (n + tpt - 1) / tpt;
         dead = row_tiles - live;
         pairs = nq == 2 ? live / 2 : 0;
         single = live - 2 * pairs;
@@ -207,8 +214,8 @@ struct Segment {
 };
 
 // The unit that holds work item w, and the tile of it.
-__device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int G, int row_tiles, int nq, Segment &s) {
-    const Shape sh(st.len[b], st.n[b], G, row_tiles, nq);
+__device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int tpt, int row_tiles, int nq, Segment &s) {
+    const Shape sh(st.len[b], st.n[b], tpt, row_tiles, nq);
     const int in_b = w - st.prefix[b], per = sh.per_head(), tiles = sh.tiles;
     s.b = b;
     s.slot = st.slot[b];
@@ -245,11 +252,11 @@ __device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int G, 
 // first item.
 struct Cut {
     int W, N, q, r;                                 // W = q N + r
-    __device__ int start(const SeqTable &st, int c, int G, int row_tiles, int nq) const {
+    __device__ int start(const SeqTable &st, int c, int tpt, int row_tiles, int nq) const {
         int w = q * c + r * c / N;                  // r c < N^2
         if (nq == 2 && c > 0 && c < N) {
             Segment s;
-            locate(st, st.find(w), w, G, row_tiles, nq, s);
+            locate(st, st.find(w), w, tpt, row_tiles, nq, s);
             w = s.unit_w + s.first * s.nq;
         }
         return w;
@@ -259,10 +266,10 @@ struct Cut {
 // Walks a CTA's share [w, w1) unit by unit.
 struct Cursor {
     int w, w1, b;
-    __device__ bool next(const SeqTable &st, int G, int row_tiles, int nq, Segment &s) {
+    __device__ bool next(const SeqTable &st, int tpt, int row_tiles, int nq, Segment &s) {
         if (w >= w1) return false;
         while (st.prefix[b + 1] <= w) ++b;
-        locate(st, b, w, G, row_tiles, nq, s);
+        locate(st, b, w, tpt, row_tiles, nq, s);
         s.count = min((w1 - w) >> (s.nq - 1), s.tiles - s.first);
         w += s.count * s.nq;
         return true;
@@ -272,7 +279,8 @@ struct Cursor {
 // ------------------------------------------------------------------ the kernel
 template <int D, int NQ>
 __global__ void __launch_bounds__(TcPlan<D, NQ>::THREADS, 1)
-verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TcArgs ta)
+verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const TcArgs ta)
 {
     using P = TcPlan<D, NQ>;
     constexpr int NG = P::NG;
@@ -292,21 +300,22 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     st.nb = ta.nb;
     float *xch = reinterpret_cast<float *>(smem_raw + P::OFF_XCH);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem_raw + P::OFF_BAR);
-    uint64_t *full = bar, *empty = bar + P::NST, *q_full = bar + 2 * P::NST;
-    uint64_t *s_full = q_full + 1, *p_full = s_full + 2 * NG, *o_done = p_full + 2 * NG, *drain = o_done + 2 * NG;   // [group][2]; drain [group]
+    uint64_t *full = bar, *empty = bar + P::NST, *q_full = bar + 2 * P::NST, *q_empty = q_full + 1;
+    uint64_t *s_full = q_empty + 1, *p_full = s_full + 2 * NG, *o_done = p_full + 2 * NG, *drain = o_done + 2 * NG;   // [group][2]; drain [group]
     unsigned long long *odd = reinterpret_cast<unsigned long long *>(drain + NG);         // [group][2]
     int *warp_sum = reinterpret_cast<int *>(odd + 2 * NG);                                // [warps]
     Cut *cut = reinterpret_cast<Cut *>(warp_sum + P::THREADS / 32);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cut + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((2 * P::NST + 1 + 9 * NG + P::THREADS / 32) * 8 + sizeof(Cut) + 8 <= 640, "barrier area");
+    static_assert((2 * P::NST + 2 + 9 * NG + P::THREADS / 32) * 8 + sizeof(Cut) + 8 <= 640, "barrier area");
 
     if (tid == 0) {
         for (int i = 0; i < P::NST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], NG);               // a commit of each group, or two of the only one that reads it
         }
-        mbar_init(q_full, P::ROWS);
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, NG);
         for (int i = 0; i < 2 * NG; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], kGroupThreads);
@@ -319,8 +328,9 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     if (warp == P::LOAD_WARP) {
         tmem_alloc(tmem_slot, P::TMEM_COLS);
-        if (lane < 2)
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tm_v : &tm_k)) : "memory");
+        if (lane < 3)
+            asm volatile("prefetch.tensormap [%0];"
+                         ::"l"(reinterpret_cast<uint64_t>(lane == 0 ? &tm_k : lane == 1 ? &tm_v : &tm_q)) : "memory");
     }
     pdl_wait();
     pdl_release();
@@ -331,11 +341,15 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         int mine = 0;
         if (i < ta.nb) {
             const Seq q = load_seq(a.s, ta.b0 + i);
-            if (!q.bad) mine = Shape(q.len, q.n, a.G, ta.row_tiles, NQ).per_head() * a.s.Hkv;
-            else if (blockIdx.x == 0) atomicOr(a.s.status, q.bad);
+            if (!q.bad) mine = Shape(q.len, q.n, ta.tpt, ta.row_tiles, NQ).per_head() * a.s.Hkv;
             st.slot[i] = q.slot;
             st.len[i] = q.len;
             st.n[i] = q.n;
+            if (q.bad && blockIdx.x == 0) {         // none of its row tiles is for the join
+                atomicOr(a.s.status, q.bad);
+                const int per = a.s.Hkv * ta.row_tiles;
+                for (int u = 0; u < per; ++u) ta.desc[static_cast<size_t>(ta.b0 + i) * per + u] = make_int2(0, -1);
+            }
         }
         int incl = mine;
 #pragma unroll
@@ -346,7 +360,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (i0 > 0) __syncthreads();                // the sums of the round before have been read
         if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-        for (int w = 0; w < P::THREADS / 32; ++w) {
+        const int warps = min(P::THREADS / 32, (ta.nb - i0 + 31) / 32);
+        for (int w = 0; w < warps; ++w) {
             if (w == warp && i < ta.nb) st.prefix[i] = before + incl - mine;
             before += warp_sum[w];
         }
@@ -365,8 +380,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t tmem = *tmem_slot;
     Cursor cur{0, 0, 0};
     if (static_cast<int>(blockIdx.x) < cut->N) {
-        cur.w = cut->start(st, blockIdx.x, a.G, ta.row_tiles, NQ);
-        cur.w1 = cut->start(st, blockIdx.x + 1, a.G, ta.row_tiles, NQ);
+        cur.w = cut->start(st, blockIdx.x, ta.tpt, ta.row_tiles, NQ);
+        cur.w1 = cut->start(st, blockIdx.x + 1, ta.tpt, ta.row_tiles, NQ);
         cur.b = st.find(cur.w);
     }
     // GDN_FLAG_TEST_EXPIRE: the wait-expiry exit, with nothing issued before it
@@ -393,6 +408,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     Segment s;
     uint32_t pos = 0;                               // load warps: tiles loaded (of keys, or of values)
     bool issued = false;                            // MMA warps: some MMA
+    uint32_t queries = 0;                           // first MMA warp: loads of queries
     if (warp >= P::LOAD_WARP && warp < P::MMA_WARP) {
         // ------------------------------------------------------ loads
         // The first warp loads the tiles of keys, the second those of values: a copy for each page of
@@ -403,7 +419,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const int ps = shift < 6 ? shift : 6;                              // rows of a copy: 16, 32 or 64
         const CUtensorMap *map = kv ? &tm_v : &tm_k;
         bool ok = !*abort;
-        while (ok && cur.next(st, a.G, ta.row_tiles, NQ, s)) {
+        while (ok && cur.next(st, ta.tpt, ta.row_tiles, NQ, s)) {
             const int32_t *tab = a.s.table + static_cast<size_t>(s.slot) * a.s.max_pages;
             const int count = __shfl_sync(0xffffffffu, s.count, 0), first = __shfl_sync(0xffffffffu, s.first, 0);
             const int total = __shfl_sync(0xffffffffu, s.total, 0), head = __shfl_sync(0xffffffffu, s.h, 0);
@@ -463,22 +479,37 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         uint64_t *sf = s_full + 2 * group, *pf = p_full + 2 * group, *od = o_done + 2 * group;
         uint32_t g = 0, tile0 = 0, segs = 0;        // this group's tiles, the CTA's tiles and segments so far
         bool ok = !*abort;
-        while (ok && cur.next(st, a.G, ta.row_tiles, NQ, s)) {
+        while (ok && cur.next(st, ta.tpt, ta.row_tiles, NQ, s)) {
             const bool alternate = NG == 2 && s.nq == 1;
             const int step = alternate ? 2 : 1, off = alternate ? (group ^ tile0) & 1 : 0;
             const int count = __shfl_sync(0xffffffffu, (s.count - off + step - 1) / step, 0);
             const bool twice = __shfl_sync(0xffffffffu, alternate ? 1 : 0, 0) != 0;
             const uint64_t dq = desc_sw128(saddr(sQ) + (s.nq == 2 ? group * P::QTILE : 0));
-            ok = __all_sync(0xffffffffu, wait(q_full, segs++ & 1)) != 0;
+            if (group == 0) {                       // the unit's queries, once the unit's before are done with
+                if (segs > 0) ok = __all_sync(0xffffffffu, wait(q_empty, (segs - 1) & 1)) != 0;
+                const int nq = __shfl_sync(0xffffffffu, s.nq, 0), y = __shfl_sync(0xffffffffu, s.h, 0) * a.G;
+                const int z = (ta.b0 + __shfl_sync(0xffffffffu, s.b, 0)) * a.s.T + __shfl_sync(0xffffffffu, s.rt, 0) * ta.tpt;
+                if (ok && elect_one()) {
+                    mbar_expect_tx(q_full, nq * P::ATOMS * ta.tpt * a.G * 128);
+                    for (int q = 0; q < nq; ++q)
+                        for (int x = 0; x < P::ATOMS; ++x)
+                            tma_load_3d(sQ + q * P::QTILE + x * (kRows * 128), &tm_q, x * 64, y, z + q * ta.tpt, q_full);
+                }
+                __syncwarp();
+                queries += ok;
+            }
+            ok = ok && __all_sync(0xffffffffu, wait(q_full, segs & 1)) != 0;
+            ++segs;
+            if (ok && count == 0 && elect_one()) mbar_arrive(q_empty);
             int sn = 0, pn = 0;                     // next tile to score, next to multiply with the values
             uint32_t idle = 0;
             while (ok && pn < count) {
                 bool did = false;
                 if (sn < count && sn < pn + 2) {
-                    // the buffer held the weights of tile sn - 2: their product must be done
+                    // the buffer held the weights of the group's tile t - 2: their product must be done
                     const uint32_t t = g + sn, kpos = 2 * (tile0 + sn * step + off), stage = kpos % P::NST;
                     const bool ready = mbar_test(&full[stage], (kpos / P::NST) & 1) &&
-                                       (sn < 2 || mbar_test(&od[t & 1], ((t - 2) >> 1) & 1));
+                                       (t < 2 || mbar_test(&od[t & 1], ((t - 2) >> 1) & 1));
                     if (__all_sync(0xffffffffu, ready)) {
                         tc_fence_after();
                         const uint64_t dk = desc_add(dk0, stage * P::STAGE);
@@ -492,6 +523,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                             mma_commit(&sf[t & 1]);
                             mma_commit(&empty[stage]);
                             if (twice) mma_commit(&empty[stage]);
+                            if (sn + 1 == count) mma_commit(q_empty);
                         }
                         issued = did = true;
                         ++sn;
@@ -542,31 +574,14 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             __syncwarp();
             tc_fence_after();
         };
-        while (cur.next(st, a.G, ta.row_tiles, NQ, s)) {
+        while (cur.next(st, ta.tpt, ta.row_tiles, NQ, s)) {
             const bool alternate = NG == 2 && s.nq == 1;
             const int step = alternate ? 2 : 1, off = alternate ? (group ^ tile0) & 1 : 0;
-            const int rt = s.rt + (s.nq == 2 ? group : 0), r0 = rt * kRows, rows = a.s.T * a.G;
+            const int rt = s.rt + (s.nq == 2 ? group : 0), per_tile = ta.tpt * a.G;
             const int b = ta.b0 + s.b;
-            if (NG == 2) bar_sync(1, P::ROWS);      // both groups have left the queries and the exchange words
-            {                                       // the unit's queries, rows not in use zero
-                constexpr int VECS = D / 8;
-                const int vecs = s.nq * kRows * VECS;
-#pragma unroll 4
-                for (int x = tid; x < vecs; x += P::ROWS) {
-                    const int q = x / (kRows * VECS), r = x / VECS % kRows, c = x % VECS;
-                    const int row = (s.rt + q) * kRows + r, t = row / a.G, qh = row - t * a.G;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < rows && t < s.n)
-                        v = __ldg(reinterpret_cast<const uint4 *>(
-                                      static_cast<const __nv_bfloat16 *>(a.q) +
-                                      ((static_cast<size_t>(b) * a.s.T + t) * a.Hq + s.h * a.G + qh) * D) + c);
-                    *reinterpret_cast<uint4 *>(sQ + q * P::QTILE + (c >> 3) * (kRows * 128) + sw128(r, c & 7)) = v;
-                }
-                fence_proxy_async();
-                mbar_arrive(q_full);
-            }
-            const int row = r0 + r_in, t = row / a.G;
-            const bool used = row < rows && t < s.n;
+            if (NG == 2) bar_sync(1, P::ROWS);      // both groups have left each other's O and exchange words
+            const int t = rt * ta.tpt + r_in / a.G, qh = r_in % a.G;       // draft token, head of the group
+            const bool exists = r_in < per_tile && t < a.s.T, used = exists && t < s.n;
             const bool warp_live = __any_sync(0xffffffffu, used);
             const uint64_t bits = used ? row_tree(a, b, t, s.n) : 0ull;
             float m = -INFINITY, l = 0.f;           // m: the same in both threads of a row; l: of this thread's keys
@@ -740,14 +755,14 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 m = mn;
             }
             const bool writer = !alternate || mine > 0;                    // a single tile leaves one group without
-            if (writer && __any_sync(0xffffffffu, row < rows)) {
+            if (writer && __any_sync(0xffffffffu, exists)) {
                 const int cols = both ? D / 4 : D / 2, c0 = both ? (2 * group + half) * (D / 4) : half * (D / 2);
                 const uint32_t o_mine = t_lane + 2 * kKeys + c0;
                 const uint32_t o_other = both ? o_mine + (group == 0 ? P::TCOLS : -P::TCOLS) : o_mine;
                 const float inv = !whole ? 1.f : used && (l > 0.f || l != l) ? 1.f / l : 0.f;
                 f0 *= inv;
                 f1 *= inv;
-                const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + s.h * a.G + (row - t * a.G);
+                const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + s.h * a.G + qh;
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c0);
                 float *slot = ta.part + static_cast<size_t>((2 * blockIdx.x + (s.first == 0 ? 1 : 0)) * NQ + (s.nq == 2 ? group : 0)) *
                                             (D + 2) * ta.rp + r_in;
@@ -763,7 +778,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = fmaf(o1[k], f1, o[k]);
                     }
-                    if (row < rows) {
+                    if (exists) {
                         if (whole) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
@@ -782,12 +797,12 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     }
                     __syncwarp();
                 }
-                if (row < rows && c0 == 0) {
+                if (exists && c0 == 0) {
                     if (whole) {
                         if (a.lse) a.lse[orow] = used ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
                     } else {
-                        slot[static_cast<size_t>(D) * ta.rp] = m;
-                        slot[static_cast<size_t>(D + 1) * ta.rp] = l;
+                        slot[static_cast<size_t>(D) * ta.rp] = used ? m : -INFINITY;
+                        slot[static_cast<size_t>(D + 1) * ta.rp] = used ? l : 0.f;
                     }
                 }
             }
@@ -804,9 +819,12 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 const uint32_t k = 2 * t + warp - P::LOAD_WARP;
                 if (!mbar_wait(&full[k % P::NST], (k / P::NST) & 1) && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
             }
-        } else if (warp >= P::MMA_WARP && issued) {
-            if (elect_one()) mma_commit(&drain[warp - P::MMA_WARP]);
-            if (!mbar_wait(&drain[warp - P::MMA_WARP], 0)) atomicOr(a.s.status, GDN_STATUS_DRAIN);
+        } else if (warp >= P::MMA_WARP) {
+            if (issued) {
+                if (elect_one()) mma_commit(&drain[warp - P::MMA_WARP]);
+                if (!mbar_wait(&drain[warp - P::MMA_WARP], 0)) atomicOr(a.s.status, GDN_STATUS_DRAIN);
+            }
+            if (queries > 0 && !mbar_wait(q_full, (queries - 1) & 1)) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
         __syncwarp();
         tc_fence_before();
@@ -816,9 +834,9 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 }
 
 // ------------------------------------------------------------------- the join
-// A task is 32 rows (a lane each) and 8 output columns of a unit; `wide` warps (a power of two,
+// A task is 32 rows (a lane each) and 8 output columns of a row tile; `wide` warps (a power of two,
 // about one for every four parts) take its parts in turn, and the first of them joins their
-// sums in a fixed order.  gridDim.y CTAs share a unit's tasks.
+// sums in a fixed order.  gridDim.y CTAs share a row tile's tasks.
 constexpr int kJoinWarps = 16;
 
 template <int D, int NQ>
@@ -831,24 +849,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) verify_tc_join_kernel(const T
     __shared__ float sums[kJoinWarps][10][32];
     pdl_wait();
     pdl_release();
-    const int2 d = ta.desc[(static_cast<size_t>(b) * a.s.Hkv + h) * ta.row_tiles + rt];
-    const Seq sq = load_seq(a.s, b);
+    const int2 d = ta.desc[static_cast<size_t>(ta.b0) * a.s.Hkv * ta.row_tiles + blockIdx.x];
     const int cta = d.x >> 1, place = d.x & 1, parts = d.y - cta + 1;
-    if (sq.bad || parts < 2 || cta < 0 || place >= NQ || d.y >= grid) return;      // finished by one CTA
+    if (parts < 2 || cta < 0 || place >= NQ || d.y >= grid) return;      // finished by one CTA, or skipped
     int wide = 1;
     while (wide < kJoinWarps && wide * 4 < parts) wide *= 2;
     const int at_once = kJoinWarps / wide, mine = warp / wide, sub = warp % wide;
-    const int rows = a.s.T * a.G, groups = min(ta.rp, rows - rt * kRows + 31) / 32, tasks = groups * (D / 8);
+    const int per_tile = ta.tpt * a.G, rows = min(per_tile, (a.s.T - rt * ta.tpt) * a.G);
+    const int tasks = (rows + 31) / 32 * (D / 8);
     for (int t0 = blockIdx.y * at_once; t0 < tasks; t0 += gridDim.y * at_once) {
         const int task = t0 + mine, r = task / (D / 8) * 32 + lane, c0 = task % (D / 8) * 8;
-        const int row = rt * kRows + r, t = row / a.G;
-        const bool used = task < tasks && row < rows && t < sq.n;
+        const bool exists = task < tasks && r < rows;
         float m = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-        if (used) {
+        if (exists) {
 #pragma unroll 4
-            for (int k = sub; k < parts; k += wide) {                      // part 0: the first CTA's second slot
+            for (int k = sub; k < parts; k += wide) {                    // part 0: the first CTA's second slot
                 const float *p = ta.part + static_cast<size_t>((2 * (cta + k) + (k == 0 ? 1 : 0)) * NQ + place) * (D + 2) * ta.rp + r;
                 const float mk = p[static_cast<size_t>(D) * ta.rp], lk = p[static_cast<size_t>(D + 1) * ta.rp];
                 float x[8];
@@ -880,9 +897,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) verify_tc_join_kernel(const T
             }
             __syncthreads();
         }
-        if (sub != 0 || task >= tasks || row >= rows) continue;
-        const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + h * a.G + (row - t * a.G);
-        const bool any = used && (l > 0.f || l != l);
+        if (sub != 0 || !exists) continue;
+        const int t = rt * ta.tpt + r / a.G;
+        const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + h * a.G + r % a.G;
+        const bool any = l > 0.f || l != l;                              // rows not in use: l = 0 in every part
         const float inv = any ? 1.f / l : 0.f;
         uint32_t w[4];
 #pragma unroll
@@ -891,7 +909,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) verify_tc_join_kernel(const T
             w[e] = any ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
         }
         *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c0) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (a.lse && c0 == 0) a.lse[orow] = used ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (a.lse && c0 == 0) a.lse[orow] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
 }
 
@@ -907,12 +925,27 @@ bool page_map(CUtensorMap *m, const void *base, const gdn_page_cache *c) {
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// The queries as [B T][Hq][d]; boxes of a row tile's tokens and a key head's queries.
+bool query_map(CUtensorMap *m, const void *base, const gdn_page_cache *c, const gdn_attn_dims *d) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const int G = d->Hq / c->Hkv;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(d->Hq),
+                          static_cast<cuuint64_t>(d->B) * d->T};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(c->d) * 2, static_cast<cuuint64_t>(c->d) * 2 * d->Hq};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(kRows / G)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+int tc_tokens(const gdn_page_cache *c, const gdn_attn_dims *d) { return kRows / (d->Hq / c->Hkv); }
 int tc_row_tiles(const gdn_page_cache *c, const gdn_attn_dims *d) {
-    return (d->T * (d->Hq / c->Hkv) + kRows - 1) / kRows;
+    return (d->T + tc_tokens(c, d) - 1) / tc_tokens(c, d);
 }
 int tc_rp(const gdn_page_cache *c, const gdn_attn_dims *d) {
-    const int rows = d->T * (d->Hq / c->Hkv);
-    return rows >= kRows ? kRows : (rows + 31) / 32 * 32;
+    const int t = d->T < tc_tokens(c, d) ? d->T : tc_tokens(c, d);
+    return (t * (d->Hq / c->Hkv) + 31) / 32 * 32;
 }
 // Row tiles of a unit: pairs where there are any and TMEM has room for two groups.
 int tc_nq(const gdn_page_cache *c, const gdn_attn_dims *d) { return c->d != 256 && tc_row_tiles(c, d) > 1 ? 2 : 1; }
@@ -930,9 +963,9 @@ int tc_grid(const gdn_page_cache *c, const gdn_attn_dims *d, int nb) {
     const int sms = sm_count();
     return static_cast<int>(all < sms ? all : sms);
 }
-// CTAs that share a unit's tasks in the join: two per SM in all, at most one per task.
+// CTAs that share a row tile's tasks in the join: two per SM in all, at most one per task.
 int join_ctas(int units, int tasks) {
-    const int want = (2 * sm_count() + units - 1) / units;
+    const int want = 2 * sm_count() / units;
     return want < 1 ? 1 : want > tasks ? tasks : want;
 }
 size_t desc_bytes(const gdn_page_cache *c, const gdn_attn_dims *d) {
@@ -942,17 +975,17 @@ size_t desc_bytes(const gdn_page_cache *c, const gdn_attn_dims *d) {
 template <int D, int NQ>
 int launch_tc(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a, cudaStream_t s) {
     using P = TcPlan<D, NQ>;
-    CUtensorMap mk, mv;
-    if (!page_map(&mk, a.k, c) || !page_map(&mv, a.v, c)) return GDN_ERR_LAUNCH;
+    CUtensorMap mq, mk, mv;
+    if (!query_map(&mq, a.q, c, d) || !page_map(&mk, a.k, c) || !page_map(&mv, a.v, c)) return GDN_ERR_LAUNCH;
     if (cudaFuncSetAttribute(verify_tc_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    TcArgs ta{a, 0, 0, tc_row_tiles(c, d), tc_rp(c, d), reinterpret_cast<int2 *>(a.ws),
+    TcArgs ta{a, 0, 0, tc_tokens(c, d), tc_row_tiles(c, d), tc_rp(c, d), reinterpret_cast<int2 *>(a.ws),
               reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + desc_bytes(c, d))};
     const int step = tc_seqs(c, d);
     for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += step) {
         ta.nb = d->B - ta.b0 < step ? d->B - ta.b0 : step;
         const int grid = tc_grid(c, d, ta.nb), units = ta.nb * c->Hkv * ta.row_tiles;
-        if (launch_pdl(verify_tc_kernel<D, NQ>, dim3(grid), dim3(P::THREADS), P::BYTES, s, mk, mv, ta) != cudaSuccess ||
+        if (launch_pdl(verify_tc_kernel<D, NQ>, dim3(grid), dim3(P::THREADS), P::BYTES, s, mq, mk, mv, ta) != cudaSuccess ||
             launch_pdl(verify_tc_join_kernel<D, NQ>, dim3(units, join_ctas(units, ta.rp / 32 * (D / 8))),
                        dim3(kJoinWarps * 32), 0, s, ta, grid) != cudaSuccess)
             return GDN_ERR_LAUNCH;
