@@ -100,7 +100,7 @@ typedef struct {
  * fp32, rounded once to dtype.
  *   q [B, T, Hq, d], k, v [B, T, Hkv, d] dtype (token strides in gdn_rope_dims; 16-byte
  *   aligned);  q_weight, k_weight fp32 [d];  cos_sin fp32 [max_pos, rot]: rot/2 cosines,
- *   then rot/2 sines (may be NULL when rot is 0);  pos int32 [B, T] rotation positions, NULL =
+ *   then rot/2 sines (NULL when rot is 0), these three 16-byte aligned;  pos int32 [B, T] rotation positions, NULL =
  *   seq_len + t;  q_out dtype [B, T, Hq, d] dense.
  * GDN_STATUS_BAD_SLOT, _BAD_LEN (seq_len or draft_len out of range) and _NO_ROOM (seq_len +
  * draft_len > max_pages * page): the sequence is skipped, q_out included; _BAD_POS: the
@@ -132,16 +132,16 @@ int gdn_tree_build(const gdn_page_cache *cache, const gdn_attn_dims *dims, const
  * rows hold (NaN and infinity included) has no effect.  The draft's keys and values are
  * read from the cache (gdn_attn_stage).
  *   q, out dtype [B, T, Hq, d] (16-byte aligned);  lse fp32 [B, T, Hq] or NULL;
- *   tree uint64 [B, T] or NULL;  workspace: gdn_attn_workspace() bytes, 16-byte aligned, no
- *   initial content; calls that overlap on the GPU need one each.
+ *   tree uint64 [B, T] or NULL;  workspace: workspace_bytes >= gdn_attn_workspace() bytes, 16-byte
+ *   aligned, no initial content; calls that overlap on the GPU need one each.
  * GDN_STATUS_BAD_SLOT, _BAD_LEN, _NO_ROOM as in gdn_attn_stage: the sequence's out and lse are
  * left unwritten; _BAD_PAGE: the sequence's out and lse are unspecified; _TIMEOUT, _DRAIN as in
  * gdnreplay.h: no output of the call may be trusted.
  */
 int gdn_attn_verify(const gdn_page_cache *cache, int32_t layer, const gdn_attn_dims *dims,
                     const int32_t *state_idx, const int32_t *draft_len, const void *q,
-                    const uint64_t *tree, void *out, float *lse, void *workspace, int32_t *status,
-                    cudaStream_t stream);
+                    const uint64_t *tree, void *out, float *lse, void *workspace,
+                    int64_t workspace_bytes, int32_t *status, cudaStream_t stream);
 
 /* Bytes of workspace that gdn_attn_verify needs for these dims on the current device, or a
  * negative GDN_ERR_* code. */

@@ -126,7 +126,7 @@ def load(rebuild: bool = False) -> ctypes.CDLL:
         C, A, R = ctypes.POINTER(PageDims), ctypes.POINTER(AttnDims), ctypes.POINTER(RopeDims)
         lib.gdn_attn_stage.argtypes = [C, I, A, R] + [P] * 12
         lib.gdn_tree_build.argtypes = [C, A] + [P] * 7
-        lib.gdn_attn_verify.argtypes = [C, I, A] + [P] * 9
+        lib.gdn_attn_verify.argtypes = [C, I, A] + [P] * 7 + [ctypes.c_int64, P, P]
         lib.gdn_attn_workspace.argtypes = [C, A]
         lib.gdn_attn_workspace.restype = ctypes.c_int64
         lib.gdn_attn_accept.argtypes = [C, I, I] + [P] * 6
@@ -441,20 +441,20 @@ def gdn_gated_rmsnorm_fp8(o, z, weight, eps: float, inv_scale: float, q, stream=
 
 
 # ------------------------------------------ attention layers: paged cache and drafts
-def _raw_stream(stream):
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+_I32, _F32 = torch.int32, torch.float32
+
+# The current stream's handle without the Stream object that torch.cuda.current_stream()
+# makes (3 us a call against 0.1); the object is the way where torch lacks the function.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _in(t, dtype, n, name):
     """Address of a dense device tensor of dtype that holds at least n elements."""
-    p = _ptr(t, dtype, name)
-    if t.numel() < n:
-        raise ValueError(f"{name}: needs at least {n} elements, got {t.numel()}")
-    return p
-
-
-def _opt(t, dtype, n, name):
-    return None if t is None else _in(t, dtype, n, name)
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    _ptr(t, dtype, name)                                # says what is wrong
+    raise ValueError(f"{name}: needs at least {n} elements, got {t.numel()}")
 
 
 class PagedCache:
@@ -493,8 +493,9 @@ class PagedCache:
             setattr(self.d, f, _ptr(x, t if f in "kv" else torch.int32, f) or None)
             self._t[f] = x
         self._c = ctypes.byref(self.d)
-        self.status = torch.zeros(1, dtype=torch.int32, device=self._t["k"].device)
-        self._status = self.status.data_ptr()
+        dev = self._t["k"].device
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._status, self._index = self.status.data_ptr(), dev.index
         self._lib = load()
 
     def __getattr__(self, name):
@@ -502,38 +503,51 @@ class PagedCache:
             return self._t[name]
         raise AttributeError(name)
 
+    def _stream(self, stream):
+        return _current_raw_stream(self._index) if stream is None else stream.cuda_stream
+
     def reserve(self, slots, extra: int, stream=None):
         """Room for ``extra`` tokens past seq_len in each of ``slots`` (int32)."""
         n = slots.numel()
-        _check("gdn_pages_reserve", self._lib.gdn_pages_reserve(
-            self._c, n, _in(slots, torch.int32, n, "slots"), extra, self._status, _raw_stream(stream)))
+        rc = self._lib.gdn_pages_reserve(self._c, n, _in(slots, _I32, n, "slots"), extra, self._status,
+                                         self._stream(stream))
+        if rc:
+            raise GdnError("gdn_pages_reserve", rc)
 
     def fork(self, src, dst, copies, stream=None):
         """Sequences ``dst`` become copies of ``src`` (int32 slots): full pages shared, the
         last page's rows copied in every layer.  ``copies`` int32 [n, 2] receives those pages."""
-        n, s = src.numel(), _raw_stream(stream)
-        c = _in(copies, torch.int32, 2 * n, "copies")
-        _check("gdn_pages_fork", self._lib.gdn_pages_fork(
-            self._c, n, _in(src, torch.int32, n, "src"), _in(dst, torch.int32, n, "dst"), c, self._status, s))
-        _check("gdn_pages_copy", self._lib.gdn_pages_copy(self._c, n, c, self._status, s))
+        n, s = src.numel(), self._stream(stream)
+        c = _in(copies, _I32, 2 * n, "copies")
+        rc = self._lib.gdn_pages_fork(self._c, n, _in(src, _I32, n, "src"), _in(dst, _I32, n, "dst"), c,
+                                      self._status, s)
+        if rc:
+            raise GdnError("gdn_pages_fork", rc)
+        rc = self._lib.gdn_pages_copy(self._c, n, c, self._status, s)
+        if rc:
+            raise GdnError("gdn_pages_copy", rc)
 
     def release(self, slots, stream=None):
         """The pages of ``slots`` (int32) go back, as far as no other sequence holds them."""
         n = slots.numel()
-        _check("gdn_pages_release", self._lib.gdn_pages_release(
-            self._c, n, _in(slots, torch.int32, n, "slots"), self._status, _raw_stream(stream)))
+        rc = self._lib.gdn_pages_release(self._c, n, _in(slots, _I32, n, "slots"), self._status,
+                                         self._stream(stream))
+        if rc:
+            raise GdnError("gdn_pages_release", rc)
 
     def accept(self, accepted, path=None, state_idx=None, new_len=None, stream=None):
         """Commit accepted[b] drafted tokens of each sequence: along ``path`` (int32 [B, T]),
         whose rows move to the front of the draft's in every layer, or, without one, the first
         accepted[b].  The lengths go to ``new_len`` (seq_len when None)."""
-        i32, B = torch.int32, accepted.numel()
+        B = accepted.numel()
         T = 64 if path is None else path.shape[-1]
-        _check("gdn_attn_accept", self._lib.gdn_attn_accept(
-            self._c, B, T, _opt(state_idx, i32, B, "state_idx"), _opt(path, i32, B * T, "path"),
-            _in(accepted, i32, B, "accepted"),
-            self.d.seq_len if new_len is None else _in(new_len, i32, self.d.n_slot, "new_len"),
-            self._status, _raw_stream(stream)))
+        rc = self._lib.gdn_attn_accept(
+            self._c, B, T, None if state_idx is None else _in(state_idx, _I32, B, "state_idx"),
+            None if path is None else _in(path, _I32, B * T, "path"), _in(accepted, _I32, B, "accepted"),
+            self.d.seq_len if new_len is None else _in(new_len, _I32, self.d.n_slot, "new_len"),
+            self._status, self._stream(stream))
+        if rc:
+            raise GdnError("gdn_attn_accept", rc)
 
 
 class AttnLayer:
@@ -547,72 +561,93 @@ class AttnLayer:
 
     def __init__(self, dims: AttnDims, cache: PagedCache, layer: int, rope: RopeDims | None = None,
                  q_weight=None, k_weight=None, cos_sin=None, state_idx=None, workspace=None):
-        c, f32 = cache.d, torch.float32
-        self.d, self.cache, self.layer, self.status = dims, cache, layer, cache.status
-        self.rope = rope
+        c = cache.d
+        self._d, self.cache, self.layer, self.status = AttnDims.from_buffer_copy(dims), cache, layer, cache.status
+        self._rope = None if rope is None else RopeDims.from_buffer_copy(rope)
+        self._ref = ctypes.byref(self._d)
         dev = cache.status.device
-        need = cache._lib.gdn_attn_workspace(cache._c, ctypes.byref(dims)) if dims.T <= 64 else 0
+        need = cache._lib.gdn_attn_workspace(cache._c, self._ref) if dims.T <= 64 else 0
         _check("gdn_attn_workspace", min(need, 0))
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         self.workspace, self.state_idx = workspace, state_idx
         self._keep = (q_weight, k_weight, cos_sin)
-        self._ws = _in(workspace, torch.uint8, need, "workspace") or None
-        self._idx = _opt(state_idx, torch.int32, dims.B, "state_idx")
+        self._ws, self._ws_bytes = _in(workspace, torch.uint8, need, "workspace") or None, workspace.numel()
+        self._idx = None if state_idx is None else _in(state_idx, _I32, dims.B, "state_idx")
         if rope is not None:
-            self._w = (_in(q_weight, f32, c.d, "q_weight"), _in(k_weight, f32, c.d, "k_weight"),
-                       _opt(cos_sin, f32, rope.max_pos * rope.rot, "cos_sin"))
+            self._w = (_in(q_weight, _F32, c.d, "q_weight"), _in(k_weight, _F32, c.d, "k_weight"),
+                       None if cos_sin is None else _in(cos_sin, _F32, rope.max_pos * rope.rot, "cos_sin"))
+        self._dtype, self._stream, self._lib = _TORCH_IN[c.dtype], cache._stream, cache._lib
+
+    @property
+    def d(self):
+        """A copy of the layer's dims."""
+        return AttnDims.from_buffer_copy(self._d)
 
     def _block(self, t, heads, name):
         """Address and token stride of q, k or v: [B, T, heads, d], dense within a token, the
         tokens evenly spaced."""
-        d, c = self.d, self.cache.d
-        if t.dim() != 4 or t.shape != (d.B, d.T, heads, c.d):
-            raise ValueError(f"{name}: expected shape {(d.B, d.T, heads, c.d)}, got {tuple(t.shape)}")
+        d, n = self._d, self.cache.d.d
+        B, T = d.B, d.T
+        if tuple(t.shape) != (B, T, heads, n):
+            raise ValueError(f"{name}: expected shape {(B, T, heads, n)}, got {tuple(t.shape)}")
         if not t.is_cuda:
             raise ValueError(f"{name}: expected a CUDA tensor")
-        if t.dtype != _TORCH_IN[c.dtype]:
-            raise TypeError(f"{name}: expected {_TORCH_IN[c.dtype]}, got {t.dtype}")
+        if t.dtype is not self._dtype:
+            raise TypeError(f"{name}: expected {self._dtype}, got {t.dtype}")
         sb, st, sh, se = t.stride()
-        if se != 1 or (heads > 1 and sh != c.d):
+        if se != 1 or (heads > 1 and sh != n):
             raise ValueError(f"{name}: the heads of a token must be dense")
-        if d.T == 1:
-            st = sb if d.B > 1 else max(heads * c.d, st)
-        elif d.B > 1 and sb != d.T * st:
+        if T == 1:
+            st = sb if B > 1 else max(heads * n, st)
+        elif B > 1 and sb != T * st:
             raise ValueError(f"{name}: tokens must be evenly spaced over the batch")
         return t.data_ptr(), st
 
     def stage(self, q, k, v, q_out, pos=None, draft_len=None, stream=None):
         """Norm and rotate q [B, T, Hq, d] into ``q_out`` and k [B, T, Hkv, d] into the cache's
         draft rows, v beside it.  q, k and v may be views of one projection's output."""
-        d, c, i32 = self.d, self.cache.d, torch.int32
-        if self.rope is None:
+        d, c, r = self._d, self.cache.d, self._rope
+        if r is None:
             raise ValueError("stage: this layer was made without rope and norm weights")
-        r = RopeDims.from_buffer_copy(self.rope)
+        r = RopeDims(r.rot, r.style, r.max_pos, r.eps)
         pq, r.q_stride = self._block(q, d.Hq, "q")
         pk, r.k_stride = self._block(k, c.Hkv, "k")
         pv, r.v_stride = self._block(v, c.Hkv, "v")
         n = d.B * d.T
-        _check("gdn_attn_stage", self.cache._lib.gdn_attn_stage(
-            self.cache._c, self.layer, ctypes.byref(d), ctypes.byref(r), self._idx,
-            _opt(draft_len, i32, d.B, "draft_len"), pq, pk, pv, _opt(pos, i32, n, "pos"), *self._w,
-            _in(q_out, _TORCH_IN[c.dtype], n * d.Hq * c.d, "q_out"), self.cache._status, _raw_stream(stream)))
+        wq, wk, tab = self._w
+        rc = self._lib.gdn_attn_stage(
+            self.cache._c, self.layer, self._ref, ctypes.byref(r), self._idx,
+            None if draft_len is None else _in(draft_len, _I32, d.B, "draft_len"), pq, pk, pv,
+            None if pos is None else _in(pos, _I32, n, "pos"), wq, wk, tab,
+            _in(q_out, self._dtype, n * d.Hq * c.d, "q_out"), self.cache._status, self._stream(stream))
+        if rc:
+            raise GdnError("gdn_attn_stage", rc)
 
     def build_tree(self, parent, tree, pos=None, draft_len=None, stream=None):
         """Ancestor words ``tree`` (int64 [B, T]) and rotation positions ``pos`` (int32 [B, T])
         of a token tree given by its parents (int32 [B, T])."""
-        d, i32, n = self.d, torch.int32, self.d.B * self.d.T
-        _check("gdn_tree_build", self.cache._lib.gdn_tree_build(
-            self.cache._c, ctypes.byref(d), self._idx, _opt(draft_len, i32, d.B, "draft_len"),
-            _in(parent, i32, n, "parent"), _in(tree, torch.int64, n, "tree"), _opt(pos, i32, n, "pos"),
-            self.cache._status, _raw_stream(stream)))
+        d, n = self._d, self.d.B * self.d.T
+        rc = self._lib.gdn_tree_build(
+            self.cache._c, self._ref, self._idx,
+            None if draft_len is None else _in(draft_len, _I32, d.B, "draft_len"),
+            _in(parent, _I32, n, "parent"), _in(tree, torch.int64, n, "tree"),
+            None if pos is None else _in(pos, _I32, n, "pos"), self.cache._status, self._stream(stream))
+        if rc:
+            raise GdnError("gdn_tree_build", rc)
 
     def verify(self, q, out, lse=None, tree=None, draft_len=None, stream=None):
         """Attention of the block's rows q [B, T, Hq, d] over the cache into ``out`` (and
         ``lse`` fp32 [B, T, Hq]); ``tree`` int64 [B, T] ancestor words, None: a chain."""
-        d, c = self.d, self.cache.d
-        n, t = d.B * d.T, _TORCH_IN[c.dtype]
-        _check("gdn_attn_verify", self.cache._lib.gdn_attn_verify(
-            self.cache._c, self.layer, ctypes.byref(d), self._idx, _opt(draft_len, torch.int32, d.B, "draft_len"),
-            _in(q, t, n * d.Hq * c.d, "q"), _opt(tree, torch.int64, n, "tree"), _in(out, t, n * d.Hq * c.d, "out"),
-            _opt(lse, torch.float32, n * d.Hq, "lse"), self._ws, self.cache._status, _raw_stream(stream)))
+        d, t = self._d, self._dtype
+        n = d.B * d.T
+        h = n * d.Hq
+        e = h * self.cache.d.d
+        rc = self._lib.gdn_attn_verify(
+            self.cache._c, self.layer, self._ref, self._idx,
+            None if draft_len is None else _in(draft_len, _I32, d.B, "draft_len"), _in(q, t, e, "q"),
+            None if tree is None else _in(tree, torch.int64, n, "tree"), _in(out, t, e, "out"),
+            None if lse is None else _in(lse, _F32, h, "lse"), self._ws, self._ws_bytes,
+            self.cache._status, self._stream(stream))
+        if rc:
+            raise GdnError("gdn_attn_verify", rc)

@@ -11,48 +11,6 @@
 namespace gdn {
 namespace {
 
-// ------------------------------------------------------------ rows of 8 elements
-// Eight consecutive elements of a row per lane: 16 bytes of bf16, 32 of fp32.
-template <typename T> struct Vec8;
-template <> struct Vec8<__nv_bfloat16> {
-    struct Raw { uint4 x; };
-    __device__ static Raw load(const __nv_bfloat16 *p) { return Raw{*reinterpret_cast<const uint4 *>(p)}; }
-    __device__ static void store(__nv_bfloat16 *p, const Raw &r) { *reinterpret_cast<uint4 *>(p) = r.x; }
-    __device__ static void unpack(const Raw &r, float (&f)[8]) {
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r.x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = __bfloat1622float2(h[i]);
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
-        }
-    }
-    __device__ static Raw pack(const float (&f)[8]) {
-        Raw r;
-        __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&r.x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        return r;
-    }
-};
-template <> struct Vec8<float> {
-    struct Raw { float4 a, b; };
-    __device__ static Raw load(const float *p) {
-        return Raw{reinterpret_cast<const float4 *>(p)[0], reinterpret_cast<const float4 *>(p)[1]};
-    }
-    __device__ static void store(float *p, const Raw &r) {
-        reinterpret_cast<float4 *>(p)[0] = r.a;
-        reinterpret_cast<float4 *>(p)[1] = r.b;
-    }
-    __device__ static void unpack(const Raw &r, float (&f)[8]) {
-        f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
-        f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
-    }
-    __device__ static Raw pack(const float (&f)[8]) {
-        return Raw{make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7])};
-    }
-};
-
 // ------------------------------------------------ norm + rotation + staging
 struct StageArgs {
     SeqArgs s;
@@ -67,110 +25,181 @@ struct StageArgs {
 
 constexpr int kStageThreads = 256;
 
-// One CTA per token; D / 8 lanes per row (head of q, k or v), eight elements a lane, so
-// every load and store is a whole 16-byte vector and a row's sum of squares is a few
-// shuffles.  Pairs (i, i + rot/2) lie rot/16 lanes apart: one shuffle per element.
-template <typename T, int D>
+// Four consecutive elements, twice per lane.
+template <typename T> struct Vec4;
+template <> struct Vec4<__nv_bfloat16> {
+    using Raw = uint2;
+    __device__ static void unpack(const uint2 &r, float (&f)[4]) {
+        f[0] = __uint_as_float(r.x << 16);
+        f[1] = __uint_as_float(r.x & 0xffff0000u);
+        f[2] = __uint_as_float(r.y << 16);
+        f[3] = __uint_as_float(r.y & 0xffff0000u);
+    }
+    __device__ static uint2 pack(const float (&f)[4]) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+        return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+};
+template <> struct Vec4<float> {
+    using Raw = uint4;
+    __device__ static void unpack(const uint4 &r, float (&f)[4]) {
+        f[0] = __uint_as_float(r.x);
+        f[1] = __uint_as_float(r.y);
+        f[2] = __uint_as_float(r.z);
+        f[3] = __uint_as_float(r.w);
+    }
+    __device__ static uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+
+// y = x r w of one row (eight elements per lane, L lanes), the rotated pairs turned.
+template <int D>
+__device__ __forceinline__ void norm_turn(float (&x)[8], const float *w, int a, int b, float eps, bool turned, bool half,
+                                          const float (&cs)[4], const float (&sn)[4])
+{
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int off = D / 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const float inv = 1.f / sqrtf(ss / D + eps);
+    const float4 wa = *reinterpret_cast<const float4 *>(w + a), wb = *reinterpret_cast<const float4 *>(w + b);
+    const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wv[e];
+    if (turned) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float &u = half ? x[e] : x[2 * e], &z = half ? x[4 + e] : x[2 * e + 1];
+            const float u0 = u, z0 = z;
+            u = u0 * cs[e] - z0 * sn[e];
+            z = z0 * cs[e] + u0 * sn[e];
+        }
+    }
+}
+
+// One CTA per token; D / 8 lanes per row (head of q, k or v).  A lane holds elements [a, a + 4) and
+// [b, b + 4) of its row: with b = a + rot / 2 among the rotated dims of the half style, so that the
+// pairs meet in one lane (turning them by shuffles cost eight more per row); elsewhere b = a + 4.
+// Bound by HBM at prompt lengths (by latency at a decode step's): NR rows per lane are requested before
+// the chain slot -> length -> page, and the rotation's row, are waited for.
+template <typename T, int D, bool HALF, int NR>
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
 {
     constexpr int L = D / 8, GROUPS = kStageThreads / L;
-    using V = Vec8<T>;
+    using V = Vec4<T>;
+    using Raw = typename V::Raw;
     const int tok = blockIdx.x, b = tok / a.s.T, t = tok - b * a.s.T;
     const int c = threadIdx.x % L, grp = threadIdx.x / L;
+    const int rows = a.Hq + 2 * a.s.Hkv;
+    const bool turned = 8 * c < a.rot;
+    const int ea = HALF && turned ? 4 * c : 8 * c, eb = HALF && turned ? 4 * c + a.rot / 2 : 8 * c + 4;
     pdl_wait();
     pdl_release();
-    const Seq sq = load_seq(a.s, b);
-    if (sq.bad) {
-        if (t == 0 && threadIdx.x == 0) atomicOr(a.s.status, sq.bad);
+    const int n = a.s.draft_len ? a.s.draft_len[b] : a.s.T;
+    const int slot = a.s.state_idx ? a.s.state_idx[b] : b;
+    const bool in_use = t < n && n <= a.s.T;
+    int p = in_use && a.pos ? a.pos[tok] : 0;
+    auto source = [&](int r) {
+        const T *base = r < a.Hq ? static_cast<const T *>(a.q) + static_cast<size_t>(tok) * a.q_stride + r * D
+                        : r < a.Hq + a.s.Hkv
+                            ? static_cast<const T *>(a.k) + static_cast<size_t>(tok) * a.k_stride + (r - a.Hq) * D
+                            : static_cast<const T *>(a.v) + static_cast<size_t>(tok) * a.v_stride + (r - a.Hq - a.s.Hkv) * D;
+        return base;
+    };
+    Raw ra[NR], rb[NR];
+    auto request = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int r = r0 + i * GROUPS + grp;
+            ra[i] = Raw{};
+            rb[i] = Raw{};
+            if (in_use && r < rows) {
+                const T *src = source(r);
+                ra[i] = __ldcs(reinterpret_cast<const Raw *>(src + ea));
+                rb[i] = __ldcs(reinterpret_cast<const Raw *>(src + eb));
+            }
+        }
+    };
+    request(0);
+    int len = 0, bad = 0;
+    if (slot < 0 || slot >= a.s.n_slot) bad = GDN_STATUS_BAD_SLOT;
+    else {
+        const int room = a.s.max_pages << a.s.page_shift;
+        len = a.s.seq_len[slot];
+        if (len < 0 || len > room || n < 0 || n > a.s.T) bad = GDN_STATUS_BAD_LEN;
+        else if (len + n > room) bad = GDN_STATUS_NO_ROOM;
+    }
+    if (bad) {
+        if (t == 0 && threadIdx.x == 0) atomicOr(a.s.status, bad);
         return;
     }
-    bool live = t < sq.n;
-    int p = 0;
+    bool live = in_use;
     if (live) {
-        p = a.pos ? a.pos[tok] : sq.len + t;
+        if (!a.pos) p = len + t;
         if (p < 0 || p >= a.max_pos) {
             if (threadIdx.x == 0) atomicOr(a.s.status, GDN_STATUS_BAD_POS);
             live = false;
         }
     }
     long long row0 = -1;                                          // cache row of head 0
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
     if (live) {
-        const int at = sq.len + t, page = 1 << a.s.page_shift;
-        const int id = a.s.table[static_cast<size_t>(sq.slot) * a.s.max_pages + (at >> a.s.page_shift)];
+        const int at = len + t, page = 1 << a.s.page_shift;
+        const int id = a.s.table[static_cast<size_t>(slot) * a.s.max_pages + (at >> a.s.page_shift)];
+        if (turned) {
+            const float *tab = a.cos_sin + static_cast<size_t>(p) * a.rot + 4 * c;
+            const float4 u = *reinterpret_cast<const float4 *>(tab);
+            const float4 w = *reinterpret_cast<const float4 *>(tab + a.rot / 2);
+            cs[0] = u.x; cs[1] = u.y; cs[2] = u.z; cs[3] = u.w;
+            sn[0] = w.x; sn[1] = w.y; sn[2] = w.z; sn[3] = w.w;
+        }
         if (id >= 0 && id < a.s.n_page) row0 = static_cast<long long>(id) * a.s.Hkv * page + (at & (page - 1));
         else if (threadIdx.x == 0) atomicOr(a.s.status, GDN_STATUS_BAD_PAGE);
     }
-    const int half = a.rot / 16;                                  // lanes of half the rotated dims
-    const bool turned = c < 2 * half;
-    float cs[8], sn[8];
-    if (live && turned) {
-        const float *tab = a.cos_sin + static_cast<size_t>(p) * a.rot;
+    for (int r0 = 0; r0 < rows; r0 += NR * GROUPS) {              // the same for the whole CTA
+        if (r0 > 0) request(r0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = a.style == GDN_ROPE_HALF ? (c < half ? c : c - half) * 8 + i : c * 4 + i / 2;
-            cs[i] = tab[j];
-            sn[i] = tab[a.rot / 2 + j];
-        }
-    }
-    const int rows = a.Hq + 2 * a.s.Hkv;
-    const int rounds = (rows + GROUPS - 1) / GROUPS;              // uniform: the shuffles take whole warps
-    for (int i = 0; i < rounds; ++i) {
-        const int r = i * GROUPS + grp;
-        const bool in = r < rows;
-        const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.s.Hkv;
-        T *dst = nullptr;
-        const T *src = nullptr;
-        if (in) {
+        for (int i = 0; i < NR; ++i) {
+            const int r = r0 + i * GROUPS + grp;
+            const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.s.Hkv;
+            Raw ya = ra[i], yb = rb[i];
+            if (__any_sync(0xffffffffu, !is_v && live)) {         // (whole warps: a row's lanes shuffle)
+                float xa[4], xb[4], x[8];
+                V::unpack(ya, xa);
+                V::unpack(yb, xb);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = xa[e], x[4 + e] = xb[e];
+                norm_turn<D>(x, is_q ? a.qw : a.kw, ea, eb, a.eps, turned, HALF, cs, sn);
+                if (!is_v) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) xa[e] = x[e], xb[e] = x[4 + e];
+                    ya = V::pack(xa);
+                    yb = V::pack(xb);
+                }
+            }
+            if (r >= rows) continue;
+            T *dst;
             if (is_q) {
-                src = static_cast<const T *>(a.q) + static_cast<size_t>(tok) * a.q_stride + r * D;
                 dst = static_cast<T *>(a.q_out) + (static_cast<size_t>(tok) * a.Hq + r) * D;
+                if (!live) ya = Raw{}, yb = Raw{};                // a query row not in use
             } else {
+                if (row0 < 0) continue;
                 const int h = is_v ? r - a.Hq - a.s.Hkv : r - a.Hq;
-                src = is_v ? static_cast<const T *>(a.v) + static_cast<size_t>(tok) * a.v_stride + h * D
-                           : static_cast<const T *>(a.k) + static_cast<size_t>(tok) * a.k_stride + h * D;
-                if (row0 >= 0) {
-                    const size_t row = static_cast<size_t>(row0) + (static_cast<size_t>(h) << a.s.page_shift);
-                    dst = static_cast<T *>(is_v ? a.vc : a.kc) + row * D;
-                }
+                dst = static_cast<T *>(is_v ? a.vc : a.kc) + (row0 + (static_cast<long long>(h) << a.s.page_shift)) * D;
             }
+            *reinterpret_cast<Raw *>(dst + ea) = ya;
+            *reinterpret_cast<Raw *>(dst + eb) = yb;
         }
-        typename V::Raw raw = {};
-        if (in && live) raw = V::load(src + c * 8);
-        float x[8];
-        V::unpack(raw, x);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        const float inv = 1.f / sqrtf(ss / D + a.eps);
-        const float *w = is_q ? a.qw : a.kw;
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e] * inv * w[c * 8 + e];
-        if (a.rot > 0) {
-            if (a.style == GDN_ROPE_HALF) {
-                const int lane = threadIdx.x & 31;
-                const int other = lane - c + (c < half ? c + half : turned ? c - half : c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float z = __shfl_sync(0xffffffffu, y[e], other);
-                    if (turned) y[e] = c < half ? y[e] * cs[e] - z * sn[e] : y[e] * cs[e] + z * sn[e];
-                }
-            } else if (turned) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float u = y[e], z = y[e + 1];
-                    y[e] = u * cs[e] - z * sn[e];
-                    y[e + 1] = z * cs[e] + u * sn[e];
-                }
-            }
-        }
-        if (!dst) continue;
-        if (is_v) V::store(dst + c * 8, raw);
-        else if (live) V::store(dst + c * 8, V::pack(y));
-        else V::store(dst + c * 8, typename V::Raw{});            // a query row not in use
     }
+}
+
+template <typename T, int D>
+cudaError_t launch_stage(const StageArgs &a, dim3 grid, cudaStream_t s) {
+    constexpr int NR = D == 256 ? 3 : 2;
+    return a.style == GDN_ROPE_HALF ? launch_pdl(stage_kernel<T, D, true, NR>, grid, dim3(kStageThreads), 0, s, a)
+                                    : launch_pdl(stage_kernel<T, D, false, NR>, grid, dim3(kStageThreads), 0, s, a);
 }
 
 // -------------------------------------------------------------- token trees
@@ -229,28 +258,43 @@ __global__ void __launch_bounds__(128) tree_kernel(const SeqArgs s, const int32_
 }
 
 // ------------------------------------------- verify on CUDA cores (fp32 caches)
+// The mathematics of gdn_attn_tc.cu's verify in fp32 throughout (the tensor cores have no fp32
+// product).  One CTA per (row tile, split of the keys, key head, sequence); key and value
+// tiles of 32 tokens arrive by cp.async, the next pair while the present one is used.  A warp owns
+// 8 rows: their scores (2 rows x 4 keys a lane), their running maximum and denominator, and their
+// D output columns, so the only barriers are those around the tiles.  Products go two at a time
+// (fma.rn.f32x2).  Bound by shared-memory reads (16 of 16 bytes for 128 products) from
+// some 16 rows per key head on, by HBM and latency below.
 constexpr int kRT = 32, kKT = 32;               // rows and keys of a tile
 constexpr int kCoreThreads = 128;
 
 template <int D> struct CorePlan {
     static constexpr int STR = D + 4;           // padded row: lanes of a warp read 8 rows without conflicts
-    static constexpr int BYTES = (kRT * STR + kKT * STR + kKT * D + kRT * (kKT + 4)) * 4;
+    static constexpr int PSTR = kKT + 4;
+    static constexpr int TILE = kKT * STR + kKT * D;              // keys, then values
+    static constexpr int BYTES = (kRT * STR + 2 * TILE + kRT * PSTR) * 4;
+    static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 2 : 1;   // per SM
+    static_assert(CTAS * (BYTES + 1024) <= 228 * 1024, "shared memory");
 };
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool valid) {      // zeros when not valid
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Partial results in the workspace: [unit][split][kRT] rows of D sums, the maximum (in
 // powers of two) and the denominator; unit = (b Hkv + h) row tiles + row tile.
 template <int D> __host__ __device__ constexpr int part_floats() { return D + 2; }
 
-// One CTA per (row tile, split of the keys, key head, sequence).  A warp owns 8 rows: their
-// scores (2 rows x 4 keys a lane), their running maximum and denominator, and their
-// D output columns (D / 32 a lane), so the only barriers are those around the shared
-// key and value tiles.
 template <int D>
-__global__ void __launch_bounds__(kCoreThreads) verify_core_kernel(const AttnArgs a, int row_tiles)
+__global__ void __launch_bounds__(kCoreThreads, CorePlan<D>::CTAS) verify_core_kernel(const AttnArgs a, int row_tiles)
 {
     using P = CorePlan<D>;
+    constexpr int VECS = D / 4;
     extern __shared__ __align__(16) float sm[];
-    float *sQ = sm, *sK = sQ + kRT * P::STR, *sV = sK + kKT * P::STR, *sP = sV + kKT * D;
+    float *sQ = sm, *tiles_s = sQ + kRT * P::STR, *sP = tiles_s + 2 * P::TILE;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles, h = blockIdx.y, b = blockIdx.z;
     pdl_wait();
@@ -260,159 +304,190 @@ __global__ void __launch_bounds__(kCoreThreads) verify_core_kernel(const AttnArg
         if (blockIdx.x == 0 && h == 0 && tid == 0) atomicOr(a.s.status, sq.bad);
         return;
     }
-    const int rows = a.s.T * a.G, r0 = rt * kRT;
-    const int total = sq.len + sq.n, tiles = (total + kKT - 1) / kKT;
-    const int j_beg = static_cast<int>(static_cast<long long>(tiles) * split / a.splits) * kKT;
-    const int j_end = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / a.splits) * kKT;
-    for (int i = tid; i < kRT * D; i += kCoreThreads) {           // queries, scaled
-        const int r = r0 + i / D, col = i % D;
-        float x = 0.f;
-        if (r < rows && r / a.G < sq.n) {
-            const size_t at = ((static_cast<size_t>(b) * a.s.T + r / a.G) * a.Hq + h * a.G + r % a.G) * D + col;
-            x = static_cast<const float *>(a.q)[at] * a.scale_log2;
+    const int rows = a.s.T * a.G, r0 = rt * kRT, live_rows = sq.n * a.G;
+    const int total = r0 < live_rows ? sq.len + sq.n : 0, tiles = (total + kKT - 1) / kKT;   // no keys without rows in use
+    const int t_beg = static_cast<int>(static_cast<long long>(tiles) * split / a.splits);
+    const int t_end = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / a.splits);
+    const int page = 1 << a.s.page_shift;
+    const int32_t *tab = a.s.table + static_cast<size_t>(sq.slot) * a.s.max_pages;
+    auto request = [&](int tile) {                                // tile's keys and values on their way
+        float *sK = tiles_s + (tile & 1) * P::TILE, *sV = sK + kKT * P::STR;
+#pragma unroll 4
+        for (int i = tid; i < kKT * VECS; i += kCoreThreads) {
+            const int j = i / VECS, c = i % VECS, at = tile * kKT + j;
+            size_t row = 0;
+            if (at < total) {
+                int id = __ldg(tab + (at >> a.s.page_shift));
+                if (id < 0 || id >= a.s.n_page) {
+                    if (c == 0) atomicOr(a.s.status, GDN_STATUS_BAD_PAGE);
+                    id = 0;
+                }
+                row = ((static_cast<size_t>(id) * a.s.Hkv + h) << a.s.page_shift) + (at & (page - 1));
+            }
+            cp_async16(sK + j * P::STR + 4 * c, static_cast<const float *>(a.k) + row * D + 4 * c, at < total);
+            cp_async16(sV + j * D + 4 * c, static_cast<const float *>(a.v) + row * D + 4 * c, at < total);
         }
-        sQ[(i / D) * P::STR + col] = x;
+    };
+    if (t_beg < t_end) request(t_beg);
+#pragma unroll 4
+    for (int i = tid; i < kRT * VECS; i += kCoreThreads) {
+        const int r = i / VECS, c = i % VECS, row = r0 + r, t = row / a.G;
+        const bool valid = row < live_rows;
+        const size_t at = valid ? ((static_cast<size_t>(b) * a.s.T + t) * a.Hq + h * a.G + row % a.G) * D + 4 * c : 0;
+        cp_async16(sQ + r * P::STR + 4 * c, static_cast<const float *>(a.q) + at, valid);
     }
-    constexpr int C = D / 32;                                     // output columns per lane
-    float acc[8][C], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    cp_async_commit();
+    constexpr int C = D / 64;                                     // pairs of output columns per lane: 2 lane + 64 i
+    float2 acc[8][C];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < 8; ++r)
 #pragma unroll
-        for (int i = 0; i < C; ++i) acc[r][i] = 0.f;
+        for (int i = 0; i < C; ++i) acc[r][i] = make_float2(0.f, 0.f);
     const int lr = lane >> 3, lk = lane & 7;                      // rows 8 warp + 2 lr + {0, 1}, keys lk + 8 i
+    const bool warp_live = r0 + 8 * warp < live_rows;
     uint64_t bits[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int t = (r0 + 8 * warp + 2 * lr + i) / a.G;
-        bits[i] = t < sq.n ? row_tree(a, b, t, sq.n) : 0ull;
-    }
     bool used[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) used[i] = (r0 + 8 * warp + 2 * lr + i) / a.G < sq.n;
-    const int page = 1 << a.s.page_shift;
-    for (int j0 = j_beg; j0 < j_end; j0 += kKT) {
+    for (int i = 0; i < 2; ++i) {
+        const int row = r0 + 8 * warp + 2 * lr + i;
+        used[i] = row < live_rows;
+        bits[i] = used[i] ? row_tree(a, b, row / a.G, sq.n) : 0ull;
+    }
+    for (int tile = t_beg; tile < t_end; ++tile) {
+        if (tile + 1 < t_end) request(tile + 1);
+        cp_async_commit();
+        cp_async_wait<1>();
         __syncthreads();
-        for (int i = tid; i < kKT * D / 8; i += kCoreThreads) {
-            const int j = i / (D / 8), c8 = i % (D / 8), at = j0 + j;
-            float fk[8], fv[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) fk[e] = fv[e] = 0.f;
-            if (at < total) {
-                const int id = a.s.table[static_cast<size_t>(sq.slot) * a.s.max_pages + (at >> a.s.page_shift)];
-                if (id >= 0 && id < a.s.n_page) {
-                    const size_t row = ((static_cast<size_t>(id) * a.s.Hkv + h) << a.s.page_shift) + (at & (page - 1));
-                    Vec8<float>::unpack(Vec8<float>::load(static_cast<const float *>(a.k) + row * D + c8 * 8), fk);
-                    Vec8<float>::unpack(Vec8<float>::load(static_cast<const float *>(a.v) + row * D + c8 * 8), fv);
-                } else if (c8 == 0) {
-                    atomicOr(a.s.status, GDN_STATUS_BAD_PAGE);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sK[j * P::STR + c8 * 8 + e] = fk[e];
-                sV[j * D + c8 * 8 + e] = fv[e];
-            }
-        }
-        __syncthreads();
-        float s[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D; c += 4) {
-            float4 q4[2], k4[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) q4[i] = *reinterpret_cast<const float4 *>(sQ + (8 * warp + 2 * lr + i) * P::STR + c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) k4[k] = *reinterpret_cast<const float4 *>(sK + (lk + 8 * k) * P::STR + c);
+        const float *sK = tiles_s + (tile & 1) * P::TILE, *sV = sK + kKT * P::STR;
+        const int j0 = tile * kKT;
+        const bool edge = j0 + kKT > sq.len;                      // some tokens may be unseen
+        if (warp_live) {
+            float2 s2[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
+                for (int k = 0; k < 4; ++k) s2[i][k] = make_float2(0.f, 0.f);
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                float4 q4[2], k4[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) q4[i] = *reinterpret_cast<const float4 *>(sQ + (8 * warp + 2 * lr + i) * P::STR + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) k4[k] = *reinterpret_cast<const float4 *>(sK + (lk + 8 * k) * P::STR + c);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        s2[i][k] = fma2(make_float2(q4[i].x, q4[i].y), make_float2(k4[k].x, k4[k].y), s2[i][k]);
+                        s2[i][k] = fma2(make_float2(q4[i].z, q4[i].w), make_float2(k4[k].z, k4[k].w), s2[i][k]);
+                    }
+            }
+            // unseen keys: -infinity before the maximum, and -1 in place of their weight, so that
+            // their values are passed over below whatever they hold
+            float fac[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                bool seen[4];
+                float s[4], top = -INFINITY;
+#pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    s[i][k] = fmaf(q4[i].x, k4[k].x, s[i][k]);
-                    s[i][k] = fmaf(q4[i].y, k4[k].y, s[i][k]);
-                    s[i][k] = fmaf(q4[i].z, k4[k].z, s[i][k]);
-                    s[i][k] = fmaf(q4[i].w, k4[k].w, s[i][k]);
+                    const int u = j0 + lk + 8 * k - sq.len;       // < 0: committed
+                    seen[k] = !edge || (used[i] && (u < 0 || (u < sq.n && ((bits[i] >> u) & 1))));
+                    s[k] = (s2[i][k].x + s2[i][k].y) * a.scale_log2;
+                    if (seen[k]) top = fmaxf(top, s[k]);
                 }
-        }
-        // unseen keys: -infinity before the maximum, and -1 in place of their weight, so that
-        // their values are passed over below whatever they hold
-        float fac[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            bool seen[4];
-            float top = -INFINITY;
+                for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const float mn = fmaxf(m[i], top), ms = mn == -INFINITY ? 0.f : mn;
+                fac[i] = exp2f(m[i] - ms);                        // 0 for the first keys
+                float sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int u = j0 + lk + 8 * k - sq.len;           // < 0: committed
-                seen[k] = used[i] && (u < 0 || (u < sq.n && ((bits[i] >> u) & 1)));
-                if (seen[k]) top = fmaxf(top, s[i][k]);
+                for (int k = 0; k < 4; ++k) {
+                    const float p = exp2f(s[k] - ms);
+                    if (seen[k]) sum += p;
+                    sP[(8 * warp + 2 * lr + i) * P::PSTR + lk + 8 * k] = seen[k] ? p : -1.f;
+                }
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                l[i] = l[i] * fac[i] + sum;
+                m[i] = mn;
             }
-#pragma unroll
-            for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float mn = fmaxf(m[i], top), ms = mn == -INFINITY ? 0.f : mn;
-            fac[i] = exp2f(m[i] - ms);                            // 0 for the first keys
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float p = exp2f(s[i][k] - ms);
-                if (seen[k]) sum += p;
-                sP[(8 * warp + 2 * lr + i) * (kKT + 4) + lk + 8 * k] = seen[k] ? p : -1.f;
-            }
-#pragma unroll
-            for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            l[i] = l[i] * fac[i] + sum;
-            m[i] = mn;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const float f = __shfl_sync(0xffffffffu, fac[r & 1], (r >> 1) * 8);
-#pragma unroll
-            for (int i = 0; i < C; ++i) acc[r][i] *= f;
-        }
-        for (int j = 0; j < kKT; ++j) {
-            float v[C];
-#pragma unroll
-            for (int i = 0; i < C; ++i) v[i] = sV[j * D + lane + 32 * i];
+            __syncwarp();
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                const float p = sP[(8 * warp + r) * (kKT + 4) + j];
-                if (p == -1.f) continue;                          // unseen (warp-uniform)
+                const float f = __shfl_sync(0xffffffffu, fac[r & 1], (r >> 1) * 8);
 #pragma unroll
-                for (int i = 0; i < C; ++i) acc[r][i] = fmaf(p, v[i], acc[r][i]);
+                for (int i = 0; i < C; ++i) acc[r][i] = make_float2(acc[r][i].x * f, acc[r][i].y * f);
+            }
+            const float *pr = sP + 8 * warp * P::PSTR, *vr = sV + 2 * lane;
+            if (!edge) {
+#pragma unroll 2
+                for (int j = 0; j < kKT; j += 4) {
+                    float2 v[4][C];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < C; ++i) v[k][i] = *reinterpret_cast<const float2 *>(vr + (j + k) * D + 64 * i);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float4 p = *reinterpret_cast<const float4 *>(pr + r * P::PSTR + j);
+#pragma unroll
+                        for (int i = 0; i < C; ++i) {
+                            acc[r][i] = fma2(make_float2(p.x, p.x), v[0][i], acc[r][i]);
+                            acc[r][i] = fma2(make_float2(p.y, p.y), v[1][i], acc[r][i]);
+                            acc[r][i] = fma2(make_float2(p.z, p.z), v[2][i], acc[r][i]);
+                            acc[r][i] = fma2(make_float2(p.w, p.w), v[3][i], acc[r][i]);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < kKT; ++j) {
+                    float2 v[C];
+#pragma unroll
+                    for (int i = 0; i < C; ++i) v[i] = *reinterpret_cast<const float2 *>(vr + j * D + 64 * i);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float p = pr[r * P::PSTR + j];
+                        if (p == -1.f) continue;                  // unseen (warp-uniform)
+#pragma unroll
+                        for (int i = 0; i < C; ++i) acc[r][i] = fma2(make_float2(p, p), v[i], acc[r][i]);
+                    }
+                }
             }
         }
-        __syncwarp();
+        __syncthreads();                                          // the tile's place is free
     }
+    cp_async_wait<0>();
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
         const float mm = __shfl_sync(0xffffffffu, m[r & 1], (r >> 1) * 8);
         const float ll = __shfl_sync(0xffffffffu, l[r & 1], (r >> 1) * 8);
         const int row = r0 + 8 * warp + r;
         if (row >= rows) continue;
+        const bool in_use = row < live_rows;
         if (a.splits > 1) {
             const size_t unit = (static_cast<size_t>(b) * a.s.Hkv + h) * row_tiles + rt;
             float *dst = a.ws + ((unit * a.splits + split) * kRT + 8 * warp + r) * part_floats<D>();
 #pragma unroll
-            for (int i = 0; i < C; ++i) dst[lane + 32 * i] = acc[r][i];
-            if (lane == 0) {
-                dst[D] = mm;
-                dst[D + 1] = ll;
-            }
+            for (int i = 0; i < C; ++i) *reinterpret_cast<float2 *>(dst + 2 * lane + 64 * i) = acc[r][i];
+            if (lane == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(in_use ? mm : -INFINITY, in_use ? ll : 0.f);
         } else {
             const size_t orow = (static_cast<size_t>(b) * a.s.T + row / a.G) * a.Hq + h * a.G + row % a.G;
-            const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
+            const bool any = in_use && (ll > 0.f || ll != ll);
+            const float inv = any ? 1.f / ll : 0.f;
 #pragma unroll
-            for (int i = 0; i < C; ++i) static_cast<float *>(a.out)[orow * D + lane + 32 * i] = acc[r][i] * inv;
-            if (a.lse && lane == 0) a.lse[orow] = (mm + log2f(ll)) * 0.69314718055994531f;
+            for (int i = 0; i < C; ++i)
+                *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + orow * D + 2 * lane + 64 * i) =
+                    any ? make_float2(acc[r][i].x * inv, acc[r][i].y * inv) : make_float2(0.f, 0.f);
+            if (a.lse && lane == 0) a.lse[orow] = any ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
         }
     }
 }
 
-// Joins the splits' partial results of a row (a warp): their common maximum, then the
-// weighted sums in the order of the splits.
+// Joins the splits' partial results of a row (a warp): lane k weighs splits k, k + 32, .., then
+// the weighted sums in the order of the splits, eight of them requested at a time.
 template <int D>
 __global__ void __launch_bounds__(128) verify_join_kernel(const AttnArgs a, int row_tiles)
 {
@@ -420,30 +495,50 @@ __global__ void __launch_bounds__(128) verify_join_kernel(const AttnArgs a, int 
     const int row = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
     pdl_wait();
     pdl_release();
-    if (row >= rows || load_seq(a.s, b).bad) return;
+    if (row >= rows) return;
     const size_t unit = (static_cast<size_t>(b) * a.s.Hkv + h) * row_tiles + row / kRT;
     const float *src = a.ws + (unit * a.splits * kRT + row % kRT) * part_floats<D>();
     const size_t step = static_cast<size_t>(kRT) * part_floats<D>();
-    float m = -INFINITY;
-    for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, src[i * step + D]);
+    if (load_seq(a.s, b).bad) return;
+    float w[4], m = -INFINITY, l = 0.f;                           // at most 128 splits
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = lane + 32 * i < a.splits ? src[(lane + 32 * i) * step + D] : -INFINITY;
+        m = fmaxf(m, w[i]);
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     const float ms = m == -INFINITY ? 0.f : m;
-    constexpr int C = D / 32;
-    float acc[C], l = 0.f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = 0.f;
-    for (int k = 0; k < a.splits; ++k) {
-        const float f = exp2f(src[k * step + D] - ms);
-        l = fmaf(f, src[k * step + D + 1], l);
+    for (int i = 0; i < 4; ++i) {
+        w[i] = exp2f(w[i] - ms);                                  // 0 past the splits
+        if (lane + 32 * i < a.splits) l = fmaf(w[i], src[(lane + 32 * i) * step + D + 1], l);
+    }
 #pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] = fmaf(f, src[k * step + lane + 32 * i], acc[i]);
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    constexpr int C = D / 64;
+    float2 acc[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k0 = 0; k0 < 128; k0 += 32) {
+        if (k0 >= a.splits) break;
+#pragma unroll 8
+        for (int k = 0; k < min(32, a.splits - k0); ++k) {
+            const float f = __shfl_sync(0xffffffffu, w[k0 / 32], k);
+            const float *p = src + (k0 + k) * step + 2 * lane;
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] = fma2(make_float2(f, f), *reinterpret_cast<const float2 *>(p + 64 * i), acc[i]);
+        }
     }
     const size_t orow = (static_cast<size_t>(b) * a.s.T + row / a.G) * a.Hq + h * a.G + row % a.G;
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const bool any = l > 0.f || l != l;                           // rows not in use: l = 0 in every split
+    const float inv = any ? 1.f / l : 0.f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) static_cast<float *>(a.out)[orow * D + lane + 32 * i] = acc[i] * inv;
-    if (a.lse && lane == 0) a.lse[orow] = (m + log2f(l)) * 0.69314718055994531f;
+    for (int i = 0; i < C; ++i)
+        *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + orow * D + 2 * lane + 64 * i) =
+            any ? make_float2(acc[i].x * inv, acc[i].y * inv) : make_float2(0.f, 0.f);
+    if (a.lse && lane == 0) a.lse[orow] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 int core_row_tiles(const gdn_page_cache *c, const gdn_attn_dims *d) {
@@ -456,12 +551,13 @@ int sm_count() {
         return 0;
     return sms;
 }
-// Parts of the key axis: enough CTAs for four per SM, each part at least two tiles of the
-// longest sequence the block table can hold.
+// Parts of the key axis: one wave of CTAs, each part at least two tiles of the longest
+// sequence that the block table can hold.
 int core_splits(const gdn_page_cache *c, const gdn_attn_dims *d) {
+    const int ctas = c->d == 64 ? CorePlan<64>::CTAS : c->d == 128 ? CorePlan<128>::CTAS : CorePlan<256>::CTAS;
     const long long units = static_cast<long long>(d->B) * c->Hkv * core_row_tiles(c, d);
     const long long tiles = (static_cast<long long>(c->max_pages) * c->page + kKT - 1) / kKT;
-    long long want = units > 0 ? (4ll * sm_count() + units - 1) / units : 1;
+    long long want = units > 0 ? static_cast<long long>(ctas) * sm_count() / units : 1;
     if (want > tiles / 2) want = tiles / 2;
     return static_cast<int>(want < 1 ? 1 : want > 128 ? 128 : want);
 }
@@ -595,22 +691,22 @@ int gdn_attn_stage(const gdn_page_cache *c, int32_t layer, const gdn_attn_dims *
         !status || (r->rot > 0 && !cos_sin))
         return GDN_ERR_NULL;
     if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || !aligned_to(q, 16) || !aligned_to(k, 16) ||
-        !aligned_to(v, 16) || !aligned_to(q_out, 16))
+        !aligned_to(v, 16) || !aligned_to(q_out, 16) || !aligned_to(q_weight, 16) || !aligned_to(k_weight, 16) ||
+        !aligned_to(cos_sin, 16))
         return GDN_ERR_DIMS;
     const size_t off = layer_elems(c) * layer * e;
     StageArgs a{seq_args(c, d->B, d->T, state_idx, draft_len, status), q, k, v, pos, q_weight, k_weight, cos_sin,
                 q_out, static_cast<char *>(c->k) + off, static_cast<char *>(c->v) + off, r->q_stride, r->k_stride,
                 r->v_stride, d->Hq, r->rot, r->style, r->max_pos, r->eps};
-    const dim3 grid(d->B * d->T), block(kStageThreads);
+    const dim3 grid(d->B * d->T);
     cudaError_t err;
     if (c->dtype == GDN_DTYPE_BF16)
-        err = c->d == 64 ? launch_pdl(stage_kernel<__nv_bfloat16, 64>, grid, block, 0, stream, a)
-              : c->d == 128 ? launch_pdl(stage_kernel<__nv_bfloat16, 128>, grid, block, 0, stream, a)
-                            : launch_pdl(stage_kernel<__nv_bfloat16, 256>, grid, block, 0, stream, a);
+        err = c->d == 64 ? launch_stage<__nv_bfloat16, 64>(a, grid, stream)
+              : c->d == 128 ? launch_stage<__nv_bfloat16, 128>(a, grid, stream)
+                            : launch_stage<__nv_bfloat16, 256>(a, grid, stream);
     else
-        err = c->d == 64 ? launch_pdl(stage_kernel<float, 64>, grid, block, 0, stream, a)
-              : c->d == 128 ? launch_pdl(stage_kernel<float, 128>, grid, block, 0, stream, a)
-                            : launch_pdl(stage_kernel<float, 256>, grid, block, 0, stream, a);
+        err = c->d == 64 ? launch_stage<float, 64>(a, grid, stream)
+              : c->d == 128 ? launch_stage<float, 128>(a, grid, stream) : launch_stage<float, 256>(a, grid, stream);
     return err == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -637,7 +733,7 @@ int64_t gdn_attn_workspace(const gdn_page_cache *c, const gdn_attn_dims *d)
 
 int gdn_attn_verify(const gdn_page_cache *c, int32_t layer, const gdn_attn_dims *d, const int32_t *state_idx,
                     const int32_t *draft_len, const void *q, const uint64_t *tree, void *out, float *lse,
-                    void *workspace, int32_t *status, cudaStream_t stream)
+                    void *workspace, int64_t workspace_bytes, int32_t *status, cudaStream_t stream)
 {
     const int64_t need = gdn_attn_workspace(c, d);
     if (need < 0) return static_cast<int>(need);
@@ -645,6 +741,7 @@ int gdn_attn_verify(const gdn_page_cache *c, int32_t layer, const gdn_attn_dims 
     if (d->B == 0) return GDN_OK;
     if (!c->k || !c->v || !c->block_table || !c->seq_len || !q || !out || !status || (need > 0 && !workspace))
         return GDN_ERR_NULL;
+    if (workspace_bytes < need) return GDN_ERR_DIMS;
     if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || !aligned_to(q, 16) || !aligned_to(out, 16) ||
         !aligned_to(workspace, 16))
         return GDN_ERR_DIMS;

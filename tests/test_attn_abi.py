@@ -32,10 +32,11 @@ def stage(c=None, a=None, r=None, layer=0, args=None):
     return lib.load().gdn_attn_stage(ctypes.byref(c), layer, ctypes.byref(a), ctypes.byref(r), *(args or [FAKE] * 11), None)
 
 
-def verify(c=None, a=None, layer=0, args=None):
+def verify(c=None, a=None, layer=0, args=None, size=1 << 40):
     c, a = c or cache(), a or dims()
     # state_idx, draft_len, q, tree, out, lse, workspace, status
-    return lib.load().gdn_attn_verify(ctypes.byref(c), layer, ctypes.byref(a), *(args or [FAKE] * 8), None)
+    args = args or [FAKE] * 8
+    return lib.load().gdn_attn_verify(ctypes.byref(c), layer, ctypes.byref(a), *args[:7], size, args[7], None)
 
 
 def test_struct_sizes_match_the_header():
@@ -97,13 +98,17 @@ def test_null_and_misaligned_pointers_refused():
         args = [FAKE] * 8
         args[i] = FAKE + 8
         assert verify(args=args) == -2, i
+    for i in (7, 8, 9):                                       # norm weights, angles
+        args = [FAKE] * 11
+        args[i - 1] = FAKE + 4
+        assert stage(args=args) == -2, i
     for f in ("k", "v", "block_table", "seq_len"):
         assert stage(cache(**{f: None})) == verify(cache(**{f: None})) == -1, f
     for f in ("k", "v"):
         assert stage(cache(**{f: FAKE + 4})) == verify(cache(**{f: FAKE + 4})) == -2, f
     for f in ("block_table", "seq_len", "n_owned", "ref", "free_list", "free_count"):
         assert so.gdn_pages_release(ctypes.byref(cache(**{f: None})), 1, FAKE, FAKE, None) == -1, f
-    assert so.gdn_attn_verify(None, 0, ctypes.byref(dims()), *([FAKE] * 8), None) == -1
+    assert so.gdn_attn_verify(None, 0, ctypes.byref(dims()), *([FAKE] * 7), 1 << 40, FAKE, None) == -1
     assert so.gdn_attn_accept(ctypes.byref(cache()), 2, 4, FAKE, FAKE, None, FAKE, FAKE, None) == -1
     # the identity slot map needs a slot per row
     args = [FAKE] * 8

@@ -271,10 +271,12 @@ def test_verify_wait_expiry(d):
     flight): the status word tells, the device stays usable, the next call is right."""
     lib = _lib()
     r = VerifyRun([100, 700], [4, 4], 4, 8, 2, d, 16, BF, seed=25)
-    r.attn.d.flags = lib.FLAG_TEST_EXPIRE
+    good, dims = r.attn, r.attn.d
+    dims.flags = lib.FLAG_TEST_EXPIRE
+    r.attn = lib.AttnLayer(dims, r.cache, 0, state_idx=r.case.state_idx.cuda())
     r.call()
     assert int(r.cache.status.item()) == lib.STATUS_TIMEOUT
-    r.attn.d.flags = 0
+    r.attn = good
     r.cache.status.zero_()
     r.call()
     r.check()
