@@ -564,7 +564,7 @@ class AttnLayer:
         c = cache.d
         self._d, self.cache, self.layer, self.status = AttnDims.from_buffer_copy(dims), cache, layer, cache.status
         self._rope = None if rope is None else RopeDims.from_buffer_copy(rope)
-        self._ref = ctypes.byref(self._d)
+        self._ref, self._n = ctypes.byref(self._d), c.d
         dev = cache.status.device
         need = cache._lib.gdn_attn_workspace(cache._c, self._ref) if dims.T <= 64 else 0
         _check("gdn_attn_workspace", min(need, 0))
@@ -587,9 +587,8 @@ class AttnLayer:
     def _block(self, t, heads, name):
         """Address and token stride of q, k or v: [B, T, heads, d], dense within a token, the
         tokens evenly spaced."""
-        d, n = self._d, self.cache.d.d
-        B, T = d.B, d.T
-        if tuple(t.shape) != (B, T, heads, n):
+        B, T, n = self._d.B, self._d.T, self._n
+        if t.shape != (B, T, heads, n):
             raise ValueError(f"{name}: expected shape {(B, T, heads, n)}, got {tuple(t.shape)}")
         if not t.is_cuda:
             raise ValueError(f"{name}: expected a CUDA tensor")
@@ -610,7 +609,7 @@ class AttnLayer:
         d, c, r = self._d, self.cache.d, self._rope
         if r is None:
             raise ValueError("stage: this layer was made without rope and norm weights")
-        r = RopeDims(r.rot, r.style, r.max_pos, r.eps)
+        r = RopeDims.from_buffer_copy(r)
         pq, r.q_stride = self._block(q, d.Hq, "q")
         pk, r.k_stride = self._block(k, c.Hkv, "k")
         pv, r.v_stride = self._block(v, c.Hkv, "v")

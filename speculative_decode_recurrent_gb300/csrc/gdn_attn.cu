@@ -23,7 +23,7 @@ struct StageArgs {
     float eps;
 };
 
-constexpr int kStageThreads = 256;
+constexpr int kStageThreads = 128;
 
 // Four consecutive elements, twice per lane.
 template <typename T> struct Vec4;
@@ -58,25 +58,37 @@ template <int D>
 __device__ __forceinline__ void norm_turn(float (&x)[8], const float *w, int a, int b, float eps, bool turned, bool half,
                                           const float (&cs)[4], const float (&sn)[4])
 {
-    float ss = 0.f;
+    float2 y[4], sq = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    for (int e = 0; e < 4; ++e) {
+        y[e] = make_float2(x[2 * e], x[2 * e + 1]);
+        sq = fma2(y[e], y[e], sq);
+    }
+    float ss = sq.x + sq.y;
 #pragma unroll
     for (int off = D / 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    const float inv = 1.f / sqrtf(ss / D + eps);
+    const float r = rsqrtf(ss * (1.f / D) + eps);                 // within 2 ulp
     const float4 wa = *reinterpret_cast<const float4 *>(w + a), wb = *reinterpret_cast<const float4 *>(w + b);
-    const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+    const float2 wv[4] = {make_float2(wa.x, wa.y), make_float2(wa.z, wa.w), make_float2(wb.x, wb.y), make_float2(wb.z, wb.w)};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wv[e];
+    for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], make_float2(r, r)), wv[e]);
     if (turned) {
+        if (half) {                                               // pairs (y[e], y[e + 2])
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float &u = half ? x[e] : x[2 * e], &z = half ? x[4 + e] : x[2 * e + 1];
-            const float u0 = u, z0 = z;
-            u = u0 * cs[e] - z0 * sn[e];
-            z = z0 * cs[e] + u0 * sn[e];
+            for (int e = 0; e < 2; ++e) {
+                const float2 c2 = make_float2(cs[2 * e], cs[2 * e + 1]), s2 = make_float2(sn[2 * e], sn[2 * e + 1]);
+                const float2 u = y[e], z = y[2 + e];
+                y[e] = fma2(u, c2, mul2(z, make_float2(-s2.x, -s2.y)));
+                y[2 + e] = fma2(z, c2, mul2(u, s2));
+            }
+        } else {                                                  // pairs within a word of y
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[e] = make_float2(y[e].x * cs[e] - y[e].y * sn[e], y[e].y * cs[e] + y[e].x * sn[e]);
         }
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[2 * e] = y[e].x, x[2 * e + 1] = y[e].y;
 }
 
 // One CTA per token; D / 8 lanes per row (head of q, k or v).  A lane holds elements [a, a + 4) and
@@ -197,7 +209,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
 
 template <typename T, int D>
 cudaError_t launch_stage(const StageArgs &a, dim3 grid, cudaStream_t s) {
-    constexpr int NR = D == 256 ? 3 : 2;
+    constexpr int NR = D == 256 ? 5 : D == 128 ? 3 : 2;           // 20 rows (16 + 2 + 2 heads) in one round
     return a.style == GDN_ROPE_HALF ? launch_pdl(stage_kernel<T, D, true, NR>, grid, dim3(kStageThreads), 0, s, a)
                                     : launch_pdl(stage_kernel<T, D, false, NR>, grid, dim3(kStageThreads), 0, s, a);
 }

@@ -1,29 +1,39 @@
 // gdn_pages.cu -- the page pool of the attention layers' cache, for sm_103a: pages reserved,
 // shared by forks, copied and released, all on the device.  C ABI: include/gdnattn.h.
 //
-// Each bookkeeping call is one thread-block cluster.  Every CTA makes the same plan (what
-// each row needs, prefix sums over the rows), the pages' entries are spread over the
-// cluster's threads, and the per-row words that the plan was read from (lengths, owned
-// pages, the free count) are written by one CTA after a cluster barrier.  Results do not
-// depend on the order in which threads run.
+// Each bookkeeping call is one CTA, or one thread-block cluster of eight where it may touch many
+// pages' entries (a cluster's barriers cost about a microsecond more per call).  Every CTA
+// makes the same plan (what each row needs, prefix sums over the rows), the pages' entries are
+// spread over the cluster's threads, and the per-row words that the plan was read from
+// (lengths, owned pages, the free count) are written by one CTA after a barrier.  Results do
+// not depend on the order in which threads run.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "attn_common.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 512, kCluster = 8, kMaxRows = GDN_PAGES_MAX_ROWS;
+constexpr int kThreads = 512, kMaxRows = GDN_PAGES_MAX_ROWS;
+constexpr int kManyEntries = 4096;              // entries from which on a cluster is worth its barriers
 
 struct PoolArgs {
     int32_t *table, *seq_len, *n_owned, *ref, *free_list, *free_count, *status;
     int n_slot, max_pages, n_page, page_shift;
 };
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ int cluster_rank() {
+template <int C> __device__ __forceinline__ void cluster_sync() {
+    if constexpr (C == 1) __syncthreads();
+    else {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+}
+template <int C> __device__ __forceinline__ int cluster_rank() {
+    if constexpr (C == 1) return 0;
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return static_cast<int>(r);
@@ -84,11 +94,11 @@ __device__ __forceinline__ int checked_free(const PoolArgs &a) {
     return f < 0 ? 0 : f > a.n_page ? a.n_page : f;
 }
 
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+template <int C> __global__ void __launch_bounds__(kThreads) __cluster_dims__(C, 1, 1)
 reserve_kernel(const PoolArgs a, int n, const int32_t *slots, int extra)
 {
     __shared__ int excl[kMaxRows], sums[kThreads / 32];
-    const int tid = threadIdx.x, rank = cluster_rank();
+    const int tid = threadIdx.x, rank = cluster_rank<C>();
     pdl_wait();
     pdl_release();
     const int free = checked_free(a);
@@ -132,14 +142,13 @@ reserve_kernel(const PoolArgs a, int n, const int32_t *slots, int extra)
         }
         given = excl[lo];                                         // that row did not fit
     }
-    for (int e = rank * kThreads + tid; e < given; e += kCluster * kThreads) {
+    for (int e = rank * kThreads + tid; e < given; e += C * kThreads) {
         const int i = row_of(excl, n, e), slot = slots[i], own = a.n_owned[slot];
         const int id = take_page(a, free, e);
         a.table[static_cast<size_t>(slot) * a.max_pages + own + (e - excl[i])] = id;
         if (id >= 0) a.ref[id] = 1;
     }
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync<C>();
     if (rank == 0) {
         for (int i = tid; i < n; i += kThreads) {
             const int next = i + 1 < n ? excl[i + 1] : total;
@@ -150,12 +159,12 @@ reserve_kernel(const PoolArgs a, int n, const int32_t *slots, int extra)
     }
 }
 
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+template <int C> __global__ void __launch_bounds__(kThreads) __cluster_dims__(C, 1, 1)
 fork_kernel(const PoolArgs a, int n, const int32_t *src, const int32_t *dst, int32_t *copies)
 {
     // of each row: full pages shared before it, and the page it takes (-1: none, -2: skipped)
     __shared__ int excl[kMaxRows], taken[kMaxRows], sums[kThreads / 32];
-    const int tid = threadIdx.x, rank = cluster_rank(), page = 1 << a.page_shift;
+    const int tid = threadIdx.x, rank = cluster_rank<C>(), page = 1 << a.page_shift;
     pdl_wait();
     pdl_release();
     const int free = checked_free(a);
@@ -193,14 +202,14 @@ fork_kernel(const PoolArgs a, int n, const int32_t *src, const int32_t *dst, int
         }
     }
     __syncthreads();
-    for (int e = rank * kThreads + tid; e < shared; e += kCluster * kThreads) {
+    for (int e = rank * kThreads + tid; e < shared; e += C * kThreads) {
         const int i = row_of(excl, n, e), c = e - excl[i];
         const int id = a.table[static_cast<size_t>(src[i]) * a.max_pages + c];
         a.table[static_cast<size_t>(dst[i]) * a.max_pages + c] = id;
         if (id >= 0 && id < a.n_page) atomicAdd(&a.ref[id], 1);
         else atomicOr(a.status, GDN_STATUS_BAD_PAGE);
     }
-    for (int i = rank * kThreads + tid; i < n; i += kCluster * kThreads) {
+    for (int i = rank * kThreads + tid; i < n; i += C * kThreads) {
         int from = -1, to = -1;
         if (taken[i] >= 0) {
             const int full = a.seq_len[src[i]] >> a.page_shift;
@@ -212,8 +221,7 @@ fork_kernel(const PoolArgs a, int n, const int32_t *src, const int32_t *dst, int
         copies[2 * i] = from;
         copies[2 * i + 1] = to;
     }
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync<C>();
     if (rank == 0) {
         for (int i = tid; i < n; i += kThreads) {
             if (taken[i] == -2) continue;
@@ -231,11 +239,11 @@ fork_kernel(const PoolArgs a, int n, const int32_t *src, const int32_t *dst, int
 // more often than shared).
 constexpr int kClaim = -(1 << 30);
 
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+template <int C> __global__ void __launch_bounds__(kThreads) __cluster_dims__(C, 1, 1)
 release_kernel(const PoolArgs a, int n, const int32_t *slots)
 {
     __shared__ int excl[kMaxRows], sums[kThreads / 32], wins;
-    const int tid = threadIdx.x, rank = cluster_rank();
+    const int tid = threadIdx.x, rank = cluster_rank<C>();
     pdl_wait();
     pdl_release();
     const int free = checked_free(a);
@@ -258,8 +266,8 @@ release_kernel(const PoolArgs a, int n, const int32_t *slots)
     }
     __syncthreads();
     // this CTA's entries, in order
-    const int e0 = static_cast<int>(static_cast<long long>(total) * rank / kCluster);
-    const int e1 = static_cast<int>(static_cast<long long>(total) * (rank + 1) / kCluster);
+    const int e0 = static_cast<int>(static_cast<long long>(total) * rank / C);
+    const int e1 = static_cast<int>(static_cast<long long>(total) * (rank + 1) / C);
     auto page_at = [&](int e) {
         const int i = row_of(excl, n, e);
         return a.table[static_cast<size_t>(slots[i]) * a.max_pages + (e - excl[i])];
@@ -269,16 +277,14 @@ release_kernel(const PoolArgs a, int n, const int32_t *slots)
         if (id >= 0 && id < a.n_page) atomicSub(&a.ref[id], 1);
         else bad |= GDN_STATUS_BAD_PAGE;
     }
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync<C>();
     for (int e = e0 + tid; e < e1; e += kThreads) {
         const int id = page_at(e);
         if (id < 0 || id >= a.n_page) continue;
         const int r = *const_cast<volatile int32_t *>(&a.ref[id]);
         if (r == 0 || r <= kClaim) atomicMin(&a.ref[id], kClaim - e);
     }
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync<C>();
     int mine = 0;
     for (int e = e0 + tid; e < e1; e += kThreads) {
         const int id = page_at(e);
@@ -287,11 +293,10 @@ release_kernel(const PoolArgs a, int n, const int32_t *slots)
     int cta;
     block_scan(mine, sums, cta);
     if (tid == 0) wins = cta;
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync<C>();
     int at = free, all = 0;
-    for (int r = 0; r < kCluster; ++r) {
-        const int w = ld_cluster(&wins, r);
+    for (int r = 0; r < C; ++r) {
+        const int w = C == 1 ? wins : ld_cluster(&wins, r);
         if (r < rank) at += w;
         all += w;
     }
@@ -321,8 +326,7 @@ release_kernel(const PoolArgs a, int n, const int32_t *slots)
         at += sum;
     }
     if (bad) atomicOr(a.status, bad);
-    cluster_arrive();                                             // also: every read of `wins` is done
-    cluster_wait();
+    cluster_sync<C>();                                            // also: every read of `wins` is done
     if (rank == 0) {
         for (int i = tid; i < n; i += kThreads) {
             const int next = i + 1 < n ? excl[i + 1] : total;
@@ -351,13 +355,23 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(void *k, void *v, const
     uint4 *base = static_cast<uint4 *>(blockIdx.y & 1 ? v : k) + static_cast<size_t>(blockIdx.y >> 1) * n_page * page_vecs;
     const uint4 *src = base + static_cast<size_t>(from) * page_vecs;
     uint4 *dst = base + static_cast<size_t>(to) * page_vecs;
-    for (int i = threadIdx.x; i < page_vecs; i += 256) dst[i] = src[i];
+    // eight vectors in flight per thread (one: 0.73 of the bandwidth)
+    int i = threadIdx.x;
+    for (; i + 7 * 256 < page_vecs; i += 8 * 256) {
+        uint4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __ldcs(src + i + j * 256);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dst[i + j * 256] = x[j];
+    }
+    for (; i < page_vecs; i += 256) dst[i] = src[i];
 }
 
 int check_pool(const gdn_page_cache *c, int n) {
     if (const int rc = check_cache(c)) return rc;
     return n < 0 || n > kMaxRows ? GDN_ERR_DIMS : GDN_OK;
 }
+bool many(int rows, int pages) { return static_cast<long long>(rows) * pages > kManyEntries; }
 bool has_pool(const gdn_page_cache *c) {
     return c->block_table && c->seq_len && c->n_owned && c->ref && c->free_list && c->free_count;
 }
@@ -380,8 +394,11 @@ int gdn_pages_reserve(const gdn_page_cache *c, int32_t n, const int32_t *slots, 
     if (extra < 0) return GDN_ERR_DIMS;
     if (n == 0) return GDN_OK;
     if (!has_pool(c) || !slots || !status) return GDN_ERR_NULL;
-    return launch_pdl(reserve_kernel, dim3(kCluster), dim3(kThreads), 0, stream, pool_args(c, status), n, slots,
-                      extra) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    const int pages = std::min(c->max_pages, extra / c->page + 2);                          // most that a row takes
+    const cudaError_t err = many(n, pages)
+        ? launch_pdl(reserve_kernel<8>, dim3(8), dim3(kThreads), 0, stream, pool_args(c, status), n, slots, extra)
+        : launch_pdl(reserve_kernel<1>, dim3(1), dim3(kThreads), 0, stream, pool_args(c, status), n, slots, extra);
+    return err == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 int gdn_pages_fork(const gdn_page_cache *c, int32_t n, const int32_t *src, const int32_t *dst, int32_t *copies,
@@ -390,8 +407,10 @@ int gdn_pages_fork(const gdn_page_cache *c, int32_t n, const int32_t *src, const
     if (const int rc = check_pool(c, n)) return rc;
     if (n == 0) return GDN_OK;
     if (!has_pool(c) || !src || !dst || !copies || !status) return GDN_ERR_NULL;
-    return launch_pdl(fork_kernel, dim3(kCluster), dim3(kThreads), 0, stream, pool_args(c, status), n, src, dst,
-                      copies) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    const cudaError_t err = many(n, c->max_pages)
+        ? launch_pdl(fork_kernel<8>, dim3(8), dim3(kThreads), 0, stream, pool_args(c, status), n, src, dst, copies)
+        : launch_pdl(fork_kernel<1>, dim3(1), dim3(kThreads), 0, stream, pool_args(c, status), n, src, dst, copies);
+    return err == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 int gdn_pages_copy(const gdn_page_cache *c, int32_t n, const int32_t *copies, int32_t *status, cudaStream_t stream)
@@ -410,8 +429,10 @@ int gdn_pages_release(const gdn_page_cache *c, int32_t n, const int32_t *slots, 
     if (const int rc = check_pool(c, n)) return rc;
     if (n == 0) return GDN_OK;
     if (!has_pool(c) || !slots || !status) return GDN_ERR_NULL;
-    return launch_pdl(release_kernel, dim3(kCluster), dim3(kThreads), 0, stream, pool_args(c, status), n, slots)
-               == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    const cudaError_t err = many(n, c->max_pages)
+        ? launch_pdl(release_kernel<8>, dim3(8), dim3(kThreads), 0, stream, pool_args(c, status), n, slots)
+        : launch_pdl(release_kernel<1>, dim3(1), dim3(kThreads), 0, stream, pool_args(c, status), n, slots);
+    return err == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 }  // extern "C"
