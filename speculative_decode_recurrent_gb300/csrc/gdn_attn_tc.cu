@@ -72,7 +72,8 @@ struct TcArgs {
     int b0, nb;                 // sequences [b0, b0 + nb) of the call
     int tpt, row_tiles;         // tokens of a row tile (128 / G), row tiles of a key head
     int rp;                     // rows of a partial result (a multiple of 32)
-    int2 *desc;                 // per row tile: 2 (first CTA) + its place in the unit, and the last CTA
+    int4 *rec;                  // records of the units that are split: row tile, row tiles of it, first CTA, parts
+    int by_cta;                 // a record's place: the first CTA's number, or (fewer units than CTAs) the row tile's
     float *part;                // [2 CTAs][NQ][D + 2][rp]
 };
 
@@ -133,6 +134,14 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok) : "r"(saddr(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// As mbar_try_wait, suspended for about `ns` at most.
+__device__ __forceinline__ bool mbar_doze(uint64_t *bar, uint32_t parity, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(saddr(bar)), "r"(parity), "r"(ns) : "memory");
     return ok != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -208,10 +217,10 @@ __device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int tpt
     s.h = in_b / per;
     const int r = in_b - s.h * per, paired = 2 * sh.pairs * tiles, live = sh.live * tiles;
     int start;
-    s.nq = 1;
+    s.nq = 1;                                       // (nq is a constant: with 1 it stays one)
     s.tiles = sh.tiles;
     s.total = sh.total;
-    if (r < paired) {
+    if (nq == 2 && r < paired) {
         const int u = sh.pairs == 1 ? 0 : r / (2 * tiles);
         s.nq = 2;
         s.rt = 2 * u;
@@ -241,11 +250,23 @@ struct Cut {
         if (nq == 2 && c > 0 && c < N) {
             Segment s;
             locate(st, st.find(w), w, tpt, row_tiles, nq, s);
-            w = s.unit_w + s.first * s.nq;
+            w = s.unit_w + (s.first << (s.nq - 1));
         }
         return w;
     }
 };
+
+// The CTAs that hold tiles of the unit, counted from the one that holds its first.
+__device__ __forceinline__ int parts_of(const Cut &cut, const Segment &s) {
+    const int last = s.unit_w + s.tiles * s.nq - 1;                // the last tile's last item
+    int lo = blockIdx.x, hi = cut.N - 1;
+    while (lo < hi) {                               // the last share that starts at or before it
+        const int mid = (lo + hi + 1) >> 1;
+        if (cut.q * mid + cut.r * mid / cut.N <= last) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo - static_cast<int>(blockIdx.x) + 1;
+}
 
 // Walks a CTA's share [w, w1) unit by unit.
 struct Cursor {
@@ -254,17 +275,48 @@ struct Cursor {
         if (w >= w1) return false;
         while (st.prefix[b + 1] <= w) ++b;
         locate(st, b, w, tpt, row_tiles, nq, s);
-        s.count = min((w1 - w) >> (s.nq - 1), s.tiles - s.first);
-        w += s.count * s.nq;
+        const int two = nq == 2 ? s.nq - 1 : 0;
+        s.count = min((w1 - w) >> two, s.tiles - s.first);
+        w += s.count << two;
         return true;
     }
 };
+
+// The infinities and NaN among the values of the tile at j0 (rows `special`) added to the sums of the
+// rows that see them (`view`, per thread); a whole warp calls it.
+template <int D>
+__device__ __noinline__ void add_odd_values(const AttnArgs &a, uint32_t t_o, int slot, int h, int j0, int half,
+                                            unsigned long long special, uint64_t view)
+{
+#pragma unroll 1
+    for (int c = 0; c < D / 2; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(t_o + c, o);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int r = 0; r < kKeys; ++r) {
+            if (!((special >> r) & 1)) continue;
+            const int j = j0 + r;
+            int id = __ldg(a.s.table + static_cast<size_t>(slot) * a.s.max_pages + (j >> a.s.page_shift));
+            if (id < 0 || id >= a.s.n_page) id = 0;
+            const size_t vrow = ((static_cast<size_t>(id) * a.s.Hkv + h) << a.s.page_shift) + (j & ((1 << a.s.page_shift) - 1));
+            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + vrow * D + half * (D / 2) + c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                const float y = __bfloat162float(v[k]);
+                if (((view >> r) & 1) && !(fabsf(y) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
+            }
+        }
+        tmem_st32(t_o + c, o);
+    }
+    tmem_wait_st();
+}
 
 // ------------------------------------------------------------------ the kernel
 template <int D, int NQ>
 __global__ void __launch_bounds__(TcPlan<D, NQ>::THREADS, 1)
 verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const TcArgs ta)
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcArgs ta)
 {
     using P = TcPlan<D, NQ>;
     constexpr int NG = P::NG;
@@ -332,7 +384,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (q.bad && blockIdx.x == 0) {         // none of its row tiles is for the join
                 atomicOr(a.s.status, q.bad);
                 const int per = a.s.Hkv * ta.row_tiles;
-                for (int u = 0; u < per; ++u) ta.desc[static_cast<size_t>(ta.b0 + i) * per + u] = make_int2(0, -1);
+                if (!ta.by_cta)
+                    for (int u = 0; u < per; ++u) ta.rec[i * per + u] = make_int4(0, 0, 0, 0);
             }
         }
         int incl = mine;
@@ -352,7 +405,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     if (tid == 0) {
         st.prefix[ta.nb] = before;
-        const int N = min(NQ == 2 ? (before + 1) / 2 : before, static_cast<int>(gridDim.x));   // every share has a tile
+        const int most = NQ == 2 && before > 1 ? before / 2 : before;     // every share has a tile (of a pair, too)
+        const int N = min(most, static_cast<int>(gridDim.x));
         cut->W = before;
         cut->N = N;
         cut->q = N ? before / N : 0;
@@ -389,6 +443,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         expire();
         return false;
     };
+    if (ta.by_cta && tid == P::ROWS - 1) ta.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
     Segment s;
     uint32_t pos = 0;                               // load warps: tiles loaded (of keys, or of values)
     bool issued = false;                            // MMA warps: some MMA
@@ -463,25 +518,31 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint64_t *sf = s_full + 2 * group, *pf = p_full + 2 * group, *od = o_done + 2 * group;
         uint32_t g = 0, tile0 = 0, segs = 0;        // this group's tiles, the CTA's tiles and segments so far
         bool ok = !*abort;
-        while (ok && cur.next(st, ta.tpt, ta.row_tiles, NQ, s)) {
-            const bool alternate = NG == 2 && s.nq == 1;
+        Segment next;
+        auto load_queries = [&](const Segment &u) {
+            const int nq = NQ == 1 ? 1 : __shfl_sync(0xffffffffu, u.nq, 0), y = __shfl_sync(0xffffffffu, u.h, 0) * a.G;
+            const int z = (ta.b0 + __shfl_sync(0xffffffffu, u.b, 0)) * a.s.T + __shfl_sync(0xffffffffu, u.rt, 0) * ta.tpt;
+            if (elect_one()) {
+                mbar_expect_tx(q_full, nq * P::ATOMS * ta.tpt * a.G * 128);
+#pragma unroll 1
+                for (int q = 0; q < nq; ++q)
+#pragma unroll
+                    for (int x = 0; x < P::ATOMS; ++x)
+                        tma_load_3d(sQ + q * P::QTILE + x * (kRows * 128), &tm_q, x * 64, y, z + q * ta.tpt, q_full);
+            }
+            __syncwarp();
+            ++queries;
+        };
+        bool have = ok && cur.next(st, ta.tpt, ta.row_tiles, NQ, s);
+        while (have) {
+            const bool alternate = NG == 2 && (NQ == 1 || s.nq == 1);
             const int step = alternate ? 2 : 1, off = alternate ? (group ^ tile0) & 1 : 0;
             const int count = __shfl_sync(0xffffffffu, (s.count - off + step - 1) / step, 0);
             const bool twice = __shfl_sync(0xffffffffu, alternate ? 1 : 0, 0) != 0;
-            const uint64_t dq = desc_sw128(saddr(sQ) + (s.nq == 2 ? group * P::QTILE : 0));
-            if (group == 0) {                       // the unit's queries, once the unit's before are done with
-                if (segs > 0) ok = __all_sync(0xffffffffu, wait(q_empty, (segs - 1) & 1)) != 0;
-                const int nq = __shfl_sync(0xffffffffu, s.nq, 0), y = __shfl_sync(0xffffffffu, s.h, 0) * a.G;
-                const int z = (ta.b0 + __shfl_sync(0xffffffffu, s.b, 0)) * a.s.T + __shfl_sync(0xffffffffu, s.rt, 0) * ta.tpt;
-                if (ok && elect_one()) {
-                    mbar_expect_tx(q_full, nq * P::ATOMS * ta.tpt * a.G * 128);
-                    for (int q = 0; q < nq; ++q)
-                        for (int x = 0; x < P::ATOMS; ++x)
-                            tma_load_3d(sQ + q * P::QTILE + x * (kRows * 128), &tm_q, x * 64, y, z + q * ta.tpt, q_full);
-                }
-                __syncwarp();
-                queries += ok;
-            }
+            const uint64_t dq = desc_sw128(saddr(sQ) + (alternate ? 0 : group * P::QTILE));
+            if (group == 0 && segs == 0) load_queries(s);
+            const bool more = group == 0 && cur.next(st, ta.tpt, ta.row_tiles, NQ, next);
+            bool wanted = more;                     // the next unit's queries, once all scores of this one are done
             ok = ok && __all_sync(0xffffffffu, wait(q_full, segs & 1)) != 0;
             ++segs;
             if (ok && count == 0 && elect_one()) mbar_arrive(q_empty);
@@ -489,6 +550,10 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             uint32_t idle = 0;
             while (ok && pn < count) {
                 bool did = false;
+                if (wanted && sn == count && __all_sync(0xffffffffu, mbar_test(q_empty, (segs - 1) & 1))) {
+                    load_queries(next);
+                    wanted = false;
+                }
                 if (sn < count && sn < pn + 2) {
                     // the buffer held the weights of the group's tile t - 2: their product must be done
                     const uint32_t t = g + sn, kpos = 2 * (tile0 + sn * step + off), stage = kpos % P::NST;
@@ -532,15 +597,34 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         ++pn;
                     }
                 }
-                idle = did ? 0 : idle + 1;
+                if (did) {
+                    idle = 0;
+                    continue;
+                }
+                // asleep until the next weights are there (or, before any, the next keys), but not
+                // for long: the other may come first
+                const uint32_t t = g + pn, kpos = 2 * (tile0 + sn * step + off), stage = kpos % P::NST;
+                if (pn < sn) mbar_doze(&pf[t & 1], (t >> 1) & 1, 200);
+                else mbar_doze(&full[stage], (kpos / P::NST) & 1, 200);
+                ++idle;
                 if (*abort || idle > kIdleLimit) {
                     if (idle > kIdleLimit) expire();
                     ok = false;
                 }
                 ok = __all_sync(0xffffffffu, ok);
             }
+            if (ok && wanted) {
+                ok = __all_sync(0xffffffffu, wait(q_empty, (segs - 1) & 1)) != 0;
+                if (ok) load_queries(next);
+            }
             g += count;
             tile0 += s.count;
+            if (group == 0) {
+                have = ok && more;
+                s = next;
+            } else {
+                have = ok && cur.next(st, ta.tpt, ta.row_tiles, NQ, s);
+            }
         }
     } else {
         // ------------------------------------------------------ rows
@@ -558,16 +642,25 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             __syncwarp();
             tc_fence_after();
         };
-        while (cur.next(st, ta.tpt, ta.row_tiles, NQ, s)) {
-            const bool alternate = NG == 2 && s.nq == 1;
+        Segment next;
+        bool more = cur.next(st, ta.tpt, ta.row_tiles, NQ, s);
+        auto token_of = [&](const Segment &u) {      // this thread's draft token in unit u
+            return (u.rt + (NQ == 2 && u.nq == 2 ? group : 0)) * ta.tpt + r_in / a.G;
+        };
+        auto word_of = [&](const Segment &u) {
+            const int t = token_of(u);
+            return r_in < ta.tpt * a.G && t < a.s.T && t < u.n ? row_tree(a, ta.b0 + u.b, t, u.n) : 0ull;
+        };
+        uint64_t bits = more ? word_of(s) : 0ull, next_bits = 0ull;
+        while (more) {
+            const bool alternate = NG == 2 && (NQ == 1 || s.nq == 1);
             const int step = alternate ? 2 : 1, off = alternate ? (group ^ tile0) & 1 : 0;
-            const int rt = s.rt + (s.nq == 2 ? group : 0), per_tile = ta.tpt * a.G;
+            const int per_tile = ta.tpt * a.G;
             const int b = ta.b0 + s.b;
             if (NG == 2) bar_sync(1, P::ROWS);      // both groups have left each other's O and exchange words
-            const int t = rt * ta.tpt + r_in / a.G, qh = r_in % a.G;       // draft token, head of the group
+            const int t = token_of(s), qh = r_in % a.G;                    // draft token, head of the group
             const bool exists = r_in < per_tile && t < a.s.T, used = exists && t < s.n;
             const bool warp_live = __any_sync(0xffffffffu, used);
-            const uint64_t bits = used ? row_tree(a, b, t, s.n) : 0ull;
             float m = -INFINITY, l = 0.f;           // m: the same in both threads of a row; l: of this thread's keys
             int mine = 0;                           // tiles of this group
             for (int i = off; i < s.count; i += step, ++g, ++mine) {
@@ -658,15 +751,15 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             *at = make_uint4(0u, 0u, 0u, 0u);
                             continue;
                         }
-                        uint32_t w[4] = {at->x, at->y, at->z, at->w};
-                        bool bad = false;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, bad = true;
-                            if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu, bad = true;
-                        }
-                        if (bad) {
-                            *at = make_uint4(w[0], w[1], w[2], w[3]);
+                        // an exponent of ones carries into its half's sign bit
+                        const uint4 w = *at;
+                        const uint4 c4 = make_uint4((w.x & 0x7f807f80u) + 0x00800080u, (w.y & 0x7f807f80u) + 0x00800080u,
+                                                    (w.z & 0x7f807f80u) + 0x00800080u, (w.w & 0x7f807f80u) + 0x00800080u);
+                        if ((c4.x | c4.y | c4.z | c4.w) & 0x80008000u) {
+                            auto keep = [](uint32_t v, uint32_t c) {
+                                return v & ~((c & 0x80000000u ? 0xffff0000u : 0u) | (c & 0x8000u ? 0xffffu : 0u));
+                            };
+                            *at = make_uint4(keep(w.x, c4.x), keep(w.y, c4.y), keep(w.z, c4.z), keep(w.w, c4.w));
                             atomicOr(flags, 1ull << r);
                         }
                     }
@@ -680,31 +773,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     wait_rows(&od[g & 1], (g >> 1) & 1);
                     if (warp_live) {
                         const int sh = s.len - j0;
-                        uint64_t view = sh >= 64 ? 0ull : sh >= 0 ? bits << sh : sh > -64 ? bits >> -sh : 0ull;
-                        view = used ? view & special : 0ull;
-#pragma unroll 1
-                        for (int c = 0; c < D / 2; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(t_o + c, o);
-                            tmem_wait_ld();
-#pragma unroll 1
-                            for (int r = 0; r < kKeys; ++r) {
-                                if (!((special >> r) & 1)) continue;
-                                const int j = j0 + r;
-                                int id = __ldg(a.s.table + static_cast<size_t>(s.slot) * a.s.max_pages + (j >> a.s.page_shift));
-                                if (id < 0 || id >= a.s.n_page) id = 0;
-                                const size_t vrow = ((static_cast<size_t>(id) * a.s.Hkv + s.h) << a.s.page_shift) +
-                                                    (j & ((1 << a.s.page_shift) - 1));
-                                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + vrow * D + half * (D / 2) + c;
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    const float y = __bfloat162float(v[k]);
-                                    if (((view >> r) & 1) && !(fabsf(y) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
-                                }
-                            }
-                            tmem_st32(t_o + c, o);
-                        }
-                        tmem_wait_st();
+                        const uint64_t view = sh >= 64 ? 0ull : sh >= 0 ? bits << sh : sh > -64 ? bits >> -sh : 0ull;
+                        add_odd_values<D>(a, t_o, s.slot, s.h, j0, half, special, used ? view & special : 0ull);
                     }
                     bar_sync(whole_id, whole_n);
                     if (who == 0) *flags = 0ull;
@@ -712,13 +782,19 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
             }
             tile0 += s.count;
+            more = cur.next(st, ta.tpt, ta.row_tiles, NQ, next);
+            next_bits = more ? word_of(next) : 0ull;
             // ---- the unit's result, or this CTA's part of it
             if (mine > 0) wait_rows(&od[(g - 1) & 1], ((g - 1) >> 1) & 1);
             const bool whole = s.count == s.tiles;
-            const size_t unit = (static_cast<size_t>(b) * a.s.Hkv + s.h) * ta.row_tiles + rt;
-            if (gtid == 0 && (group == 0 || s.nq == 2)) {
-                if (s.first == 0) ta.desc[unit].x = 2 * blockIdx.x + (s.nq == 2 ? group : 0);
-                if (s.first + s.count == s.tiles) ta.desc[unit].y = blockIdx.x;
+            if (tid == P::ROWS - 1 && s.first == 0) {             // the unit's record
+                const int tile = (s.b * a.s.Hkv + s.h) * ta.row_tiles + s.rt;
+                if (ta.by_cta) {
+                    if (!whole) ta.rec[blockIdx.x] = make_int4(tile, s.nq, blockIdx.x, parts_of(*cut, s));
+                } else {
+                    ta.rec[tile] = make_int4(tile, s.nq, blockIdx.x, whole ? 0 : parts_of(*cut, s));
+                    if (s.nq == 2) ta.rec[tile + 1] = make_int4(0, 0, 0, 0);
+                }
             }
             // the row's threads: two, or four when both groups worked on it (each group's O scaled to
             // the common maximum)
@@ -748,7 +824,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 f1 *= inv;
                 const size_t orow = (static_cast<size_t>(b) * a.s.T + t) * a.Hq + s.h * a.G + qh;
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c0);
-                float *slot = ta.part + static_cast<size_t>((2 * blockIdx.x + (s.first == 0 ? 1 : 0)) * NQ + (s.nq == 2 ? group : 0)) *
+                float *slot = ta.part + static_cast<size_t>((2 * blockIdx.x + (s.first == 0 ? 1 : 0)) * NQ + (NQ == 2 && s.nq == 2 ? group : 0)) *
                                             (D + 2) * ta.rp + r_in;
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 16) {
@@ -792,6 +868,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             tc_fence_before();
             if (NG == 1) bar_sync(1, P::ROWS);      // the exchange words have been read
+            s = next;
+            bits = next_bits;
         }
     }
     __syncwarp();
@@ -818,49 +896,66 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // ------------------------------------------------------------------- the join
-// A task is 32 rows (a lane each) and 8 output columns of a row tile; `wide` warps (a power of two,
-// about one for every four parts) take its parts in turn, and the first of them joins their
-// sums in a fixed order.  gridDim.y CTAs share a row tile's tasks.
-constexpr int kJoinWarps = 16;
+// A task is 32 rows (a lane each) and 8 output columns of a split unit; `wide` warps (a power of
+// two, about one for every four parts) take its parts in turn, and the first of them joins
+// their sums in a fixed order.  gridDim.y CTAs share a record's tasks.
+constexpr int kJoinWarps = 8;
 
 template <int D, int NQ>
-__global__ void __launch_bounds__(kJoinWarps * 32) verify_tc_join_kernel(const TcArgs ta, int grid)
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) verify_tc_join_kernel(const TcArgs ta, int grid)
 {
     const AttnArgs &a = ta.a;
-    const int rt = blockIdx.x % ta.row_tiles, bh = blockIdx.x / ta.row_tiles;
-    const int h = bh % a.s.Hkv, b = ta.b0 + bh / a.s.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __shared__ float sums[kJoinWarps][10][32];
     pdl_wait();
     pdl_release();
-    const int2 d = ta.desc[static_cast<size_t>(ta.b0) * a.s.Hkv * ta.row_tiles + blockIdx.x];
-    const int cta = d.x >> 1, place = d.x & 1, parts = d.y - cta + 1;
-    if (parts < 2 || cta < 0 || place >= NQ || d.y >= grid) return;      // finished by one CTA, or skipped
+    const int4 rec = ta.rec[blockIdx.x];
+    const int cta = rec.z, parts = rec.w;
+    if (parts < 2 || cta < 0 || cta + parts > grid || rec.x < 0 || rec.y < 1 || rec.y > NQ) return;
+    const int rt0 = rec.x % ta.row_tiles, bh = rec.x / ta.row_tiles, h = bh % a.s.Hkv, b = ta.b0 + bh / a.s.Hkv;
+    if (b >= ta.b0 + ta.nb || rt0 + rec.y > ta.row_tiles) return;
     int wide = 1;
     while (wide < kJoinWarps && wide * 4 < parts) wide *= 2;
     const int at_once = kJoinWarps / wide, mine = warp / wide, sub = warp % wide;
-    const int per_tile = ta.tpt * a.G, rows = min(per_tile, (a.s.T - rt * ta.tpt) * a.G);
-    const int tasks = (rows + 31) / 32 * (D / 8);
+    const int per_tile = ta.tpt * a.G, tasks = rec.y * (ta.rp / 32) * (D / 8), slot = (D + 2) * ta.rp;
     for (int t0 = blockIdx.y * at_once; t0 < tasks; t0 += gridDim.y * at_once) {
-        const int task = t0 + mine, r = task / (D / 8) * 32 + lane, c0 = task % (D / 8) * 8;
+        const int task = t0 + mine, c0 = task % (D / 8) * 8, rg = task / (D / 8);
+        const int place = rg / (ta.rp / 32), r = rg % (ta.rp / 32) * 32 + lane, rt = rt0 + place;
+        const int rows = min(per_tile, (a.s.T - rt * ta.tpt) * a.G);
         const bool exists = task < tasks && r < rows;
         float m = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[c] = 0.f;
         if (exists) {
-#pragma unroll 4
-            for (int k = sub; k < parts; k += wide) {                    // part 0: the first CTA's second slot
-                const float *p = ta.part + static_cast<size_t>((2 * (cta + k) + (k == 0 ? 1 : 0)) * NQ + place) * (D + 2) * ta.rp + r;
-                const float mk = p[static_cast<size_t>(D) * ta.rp], lk = p[static_cast<size_t>(D + 1) * ta.rp];
-                float x[8];
+            // part k: the first slot of CTA cta + k, but the second one of the first CTA
+            const float *first = ta.part + static_cast<size_t>(2 * cta * NQ + place) * slot + r;
+            const float *col = first + c0 * ta.rp;
+#pragma unroll 1
+            for (int k0 = sub; k0 < parts; k0 += 4 * wide) {             // four parts requested at a time
+                float mk[4], lk[4], x[4][8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) x[c] = p[static_cast<size_t>(c0 + c) * ta.rp];
-                const float mn = fmaxf(m, mk), ms = mn == -INFINITY ? 0.f : mn;
-                const float f0 = ex2(m - ms), f1 = ex2(mk - ms);
+                for (int i = 0; i < 4; ++i) {
+                    const int k = k0 + i * wide;
+                    const bool in = k < parts;
+                    const int at = (2 * k + (k == 0 ? 1 : 0)) * NQ * slot;        // < 2^31: 2 N NQ (D + 2) rp floats
+                    mk[i] = in ? first[at + D * ta.rp] : -INFINITY;
+                    lk[i] = in ? first[at + (D + 1) * ta.rp] : 0.f;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) x[i][c] = in ? col[at + c * ta.rp] : 0.f;
+                }
+                const float mn = fmaxf(m, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])));
+                const float ms = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - ms);
                 m = mn;
-                l = l * f0 + lk * f1;
+                l *= f0;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) acc[c] = acc[c] * f0 + x[c] * f1;
+                for (int c = 0; c < 8; ++c) acc[c] *= f0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = ex2(mk[i] - ms);
+                    l = fmaf(lk[i], f, l);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] = fmaf(x[i][c], f, acc[c]);
+                }
             }
         }
         if (wide > 1) {                                                  // the same in the whole CTA
@@ -947,13 +1042,16 @@ int tc_grid(const gdn_page_cache *c, const gdn_attn_dims *d, int nb) {
     const int sms = sm_count();
     return static_cast<int>(all < sms ? all : sms);
 }
-// CTAs that share a row tile's tasks in the join: two per SM in all, at most one per task.
-int join_ctas(int units, int tasks) {
-    const int want = 2 * sm_count() / units;
-    return want < 1 ? 1 : want > tasks ? tasks : want;
+// Records of a launch: one per CTA, or per row tile where those are fewer.
+int tc_records(const gdn_page_cache *c, const gdn_attn_dims *d, int nb, bool *by_cta) {
+    const long long units = static_cast<long long>(nb) * c->Hkv * tc_row_tiles(c, d);
+    const int grid = tc_grid(c, d, nb);
+    *by_cta = grid < units;
+    return *by_cta ? grid : static_cast<int>(units);
 }
-size_t desc_bytes(const gdn_page_cache *c, const gdn_attn_dims *d) {
-    return (static_cast<size_t>(d->B) * c->Hkv * tc_row_tiles(c, d) * sizeof(int2) + 15) & ~static_cast<size_t>(15);
+size_t rec_bytes(const gdn_page_cache *c, const gdn_attn_dims *d) {
+    bool by_cta;
+    return static_cast<size_t>(tc_records(c, d, tc_seqs(c, d), &by_cta)) * sizeof(int4);
 }
 
 template <int D, int NQ>
@@ -963,14 +1061,18 @@ int launch_tc(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a
     if (!query_map(&mq, a.q, c, d) || !page_map(&mk, a.k, c) || !page_map(&mv, a.v, c)) return GDN_ERR_LAUNCH;
     if (cudaFuncSetAttribute(verify_tc_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    TcArgs ta{a, 0, 0, tc_tokens(c, d), tc_row_tiles(c, d), tc_rp(c, d), reinterpret_cast<int2 *>(a.ws),
-              reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + desc_bytes(c, d))};
+    TcArgs ta{a, 0, 0, tc_tokens(c, d), tc_row_tiles(c, d), tc_rp(c, d), reinterpret_cast<int4 *>(a.ws), 0,
+              reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + rec_bytes(c, d))};
     const int step = tc_seqs(c, d);
     for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += step) {
         ta.nb = d->B - ta.b0 < step ? d->B - ta.b0 : step;
-        const int grid = tc_grid(c, d, ta.nb), units = ta.nb * c->Hkv * ta.row_tiles;
+        const int grid = tc_grid(c, d, ta.nb);
+        bool by_cta;
+        const int recs = tc_records(c, d, ta.nb, &by_cta), tasks = NQ * (ta.rp / 32) * (D / 8);
+        ta.by_cta = by_cta;
+        const int share = 8 * sm_count() / recs;                  // CTAs of a record: two or three waves
         if (launch_pdl(verify_tc_kernel<D, NQ>, dim3(grid), dim3(P::THREADS), P::BYTES, s, mq, mk, mv, ta) != cudaSuccess ||
-            launch_pdl(verify_tc_join_kernel<D, NQ>, dim3(units, join_ctas(units, ta.rp / 32 * (D / 8))),
+            launch_pdl(verify_tc_join_kernel<D, NQ>, dim3(recs, share < 1 ? 1 : share > tasks ? tasks : share),
                        dim3(kJoinWarps * 32), 0, s, ta, grid) != cudaSuccess)
             return GDN_ERR_LAUNCH;
     }
@@ -980,7 +1082,7 @@ int launch_tc(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a
 }  // namespace
 
 int64_t attn_tc_workspace(const gdn_page_cache *c, const gdn_attn_dims *d) {
-    return static_cast<int64_t>(desc_bytes(c, d)) +
+    return static_cast<int64_t>(rec_bytes(c, d)) +
            static_cast<int64_t>(2) * tc_grid(c, d, tc_seqs(c, d)) * tc_nq(c, d) * (c->d + 2) * tc_rp(c, d) * 4;
 }
 
