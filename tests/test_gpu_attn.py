@@ -128,6 +128,51 @@ def test_verify_tree(i, dtype):
     r.check()
 
 
+# several row tiles per key head (in pairs, with one left over, with tiles whose rows are all past
+# the draft), head groups that do not divide a row tile
+ROW_TILES = [
+    ([150, 40, 0], [48, 20, 3], 48, 16, 2, 128, 64),        # 3 tiles: a pair and one
+    ([70, 300], [64, 17], 64, 16, 1, 64, 16),               # 8 tiles
+    ([33, 129], [64, 64], 64, 64, 1, 128, 32),              # 32 tiles, two tokens each
+    ([100, 65], [40, 26], 40, 15, 3, 128, 16),              # 25 tokens of 5 heads: 125 rows a tile
+    ([513], [64], 64, 24, 2, 64, 128),                      # 10 tokens of 12 heads
+    ([77, 5], [50, 50], 50, 9, 3, 256, 16),                 # wide heads: one group, two tiles
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("i", range(len(ROW_TILES)))
+def test_verify_row_tiles(i, dtype):
+    lens, drafts, T, Hq, Hkv, d, page = ROW_TILES[i]
+    par = R.random_parents(len(lens), T, torch.Generator().manual_seed(200 + i))
+    words = [R.ancestors(par[b], T)[0] for b in range(len(lens))] if i % 2 else None
+    r = VerifyRun(lens, drafts, T, Hq, Hkv, d, page, dtype, words=words, seed=210 + i)
+    r.call()
+    r.check()
+
+
+@pytest.mark.parametrize("T,Hq,d", [(16, 8, 128), (40, 8, 64), (24, 16, 128), (9, 4, 256)])
+def test_verify_ragged_batch(T, Hq, d):
+    """Shares that begin and end anywhere in units of very different lengths: units of one CTA, of
+    two and of many, several units of one CTA; the same bits from one call to the next."""
+    lens = [3000, 7, 64, 0, 1900, 333, 128, 5000, 12, 700]
+    r = VerifyRun(lens, [max(0, T - (3 * b) % (T + 1)) for b in range(len(lens))], T, Hq, 1, d, 32, BF, seed=230)
+    r.call()
+    r.check()
+    first = r.out.clone(), r.lse.clone()
+    for _ in range(3):
+        r.call()
+        assert torch.equal(first[0], r.out) and torch.equal(first[1], r.lse)
+
+
+def test_verify_more_sequences_than_one_launch_takes():
+    B = 1100
+    lens = [(29 * b) % 150 for b in range(B)]
+    r = VerifyRun(lens, [b % 3 for b in range(B)], 2, 2, 1, 64, 16, BF, seed=240)
+    r.call()
+    r.check()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_verify_rows_that_see_nothing(dtype):
     """Words without bits over an empty context, and words whose bits lie past the draft."""
