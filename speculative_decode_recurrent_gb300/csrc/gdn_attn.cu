@@ -455,16 +455,24 @@ __global__ void __launch_bounds__(kCoreThreads, CorePlan<D>::CTAS) verify_core_k
                 }
             } else {
 #pragma unroll 1
-                for (int j = 0; j < kKT; ++j) {
-                    float2 v[C];
+                for (int j = 0; j < kKT; j += 4) {
+                    float2 v[4][C];
 #pragma unroll
-                    for (int i = 0; i < C; ++i) v[i] = *reinterpret_cast<const float2 *>(vr + j * D + 64 * i);
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < C; ++i) v[k][i] = *reinterpret_cast<const float2 *>(vr + (j + k) * D + 64 * i);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float p = pr[r * P::PSTR + j];
-                        if (p == -1.f) continue;                  // unseen (warp-uniform)
+                        const float4 p4 = *reinterpret_cast<const float4 *>(pr + r * P::PSTR + j);
+                        const float p[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
-                        for (int i = 0; i < C; ++i) acc[r][i] = fma2(make_float2(p, p), v[i], acc[r][i]);
+                        for (int k = 0; k < 4; ++k) {
+                            const bool seen = p[k] != -1.f;       // unseen: zero times zero, whatever the value is
+                            const float2 pp = seen ? make_float2(p[k], p[k]) : make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int i = 0; i < C; ++i)
+                                acc[r][i] = fma2(pp, seen ? v[k][i] : make_float2(0.f, 0.f), acc[r][i]);
+                        }
                     }
                 }
             }

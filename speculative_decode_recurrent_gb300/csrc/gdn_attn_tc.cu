@@ -54,8 +54,8 @@ template <int D, int NQ> struct TcPlan {
     static constexpr int THREADS = ROWS + 32 * (2 + NG);
     static constexpr int QTILE = kRows * D * 2;
     static constexpr int OFF_RING = NQ * QTILE;                 // after the queries
-    static constexpr int OFF_SEQ = OFF_RING + NST * STAGE;      // prefix, slot, len, n
-    static constexpr int OFF_XCH = OFF_SEQ + (4 * kMaxSeqs + 4) * 4;                      // two words per row thread
+    static constexpr int OFF_SEQ = OFF_RING + NST * STAGE;      // prefix, slot, len, n, units
+    static constexpr int OFF_XCH = OFF_SEQ + (5 * kMaxSeqs + 4) * 4;                      // two words per row thread
     static constexpr int OFF_BAR = OFF_XCH + ROWS * 8;
     static constexpr int BYTES = OFF_BAR + 640;
     static constexpr int TCOLS = 2 * kKeys + D;                 // TMEM of a group: S in [0, 64) and [64, 128), then O
@@ -169,7 +169,8 @@ __device__ __forceinline__ float ex2(float x) {
 // ------------------------------------------------------------- the work's layout
 // Units of one (sequence, key head): the row tiles that hold rows in use, in pairs where NQ is 2
 // (`pairs`, then `single`), take every tile of keys; each of the others is one tile without keys (its
-// rows get zeros).  Work is counted in row tiles times tiles of keys: a pair's tile counts 2.
+// rows get zeros).  Work is counted in row tiles times tiles of keys (a pair's tile counts 2), and a
+// unit counts `fixed` more: beginning and ending one costs a CTA as much as some tiles.
 struct Shape {
     int live, dead, pairs, single, tiles, total;    // total: keys
     __device__ Shape(int len, int n, int tpt, int row_tiles, int nq) {
@@ -180,12 +181,20 @@ struct Shape {
         total = len + n;
         tiles = (total + kKeys - 1) / kKeys;        // >= 1 when live > 0
     }
-    __device__ int per_head() const { return live * tiles + dead; }
+    __device__ int units() const { return pairs + single + dead; }
+    __device__ int per_head(int fixed) const { return live * tiles + dead + fixed * units(); }
 };
+// Measured: 4 of 4, 6, 8 and 10 is best where all units are single (B 128, T 8, Hq 16, Hkv 2, d 256: 0 and
+// 8 cost 1 to 2 % more), 8 where there are pairs (B 12, T 48, Hq 32, Hkv 4, d 128: 71 us with 0, 64 with
+// 4, 62 with 8 and 10).
+template <int NQ> constexpr int kFixed = NQ == 2 ? 8 : 4;
+constexpr int kFixedFrom = 16;                      // tiles a CTA from which on it is counted: below, every tile
+                                                    // on a CTA of its own is faster
 
 struct SeqTable {
     int *prefix;                                    // [nb + 1] work before each sequence
     int *slot, *len, *n;                            // [nb]
+    int *units;                                     // [nb] units before each sequence
     int nb;
     // The last sequence that starts at or before w, among those with work.
     __device__ int find(int w) const {
@@ -203,54 +212,57 @@ struct Segment {
     int b, h, rt, nq;                               // sequence (within the launch), key head, first row tile, row tiles
     int slot, len, n, total;                        // total 0: a row tile without rows in use
     int first, count, tiles;                        // tiles [first, first + count) of the unit's `tiles`
-    int unit_w;                                     // the unit's place in the launch's work
+    int begin, end;                                 // the unit's place in the launch's work
 };
 
 // The unit that holds work item w, and the tile of it.
-__device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int tpt, int row_tiles, int nq, Segment &s) {
+__device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int tpt, int row_tiles, int nq, int fixed, Segment &s) {
     const Shape sh(st.len[b], st.n[b], tpt, row_tiles, nq);
-    const int in_b = w - st.prefix[b], per = sh.per_head(), tiles = sh.tiles;
+    const int in_b = w - st.prefix[b], per = sh.per_head(fixed);
     s.b = b;
     s.slot = st.slot[b];
     s.len = st.len[b];
     s.n = st.n[b];
     s.h = in_b / per;
-    const int r = in_b - s.h * per, paired = 2 * sh.pairs * tiles, live = sh.live * tiles;
-    int start;
+    int r = in_b - s.h * per, size = 2 * sh.tiles + fixed, u;
+    const int head = w - r, paired = sh.pairs * size, live = paired + sh.single * (sh.tiles + fixed);
     s.nq = 1;                                       // (nq is a constant: with 1 it stays one)
     s.tiles = sh.tiles;
     s.total = sh.total;
+    int start = 0;
     if (nq == 2 && r < paired) {
-        const int u = sh.pairs == 1 ? 0 : r / (2 * tiles);
+        u = sh.pairs == 1 ? 0 : r / size;
         s.nq = 2;
         s.rt = 2 * u;
-        start = u * 2 * tiles;
-        s.first = (r - start) / 2;
     } else if (r < live) {
-        const int u = sh.single == 1 ? 0 : (r - paired) / tiles;
+        start = nq == 2 ? paired : 0;
+        size = sh.tiles + fixed;
+        u = sh.single == 1 ? 0 : (r - start) / size;
         s.rt = 2 * sh.pairs + u;
-        start = paired + u * tiles;
-        s.first = r - start;
     } else {
-        s.rt = sh.live + r - live;
-        start = r;
-        s.first = 0;
+        start = live;
+        size = 1 + fixed;
+        u = (r - start) / size;
+        s.rt = sh.live + u;
         s.tiles = 1;
         s.total = 0;
     }
-    s.unit_w = st.prefix[b] + s.h * per + start;
+    s.begin = head + start + u * size;
+    s.end = s.begin + size;
+    s.first = max(0, w - s.begin - fixed) >> (nq == 2 ? s.nq - 1 : 0);
 }
 
-// W work items cut into N shares: share c starts at c W / N, at a pair's tile rounded down to its
-// first item.
+// W work items cut into N shares: share c starts at c W / N, rounded down to where a tile (or,
+// in a unit's fixed part and its first tile, the unit) begins.
 struct Cut {
-    int W, N, q, r;                                 // W = q N + r
+    int W, N, q, r, fixed;                          // W = q N + r
+    __device__ int raw(int c) const { return q * c + r * c / N; }                  // r c < N^2
     __device__ int start(const SeqTable &st, int c, int tpt, int row_tiles, int nq) const {
-        int w = q * c + r * c / N;                  // r c < N^2
-        if (nq == 2 && c > 0 && c < N) {
+        int w = raw(c);
+        if ((nq == 2 || fixed) && c > 0 && c < N) {
             Segment s;
-            locate(st, st.find(w), w, tpt, row_tiles, nq, s);
-            w = s.unit_w + (s.first << (s.nq - 1));
+            locate(st, st.find(w), w, tpt, row_tiles, nq, fixed, s);
+            w = s.first == 0 ? s.begin : s.begin + fixed + (s.first << (nq == 2 ? s.nq - 1 : 0));
         }
         return w;
     }
@@ -258,11 +270,10 @@ struct Cut {
 
 // The CTAs that hold tiles of the unit, counted from the one that holds its first.
 __device__ __forceinline__ int parts_of(const Cut &cut, const Segment &s) {
-    const int last = s.unit_w + s.tiles * s.nq - 1;                // the last tile's last item
     int lo = blockIdx.x, hi = cut.N - 1;
-    while (lo < hi) {                               // the last share that starts at or before it
+    while (lo < hi) {                               // the last share that starts before the unit's end
         const int mid = (lo + hi + 1) >> 1;
-        if (cut.q * mid + cut.r * mid / cut.N <= last) lo = mid;
+        if (cut.raw(mid) < s.end) lo = mid;
         else hi = mid - 1;
     }
     return lo - static_cast<int>(blockIdx.x) + 1;
@@ -270,14 +281,14 @@ __device__ __forceinline__ int parts_of(const Cut &cut, const Segment &s) {
 
 // Walks a CTA's share [w, w1) unit by unit.
 struct Cursor {
-    int w, w1, b;
+    int w, w1, b, fixed;
     __device__ bool next(const SeqTable &st, int tpt, int row_tiles, int nq, Segment &s) {
         if (w >= w1) return false;
         while (st.prefix[b + 1] <= w) ++b;
-        locate(st, b, w, tpt, row_tiles, nq, s);
-        const int two = nq == 2 ? s.nq - 1 : 0;
-        s.count = min((w1 - w) >> two, s.tiles - s.first);
-        w += s.count << two;
+        locate(st, b, w, tpt, row_tiles, nq, fixed, s);
+        if (w1 >= s.end) s.count = s.tiles - s.first;
+        else s.count = ((w1 - s.begin - fixed) >> (nq == 2 ? s.nq - 1 : 0)) - s.first;
+        w = min(w1, s.end);
         return true;
     }
 };
@@ -333,13 +344,14 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     st.slot = st.prefix + kMaxSeqs + 4;
     st.len = st.slot + kMaxSeqs;
     st.n = st.len + kMaxSeqs;
+    st.units = st.n + kMaxSeqs;
     st.nb = ta.nb;
     float *xch = reinterpret_cast<float *>(smem_raw + P::OFF_XCH);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem_raw + P::OFF_BAR);
     uint64_t *full = bar, *empty = bar + P::NST, *q_full = bar + 2 * P::NST, *q_empty = q_full + 1;
     uint64_t *s_full = q_empty + 1, *p_full = s_full + 2 * NG, *o_done = p_full + 2 * NG, *drain = o_done + 2 * NG;   // [group][2]; drain [group]
     unsigned long long *odd = reinterpret_cast<unsigned long long *>(drain + NG);         // [group][2]
-    int *warp_sum = reinterpret_cast<int *>(odd + 2 * NG);                                // [warps]
+    int2 *warp_sum = reinterpret_cast<int2 *>(odd + 2 * NG);                              // [warps]
     Cut *cut = reinterpret_cast<Cut *>(warp_sum + P::THREADS / 32);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cut + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -371,13 +383,17 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     pdl_wait();
     pdl_release();
     // ---- the sequences' table: the work before each
-    int before = 0;
+    int before = 0, units = 0;
     for (int i0 = 0; i0 < ta.nb; i0 += P::THREADS) {
         const int i = i0 + tid;
-        int mine = 0;
+        int mine = 0, own_units = 0;
         if (i < ta.nb) {
             const Seq q = load_seq(a.s, ta.b0 + i);
-            if (!q.bad) mine = Shape(q.len, q.n, ta.tpt, ta.row_tiles, NQ).per_head() * a.s.Hkv;
+            if (!q.bad) {
+                const Shape sh(q.len, q.n, ta.tpt, ta.row_tiles, NQ);
+                mine = sh.per_head(0) * a.s.Hkv;
+                own_units = sh.units() * a.s.Hkv;
+            }
             st.slot[i] = q.slot;
             st.len[i] = q.len;
             st.n[i] = q.n;
@@ -388,35 +404,40 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     for (int u = 0; u < per; ++u) ta.rec[i * per + u] = make_int4(0, 0, 0, 0);
             }
         }
-        int incl = mine;
+        int incl = mine, incl_u = own_units;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
+            const int y = __shfl_up_sync(0xffffffffu, incl, off), z = __shfl_up_sync(0xffffffffu, incl_u, off);
+            if (lane >= off) incl += y, incl_u += z;
         }
         if (i0 > 0) __syncthreads();                // the sums of the round before have been read
-        if (lane == 31) warp_sum[warp] = incl;
+        if (lane == 31) warp_sum[warp] = make_int2(incl, incl_u);
         __syncthreads();
         const int warps = min(P::THREADS / 32, (ta.nb - i0 + 31) / 32);
         for (int w = 0; w < warps; ++w) {
-            if (w == warp && i < ta.nb) st.prefix[i] = before + incl - mine;
-            before += warp_sum[w];
+            if (w == warp && i < ta.nb) {
+                st.prefix[i] = before + incl - mine;
+                st.units[i] = units + incl_u - own_units;
+            }
+            before += warp_sum[w].x;
+            units += warp_sum[w].y;
         }
     }
+    // (every thread has the totals)
+    const int fixed = before >= kFixedFrom * static_cast<int>(gridDim.x) ? kFixed<NQ> : 0;
+    if (fixed)
+        for (int i = tid; i < ta.nb; i += P::THREADS) st.prefix[i] += fixed * st.units[i];
     if (tid == 0) {
-        st.prefix[ta.nb] = before;
-        const int most = NQ == 2 && before > 1 ? before / 2 : before;     // every share has a tile (of a pair, too)
+        const int W = before + fixed * units, most = NQ == 2 && W > 1 ? W / 2 : W;         // every share has a tile
         const int N = min(most, static_cast<int>(gridDim.x));
-        cut->W = before;
-        cut->N = N;
-        cut->q = N ? before / N : 0;
-        cut->r = N ? before % N : 0;
+        st.prefix[ta.nb] = W;
+        *cut = Cut{W, N, N ? W / N : 0, N ? W % N : 0, fixed};
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Cursor cur{0, 0, 0};
+    Cursor cur{0, 0, 0, fixed};
     if (static_cast<int>(blockIdx.x) < cut->N) {
         cur.w = cut->start(st, blockIdx.x, ta.tpt, ta.row_tiles, NQ);
         cur.w1 = cut->start(st, blockIdx.x + 1, ta.tpt, ta.row_tiles, NQ);
