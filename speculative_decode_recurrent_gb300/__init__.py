@@ -564,7 +564,10 @@ class AttnLayer:
         c = cache.d
         self._d, self.cache, self.layer, self.status = AttnDims.from_buffer_copy(dims), cache, layer, cache.status
         self._rope = None if rope is None else RopeDims.from_buffer_copy(rope)
-        self._ref, self._n = ctypes.byref(self._d), c.d
+        self._ref, self._B, self._T, self._Hq = ctypes.byref(self._d), dims.B, dims.T, dims.Hq
+        self._Hkv, self._n, self._rows = c.Hkv, c.d, dims.B * dims.T
+        self._heads = self._rows * dims.Hq                      # rows of queries
+        self._elems = self._heads * c.d
         dev = cache.status.device
         need = cache._lib.gdn_attn_workspace(cache._c, self._ref) if dims.T <= 64 else 0
         _check("gdn_attn_workspace", min(need, 0))
@@ -587,7 +590,7 @@ class AttnLayer:
     def _block(self, t, heads, name):
         """Address and token stride of q, k or v: [B, T, heads, d], dense within a token, the
         tokens evenly spaced."""
-        B, T, n = self._d.B, self._d.T, self._n
+        B, T, n = self._B, self._T, self._n
         if t.shape != (B, T, heads, n):
             raise ValueError(f"{name}: expected shape {(B, T, heads, n)}, got {tuple(t.shape)}")
         if not t.is_cuda:
@@ -606,30 +609,29 @@ class AttnLayer:
     def stage(self, q, k, v, q_out, pos=None, draft_len=None, stream=None):
         """Norm and rotate q [B, T, Hq, d] into ``q_out`` and k [B, T, Hkv, d] into the cache's
         draft rows, v beside it.  q, k and v may be views of one projection's output."""
-        d, c, r = self._d, self.cache.d, self._rope
-        if r is None:
+        if self._rope is None:
             raise ValueError("stage: this layer was made without rope and norm weights")
-        r = RopeDims.from_buffer_copy(r)
-        pq, r.q_stride = self._block(q, d.Hq, "q")
-        pk, r.k_stride = self._block(k, c.Hkv, "k")
-        pv, r.v_stride = self._block(v, c.Hkv, "v")
-        n = d.B * d.T
+        r = RopeDims.from_buffer_copy(self._rope)
+        pq, r.q_stride = self._block(q, self._Hq, "q")
+        pk, r.k_stride = self._block(k, self._Hkv, "k")
+        pv, r.v_stride = self._block(v, self._Hkv, "v")
         wq, wk, tab = self._w
+        cache = self.cache
         rc = self._lib.gdn_attn_stage(
-            self.cache._c, self.layer, self._ref, ctypes.byref(r), self._idx,
-            None if draft_len is None else _in(draft_len, _I32, d.B, "draft_len"), pq, pk, pv,
-            None if pos is None else _in(pos, _I32, n, "pos"), wq, wk, tab,
-            _in(q_out, self._dtype, n * d.Hq * c.d, "q_out"), self.cache._status, self._stream(stream))
+            cache._c, self.layer, self._ref, ctypes.byref(r), self._idx,
+            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"), pq, pk, pv,
+            None if pos is None else _in(pos, _I32, self._rows, "pos"), wq, wk, tab,
+            _in(q_out, self._dtype, self._elems, "q_out"), cache._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_attn_stage", rc)
 
     def build_tree(self, parent, tree, pos=None, draft_len=None, stream=None):
         """Ancestor words ``tree`` (int64 [B, T]) and rotation positions ``pos`` (int32 [B, T])
         of a token tree given by its parents (int32 [B, T])."""
-        d, n = self._d, self.d.B * self.d.T
+        n = self._rows
         rc = self._lib.gdn_tree_build(
             self.cache._c, self._ref, self._idx,
-            None if draft_len is None else _in(draft_len, _I32, d.B, "draft_len"),
+            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"),
             _in(parent, _I32, n, "parent"), _in(tree, torch.int64, n, "tree"),
             None if pos is None else _in(pos, _I32, n, "pos"), self.cache._status, self._stream(stream))
         if rc:
@@ -638,15 +640,12 @@ class AttnLayer:
     def verify(self, q, out, lse=None, tree=None, draft_len=None, stream=None):
         """Attention of the block's rows q [B, T, Hq, d] over the cache into ``out`` (and
         ``lse`` fp32 [B, T, Hq]); ``tree`` int64 [B, T] ancestor words, None: a chain."""
-        d, t = self._d, self._dtype
-        n = d.B * d.T
-        h = n * d.Hq
-        e = h * self.cache.d.d
+        t, e, cache = self._dtype, self._elems, self.cache
         rc = self._lib.gdn_attn_verify(
-            self.cache._c, self.layer, self._ref, self._idx,
-            None if draft_len is None else _in(draft_len, _I32, d.B, "draft_len"), _in(q, t, e, "q"),
-            None if tree is None else _in(tree, torch.int64, n, "tree"), _in(out, t, e, "out"),
-            None if lse is None else _in(lse, _F32, h, "lse"), self._ws, self._ws_bytes,
-            self.cache._status, self._stream(stream))
+            cache._c, self.layer, self._ref, self._idx,
+            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"), _in(q, t, e, "q"),
+            None if tree is None else _in(tree, torch.int64, self._rows, "tree"), _in(out, t, e, "out"),
+            None if lse is None else _in(lse, _F32, self._heads, "lse"), self._ws, self._ws_bytes, cache._status,
+            self._stream(stream))
         if rc:
             raise GdnError("gdn_attn_verify", rc)

@@ -23,7 +23,7 @@ struct StageArgs {
     float eps;
 };
 
-constexpr int kStageThreads = 128;
+constexpr int kManyTokens = 4096;               // from which on a token gets one warp (some 27 tokens per SM)
 
 // Four consecutive elements, twice per lane.
 template <typename T> struct Vec4;
@@ -55,7 +55,7 @@ template <> struct Vec4<float> {
 
 // y = x r w of one row (eight elements per lane, L lanes), the rotated pairs turned.
 template <int D>
-__device__ __forceinline__ void norm_turn(float (&x)[8], const float *w, int a, int b, float eps, bool turned, bool half,
+__device__ __forceinline__ void norm_turn(float (&x)[8], float4 wa, float4 wb, float eps, bool turned, bool half,
                                           const float (&cs)[4], const float (&sn)[4])
 {
     float2 y[4], sq = make_float2(0.f, 0.f);
@@ -68,7 +68,6 @@ __device__ __forceinline__ void norm_turn(float (&x)[8], const float *w, int a, 
 #pragma unroll
     for (int off = D / 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
     const float r = rsqrtf(ss * (1.f / D) + eps);                 // within 2 ulp
-    const float4 wa = *reinterpret_cast<const float4 *>(w + a), wb = *reinterpret_cast<const float4 *>(w + b);
     const float2 wv[4] = {make_float2(wa.x, wa.y), make_float2(wa.z, wa.w), make_float2(wb.x, wb.y), make_float2(wb.z, wb.w)};
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], make_float2(r, r)), wv[e]);
@@ -91,15 +90,18 @@ __device__ __forceinline__ void norm_turn(float (&x)[8], const float *w, int a, 
     for (int e = 0; e < 4; ++e) x[2 * e] = y[e].x, x[2 * e + 1] = y[e].y;
 }
 
-// One CTA per token; D / 8 lanes per row (head of q, k or v).  A lane holds elements [a, a + 4) and
+// A CTA of W warps per token; D / 8 lanes per row (head of q, k or v).  A lane holds elements [a, a + 4) and
 // [b, b + 4) of its row: with b = a + rot / 2 among the rotated dims of the half style, so that the
 // pairs meet in one lane (turning them by shuffles cost eight more per row); elsewhere b = a + 4.
-// Bound by HBM at prompt lengths (by latency at a decode step's): NR rows per lane are requested before
-// the chain slot -> length -> page, and the rotation's row, are waited for.
-template <typename T, int D, bool HALF, int NR>
-__global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
+// NR rows per lane are requested before the chain slot -> length -> page, and the rotation's row, are
+// waited for.  Few tokens are bound by that chain, and four warps share a token's rows (W 4: B 32,
+// T 16, 20 heads of 128 in 3.4 us, with one warp 5.9); many are bound by instructions and then HBM,
+// and one warp a token spends the least on the chain (W 1: 16,800 rows in use of 6 x 4096, 20 heads
+// of 256: 75 us, 0.75 of the HBM peak; W 4: 89).
+template <typename T, int D, bool HALF, int W, int NR>
+__global__ void __launch_bounds__(32 * W) stage_kernel(const StageArgs a)
 {
-    constexpr int L = D / 8, GROUPS = kStageThreads / L;
+    constexpr int L = D / 8, GROUPS = 32 * W / L;
     using V = Vec4<T>;
     using Raw = typename V::Raw;
     const int tok = blockIdx.x, b = tok / a.s.T, t = tok - b * a.s.T;
@@ -135,6 +137,8 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
         }
     };
     request(0);
+    // most rows are queries': their weights stay in registers
+    const float4 wqa = *reinterpret_cast<const float4 *>(a.qw + ea), wqb = *reinterpret_cast<const float4 *>(a.qw + eb);
     int len = 0, bad = 0;
     if (slot < 0 || slot >= a.s.n_slot) bad = GDN_STATUS_BAD_SLOT;
     else {
@@ -183,7 +187,12 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
                 V::unpack(yb, xb);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = xa[e], x[4 + e] = xb[e];
-                norm_turn<D>(x, is_q ? a.qw : a.kw, ea, eb, a.eps, turned, HALF, cs, sn);
+                float4 wa = wqa, wb = wqb;
+                if (!is_q) {
+                    wa = *reinterpret_cast<const float4 *>(a.kw + ea);
+                    wb = *reinterpret_cast<const float4 *>(a.kw + eb);
+                }
+                norm_turn<D>(x, wa, wb, a.eps, turned, HALF, cs, sn);
                 if (!is_v) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) xa[e] = x[e], xb[e] = x[4 + e];
@@ -208,10 +217,16 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
 }
 
 template <typename T, int D>
-cudaError_t launch_stage(const StageArgs &a, dim3 grid, cudaStream_t s) {
-    constexpr int NR = D == 256 ? 5 : D == 128 ? 3 : 2;           // 20 rows (16 + 2 + 2 heads) in one round
-    return a.style == GDN_ROPE_HALF ? launch_pdl(stage_kernel<T, D, true, NR>, grid, dim3(kStageThreads), 0, s, a)
-                                    : launch_pdl(stage_kernel<T, D, false, NR>, grid, dim3(kStageThreads), 0, s, a);
+cudaError_t launch_stage(const StageArgs &a, cudaStream_t s) {
+    constexpr int NR4 = D == 256 ? 5 : D == 128 ? 3 : 2;          // 20 rows (16 + 2 + 2 heads) in one round
+    const int tokens = a.s.B * a.s.T, W = tokens < kManyTokens ? 4 : 1;
+    const dim3 grid(tokens), block(32 * W);
+    const bool half = a.style == GDN_ROPE_HALF;
+    if (W == 4)
+        return half ? launch_pdl(stage_kernel<T, D, true, 4, NR4>, grid, block, 0, s, a)
+                    : launch_pdl(stage_kernel<T, D, false, 4, NR4>, grid, block, 0, s, a);
+    return half ? launch_pdl(stage_kernel<T, D, true, 1, 5>, grid, block, 0, s, a)
+                : launch_pdl(stage_kernel<T, D, false, 1, 5>, grid, block, 0, s, a);
 }
 
 // -------------------------------------------------------------- token trees
@@ -718,15 +733,14 @@ int gdn_attn_stage(const gdn_page_cache *c, int32_t layer, const gdn_attn_dims *
     StageArgs a{seq_args(c, d->B, d->T, state_idx, draft_len, status), q, k, v, pos, q_weight, k_weight, cos_sin,
                 q_out, static_cast<char *>(c->k) + off, static_cast<char *>(c->v) + off, r->q_stride, r->k_stride,
                 r->v_stride, d->Hq, r->rot, r->style, r->max_pos, r->eps};
-    const dim3 grid(d->B * d->T);
     cudaError_t err;
     if (c->dtype == GDN_DTYPE_BF16)
-        err = c->d == 64 ? launch_stage<__nv_bfloat16, 64>(a, grid, stream)
-              : c->d == 128 ? launch_stage<__nv_bfloat16, 128>(a, grid, stream)
-                            : launch_stage<__nv_bfloat16, 256>(a, grid, stream);
+        err = c->d == 64 ? launch_stage<__nv_bfloat16, 64>(a, stream)
+              : c->d == 128 ? launch_stage<__nv_bfloat16, 128>(a, stream)
+                            : launch_stage<__nv_bfloat16, 256>(a, stream);
     else
-        err = c->d == 64 ? launch_stage<float, 64>(a, grid, stream)
-              : c->d == 128 ? launch_stage<float, 128>(a, grid, stream) : launch_stage<float, 256>(a, grid, stream);
+        err = c->d == 64 ? launch_stage<float, 64>(a, stream)
+              : c->d == 128 ? launch_stage<float, 128>(a, stream) : launch_stage<float, 256>(a, stream);
     return err == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 

@@ -920,10 +920,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // A task is 32 rows (a lane each) and 8 output columns of a split unit; `wide` warps (a power of
 // two, about one for every four parts) take its parts in turn, and the first of them joins
 // their sums in a fixed order.  gridDim.y CTAs share a record's tasks.
-constexpr int kJoinWarps = 8;
-
-template <int D, int NQ>
-__global__ void __launch_bounds__(kJoinWarps * 32, 3) verify_tc_join_kernel(const TcArgs ta, int grid)
+template <int D, int NQ, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinWarps == 8 ? 3 : 1) verify_tc_join_kernel(const TcArgs ta, int grid)
 {
     const AttnArgs &a = ta.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1091,10 +1089,15 @@ int launch_tc(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a
         bool by_cta;
         const int recs = tc_records(c, d, ta.nb, &by_cta), tasks = NQ * (ta.rp / 32) * (D / 8);
         ta.by_cta = by_cta;
-        const int share = 8 * sm_count() / recs;                  // CTAs of a record: two or three waves
+        // Where records may be of many parts, 16 warps take a task's parts (one sequence of 131,001
+        // tokens, 2 key heads, 76 parts: 37.5 us against 40 with 8); elsewhere 8 do (700 tokens, 11 parts:
+        // 10.0 us against 10.9 with 16; 32 sequences: 44.5 against 46).  Two or three waves of CTAs.
+        const bool few = grid >= 32 * recs;
+        const int share = (few ? 4 : 8) * sm_count() / recs;
+        const dim3 jgrid(recs, share < 1 ? 1 : share > tasks ? tasks : share);
         if (launch_pdl(verify_tc_kernel<D, NQ>, dim3(grid), dim3(P::THREADS), P::BYTES, s, mq, mk, mv, ta) != cudaSuccess ||
-            launch_pdl(verify_tc_join_kernel<D, NQ>, dim3(recs, share < 1 ? 1 : share > tasks ? tasks : share),
-                       dim3(kJoinWarps * 32), 0, s, ta, grid) != cudaSuccess)
+            (few ? launch_pdl(verify_tc_join_kernel<D, NQ, 16>, jgrid, dim3(16 * 32), 0, s, ta, grid)
+                 : launch_pdl(verify_tc_join_kernel<D, NQ, 8>, jgrid, dim3(8 * 32), 0, s, ta, grid)) != cudaSuccess)
             return GDN_ERR_LAUNCH;
     }
     return GDN_OK;
