@@ -231,7 +231,8 @@ cudaError_t launch_stage(const StageArgs &a, cudaStream_t s) {
 
 // -------------------------------------------------------------- token trees
 // One warp per sequence, tokens lane and lane + 32.  The ancestors of a token are its
-// parent's and itself: pointer doubling joins them in six rounds.
+// parent's and itself: pointer doubling joins them in six rounds (a chain of 64 followed token by
+// token would take 64).  Bound by latency.
 __global__ void __launch_bounds__(128) tree_kernel(const SeqArgs s, const int32_t *parent, uint64_t *tree, int32_t *pos)
 {
     __shared__ uint64_t bits[4][64];
@@ -290,8 +291,8 @@ __global__ void __launch_bounds__(128) tree_kernel(const SeqArgs s, const int32_
 // tiles of 32 tokens arrive by cp.async, the next pair while the present one is used.  A warp owns
 // 8 rows: their scores (2 rows x 4 keys a lane), their running maximum and denominator, and their
 // D output columns, so the only barriers are those around the tiles.  Products go two at a time
-// (fma.rn.f32x2).  Bound by shared-memory reads (16 of 16 bytes for 128 products) from
-// some 16 rows per key head on, by HBM and latency below.
+// (fma.rn.f32x2).  B 5, T 7, 12 query and 3 key heads of 64 over 333 to 2100 tokens: 17.5 us, 8 of them the
+// products and shared-memory reads of a CTA's two tiles, 5 the join, the rest latency.
 constexpr int kRT = 32, kKT = 32;               // rows and keys of a tile
 constexpr int kCoreThreads = 128;
 
@@ -631,7 +632,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // moves it row by row.  path[j] >= j and path increases, so a row is read before any
 // later row's move writes over it; eight rows are read before the first of them is
 // written (the eight writes go to rows below every row read later).  The length
-// is written once every CTA of the cluster has read it (new_len may be seq_len).
+// is written once every CTA of the cluster has read it (new_len may be seq_len).  Bound by HBM where
+// there is much to move (96 sequences, T 64, 12 layers, 4 heads of 128: 149 MB in 28 us, 0.77 of
+// the peak), by its chain of dependent reads elsewhere (32 sequences, 6 layers: 4.6 us).
 __global__ void __launch_bounds__(kAcceptThreads) __cluster_dims__(kAcceptCluster, 1, 1)
 accept_rows_kernel(const AcceptArgs a)
 {
