@@ -57,8 +57,8 @@ template <int D, int NQ> struct TcPlan {
     static constexpr int THREADS = ROWS + 32 * (2 + NG);
     static constexpr int QTILE = kRows * D * 2;
     static constexpr int OFF_RING = NQ * QTILE;                 // after the queries
-    static constexpr int OFF_SEQ = OFF_RING + NST * STAGE;      // prefix, slot, len, n, units
-    static constexpr int OFF_XCH = OFF_SEQ + (5 * kMaxSeqs + 4) * 4;                      // two words per row thread
+    static constexpr int OFF_SEQ = OFF_RING + NST * STAGE;      // prefix, slot, len, n, live, units
+    static constexpr int OFF_XCH = OFF_SEQ + (6 * kMaxSeqs + 4) * 4;                      // two words per row thread
     static constexpr int OFF_BAR = OFF_XCH + ROWS * 8;
     static constexpr int BYTES = OFF_BAR + 640;
     static constexpr int TCOLS = 2 * kKeys + D;                 // TMEM of a group: S in [0, 64) and [64, 128), then O
@@ -178,8 +178,8 @@ __device__ __forceinline__ float ex2(float x) {
 // unit counts `fixed` more: beginning and ending one costs a CTA as much as some tiles.
 struct Shape {
     int live, dead, pairs, single, tiles, total;    // total: keys
-    __device__ Shape(int len, int n, int tpt, int row_tiles, int nq) {
-        live = (n + tpt - 1) / tpt;
+    __device__ Shape(int len, int n, int live_, int row_tiles, int nq) {
+        live = live_;
         dead = row_tiles - live;
         pairs = nq == 2 ? live / 2 : 0;
         single = live - 2 * pairs;
@@ -196,9 +196,18 @@ template <int NQ> constexpr int kFixed = NQ == 2 ? 8 : 4;
 constexpr int kFixedFrom = 16;                      // tiles a CTA from which on it is counted: below, every tile
                                                     // on a CTA of its own is faster
 
+// a / b for quotients below 2^20 (a >= 0, b > 0): one step corrects the float quotient.  The compiler's
+// integer division takes three times as long, and several follow one another before the first load.
+__device__ __forceinline__ int quotient(int a, int b) {
+    int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+    const int r = a - q * b;
+    return r < 0 ? q - 1 : r >= b ? q + 1 : q;
+}
+
 struct SeqTable {
     int *prefix;                                    // [nb + 1] work before each sequence
     int *slot, *len, *n;                            // [nb]
+    int *live;                                      // [nb] row tiles with rows in use
     int *units;                                     // [nb] units before each sequence
     int nb;
     // The last sequence that starts at or before w, among those with work.
@@ -221,14 +230,14 @@ struct Segment {
 };
 
 // The unit that holds work item w, and the tile of it.
-__device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int tpt, int row_tiles, int nq, int fixed, Segment &s) {
-    const Shape sh(st.len[b], st.n[b], tpt, row_tiles, nq);
+__device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int row_tiles, int nq, int fixed, Segment &s) {
+    const Shape sh(st.len[b], st.n[b], st.live[b], row_tiles, nq);
     const int in_b = w - st.prefix[b], per = sh.per_head(fixed);
     s.b = b;
     s.slot = st.slot[b];
     s.len = st.len[b];
     s.n = st.n[b];
-    s.h = in_b / per;
+    s.h = quotient(in_b, per);
     int r = in_b - s.h * per, size = 2 * sh.tiles + fixed, u;
     const int head = w - r, paired = sh.pairs * size, live = paired + sh.single * (sh.tiles + fixed);
     s.nq = 1;                                       // (nq is a constant: with 1 it stays one)
@@ -236,18 +245,18 @@ __device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int tpt
     s.total = sh.total;
     int start = 0;
     if (nq == 2 && r < paired) {
-        u = sh.pairs == 1 ? 0 : r / size;
+        u = sh.pairs == 1 ? 0 : quotient(r, size);
         s.nq = 2;
         s.rt = 2 * u;
     } else if (r < live) {
         start = nq == 2 ? paired : 0;
         size = sh.tiles + fixed;
-        u = sh.single == 1 ? 0 : (r - start) / size;
+        u = sh.single == 1 ? 0 : quotient(r - start, size);
         s.rt = 2 * sh.pairs + u;
     } else {
         start = live;
         size = 1 + fixed;
-        u = (r - start) / size;
+        u = quotient(r - start, size);
         s.rt = sh.live + u;
         s.tiles = 1;
         s.total = 0;
@@ -261,17 +270,11 @@ __device__ __forceinline__ void locate(const SeqTable &st, int b, int w, int tpt
 // in a unit's fixed part and its first tile, the unit) begins.
 struct Cut {
     int W, N, q, r, fixed;                          // W = q N + r
-    __device__ int raw(int c) const { return q * c + r * c / N; }                  // r c < N^2
-    __device__ int start(const SeqTable &st, int c, int tpt, int row_tiles, int nq) const {
-        int w = raw(c);
-        if ((nq == 2 || fixed) && c > 0 && c < N) {
-            Segment s;
-            locate(st, st.find(w), w, tpt, row_tiles, nq, fixed, s);
-            w = s.first == 0 ? s.begin : s.begin + fixed + (s.first << (nq == 2 ? s.nq - 1 : 0));
-        }
-        return w;
-    }
+    __device__ int raw(int c) const { return q * c + quotient(r * c, N); }         // r c < N^2
 };
+template <int NQ> __device__ __forceinline__ int rounded(const Segment &s, int fixed) {
+    return s.first == 0 ? s.begin : s.begin + fixed + (s.first << (NQ == 2 ? s.nq - 1 : 0));
+}
 
 // The CTAs that hold tiles of the unit, counted from the one that holds its first.
 __device__ __forceinline__ int parts_of(const Cut &cut, const Segment &s) {
@@ -287,13 +290,16 @@ __device__ __forceinline__ int parts_of(const Cut &cut, const Segment &s) {
 // Walks a CTA's share [w, w1) unit by unit.
 struct Cursor {
     int w, w1, b, fixed;
-    __device__ bool next(const SeqTable &st, int tpt, int row_tiles, int nq, Segment &s) {
-        if (w >= w1) return false;
-        while (st.prefix[b + 1] <= w) ++b;
-        locate(st, b, w, tpt, row_tiles, nq, fixed, s);
+    __device__ void take(int nq, Segment &s) {      // as much of the unit at w as is in the share
         if (w1 >= s.end) s.count = s.tiles - s.first;
         else s.count = ((w1 - s.begin - fixed) >> (nq == 2 ? s.nq - 1 : 0)) - s.first;
         w = min(w1, s.end);
+    }
+    __device__ bool next(const SeqTable &st, int row_tiles, int nq, Segment &s) {
+        if (w >= w1) return false;
+        while (st.prefix[b + 1] <= w) ++b;
+        locate(st, b, w, row_tiles, nq, fixed, s);
+        take(nq, s);
         return true;
     }
 };
@@ -349,7 +355,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     st.slot = st.prefix + kMaxSeqs + 4;
     st.len = st.slot + kMaxSeqs;
     st.n = st.len + kMaxSeqs;
-    st.units = st.n + kMaxSeqs;
+    st.live = st.n + kMaxSeqs;
+    st.units = st.live + kMaxSeqs;
     st.nb = ta.nb;
     float *xch = reinterpret_cast<float *>(smem_raw + P::OFF_XCH);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem_raw + P::OFF_BAR);
@@ -394,8 +401,10 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         int mine = 0, own_units = 0;
         if (i < ta.nb) {
             const Seq q = load_seq(a.s, ta.b0 + i);
+            const int live = q.bad ? 0 : quotient(q.n + ta.tpt - 1, ta.tpt);
+            st.live[i] = live;
             if (!q.bad) {
-                const Shape sh(q.len, q.n, ta.tpt, ta.row_tiles, NQ);
+                const Shape sh(q.len, q.n, live, ta.row_tiles, NQ);
                 mine = sh.per_head(0) * a.s.Hkv;
                 own_units = sh.units() * a.s.Hkv;
             }
@@ -436,17 +445,44 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int W = before + fixed * units, most = NQ == 2 && W > 1 ? W / 2 : W;         // every share has a tile
         const int N = min(most, static_cast<int>(gridDim.x));
         st.prefix[ta.nb] = W;
-        *cut = Cut{W, N, N ? W / N : 0, N ? W % N : 0, fixed};
+        const int q = N ? W / N : 0;
+        *cut = Cut{W, N, q, W - q * N, fixed};
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // This CTA's share and its first unit: every warp for itself, the share's two ends in its even and
+    // odd lanes.
+    const Cut c = *cut;
     Cursor cur{0, 0, 0, fixed};
-    if (static_cast<int>(blockIdx.x) < cut->N) {
-        cur.w = cut->start(st, blockIdx.x, ta.tpt, ta.row_tiles, NQ);
-        cur.w1 = cut->start(st, blockIdx.x + 1, ta.tpt, ta.row_tiles, NQ);
-        cur.b = st.find(cur.w);
+    Segment s;
+    const bool any_work = static_cast<int>(blockIdx.x) < c.N;
+    if (any_work) {
+        const int raw0 = c.raw(blockIdx.x), raw1 = c.raw(blockIdx.x + 1);       // (the last share ends at W)
+        const bool odd_lane = lane & 1;
+        const int raw = odd_lane ? raw1 : raw0;
+        int seq;
+        if (ta.nb <= 32) {
+            const int pre = lane < ta.nb ? st.prefix[lane] : 0x7fffffff;
+            const uint32_t m0 = __ballot_sync(0xffffffffu, pre <= raw0), m1 = __ballot_sync(0xffffffffu, pre <= raw1);
+            seq = 31 - __clz(odd_lane ? m1 : m0);
+        } else {
+            seq = st.find(raw);
+        }
+        int w = raw;
+        if (raw < c.W) {
+            locate(st, seq, raw, ta.row_tiles, NQ, fixed, s);
+            w = rounded<NQ>(s, fixed);
+        }
+        __syncwarp();
+        int *word = reinterpret_cast<int *>(&s);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(Segment) / 4); ++i) word[i] = __shfl_sync(0xffffffffu, word[i], 0);
+        cur.w = __shfl_sync(0xffffffffu, w, 0);
+        cur.w1 = __shfl_sync(0xffffffffu, w, 1);
+        cur.b = s.b;
+        cur.take(NQ, s);
     }
     // GDN_FLAG_TEST_EXPIRE: the wait-expiry exit, with nothing issued before it
     if (a.flags & GDN_FLAG_TEST_EXPIRE) {
@@ -470,7 +506,6 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         return false;
     };
     if (ta.by_cta && tid == P::ROWS - 1) ta.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
-    Segment s;
     uint32_t pos = 0;                               // load warps: tiles loaded (of keys, or of values)
     bool issued = false;                            // MMA warps: some MMA
     uint32_t queries = 0;                           // first MMA warp: loads of queries
@@ -484,7 +519,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int ps = shift < 6 ? shift : 6;                              // rows of a copy: 16, 32 or 64
         const CUtensorMap *map = kv ? &tm_v : &tm_k;
         bool ok = !*abort;
-        while (ok && cur.next(st, ta.tpt, ta.row_tiles, NQ, s)) {
+        for (bool have = ok && any_work; have; have = ok && cur.next(st, ta.row_tiles, NQ, s)) {
             const int32_t *tab = a.s.table + static_cast<size_t>(s.slot) * a.s.max_pages;
             const int count = __shfl_sync(0xffffffffu, s.count, 0), first = __shfl_sync(0xffffffffu, s.first, 0);
             const int total = __shfl_sync(0xffffffffu, s.total, 0), head = __shfl_sync(0xffffffffu, s.h, 0);
@@ -559,7 +594,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             __syncwarp();
             ++queries;
         };
-        bool have = ok && cur.next(st, ta.tpt, ta.row_tiles, NQ, s);
+        bool have = ok && any_work;
         while (have) {
             const bool alternate = NG == 2 && (NQ == 1 || s.nq == 1);
             const int step = alternate ? 2 : 1, off = alternate ? (group ^ tile0) & 1 : 0;
@@ -567,7 +602,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const bool twice = __shfl_sync(0xffffffffu, alternate ? 1 : 0, 0) != 0;
             const uint64_t dq = desc_sw128(saddr(sQ) + (alternate ? 0 : group * P::QTILE));
             if (group == 0 && segs == 0) load_queries(s);
-            const bool more = group == 0 && cur.next(st, ta.tpt, ta.row_tiles, NQ, next);
+            const bool more = group == 0 && cur.next(st, ta.row_tiles, NQ, next);
             bool wanted = more;                     // the next unit's queries, once all scores of this one are done
             ok = ok && __all_sync(0xffffffffu, wait(q_full, segs & 1)) != 0;
             ++segs;
@@ -649,7 +684,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 have = ok && more;
                 s = next;
             } else {
-                have = ok && cur.next(st, ta.tpt, ta.row_tiles, NQ, s);
+                have = ok && cur.next(st, ta.row_tiles, NQ, s);
             }
         }
     } else {
@@ -669,7 +704,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc_fence_after();
         };
         Segment next;
-        bool more = cur.next(st, ta.tpt, ta.row_tiles, NQ, s);
+        bool more = any_work;
         auto token_of = [&](const Segment &u) {      // this thread's draft token in unit u
             return (u.rt + (NQ == 2 && u.nq == 2 ? group : 0)) * ta.tpt + r_in / a.G;
         };
@@ -808,7 +843,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
             }
             tile0 += s.count;
-            more = cur.next(st, ta.tpt, ta.row_tiles, NQ, next);
+            more = cur.next(st, ta.row_tiles, NQ, next);
             next_bits = more ? word_of(next) : 0ull;
             // ---- the unit's result, or this CTA's part of it
             if (mine > 0) wait_rows(&od[(g - 1) & 1], ((g - 1) >> 1) & 1);
