@@ -13,7 +13,7 @@
 // What bounds it: the keys and values are read once for all T x (Hq / Hkv) rows of a key head,
 // so up to about 128 rows the tiles go by at the HBM rate (d 128: 1400 cycles each); above, by the softmax
 // and the MMAs (a pair of row tiles: 2400 cycles a tile of keys).  B 32, T 16, Hq 16, Hkv 2, d 128 over 900 to
-// 8000 tokens: 44.7 us with the join, 3.4 TB/s; B 128, T 8, d 256: 105 us, 5.1 TB/s; one token over 700: 10 us.  Some 5 us
+// 8000 tokens: 43.1 us with the join, 3.6 TB/s; B 128, T 8, d 256: 104 us, 5.2 TB/s; one token over 700: 10 us.  Some 4 us
 // pass before the first tile (length, share, unit, page, first load), 3 at the end.
 //
 // Work.  A unit is (sequence, key head, tile of 128 rows or pair of such tiles); its keys come in
@@ -1130,8 +1130,8 @@ int launch_tc(const gdn_page_cache *c, const gdn_attn_dims *d, const AttnArgs &a
         const int recs = tc_records(c, d, ta.nb, &by_cta), tasks = NQ * (ta.rp / 32) * (D / 8);
         ta.by_cta = by_cta;
         // Where records may be of many parts, 16 warps take a task's parts (one sequence of 131,001
-        // tokens, 2 key heads, 76 parts: 37.5 us against 40 with 8); elsewhere 8 do (700 tokens, 11 parts:
-        // 10.0 us against 10.9 with 16; 32 sequences: 44.5 against 46).  Two or three waves of CTAs.
+        // tokens, 2 key heads, 76 parts: 36.1 us against 38.9 with 8); elsewhere 8 do (700 tokens, 11 parts:
+        // 9.9 us against 10.7 with 16; 32 sequences: 42.8 against 44.3).  Two or three waves of CTAs.
         const bool few = grid >= 32 * recs;
         const int share = (few ? 4 : 8) * sm_count() / recs;
         const dim3 jgrid(recs, share < 1 ? 1 : share > tasks ? tasks : share);
