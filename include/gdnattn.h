@@ -59,7 +59,7 @@ typedef struct {
     int32_t max_pages;  /* block-table entries per slot, 1..2^18; max_pages * page <= 2^24 */
     int32_t n_page;     /* pages, >= 1; n_page * Hkv * page < 2^31 */
     int32_t page;       /* tokens per page: 16, 32, 64 or 128 */
-    int32_t n_layer;    /* >= 1 */
+    int32_t n_layer;    /* 1..32767 */
     int32_t Hkv;        /* key/value heads, 1..128 */
     int32_t d;          /* head dim: 64, 128 or 256 */
     int32_t dtype;      /* GDN_DTYPE_BF16 or GDN_DTYPE_F32 (q, k, v and out too) */

@@ -94,7 +94,8 @@ inline int elem_size(int dtype) { return dtype == GDN_DTYPE_BF16 ? 2 : 4; }
 inline int check_cache(const gdn_page_cache *c) {
     if (!c) return GDN_ERR_NULL;
     if (c->dtype != GDN_DTYPE_BF16 && c->dtype != GDN_DTYPE_F32) return GDN_ERR_DTYPE;
-    if (c->n_slot < 0 || c->max_pages < 1 || c->n_page < 1 || c->n_layer < 1 || c->Hkv < 1 || c->Hkv > 128)
+    if (c->n_slot < 0 || c->max_pages < 1 || c->n_page < 1 || c->n_layer < 1 || c->n_layer > 32767 ||
+        c->Hkv < 1 || c->Hkv > 128)
         return GDN_ERR_DIMS;
     if (page_shift(c->page) < 0 || (c->d != 64 && c->d != 128 && c->d != 256)) return GDN_ERR_DIMS;
     if (c->max_pages > 1 << 18 || static_cast<long long>(c->max_pages) * c->page > 1 << 24)

@@ -418,7 +418,7 @@ int gdn_pages_copy(const gdn_page_cache *c, int32_t n, const int32_t *copies, in
     if (const int rc = check_pool(c, n)) return rc;
     if (n == 0) return GDN_OK;
     if (!c->k || !c->v || !copies || !status) return GDN_ERR_NULL;
-    if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || c->n_layer > 32767) return GDN_ERR_DIMS;
+    if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16)) return GDN_ERR_DIMS;
     const int vecs = c->Hkv * c->page * (c->d * elem_size(c->dtype) / 16);
     return launch_pdl(copy_pages_kernel, dim3(n, 2 * c->n_layer), dim3(256), 0, stream, c->k, c->v, copies, c->n_page,
                       vecs, status) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;

@@ -84,6 +84,15 @@ def test_bad_rotation_refused(kw):
     assert stage(r=rope(**kw)) == -2
 
 
+def test_more_layers_than_a_call_can_count_refused():
+    # an accept of 128 fp32 heads of 256 counts 2^14 columns per layer, in 32 bits
+    c, so = cache(n_layer=1 << 17, Hkv=128, d=256, dtype=lib.DTYPE_F32), lib.load()
+    p = ctypes.byref(c)
+    assert so.gdn_attn_accept(p, 2, 4, FAKE, FAKE, FAKE, FAKE, FAKE, None) == -2
+    assert so.gdn_pages_copy(p, 1, FAKE, FAKE, None) == -2
+    assert stage(cache(n_layer=32768)) == verify(cache(n_layer=32768)) == -2
+
+
 def test_null_and_misaligned_pointers_refused():
     so = lib.load()
     for i in (2, 3, 4, 6, 7, 8, 9, 10):                       # state_idx, draft_len and pos may be NULL
