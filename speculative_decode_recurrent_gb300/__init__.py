@@ -601,7 +601,7 @@ class AttnLayer:
         if se != 1 or (heads > 1 and sh != n):
             raise ValueError(f"{name}: the heads of a token must be dense")
         if T == 1:
-            st = sb if B > 1 else max(heads * n, st)
+            st = sb if B > 1 else heads * n              # a single token's stride says nothing
         elif B > 1 and sb != T * st:
             raise ValueError(f"{name}: tokens must be evenly spaced over the batch")
         return t.data_ptr(), st

@@ -237,6 +237,20 @@ def test_verify_long_contexts_are_split(dtype, lens, T, Hq, Hkv):
     assert torch.equal(first[0], r.out) and torch.equal(first[1], r.lse)     # the same bits again
 
 
+@pytest.mark.parametrize("lens,drafts,T,Hq,Hkv,d", [
+    ([30000, 17, 9000, 20011], [5, 5, 0, 3], 5, 8, 4, 64),                # one row tile
+    ([14000, 17, 0, 20011], [40, 40, 0, 17], 40, 32, 4, 128),             # a pair and one more; a pair; none
+    ([30000, 63, 64, 52000], [7, 7, 1, 2], 7, 16, 2, 256)])               # one group
+def test_verify_many_tiles_per_cta(lens, drafts, T, Hq, Hkv, d):
+    """Enough keys that a unit's beginning and end count as work."""
+    r = VerifyRun(lens, drafts, T, Hq, Hkv, d, 64, BF, seed=26)
+    r.call()
+    r.check()
+    first = r.out.clone(), r.lse.clone()
+    r.call()
+    assert torch.equal(first[0], r.out) and torch.equal(first[1], r.lse)     # the same bits again
+
+
 def test_verify_many_sequences():
     """More (sequence, head) units than resident CTAs, lengths from none to several tiles."""
     B = 300
@@ -422,6 +436,72 @@ def test_stage_faults():
     assert torch.equal(k[0, p, :, r], c.k[0, p, :, r])        # the skipped token's row
     p, r = c.cell(1, 33)
     assert not torch.equal(k[0, p, :, r], c.k[0, p, :, r])
+
+
+@pytest.mark.parametrize("d,dtype,pairs", [(64, BF, True), (128, F32, False), (256, BF, False)])
+def test_stage_many_tokens(d, dtype, pairs):
+    """Ragged prompts of some thousand tokens: a sample against the formula, and every row the same
+    bits as when the tokens come some hundred at a time (a row's arithmetic does not depend on how
+    many tokens a call has)."""
+    lib = _lib()
+    lens, drafts, T, Hq, Hkv, rot, eps = [3, 100, 0], [1700, 0, 1033], 1700, 6, 2, 48, 1e-6
+    c = R.CacheCase(lens, T, Hkv, d, 32, dtype, seed=71)
+    B, g, width, max_pos = len(lens), c.g, (Hq + 2 * Hkv) * d, max(lens) + T
+    rows = torch.randn(B, T, width, generator=g).to(dtype)
+    q, k, v = (x.unflatten(-1, (-1, d)) for x in rows.cuda().split([Hq * d, Hkv * d, Hkv * d], -1))
+    qw, kw = 1 + 0.3 * torch.randn(d, generator=g), 1 + 0.3 * torch.randn(d, generator=g)
+    a = torch.rand(max_pos, rot // 2, generator=g, dtype=torch.float64) * 6.28
+    tab = torch.cat([a.cos(), a.sin()], 1).float()
+    rope = lib.RopeDims(rot=rot, style=lib.ROPE_PAIRS if pairs else lib.ROPE_HALF, max_pos=max_pos, eps=eps)
+
+    def layer(cache, B, T, idx):
+        return lib.AttnLayer(lib.AttnDims(B=B, T=T, Hq=Hq, scale=1.0), cache, 0, rope, qw.cuda(), kw.cuda(), tab.cuda(),
+                             state_idx=idx.cuda())
+    whole, parts = lib.PagedCache(c.dims(lib), c.init()), lib.PagedCache(c.dims(lib), c.init())
+    q_out, intact = _guarded((B, T, Hq, d), dtype, 7.0)
+    layer(whole, B, T, c.state_idx).stage(q, k, v, q_out, draft_len=torch.tensor(drafts, dtype=torch.int32).cuda())
+    other = torch.zeros(B, T, Hq, d, dtype=dtype, device="cuda")
+    for b in range(B):
+        idx = c.state_idx[b:b + 1]
+        for t in range(0, drafts[b], 300):
+            n = min(300, drafts[b] - t)
+            parts.seq_len[int(idx)] = lens[b] + t
+            layer(parts, 1, n, idx).stage(q[b:b + 1, t:t + n], k[b:b + 1, t:t + n], v[b:b + 1, t:t + n], other[b:b + 1, t:t + n])
+    torch.cuda.synchronize()
+    assert int(whole.status.item()) == int(parts.status.item()) == 0 and intact()
+    assert torch.equal(q_out, other)
+    np.testing.assert_array_equal(R.f64(whole.k.cpu()), R.f64(parts.k.cpu()))
+    np.testing.assert_array_equal(R.f64(whole.v.cpu()), R.f64(parts.v.cpu()))
+    x, tol, got = R.f64(rows), (d / 2 + 16) * 2.0 ** -24, q_out.cpu()
+    for b, t in [(0, 0), (0, 28), (0, 29), (0, 1699), (2, 0), (2, 517), (2, 1032)]:
+        p = lens[b] + t
+        cos, sin = R.f64(tab[p, :rot // 2]), R.f64(tab[p, rot // 2:])
+        y, size = R.norm_rotate(x[b, t, :Hq * d].reshape(Hq, d), R.f64(qw), eps, cos, sin, rot, pairs)
+        if dtype == BF:
+            assert_bf16_rounding(f"q {b} {t}", got[b, t], y, tol * size + 1e-30)
+        else:
+            assert (np.abs(R.f64(got[b, t]) - y) <= tol * size + 1e-30).all(), (b, t)
+
+
+def test_stage_single_token_of_any_stride():
+    """One token's stride says nothing: a row of a width that is no multiple of 16 bytes is taken."""
+    lib = _lib()
+    c = R.CacheCase([20], 1, 2, 64, 16, BF, seed=72)
+    rope = lib.RopeDims(rot=16, style=lib.ROPE_HALF, max_pos=64, eps=1e-6)
+    w, tab = torch.ones(64, device="cuda"), torch.rand(64, 16, generator=c.g).cuda()
+    row = torch.randn(1, 1, 8 * 64 + 4, generator=c.g).to(BF).cuda()
+    q, k, v = (x.unflatten(-1, (-1, 64)) for x in row[..., :8 * 64].split([4 * 64, 2 * 64, 2 * 64], -1))
+    got = []
+    for dense in (False, True):
+        cache = lib.PagedCache(c.dims(lib), c.init())
+        layer = lib.AttnLayer(lib.AttnDims(B=1, T=1, Hq=4, scale=1.0), cache, 0, rope, w, w, tab, state_idx=c.state_idx.cuda())
+        q_out = torch.zeros(1, 1, 4, 64, dtype=BF, device="cuda")
+        layer.stage(*((x.contiguous() for x in (q, k, v)) if dense else (q, k, v)), q_out)
+        torch.cuda.synchronize()
+        assert int(cache.status.item()) == 0
+        got.append((q_out, cache.k, cache.v))
+    for x, y in zip(*got):
+        np.testing.assert_array_equal(R.f64(x.cpu()), R.f64(y.cpu()))
 
 
 # ------------------------------------------------------------------------ trees
