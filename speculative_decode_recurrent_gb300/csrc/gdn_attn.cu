@@ -587,13 +587,20 @@ int sm_count() {
         return 0;
     return sms;
 }
-// Parts of the key axis: one wave of CTAs, each part at least two tiles of the longest
-// sequence that the block table can hold.
+// Parts of the key axis: the CTAs of as few whole waves as make kParts of them, of kWaves at most, each part
+// at least two tiles of the longest sequence that the block table can hold.  A wave alone makes two parts
+// or none where there are many units, and ragged batches end with the longest sequence's part: B 32, T 16,
+// 8 and 2 heads of 128 over 500 to 4747 tokens 369 us with one wave, 234 so; B 64, T 4, 16 and 4 heads over
+// 100 to 4000: 558 and 316; all sequences of one length cost the join instead (B 200, 128 tokens: 48 and
+// 54 us; B 32, 4000 tokens: 340 and 311).  More parts (12): 230 and 310 us, but 28 instead of 26 for B 16.
+constexpr int kParts = 8, kWaves = 6;
 int core_splits(const gdn_page_cache *c, const gdn_attn_dims *d) {
     const int ctas = c->d == 64 ? CorePlan<64>::CTAS : c->d == 128 ? CorePlan<128>::CTAS : CorePlan<256>::CTAS;
     const long long units = static_cast<long long>(d->B) * c->Hkv * core_row_tiles(c, d);
     const long long tiles = (static_cast<long long>(c->max_pages) * c->page + kKT - 1) / kKT;
-    long long want = units > 0 ? static_cast<long long>(ctas) * sm_count() / units : 1;
+    const long long wave = static_cast<long long>(ctas) * sm_count();
+    long long want = 1;
+    for (int k = 1; k <= kWaves && units > 0 && want < kParts; ++k) want = k * wave / units;
     if (want > tiles / 2) want = tiles / 2;
     return static_cast<int>(want < 1 ? 1 : want > 128 ? 128 : want);
 }
