@@ -21,7 +21,7 @@
 // balance and one long sequence fills the GPU.  A unit that one CTA covers is finished there; the
 // others leave partial results (o, m, l) that a second kernel joins in a fixed order.
 //
-// A CTA.  Two warps load (TMA, one copy per page and 64-column atom, through the block table) into a
+// A CTA.  Two warps load (TMA through the block table, one copy a tile or, of pages below 64, per page and atom) into a
 // ring of four tiles of keys and values.  Two groups of 256 threads with an MMA warp
 // each work side by side: on a pair of row tiles, both on every tile of keys; on a single one, on
 // every second tile, their results joined at the end (d = 256 has TMEM for one group).  A
@@ -511,8 +511,10 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint32_t queries = 0;                           // first MMA warp: loads of queries
     if (warp >= P::LOAD_WARP && warp < P::MMA_WARP) {
         // ------------------------------------------------------ loads
-        // The first warp loads the tiles of keys, the second those of values: a copy for each page of
-        // the tile and 64-column atom.  Lane c holds the page of place c in the block table's next 32
+        // The first warp loads the tiles of keys, the second those of values: one copy a tile, or one for
+        // each page and 64-column atom of it where pages are shorter.  (Where one key head has few rows, all
+        // warps with rows in use share a scheduler with the keys' warp, and its instructions count: B 64, T 4,
+        // 8 heads of 64 over 100 to 8000 tokens in pages of 64: 121 us, with the short pages' loop 134.)  Lane c holds the page of place c in the block table's next 32
         // entries, read 32 entries ahead; the copies are issued by one lane from values that are
         // the same in every lane (issued lane by lane, each cost 100 cycles).
         const int kv = warp - P::LOAD_WARP, shift = a.s.page_shift;
@@ -534,37 +536,51 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 return 0;
             };
             int ids = read_ids(0), ids_next = read_ids(32), base = 0;
-            for (int i = 0; i < count; ++i, ++pos) {
-                const int j0 = (first + i) * kKeys, at = (j0 >> shift) - p0;
-                if (at - base >= 32) {
-                    base += 32;
-                    ids = ids_next;
-                    ids_next = read_ids(base + 32);
+            auto tiles = [&](auto load) {
+                for (int i = 0; i < count; ++i, ++pos) {
+                    const int j0 = (first + i) * kKeys, at = (j0 >> shift) - p0;
+                    if (at - base >= 32) {
+                        base += 32;
+                        ids = ids_next;
+                        ids_next = read_ids(base + 32);
+                    }
+                    const uint32_t spos = 2 * pos + kv, stage = spos % P::NST, round = spos / P::NST;
+                    if (round > 0) ok = __all_sync(0xffffffffu, wait(&empty[stage], (round - 1) & 1)) != 0;
+                    if (!ok) break;
+                    load(j0, at - base, ring + stage * P::STAGE, &full[stage]);
+                    __syncwarp();
                 }
-                const uint32_t spos = 2 * pos + kv, stage = spos % P::NST, round = spos / P::NST;
-                if (round > 0) ok = __all_sync(0xffffffffu, wait(&empty[stage], (round - 1) & 1)) != 0;
-                if (!ok) break;
-                int row[kKeys / 16];
-                uint32_t bytes = 0;
+            };
+            if (ps == 6) {                          // one copy for all of a tile
+                tiles([&](int j0, int place, uint8_t *dst, uint64_t *done) {
+                    const int id = __shfl_sync(0xffffffffu, ids, place & 31);
+                    const int row = ((id * a.s.Hkv + head) << shift) + (j0 & ((1 << shift) - 1));
+                    if (elect_one()) {
+                        mbar_expect_tx(done, total ? P::STAGE : 0);
+                        if (total) tma_load_3d(dst, map, 0, row, 0, done);
+                    }
+                });
+            } else {
+                tiles([&](int j0, int place, uint8_t *dst, uint64_t *done) {
+                    int row[kKeys / 16];
+                    uint32_t bytes = 0;
 #pragma unroll
-                for (int c = 0; c < kKeys / 16; ++c) {
-                    const int id = __shfl_sync(0xffffffffu, ids, (at - base + c) & 31);
-                    row[c] = c < (kKeys >> ps) && j0 + (c << ps) < total
-                                 ? ((id * a.s.Hkv + head) << shift) + (j0 & ((1 << shift) - 1) & ~((1 << ps) - 1)) : -1;
-                    bytes += row[c] >= 0 ? (P::ATOMS * 128u) << ps : 0u;
-                }
-                uint8_t *dst = ring + stage * P::STAGE;
-                if (elect_one()) {
-                    mbar_expect_tx(&full[stage], bytes);
+                    for (int c = 0; c < kKeys / 16; ++c) {
+                        const int id = __shfl_sync(0xffffffffu, ids, (place + c) & 31);
+                        row[c] = c < (kKeys >> ps) && j0 + (c << ps) < total ? (id * a.s.Hkv + head) << shift : -1;
+                        bytes += row[c] >= 0 ? (P::ATOMS * 128u) << ps : 0u;
+                    }
+                    if (elect_one()) {
+                        mbar_expect_tx(done, bytes);
 #pragma unroll
-                    for (int c = 0; c < kKeys / 16; ++c)
-                        if (row[c] >= 0) {
+                        for (int c = 0; c < kKeys / 16; ++c)
+                            if (row[c] >= 0) {
 #pragma unroll
-                            for (int x = 0; x < P::ATOMS; ++x)
-                                tma_load_2d(dst + x * (kKeys * 128) + (c << (ps + 7)), map, x * 64, row[c], &full[stage]);
-                        }
-                }
-                __syncwarp();
+                                for (int x = 0; x < P::ATOMS; ++x)
+                                    tma_load_2d(dst + x * (kKeys * 128) + (c << (ps + 7)), map, x * 64, row[c], done);
+                            }
+                    }
+                });
             }
         }
     } else if (warp >= P::MMA_WARP) {
@@ -1052,14 +1068,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinWarps == 8 ? 3 : 1) veri
 }
 
 // ------------------------------------------------------------------- host side
+// A layer's keys or values: as [d / 64][rows of all pages][64] in boxes of a tile, in the column atoms that
+// the MMAs read; where the pages are shorter, as [rows][d] in boxes of a page's rows of one atom.
 bool page_map(CUtensorMap *m, const void *base, const gdn_page_cache *c) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->n_page) * c->Hkv * c->page};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(c->d) * 2};
-    cuuint32_t box[2] = {64, static_cast<cuuint32_t>(c->page < kKeys ? c->page : kKeys)};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+    const bool tile = c->page >= kKeys;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(tile ? 64 : c->d), static_cast<cuuint64_t>(c->n_page) * c->Hkv * c->page,
+                          static_cast<cuuint64_t>(c->d) / 64};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(c->d) * 2, 128};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(tile ? kKeys : c->page), static_cast<cuuint32_t>(c->d) / 64};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, tile ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
