@@ -153,8 +153,10 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
 }
 // Named barriers of the row threads: of all of them (id 1), of a group (2, 3), and of the 64 threads
-// of a group's TMEM lane quarter (4 ..).  No row warp leaves its loops early (an expired wait only
-// stops the waiting), so they always complete.
+// of a group's TMEM lane quarter (4 ..).  They complete because all threads of a barrier take it equally
+// often: no row warp leaves its loops early (an expired wait only stops the waiting), loop counts
+// and branches around a barrier follow from the share alone or, for a tile's non-finite values, from
+// one word in shared memory that all threads of the barrier read between the same two barriers.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -809,7 +811,10 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     tmem_st16(t_s + 32 + 16 * half, lo);
                     tmem_wait_st();
                 }
-                unsigned long long special = 0ull, *flags = &odd[(alternate ? 2 * group : 0) + (g & 1)];
+                // The word of the tile's non-finite values: a group's own where it is alone on the tile; on
+                // a pair, one for both groups, chosen by what they both count, the CTA's tiles (their own
+                // counts g differ by one after a single row tile of an odd number of tiles).
+                unsigned long long special = 0ull, *flags = &odd[alternate ? 2 * group + (g & 1) : (tile0 + i) & 1];
                 const int who = alternate || NG == 1 ? gtid : tid, whole_id = alternate ? 2 + group : 1;
                 const int whole_n = alternate || NG == 1 ? kGroupThreads : P::ROWS;
                 if (edge) {
@@ -846,7 +851,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 tc_fence_before();
                 mbar_arrive(&pf[g & 1]);
-                if (special) {                      // the same for all threads that use the tile
+                if (special) {                      // read from one word by all threads that use the tile
                     wait_rows(&od[g & 1], (g >> 1) & 1);
                     if (warp_live) {
                         const int sh = s.len - j0;
