@@ -33,7 +33,8 @@ extern "C" {
 #endif
 
 #define GDN_STATUS_BAD_PAGE   64   /* a block-table entry, a copy pair or a free-list entry that the
-                                      call needs is outside [0, n_page), or a page was released more
+                                      call needs is outside [0, n_page), the entry is not one of the
+                                      sequence's own (n_owned), or a page was released more
                                       often than it was shared; see each call */
 #define GDN_STATUS_BAD_POS   128   /* a rotation position outside [0, max_pos); the token is skipped */
 #define GDN_STATUS_BAD_TREE  256   /* a parent not in [-1, t) or an accepted path that is not strictly
@@ -51,8 +52,11 @@ extern "C" {
  *   free_list    int32  [n_page]             the free pages are its first free_count entries;
  *   free_count   int32  [1]                  pages are taken from the end
  * Token p of a sequence sits in row p % page of page block_table[slot][p / page].  The
- * attention calls use k, v, block_table and seq_len only; the other pointers may then be
- * NULL.
+ * attention calls use k, v, block_table, seq_len and n_owned; the other pointers may then be
+ * NULL, and n_owned too where the caller keeps the pages by means of its own.  Entries of a block-table
+ * row from n_owned on say nothing: a release leaves its ids there, and a reserve or fork that finds no
+ * free page does not replace them.  The attention calls therefore use none of them: a token
+ * that would lie there is one without a page (GDN_STATUS_BAD_PAGE).
  */
 typedef struct {
     int32_t n_slot;     /* sequence slots, >= 0 */

@@ -465,7 +465,10 @@ class PagedCache:
     free_count with the header's layouts; they are moved to ``device`` once (a tensor that
     is there already is used as it is).  Without ``init`` every page is free and k and v are
     zeros.  The tensors are attributes; write into them, do not replace them.  ``status``
-    collects GDN_STATUS_* bits.  The methods enqueue the library calls.
+    collects GDN_STATUS_* bits: a row without free pages, say, is skipped on the device, and the
+    calls after it refuse its tokens there (STATUS_BAD_PAGE).  Whoever fills the block table without
+    ``reserve`` and ``fork`` sets n_owned as well: entries past it are not used.  The methods enqueue
+    the library calls.
     """
 
     _FIELDS = ("k", "v", "block_table", "seq_len", "n_owned", "ref", "free_list", "free_count")

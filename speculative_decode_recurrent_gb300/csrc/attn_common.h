@@ -14,6 +14,7 @@ namespace gdn {
 // What a kernel needs to find a sequence's rows in the cache.
 struct SeqArgs {
     const int32_t *state_idx, *draft_len, *seq_len, *table;
+    const int32_t *owned;                       // NULL: the caller keeps the pages
     int32_t *status;
     int B, T, n_slot, max_pages, n_page, page_shift, Hkv;
 };
@@ -23,7 +24,12 @@ struct Seq {
     int bad;                    // GDN_STATUS_* bit, 0 when the sequence is sound
 };
 
-__device__ __forceinline__ Seq load_seq(const SeqArgs &s, int b) {
+// Block-table entries of a slot that are its own.  Those behind them may hold pages that another
+// sequence has by now (a release leaves them, a reserve without free pages does not replace them).
+__device__ __forceinline__ int owned_pages(const SeqArgs &s, int slot) { return s.owned ? s.owned[slot] : s.max_pages; }
+
+// PAGES: the sequence's committed and drafted tokens have to lie in pages of its own.
+template <bool PAGES> __device__ __forceinline__ Seq load_seq(const SeqArgs &s, int b) {
     Seq q;
     q.slot = s.state_idx ? s.state_idx[b] : b;
     q.n = s.draft_len ? s.draft_len[b] : s.T;
@@ -34,9 +40,11 @@ __device__ __forceinline__ Seq load_seq(const SeqArgs &s, int b) {
         return q;
     }
     q.len = s.seq_len[q.slot];
+    const int own = PAGES ? owned_pages(s, q.slot) : 0;
     const int room = s.max_pages << s.page_shift;                 // <= 2^24
     if (q.len < 0 || q.len > room || q.n < 0 || q.n > s.T) q.bad = GDN_STATUS_BAD_LEN;
     else if (q.len + q.n > room) q.bad = GDN_STATUS_NO_ROOM;
+    else if (PAGES && (q.len + q.n + (1 << s.page_shift) - 1) >> s.page_shift > own) q.bad = GDN_STATUS_BAD_PAGE;
     return q;
 }
 
@@ -114,7 +122,7 @@ inline int check_attn(const gdn_page_cache *c, const gdn_attn_dims *a, int max_T
 }
 inline SeqArgs seq_args(const gdn_page_cache *c, int B, int T, const int32_t *state_idx, const int32_t *draft_len,
                         int32_t *status) {
-    return SeqArgs{state_idx, draft_len, c->seq_len, c->block_table, status, B, T, c->n_slot, c->max_pages,
+    return SeqArgs{state_idx, draft_len, c->seq_len, c->block_table, c->n_owned, status, B, T, c->n_slot, c->max_pages,
                    c->n_page, page_shift(c->page), c->Hkv};
 }
 // Elements of one layer's keys (or values).

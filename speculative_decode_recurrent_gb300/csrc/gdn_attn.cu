@@ -139,11 +139,12 @@ __global__ void __launch_bounds__(32 * W) stage_kernel(const StageArgs a)
     request(0);
     // most rows are queries': their weights stay in registers
     const float4 wqa = *reinterpret_cast<const float4 *>(a.qw + ea), wqb = *reinterpret_cast<const float4 *>(a.qw + eb);
-    int len = 0, bad = 0;
+    int len = 0, own = 0, bad = 0;
     if (slot < 0 || slot >= a.s.n_slot) bad = GDN_STATUS_BAD_SLOT;
     else {
         const int room = a.s.max_pages << a.s.page_shift;
         len = a.s.seq_len[slot];
+        own = owned_pages(a.s, slot);
         if (len < 0 || len > room || n < 0 || n > a.s.T) bad = GDN_STATUS_BAD_LEN;
         else if (len + n > room) bad = GDN_STATUS_NO_ROOM;
     }
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(32 * W) stage_kernel(const StageArgs a)
             cs[0] = u.x; cs[1] = u.y; cs[2] = u.z; cs[3] = u.w;
             sn[0] = w.x; sn[1] = w.y; sn[2] = w.z; sn[3] = w.w;
         }
-        if (id >= 0 && id < a.s.n_page) row0 = static_cast<long long>(id) * a.s.Hkv * page + (at & (page - 1));
+        if (id >= 0 && id < a.s.n_page && at >> a.s.page_shift < own) row0 = static_cast<long long>(id) * a.s.Hkv * page + (at & (page - 1));
         else if (threadIdx.x == 0) atomicOr(a.s.status, GDN_STATUS_BAD_PAGE);
     }
     for (int r0 = 0; r0 < rows; r0 += NR * GROUPS) {              // the same for the whole CTA
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(128) tree_kernel(const SeqArgs s, const int32_
     pdl_release();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x * 4 + w;
     if (b >= s.B) return;
-    const Seq q = load_seq(s, b);
+    const Seq q = load_seq<false>(s, b);
     int bad = q.bad;
     if (!bad) {
         bool wrong = false;
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kCoreThreads, CorePlan<D>::CTAS) verify_core_k
     const int split = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles, h = blockIdx.y, b = blockIdx.z;
     pdl_wait();
     pdl_release();
-    const Seq sq = load_seq(a.s, b);
+    const Seq sq = load_seq<true>(a.s, b);
     if (sq.bad) {
         if (blockIdx.x == 0 && h == 0 && tid == 0) atomicOr(a.s.status, sq.bad);
         return;
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(128) verify_join_kernel(const AttnArgs a, int 
     const size_t unit = (static_cast<size_t>(b) * a.s.Hkv + h) * row_tiles + row / kRT;
     const float *src = a.ws + (unit * a.splits * kRT + row % kRT) * part_floats<D>();
     const size_t step = static_cast<size_t>(kRT) * part_floats<D>();
-    if (load_seq(a.s, b).bad) return;
+    if (load_seq<true>(a.s, b).bad) return;
     float w[4], m = -INFINITY, l = 0.f;                           // at most 128 splits
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -651,11 +652,12 @@ accept_rows_kernel(const AcceptArgs a)
     if (tid == 0) fault = 0;
     pdl_wait();
     pdl_release();
-    const Seq sq = load_seq(a.s, b);             // n = T
+    const Seq sq = load_seq<false>(a.s, b);      // n = T
     const int p = a.accepted[b];
     int bad = sq.bad & ~GDN_STATUS_NO_ROOM;      // the draft's rows past the path need no room
     if (!bad && (p < 0 || p > a.s.T)) bad = GDN_STATUS_BAD_ACCEPT;
     const int page = 1 << a.s.page_shift, room = a.s.max_pages << a.s.page_shift;
+    const int own = sq.bad & GDN_STATUS_BAD_SLOT ? 0 : owned_pages(a.s, sq.slot);
     __syncthreads();
     if (!bad && tid < p) {
         const int j = tid;
@@ -667,6 +669,8 @@ accept_rows_kernel(const AcceptArgs a)
         }
         if (sq.len + src >= room) {
             atomicOr(&fault, GDN_STATUS_NO_ROOM);
+        } else if ((sq.len + src) >> a.s.page_shift >= own) {
+            atomicOr(&fault, GDN_STATUS_BAD_PAGE);
         } else if (a.path) {
             const int32_t *tab = a.s.table + static_cast<size_t>(sq.slot) * a.s.max_pages;
             const int pf = sq.len + src, pt = sq.len + j;

@@ -402,7 +402,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int i = i0 + tid;
         int mine = 0, own_units = 0;
         if (i < ta.nb) {
-            const Seq q = load_seq(a.s, ta.b0 + i);
+            const Seq q = load_seq<true>(a.s, ta.b0 + i);
             const int live = q.bad ? 0 : quotient(q.n + ta.tpt - 1, ta.tpt);
             st.live[i] = live;
             if (!q.bad) {
