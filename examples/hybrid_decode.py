@@ -86,7 +86,7 @@ def run(steps=6, seed=1):
         p = torch.randint(0, T + 1, (B,), generator=g).tolist()
         gdn.accept(i32(p))
         gdn.flush()
-        cache.accept(i32(p), state_idx=rows)
+        cache.accept(i32(p), state_idx=rows, T=T)
         committed = [a + b for a, b in zip(committed, p)]
         if step == 2:                                       # a continuation of sequence 0, given up again later
             cache.fork(i32([0]), i32([B]), torch.empty(1, 2, dtype=torch.int32, device="cuda"))

@@ -538,12 +538,19 @@ class PagedCache:
         if rc:
             raise GdnError("gdn_pages_release", rc)
 
-    def accept(self, accepted, path=None, state_idx=None, new_len=None, stream=None):
+    def accept(self, accepted, path=None, state_idx=None, new_len=None, stream=None, T=None):
         """Commit accepted[b] drafted tokens of each sequence: along ``path`` (int32 [B, T]),
         whose rows move to the front of the draft's in every layer, or, without one, the first
-        accepted[b].  The lengths go to ``new_len`` (seq_len when None)."""
+        accepted[b].  More than ``T`` (the draft's tokens per sequence; 64, the most there can be, when
+        neither it nor a path says) are refused on the device (STATUS_BAD_ACCEPT).  The lengths go
+        to ``new_len`` (seq_len when None)."""
         B = accepted.numel()
-        T = 64 if path is None else path.shape[-1]
+        if path is not None:
+            if T is not None and T != path.shape[-1]:
+                raise ValueError(f"path: expected {T} tokens per sequence, got {path.shape[-1]}")
+            T = path.shape[-1]
+        elif T is None:
+            T = 64
         rc = self._lib.gdn_attn_accept(
             self._c, B, T, None if state_idx is None else _in(state_idx, _I32, B, "state_idx"),
             None if path is None else _in(path, _I32, B * T, "path"), _in(accepted, _I32, B, "accepted"),
