@@ -9,6 +9,7 @@ fallback: if the shared library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -449,12 +450,29 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _in(t, dtype, n, name):
-    """Address of a dense device tensor of dtype that holds at least n elements."""
+def _in(t, dtype, n, name, tails=None):
+    """Address of a dense device tensor of dtype that holds at least n elements, its extents behind
+    the first among ``tails`` (from _tails)."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= n:
+        if tails is not None and t.shape[1:] not in tails and tuple(x for x in t.shape[1:] if x != 1) not in tails:
+            raise ValueError(f"{name}: expected shape {tails[()]}, or neighbouring extents of it in one, got {tuple(t.shape)}")
         return t.data_ptr()
     _ptr(t, dtype, name)                                # says what is wrong
     raise ValueError(f"{name}: needs at least {n} elements, got {t.numel()}")
+
+
+def _tails(*shape):
+    """The extents behind the first of dense tensors that hold ``shape`` in row-major order (the first may be
+    longer, neighbouring extents may be one, extents of 1 left out), as keys; the values are ``shape``."""
+    def merged(s):
+        if not s:
+            return {()}
+        return {(math.prod(s[:i]),) + rest for i in range(1, len(s) + 1) for rest in merged(s[i:])}
+    found = set()
+    for s in (shape, tuple(x for x in shape if x != 1)):
+        for i in range(len(s) + 1):
+            found |= merged(s[i:])
+    return dict.fromkeys(found, shape)
 
 
 class PagedCache:
@@ -578,6 +596,8 @@ class AttnLayer:
         self._Hkv, self._n, self._rows = c.Hkv, c.d, dims.B * dims.T
         self._heads = self._rows * dims.Hq                      # rows of queries
         self._elems = self._heads * c.d
+        B, T, Hq = dims.B, dims.T, dims.Hq
+        self._tok, self._row, self._vec = _tails(B, T), _tails(B, T, Hq), _tails(B, T, Hq, c.d)
         dev = cache.status.device
         need = cache._lib.gdn_attn_workspace(cache._c, self._ref) if dims.T <= 64 else 0
         _check("gdn_attn_workspace", min(need, 0))
@@ -630,32 +650,33 @@ class AttnLayer:
         rc = self._lib.gdn_attn_stage(
             cache._c, self.layer, self._ref, ctypes.byref(r), self._idx,
             None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"), pq, pk, pv,
-            None if pos is None else _in(pos, _I32, self._rows, "pos"), wq, wk, tab,
-            _in(q_out, self._dtype, self._elems, "q_out"), cache._status, self._stream(stream))
+            None if pos is None else _in(pos, _I32, self._rows, "pos", self._tok), wq, wk, tab,
+            _in(q_out, self._dtype, self._elems, "q_out", self._vec), cache._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_attn_stage", rc)
 
     def build_tree(self, parent, tree, pos=None, draft_len=None, stream=None):
         """Ancestor words ``tree`` (int64 [B, T]) and rotation positions ``pos`` (int32 [B, T])
         of a token tree given by its parents (int32 [B, T])."""
-        n = self._rows
+        n, tok = self._rows, self._tok
         rc = self._lib.gdn_tree_build(
             self.cache._c, self._ref, self._idx,
             None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"),
-            _in(parent, _I32, n, "parent"), _in(tree, torch.int64, n, "tree"),
-            None if pos is None else _in(pos, _I32, n, "pos"), self.cache._status, self._stream(stream))
+            _in(parent, _I32, n, "parent", tok), _in(tree, torch.int64, n, "tree", tok),
+            None if pos is None else _in(pos, _I32, n, "pos", tok), self.cache._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_tree_build", rc)
 
     def verify(self, q, out, lse=None, tree=None, draft_len=None, stream=None):
         """Attention of the block's rows q [B, T, Hq, d] over the cache into ``out`` (and
-        ``lse`` fp32 [B, T, Hq]); ``tree`` int64 [B, T] ancestor words, None: a chain."""
+        ``lse`` fp32 [B, T, Hq]); ``tree`` int64 [B, T] ancestor words, None: a chain.  Neighbouring
+        extents may be one ([B, T, Hq d]), and the first may be longer."""
         t, e, cache = self._dtype, self._elems, self.cache
         rc = self._lib.gdn_attn_verify(
             cache._c, self.layer, self._ref, self._idx,
-            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"), _in(q, t, e, "q"),
-            None if tree is None else _in(tree, torch.int64, self._rows, "tree"), _in(out, t, e, "out"),
-            None if lse is None else _in(lse, _F32, self._heads, "lse"), self._ws, self._ws_bytes, cache._status,
+            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"), _in(q, t, e, "q", self._vec),
+            None if tree is None else _in(tree, torch.int64, self._rows, "tree", self._tok),
+            _in(out, t, e, "out", self._vec), None if lse is None else _in(lse, _F32, self._heads, "lse", self._row), self._ws, self._ws_bytes, cache._status,
             self._stream(stream))
         if rc:
             raise GdnError("gdn_attn_verify", rc)

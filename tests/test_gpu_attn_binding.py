@@ -41,3 +41,60 @@ def test_accept_of_more_than_the_draft():
     with pytest.raises(lib.GdnError):
         cache.accept(_i32([1, 1, 1]), state_idx=idx, T=65)
     assert torch.equal(cache.seq_len.cpu(), want)
+
+
+def test_shapes_of_the_calls():
+    """A tensor of the right size in another order is refused; one that lies in memory as the call reads
+    it is taken, whatever it is called."""
+    lib = _lib()
+    B, T, Hq, Hkv, d = 3, 5, 6, 2, 64
+    c = R.CacheCase([20, 30, 40], T, Hkv, d, 16, BF, seed=301)
+    cache = lib.PagedCache(c.dims(lib), c.init())
+    rope = lib.RopeDims(rot=16, style=lib.ROPE_HALF, max_pos=64, eps=1e-6)
+    w, tab = torch.ones(d, device="cuda"), torch.ones(64, 16, device="cuda")
+    layer = lib.AttnLayer(lib.AttnDims(B=B, T=T, Hq=Hq, scale=0.1), cache, 0, rope, w, w, tab, state_idx=c.state_idx.cuda())
+    kv = [torch.randn(B, T, Hkv, d, generator=c.g).to(BF).cuda() for _ in range(2)]
+    q = torch.randn(B, T, Hq, d, generator=c.g).to(BF).cuda()
+    parent = (torch.arange(T, dtype=torch.int32, device="cuda") - 1).repeat(B, 1)
+    i64, i32, f32 = (dict(dtype=x, device="cuda") for x in (torch.int64, torch.int32, torch.float32))
+
+    def same(shape):
+        return torch.empty(shape, dtype=BF, device="cuda")
+    tree, pos, lse, out = torch.empty(B, T, **i64), torch.empty(B, T, **i32), torch.empty(B, T, Hq, **f32), same((B, T, Hq, d))
+    refused = [
+        ("q", lambda: layer.verify(q.transpose(1, 2).contiguous(), out)),
+        ("q", lambda: layer.verify(q.transpose(1, 2).reshape(B * Hq, T, d), out)),
+        ("out", lambda: layer.verify(q, same((B, Hq, T, d)))),
+        ("lse", lambda: layer.verify(q, out, lse=torch.empty(B, Hq, T, **f32))),
+        ("tree", lambda: layer.verify(q, out, tree=torch.empty(T, B, **i64))),
+        ("q_out", lambda: layer.stage(q, *kv, same((B, Hq, T, d)))),
+        ("pos", lambda: layer.stage(q, *kv, out, pos=torch.zeros(T, B, **i32))),
+        ("parent", lambda: layer.build_tree(parent.t().contiguous(), tree)),
+        ("tree", lambda: layer.build_tree(parent, torch.empty(T, B, **i64))),
+        ("pos", lambda: layer.build_tree(parent, tree, torch.empty(T, B, **i32)))]
+    for name, call in refused:
+        with pytest.raises(ValueError, match=f"^{name}: expected shape"):
+            call()
+    layer.build_tree(parent.flatten(), tree.view(1, B, T), pos)
+    layer.stage(q, *kv, out, pos=pos.flatten())
+    got = []
+    for shape in ((B, T, Hq, d), (B, T, Hq * d), (B * T, Hq, d), (B * T * Hq, d), (-1,), (1, B, T, Hq, d), (B, T * Hq, 1, d)):
+        o, z = torch.zeros(B + 1, T, Hq, d, dtype=BF, device="cuda"), torch.zeros(B, T, Hq, **f32)
+        layer.verify(q.view(shape), o, lse=z.view(B, -1), tree=tree.view(-1))
+        got.append(o[:B])
+    torch.cuda.synchronize()
+    assert int(cache.status.item()) == 0 and all(torch.equal(got[0], x) for x in got[1:])
+
+
+def test_one_token_in_any_order_of_its_extents():
+    """[B, Hq, 1, d] lies in memory as [B, 1, Hq, d]."""
+    lib = _lib()
+    c = R.CacheCase([20, 30], 1, 2, 64, 16, BF, seed=302)
+    cache = lib.PagedCache(c.dims(lib), c.init())
+    layer = lib.AttnLayer(lib.AttnDims(B=2, T=1, Hq=4, scale=0.1), cache, 0, state_idx=c.state_idx.cuda())
+    q = torch.randn(2, 1, 4, 64, generator=c.g).to(BF).cuda()
+    a, b = torch.zeros_like(q), torch.zeros(2, 4, 1, 64, dtype=BF, device="cuda")
+    layer.verify(q, a)
+    layer.verify(q.transpose(1, 2), b)
+    torch.cuda.synchronize()
+    assert torch.equal(a.flatten(), b.flatten()) and bool(a.any())
