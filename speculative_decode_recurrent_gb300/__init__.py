@@ -450,10 +450,12 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _in(t, dtype, n, name, tails=None):
-    """Address of a dense device tensor of dtype that holds at least n elements, its extents behind
-    the first among ``tails`` (from _tails)."""
+def _in(t, dtype, n, name, index=None, tails=None):
+    """Address of a dense tensor of dtype that holds at least n elements, on the CUDA device of that
+    index (None: any), its extents behind the first among ``tails`` (from _tails)."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= n:
+        if index is not None and t.get_device() != index:
+            raise ValueError(f"{name}: expected a tensor on the cache's device (cuda:{index}), got {t.device}")
         if tails is not None and t.shape[1:] not in tails and tuple(x for x in t.shape[1:] if x != 1) not in tails:
             raise ValueError(f"{name}: expected shape {tails[()]}, or neighbouring extents of it in one, got {tuple(t.shape)}")
         return t.data_ptr()
@@ -530,8 +532,8 @@ class PagedCache:
     def reserve(self, slots, extra: int, stream=None):
         """Room for ``extra`` tokens past seq_len in each of ``slots`` (int32)."""
         n = slots.numel()
-        rc = self._lib.gdn_pages_reserve(self._c, n, _in(slots, _I32, n, "slots"), extra, self._status,
-                                         self._stream(stream))
+        rc = self._lib.gdn_pages_reserve(self._c, n, _in(slots, _I32, n, "slots", self._index), extra,
+                                         self._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_pages_reserve", rc)
 
@@ -539,8 +541,8 @@ class PagedCache:
         """Sequences ``dst`` become copies of ``src`` (int32 slots): full pages shared, the
         last page's rows copied in every layer.  ``copies`` int32 [n, 2] receives those pages."""
         n, s = src.numel(), self._stream(stream)
-        c = _in(copies, _I32, 2 * n, "copies")
-        rc = self._lib.gdn_pages_fork(self._c, n, _in(src, _I32, n, "src"), _in(dst, _I32, n, "dst"), c,
+        c, at = _in(copies, _I32, 2 * n, "copies", self._index), self._index
+        rc = self._lib.gdn_pages_fork(self._c, n, _in(src, _I32, n, "src", at), _in(dst, _I32, n, "dst", at), c,
                                       self._status, s)
         if rc:
             raise GdnError("gdn_pages_fork", rc)
@@ -551,7 +553,7 @@ class PagedCache:
     def release(self, slots, stream=None):
         """The pages of ``slots`` (int32) go back, as far as no other sequence holds them."""
         n = slots.numel()
-        rc = self._lib.gdn_pages_release(self._c, n, _in(slots, _I32, n, "slots"), self._status,
+        rc = self._lib.gdn_pages_release(self._c, n, _in(slots, _I32, n, "slots", self._index), self._status,
                                          self._stream(stream))
         if rc:
             raise GdnError("gdn_pages_release", rc)
@@ -562,7 +564,7 @@ class PagedCache:
         accepted[b].  More than ``T`` (the draft's tokens per sequence; 64, the most there can be, when
         neither it nor a path says) are refused on the device (STATUS_BAD_ACCEPT).  The lengths go
         to ``new_len`` (seq_len when None)."""
-        B = accepted.numel()
+        B, at = accepted.numel(), self._index
         if path is not None:
             if T is not None and T != path.shape[-1]:
                 raise ValueError(f"path: expected {T} tokens per sequence, got {path.shape[-1]}")
@@ -570,9 +572,9 @@ class PagedCache:
         elif T is None:
             T = 64
         rc = self._lib.gdn_attn_accept(
-            self._c, B, T, None if state_idx is None else _in(state_idx, _I32, B, "state_idx"),
-            None if path is None else _in(path, _I32, B * T, "path"), _in(accepted, _I32, B, "accepted"),
-            self.d.seq_len if new_len is None else _in(new_len, _I32, self.d.n_slot, "new_len"),
+            self._c, B, T, None if state_idx is None else _in(state_idx, _I32, B, "state_idx", at),
+            None if path is None else _in(path, _I32, B * T, "path", at), _in(accepted, _I32, B, "accepted", at),
+            self.d.seq_len if new_len is None else _in(new_len, _I32, self.d.n_slot, "new_len", at),
             self._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_attn_accept", rc)
@@ -605,11 +607,12 @@ class AttnLayer:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         self.workspace, self.state_idx = workspace, state_idx
         self._keep = (q_weight, k_weight, cos_sin)
-        self._ws, self._ws_bytes = _in(workspace, torch.uint8, need, "workspace") or None, workspace.numel()
-        self._idx = None if state_idx is None else _in(state_idx, _I32, dims.B, "state_idx")
+        self._index = at = cache._index
+        self._ws, self._ws_bytes = _in(workspace, torch.uint8, need, "workspace", at) or None, workspace.numel()
+        self._idx = None if state_idx is None else _in(state_idx, _I32, dims.B, "state_idx", at)
         if rope is not None:
-            self._w = (_in(q_weight, _F32, c.d, "q_weight"), _in(k_weight, _F32, c.d, "k_weight"),
-                       None if cos_sin is None else _in(cos_sin, _F32, rope.max_pos * rope.rot, "cos_sin"))
+            self._w = (_in(q_weight, _F32, c.d, "q_weight", at), _in(k_weight, _F32, c.d, "k_weight", at),
+                       None if cos_sin is None else _in(cos_sin, _F32, rope.max_pos * rope.rot, "cos_sin", at))
         self._dtype, self._stream, self._lib = _TORCH_IN[c.dtype], cache._stream, cache._lib
 
     @property
@@ -625,6 +628,8 @@ class AttnLayer:
             raise ValueError(f"{name}: expected shape {(B, T, heads, n)}, got {tuple(t.shape)}")
         if not t.is_cuda:
             raise ValueError(f"{name}: expected a CUDA tensor")
+        if t.get_device() != self._index:
+            raise ValueError(f"{name}: expected a tensor on the cache's device (cuda:{self._index}), got {t.device}")
         if t.dtype is not self._dtype:
             raise TypeError(f"{name}: expected {self._dtype}, got {t.dtype}")
         sb, st, sh, se = t.stride()
@@ -646,24 +651,24 @@ class AttnLayer:
         pk, r.k_stride = self._block(k, self._Hkv, "k")
         pv, r.v_stride = self._block(v, self._Hkv, "v")
         wq, wk, tab = self._w
-        cache = self.cache
+        cache, at = self.cache, self._index
         rc = self._lib.gdn_attn_stage(
             cache._c, self.layer, self._ref, ctypes.byref(r), self._idx,
-            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"), pq, pk, pv,
-            None if pos is None else _in(pos, _I32, self._rows, "pos", self._tok), wq, wk, tab,
-            _in(q_out, self._dtype, self._elems, "q_out", self._vec), cache._status, self._stream(stream))
+            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len", at), pq, pk, pv,
+            None if pos is None else _in(pos, _I32, self._rows, "pos", at, self._tok), wq, wk, tab,
+            _in(q_out, self._dtype, self._elems, "q_out", at, self._vec), cache._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_attn_stage", rc)
 
     def build_tree(self, parent, tree, pos=None, draft_len=None, stream=None):
         """Ancestor words ``tree`` (int64 [B, T]) and rotation positions ``pos`` (int32 [B, T])
         of a token tree given by its parents (int32 [B, T])."""
-        n, tok = self._rows, self._tok
+        n, tok, at = self._rows, self._tok, self._index
         rc = self._lib.gdn_tree_build(
             self.cache._c, self._ref, self._idx,
-            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"),
-            _in(parent, _I32, n, "parent", tok), _in(tree, torch.int64, n, "tree", tok),
-            None if pos is None else _in(pos, _I32, n, "pos", tok), self.cache._status, self._stream(stream))
+            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len", at),
+            _in(parent, _I32, n, "parent", at, tok), _in(tree, torch.int64, n, "tree", at, tok),
+            None if pos is None else _in(pos, _I32, n, "pos", at, tok), self.cache._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_tree_build", rc)
 
@@ -671,12 +676,14 @@ class AttnLayer:
         """Attention of the block's rows q [B, T, Hq, d] over the cache into ``out`` (and
         ``lse`` fp32 [B, T, Hq]); ``tree`` int64 [B, T] ancestor words, None: a chain.  Neighbouring
         extents may be one ([B, T, Hq d]), and the first may be longer."""
-        t, e, cache = self._dtype, self._elems, self.cache
+        t, e, cache, at = self._dtype, self._elems, self.cache, self._index
         rc = self._lib.gdn_attn_verify(
             cache._c, self.layer, self._ref, self._idx,
-            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len"), _in(q, t, e, "q", self._vec),
-            None if tree is None else _in(tree, torch.int64, self._rows, "tree", self._tok),
-            _in(out, t, e, "out", self._vec), None if lse is None else _in(lse, _F32, self._heads, "lse", self._row), self._ws, self._ws_bytes, cache._status,
-            self._stream(stream))
+            None if draft_len is None else _in(draft_len, _I32, self._B, "draft_len", at),
+            _in(q, t, e, "q", at, self._vec),
+            None if tree is None else _in(tree, torch.int64, self._rows, "tree", at, self._tok),
+            _in(out, t, e, "out", at, self._vec),
+            None if lse is None else _in(lse, _F32, self._heads, "lse", at, self._row), self._ws, self._ws_bytes,
+            cache._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_attn_verify", rc)

@@ -98,3 +98,28 @@ def test_one_token_in_any_order_of_its_extents():
     layer.verify(q.transpose(1, 2), b)
     torch.cuda.synchronize()
     assert torch.equal(a.flatten(), b.flatten()) and bool(a.any())
+
+
+def test_tensors_of_another_device():
+    """Tensors are compared with the cache's device before anything is launched (one GPU: the cache is
+    told that its device is another one)."""
+    lib = _lib()
+    B, T, Hq, Hkv, d = 2, 3, 4, 2, 64
+    c = R.CacheCase([20, 30], T, Hkv, d, 16, BF, seed=303)
+    cache, idx = lib.PagedCache(c.dims(lib), c.init()), c.state_idx.cuda()
+    rope = lib.RopeDims(rot=16, style=lib.ROPE_HALF, max_pos=64, eps=1e-6)
+    w, tab = torch.ones(d, device="cuda"), torch.ones(64, 16, device="cuda")
+    dims = lib.AttnDims(B=B, T=T, Hq=Hq, scale=0.1)
+    layer = lib.AttnLayer(dims, cache, 0, rope, w, w, tab, state_idx=idx)
+    x, kv = torch.zeros(B, T, Hq, d, dtype=BF, device="cuda"), torch.zeros(B, T, Hkv, d, dtype=BF, device="cuda")
+    n, tree = _i32([1, 1]), torch.zeros(B, T, dtype=torch.int64, device="cuda")
+    cache._index = layer._index = 5
+    stream = torch.cuda.current_stream()
+    for call in (lambda: cache.reserve(n, 1, stream), lambda: cache.release(n, stream),
+                 lambda: cache.fork(n, n, torch.zeros(2, 2, dtype=torch.int32, device="cuda"), stream),
+                 lambda: cache.accept(n, stream=stream), lambda: cache.accept(n, path=_i32([[0], [0]]), stream=stream),
+                 lambda: layer.stage(x, kv, kv, x, stream=stream), lambda: layer.verify(x, x, stream=stream),
+                 lambda: layer.build_tree(tree.to(torch.int32), tree, stream=stream),
+                 lambda: lib.AttnLayer(dims, cache, 0, state_idx=idx)):
+        with pytest.raises(ValueError, match="cache's device"):
+            call()
