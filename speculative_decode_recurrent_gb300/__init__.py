@@ -9,7 +9,6 @@ fallback: if the shared library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 import torch
@@ -450,31 +449,36 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _in(t, dtype, n, name, index=None, tails=None):
+def _in(t, dtype, n, name, index=None, shape=None):
     """Address of a dense tensor of dtype that holds at least n elements, on the CUDA device of that
-    index (None: any), its extents behind the first among ``tails`` (from _tails)."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= n:
-        if index is not None and t.get_device() != index:
-            raise ValueError(f"{name}: expected a tensor on the cache's device (cuda:{index}), got {t.device}")
-        if tails is not None and t.shape[1:] not in tails and tuple(x for x in t.shape[1:] if x != 1) not in tails:
-            raise ValueError(f"{name}: expected shape {tails[()]}, or neighbouring extents of it in one, got {tuple(t.shape)}")
-        return t.data_ptr()
+    index (None: any) and in an order of extents that _fits ``shape``."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous():
+        at = t.get_device()                             # (-1 for the CPU's)
+        if at >= 0 and (index is None or at == index):
+            # one comparison for the usual tensor; a host call of a short kernel is made of such checks
+            if (shape is not None and t.shape == shape) or (t.numel() >= n and (shape is None or _fits(t.shape, shape))):
+                return t.data_ptr()
     _ptr(t, dtype, name)                                # says what is wrong
-    raise ValueError(f"{name}: needs at least {n} elements, got {t.numel()}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name}: expected a tensor on the cache's device (cuda:{index}), got {t.device}")
+    if t.numel() < n:
+        raise ValueError(f"{name}: needs at least {n} elements, got {t.numel()}")
+    raise ValueError(f"{name}: expected shape {shape} or neighbouring extents of it in one, got {tuple(t.shape)}")
 
 
-def _tails(*shape):
-    """The extents behind the first of dense tensors that hold ``shape`` in row-major order (the first may be
-    longer, neighbouring extents may be one, extents of 1 left out), as keys; the values are ``shape``."""
-    def merged(s):
-        if not s:
-            return {()}
-        return {(math.prod(s[:i]),) + rest for i in range(1, len(s) + 1) for rest in merged(s[i:])}
-    found = set()
-    for s in (shape, tuple(x for x in shape if x != 1)):
-        for i in range(len(s) + 1):
-            found |= merged(s[i:])
-    return dict.fromkeys(found, shape)
+def _fits(got, shape):
+    """Whether a dense tensor of extents ``got`` holds ``shape`` in row-major order: its extents behind the
+    first are those of ``shape``, neighbours in one or not, extents of 1 anywhere; the first may be longer."""
+    ends, n = {1}, 1                                    # elements behind each extent of shape
+    for x in reversed(shape):
+        n *= x
+        ends.add(n)
+    n = 1
+    for x in reversed(got[1:]):
+        n *= x
+        if n not in ends:
+            return False
+    return True
 
 
 class PagedCache:
@@ -594,12 +598,11 @@ class AttnLayer:
         c = cache.d
         self._d, self.cache, self.layer, self.status = AttnDims.from_buffer_copy(dims), cache, layer, cache.status
         self._rope = None if rope is None else RopeDims.from_buffer_copy(rope)
-        self._ref, self._B, self._T, self._Hq = ctypes.byref(self._d), dims.B, dims.T, dims.Hq
-        self._Hkv, self._n, self._rows = c.Hkv, c.d, dims.B * dims.T
+        self._ref, self._B, self._rows = ctypes.byref(self._d), dims.B, dims.B * dims.T
         self._heads = self._rows * dims.Hq                      # rows of queries
         self._elems = self._heads * c.d
-        B, T, Hq = dims.B, dims.T, dims.Hq
-        self._tok, self._row, self._vec = _tails(B, T), _tails(B, T, Hq), _tails(B, T, Hq, c.d)
+        self._tok, self._row = (dims.B, dims.T), (dims.B, dims.T, dims.Hq)
+        self._vec, self._kv = self._row + (c.d,), self._tok + (c.Hkv, c.d)
         dev = cache.status.device
         need = cache._lib.gdn_attn_workspace(cache._c, self._ref) if dims.T <= 64 else 0
         _check("gdn_attn_workspace", min(need, 0))
@@ -620,15 +623,15 @@ class AttnLayer:
         """A copy of the layer's dims."""
         return AttnDims.from_buffer_copy(self._d)
 
-    def _block(self, t, heads, name):
+    def _block(self, t, shape, name):
         """Address and token stride of q, k or v: [B, T, heads, d], dense within a token, the
         tokens evenly spaced."""
-        B, T, n = self._B, self._T, self._n
-        if t.shape != (B, T, heads, n):
-            raise ValueError(f"{name}: expected shape {(B, T, heads, n)}, got {tuple(t.shape)}")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: expected a CUDA tensor")
+        B, T, heads, n = shape
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
         if t.get_device() != self._index:
+            if not t.is_cuda:
+                raise ValueError(f"{name}: expected a CUDA tensor")
             raise ValueError(f"{name}: expected a tensor on the cache's device (cuda:{self._index}), got {t.device}")
         if t.dtype is not self._dtype:
             raise TypeError(f"{name}: expected {self._dtype}, got {t.dtype}")
@@ -647,9 +650,9 @@ class AttnLayer:
         if self._rope is None:
             raise ValueError("stage: this layer was made without rope and norm weights")
         r = RopeDims.from_buffer_copy(self._rope)
-        pq, r.q_stride = self._block(q, self._Hq, "q")
-        pk, r.k_stride = self._block(k, self._Hkv, "k")
-        pv, r.v_stride = self._block(v, self._Hkv, "v")
+        pq, r.q_stride = self._block(q, self._vec, "q")
+        pk, r.k_stride = self._block(k, self._kv, "k")
+        pv, r.v_stride = self._block(v, self._kv, "v")
         wq, wk, tab = self._w
         cache, at = self.cache, self._index
         rc = self._lib.gdn_attn_stage(
