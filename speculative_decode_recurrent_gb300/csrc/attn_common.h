@@ -21,6 +21,7 @@ struct SeqArgs {
 
 struct Seq {
     int slot, len, n;           // slot, committed tokens, draft rows in use
+    int own;                    // block-table entries of its own
     int bad;                    // GDN_STATUS_* bit, 0 when the sequence is sound
 };
 
@@ -34,17 +35,17 @@ template <bool PAGES> __device__ __forceinline__ Seq load_seq(const SeqArgs &s, 
     q.slot = s.state_idx ? s.state_idx[b] : b;
     q.n = s.draft_len ? s.draft_len[b] : s.T;
     q.bad = 0;
-    q.len = 0;
+    q.len = q.own = 0;
     if (q.slot < 0 || q.slot >= s.n_slot) {
         q.bad = GDN_STATUS_BAD_SLOT;
         return q;
     }
     q.len = s.seq_len[q.slot];
-    const int own = PAGES ? owned_pages(s, q.slot) : 0;
+    q.own = owned_pages(s, q.slot);
     const int room = s.max_pages << s.page_shift;                 // <= 2^24
     if (q.len < 0 || q.len > room || q.n < 0 || q.n > s.T) q.bad = GDN_STATUS_BAD_LEN;
     else if (q.len + q.n > room) q.bad = GDN_STATUS_NO_ROOM;
-    else if (PAGES && (q.len + q.n + (1 << s.page_shift) - 1) >> s.page_shift > own) q.bad = GDN_STATUS_BAD_PAGE;
+    else if (PAGES && (q.len + q.n + (1 << s.page_shift) - 1) >> s.page_shift > q.own) q.bad = GDN_STATUS_BAD_PAGE;
     return q;
 }
 

@@ -657,7 +657,6 @@ accept_rows_kernel(const AcceptArgs a)
     int bad = sq.bad & ~GDN_STATUS_NO_ROOM;      // the draft's rows past the path need no room
     if (!bad && (p < 0 || p > a.s.T)) bad = GDN_STATUS_BAD_ACCEPT;
     const int page = 1 << a.s.page_shift, room = a.s.max_pages << a.s.page_shift;
-    const int own = sq.bad & GDN_STATUS_BAD_SLOT ? 0 : owned_pages(a.s, sq.slot);
     __syncthreads();
     if (!bad && tid < p) {
         const int j = tid;
@@ -669,18 +668,17 @@ accept_rows_kernel(const AcceptArgs a)
         }
         if (sq.len + src >= room) {
             atomicOr(&fault, GDN_STATUS_NO_ROOM);
-        } else if ((sq.len + src) >> a.s.page_shift >= own) {
-            atomicOr(&fault, GDN_STATUS_BAD_PAGE);
-        } else if (a.path) {
-            const int32_t *tab = a.s.table + static_cast<size_t>(sq.slot) * a.s.max_pages;
+        } else {
             const int pf = sq.len + src, pt = sq.len + j;
-            const int idf = tab[pf >> a.s.page_shift], idt = tab[pt >> a.s.page_shift];
-            if (idf < 0 || idf >= a.s.n_page || idt < 0 || idt >= a.s.n_page) {
-                atomicOr(&fault, GDN_STATUS_BAD_PAGE);
-            } else {
+            bool lost = false;
+            if (a.path) {
+                const int32_t *tab = a.s.table + static_cast<size_t>(sq.slot) * a.s.max_pages;
+                const int idf = tab[pf >> a.s.page_shift], idt = tab[pt >> a.s.page_shift];
+                lost = idf < 0 || idf >= a.s.n_page || idt < 0 || idt >= a.s.n_page;
                 from[j] = ((static_cast<long long>(idf) * a.s.Hkv << a.s.page_shift) + (pf & (page - 1))) * a.row_vecs;
                 to[j] = ((static_cast<long long>(idt) * a.s.Hkv << a.s.page_shift) + (pt & (page - 1))) * a.row_vecs;
             }
+            if (lost || pf >> a.s.page_shift >= sq.own) atomicOr(&fault, GDN_STATUS_BAD_PAGE);       // (pt <= pf)
         }
     }
     __syncthreads();
