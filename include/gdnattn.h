@@ -133,8 +133,10 @@ int gdn_tree_build(const gdn_page_cache *cache, const gdn_attn_dims *dims, const
  * bits at or past draft_len[b] are ignored):
  *     s_j = scale q_t . k_j,   out = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}.
  * A row that sees no token, or is not in use, gets out 0 and lse -inf.  What an unseen token's
- * rows hold (NaN and infinity included) has no effect.  The draft's keys and values are
- * read from the cache (gdn_attn_stage).
+ * rows hold (NaN and infinity included) has no effect.  A drafted token's infinite or NaN value is added as it
+ * is to the rows that see it; a committed one's leaves infinity or NaN in its column (bf16: the weight's
+ * second term may turn an infinity into NaN).  The draft's keys and values are read from the cache
+ * (gdn_attn_stage).
  *   q, out dtype [B, T, Hq, d] (16-byte aligned);  lse fp32 [B, T, Hq] or NULL;
  *   tree uint64 [B, T] or NULL;  workspace: workspace_bytes >= gdn_attn_workspace() bytes, 16-byte
  *   aligned, no initial content; calls that overlap on the GPU need one each.

@@ -21,11 +21,11 @@
 // balance and one long sequence fills the GPU.  A unit that one CTA covers is finished there; the
 // others leave partial results (o, m, l) that a second kernel joins in a fixed order.
 //
-// A CTA.  Two warps load (TMA through the block table, one copy a tile or, of pages below 64, per page and atom) into a
-// ring of four tiles of keys and values.  Two groups of 256 threads with an MMA warp
-// each work side by side: on a pair of row tiles, both on every tile of keys; on a single one, on
-// every second tile, their results joined at the end (d = 256 has TMEM for one group).  A
-// group forms S = Q K^T (M 128, N 64) in two TMEM buffers; its threads, two per row, each take
+// A CTA.  Two warps load (TMA through the block table, one copy a tile or, of pages below 64, per page and
+// atom) into a ring of NST / 2 tiles of keys and as many of values (8, 4 or 2 for d 64, 128, 256).  Two
+// groups of 256 threads with an MMA warp each work side by side: on a pair of row tiles, both on every
+// tile of keys; on a single one, on every second tile, their results joined at the end (d = 256 has TMEM for
+// one group).  A group forms S = Q K^T (M 128, N 64) in two TMEM buffers; its threads, two per row, each take
 // half of the tile's keys; the weights' two terms go back over S and are the A operands of
 // O += P V straight from TMEM, with the value rows read MN-major as they lie.
 #include <cuda.h>
@@ -68,6 +68,10 @@ template <int D, int NQ> struct TcPlan {
     // its tile's parity): a group that had not seen a stage's last round could take its phase for the
     // next.  From such a unit to a pair the queries' barriers (all scores of the unit before are
     // done) and the row threads' (all its products are) keep a group from running ahead.
+    // Row threads wait for values in the draft's tiles alone and skip a stage's other rounds; the stage's
+    // round before must then be over, or its phase would pass for this one's.  It is: scores of a group's
+    // tile t wait for its product of t - 2, and a stage comes round after NST / 2 tiles, two of the one
+    // group at d 256, two or four of each where the groups take turns, four or eight on pairs.
     static_assert(NST % 4 == 0, "stages of a tile alternate between the groups");
     static_assert(OFF_BAR % 16 == 0 && BYTES <= 227 * 1024, "shared memory");
 };
