@@ -85,3 +85,32 @@ def test_verify_non_finite_drafts(i):
     first = r.out.clone(), r.lse.clone()
     r.call()                                                 # the words of the call before are clear
     assert torch.equal(first[0].view(torch.uint8), r.out.view(torch.uint8)) and torch.equal(first[1], r.lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_verify_nan_keys_in_pairs(d):
+    """A drafted token's NaN key reaches the rows that see it, in every row tile, and no other; the same bits
+    for those as without it."""
+    B, T, Hq, Hkv = 6, 48, 16, 2
+    lens, drafts = _batch(B, T, 0, 300)
+    g = torch.Generator().manual_seed(530)
+    par = R.random_parents(B, T, g, width=6)
+    words = [R.ancestors(par[b], T)[0] for b in range(B)]
+    r = VerifyRun(lens, drafts, T, Hq, Hkv, d, 32, BF, words=words, seed=531)
+    r.call()
+    r.check()
+    clean = R.f64(r.out)
+    at = [max(0, n - 20) for n in drafts]
+    for b, n in enumerate(drafts):
+        if n:
+            p, row = r.case.cell(b, lens[b] + at[b])
+            r.cache.k[0, p, :, row] = float("nan")
+    r.call()
+    out, lse = R.f64(r.out), R.f64(r.lse)
+    seen_by = 0
+    for b, n in enumerate(drafts):
+        sees = np.array([(words[b][t] >> at[b]) & 1 for t in range(n)], bool)
+        seen_by += sees.sum()
+        assert np.isnan(out[b, :n][sees]).all() and np.isnan(lse[b, :n][sees]).all(), b
+        np.testing.assert_array_equal(out[b, :n][~sees], clean[b, :n][~sees])
+    assert seen_by > B                                       # more than the tokens themselves
