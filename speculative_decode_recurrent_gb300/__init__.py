@@ -609,7 +609,7 @@ class AttnLayer:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         self.workspace, self.state_idx = workspace, state_idx
-        self._keep = (q_weight, k_weight, cos_sin)
+        self._keep = (q_weight, k_weight, cos_sin, state_idx, workspace)     # the calls use their addresses
         self._index = at = cache._index
         self._ws, self._ws_bytes = _in(workspace, torch.uint8, need, "workspace", at) or None, workspace.numel()
         self._idx = None if state_idx is None else _in(state_idx, _I32, dims.B, "state_idx", at)

@@ -123,3 +123,18 @@ def test_tensors_of_another_device():
                  lambda: lib.AttnLayer(dims, cache, 0, state_idx=idx)):
         with pytest.raises(ValueError, match="cache's device"):
             call()
+
+
+def test_the_layer_keeps_what_its_calls_read():
+    """The calls use the tensors that the layer was made with; it holds on to them, whatever its attributes
+    are set to."""
+    import gc
+    import weakref
+    lib = _lib()
+    c = R.CacheCase([20, 30], 3, 2, 64, 16, BF, seed=304)
+    cache = lib.PagedCache(c.dims(lib), c.init())
+    layer = lib.AttnLayer(lib.AttnDims(B=2, T=3, Hq=4, scale=0.1), cache, 0, state_idx=c.state_idx.cuda())
+    held = [weakref.ref(layer.state_idx), weakref.ref(layer.workspace)]
+    layer.state_idx = layer.workspace = None
+    gc.collect()
+    assert all(x() is not None for x in held)
