@@ -75,7 +75,8 @@ typedef struct {
  * (draft_len NULL: every row). */
 typedef struct {
     int32_t B;          /* sequences in this call, 0..65535 */
-    int32_t T;          /* rows per sequence: 1..64; gdn_attn_stage: 1..2^20, B * T <= 2^30 */
+    int32_t T;          /* rows per sequence: 1..64; gdn_attn_stage: 1..2^20, B * T <= 2^30;
+                           gdn_attn_chunk: 1..2^20, B * T <= 2^28 */
     int32_t Hq;         /* query heads, a multiple of Hkv, Hq / Hkv <= 64; head h reads key head
                            h / (Hq / Hkv) */
     float   scale;      /* score scale, normally 1/sqrt(d) */
@@ -152,6 +153,27 @@ int gdn_attn_verify(const gdn_page_cache *cache, int32_t layer, const gdn_attn_d
 /* Bytes of workspace that gdn_attn_verify needs for these dims on the current device, or a
  * negative GDN_ERR_* code. */
 int64_t gdn_attn_workspace(const gdn_page_cache *cache, const gdn_attn_dims *dims);
+
+/*
+ * gdn_attn_chunk -- attention of a chunk of new tokens (a prompt, a part of one) over the cache,
+ * which holds their keys and values already (gdn_attn_stage).  For row t < n = chunk_len[b] (NULL: T) and query
+ * head h, over the tokens j <= seq_len + t, as in gdn_attn_verify:
+ *     s_j = scale q_t . k_j,   out = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}.
+ * Rows t >= n get out 0 and lse -inf.  Keys and values of tokens past the chunk's end may hold anything (NaN and
+ * infinity included); an infinite or NaN value of a token within it may leave NaN in its column of rows before it.
+ * T is 1..2^20, B * T <= 2^28; chunks of up to 64 tokens are a chain to gdn_attn_verify and go there.
+ *   q, out dtype [B, T, Hq, d] (16-byte aligned);  lse fp32 [B, T, Hq] or NULL;  workspace:
+ *   workspace_bytes >= gdn_attn_chunk_workspace() bytes, 16-byte aligned, no initial content; calls that
+ *   overlap on the GPU need one each.
+ * GDN_STATUS_* as for gdn_attn_verify.
+ */
+int gdn_attn_chunk(const gdn_page_cache *cache, int32_t layer, const gdn_attn_dims *dims,
+                   const int32_t *state_idx, const int32_t *chunk_len, const void *q, void *out, float *lse,
+                   void *workspace, int64_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
+/* Bytes of workspace that gdn_attn_chunk needs for these dims on the current device, or a
+ * negative GDN_ERR_* code. */
+int64_t gdn_attn_chunk_workspace(const gdn_page_cache *cache, const gdn_attn_dims *dims);
 
 /*
  * gdn_attn_accept -- for every sequence, p = accepted[b] and path int32 [B, T] (strictly

@@ -76,6 +76,18 @@ int gdn_conv_accept(const gdn_conv_dims *dims, int32_t *ring_pos, const int32_t 
                     const int32_t *accepted, int32_t *status, cudaStream_t stream);
 
 /*
+ * gdn_conv_advance -- the same convolution over committed tokens: a prompt, a chunk of one or single
+ * tokens.  y for x_0 .. x_{n-1} (n = chunk_len[b], NULL: T) after the ring's window, or after zeros where
+ * fresh[b] is not 0 (NULL: none; the ring is then not read); the last W-1 inputs go to the ring and ring_pos moves on
+ * by n (mod cap).  Rows t >= n of y get 0.  dims as above, but T is 1..2^20 (B * T <= 2^28, B <= 65535, T * D <= 2^40) and cap >= W - 1,
+ * cap >= 1 is enough.  Status bits as for gdn_conv_verify, _BAD_LEN also for chunk_len
+ * outside [0, T]; the sequence is skipped.
+ */
+int gdn_conv_advance(const gdn_conv_dims *dims, void *ring, int32_t *ring_pos, const int32_t *state_idx,
+                     const int32_t *chunk_len, const int32_t *fresh, const void *x, const float *weight,
+                     const float *bias, void *y, int32_t *status, cudaStream_t stream);
+
+/*
  * Gated RMSNorm fused with FP8 (E4M3) quantisation, per row of d values:
  *     r = 1 / sqrt(mean_i(o_i^2) + eps),   y_i = o_i * r * weight[i] * silu(z_i),
  *     q_i = E4M3(y_i * inv_scale)   (round to nearest even, saturated to +-448).

@@ -198,6 +198,46 @@ int gdn_replay_accept_fold(const gdn_replay_dims *dims, int32_t *buf_len,
                            int32_t *status, cudaStream_t stream);
 
 /*
+ * gdn_replay_advance -- committed tokens over the checkpoint itself: a prompt, a chunk of one, or
+ * single tokens that are decoded without a draft.  For every b with slot s = state_idx[b], token
+ * t < chunk_len[b] and value head h (its key head h / (H / Hk)), from S = state[s,h] (zero where
+ * fresh[b] is not 0; the old state is then not read):
+ *     S_t = alpha_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,   out[b,t,h,:] = S_t (scale q_t),
+ * and state[s,h] = S after the last token.  Rows t >= chunk_len[b] of out get 0.  The buffer has to be empty
+ * (buf_len[s] == 0; NULL: there is none): a sequence with buffered tokens is flushed first (force).
+ *   q, k  in_dtype [B, T, Hk, dk], v in_dtype [B, T, H, dv]: heads of a token dense, tokens a stride
+ *   apart (views of one projection's output), 16-byte aligned;  g, beta fp32 [B, T, H] (g <= 0, as above);
+ *   out fp32 [B, T, H, dv];  chunk_len int32 [B], NULL: T;  fresh int32 [B], NULL: none;
+ *   workspace: workspace_bytes >= gdn_replay_advance_workspace() bytes, 16-byte aligned, no initial
+ *   content; calls that overlap on the GPU need one each.
+ * GDN_STATUS_BAD_SLOT; _BAD_LEN (chunk_len outside [0, T], or a buffer that is not empty): the sequence is
+ * skipped, out and state unwritten.  _TIMEOUT, _DRAIN: no output or state of the call may be trusted.
+ */
+typedef struct {
+    int32_t B;          /* sequences, 0..65535 */
+    int32_t T;          /* rows per sequence, 1..2^20; B * T <= 2^28 */
+    int32_t H;          /* value heads, 1..1024 */
+    int32_t Hk;         /* key and query heads; H is a multiple */
+    int32_t dk, dv;     /* 64 or 128 */
+    int32_t n_slot;     /* >= B */
+    int32_t in_dtype;
+    float   scale;
+    int32_t flags;      /* GDN_FLAG_TEST_EXPIRE or 0 */
+    int64_t q_stride, k_stride, v_stride;   /* elements from token to token: >= Hk dk, Hk dk, H dv;
+                                               multiples of 16 bytes */
+} gdn_advance_dims;
+
+int gdn_replay_advance(const gdn_advance_dims *dims, float *state, const int32_t *state_idx,
+                       const int32_t *buf_len, const int32_t *chunk_len, const int32_t *fresh,
+                       const void *q, const void *k, const void *v, const float *g, const float *beta,
+                       float *out, void *workspace, int64_t workspace_bytes, int32_t *status,
+                       cudaStream_t stream);
+
+/* Bytes of workspace that gdn_replay_advance needs for these dims on the current device, or a
+ * negative GDN_ERR_* code. */
+int64_t gdn_replay_advance_workspace(const gdn_advance_dims *dims);
+
+/*
  * gdn_replay_kernel_family -- which kernels a verify / flush / verify_fold call with
  * these dims launches: GDN_FAMILY_TCGEN05 or GDN_FAMILY_PERTOKEN, or a negative
  * GDN_ERR_* code for dims the calls would reject.  Host only; launches nothing.  A

@@ -24,12 +24,15 @@ __all__ = ["Dims", "GdnError", "load", "gdn_replay_verify", "gdn_replay_accept",
            "gdn_gated_rmsnorm_fp8", "ConvLayer", "CONV_ACT_NONE", "CONV_ACT_SILU",
            "gdn_nonreplay_verify", "gdn_nonreplay_accept", "NonReplayLayer",
            "PageDims", "AttnDims", "RopeDims", "PagedCache", "AttnLayer", "ROPE_HALF", "ROPE_PAIRS",
-           "STATUS_BAD_PAGE", "STATUS_BAD_POS", "STATUS_BAD_TREE", "STATUS_NO_PAGES"]
+           "STATUS_BAD_PAGE", "STATUS_BAD_POS", "STATUS_BAD_TREE", "STATUS_NO_PAGES", "AdvanceDims",
+           "gdn_replay_advance", "gdn_replay_advance_workspace", "gdn_conv_advance", "DraftDims", "DraftSampler",
+           "STATUS_BAD_TOKEN", "STATUS_BAD_PROB"]
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
 STATUS_BAD_ACCEPT, STATUS_NO_ROOM, STATUS_BAD_LEN, STATUS_BAD_SLOT, STATUS_TIMEOUT = 1, 2, 4, 8, 16
 STATUS_DRAIN = 32
 STATUS_BAD_PAGE, STATUS_BAD_POS, STATUS_BAD_TREE, STATUS_NO_PAGES = 64, 128, 256, 512
+STATUS_BAD_TOKEN, STATUS_BAD_PROB = 1024, 2048
 FLAG_TEST_EXPIRE = 1
 FAMILY_TCGEN05, FAMILY_PERTOKEN = 1, 2
 FAMILY_NAMES = {FAMILY_TCGEN05: "tcgen05", FAMILY_PERTOKEN: "per-token"}
@@ -47,6 +50,25 @@ class Dims(ctypes.Structure):
 
     def __repr__(self):
         return "Dims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class AdvanceDims(ctypes.Structure):
+    """Mirror of ``gdn_advance_dims``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "H", "Hk", "dk", "dv", "n_slot", "in_dtype")] + \
+               [("scale", ctypes.c_float), ("flags", ctypes.c_int32)] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")]
+
+    def __repr__(self):
+        return "AdvanceDims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class DraftDims(ctypes.Structure):
+    """Mirror of ``gdn_draft_dims`` (include/gdndraft.h); the strides are taken from each call's tensors."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "V", "flags")] + \
+               [(n, ctypes.c_int64) for n in ("p_stride", "q_stride")]
+
+    def __repr__(self):
+        return "DraftDims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
 class ConvDims(ctypes.Structure):
@@ -134,6 +156,17 @@ def load(rebuild: bool = False) -> ctypes.CDLL:
         lib.gdn_pages_fork.argtypes = [C, I] + [P] * 5
         lib.gdn_pages_copy.argtypes = [C, I] + [P] * 3
         lib.gdn_pages_release.argtypes = [C, I] + [P] * 3
+        AD, DD = ctypes.POINTER(AdvanceDims), ctypes.POINTER(DraftDims)
+        lib.gdn_replay_advance.argtypes = [AD] + [P] * 12 + [ctypes.c_int64, P, P]
+        lib.gdn_replay_advance_workspace.argtypes = [AD]
+        lib.gdn_replay_advance_workspace.restype = ctypes.c_int64
+        lib.gdn_conv_advance.argtypes = [CD] + [P] * 11
+        lib.gdn_attn_chunk.argtypes = [C, I, A] + [P] * 6 + [ctypes.c_int64, P, P]
+        lib.gdn_attn_chunk_workspace.argtypes = [C, A]
+        lib.gdn_attn_chunk_workspace.restype = ctypes.c_int64
+        lib.gdn_draft_accept.argtypes = [DD] + [P] * 11
+        for f in (lib.gdn_replay_advance, lib.gdn_conv_advance, lib.gdn_attn_chunk, lib.gdn_draft_accept):
+            f.restype = ctypes.c_int
         for f in (lib.gdn_attn_stage, lib.gdn_tree_build, lib.gdn_attn_verify, lib.gdn_attn_accept,
                   lib.gdn_pages_reserve, lib.gdn_pages_fork, lib.gdn_pages_copy, lib.gdn_pages_release):
             f.restype = ctypes.c_int
@@ -268,6 +301,42 @@ def gdn_replay_flush(d: Dims, state, state_idx, buf_k, buf_v, buf_g, buf_beta, b
     _check("gdn_replay_flush", rc)
 
 
+def gdn_replay_advance_workspace(d: AdvanceDims) -> int:
+    """Bytes of workspace that gdn_replay_advance needs for these dims."""
+    n = load().gdn_replay_advance_workspace(ctypes.byref(d))
+    _check("gdn_replay_advance_workspace", min(n, 0))
+    return n
+
+
+def gdn_replay_advance(d: AdvanceDims, state, state_idx, buf_len, chunk_len, fresh, q, k, v, g, beta, out, workspace,
+                       status, stream=None):
+    """Committed tokens over the checkpoint (include/gdnreplay.h).  q, k and v may be views of one projection's
+    output; their strides are set in a copy of d."""
+    tin = _TORCH_IN.get(d.in_dtype)
+    if tin is None:
+        raise GdnError("gdn_replay_advance", -3)
+    d = AdvanceDims.from_buffer_copy(d)
+    dev = state.get_device() if isinstance(state, torch.Tensor) else -1
+    rows, tok = d.B * d.T, (d.B, d.T)
+    pq, d.q_stride = _tokens(q, tok + (d.Hk, d.dk), tin, dev, "q")
+    pk, d.k_stride = _tokens(k, tok + (d.Hk, d.dk), tin, dev, "k")
+    pv, d.v_stride = _tokens(v, tok + (d.H, d.dv), tin, dev, "v")
+    gate = tok + (d.H,)
+    rc = load().gdn_replay_advance(
+        ctypes.byref(d), _in(state, _F32, d.n_slot * d.H * d.dv * d.dk, "state"),
+        None if state_idx is None else _in(state_idx, _I32, d.B, "state_idx", dev),
+        None if buf_len is None else _in(buf_len, _I32, d.n_slot, "buf_len", dev),
+        None if chunk_len is None else _in(chunk_len, _I32, d.B, "chunk_len", dev),
+        None if fresh is None else _in(fresh, _I32, d.B, "fresh", dev), pq, pk, pv,
+        _in(g, _F32, rows * d.H, "g", dev, gate), _in(beta, _F32, rows * d.H, "beta", dev, gate),
+        _in(out, _F32, rows * d.H * d.dv, "out", dev, gate + (d.dv,)),
+        None if workspace is None else _in(workspace, torch.uint8, 0, "workspace", dev),
+        0 if workspace is None else workspace.numel(), _in(status, _I32, 1, "status", dev),
+        _raw_stream(stream, dev))
+    if rc:
+        raise GdnError("gdn_replay_advance", rc)
+
+
 class ReplayLayer:
     """Device-resident checkpoint, buffer and lengths of one GDN layer.
 
@@ -306,6 +375,36 @@ class ReplayLayer:
     def accept_fold(self, accepted, stream=None):
         gdn_replay_accept_fold(self.d, self.t["buf_len"], self.t["state_idx"], accepted,
                                self.status, stream)
+
+    def _advance_dims(self, T, Hk):
+        d = self.d
+        e = 16 // (2 if d.in_dtype == DTYPE_BF16 else 4)
+        return AdvanceDims(B=d.B, T=T, H=d.H, Hk=Hk, dk=d.dk, dv=d.dv, n_slot=d.n_slot, in_dtype=d.in_dtype, scale=d.scale,
+                           flags=d.flags, q_stride=Hk * d.dk // e * e, k_stride=Hk * d.dk // e * e, v_stride=d.H * d.dv)
+
+    def advance_workspace(self, T, Hk=None):
+        """A workspace for ``advance`` with T tokens per sequence and Hk key heads (None: as many as value
+        heads), or None where none is needed.  Layers that run one after the other may share one."""
+        n = gdn_replay_advance_workspace(self._advance_dims(T, self.d.H if Hk is None else Hk))
+        return torch.empty(n, dtype=torch.uint8, device=self.status.device) if n else None
+
+    def advance(self, q, k, v, g, beta, out, chunk_len=None, fresh=None, workspace=None, stream=None):
+        """Committed tokens (a prompt, a chunk of one, a single token) over the checkpoint, in place: q, k
+        [B, T, Hk, dk], v [B, T, H, dv] (views of one projection's output, say), g, beta [B, T, H], out fp32
+        [B, T, H, dv]; chunk_len int32 [B] tokens in use (None: T); fresh int32 [B], not 0: the sequence
+        starts from a zero state.  The sequences' buffers have to be empty (flush(force=True)).  Without
+        ``workspace`` (advance_workspace) one is allocated for the call."""
+        if q.dim() != 4 or k.dim() != 4:
+            raise ValueError("q, k: expected [B, T, Hk, dk]")
+        d = self._advance_dims(q.shape[1], k.shape[2])
+        if workspace is None:
+            n = gdn_replay_advance_workspace(d)
+            if n:
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(n, dtype=torch.uint8, device=self.status.device)
+        t = self.t
+        gdn_replay_advance(d, t["state"], t["state_idx"], t["buf_len"], chunk_len, fresh, q, k, v, g, beta, out, workspace,
+                           self.status, stream)
 
 
 # ---------------------------------------------------------- non-replay baseline
@@ -402,6 +501,24 @@ def gdn_conv_accept(d: ConvDims, ring_pos, state_idx, accepted, status, stream=N
     _check("gdn_conv_accept", rc)
 
 
+def gdn_conv_advance(d: ConvDims, ring, ring_pos, state_idx, chunk_len, fresh, x, weight, bias, y, status, stream=None):
+    """The convolution over committed tokens (include/gdnlayer.h); d.T tokens per sequence."""
+    tin, tout = _TORCH_IN.get(d.in_dtype), _TORCH_IN.get(d.out_dtype)
+    if tin is None or tout is None:
+        raise GdnError("gdn_conv_advance", -3)
+    dev = ring.get_device() if isinstance(ring, torch.Tensor) else -1
+    n, block = d.B * d.T * d.D, (d.B, d.T, d.D)
+    rc = load().gdn_conv_advance(
+        ctypes.byref(d), _in(ring, tin, d.n_slot * d.cap * d.D, "ring"), _in(ring_pos, _I32, d.n_slot, "ring_pos", dev),
+        None if state_idx is None else _in(state_idx, _I32, d.B, "state_idx", dev),
+        None if chunk_len is None else _in(chunk_len, _I32, d.B, "chunk_len", dev),
+        None if fresh is None else _in(fresh, _I32, d.B, "fresh", dev), _in(x, tin, n, "x", dev, block),
+        _in(weight, _F32, d.D * d.W, "weight", dev), None if bias is None else _in(bias, _F32, d.D, "bias", dev),
+        _in(y, tout, n, "y", dev, block), _in(status, _I32, 1, "status", dev), _raw_stream(stream, dev))
+    if rc:
+        raise GdnError("gdn_conv_advance", rc)
+
+
 class ConvLayer:
     """Device-resident convolution ring, write positions, weight and bias of one
     layer (``init``: CPU tensors ring, pos, state_idx, weight, bias; a state_idx of
@@ -421,6 +538,16 @@ class ConvLayer:
 
     def accept(self, accepted, stream=None):
         gdn_conv_accept(self.d, self.t["pos"], self.t["state_idx"], accepted, self.status, stream)
+
+    def advance(self, x, y, chunk_len=None, fresh=None, stream=None):
+        """Committed tokens (a prompt, a chunk of one, a single token): x, y [B, T, D]; chunk_len int32 [B]
+        tokens in use (None: T); fresh int32 [B], not 0: the sequence starts from a window of zeros."""
+        if x.dim() != 3:
+            raise ValueError(f"x: expected [B, T, D], got {tuple(x.shape)}")
+        d, t = ConvDims.from_buffer_copy(self.d), self.t
+        d.T = x.shape[1]
+        gdn_conv_advance(d, t["ring"], t["pos"], t["state_idx"], chunk_len, fresh, x, t["weight"], t["bias"], y, self.status,
+                         stream)
 
 
 # ---------------------------------------------------- gated RMSNorm + E4M3 codes
@@ -447,6 +574,35 @@ _I32, _F32 = torch.int32, torch.float32
 # makes (3 us a call against 0.1); the object is the way where torch lacks the function.
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _raw_stream(stream, index):
+    """Handle of ``stream``, of the device's current one when None."""
+    return _current_raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _tokens(t, shape, dtype, index, name):
+    """Address and token stride of a [B, T, heads, d] tensor that is dense within a token, its tokens
+    evenly spaced."""
+    B, T, heads, n = shape
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != index or index < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        raise ValueError(f"{name}: expected a tensor on the layer's device (cuda:{index}), got {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    sb, st, sh, se = t.stride()
+    if se != 1 or (heads > 1 and sh != n):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    if T == 1:
+        st = sb if B > 1 else heads * n                  # a single token's stride says nothing
+    elif B > 1 and sb != T * st:
+        raise ValueError(f"{name}: tokens must be evenly spaced over the batch")
+    return t.data_ptr(), st
 
 
 def _in(t, dtype, n, name, index=None, shape=None):
@@ -604,8 +760,9 @@ class AttnLayer:
         self._tok, self._row = (dims.B, dims.T), (dims.B, dims.T, dims.Hq)
         self._vec, self._kv = self._row + (c.d,), self._tok + (c.Hkv, c.d)
         dev = cache.status.device
-        need = cache._lib.gdn_attn_workspace(cache._c, self._ref) if dims.T <= 64 else 0
-        _check("gdn_attn_workspace", min(need, 0))
+        # (a chunk of up to 64 tokens is a verify, and needs its workspace; stage takes more rows than a chunk may have)
+        need = cache._lib.gdn_attn_chunk_workspace(cache._c, self._ref) if dims.B * dims.T <= 1 << 28 else 0
+        _check("gdn_attn_chunk_workspace", min(need, 0))
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         self.workspace, self.state_idx = workspace, state_idx
@@ -690,3 +847,67 @@ class AttnLayer:
             cache._status, self._stream(stream))
         if rc:
             raise GdnError("gdn_attn_verify", rc)
+
+    def chunk(self, q, out, lse=None, chunk_len=None, stream=None):
+        """Causal attention of a chunk of new tokens (a prompt, a part of one), staged already: q [B, T, Hq, d]
+        over the committed tokens and the chunk's own into ``out`` (and ``lse`` fp32 [B, T, Hq]).  chunk_len
+        int32 [B]: tokens in use (None: T, any number that the layer was made for).  seq_len does not move:
+        accept the chunk, or write the new lengths, afterwards."""
+        t, e, cache, at = self._dtype, self._elems, self.cache, self._index
+        rc = self._lib.gdn_attn_chunk(
+            cache._c, self.layer, self._ref, self._idx,
+            None if chunk_len is None else _in(chunk_len, _I32, self._B, "chunk_len", at),
+            _in(q, t, e, "q", at, self._vec), _in(out, t, e, "out", at, self._vec),
+            None if lse is None else _in(lse, _F32, self._heads, "lse", at, self._row), self._ws, self._ws_bytes,
+            cache._status, self._stream(stream))
+        if rc:
+            raise GdnError("gdn_attn_chunk", rc)
+
+
+# ------------------------------------------------------ drafted tokens against the target
+class DraftSampler:
+    """Speculative sampling: which drafted tokens of a block the target accepts, and the next token
+    (include/gdndraft.h).  ``status`` int32 [1] collects GDN_STATUS_* bits."""
+
+    def __init__(self, dims: DraftDims, device="cuda"):
+        self.d = DraftDims.from_buffer_copy(dims)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._lib, self._index = load(), self.status.get_device()
+
+    def _table(self, t, name):
+        """Address and row stride of probabilities [B, T, V], dense within a row, rows evenly spaced."""
+        d = self.d
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        if t.shape != (d.B, d.T, d.V):
+            raise ValueError(f"{name}: expected shape {(d.B, d.T, d.V)}, got {tuple(t.shape)}")
+        if t.get_device() != self._index:
+            raise ValueError(f"{name}: expected a tensor on cuda:{self._index}, got {t.device}")
+        if t.dtype is not _F32:
+            raise TypeError(f"{name}: expected torch.float32, got {t.dtype}")
+        sb, st, sv = t.stride()
+        if d.T == 1:
+            st = sb if d.B > 1 else d.V
+        if (d.V > 1 and sv != 1) or (d.B > 1 and d.T > 1 and sb != d.T * st):
+            raise ValueError(f"{name}: rows must be dense and evenly spaced over the batch")
+        return t.data_ptr(), st
+
+    def accept(self, tokens, probs, u, accepted, next_token, draft=None, parent=None, path=None, draft_len=None,
+               stream=None):
+        """tokens int32 [B, T], of which token 0 is decided already; probs fp32 [B, T, V] the target's
+        distribution after each token, draft fp32 [B, T, V] the drafter's that its children were drawn from (None: a
+        drafter certain of its tokens); u fp32 [B, T] uniform in [0, 1).  parent int32 [B, T] as for build_tree
+        (None: a chain).  Writes accepted int32 [B] (token 0 counted), next_token int32 [B] and path int32 [B, T]
+        (the accepted tokens' numbers, then -1; a chain needs none): what the layers' accepts take."""
+        d, at, n = DraftDims.from_buffer_copy(self.d), self._index, self.d.B * self.d.T
+        tok = (d.B, d.T)
+        pp, d.p_stride = self._table(probs, "probs")
+        pq, d.q_stride = (None, 0) if draft is None else self._table(draft, "draft")
+        rc = self._lib.gdn_draft_accept(
+            ctypes.byref(d), _in(tokens, _I32, n, "tokens", at, tok),
+            None if parent is None else _in(parent, _I32, n, "parent", at, tok), pp, pq, _in(u, _F32, n, "u", at, tok),
+            None if draft_len is None else _in(draft_len, _I32, d.B, "draft_len", at),
+            _in(accepted, _I32, d.B, "accepted", at), _in(next_token, _I32, d.B, "next_token", at),
+            None if path is None else _in(path, _I32, n, "path", at, tok), self.status.data_ptr(), _raw_stream(stream, at))
+        if rc:
+            raise GdnError("gdn_draft_accept", rc)

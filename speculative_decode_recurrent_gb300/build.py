@@ -14,11 +14,13 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f)
            for f in ("gdn_replay.cu", "gdn_replay_tc.cu", "gdn_layer_ops.cu", "gdn_nonreplay.cu",
-                     "gdn_attn.cu", "gdn_attn_tc.cu", "gdn_pages.cu")]
+                     "gdn_attn.cu", "gdn_attn_tc.cu", "gdn_pages.cu", "gdn_advance.cu", "gdn_advance_tc.cu",
+                     "gdn_attn_chunk.cu", "gdn_attn_chunk_tc.cu", "gdn_draft.cu")]
 HEADERS = [os.path.join(ROOT, "include", "gdnreplay.h"), os.path.join(ROOT, "include", "gdnlayer.h"),
            os.path.join(ROOT, "include", "gdnnonreplay.h"), os.path.join(ROOT, "include", "gdnattn.h"),
            os.path.join(PKG, "csrc", "replay_common.h"), os.path.join(PKG, "csrc", "tc_common.cuh"),
-           os.path.join(PKG, "csrc", "attn_common.h")]
+           os.path.join(ROOT, "include", "gdndraft.h"),
+           *(os.path.join(PKG, "csrc", f) for f in ("attn_common.h", "advance_common.h", "chunk_common.h", "tc_async.cuh"))]
 LIB = os.path.join(PKG, "_build", "libgdnreplay.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

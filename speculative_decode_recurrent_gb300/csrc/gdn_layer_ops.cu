@@ -1,6 +1,6 @@
 // gdn_layer_ops.cu -- the GDN layer steps either side of the recurrence, for
-// sm_103a: the causal convolution with pointer rollback, and the gated RMSNorm
-// fused with FP8 (E4M3) quantisation.  C ABI and layouts: include/gdnlayer.h.
+// sm_103a: the causal convolution with pointer rollback, the same over committed
+// tokens, and the gated RMSNorm fused with FP8 (E4M3) quantisation.  C ABI and layouts: include/gdnlayer.h.
 //
 // Both are streaming kernels (a few flops per byte): the design goal is whole
 // 16-byte vectors per thread, every load of a thread issued before its first use,
@@ -174,6 +174,136 @@ __global__ void conv_accept_kernel(int32_t *ring_pos, const int32_t *state_idx, 
     ring_pos[slot] = (pos + p) % cap;
 }
 
+// ------------------------------------------------- the convolution over committed tokens
+// A thread owns 16 bytes of channels (8 of bf16, 4 of fp32) of one sequence for kRun positions in a row: it reads its
+// run and the W - 1 inputs before it (the ring's window for the first run) and writes the run's outputs.  Inputs
+// are read (1 + (W - 1) / kRun) times, the second time from L2.  The ring is left alone here, its window is still
+// being read; the kernel after it (one launch on) puts the last inputs there.
+constexpr int kRun = 8;
+
+struct ConvAdvanceArgs {
+    void *ring;
+    int32_t *ring_pos;
+    const int32_t *state_idx, *chunk_len, *fresh;
+    const void *x;
+    const float *weight, *bias;
+    void *y;
+    int32_t *status;
+    int B, D, W, T, cap, n_slot, act;
+};
+
+struct ConvSeq {
+    int slot, pos, n, bad;
+    bool fresh;
+};
+__device__ __forceinline__ ConvSeq conv_seq(const ConvAdvanceArgs &a, int b) {
+    ConvSeq s;
+    s.slot = a.state_idx ? a.state_idx[b] : b;
+    s.n = a.chunk_len ? a.chunk_len[b] : a.T;
+    s.fresh = a.fresh && a.fresh[b] != 0;
+    s.pos = s.bad = 0;
+    if (s.slot < 0 || s.slot >= a.n_slot) {
+        s.bad = GDN_STATUS_BAD_SLOT;
+    } else {
+        s.pos = a.ring_pos[s.slot];
+        if (s.pos < 0 || s.pos >= a.cap || s.n < 0 || s.n > a.T) s.bad = GDN_STATUS_BAD_LEN;
+    }
+    return s;
+}
+
+template <typename TIn, typename TOut, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_advance_kernel(const ConvAdvanceArgs a, int chan_blocks)
+{
+    using Raw = typename In4<TIn>::Raw;
+    const int b = blockIdx.y, t0 = blockIdx.x / chan_blocks * kRun;
+    const int c0 = (blockIdx.x % chan_blocks * kConvThreads + threadIdx.x) * 4;
+    pdl_wait();
+    pdl_release();
+    if (c0 >= a.D) return;
+    const int D = a.D;
+    const ConvSeq sq = conv_seq(a, b);
+    if (sq.bad) {
+        if (c0 == 0 && t0 == 0) atomicOr(a.status, sq.bad);
+        return;
+    }
+    const int n = sq.n;
+    const size_t base = static_cast<size_t>(b) * a.T * D + c0;
+    const TIn *x = reinterpret_cast<const TIn *>(a.x) + base;
+    TOut *y = reinterpret_cast<TOut *>(a.y) + base;
+    Raw xr[kRun + W - 1];                                // inputs t0 - (W - 1) .. t0 + kRun - 1
+#pragma unroll
+    for (int i = 0; i < kRun + W - 1; ++i) {
+        const int t = t0 - (W - 1) + i;
+        xr[i] = Raw{};
+        if (t >= 0 && t < n) {
+            xr[i] = __ldg(reinterpret_cast<const Raw *>(x + static_cast<size_t>(t) * D));
+        } else if (t < 0 && !sq.fresh) {                 // (cap >= W - 1)
+            const TIn *ring = reinterpret_cast<const TIn *>(a.ring) + static_cast<size_t>(sq.slot) * a.cap * D + c0;
+            xr[i] = __ldg(reinterpret_cast<const Raw *>(ring + static_cast<size_t>((t + sq.pos + a.cap) % a.cap) * D));
+        }
+    }
+    float wt[4 * W], bias[4];
+#pragma unroll
+    for (int q = 0; q < W; ++q) {
+        const float4 w4 = __ldg(reinterpret_cast<const float4 *>(a.weight + static_cast<size_t>(c0) * W) + q);
+        wt[4 * q] = w4.x; wt[4 * q + 1] = w4.y; wt[4 * q + 2] = w4.z; wt[4 * q + 3] = w4.w;
+    }
+    bias[0] = bias[1] = bias[2] = bias[3] = 0.f;
+    if (a.bias) {
+        const float4 b4 = __ldg(reinterpret_cast<const float4 *>(a.bias + c0));
+        bias[0] = b4.x; bias[1] = b4.y; bias[2] = b4.z; bias[3] = b4.w;
+    }
+    float h[W][4];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) In4<TIn>::unpack(xr[j], h[j]);
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+        const int t = t0 + u;
+        if (t >= a.T) break;
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        if (t < n) {
+            In4<TIn>::unpack(xr[W - 1 + u], h[W - 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float acc = bias[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) acc = fmaf(wt[i * W + j], h[j][i], acc);
+                o[i] = a.act == GDN_CONV_ACT_SILU ? __fdividef(acc, 1.f + __expf(-acc)) : acc;   // 0 below -87
+            }
+#pragma unroll
+            for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[j][i] = h[j + 1][i];
+        }
+        store_out4<TOut>(y + static_cast<size_t>(t) * D, o);
+    }
+}
+
+// The last W - 1 inputs of each sequence into its ring, and its position.  A CTA has all channels of a
+// sequence, so that the position moves once all of it has been read.
+template <typename TIn>
+__global__ void __launch_bounds__(512) conv_ring_kernel(const ConvAdvanceArgs a)
+{
+    using Raw = typename In4<TIn>::Raw;
+    pdl_wait();
+    pdl_release();
+    const int b = blockIdx.x, D = a.D;
+    const ConvSeq sq = conv_seq(a, b);
+    if (sq.bad) return;                                  // (reported by the kernel before)
+    const int n = sq.n, cap = a.cap;
+    const TIn *x = reinterpret_cast<const TIn *>(a.x) + static_cast<size_t>(b) * a.T * D;
+    TIn *ring = reinterpret_cast<TIn *>(a.ring) + static_cast<size_t>(sq.slot) * cap * D;
+    for (int j = 1; j < a.W; ++j) {                      // input n - j
+        const int t = n - j;
+        if (t < 0 && !sq.fresh) break;                   // it is in the ring already
+        TIn *dst = ring + static_cast<size_t>(((sq.pos + t) % cap + cap) % cap) * D;
+        for (int c = threadIdx.x * 4; c < D; c += 512 * 4)
+            *reinterpret_cast<Raw *>(dst + c) = t >= 0 ? __ldg(reinterpret_cast<const Raw *>(x + static_cast<size_t>(t) * D + c)) : Raw{};
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) a.ring_pos[sq.slot] = (sq.pos + n) % cap;
+}
+
 // ------------------------------------------------- gated RMSNorm + E4M3 codes
 constexpr int kNormWarps = 8;
 
@@ -253,14 +383,20 @@ __global__ void __launch_bounds__(kNormWarps * 32) gated_rmsnorm_fp8_kernel(
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-int check_conv(const gdn_conv_dims *d) {
+int check_conv(const gdn_conv_dims *d, bool advance = false) {
     if (!d) return GDN_ERR_NULL;
     if ((d->in_dtype != GDN_DTYPE_BF16 && d->in_dtype != GDN_DTYPE_F32) ||
         (d->out_dtype != GDN_DTYPE_BF16 && d->out_dtype != GDN_DTYPE_F32))
         return GDN_ERR_DTYPE;
     if (d->B < 0 || d->n_slot < d->B || d->D < 8 || d->D % 8 != 0) return GDN_ERR_DIMS;
-    if (d->W < 1 || d->W > kTaps || d->T < 1 || d->T > 64) return GDN_ERR_DIMS;
-    if (d->cap < d->W - 1 + d->T || d->cap > 4096) return GDN_ERR_DIMS;
+    if (d->W < 1 || d->W > kTaps || d->T < 1) return GDN_ERR_DIMS;
+    if (advance) {
+        if (d->B > 65535 || d->T > 1 << 20 || static_cast<long long>(d->T) * d->D > 1ll << 40 || static_cast<long long>(d->B) * d->T > 1 << 28 || d->cap < 1 || d->cap < d->W - 1)
+            return GDN_ERR_DIMS;
+    } else if (d->T > 64 || d->cap < d->W - 1 + d->T) {
+        return GDN_ERR_DIMS;
+    }
+    if (d->cap > 4096) return GDN_ERR_DIMS;
     if (d->act != GDN_CONV_ACT_NONE && d->act != GDN_CONV_ACT_SILU) return GDN_ERR_DIMS;
     if (static_cast<long long>(d->n_slot) * d->cap * d->D > 0x7fffffffLL) return GDN_ERR_DIMS;
     return GDN_OK;
@@ -282,6 +418,17 @@ int launch_conv(const gdn_conv_dims *d, const ConvArgs &a, cudaStream_t s) {
         case 3: return launch_conv_w<TIn, TOut, 3>(d, a, s);
         default: return launch_conv_w<TIn, TOut, 4>(d, a, s);
     }
+}
+
+template <typename TIn, typename TOut>
+cudaError_t launch_conv_advance(const gdn_conv_dims *d, const ConvAdvanceArgs &a, cudaStream_t s) {
+    const int cb = (d->D / 4 + kConvThreads - 1) / kConvThreads;      // (runs x cb < 2^31: check_conv)
+    const dim3 grid(static_cast<unsigned>((d->T + kRun - 1) / kRun) * cb, d->B), block(kConvThreads);
+    const cudaError_t e = d->W == 1   ? launch_pdl(conv_advance_kernel<TIn, TOut, 1>, grid, block, 0, s, a, cb)
+                          : d->W == 2 ? launch_pdl(conv_advance_kernel<TIn, TOut, 2>, grid, block, 0, s, a, cb)
+                          : d->W == 3 ? launch_pdl(conv_advance_kernel<TIn, TOut, 3>, grid, block, 0, s, a, cb)
+                                      : launch_pdl(conv_advance_kernel<TIn, TOut, 4>, grid, block, 0, s, a, cb);
+    return e != cudaSuccess ? e : launch_pdl(conv_ring_kernel<TIn>, dim3(d->B), dim3(512), 0, s, a);
 }
 
 template <int D>
@@ -330,6 +477,27 @@ int gdn_conv_accept(const gdn_conv_dims *d, int32_t *ring_pos, const int32_t *st
     return launch_pdl(conv_accept_kernel, dim3((d->B + 127) / 128), dim3(128), 0, stream, ring_pos, state_idx,
                       accepted, d->B, d->n_slot, d->T, d->cap, status) == cudaSuccess
                ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int gdn_conv_advance(const gdn_conv_dims *d, void *ring, int32_t *ring_pos, const int32_t *state_idx,
+                     const int32_t *chunk_len, const int32_t *fresh, const void *x, const float *weight,
+                     const float *bias, void *y, int32_t *status, cudaStream_t stream)
+{
+    const int rc = check_conv(d, true);
+    if (rc) return rc;
+    if (d->B == 0) return GDN_OK;
+    if (!ring || !ring_pos || !x || !weight || !y || !status) return GDN_ERR_NULL;
+    if (!aligned(ring, 16) || !aligned(x, 16) || !aligned(y, 16) || !aligned(weight, 16) ||
+        (bias && !aligned(bias, 16)))
+        return GDN_ERR_DIMS;
+    const ConvAdvanceArgs a{ring, ring_pos, state_idx, chunk_len, fresh, x, weight, bias, y, status,
+                            d->B, d->D, d->W, d->T, d->cap, d->n_slot, d->act};
+    const bool in_bf = d->in_dtype == GDN_DTYPE_BF16, out_bf = d->out_dtype == GDN_DTYPE_BF16;
+    const cudaError_t e = in_bf ? (out_bf ? launch_conv_advance<__nv_bfloat16, __nv_bfloat16>(d, a, stream)
+                                          : launch_conv_advance<__nv_bfloat16, float>(d, a, stream))
+                                : (out_bf ? launch_conv_advance<float, __nv_bfloat16>(d, a, stream)
+                                          : launch_conv_advance<float, float>(d, a, stream));
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 int gdn_gated_rmsnorm_fp8(int32_t rows, int32_t d, const float *o, const void *z, int32_t z_dtype,
