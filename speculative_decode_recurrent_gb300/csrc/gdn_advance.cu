@@ -172,7 +172,7 @@ int check_advance(const gdn_advance_dims *d) {
     if ((d->dk != 64 && d->dk != 128) || (d->dv != 64 && d->dv != 128) || (d->flags & ~GDN_FLAG_TEST_EXPIRE)) return GDN_ERR_DIMS;
     if (static_cast<long long>(d->n_slot) * d->H * d->dv > 0x7fffffffLL) return GDN_ERR_DIMS;
     const int e = d->in_dtype == GDN_DTYPE_BF16 ? 2 : 4;
-    const int64_t lim = 1ll << 40;                                    // (T strides stay far below 2^63 bytes)
+    const int64_t lim = 1ll << 38;                                    // (a tensor map's stride is below 2^40 bytes)
     if (d->q_stride < static_cast<int64_t>(d->Hk) * d->dk || d->k_stride < static_cast<int64_t>(d->Hk) * d->dk ||
         d->v_stride < static_cast<int64_t>(d->H) * d->dv || d->q_stride * e % 16 || d->k_stride * e % 16 ||
         d->v_stride * e % 16 || d->q_stride > lim || d->k_stride > lim || d->v_stride > lim)
@@ -197,7 +197,7 @@ extern "C" {
 
 int64_t gdn_replay_advance_workspace(const gdn_advance_dims *d) {
     if (const int rc = check_advance(d)) return rc;
-    return 0;
+    return advance_tc_shape(d) && d->B > 0 ? advance_tc_workspace(d) : 0;
 }
 
 int gdn_replay_advance(const gdn_advance_dims *d, float *state, const int32_t *state_idx, const int32_t *buf_len,
@@ -213,6 +213,7 @@ int gdn_replay_advance(const gdn_advance_dims *d, float *state, const int32_t *s
         return GDN_ERR_DIMS;
     const AdvanceArgs a{state, state_idx, buf_len, chunk_len, fresh, q, k, v, g, beta, out, static_cast<char *>(workspace),
                         status, d->q_stride, d->k_stride, d->v_stride, d->B, d->T, d->H, d->Hk, d->n_slot, d->flags, d->scale};
+    if (advance_tc_shape(d)) return advance_tc(d, a, stream);
     const cudaError_t e = d->in_dtype == GDN_DTYPE_BF16 ? launch_tokens<__nv_bfloat16>(d, a, stream)
                                                         : launch_tokens<float>(d, a, stream);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;

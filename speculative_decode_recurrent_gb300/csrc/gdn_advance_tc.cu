@@ -1,6 +1,713 @@
+// gdn_advance_tc.cu -- gdn_replay_advance on the tensor cores (tcgen05), for sm_103a: the gated delta rule over
+// long bf16 chunks, 64 tokens at a time.  C ABI and layouts: include/gdnreplay.h.
+//
+// Mathematics.  For 64 tokens of one head, with G_t the running sum of the log-decays, gamma_t = e^{G_t}, and
+// A[t][s] = beta_t e^{G_t - G_s} (k_t.k_s) (s < t), the recurrence unrolls into the chunkwise form of "Parallelizing
+// Linear Transformers with the Delta Rule over Sequence Length" (NeurIPS 2024): with P = (I + A)^-1 diag(beta) and
+//     x_t = v_t - gamma_t S k_t                  (rows of x; S the state before the chunk)
+// the updates are u = P x, and so, with M[t][s] = scale e^{G_t - G_s} (q_t.k_s) (s <= t) and
+// D = diag(e^{G_63 - G_t}),
+//     o = scale gamma S q + (M P) x,    S' = gamma_63 S + E x,  E = K^T D P.
+// E (dk x 64) and M P (64 x 64) do not involve the state: the first kernel makes them for all chunks at once.  The
+// second walks the chunks of a head with the state at hand, two dependent products a chunk: [K;Q] S^T, then
+// E x (and (M P) x beside the next).  A slice of 32 value columns needs nothing of the others, so few heads still fill
+// many SMs.
+//
+// Precision.  Keys and queries are exact in bf16.  S, x, E and M P enter as two bf16 terms each (relative 2^-17), with
+// one product less where both operands have two; the state itself stays in fp32 registers through the walk.  (One tf32
+// term would leave 2^-11 of S per chunk in the state.)  The inverse is formed in fp32 by 16 x 16 blocks.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
 #include "advance_common.h"
+#include "tc_async.cuh"
+
 namespace gdn {
-bool advance_tc_shape(const gdn_advance_dims *) { return false; }
-int64_t advance_tc_workspace(const gdn_advance_dims *) { return 0; }
-int advance_tc(const gdn_advance_dims *, const AdvanceArgs &, cudaStream_t) { return 1; }
+namespace {
+
+using namespace tc;
+
+constexpr int kC = 64;                              // tokens of a chunk
+constexpr int kSlice = 32;                          // value columns of a slice
+
+// What the first kernel leaves of a chunk of a head, as the second one's operands lie in shared memory:
+// E as [dk][64 tokens] bf16 rows of 128 bytes (swizzled), first and second terms; M P as [64][64] likewise; gamma.
+template <int DK> struct Unit {
+    static constexpr int E_BYTES = DK * 128, MP_BYTES = kC * 128;
+    static constexpr int TILES = 2 * E_BYTES + 2 * MP_BYTES;
+    static constexpr int BYTES = TILES + 512;       // gamma [64] fp32 at TILES
+};
+
+struct TcAdvance {
+    AdvanceArgs a;
+    int b0;                                         // first sequence of the launch
+    int c0, chunks;                                 // first chunk, chunks of the launch
+    int dv;
+};
+
+// Tokens of the launch's chunks that are in use.
+__device__ __forceinline__ int tokens_here(const TcAdvance &ta, int n) { return max(0, min(n - ta.c0 * kC, ta.chunks * kC)); }
+
+// ------------------------------------------------------------- E and M P of every chunk
+constexpr int kPrepThreads = 128;
+
+template <int DK> struct PrepPlan {
+    static constexpr int LD = 68;                   // floats of a row of A and T: 16-byte rows, 4 banks apart
+    static constexpr int KQ = DK * 256;             // [K;Q]: atoms of 64 columns, 128 rows of 128 bytes each
+    static constexpr int OFF_P = KQ, OFF_M = OFF_P + 16384, OFF_A = OFF_M + 16384, OFF_T = OFF_A + 18432;
+    static constexpr int OFF_F = OFF_A;             // over A, once the inverse is formed
+    static constexpr int OFF_G = OFF_T + kC * LD * 4;      // G (two words), gamma, beta, decay to the end
+    static constexpr int OFF_BAR = OFF_G + 5 * kC * 4;
+    static constexpr int BYTES = OFF_BAR + 64;
+    static_assert(kC * LD * 4 <= 18432 && OFF_F % 1024 == 0, "A's room");
+};
+
+// 64 columns of this thread's lane from tcol on as two bf16 terms each, in the swizzled row `row` of the
+// tiles hi and lo in global memory.
+__device__ __forceinline__ void spill_row(uint32_t tcol, char *hi, char *lo, int row) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t r[32];
+        tmem_ld32(tcol + 32 * half, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                __nv_bfloat16 h0, l0, h1, l1;
+                split2(__uint_as_float(r[8 * c + 2 * i]), h0, l0);
+                split2(__uint_as_float(r[8 * c + 2 * i + 1]), h1, l1);
+                h[i] = pack2(h0, h1);
+                l[i] = pack2(l0, l1);
+            }
+            const uint32_t at = sw128(row, 4 * half + c);
+            *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+    }
 }
+
+// One CTA per (head, chunk, sequence).
+template <int DK>
+__global__ void __launch_bounds__(kPrepThreads) advance_prep_kernel(const TcAdvance ta)
+{
+    using P = PrepPlan<DK>;
+    const AdvanceArgs &a = ta.a;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int h = blockIdx.x, c = blockIdx.y, b = ta.b0 + blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
+    pdl_release();
+    const AdvanceSeq sq = advance_seq(a, b);
+    const int n = sq.bad ? 0 : tokens_here(ta, sq.n) - c * kC;          // tokens of this chunk in use
+    if (n <= 0) return;
+    if ((saddr(smem) & 1023u) || (a.flags & GDN_FLAG_TEST_EXPIRE)) {
+        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
+    float *sA = reinterpret_cast<float *>(smem + P::OFF_A), *sT = reinterpret_cast<float *>(smem + P::OFF_T);
+    float *sGh = reinterpret_cast<float *>(smem + P::OFF_G), *sGl = sGh + kC, *sGam = sGl + kC, *sBeta = sGam + kC, *sEnd = sBeta + kC;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 4);
+    if (tid == 0) {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, 256);
+    // ---- keys and queries into the swizzled tile, zeros past the last token
+    const size_t tok0 = static_cast<size_t>(b) * a.T + (ta.c0 + c) * kC;
+    const int hk = h / (a.H / a.Hk);
+    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k) + tok0 * a.k_stride + hk * DK;
+    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + tok0 * a.q_stride + hk * DK;
+    constexpr int VR = DK / 8, ROWS = kPrepThreads / VR, IT = kC / ROWS;      // 16-byte vectors of a row, rows at a time
+    {
+        const int vc = tid % VR, vr = tid / VR;
+        uint4 kr[IT], qr[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int t = vr + i * ROWS;
+            kr[i] = qr[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (t < n) {
+                kr[i] = __ldg(reinterpret_cast<const uint4 *>(kp + t * a.k_stride) + vc);
+                qr[i] = __ldg(reinterpret_cast<const uint4 *>(qp + t * a.q_stride) + vc);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int t = vr + i * ROWS;
+            uint8_t *at = smem + (vc >> 3) * 16384;
+            *reinterpret_cast<uint4 *>(at + sw128(t, vc & 7)) = kr[i];
+            *reinterpret_cast<uint4 *>(at + sw128(kC + t, vc & 7)) = qr[i];
+        }
+    }
+    if (warp == 0) {                                // compensated running sums of g
+        float hi[2], lo[2], be[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = lane + 32 * i;
+            const size_t at = (tok0 + t) * a.H + h;
+            hi[i] = t < n ? a.g[at] : 0.f;
+            be[i] = t < n ? a.beta[at] : 0.f;
+            lo[i] = 0.f;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float h2 = __shfl_up_sync(0xffffffffu, hi[i], off), l2 = __shfl_up_sync(0xffffffffu, lo[i], off);
+                if (lane >= off) {
+                    const float s1 = hi[i] + h2, bp = s1 - hi[i];
+                    lo[i] += l2 + ((hi[i] - (s1 - bp)) + (h2 - bp));
+                    hi[i] = s1;
+                }
+            }
+        }
+        {
+            const float ch = __shfl_sync(0xffffffffu, hi[0], 31), cl = __shfl_sync(0xffffffffu, lo[0], 31);
+            const float s1 = hi[1] + ch, bp = s1 - hi[1];
+            lo[1] += cl + ((hi[1] - (s1 - bp)) + (ch - bp));
+            hi[1] = s1;
+        }
+        const float eh = __shfl_sync(0xffffffffu, hi[1], 31), el = __shfl_sync(0xffffffffu, lo[1], 31);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = lane + 32 * i;
+            sGh[t] = hi[i];
+            sGl[t] = lo[i];
+            sGam[t] = __expf(hi[i] + lo[i]);
+            sEnd[t] = __expf((eh - hi[i]) + (el - lo[i]));
+            sBeta[t] = be[i];
+        }
+    }
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    // ---- [K;Q] K^T
+    if (warp == 0) {
+        const uint64_t d = desc_sw128(saddr(smem));
+        if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks) {
+                const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+                mma_bf16(tmem, desc_add(d, off), desc_add(d, off), idesc_mn(1, 128, kC), ks > 0);
+            }
+            mma_commit(&bar[0]);
+        }
+        __syncwarp();
+    }
+    bool ok = mbar_wait(&bar[0], 0);
+    tc_fence_after();
+    // ---- A in fp32 (rows of K), M as two bf16 terms (rows of Q)
+    const int t = tid & (kC - 1);
+    if (__all_sync(0xffffffffu, ok)) {
+        const float gh = sGh[t], gl = sGl[t], bt = sBeta[t];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t r[32];
+            tmem_ld32(tmem + lanes + 32 * half, r);
+            tmem_wait_ld();
+            float y[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const int s = 32 * half + j;
+                const float e = __expf((gh - sGh[s]) + (gl - sGl[s]));
+                y[j] = (warp < 2 ? s < t : s <= t) ? __uint_as_float(r[j]) * e * (warp < 2 ? bt : a.scale) : 0.f;
+            }
+            if (warp < 2) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4 *>(sA + t * P::LD + 32 * half + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t hh[4], ll[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        __nv_bfloat16 h0, l0, h1, l1;
+                        split2(y[8 * v + 2 * i], h0, l0);
+                        split2(y[8 * v + 2 * i + 1], h1, l1);
+                        hh[i] = pack2(h0, h1);
+                        ll[i] = pack2(l0, l1);
+                    }
+                    const uint32_t at = sw128(t, 4 * half + v);
+                    *reinterpret_cast<uint4 *>(smem + P::OFF_M + at) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                    *reinterpret_cast<uint4 *>(smem + P::OFF_M + 8192 + at) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    // ---- T = (I + A)^-1: the diagonal blocks by substitution, a thread per column
+    if (tid < kC) {
+        const int bi = tid >> 4, j = tid & 15;
+        const float *Ab = sA + 16 * bi * P::LD + 16 * bi;
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < r; k += 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(Ab + r * P::LD + k);       // (A is 0 from the diagonal on)
+                s0 = fmaf(y.x, x[k], s0);
+                if (k + 1 < r) s1 = fmaf(y.y, x[k + 1], s1);
+                if (k + 2 < r) s0 = fmaf(y.z, x[k + 2], s0);
+                if (k + 3 < r) s1 = fmaf(y.w, x[k + 3], s1);
+            }
+            x[r] = r == j ? 1.f : r < j ? 0.f : -(s0 + s1);
+            sT[(16 * bi + r) * P::LD + 16 * bi + j] = x[r];
+        }
+    }
+    __syncthreads();
+    // ---- the blocks below: T_ij = -T_ii sum_k A_ik T_kj, the sum kept in the block (j, i) for the moment
+    for (int d = 1; d < 4; ++d) {
+        for (int task = tid; task < (4 - d) * 64; task += kPrepThreads) {
+            const int j = task >> 6, i = j + d, r = (task >> 2) & 15, c4 = (task & 3) * 4;
+            const float *Ar = sA + (16 * i + r) * P::LD, *Tc = sT + 16 * j + c4;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = 16 * j; k < 16 * i; ++k) {
+                const float y = Ar[k];
+                const float4 z = *reinterpret_cast<const float4 *>(Tc + k * P::LD);
+                s.x = fmaf(y, z.x, s.x); s.y = fmaf(y, z.y, s.y); s.z = fmaf(y, z.z, s.z); s.w = fmaf(y, z.w, s.w);
+            }
+            *reinterpret_cast<float4 *>(sT + (16 * j + r) * P::LD + 16 * i + c4) = s;
+        }
+        __syncthreads();
+        for (int task = tid; task < (4 - d) * 64; task += kPrepThreads) {
+            const int j = task >> 6, i = j + d, r = (task >> 2) & 15, c4 = (task & 3) * 4;
+            const float *Tr = sT + (16 * i + r) * P::LD + 16 * i, *X = sT + 16 * j * P::LD + 16 * i + c4;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float y = -Tr[k];
+                const float4 z = *reinterpret_cast<const float4 *>(X + k * P::LD);
+                s.x = fmaf(y, z.x, s.x); s.y = fmaf(y, z.y, s.y); s.z = fmaf(y, z.z, s.z); s.w = fmaf(y, z.w, s.w);
+            }
+            *reinterpret_cast<float4 *>(sT + (16 * i + r) * P::LD + 16 * j + c4) = s;
+        }
+        __syncthreads();
+    }
+    // ---- P = T diag(beta) and F = D P as two bf16 terms each: row t, half of its columns
+    {
+        const int s0 = (tid >> 6) * 32;
+        const float end = sEnd[t];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            uint32_t ph[4], pl[4], fh[4], fl[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int s = s0 + 8 * v + 2 * i + e;
+                    y[e] = s <= t ? sT[t * P::LD + s] * sBeta[s] : 0.f;
+                }
+                __nv_bfloat16 h0, l0, h1, l1;
+                split2(y[0], h0, l0);
+                split2(y[1], h1, l1);
+                ph[i] = pack2(h0, h1);
+                pl[i] = pack2(l0, l1);
+                split2(y[0] * end, h0, l0);
+                split2(y[1] * end, h1, l1);
+                fh[i] = pack2(h0, h1);
+                fl[i] = pack2(l0, l1);
+            }
+            const uint32_t at = sw128(t, (s0 >> 3) + v);
+            *reinterpret_cast<uint4 *>(smem + P::OFF_P + at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+            *reinterpret_cast<uint4 *>(smem + P::OFF_P + 8192 + at) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+            *reinterpret_cast<uint4 *>(smem + P::OFF_F + at) = make_uint4(fh[0], fh[1], fh[2], fh[3]);
+            *reinterpret_cast<uint4 *>(smem + P::OFF_F + 8192 + at) = make_uint4(fl[0], fl[1], fl[2], fl[3]);
+        }
+    }
+    fence_proxy_async();
+    __syncthreads();
+    // ---- E = K^T F (rows dk: the keys read MN-major) and M P (lanes 64..127: M begins 64 rows into its operand)
+    if (warp == 0) {
+        tc_fence_after();
+        const uint64_t dk = desc_mn_sw128(saddr(smem), 16384), df = desc_mn_sw128(saddr(smem) + P::OFF_F, 8192);
+        const uint64_t dp = desc_mn_sw128(saddr(smem) + P::OFF_P, 8192), dm = desc_sw128(saddr(smem) + P::OFF_M - 8192);
+        constexpr uint32_t idE = idesc_mn(1, 128, kC) | kIdescMnMajorA | kIdescMnMajorB, idM = idesc_mn(1, 128, kC) | kIdescMnMajorB;
+        if (elect_one() && ok) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                mma_bf16(tmem + 64, desc_add(dk, ks * 2048), desc_add(df, ks * 2048), idE, ks > 0);
+                mma_bf16(tmem + 64, desc_add(dk, ks * 2048), desc_add(df, 8192 + ks * 2048), idE, 1);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                mma_bf16(tmem + 128, desc_add(dm, ks * 32), desc_add(dp, ks * 2048), idM, ks > 0);
+                mma_bf16(tmem + 128, desc_add(dm, ks * 32), desc_add(dp, 8192 + ks * 2048), idM, 1);
+                mma_bf16(tmem + 128, desc_add(dm, 8192 + ks * 32), desc_add(dp, ks * 2048), idM, 1);
+            }
+            mma_commit(&bar[1]);
+        }
+        __syncwarp();
+    }
+    ok = ok && mbar_wait(&bar[1], 0);
+    tc_fence_after();
+    char *unit = a.ws + ((static_cast<size_t>(blockIdx.z) * ta.chunks + c) * a.H + h) * Unit<DK>::BYTES;
+    if (__all_sync(0xffffffffu, ok)) {
+        if (warp * 32 < DK) spill_row(tmem + lanes + 64, unit, unit + Unit<DK>::E_BYTES, tid);
+        if (warp >= 2)
+            spill_row(tmem + lanes + 128, unit + 2 * Unit<DK>::E_BYTES, unit + 2 * Unit<DK>::E_BYTES + Unit<DK>::MP_BYTES, t);
+        if (tid < kC) reinterpret_cast<float *>(unit + Unit<DK>::TILES)[tid] = sGam[tid];
+    } else if (lane == 0) {                         // (nothing more was issued unless the second wait ran out: one more bounded wait)
+        atomicOr(a.status, kStatusTimeout);
+        if (!mbar_wait(&bar[1], 0)) atomicOr(a.status, GDN_STATUS_DRAIN);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 256);
+}
+
+// ------------------------------------------------------------- the walk over the chunks
+template <int DK, int NS> struct ScanPlan {
+    static constexpr int KQ = DK * 256, STAGE = KQ + Unit<DK>::TILES, STAGES = 2;
+    static constexpr int S_BYTES = DK * 128, X_BYTES = kC * 128;      // rows of 32 first terms, 32 second ones
+    static constexpr int OFF_S = STAGES * STAGE, OFF_X = OFF_S + NS * S_BYTES, OFF_BAR = OFF_X + NS * X_BYTES;
+    static constexpr int BYTES = OFF_BAR + 256;
+    static constexpr int ROWS = NS * 128, LOAD_WARP = ROWS / 32, MMA_WARP = LOAD_WARP + 1, THREADS = ROWS + 32 + NS * 32;
+    static constexpr int TCOLS = 192, TMEM_COLS = NS == 1 ? 256 : 512;         // of a slice: [K;Q] S^T, E x, M P x, 64 columns each
+    static_assert(NS * TCOLS <= TMEM_COLS && BYTES <= 227 * 1024 && STAGE % 1024 == 0, "plan");
+};
+
+// 32 numbers as two bf16 terms in row `row` of a tile of 128-byte rows: first terms, then second ones.
+__device__ __forceinline__ void put_row(uint8_t *tile, int row, const float (&y)[32]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __nv_bfloat16 h0, l0, h1, l1;
+            split2(y[8 * c + 2 * i], h0, l0);
+            split2(y[8 * c + 2 * i + 1], h1, l1);
+            h[i] = pack2(h0, h1);
+            l[i] = pack2(l0, l1);
+        }
+        *reinterpret_cast<uint4 *>(tile + sw128(row, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(tile + sw128(row, c + 4)) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+// The product's 32 columns: those with the first terms and those with the second ones added.
+__device__ __forceinline__ void get_row(uint32_t tcol, float (&y)[32]) {
+    uint32_t r[32], s[32];
+    tmem_ld32(tcol, r);
+    tmem_ld32(tcol + 32, s);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]) + __uint_as_float(s[j]);
+}
+
+// One CTA per (NS slices of value columns, head, sequence).  A slice has four row warps and an MMA warp; one warp loads for
+// all.  Row r of a slice's warps has token r (K's products, r < 64), token r - 64 (Q's) and key dimension r of
+// the state.  Everything that a buffer's next use overwrites has been read by then: see each arrival.
+template <int DK, int NS>
+__global__ void __launch_bounds__(ScanPlan<DK, NS>::THREADS, 1)
+advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ TcAdvance ta)
+{
+    using P = ScanPlan<DK, NS>;
+    const AdvanceArgs &a = ta.a;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int h = blockIdx.y, b = ta.b0 + blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty = full + 2, *d1 = empty + 2, *d2 = d1 + NS,
+             *d3 = d2 + NS, *s_ready = d3 + NS, *x_ready = s_ready + NS, *drain = x_ready + NS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + NS);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    static_assert((4 + 6 * NS) * 8 + 8 <= 256, "barriers");
+    pdl_wait();
+    pdl_release();
+    const AdvanceSeq sq = advance_seq(a, b);
+    if (sq.bad) {
+        if (tid == 0 && blockIdx.x == 0 && h == 0 && ta.c0 == 0) atomicOr(a.status, sq.bad);
+        return;
+    }
+    const int n = tokens_here(ta, sq.n), chunks = (n + kC - 1) / kC;
+    const int dv0 = blockIdx.x * (NS * kSlice);
+    // rows of this launch past the sequence's last token
+    {
+        const int t1 = min(a.T, (ta.c0 + ta.chunks) * kC);
+        float *out = a.out + (static_cast<size_t>(b) * a.T * a.H + h) * ta.dv + dv0;
+        for (int e = tid; ; e += P::THREADS) {
+            const int t = ta.c0 * kC + n + e / (NS * kSlice);
+            if (t >= t1) break;
+            out[static_cast<size_t>(t) * a.H * ta.dv + e % (NS * kSlice)] = 0.f;
+        }
+    }
+    const bool zero = sq.fresh && ta.c0 == 0;       // starts from a zero state
+    if (n == 0) {
+        if (zero)
+            for (int e = tid; e < NS * kSlice * DK; e += P::THREADS)
+                a.state[((static_cast<size_t>(sq.slot) * a.H + h) * ta.dv + dv0) * DK + e] = 0.f;
+        return;
+    }
+    if (saddr(smem) & 1023u) {
+        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
+    if (tid == 0) {
+        const bool expire = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], NS);
+        }
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&d1[i], 1);
+            mbar_init(&d2[i], 1);
+            mbar_init(&d3[i], 1);
+            mbar_init(&s_ready[i], 128);
+            mbar_init(&x_ready[i], 128);
+            mbar_init(&drain[i], 1);
+        }
+        *abort = expire;
+        if (expire) atomicOr(a.status, kStatusTimeout);
+        fence_mbar_init();
+    }
+    if (warp == P::LOAD_WARP) tmem_alloc(tmem_slot, P::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {         // the same answer in a whole warp
+        bool ok = !*abort && mbar_wait(bar, parity);
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        if (!ok && lane == 0 && !*abort) {
+            *abort = 1;
+            atomicOr(a.status, kStatusTimeout);
+        }
+        return ok;
+    };
+    const char *units = a.ws + (static_cast<size_t>(blockIdx.z) * ta.chunks * a.H + h) * Unit<DK>::BYTES;
+    const size_t ustep = static_cast<size_t>(a.H) * Unit<DK>::BYTES;
+    if (warp == P::LOAD_WARP) {
+        // ------------------------------------------------------ loads
+        const int hk = h / (a.H / a.Hk);
+        int c = 0;
+        for (; c < chunks; ++c) {
+            const int st = c & 1;
+            if (c >= 2 && !wait(&empty[st], ((c >> 1) - 1) & 1)) break;
+            if (*abort) break;
+            if (elect_one()) {
+                uint8_t *dst = smem + st * P::STAGE;
+                const int tok = b * a.T + (ta.c0 + c) * kC;           // (B T <= 2^28)
+                mbar_expect_tx(&full[st], P::STAGE);
+#pragma unroll
+                for (int at = 0; at < DK / 64; ++at) {
+                    tma_load_3d(dst + at * 16384, &tm_k, at * 64, hk, tok, &full[st]);
+                    tma_load_3d(dst + at * 16384 + 8192, &tm_q, at * 64, hk, tok, &full[st]);
+                }
+                bulk_load(dst + P::KQ, units + c * ustep, Unit<DK>::TILES, &full[st]);
+            }
+            __syncwarp();
+        }
+        if (*abort) {                               // copies in flight end before the CTA does
+            for (int i = max(0, c - 2); i < c; ++i)
+                if (!mbar_wait(&full[i & 1], (i >> 1) & 1) && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
+        }
+    } else if (warp >= P::MMA_WARP) {
+        // ------------------------------------------------------ MMAs
+        const int sl = warp - P::MMA_WARP;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + sl * P::TCOLS;
+        const uint64_t dS = desc_mn_sw128(saddr(smem) + P::OFF_S + sl * P::S_BYTES, 8192);
+        const uint64_t dX = desc_mn_sw128(saddr(smem) + P::OFF_X + sl * P::X_BYTES, 8192);
+        const uint64_t dA = desc_sw128(saddr(smem));
+        constexpr uint32_t id = idesc_mn(1, 128, 64) | kIdescMnMajorB;
+        bool ok = true;
+        int c = 0;
+        for (; c < chunks; ++c) {
+            const int st = c & 1;
+            ok = wait(&full[st], (c >> 1) & 1) && wait(&s_ready[sl], c & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kq = desc_add(dA, st * P::STAGE), e = desc_add(kq, P::KQ), mp = desc_add(e, 2 * Unit<DK>::E_BYTES - 8192);
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    mma_bf16(tm, desc_add(kq, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dS, ks * 2048), id, ks > 0);
+                mma_commit(&d1[sl]);
+            }
+            __syncwarp();
+            ok = wait(&x_ready[sl], c & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)      // the first terms of E, then the second ones
+                    mma_bf16(tm + 64, desc_add(e, (ks >> 2) * Unit<DK>::E_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
+                mma_commit(&d2[sl]);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_bf16(tm + 128, desc_add(mp, (ks >> 2) * Unit<DK>::MP_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
+                mma_commit(&d3[sl]);
+                mma_commit(&empty[st]);
+            }
+            __syncwarp();
+        }
+        if (!ok && c > 0) {                         // MMAs in flight end before their memory is given back
+            if (elect_one()) mma_commit(&drain[sl]);
+            __syncwarp();
+            if (!mbar_wait(&drain[sl], 0) && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
+        }
+    } else {
+        // ------------------------------------------------------ rows
+        const int sl = warp >> 2, row = tid & 127, t = row & (kC - 1);
+        const bool keys = row < kC;                 // (the same in a warp, as the next)
+        const bool has = row < DK;
+        const uint32_t tm = tmem + sl * P::TCOLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        uint8_t *sS = smem + P::OFF_S + sl * P::S_BYTES, *sX = smem + P::OFF_X + sl * P::X_BYTES;
+        const int col0 = dv0 + sl * kSlice;
+        float *st = a.state + ((static_cast<size_t>(sq.slot) * a.H + h) * ta.dv + col0) * DK + row;
+        float S[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[j] = has && !zero ? st[j * DK] : 0.f;
+        const size_t tok0 = static_cast<size_t>(b) * a.T + ta.c0 * kC + t;
+        const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v) + tok0 * a.v_stride + h * ta.dv + col0;
+        float *op = a.out + (tok0 * a.H + h) * ta.dv + col0;
+        uint4 v[4];
+        float gam = 0.f, gend = 0.f;
+        auto fetch = [&](int c) {
+            const float *gp = reinterpret_cast<const float *>(units + c * ustep + Unit<DK>::TILES);
+            gam = __ldcg(gp + t);
+            gend = __ldcg(gp + kC - 1);
+            if (keys) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = c * kC + t < n ? __ldg(reinterpret_cast<const uint4 *>(vp + static_cast<size_t>(c) * kC * a.v_stride) + i)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        fetch(0);
+        if (has) put_row(sS, row, S);
+        fence_proxy_async();
+        mbar_arrive(&s_ready[sl]);
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            float y[32], o[32];
+            ok = wait(&d1[sl], c & 1);
+            if (!ok) break;
+            tc_fence_after();
+            get_row(tm, y);
+            if (keys) {                             // x = v - gamma S k; nothing of rows past the last token
+                const bool live = c * kC + t < n;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f[8];
+                    bf16x8_to_f32(v[i], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[8 * i + e] = live ? fmaf(-gam, y[8 * i + e], f[e]) : 0.f;
+                }
+                put_row(sX, t, y);
+                fence_proxy_async();
+            } else {
+                const float f = gam * a.scale;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = f * y[j];
+            }
+            const float ge = gend;
+            tc_fence_before();
+            mbar_arrive(&x_ready[sl]);              // this row has read [K;Q] S^T (and, before it, the last M P x)
+            if (c + 1 < chunks) fetch(c + 1);
+            ok = wait(&d2[sl], c & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (has) {
+                get_row(tm + 64, y);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[j] = fmaf(ge, S[j], y[j]);
+                put_row(sS, row, S);
+                fence_proxy_async();
+            }
+            tc_fence_before();
+            mbar_arrive(&s_ready[sl]);              // this row has read E x; S is in place
+            if (!keys) {
+                ok = wait(&d3[sl], c & 1);
+                if (!ok) break;
+                tc_fence_after();
+                get_row(tm + 128, y);
+                if (c * kC + t < n) {
+                    float4 *dst = reinterpret_cast<float4 *>(op + static_cast<size_t>(c) * kC * a.H * ta.dv);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dst[j] = make_float4(o[4 * j] + y[4 * j], o[4 * j + 1] + y[4 * j + 1], o[4 * j + 2] + y[4 * j + 2],
+                                             o[4 * j + 3] + y[4 * j + 3]);
+                }
+            }
+        }
+        if (ok && has)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) st[j * DK] = S[j];
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == P::LOAD_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, P::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+constexpr int64_t kBudget = 256ll << 20;            // of workspace: chunks beyond it follow in further launches
+
+int64_t unit_bytes(const gdn_advance_dims *d) { return d->dk == 64 ? Unit<64>::BYTES : Unit<128>::BYTES; }
+int seqs_per_launch(const gdn_advance_dims *d) {
+    const int64_t n = kBudget / (unit_bytes(d) * d->H);
+    return static_cast<int>(n < 1 ? 1 : n < d->B ? n : d->B);
+}
+int chunks_per_launch(const gdn_advance_dims *d) {
+    const int64_t all = (d->T + kC - 1) / kC, n = kBudget / (unit_bytes(d) * d->H * seqs_per_launch(d));
+    return static_cast<int>(n < 1 ? 1 : n < all ? n : all);
+}
+
+// Keys or queries as [B T][Hk][dk]; boxes of 64 columns of one head, 64 tokens.
+bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int64_t stride) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d->dk), static_cast<cuuint64_t>(d->Hk), static_cast<cuuint64_t>(d->B) * d->T};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d->dk) * 2, static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[3] = {64, 1, kC}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int NS>
+int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
+    using P = ScanPlan<DK, NS>;
+    CUtensorMap mk, mq;
+    if (!token_map(&mk, a.k, d, d->k_stride) || !token_map(&mq, a.q, d, d->q_stride)) return GDN_ERR_LAUNCH;
+    if (cudaFuncSetAttribute(advance_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepPlan<DK>::BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(advance_scan_kernel<DK, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    const int all = (d->T + kC - 1) / kC, step = chunks_per_launch(d), seqs = seqs_per_launch(d);
+    TcAdvance ta{a, 0, 0, 0, d->dv};
+    for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += seqs)
+        for (ta.c0 = 0; ta.c0 < all; ta.c0 += step) {
+            const int nb = d->B - ta.b0 < seqs ? d->B - ta.b0 : seqs;
+            ta.chunks = all - ta.c0 < step ? all - ta.c0 : step;
+            if (launch_pdl(advance_prep_kernel<DK>, dim3(d->H, ta.chunks, nb), dim3(kPrepThreads), PrepPlan<DK>::BYTES, s, ta) != cudaSuccess ||
+                launch_pdl(advance_scan_kernel<DK, NS>, dim3(d->dv / (NS * kSlice), d->H, nb), dim3(P::THREADS), P::BYTES, s, mk, mq, ta) !=
+                    cudaSuccess)
+                return GDN_ERR_LAUNCH;
+        }
+    return GDN_OK;
+}
+
+}  // namespace
+
+// Up to 32 tokens the token-by-token kernel is faster.
+bool advance_tc_shape(const gdn_advance_dims *d) { return d->in_dtype == GDN_DTYPE_BF16 && d->T > 32; }
+
+int64_t advance_tc_workspace(const gdn_advance_dims *d) {
+    return unit_bytes(d) * d->H * seqs_per_launch(d) * chunks_per_launch(d);
+}
+
+int advance_tc(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
+    // Slices of a CTA: one where that leaves SMs without work, else two.
+    const bool one = static_cast<long long>(d->B) * d->H * (d->dv / kSlice) <= sm_count();
+    return d->dk == 64 ? (one ? launch<64, 1>(d, a, s) : launch<64, 2>(d, a, s)) : one ? launch<128, 1>(d, a, s) : launch<128, 2>(d, a, s);
+}
+
+}  // namespace gdn
