@@ -49,49 +49,94 @@ struct TcAdvance {
 // Tokens of the launch's chunks that are in use.
 __device__ __forceinline__ int tokens_here(const TcAdvance &ta, int n) { return max(0, min(n - ta.c0 * kC, ta.chunks * kC)); }
 
-// ------------------------------------------------------------- E and M P of every chunk
-constexpr int kPrepThreads = 128;
+// Two numbers as two packed bf16 terms each (the sum is the number to a relative 2^-17); NaN stays in both.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t &h, uint32_t &l) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x, y);
+    h = *reinterpret_cast<const uint32_t *>(&a);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x - __uint_as_float(h << 16), y - __uint_as_float(h & 0xffff0000u));
+    l = *reinterpret_cast<const uint32_t *>(&b);
+}
+// Eight of them as one 16-byte chunk of each term.
+__device__ __forceinline__ void split8(const float *y, uint4 &h, uint4 &l) {
+    split_pair(y[0], y[1], h.x, l.x);
+    split_pair(y[2], y[3], h.y, l.y);
+    split_pair(y[4], y[5], h.z, l.z);
+    split_pair(y[6], y[7], h.w, l.w);
+}
 
+// ------------------------------------------------------------- E and M P of every chunk
+constexpr int kPrepThreads = 256;
+
+// Shared memory, 70 KB, so that three CTAs share an SM: [K;Q] as atoms of 64 columns, 128 rows of 128 bytes each (M's
+// terms go over the queries' rows of the two, E's over the whole at the end); A in fp32 (then F, then M P's terms); T in
+// fp32 (then P).
 template <int DK> struct PrepPlan {
     static constexpr int LD = 68;                   // floats of a row of A and T: 16-byte rows, 4 banks apart
-    static constexpr int KQ = DK * 256;             // [K;Q]: atoms of 64 columns, 128 rows of 128 bytes each
-    static constexpr int OFF_P = KQ, OFF_M = OFF_P + 16384, OFF_A = OFF_M + 16384, OFF_T = OFF_A + 18432;
-    static constexpr int OFF_F = OFF_A;             // over A, once the inverse is formed
+    static constexpr int OFF_M = 8192, ATOM = 16384;
+    static constexpr int OFF_A = 32768, OFF_T = OFF_A + 18432;
     static constexpr int OFF_G = OFF_T + kC * LD * 4;      // G (two words), gamma, beta, decay to the end
     static constexpr int OFF_BAR = OFF_G + 5 * kC * 4;
     static constexpr int BYTES = OFF_BAR + 64;
-    static_assert(kC * LD * 4 <= 18432 && OFF_F % 1024 == 0, "A's room");
+    static_assert(kC * LD * 4 <= 18432 && OFF_T % 1024 == 0, "A's room");
 };
 
-// 64 columns of this thread's lane from tcol on as two bf16 terms each, in the swizzled row `row` of the
-// tiles hi and lo in global memory.
-__device__ __forceinline__ void spill_row(uint32_t tcol, char *hi, char *lo, int row) {
+// One level of the inverse: with the diagonal blocks of N rows of T = (I + A)^-1 in place, those of 2 N:
+// T21 = -T22 A21 T11.  X = A21 T11 lies in the block (1, 2) for the moment, so the loops stay clear of what
+// is above the diagonal blocks of 8.  A thread has N / 8 neighbouring elements.
+template <int N, int LD>
+__device__ __forceinline__ void inverse_level(const float *sA, float *sT, int tid) {
+    constexpr int W = N / 8;
+    const int c = (tid & 7) * W, r = (tid >> 3) % N, lo = tid / (8 * N) * 2 * N, hi = lo + N;
+    float x[W];
+    auto product = [&](const float *row, const float *cols, int k0, int k1, float sign) {      // sums over [k0, k1), multiples of 4
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        uint32_t r[32];
-        tmem_ld32(tcol + 32 * half, r);
-        tmem_wait_ld();
+        for (int i = 0; i < W; ++i) x[i] = 0.f;
+#pragma unroll 2
+        for (int k = k0; k < k1; k += 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(row + k);
+            const float yy[4] = {sign * y.x, sign * y.y, sign * y.z, sign * y.w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t h[4], l[4];
+            for (int q = 0; q < 4; ++q) {
+                const float *z = cols + (k + q) * LD;
+                if constexpr (W == 4) {
+                    const float4 zz = *reinterpret_cast<const float4 *>(z);
+                    x[0] = fmaf(yy[q], zz.x, x[0]); x[1] = fmaf(yy[q], zz.y, x[1]);
+                    x[2] = fmaf(yy[q], zz.z, x[2]); x[3] = fmaf(yy[q], zz.w, x[3]);
+                } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                __nv_bfloat16 h0, l0, h1, l1;
-                split2(__uint_as_float(r[8 * c + 2 * i]), h0, l0);
-                split2(__uint_as_float(r[8 * c + 2 * i + 1]), h1, l1);
-                h[i] = pack2(h0, h1);
-                l[i] = pack2(l0, l1);
+                    for (int i = 0; i < W; ++i) x[i] = fmaf(yy[q], z[i], x[i]);
+                }
             }
-            const uint32_t at = sw128(row, 4 * half + c);
-            *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
         }
+    };
+    product(sA + (hi + r) * LD + lo, sT + lo * LD + lo + c, c & ~7, N, 1.f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) sT[(lo + r) * LD + hi + c + i] = x[i];
+    __syncthreads();
+    product(sT + (hi + r) * LD + hi, sT + lo * LD + hi + c, 0, (r | 7) + 1, -1.f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) sT[(hi + r) * LD + lo + c + i] = x[i];
+    __syncthreads();
+}
+
+// 32 columns of this thread's lane from tcol on as two terms each, in columns 32 half .. of row `row` of the tiles hi and lo.
+__device__ __forceinline__ void stage_row(uint32_t tcol, uint8_t *hi, uint8_t *lo, int row, int half) {
+    uint32_t r[32];
+    tmem_ld32(tcol, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint4 h, l;
+        split8(reinterpret_cast<const float *>(r) + 8 * c, h, l);
+        const uint32_t at = sw128(row, 4 * half + c);
+        *reinterpret_cast<uint4 *>(hi + at) = h;
+        *reinterpret_cast<uint4 *>(lo + at) = l;
     }
 }
 
-// One CTA per (head, chunk, sequence).
+// One CTA per (head, chunk, sequence).  Warps w and w + 4 share TMEM lanes 32 (w % 4) .. and halve the columns.
 template <int DK>
-__global__ void __launch_bounds__(kPrepThreads) advance_prep_kernel(const TcAdvance ta)
+__global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcAdvance ta)
 {
     using P = PrepPlan<DK>;
     const AdvanceArgs &a = ta.a;
@@ -115,7 +160,7 @@ __global__ void __launch_bounds__(kPrepThreads) advance_prep_kernel(const TcAdva
         mbar_init(&bar[1], 1);
         fence_mbar_init();
     }
-    if (warp == 0) tmem_alloc(tmem_slot, 256);
+    if (warp == 1) tmem_alloc(tmem_slot, 128);
     // ---- keys and queries into the swizzled tile, zeros past the last token
     const size_t tok0 = static_cast<size_t>(b) * a.T + (ta.c0 + c) * kC;
     const int hk = h / (a.H / a.Hk);
@@ -134,63 +179,66 @@ __global__ void __launch_bounds__(kPrepThreads) advance_prep_kernel(const TcAdva
                 qr[i] = __ldg(reinterpret_cast<const uint4 *>(qp + t * a.q_stride) + vc);
             }
         }
+        if (warp == 0) {                            // compensated running sums of g
+            float hi[2], lo[2], be[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = lane + 32 * i;
+                const size_t at = (tok0 + t) * a.H + h;
+                hi[i] = t < n ? a.g[at] : 0.f;
+                be[i] = t < n ? a.beta[at] : 0.f;
+                lo[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const float h2 = __shfl_up_sync(0xffffffffu, hi[i], off), l2 = __shfl_up_sync(0xffffffffu, lo[i], off);
+                    if (lane >= off) {
+                        const float s1 = hi[i] + h2, bp = s1 - hi[i];
+                        lo[i] += l2 + ((hi[i] - (s1 - bp)) + (h2 - bp));
+                        hi[i] = s1;
+                    }
+                }
+            {
+                const float ch = __shfl_sync(0xffffffffu, hi[0], 31), cl = __shfl_sync(0xffffffffu, lo[0], 31);
+                const float s1 = hi[1] + ch, bp = s1 - hi[1];
+                lo[1] += cl + ((hi[1] - (s1 - bp)) + (ch - bp));
+                hi[1] = s1;
+            }
+            const float eh = __shfl_sync(0xffffffffu, hi[1], 31), el = __shfl_sync(0xffffffffu, lo[1], 31);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = lane + 32 * i;
+                sGh[t] = hi[i];
+                sGl[t] = lo[i];
+                sGam[t] = __expf(hi[i] + lo[i]);
+                sEnd[t] = __expf((eh - hi[i]) + (el - lo[i]));
+                sBeta[t] = be[i];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int t = vr + i * ROWS;
-            uint8_t *at = smem + (vc >> 3) * 16384;
+            uint8_t *at = smem + (vc >> 3) * P::ATOM;
             *reinterpret_cast<uint4 *>(at + sw128(t, vc & 7)) = kr[i];
             *reinterpret_cast<uint4 *>(at + sw128(kC + t, vc & 7)) = qr[i];
-        }
-    }
-    if (warp == 0) {                                // compensated running sums of g
-        float hi[2], lo[2], be[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = lane + 32 * i;
-            const size_t at = (tok0 + t) * a.H + h;
-            hi[i] = t < n ? a.g[at] : 0.f;
-            be[i] = t < n ? a.beta[at] : 0.f;
-            lo[i] = 0.f;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float h2 = __shfl_up_sync(0xffffffffu, hi[i], off), l2 = __shfl_up_sync(0xffffffffu, lo[i], off);
-                if (lane >= off) {
-                    const float s1 = hi[i] + h2, bp = s1 - hi[i];
-                    lo[i] += l2 + ((hi[i] - (s1 - bp)) + (h2 - bp));
-                    hi[i] = s1;
-                }
-            }
-        }
-        {
-            const float ch = __shfl_sync(0xffffffffu, hi[0], 31), cl = __shfl_sync(0xffffffffu, lo[0], 31);
-            const float s1 = hi[1] + ch, bp = s1 - hi[1];
-            lo[1] += cl + ((hi[1] - (s1 - bp)) + (ch - bp));
-            hi[1] = s1;
-        }
-        const float eh = __shfl_sync(0xffffffffu, hi[1], 31), el = __shfl_sync(0xffffffffu, lo[1], 31);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = lane + 32 * i;
-            sGh[t] = hi[i];
-            sGl[t] = lo[i];
-            sGam[t] = __expf(hi[i] + lo[i]);
-            sEnd[t] = __expf((eh - hi[i]) + (el - lo[i]));
-            sBeta[t] = be[i];
         }
     }
     fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int half = warp >> 2;
     // ---- [K;Q] K^T
     if (warp == 0) {
         const uint64_t d = desc_sw128(saddr(smem));
         if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+                const uint32_t off = (ks >> 2) * P::ATOM + (ks & 3) * 32;
                 mma_bf16(tmem, desc_add(d, off), desc_add(d, off), idesc_mn(1, 128, kC), ks > 0);
             }
             mma_commit(&bar[0]);
@@ -200,135 +248,91 @@ __global__ void __launch_bounds__(kPrepThreads) advance_prep_kernel(const TcAdva
     bool ok = mbar_wait(&bar[0], 0);
     tc_fence_after();
     // ---- A in fp32 (rows of K), M as two bf16 terms (rows of Q)
-    const int t = tid & (kC - 1);
+    const int t = ((warp & 1) << 5) + lane;
+    const bool keys = (warp & 3) < 2;
     if (__all_sync(0xffffffffu, ok)) {
-        const float gh = sGh[t], gl = sGl[t], bt = sBeta[t];
+        const float gh = sGh[t], gl = sGl[t], f = keys ? sBeta[t] : a.scale;
+        uint32_t r[32];
+        tmem_ld32(tmem + lanes + 32 * half, r);
+        tmem_wait_ld();
+        float y[32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t r[32];
-            tmem_ld32(tmem + lanes + 32 * half, r);
-            tmem_wait_ld();
-            float y[32];
+        for (int j = 0; j < 32; ++j) {
+            const int s = 32 * half + j;
+            const float e = __expf((gh - sGh[s]) + (gl - sGl[s]));
+            y[j] = (keys ? s < t : s <= t) ? __uint_as_float(r[j]) * e * f : 0.f;
+        }
+        if (keys) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int s = 32 * half + j;
-                const float e = __expf((gh - sGh[s]) + (gl - sGl[s]));
-                y[j] = (warp < 2 ? s < t : s <= t) ? __uint_as_float(r[j]) * e * (warp < 2 ? bt : a.scale) : 0.f;
-            }
-            if (warp < 2) {
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4 *>(sA + t * P::LD + 32 * half + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+        } else {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<float4 *>(sA + t * P::LD + 32 * half + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-            } else {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint32_t hh[4], ll[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        __nv_bfloat16 h0, l0, h1, l1;
-                        split2(y[8 * v + 2 * i], h0, l0);
-                        split2(y[8 * v + 2 * i + 1], h1, l1);
-                        hh[i] = pack2(h0, h1);
-                        ll[i] = pack2(l0, l1);
-                    }
-                    const uint32_t at = sw128(t, 4 * half + v);
-                    *reinterpret_cast<uint4 *>(smem + P::OFF_M + at) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
-                    *reinterpret_cast<uint4 *>(smem + P::OFF_M + 8192 + at) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
-                }
+            for (int v = 0; v < 4; ++v) {
+                uint4 hh, ll;
+                split8(y + 8 * v, hh, ll);
+                const uint32_t at = P::OFF_M + sw128(t, 4 * half + v);
+                *reinterpret_cast<uint4 *>(smem + at) = hh;
+                *reinterpret_cast<uint4 *>(smem + P::ATOM + at) = ll;
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    // ---- T = (I + A)^-1: the diagonal blocks by substitution, a thread per column
+    // ---- T = (I + A)^-1: diagonal blocks of 8 by substitution, a thread per column; then blocks of twice the size
     if (tid < kC) {
-        const int bi = tid >> 4, j = tid & 15;
-        const float *Ab = sA + 16 * bi * P::LD + 16 * bi;
-        float x[16];
+        const int bi = tid >> 3, j = tid & 7;
+        const float *Ab = sA + 8 * bi * P::LD + 8 * bi;
+        float x[8];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < 8; ++r) {
+            const float4 y0 = *reinterpret_cast<const float4 *>(Ab + r * P::LD), y1 = *reinterpret_cast<const float4 *>(Ab + r * P::LD + 4);
+            const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int k = 0; k < r; k += 4) {
-                const float4 y = *reinterpret_cast<const float4 *>(Ab + r * P::LD + k);       // (A is 0 from the diagonal on)
-                s0 = fmaf(y.x, x[k], s0);
-                if (k + 1 < r) s1 = fmaf(y.y, x[k + 1], s1);
-                if (k + 2 < r) s0 = fmaf(y.z, x[k + 2], s0);
-                if (k + 3 < r) s1 = fmaf(y.w, x[k + 3], s1);
+            for (int k = 0; k < r; ++k) {
+                if (k & 1) s1 = fmaf(y[k], x[k], s1);
+                else s0 = fmaf(y[k], x[k], s0);
             }
             x[r] = r == j ? 1.f : r < j ? 0.f : -(s0 + s1);
-            sT[(16 * bi + r) * P::LD + 16 * bi + j] = x[r];
+            sT[(8 * bi + r) * P::LD + 8 * bi + j] = x[r];
         }
     }
     __syncthreads();
-    // ---- the blocks below: T_ij = -T_ii sum_k A_ik T_kj, the sum kept in the block (j, i) for the moment
-    for (int d = 1; d < 4; ++d) {
-        for (int task = tid; task < (4 - d) * 64; task += kPrepThreads) {
-            const int j = task >> 6, i = j + d, r = (task >> 2) & 15, c4 = (task & 3) * 4;
-            const float *Ar = sA + (16 * i + r) * P::LD, *Tc = sT + 16 * j + c4;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = 16 * j; k < 16 * i; ++k) {
-                const float y = Ar[k];
-                const float4 z = *reinterpret_cast<const float4 *>(Tc + k * P::LD);
-                s.x = fmaf(y, z.x, s.x); s.y = fmaf(y, z.y, s.y); s.z = fmaf(y, z.z, s.z); s.w = fmaf(y, z.w, s.w);
-            }
-            *reinterpret_cast<float4 *>(sT + (16 * j + r) * P::LD + 16 * i + c4) = s;
-        }
-        __syncthreads();
-        for (int task = tid; task < (4 - d) * 64; task += kPrepThreads) {
-            const int j = task >> 6, i = j + d, r = (task >> 2) & 15, c4 = (task & 3) * 4;
-            const float *Tr = sT + (16 * i + r) * P::LD + 16 * i, *X = sT + 16 * j * P::LD + 16 * i + c4;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float y = -Tr[k];
-                const float4 z = *reinterpret_cast<const float4 *>(X + k * P::LD);
-                s.x = fmaf(y, z.x, s.x); s.y = fmaf(y, z.y, s.y); s.z = fmaf(y, z.z, s.z); s.w = fmaf(y, z.w, s.w);
-            }
-            *reinterpret_cast<float4 *>(sT + (16 * i + r) * P::LD + 16 * j + c4) = s;
-        }
-        __syncthreads();
-    }
-    // ---- P = T diag(beta) and F = D P as two bf16 terms each: row t, half of its columns
+    inverse_level<8, P::LD>(sA, sT, tid);
+    inverse_level<16, P::LD>(sA, sT, tid);
+    inverse_level<32, P::LD>(sA, sT, tid);
+    // ---- P = T diag(beta) and F = D P as two bf16 terms each: a row's 16 columns, P over T and F over A
     {
-        const int s0 = (tid >> 6) * 32;
-        const float end = sEnd[t];
+        const int row = tid & (kC - 1), s0 = (tid >> 6) * 16;
+        const float end = sEnd[row];
+        float y[16], z[16];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            uint32_t ph[4], pl[4], fh[4], fl[4];
+        for (int j = 0; j < 16; ++j) {
+            y[j] = s0 + j <= row ? sT[row * P::LD + s0 + j] * sBeta[s0 + j] : 0.f;
+            z[j] = y[j] * end;
+        }
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int s = s0 + 8 * v + 2 * i + e;
-                    y[e] = s <= t ? sT[t * P::LD + s] * sBeta[s] : 0.f;
-                }
-                __nv_bfloat16 h0, l0, h1, l1;
-                split2(y[0], h0, l0);
-                split2(y[1], h1, l1);
-                ph[i] = pack2(h0, h1);
-                pl[i] = pack2(l0, l1);
-                split2(y[0] * end, h0, l0);
-                split2(y[1] * end, h1, l1);
-                fh[i] = pack2(h0, h1);
-                fl[i] = pack2(l0, l1);
-            }
-            const uint32_t at = sw128(t, (s0 >> 3) + v);
-            *reinterpret_cast<uint4 *>(smem + P::OFF_P + at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-            *reinterpret_cast<uint4 *>(smem + P::OFF_P + 8192 + at) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-            *reinterpret_cast<uint4 *>(smem + P::OFF_F + at) = make_uint4(fh[0], fh[1], fh[2], fh[3]);
-            *reinterpret_cast<uint4 *>(smem + P::OFF_F + 8192 + at) = make_uint4(fl[0], fl[1], fl[2], fl[3]);
+        for (int v = 0; v < 2; ++v) {
+            uint4 hh, ll;
+            const uint32_t at = sw128(row, (s0 >> 3) + v);
+            split8(y + 8 * v, hh, ll);
+            *reinterpret_cast<uint4 *>(smem + P::OFF_T + at) = hh;
+            *reinterpret_cast<uint4 *>(smem + P::OFF_T + 8192 + at) = ll;
+            split8(z + 8 * v, hh, ll);
+            *reinterpret_cast<uint4 *>(smem + P::OFF_A + at) = hh;
+            *reinterpret_cast<uint4 *>(smem + P::OFF_A + 8192 + at) = ll;
         }
     }
     fence_proxy_async();
     __syncthreads();
-    // ---- E = K^T F (rows dk: the keys read MN-major) and M P (lanes 64..127: M begins 64 rows into its operand)
+    // ---- E = K^T F (rows dk: the keys read MN-major) and, over [K;Q] K^T, M P (lanes 64..127: M's rows follow the keys' in each
+    //      atom; where dk is 64 the rows before M's second term are no data, and lanes 0..63 are not read)
     if (warp == 0) {
         tc_fence_after();
-        const uint64_t dk = desc_mn_sw128(saddr(smem), 16384), df = desc_mn_sw128(saddr(smem) + P::OFF_F, 8192);
-        const uint64_t dp = desc_mn_sw128(saddr(smem) + P::OFF_P, 8192), dm = desc_sw128(saddr(smem) + P::OFF_M - 8192);
+        const uint64_t dk = desc_mn_sw128(saddr(smem), P::ATOM), df = desc_mn_sw128(saddr(smem) + P::OFF_A, 8192);
+        const uint64_t dp = desc_mn_sw128(saddr(smem) + P::OFF_T, 8192), dm = desc_sw128(saddr(smem));
         constexpr uint32_t idE = idesc_mn(1, 128, kC) | kIdescMnMajorA | kIdescMnMajorB, idM = idesc_mn(1, 128, kC) | kIdescMnMajorB;
         if (elect_one() && ok) {
 #pragma unroll
@@ -338,9 +342,9 @@ __global__ void __launch_bounds__(kPrepThreads) advance_prep_kernel(const TcAdva
             }
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                mma_bf16(tmem + 128, desc_add(dm, ks * 32), desc_add(dp, ks * 2048), idM, ks > 0);
-                mma_bf16(tmem + 128, desc_add(dm, ks * 32), desc_add(dp, 8192 + ks * 2048), idM, 1);
-                mma_bf16(tmem + 128, desc_add(dm, 8192 + ks * 32), desc_add(dp, ks * 2048), idM, 1);
+                mma_bf16(tmem, desc_add(dm, ks * 32), desc_add(dp, ks * 2048), idM, ks > 0);
+                mma_bf16(tmem, desc_add(dm, ks * 32), desc_add(dp, 8192 + ks * 2048), idM, 1);
+                mma_bf16(tmem, desc_add(dm, P::ATOM + ks * 32), desc_add(dp, ks * 2048), idM, 1);
             }
             mma_commit(&bar[1]);
         }
@@ -348,19 +352,27 @@ __global__ void __launch_bounds__(kPrepThreads) advance_prep_kernel(const TcAdva
     }
     ok = ok && mbar_wait(&bar[1], 0);
     tc_fence_after();
+    // ---- the terms of both into shared memory as the walk wants them, and out in two copies
     char *unit = a.ws + ((static_cast<size_t>(blockIdx.z) * ta.chunks + c) * a.H + h) * Unit<DK>::BYTES;
     if (__all_sync(0xffffffffu, ok)) {
-        if (warp * 32 < DK) spill_row(tmem + lanes + 64, unit, unit + Unit<DK>::E_BYTES, tid);
-        if (warp >= 2)
-            spill_row(tmem + lanes + 128, unit + 2 * Unit<DK>::E_BYTES, unit + 2 * Unit<DK>::E_BYTES + Unit<DK>::MP_BYTES, t);
+        if ((warp & 3) * 32 < DK)
+            stage_row(tmem + lanes + 64 + 32 * half, smem, smem + Unit<DK>::E_BYTES, (warp & 3) * 32 + lane, half);
+        if (!keys)
+            stage_row(tmem + lanes + 32 * half, smem + P::OFF_A, smem + P::OFF_A + Unit<DK>::MP_BYTES, t, half);
         if (tid < kC) reinterpret_cast<float *>(unit + Unit<DK>::TILES)[tid] = sGam[tid];
     } else if (lane == 0) {                         // (nothing more was issued unless the second wait ran out: one more bounded wait)
         atomicOr(a.status, kStatusTimeout);
         if (!mbar_wait(&bar[1], 0)) atomicOr(a.status, GDN_STATUS_DRAIN);
     }
+    fence_proxy_async();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 256);
+    if (tid == 0) {
+        bulk_store(unit, smem, 2 * Unit<DK>::E_BYTES);
+        bulk_store(unit + 2 * Unit<DK>::E_BYTES, smem + P::OFF_A, 2 * Unit<DK>::MP_BYTES);
+        bulk_store_wait();
+    }
+    if (warp == 1) tmem_dealloc(tmem, 128);
 }
 
 // ------------------------------------------------------------- the walk over the chunks
@@ -369,41 +381,34 @@ template <int DK, int NS> struct ScanPlan {
     static constexpr int S_BYTES = DK * 128, X_BYTES = kC * 128;      // rows of 32 first terms, 32 second ones
     static constexpr int OFF_S = STAGES * STAGE, OFF_X = OFF_S + NS * S_BYTES, OFF_BAR = OFF_X + NS * X_BYTES;
     static constexpr int BYTES = OFF_BAR + 256;
-    static constexpr int ROWS = NS * 128, LOAD_WARP = ROWS / 32, MMA_WARP = LOAD_WARP + 1, THREADS = ROWS + 32 + NS * 32;
+    static constexpr int ROWS = NS * 256, LOAD_WARP = ROWS / 32, MMA_WARP = LOAD_WARP + 1, THREADS = ROWS + 32 + NS * 32;
     static constexpr int TCOLS = 192, TMEM_COLS = NS == 1 ? 256 : 512;         // of a slice: [K;Q] S^T, E x, M P x, 64 columns each
     static_assert(NS * TCOLS <= TMEM_COLS && BYTES <= 227 * 1024 && STAGE % 1024 == 0, "plan");
 };
 
-// 32 numbers as two bf16 terms in row `row` of a tile of 128-byte rows: first terms, then second ones.
-__device__ __forceinline__ void put_row(uint8_t *tile, int row, const float (&y)[32]) {
+// A thread's 16 numbers as two bf16 terms in row `row` of a tile of 128-byte rows: 32 first terms, then 32 second ones.
+__device__ __forceinline__ void put_row(uint8_t *tile, int row, int half, const float (&y)[16]) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __nv_bfloat16 h0, l0, h1, l1;
-            split2(y[8 * c + 2 * i], h0, l0);
-            split2(y[8 * c + 2 * i + 1], h1, l1);
-            h[i] = pack2(h0, h1);
-            l[i] = pack2(l0, l1);
-        }
-        *reinterpret_cast<uint4 *>(tile + sw128(row, c)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(tile + sw128(row, c + 4)) = make_uint4(l[0], l[1], l[2], l[3]);
+    for (int c = 0; c < 2; ++c) {
+        uint4 h, l;
+        split8(y + 8 * c, h, l);
+        *reinterpret_cast<uint4 *>(tile + sw128(row, 2 * half + c)) = h;
+        *reinterpret_cast<uint4 *>(tile + sw128(row, 2 * half + c + 4)) = l;
     }
 }
-// The product's 32 columns: those with the first terms and those with the second ones added.
-__device__ __forceinline__ void get_row(uint32_t tcol, float (&y)[32]) {
-    uint32_t r[32], s[32];
-    tmem_ld32(tcol, r);
-    tmem_ld32(tcol + 32, s);
+// The product's 16 columns: those with the first terms and those with the second ones added.
+__device__ __forceinline__ void get_row(uint32_t tcol, float (&y)[16]) {
+    uint32_t r[16], s[16];
+    tmem_load16(tcol, r);
+    tmem_load16(tcol + 32, s);
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]) + __uint_as_float(s[j]);
+    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(r[j]) + __uint_as_float(s[j]);
 }
 
-// One CTA per (NS slices of value columns, head, sequence).  A slice has four row warps and an MMA warp; one warp loads for
-// all.  Row r of a slice's warps has token r (K's products, r < 64), token r - 64 (Q's) and key dimension r of
-// the state.  Everything that a buffer's next use overwrites has been read by then: see each arrival.
+// One CTA per (NS slices of value columns, head, sequence).  A slice has eight row warps and an MMA warp; one warp loads for
+// all.  Row r of a slice has token r (K's products, r < 64), token r - 64 (Q's) and key dimension r of the state, 16
+// columns in each of two warps (one per row: 800 cycles for x and as many for S instead of half).  Everything that a buffer's next use overwrites has been read by then: see each arrival.
 template <int DK, int NS>
 __global__ void __launch_bounds__(ScanPlan<DK, NS>::THREADS, 1)
 advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
@@ -458,8 +463,8 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             mbar_init(&d1[i], 1);
             mbar_init(&d2[i], 1);
             mbar_init(&d3[i], 1);
-            mbar_init(&s_ready[i], 128);
-            mbar_init(&x_ready[i], 128);
+            mbar_init(&s_ready[i], 256);
+            mbar_init(&x_ready[i], 256);
             mbar_init(&drain[i], 1);
         }
         *abort = expire;
@@ -553,20 +558,20 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
     } else {
         // ------------------------------------------------------ rows
-        const int sl = warp >> 2, row = tid & 127, t = row & (kC - 1);
+        const int sl = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, t = row & (kC - 1);
         const bool keys = row < kC;                 // (the same in a warp, as the next)
         const bool has = row < DK;
-        const uint32_t tm = tmem + sl * P::TCOLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t tm = tmem + sl * P::TCOLS + 16 * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         uint8_t *sS = smem + P::OFF_S + sl * P::S_BYTES, *sX = smem + P::OFF_X + sl * P::X_BYTES;
-        const int col0 = dv0 + sl * kSlice;
+        const int col0 = dv0 + sl * kSlice + 16 * half;
         float *st = a.state + ((static_cast<size_t>(sq.slot) * a.H + h) * ta.dv + col0) * DK + row;
-        float S[32];
+        float S[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[j] = has && !zero ? st[j * DK] : 0.f;
+        for (int j = 0; j < 16; ++j) S[j] = has && !zero ? st[j * DK] : 0.f;
         const size_t tok0 = static_cast<size_t>(b) * a.T + ta.c0 * kC + t;
         const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v) + tok0 * a.v_stride + h * ta.dv + col0;
         float *op = a.out + (tok0 * a.H + h) * ta.dv + col0;
-        uint4 v[4];
+        uint4 v[2];
         float gam = 0.f, gend = 0.f;
         auto fetch = [&](int c) {
             const float *gp = reinterpret_cast<const float *>(units + c * ustep + Unit<DK>::TILES);
@@ -574,18 +579,18 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             gend = __ldcg(gp + kC - 1);
             if (keys) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 2; ++i)
                     v[i] = c * kC + t < n ? __ldg(reinterpret_cast<const uint4 *>(vp + static_cast<size_t>(c) * kC * a.v_stride) + i)
                                           : make_uint4(0u, 0u, 0u, 0u);
             }
         };
         fetch(0);
-        if (has) put_row(sS, row, S);
+        if (has) put_row(sS, row, half, S);
         fence_proxy_async();
         mbar_arrive(&s_ready[sl]);
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
-            float y[32], o[32];
+            float y[16], o[16];
             ok = wait(&d1[sl], c & 1);
             if (!ok) break;
             tc_fence_after();
@@ -593,18 +598,18 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (keys) {                             // x = v - gamma S k; nothing of rows past the last token
                 const bool live = c * kC + t < n;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     float f[8];
                     bf16x8_to_f32(v[i], f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[8 * i + e] = live ? fmaf(-gam, y[8 * i + e], f[e]) : 0.f;
                 }
-                put_row(sX, t, y);
+                put_row(sX, t, half, y);
                 fence_proxy_async();
             } else {
                 const float f = gam * a.scale;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = f * y[j];
+                for (int j = 0; j < 16; ++j) o[j] = f * y[j];
             }
             const float ge = gend;
             tc_fence_before();
@@ -616,8 +621,8 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (has) {
                 get_row(tm + 64, y);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) S[j] = fmaf(ge, S[j], y[j]);
-                put_row(sS, row, S);
+                for (int j = 0; j < 16; ++j) S[j] = fmaf(ge, S[j], y[j]);
+                put_row(sS, row, half, S);
                 fence_proxy_async();
             }
             tc_fence_before();
@@ -630,7 +635,7 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (c * kC + t < n) {
                     float4 *dst = reinterpret_cast<float4 *>(op + static_cast<size_t>(c) * kC * a.H * ta.dv);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < 4; ++j)
                         dst[j] = make_float4(o[4 * j] + y[4 * j], o[4 * j + 1] + y[4 * j + 1], o[4 * j + 2] + y[4 * j + 2],
                                              o[4 * j + 3] + y[4 * j + 3]);
                 }
@@ -638,7 +643,7 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
         if (ok && has)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) st[j * DK] = S[j];
+            for (int j = 0; j < 16; ++j) st[j * DK] = S[j];
         tc_fence_before();
     }
     __syncthreads();
