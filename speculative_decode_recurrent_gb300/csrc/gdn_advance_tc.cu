@@ -381,9 +381,9 @@ template <int DK, int NS> struct ScanPlan {
     static constexpr int S_BYTES = DK * 128, X_BYTES = kC * 128;      // rows of 32 first terms, 32 second ones
     static constexpr int OFF_S = STAGES * STAGE, OFF_X = OFF_S + NS * S_BYTES, OFF_BAR = OFF_X + NS * X_BYTES;
     static constexpr int BYTES = OFF_BAR + 256;
-    static constexpr int ROWS = NS * 256, LOAD_WARP = ROWS / 32, MMA_WARP = LOAD_WARP + 1, THREADS = ROWS + 32 + NS * 32;
-    static constexpr int TCOLS = 192, TMEM_COLS = NS == 1 ? 256 : 512;         // of a slice: [K;Q] S^T, E x, M P x, 64 columns each
-    static_assert(NS * TCOLS <= TMEM_COLS && BYTES <= 227 * 1024 && STAGE % 1024 == 0, "plan");
+    static constexpr int ROWS = NS * 256, LOAD_WARP = ROWS / 32, MMA_WARP = LOAD_WARP + 1, THREADS = ROWS + 64;
+    static constexpr int N = NS * 64, TMEM_COLS = NS == 1 ? 256 : 512;         // columns of a product; [K;Q] S^T, E x, M P x
+    static_assert(3 * N <= TMEM_COLS && BYTES <= 227 * 1024 && STAGE % 1024 == 0, "plan");
 };
 
 // A thread's 16 numbers as two bf16 terms in row `row` of a tile of 128-byte rows: 32 first terms, then 32 second ones.
@@ -406,8 +406,9 @@ __device__ __forceinline__ void get_row(uint32_t tcol, float (&y)[16]) {
     for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(r[j]) + __uint_as_float(s[j]);
 }
 
-// One CTA per (NS slices of value columns, head, sequence).  A slice has eight row warps and an MMA warp; one warp loads for
-// all.  Row r of a slice has token r (K's products, r < 64), token r - 64 (Q's) and key dimension r of the state, 16
+// One CTA per (NS slices of value columns, head, sequence).  A slice has eight row warps; one warp loads and one issues
+// the products of all slices together (a product's rows are read once for them: an MMA of 64 columns takes 50 cycles
+// for its 128 rows of 32 bytes, one of 128 columns 67).  Row r of a slice has token r (K's products, r < 64), token r - 64 (Q's) and key dimension r of the state, 16
 // columns in each of two warps (one per row: 800 cycles for x and as many for S instead of half).  Everything that a buffer's next use overwrites has been read by then: see each arrival.
 template <int DK, int NS>
 __global__ void __launch_bounds__(ScanPlan<DK, NS>::THREADS, 1)
@@ -418,11 +419,10 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const AdvanceArgs &a = ta.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int h = blockIdx.y, b = ta.b0 + blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty = full + 2, *d1 = empty + 2, *d2 = d1 + NS,
-             *d3 = d2 + NS, *s_ready = d3 + NS, *x_ready = s_ready + NS, *drain = x_ready + NS;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + NS);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty = full + 2, *d1 = empty + 2, *d2 = d1 + 1,
+             *d3 = d2 + 1, *s_ready = d3 + 1, *x_ready = s_ready + 1, *drain = x_ready + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((4 + 6 * NS) * 8 + 8 <= 256, "barriers");
     pdl_wait();
     pdl_release();
     const AdvanceSeq sq = advance_seq(a, b);
@@ -457,16 +457,14 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const bool expire = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], NS);
+            mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&d1[i], 1);
-            mbar_init(&d2[i], 1);
-            mbar_init(&d3[i], 1);
-            mbar_init(&s_ready[i], 256);
-            mbar_init(&x_ready[i], 256);
-            mbar_init(&drain[i], 1);
-        }
+        mbar_init(d1, 1);
+        mbar_init(d2, 1);
+        mbar_init(d3, 1);
+        mbar_init(s_ready, P::ROWS / 32);           // a warp arrives once: 256 arrivals at one word take 500 cycles
+        mbar_init(x_ready, P::ROWS / 32);
+        mbar_init(drain, 1);
         *abort = expire;
         if (expire) atomicOr(a.status, kStatusTimeout);
         fence_mbar_init();
@@ -512,19 +510,17 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int i = max(0, c - 2); i < c; ++i)
                 if (!mbar_wait(&full[i & 1], (i >> 1) & 1) && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
         }
-    } else if (warp >= P::MMA_WARP) {
+    } else if (warp == P::MMA_WARP) {
         // ------------------------------------------------------ MMAs
-        const int sl = warp - P::MMA_WARP;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + sl * P::TCOLS;
-        const uint64_t dS = desc_mn_sw128(saddr(smem) + P::OFF_S + sl * P::S_BYTES, 8192);
-        const uint64_t dX = desc_mn_sw128(saddr(smem) + P::OFF_X + sl * P::X_BYTES, 8192);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dS = desc_mn_sw128(saddr(smem) + P::OFF_S, P::S_BYTES), dX = desc_mn_sw128(saddr(smem) + P::OFF_X, P::X_BYTES);
         const uint64_t dA = desc_sw128(saddr(smem));
-        constexpr uint32_t id = idesc_mn(1, 128, 64) | kIdescMnMajorB;
+        constexpr uint32_t id = idesc_mn(1, 128, P::N) | kIdescMnMajorB;
         bool ok = true;
         int c = 0;
         for (; c < chunks; ++c) {
             const int st = c & 1;
-            ok = wait(&full[st], (c >> 1) & 1) && wait(&s_ready[sl], c & 1);
+            ok = wait(&full[st], (c >> 1) & 1) && wait(s_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kq = desc_add(dA, st * P::STAGE), e = desc_add(kq, P::KQ), mp = desc_add(e, 2 * Unit<DK>::E_BYTES - 8192);
@@ -532,36 +528,36 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks)
                     mma_bf16(tm, desc_add(kq, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dS, ks * 2048), id, ks > 0);
-                mma_commit(&d1[sl]);
+                mma_commit(d1);
             }
             __syncwarp();
-            ok = wait(&x_ready[sl], c & 1);
+            ok = wait(x_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)      // the first terms of E, then the second ones
-                    mma_bf16(tm + 64, desc_add(e, (ks >> 2) * Unit<DK>::E_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
-                mma_commit(&d2[sl]);
+                    mma_bf16(tm + P::N, desc_add(e, (ks >> 2) * Unit<DK>::E_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
+                mma_commit(d2);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    mma_bf16(tm + 128, desc_add(mp, (ks >> 2) * Unit<DK>::MP_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
-                mma_commit(&d3[sl]);
+                    mma_bf16(tm + 2 * P::N, desc_add(mp, (ks >> 2) * Unit<DK>::MP_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
+                mma_commit(d3);
                 mma_commit(&empty[st]);
             }
             __syncwarp();
         }
         if (!ok && c > 0) {                         // MMAs in flight end before their memory is given back
-            if (elect_one()) mma_commit(&drain[sl]);
+            if (elect_one()) mma_commit(drain);
             __syncwarp();
-            if (!mbar_wait(&drain[sl], 0) && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
+            if (!mbar_wait(drain, 0) && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
         }
     } else {
         // ------------------------------------------------------ rows
         const int sl = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, t = row & (kC - 1);
         const bool keys = row < kC;                 // (the same in a warp, as the next)
         const bool has = row < DK;
-        const uint32_t tm = tmem + sl * P::TCOLS + 16 * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t tm = tmem + sl * 64 + 16 * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         uint8_t *sS = smem + P::OFF_S + sl * P::S_BYTES, *sX = smem + P::OFF_X + sl * P::X_BYTES;
         const int col0 = dv0 + sl * kSlice + 16 * half;
         float *st = a.state + ((static_cast<size_t>(sq.slot) * a.H + h) * ta.dv + col0) * DK + row;
@@ -573,6 +569,10 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         float *op = a.out + (tok0 * a.H + h) * ta.dv + col0;
         uint4 v[2];
         float gam = 0.f, gend = 0.f;
+        auto arrive = [&](uint64_t *bar) {          // for the warp, behind each lane's fences
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
         auto fetch = [&](int c) {
             const float *gp = reinterpret_cast<const float *>(units + c * ustep + Unit<DK>::TILES);
             gam = __ldcg(gp + t);
@@ -587,11 +587,11 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         fetch(0);
         if (has) put_row(sS, row, half, S);
         fence_proxy_async();
-        mbar_arrive(&s_ready[sl]);
+        arrive(s_ready);
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
             float y[16], o[16];
-            ok = wait(&d1[sl], c & 1);
+            ok = wait(d1, c & 1);
             if (!ok) break;
             tc_fence_after();
             get_row(tm, y);
@@ -613,25 +613,25 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             const float ge = gend;
             tc_fence_before();
-            mbar_arrive(&x_ready[sl]);              // this row has read [K;Q] S^T (and, before it, the last M P x)
+            arrive(x_ready);                        // this row has read [K;Q] S^T (and, before it, the last M P x)
             if (c + 1 < chunks) fetch(c + 1);
-            ok = wait(&d2[sl], c & 1);
+            ok = wait(d2, c & 1);
             if (!ok) break;
             tc_fence_after();
             if (has) {
-                get_row(tm + 64, y);
+                get_row(tm + P::N, y);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) S[j] = fmaf(ge, S[j], y[j]);
                 put_row(sS, row, half, S);
                 fence_proxy_async();
             }
             tc_fence_before();
-            mbar_arrive(&s_ready[sl]);              // this row has read E x; S is in place
+            arrive(s_ready);                        // this row has read E x; S is in place
             if (!keys) {
-                ok = wait(&d3[sl], c & 1);
+                ok = wait(d3, c & 1);
                 if (!ok) break;
                 tc_fence_after();
-                get_row(tm + 128, y);
+                get_row(tm + 2 * P::N, y);
                 if (c * kC + t < n) {
                     float4 *dst = reinterpret_cast<float4 *>(op + static_cast<size_t>(c) * kC * a.H * ta.dv);
 #pragma unroll
