@@ -30,6 +30,7 @@ using namespace tc;
 
 constexpr int kC = 64;                              // tokens of a chunk
 constexpr int kSlice = 32;                          // value columns of a slice
+constexpr float kLog2e = 1.4426950408889634f;
 
 // What the first kernel leaves of a chunk of a head, as the second one's operands lie in shared memory:
 // E as [dk][64 tokens] bf16 rows of 128 bytes (swizzled), first and second terms; M P as [64][64] likewise; gamma.
@@ -256,12 +257,18 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
         tmem_ld32(tmem + lanes + 32 * half, r);
         tmem_wait_ld();
         float y[32];
+        const int seen = t - 32 * half + (keys ? 0 : 1);          // columns j < seen count
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const int s = 32 * half + j;
-            const float e = __expf((gh - sGh[s]) + (gl - sGl[s]));
-            y[j] = (keys ? s < t : s <= t) ? __uint_as_float(r[j]) * e * f : 0.f;
+        for (int j = 0; j < 32; j += 4) {
+            const float4 h4 = *reinterpret_cast<const float4 *>(sGh + 32 * half + j), l4 = *reinterpret_cast<const float4 *>(sGl + 32 * half + j);
+            y[j] = ex2(((gh - h4.x) + (gl - l4.x)) * kLog2e);
+            y[j + 1] = ex2(((gh - h4.y) + (gl - l4.y)) * kLog2e);
+            y[j + 2] = ex2(((gh - h4.z) + (gl - l4.z)) * kLog2e);
+            y[j + 3] = ex2(((gh - h4.w) + (gl - l4.w)) * kLog2e);
         }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)                              // (as bits: a select here became 32 branches)
+            y[j] = __uint_as_float(__float_as_uint(__uint_as_float(r[j]) * y[j] * f) & (j < seen ? 0xffffffffu : 0u));
         if (keys) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
@@ -308,8 +315,16 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
         const float end = sEnd[row];
         float y[16], z[16];
 #pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            const float4 x4 = *reinterpret_cast<const float4 *>(sT + row * P::LD + s0 + j), b4 = *reinterpret_cast<const float4 *>(sBeta + s0 + j);
+            y[j] = x4.x * b4.x;
+            y[j + 1] = x4.y * b4.y;
+            y[j + 2] = x4.z * b4.z;
+            y[j + 3] = x4.w * b4.w;
+        }
+#pragma unroll
         for (int j = 0; j < 16; ++j) {
-            y[j] = s0 + j <= row ? sT[row * P::LD + s0 + j] * sBeta[s0 + j] : 0.f;
+            y[j] = __uint_as_float(__float_as_uint(y[j]) & (s0 + j <= row ? 0xffffffffu : 0u));
             z[j] = y[j] * end;
         }
         __syncthreads();
@@ -419,8 +434,8 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const AdvanceArgs &a = ta.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int h = blockIdx.y, b = ta.b0 + blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty = full + 2, *d1 = empty + 2, *d2 = d1 + 1,
-             *d3 = d2 + 1, *s_ready = d3 + 1, *x_ready = s_ready + 1, *drain = x_ready + 1;
+    uint64_t *full_k = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty_k = full_k + 2, *full_e = empty_k + 2,
+             *empty_e = full_e + 2, *d1 = empty_e + 2, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1, *x_ready = s_ready + 1, *drain = x_ready + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     pdl_wait();
@@ -456,8 +471,10 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     if (tid == 0) {
         const bool expire = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&full_k[i], 1);
+            mbar_init(&empty_k[i], 1);
+            mbar_init(&full_e[i], 1);
+            mbar_init(&empty_e[i], 1);
         }
         mbar_init(d1, 1);
         mbar_init(d2, 1);
@@ -475,7 +492,9 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {         // the same answer in a whole warp
-        bool ok = !*abort && mbar_wait(bar, parity);
+        bool ok = false;
+        for (uint32_t i = 0; i < kWaitLimit && !(ok = mbar_try_wait(bar, parity)); ++i)
+            if (*abort) break;
         ok = __all_sync(0xffffffffu, ok) != 0;
         if (!ok && lane == 0 && !*abort) {
             *abort = 1;
@@ -487,28 +506,39 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const size_t ustep = static_cast<size_t>(a.H) * Unit<DK>::BYTES;
     if (warp == P::LOAD_WARP) {
         // ------------------------------------------------------ loads
+        // Keys and queries go when the first product of two chunks before is done, E and M P after its last: with one
+        // barrier for both, a chunk's 80 KB came no sooner than it was needed (3000 cycles a chunk instead of 2400).
         const int hk = h / (a.H / a.Hk);
-        int c = 0;
+        int c = 0, half = 0;
         for (; c < chunks; ++c) {
-            const int st = c & 1;
-            if (c >= 2 && !wait(&empty[st], ((c >> 1) - 1) & 1)) break;
-            if (*abort) break;
+            const int st = c & 1, before = ((c >> 1) - 1) & 1;
+            uint8_t *dst = smem + st * P::STAGE;
+            half = 0;
+            if (*abort || (c >= 2 && !wait(&empty_k[st], before))) break;
             if (elect_one()) {
-                uint8_t *dst = smem + st * P::STAGE;
                 const int tok = b * a.T + (ta.c0 + c) * kC;           // (B T <= 2^28)
-                mbar_expect_tx(&full[st], P::STAGE);
+                mbar_expect_tx(&full_k[st], P::KQ);
 #pragma unroll
                 for (int at = 0; at < DK / 64; ++at) {
-                    tma_load_3d(dst + at * 16384, &tm_k, at * 64, hk, tok, &full[st]);
-                    tma_load_3d(dst + at * 16384 + 8192, &tm_q, at * 64, hk, tok, &full[st]);
+                    tma_load_3d(dst + at * 16384, &tm_k, at * 64, hk, tok, &full_k[st]);
+                    tma_load_3d(dst + at * 16384 + 8192, &tm_q, at * 64, hk, tok, &full_k[st]);
                 }
-                bulk_load(dst + P::KQ, units + c * ustep, Unit<DK>::TILES, &full[st]);
+            }
+            __syncwarp();
+            half = 1;
+            if (c >= 2 && !wait(&empty_e[st], before)) break;
+            if (elect_one()) {
+                mbar_expect_tx(&full_e[st], Unit<DK>::TILES);
+                bulk_load(dst + P::KQ, units + c * ustep, Unit<DK>::TILES, &full_e[st]);
             }
             __syncwarp();
         }
         if (*abort) {                               // copies in flight end before the CTA does
-            for (int i = max(0, c - 2); i < c; ++i)
-                if (!mbar_wait(&full[i & 1], (i >> 1) & 1) && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
+            bool done = true;
+            const int keys = c < chunks ? c + half : c;               // chunks whose keys, and whose E, have been requested
+            for (int i = max(0, keys - 2); i < keys; ++i) done = done && mbar_wait(&full_k[i & 1], (i >> 1) & 1);
+            for (int i = max(0, c - 2); i < c; ++i) done = done && mbar_wait(&full_e[i & 1], (i >> 1) & 1);
+            if (!done && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
         }
     } else if (warp == P::MMA_WARP) {
         // ------------------------------------------------------ MMAs
@@ -520,7 +550,7 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         int c = 0;
         for (; c < chunks; ++c) {
             const int st = c & 1;
-            ok = wait(&full[st], (c >> 1) & 1) && wait(s_ready, c & 1);
+            ok = wait(&full_k[st], (c >> 1) & 1) && wait(s_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kq = desc_add(dA, st * P::STAGE), e = desc_add(kq, P::KQ), mp = desc_add(e, 2 * Unit<DK>::E_BYTES - 8192);
@@ -529,9 +559,10 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 for (int ks = 0; ks < DK / 16; ++ks)
                     mma_bf16(tm, desc_add(kq, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dS, ks * 2048), id, ks > 0);
                 mma_commit(d1);
+                mma_commit(&empty_k[st]);
             }
             __syncwarp();
-            ok = wait(x_ready, c & 1);
+            ok = wait(&full_e[st], (c >> 1) & 1) && wait(x_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -543,7 +574,7 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 for (int ks = 0; ks < 8; ++ks)
                     mma_bf16(tm + 2 * P::N, desc_add(mp, (ks >> 2) * Unit<DK>::MP_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
                 mma_commit(d3);
-                mma_commit(&empty[st]);
+                mma_commit(&empty_e[st]);
             }
             __syncwarp();
         }
