@@ -277,3 +277,18 @@ def test_conv_advance_bad_sequences_are_skipped():
     torch.cuda.synchronize()
     assert int(layer.status.item()) == lib.STATUS_BAD_SLOT | lib.STATUS_BAD_LEN
     assert (y == 7).all() and (layer.t["ring"] == 1).all() and layer.t["pos"].tolist() == [1, 9, 2]
+
+
+def test_advance_expired_wait_writes_nothing():
+    """The tensor-core kernels' exit at their first bounded wait, with nothing issued; the layer is sound afterwards."""
+    import speculative_decode_recurrent_gb300 as lib
+    c = Case([150, 90], 150, 2, 2, 128, 128, BF, seed=18)
+    c.layer.d.flags = lib.FLAG_TEST_EXPIRE
+    c.run()
+    torch.cuda.synchronize()
+    assert int(c.layer.status.item()) == lib.STATUS_TIMEOUT
+    assert torch.equal(c.layer.t["state"].cpu(), c.state)
+    c.layer.status.zero_()
+    c.layer.d.flags = 0
+    c.run()
+    c.check(True)
