@@ -15,7 +15,7 @@
 //
 // What bounds it: a few rows of V numbers per sequence, and a chain of dependent steps (tokens, their probabilities,
 // the walk, the pass, its sum across the cluster, the search).  A cluster of eight CTAs takes a sequence, each a
-// stretch of the vocabulary, in segments of 1024 terms per warp (eight 16-byte loads of each row in flight per lane).
+// stretch of the vocabulary, in segments of 1024 terms per warp (four 16-byte loads of each row in flight per lane, two CTAs on an SM).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -94,24 +94,28 @@ __device__ __forceinline__ void load4(const float *row, int v, int V, float (&x)
     }
 }
 
-// The sum of the segment at v0, in every lane.
+// The sum of the segment at v0, in every lane.  Half of it at a time: with 64 registers two CTAs share an SM.
 template <bool VEC>
 __device__ __forceinline__ double segment_sum(const Rest &r, int v0, int V, int lane) {
-    float p[kSeg / 128][4], q[kSeg / 128][4];
-#pragma unroll
-    for (int i = 0; i < kSeg / 128; ++i) load4<VEC>(r.p, v0 + i * 128 + lane * 4, V, p[i]);
-    if (r.q)
-#pragma unroll
-        for (int i = 0; i < kSeg / 128; ++i) load4<VEC>(r.q, v0 + i * 128 + lane * 4, V, q[i]);
+    constexpr int ROWS = kSeg / 256;                // rows of 128 terms in half a segment
     Sum2 s{0.f, 0.f};
+#pragma unroll 1
+    for (int at = v0; at < v0 + kSeg; at += kSeg / 2) {
+        float p[ROWS][4], q[ROWS][4];
 #pragma unroll
-    for (int i = 0; i < kSeg / 128; ++i)
+        for (int i = 0; i < ROWS; ++i) load4<VEC>(r.p, at + i * 128 + lane * 4, V, p[i]);
+        if (r.q)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float h, l;
-            r.term(v0 + i * 128 + lane * 4 + j, p[i][j], r.q ? q[i][j] : 0.f, h, l);
-            s.add(h, l);
-        }
+            for (int i = 0; i < ROWS; ++i) load4<VEC>(r.q, at + i * 128 + lane * 4, V, q[i]);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float h, l;
+                r.term(at + i * 128 + lane * 4 + j, p[i][j], r.q ? q[i][j] : 0.f, h, l);
+                s.add(h, l);
+            }
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         const float h = __shfl_xor_sync(0xffffffffu, s.hi, off), l = __shfl_xor_sync(0xffffffffu, s.lo, off);
@@ -121,44 +125,86 @@ __device__ __forceinline__ double segment_sum(const Rest &r, int v0, int V, int 
 }
 
 // The first term of the segment at v0 at which the running sum passes `target`; the last term above 0 where none does (the
-// segment's sum was taken in another order), -1 where there is none.
+// segment's sum was taken in another order), -1 where there is none.  The sums of the segment's eight rows of 128 terms
+// in two words first, so that the chain of 64-bit additions is one row's: 8 for the rows, 5 across the lanes, 4 in a lane.
 template <bool VEC>
 __device__ __forceinline__ int segment_find(const Rest &r, int v0, int V, int lane, double target) {
-    double before = 0.0;
-    int last = -1;
-    for (int i = 0; i < kSeg / 128; ++i) {
+    constexpr int ROWS = kSeg / 128;
+    float hi[ROWS], lo[ROWS];                       // of this lane's four terms in each row, then of whole rows
+    unsigned some = 0u;                             // rows with a term above 0 (this lane's, then all)
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
         const int v = v0 + i * 128 + lane * 4;
         float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
         load4<VEC>(r.p, v, V, p);
         if (r.q) load4<VEC>(r.q, v, V, q);
-        double x[4], sum = 0.0;
-        int mine = -1;
+        Sum2 s{0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float h, l;
             r.term(v + j, p[j], q[j], h, l);
-            sum += static_cast<double>(h) + static_cast<double>(l);
-            x[j] = sum;
-            if (h > 0.f) mine = v + j;
+            s.add(h, l);
+            if (h > 0.f) some |= 1u << i;
         }
-        double incl = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
-        }
-        const double excl = before + (incl - sum);
-        int hit = -1;
-#pragma unroll
-        for (int j = 3; j >= 0; --j)
-            if (excl + x[j] > target && (j == 0 ? x[0] > 0.0 : x[j] > x[j - 1])) hit = v + j;
-        const unsigned m = __ballot_sync(0xffffffffu, hit >= 0);
-        if (m) return __shfl_sync(0xffffffffu, hit, __ffs(m) - 1);
-        const unsigned some = __ballot_sync(0xffffffffu, mine >= 0);
-        if (some) last = __shfl_sync(0xffffffffu, mine, 31 - __clz(some));
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        hi[i] = s.hi;
+        lo[i] = s.lo;
     }
-    return last;
+    some = __reduce_or_sync(0xffffffffu, some);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            Sum2 s{hi[i], lo[i]};
+            const float h = __shfl_xor_sync(0xffffffffu, s.hi, off), l = __shfl_xor_sync(0xffffffffu, s.lo, off);
+            s.add(h, l);
+            hi[i] = s.hi;
+            lo[i] = s.lo;
+        }
+    if (!some) return -1;
+    // the row: every lane takes the same steps
+    double before = 0.0, sum = 0.0;
+    int row = -1;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const double next = sum + Sum2{hi[i], lo[i]}.value();
+        if (row < 0 && ((some >> i) & 1) && next > target) {
+            row = i;
+            before = sum;
+        }
+        sum = next;
+    }
+    const bool past = row < 0;                      // none: the last term of the last row with one
+    if (past) row = 31 - __clz(some);
+    const int v = v0 + row * 128 + lane * 4;
+    float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
+    load4<VEC>(r.p, v, V, p);
+    if (r.q) load4<VEC>(r.q, v, V, q);
+    double x[4], mine = 0.0;
+    int last = -1;
+    bool over0[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float h, l;
+        r.term(v + j, p[j], q[j], h, l);
+        mine += static_cast<double>(h) + static_cast<double>(l);
+        x[j] = mine;
+        over0[j] = h > 0.f;
+        if (over0[j]) last = v + j;
+    }
+    double incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    const double excl = before + (incl - mine);
+    int hit = -1;
+#pragma unroll
+    for (int j = 3; j >= 0; --j)
+        if (!past && over0[j] && excl + x[j] > target) hit = v + j;
+    const unsigned m = __ballot_sync(0xffffffffu, hit >= 0);
+    if (m) return __shfl_sync(0xffffffffu, hit, __ffs(m) - 1);
+    return __shfl_sync(0xffffffffu, last, 31 - __clz(__ballot_sync(0xffffffffu, last >= 0)));
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -178,35 +224,46 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     __shared__ double totals[2][kCluster];          // of the cluster's CTAs; by turns
     __shared__ int tok[kMaxT], par[kMaxT], taken[kMaxT], gone[kMaxT];
     __shared__ float sp[kMaxT], sq[kMaxT], su[kMaxT];
+    __shared__ unsigned okay[2];                    // tokens that would be accepted as first children
     __shared__ int bad;
     const int b = blockIdx.y, rank = C > 1 ? blockIdx.x : 0, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = a.T, V = a.V;
     if (tid == 0) bad = 0;
     pdl_wait();
     pdl_release();
+    const size_t row0 = static_cast<size_t>(b) * T;
     const int n = a.draft_len ? a.draft_len[b] : T;
+    int up = tid - 1, x = 0;                        // (requested with draft_len)
+    float u = 0.f;
+    if (tid < T) {
+        if (a.parent) up = a.parent[row0 + tid];
+        x = a.tokens[row0 + tid];
+        u = a.u[row0 + tid];
+    }
     __syncthreads();
     if (n < 0 || n > T) {                           // the same in the whole cluster
-        bad = GDN_STATUS_BAD_LEN;
-    } else if (tid < n) {
-        const size_t row = static_cast<size_t>(b) * T;
-        const int up = a.parent ? a.parent[row + tid] : tid - 1;
-        su[tid] = a.u[row + tid];
-        par[tid] = up;
-        tok[tid] = 0;
-        sp[tid] = sq[tid] = 0.f;
-        if (tid > 0) {
-            const int x = a.tokens[row + tid];
-            tok[tid] = x;
+        if (tid == 0) bad = GDN_STATUS_BAD_LEN;
+    } else if (tid < kMaxT) {                       // (two whole warps)
+        float p = 0.f, q = 0.f;
+        bool first = false;                         // whether it would be accepted as a first child
+        if (tid > 0 && tid < n) {
             if (x < 0 || x >= V) {
                 atomicOr(&bad, GDN_STATUS_BAD_TOKEN);
             } else if (up < -1 || up >= tid) {
                 atomicOr(&bad, GDN_STATUS_BAD_TREE);
             } else if (up >= 0) {
-                sp[tid] = a.probs[(row + up) * a.p_stride + x];
-                sq[tid] = a.draft ? a.draft[(row + up) * a.q_stride + x] : 1.f;
+                p = fmaxf(a.probs[(row0 + up) * a.p_stride + x], 0.f);
+                q = a.draft ? a.draft[(row0 + up) * a.q_stride + x] : 1.f;
+                first = static_cast<double>(u) * q < p;               // (both sides exact)
             }
         }
+        par[tid] = tid > 0 && tid < n ? up : -1;
+        tok[tid] = x;
+        sp[tid] = p;
+        sq[tid] = q;
+        su[tid] = u;
+        const unsigned m = __ballot_sync(0xffffffffu, first);
+        if (lane == 0) okay[warp] = m;
     }
     __syncthreads();
     if (bad || n == 0) {
@@ -257,7 +314,7 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
         return all;
     };
     auto rest_of = [&](int cur, double c, int lost) {
-        const size_t row = static_cast<size_t>(b) * T + cur;
+        const size_t row = row0 + cur;
         const float ch = static_cast<float>(c);
         return Rest{a.probs + row * a.p_stride, a.draft && c > 0.0 ? a.draft + row * a.q_stride : nullptr, ch,
                     static_cast<float>(c - static_cast<double>(ch)), gone, a.draft ? 0 : lost};
@@ -267,26 +324,42 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     bool known = true;                              // whether mass is that of the present r
     double before, own;
     if (tid == 0) taken[0] = 0;
-    for (int t = 1; t < n; ++t) {
-        if (par[t] != cur) continue;
-        if (!known) {                               // a second child (trees): the first one's rejection is carried out
-            mass = pass(rest_of(cur, c, lost), before, own);
-            known = true;
-            __syncthreads();                        // seg and gone have been read
+    const unsigned long long okays = static_cast<unsigned long long>(okay[1]) << 32 | okay[0];
+    const int par0 = par[lane], par1 = par[lane + 32];
+    auto children = [&](int node) {
+        return static_cast<unsigned long long>(__ballot_sync(0xffffffffu, par1 == node)) << 32 | __ballot_sync(0xffffffffu, par0 == node);
+    };
+    for (unsigned long long left = children(0); left;) {
+        const int t = __ffsll(left) - 1;
+        left &= left - 1;
+        bool accept;
+        double r = 0.0;
+        if (c == 0.0 && lost == 0) {
+            accept = (okays >> t) & 1;
+            r = sp[t];
+        } else {
+            if (!known) {                           // a second child (trees): the first one's rejection is carried out
+                mass = pass(rest_of(cur, c, lost), before, own);
+                known = true;
+                __syncthreads();                    // seg has been read
+            }
+            if (!(mass > 0.0)) continue;
+            const double p = sp[t], q = sq[t];
+            r = a.draft ? fmax(p - c * q, 0.0) : p;
+            if (!a.draft)
+                for (int i = 0; i < lost; ++i)
+                    if (gone[i] == tok[t]) r = 0.0;
+            accept = static_cast<double>(su[t]) * q * mass < r;
         }
-        if (!(mass > 0.0)) continue;
-        const double p = fmaxf(sp[t], 0.f), q = sq[t];
-        double r = a.draft ? fmax(p - c * q, 0.0) : p;
-        if (!a.draft)
-            for (int i = 0; i < lost; ++i)
-                if (gone[i] == tok[t]) r = 0.0;
-        if (static_cast<double>(su[t]) * q * mass < r) {
+        if (accept) {
             cur = t;
             if (tid == 0) taken[count] = t;
             ++count;
             lost = 0;
             c = 0.0;
             mass = 1.0;
+            known = true;
+            left = children(t);
         } else if (a.draft) {
             c += mass;
             known = false;
@@ -368,12 +441,12 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) draft_accept_kernel(const DraftArgs a)
+__global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1) draft_accept_kernel(const DraftArgs a)
 {
     accept_body<kCluster, VEC>(a);
 }
 template <bool VEC>
-__global__ void __launch_bounds__(kThreads) draft_accept_small_kernel(const DraftArgs a)
+__global__ void __launch_bounds__(kThreads, 2) draft_accept_small_kernel(const DraftArgs a)
 {
     accept_body<1, VEC>(a);
 }
