@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "gdnlayer.h"
+#include "pair_math.cuh"
 #include "replay_common.h"
 
 namespace {
@@ -175,11 +176,12 @@ __global__ void conv_accept_kernel(int32_t *ring_pos, const int32_t *state_idx, 
 }
 
 // ------------------------------------------------- the convolution over committed tokens
-// A thread owns 16 bytes of channels (8 of bf16, 4 of fp32) of one sequence for kRun positions in a row: it reads its
-// run and the W - 1 inputs before it (the ring's window for the first run) and writes the run's outputs.  Inputs
-// are read (1 + (W - 1) / kRun) times, the second time from L2.  The ring is left alone here, its window is still
-// being read; the kernel after it (one launch on) puts the last inputs there.
-constexpr int kRun = 8;
+// A thread owns four channels of one sequence for a run of 8 BLOCKS positions: it reads the W - 1 inputs before the run (the
+// ring's window for the first run) and the run's own, eight positions ahead of their use.  Long runs read the taps and
+// the window less often (8 prompts, 6144 channels: 79 us with runs of 8), short ones fill the GPU where there is
+// little to do.  The first run's thread is the only one that reads its channels of the ring, so it also
+// puts the last W - 1 inputs there; the position moves one launch on, when every CTA has read it.
+constexpr int kStep = 8;
 
 struct ConvAdvanceArgs {
     void *ring;
@@ -211,11 +213,12 @@ __device__ __forceinline__ ConvSeq conv_seq(const ConvAdvanceArgs &a, int b) {
     return s;
 }
 
-template <typename TIn, typename TOut, int W>
+template <typename TIn, typename TOut, int W, int BLOCKS>
 __global__ void __launch_bounds__(kConvThreads) conv_advance_kernel(const ConvAdvanceArgs a, int chan_blocks)
 {
     using Raw = typename In4<TIn>::Raw;
-    const int b = blockIdx.y, t0 = blockIdx.x / chan_blocks * kRun;
+    constexpr int RUN = kStep * BLOCKS;
+    const int b = blockIdx.y, t0 = blockIdx.x / chan_blocks * RUN;
     const int c0 = (blockIdx.x % chan_blocks * kConvThreads + threadIdx.x) * 4;
     pdl_wait();
     pdl_release();
@@ -227,81 +230,119 @@ __global__ void __launch_bounds__(kConvThreads) conv_advance_kernel(const ConvAd
         return;
     }
     const int n = sq.n;
-    const size_t base = static_cast<size_t>(b) * a.T * D + c0;
+    const size_t base = (static_cast<size_t>(b) * a.T + t0) * D + c0;
     const TIn *x = reinterpret_cast<const TIn *>(a.x) + base;
     TOut *y = reinterpret_cast<TOut *>(a.y) + base;
-    Raw xr[kRun + W - 1];                                // inputs t0 - (W - 1) .. t0 + kRun - 1
+    Raw next[kStep], before[W > 1 ? W - 1 : 1];
+    auto load = [&](int u) { return t0 + u < n ? __ldg(reinterpret_cast<const Raw *>(x + static_cast<ptrdiff_t>(u) * D)) : Raw{}; };
 #pragma unroll
-    for (int i = 0; i < kRun + W - 1; ++i) {
-        const int t = t0 - (W - 1) + i;
-        xr[i] = Raw{};
-        if (t >= 0 && t < n) {
-            xr[i] = __ldg(reinterpret_cast<const Raw *>(x + static_cast<size_t>(t) * D));
-        } else if (t < 0 && !sq.fresh) {                 // (cap >= W - 1)
-            const TIn *ring = reinterpret_cast<const TIn *>(a.ring) + static_cast<size_t>(sq.slot) * a.cap * D + c0;
-            xr[i] = __ldg(reinterpret_cast<const Raw *>(ring + static_cast<size_t>((t + sq.pos + a.cap) % a.cap) * D));
-        }
+    for (int u = 0; u < kStep; ++u) next[u] = load(u);
+    TIn *ring = reinterpret_cast<TIn *>(a.ring) + static_cast<size_t>(sq.slot) * a.cap * D + c0;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {                    // inputs t0 - (W - 1) + j
+        before[j] = Raw{};
+        if (t0 > 0) before[j] = load(j - (W - 1));       // (RUN >= W - 1)
+        else if (!sq.fresh)                              // (cap >= W - 1)
+            before[j] = *reinterpret_cast<const Raw *>(ring + static_cast<size_t>((j - (W - 1) + sq.pos + a.cap) % a.cap) * D);
     }
-    float wt[4 * W], bias[4];
+    // taps of channel pairs: two products an instruction
+    float wt[4 * W];
 #pragma unroll
     for (int q = 0; q < W; ++q) {
         const float4 w4 = __ldg(reinterpret_cast<const float4 *>(a.weight + static_cast<size_t>(c0) * W) + q);
         wt[4 * q] = w4.x; wt[4 * q + 1] = w4.y; wt[4 * q + 2] = w4.z; wt[4 * q + 3] = w4.w;
     }
-    bias[0] = bias[1] = bias[2] = bias[3] = 0.f;
+    float2 bias[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     if (a.bias) {
         const float4 b4 = __ldg(reinterpret_cast<const float4 *>(a.bias + c0));
-        bias[0] = b4.x; bias[1] = b4.y; bias[2] = b4.z; bias[3] = b4.w;
+        bias[0] = make_float2(b4.x, b4.y);
+        bias[1] = make_float2(b4.z, b4.w);
     }
-    float h[W][4];
+    if (W > 1 && t0 == 0) {                              // the ring's new window: inputs n - W + 1 .. n - 1
+        Raw last[W > 1 ? W - 1 : 1];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) In4<TIn>::unpack(xr[j], h[j]);
+        for (int j = 0; j < W - 1; ++j) {
+            const int t = n - (W - 1) + j;               // one before the chunk stays as the window had it
+            last[j] = t >= 0 ? load(t) : Raw{};
 #pragma unroll
-    for (int u = 0; u < kRun; ++u) {
-        const int t = t0 + u;
-        if (t >= a.T) break;
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-        if (t < n) {
-            In4<TIn>::unpack(xr[W - 1 + u], h[W - 1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float acc = bias[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j) acc = fmaf(wt[i * W + j], h[j][i], acc);
-                o[i] = a.act == GDN_CONV_ACT_SILU ? __fdividef(acc, 1.f + __expf(-acc)) : acc;   // 0 below -87
-            }
-#pragma unroll
-            for (int j = 0; j + 1 < W; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[j][i] = h[j + 1][i];
+            for (int i = 0; i < W - 1; ++i)
+                if (t < 0 && t + W - 1 == i) last[j] = before[i];
         }
-        store_out4<TOut>(y + static_cast<size_t>(t) * D, o);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            const int at = (sq.pos + n - (W - 1) + j) % a.cap;
+            *reinterpret_cast<Raw *>(ring + static_cast<size_t>(at < 0 ? at + a.cap : at) * D) = last[j];
+        }
+    }
+    float2 h[W][2];
+    auto widen = [](const Raw &r, float2 (&f)[2]) {
+        float z[4];
+        In4<TIn>::unpack(r, z);
+        f[0] = make_float2(z[0], z[1]);
+        f[1] = make_float2(z[2], z[3]);
+    };
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) widen(before[j], h[j]);
+#pragma unroll 1
+    for (int u0 = 0; u0 < RUN; u0 += kStep) {
+        if (t0 + u0 >= a.T) break;
+        Raw cur[kStep];
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) cur[u] = next[u];
+        if (u0 + kStep < RUN)
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) next[u] = load(u0 + kStep + u);
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            const int t = t0 + u0 + u;
+            if (t >= a.T) break;
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            widen(cur[u], h[(W - 1 + u) % W]);           // (the window turns round in place: 8 is a multiple of 1, 2 and 4)
+            if (t < n) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float2 acc = bias[i];
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        acc = gdn::fma2(make_float2(wt[2 * i * W + j], wt[(2 * i + 1) * W + j]), h[(u + j) % W][i], acc);
+                    if (a.act == GDN_CONV_ACT_SILU) {
+                        // acc / (1 + 2^(-acc log2 e)): 0 below -87 (a reciprocal of infinity)
+                        float2 e = gdn::mul2(acc, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+                        e = gdn::add2(e, make_float2(1.f, 1.f));
+                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+                        acc = gdn::mul2(acc, e);
+                    }
+                    o[2 * i] = acc.x;
+                    o[2 * i + 1] = acc.y;
+                }
+            }
+            store_out4<TOut>(y + static_cast<size_t>(u0 + u) * D, o);
+        }
+        if (W == 3) {                                    // 8 positions turn a window of three by two
+            float2 z[W][2];
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) z[j][i] = h[(j + kStep) % W][i];
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) h[j][i] = z[j][i];
+        }
     }
 }
 
-// The last W - 1 inputs of each sequence into its ring, and its position.  A CTA has all channels of a
-// sequence, so that the position moves once all of it has been read.
-template <typename TIn>
-__global__ void __launch_bounds__(512) conv_ring_kernel(const ConvAdvanceArgs a)
+__global__ void conv_position_kernel(const ConvAdvanceArgs a)
 {
-    using Raw = typename In4<TIn>::Raw;
     pdl_wait();
     pdl_release();
-    const int b = blockIdx.x, D = a.D;
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b >= a.B) return;
     const ConvSeq sq = conv_seq(a, b);
-    if (sq.bad) return;                                  // (reported by the kernel before)
-    const int n = sq.n, cap = a.cap;
-    const TIn *x = reinterpret_cast<const TIn *>(a.x) + static_cast<size_t>(b) * a.T * D;
-    TIn *ring = reinterpret_cast<TIn *>(a.ring) + static_cast<size_t>(sq.slot) * cap * D;
-    for (int j = 1; j < a.W; ++j) {                      // input n - j
-        const int t = n - j;
-        if (t < 0 && !sq.fresh) break;                   // it is in the ring already
-        TIn *dst = ring + static_cast<size_t>(((sq.pos + t) % cap + cap) % cap) * D;
-        for (int c = threadIdx.x * 4; c < D; c += 512 * 4)
-            *reinterpret_cast<Raw *>(dst + c) = t >= 0 ? __ldg(reinterpret_cast<const Raw *>(x + static_cast<size_t>(t) * D + c)) : Raw{};
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) a.ring_pos[sq.slot] = (sq.pos + n) % cap;
+    if (!sq.bad) a.ring_pos[sq.slot] = (sq.pos + sq.n) % a.cap;          // (reported by the kernel before)
 }
 
 // ------------------------------------------------- gated RMSNorm + E4M3 codes
@@ -420,15 +461,22 @@ int launch_conv(const gdn_conv_dims *d, const ConvArgs &a, cudaStream_t s) {
     }
 }
 
+template <typename TIn, typename TOut, int BLOCKS>
+cudaError_t launch_conv_runs(const gdn_conv_dims *d, const ConvAdvanceArgs &a, cudaStream_t s) {
+    const int cb = (d->D / 4 + kConvThreads - 1) / kConvThreads, run = kStep * BLOCKS;      // (runs x cb < 2^31: check_conv)
+    const dim3 grid(static_cast<unsigned>((d->T + run - 1) / run) * cb, d->B), block(kConvThreads);
+    return d->W == 1   ? launch_pdl(conv_advance_kernel<TIn, TOut, 1, BLOCKS>, grid, block, 0, s, a, cb)
+           : d->W == 2 ? launch_pdl(conv_advance_kernel<TIn, TOut, 2, BLOCKS>, grid, block, 0, s, a, cb)
+           : d->W == 3 ? launch_pdl(conv_advance_kernel<TIn, TOut, 3, BLOCKS>, grid, block, 0, s, a, cb)
+                       : launch_pdl(conv_advance_kernel<TIn, TOut, 4, BLOCKS>, grid, block, 0, s, a, cb);
+}
+
 template <typename TIn, typename TOut>
 cudaError_t launch_conv_advance(const gdn_conv_dims *d, const ConvAdvanceArgs &a, cudaStream_t s) {
-    const int cb = (d->D / 4 + kConvThreads - 1) / kConvThreads;      // (runs x cb < 2^31: check_conv)
-    const dim3 grid(static_cast<unsigned>((d->T + kRun - 1) / kRun) * cb, d->B), block(kConvThreads);
-    const cudaError_t e = d->W == 1   ? launch_pdl(conv_advance_kernel<TIn, TOut, 1>, grid, block, 0, s, a, cb)
-                          : d->W == 2 ? launch_pdl(conv_advance_kernel<TIn, TOut, 2>, grid, block, 0, s, a, cb)
-                          : d->W == 3 ? launch_pdl(conv_advance_kernel<TIn, TOut, 3>, grid, block, 0, s, a, cb)
-                                      : launch_pdl(conv_advance_kernel<TIn, TOut, 4>, grid, block, 0, s, a, cb);
-    return e != cudaSuccess ? e : launch_pdl(conv_ring_kernel<TIn>, dim3(d->B), dim3(512), 0, s, a);
+    // runs of 32 where that still gives each SM's schedulers a few thousand threads (2^19 in all)
+    const bool many = static_cast<long long>(d->B) * d->T * (d->D / 4) >= 32ll << 19;
+    const cudaError_t e = many ? launch_conv_runs<TIn, TOut, 4>(d, a, s) : launch_conv_runs<TIn, TOut, 1>(d, a, s);
+    return e != cudaSuccess ? e : launch_pdl(conv_position_kernel, dim3((d->B + 127) / 128), dim3(128), 0, s, a);
 }
 
 template <int D>
