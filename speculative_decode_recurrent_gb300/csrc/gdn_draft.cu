@@ -8,14 +8,15 @@
 // row from which the next token is drawn, and one pass over the rows serves both.
 //
 // Precision.  The next token is where a running sum of up to 2^24 terms passes a threshold: in 32 bits the
-// sums of 10^5 terms are off by more than many a term.  A term is p - c q in two fp32 words (exact for c = 1), sums
-// are kept in two words (48 bits) by lanes and in 64 bits above, so a token differs from the 64-bit one's only where the
-// threshold lies within some 2^-44 of a border.  Two fp32 words, because fp64 runs at 2 results a clock
-// and SM here.
+// sums of 10^5 terms are off by more than many a term.  A term is p - c q in two fp32 words (exact for c = 1), and sums,
+// masses and thresholds are two words throughout (46 bits and more), so a token differs from the 64-bit one's
+// only where the threshold lies within some 2^-44 of a border.  Two words, because fp64 is slow on this chip: with 64-bit
+// sums above the lanes' the search alone took 12 us, a whole call over 32768 probabilities 23.
 //
 // What bounds it: a few rows of V numbers per sequence, and a chain of dependent steps (tokens, their probabilities,
 // the walk, the pass, its sum across the cluster, the search).  A cluster of eight CTAs takes a sequence, each a
-// stretch of the vocabulary, in segments of 1024 terms per warp (four 16-byte loads of each row in flight per lane, two CTAs on an SM).
+// stretch of the vocabulary, in segments of 1024 terms per warp (256 or 512 where those would leave warps without one); two
+// CTAs share an SM.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -28,7 +29,6 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kSeg = 1024;                          // terms of a segment: a warp's unit
 constexpr int kMaxT = 64;
 constexpr int kSmallV = 4096;                       // vocabularies that one CTA takes alone
 
@@ -42,21 +42,55 @@ struct DraftArgs {
     int segs;                                       // segments of a CTA's stretch
 };
 
-// A sum in two fp32 words.
-struct Sum2 {
-    float hi, lo;
-    __device__ void add(float h, float l) {
-        const float s = hi + h, bp = s - hi;
-        lo += ((hi - (s - bp)) + (h - bp)) + l;
-        hi = s;
-    }
-    __device__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+// A number in two fp32 words: h + l.
+struct Two {
+    float h, l;
 };
+__device__ __forceinline__ Two sum_of(float a, float b) {             // exact
+    const float s = a + b, bp = s - a;
+    return Two{s, (a - (s - bp)) + (b - bp)};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    Two s = sum_of(a.h, b.h);
+    s.l += a.l + b.l;
+    const float h = s.h + s.l;                      // (|l| is far below |h|)
+    return Two{h, s.l - (h - s.h)};
+}
+__device__ __forceinline__ Two operator-(Two a, Two b) { return a + Two{-b.h, -b.l}; }
+__device__ __forceinline__ Two operator*(Two a, float b) {
+    const float h = a.h * b;
+    return Two{h, fmaf(a.h, b, -h) + a.l * b};
+}
+__device__ __forceinline__ bool operator<(Two a, Two b) {
+    const Two d = sum_of(a.h, -b.h);
+    return d.h + (d.l + (a.l - b.l)) < 0.f;
+}
+// (adding only, without bringing l back below h's last place)
+__device__ __forceinline__ void gather(Two &s, float h, float l) {
+    const Two t = sum_of(s.h, h);
+    s.h = t.h;
+    s.l += t.l + l;
+}
+__device__ __forceinline__ Two shuffle_xor(Two x, int off) {
+    return Two{__shfl_xor_sync(0xffffffffu, x.h, off), __shfl_xor_sync(0xffffffffu, x.l, off)};
+}
+__device__ __forceinline__ Two shuffle(Two x, int lane) {
+    return Two{__shfl_sync(0xffffffffu, x.h, lane), __shfl_sync(0xffffffffu, x.l, lane)};
+}
+// Sum over the lanes up to this one.
+__device__ __forceinline__ Two scan(Two x, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const Two y{__shfl_up_sync(0xffffffffu, x.h, off), __shfl_up_sync(0xffffffffu, x.l, off)};
+        if (lane >= off) x = x + y;
+    }
+    return x;
+}
 
-// max(p - c q, 0) in two words, c in two.
-__device__ __forceinline__ void rest(float p, float q, float ch, float cl, float &h, float &l) {
+// max(p - c q, 0) in two words.
+__device__ __forceinline__ void rest(float p, float q, Two c, float &h, float &l) {
     p = fmaxf(p, 0.f);                              // (NaN: 0)
-    const float t = ch * q, e = fmaf(cl, q, fmaf(ch, q, -t));
+    const float t = c.h * q, e = fmaf(c.l, q, fmaf(c.h, q, -t));
     const float d = p - t, bb = d - p;
     const float err = (p - (d - bb)) - (t + bb) - e;
     const bool some = !(d + err <= 0.f);            // (an infinity leaves NaN: the row has no sound sum)
@@ -67,12 +101,12 @@ __device__ __forceinline__ void rest(float p, float q, float ch, float cl, float
 // What a row of r is made of.
 struct Rest {
     const float *p, *q;                             // q NULL: r is p
-    float ch, cl;
+    Two c;
     const int *gone;                                // tokens that r has lost (draft NULL)
     int n_gone;
     __device__ void term(int v, float pv, float qv, float &h, float &l) const {
         if (q) {
-            rest(pv, qv, ch, cl, h, l);
+            rest(pv, qv, c, h, l);
         } else {
             h = fmaxf(pv, 0.f);
             l = 0.f;
@@ -94,43 +128,39 @@ __device__ __forceinline__ void load4(const float *row, int v, int V, float (&x)
     }
 }
 
-// The sum of the segment at v0, in every lane.  Half of it at a time: with 64 registers two CTAs share an SM.
-template <bool VEC>
-__device__ __forceinline__ double segment_sum(const Rest &r, int v0, int V, int lane) {
-    constexpr int ROWS = kSeg / 256;                // rows of 128 terms in half a segment
-    Sum2 s{0.f, 0.f};
+// The sum of the segment of 128 ROWS terms at v0, in every lane.  Four rows at a time: with 64 registers two CTAs share an SM.
+template <int ROWS, bool VEC>
+__device__ __forceinline__ Two segment_sum(const Rest &r, int v0, int V, int lane) {
+    constexpr int SOME = ROWS < 4 ? ROWS : 4;
+    Two s[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll 1
-    for (int at = v0; at < v0 + kSeg; at += kSeg / 2) {
-        float p[ROWS][4], q[ROWS][4];
+    for (int at = v0 + lane * 4; at < v0 + ROWS * 128; at += SOME * 128) {
+        float p[SOME][4], q[SOME][4];
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) load4<VEC>(r.p, at + i * 128 + lane * 4, V, p[i]);
+        for (int i = 0; i < SOME; ++i) load4<VEC>(r.p, at + i * 128, V, p[i]);
         if (r.q)
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) load4<VEC>(r.q, at + i * 128 + lane * 4, V, q[i]);
+            for (int i = 0; i < SOME; ++i) load4<VEC>(r.q, at + i * 128, V, q[i]);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i)
+        for (int i = 0; i < SOME; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float h, l;
-                r.term(at + i * 128 + lane * 4 + j, p[i][j], r.q ? q[i][j] : 0.f, h, l);
-                s.add(h, l);
+                r.term(at + i * 128 + j, p[i][j], r.q ? q[i][j] : 0.f, h, l);
+                gather(s[j & 1], h, l);
             }
     }
+    Two x = s[0] + s[1];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const float h = __shfl_xor_sync(0xffffffffu, s.hi, off), l = __shfl_xor_sync(0xffffffffu, s.lo, off);
-        s.add(h, l);
-    }
-    return __shfl_sync(0xffffffffu, s.value(), 0);
+    for (int off = 16; off > 0; off >>= 1) x = x + shuffle_xor(x, off);
+    return shuffle(x, 0);
 }
 
 // The first term of the segment at v0 at which the running sum passes `target`; the last term above 0 where none does (the
-// segment's sum was taken in another order), -1 where there is none.  The sums of the segment's eight rows of 128 terms
-// in two words first, so that the chain of 64-bit additions is one row's: 8 for the rows, 5 across the lanes, 4 in a lane.
-template <bool VEC>
-__device__ __forceinline__ int segment_find(const Rest &r, int v0, int V, int lane, double target) {
-    constexpr int ROWS = kSeg / 128;
-    float hi[ROWS], lo[ROWS];                       // of this lane's four terms in each row, then of whole rows
+// segment's sum was taken in another order) or `past` says so, -1 where there is none.
+template <int ROWS, bool VEC>
+__device__ __forceinline__ int segment_find(const Rest &r, int v0, int V, int lane, Two target, bool past) {
+    Two s[ROWS];                                    // of this lane's four terms in each row, then of whole rows
     unsigned some = 0u;                             // rows with a term above 0 (this lane's, then all)
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -138,70 +168,57 @@ __device__ __forceinline__ int segment_find(const Rest &r, int v0, int V, int la
         float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
         load4<VEC>(r.p, v, V, p);
         if (r.q) load4<VEC>(r.q, v, V, q);
-        Sum2 s{0.f, 0.f};
+        s[i] = Two{0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float h, l;
             r.term(v + j, p[j], q[j], h, l);
-            s.add(h, l);
+            gather(s[i], h, l);
             if (h > 0.f) some |= 1u << i;
         }
-        hi[i] = s.hi;
-        lo[i] = s.lo;
     }
     some = __reduce_or_sync(0xffffffffu, some);
+    if (!some) return -1;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            Sum2 s{hi[i], lo[i]};
-            const float h = __shfl_xor_sync(0xffffffffu, s.hi, off), l = __shfl_xor_sync(0xffffffffu, s.lo, off);
-            s.add(h, l);
-            hi[i] = s.hi;
-            lo[i] = s.lo;
-        }
-    if (!some) return -1;
+        for (int i = 0; i < ROWS; ++i) s[i] = s[i] + shuffle_xor(s[i], off);
     // the row: every lane takes the same steps
-    double before = 0.0, sum = 0.0;
+    Two before{0.f, 0.f}, sum{0.f, 0.f};
     int row = -1;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const double next = sum + Sum2{hi[i], lo[i]}.value();
-        if (row < 0 && ((some >> i) & 1) && next > target) {
+        const Two next = sum + s[i];
+        if (!past && row < 0 && ((some >> i) & 1) && target < next) {
             row = i;
             before = sum;
         }
         sum = next;
     }
-    const bool past = row < 0;                      // none: the last term of the last row with one
+    past = row < 0;                                 // none: the last term of the last row with one
     if (past) row = 31 - __clz(some);
+    row = __shfl_sync(0xffffffffu, row, 0);
     const int v = v0 + row * 128 + lane * 4;
     float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
     load4<VEC>(r.p, v, V, p);
     if (r.q) load4<VEC>(r.q, v, V, q);
-    double x[4], mine = 0.0;
+    Two x[4], mine{0.f, 0.f};
     int last = -1;
     bool over0[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float h, l;
         r.term(v + j, p[j], q[j], h, l);
-        mine += static_cast<double>(h) + static_cast<double>(l);
+        gather(mine, h, l);
         x[j] = mine;
         over0[j] = h > 0.f;
         if (over0[j]) last = v + j;
     }
-    double incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-    }
-    const double excl = before + (incl - mine);
+    const Two excl = before + (scan(mine, lane) - mine);
     int hit = -1;
 #pragma unroll
     for (int j = 3; j >= 0; --j)
-        if (!past && over0[j] && excl + x[j] > target) hit = v + j;
+        if (!past && over0[j] && target < excl + x[j]) hit = v + j;
     const unsigned m = __ballot_sync(0xffffffffu, hit >= 0);
     if (m) return __shfl_sync(0xffffffffu, hit, __ffs(m) - 1);
     return __shfl_sync(0xffffffffu, last, 31 - __clz(__ballot_sync(0xffffffffu, last >= 0)));
@@ -210,18 +227,20 @@ __device__ __forceinline__ int segment_find(const Rest &r, int v0, int V, int la
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// `x` to word `slot` of the same array in the CTA of rank `to`.
-__device__ __forceinline__ void put_remote(double *word, int to, double x) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(word)), r;
+// `x` to the same place of the CTA of rank `to`.
+__device__ __forceinline__ void put_remote(Two *at, int to, Two x) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(at)), r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(to));
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(r), "d"(x) : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(x.h), "f"(x.l) : "memory");
 }
 
-template <int C, bool VEC>
+template <int C, int ROWS, bool VEC>
 __device__ __forceinline__ void accept_body(const DraftArgs &a)
 {
-    extern __shared__ double seg[];                 // [segs] sums of this CTA's segments
-    __shared__ double totals[2][kCluster];          // of the cluster's CTAs; by turns
+    constexpr int SEG = ROWS * 128;                 // terms of a segment
+    extern __shared__ __align__(16) float seg_raw[];
+    Two *seg = reinterpret_cast<Two *>(seg_raw);    // [segs] sums of this CTA's segments
+    __shared__ __align__(8) Two totals[2][kCluster];          // of the cluster's CTAs; by turns
     __shared__ int tok[kMaxT], par[kMaxT], taken[kMaxT], gone[kMaxT];
     __shared__ float sp[kMaxT], sq[kMaxT], su[kMaxT];
     __shared__ unsigned okay[2];                    // tokens that would be accepted as first children
@@ -254,7 +273,8 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
             } else if (up >= 0) {
                 p = fmaxf(a.probs[(row0 + up) * a.p_stride + x], 0.f);
                 q = a.draft ? a.draft[(row0 + up) * a.q_stride + x] : 1.f;
-                first = static_cast<double>(u) * q < p;               // (both sides exact)
+                const float y = u * q;                                // u q < p, exactly
+                first = y < p || (y == p && fmaf(u, q, -y) < 0.f);
             }
         }
         par[tid] = tid > 0 && tid < n ? up : -1;
@@ -282,18 +302,19 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     int turn = 0;
     // The mass of r over the whole vocabulary, and what lies before this CTA's stretch; fills seg.
     const int first = rank * a.segs;                // this CTA's first segment
-    auto pass = [&](const Rest &r, double &before, double &own) -> double {
+    auto pass = [&](const Rest &r, Two &before) -> Two {
         for (int s = warp; s < a.segs; s += kWarps) {
-            const int v0 = (first + s) * kSeg;      // (below 2^24 + 2^13 kSeg)
-            const double x = v0 < V ? segment_sum<VEC>(r, v0, V, lane) : 0.0;
+            const int v0 = (first + s) * SEG;       // (below 2^24 + 2^13 SEG)
+            const Two x = v0 < V ? segment_sum<ROWS, VEC>(r, v0, V, lane) : Two{0.f, 0.f};
             if (lane == 0) seg[s] = x;
         }
         __syncthreads();
         if (warp == 0) {                            // lane l adds segments l, l + 32, ..
-            double x = 0.0;
-            for (int s = lane; s < a.segs; s += 32) x += seg[s];
+            Two x{0.f, 0.f};
+            for (int s = lane; s < a.segs; s += 32) x = x + seg[s];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+            for (int off = 16; off > 0; off >>= 1) x = x + shuffle_xor(x, off);
+            x = shuffle(x, 0);
             if (C == 1) {
                 if (lane == 0) totals[turn][0] = x;
             } else if (lane < C) {
@@ -302,27 +323,23 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
         }
         if (C == 1) __syncthreads();
         else cluster_sync();
-        double all = 0.0;
-        before = 0.0;
+        Two all{0.f, 0.f};
+        before = Two{0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             if (i == rank) before = all;
-            all += totals[turn][i];
+            all = all + totals[turn][i];
         }
-        own = totals[turn][rank];
         turn ^= 1;                                  // (the other words were read before the last barrier)
         return all;
     };
-    auto rest_of = [&](int cur, double c, int lost) {
+    auto rest_of = [&](int cur, Two c, int lost) {
         const size_t row = row0 + cur;
-        const float ch = static_cast<float>(c);
-        return Rest{a.probs + row * a.p_stride, a.draft && c > 0.0 ? a.draft + row * a.q_stride : nullptr, ch,
-                    static_cast<float>(c - static_cast<double>(ch)), gone, a.draft ? 0 : lost};
+        return Rest{a.probs + row * a.p_stride, a.draft && c.h > 0.f ? a.draft + row * a.q_stride : nullptr, c, gone, a.draft ? 0 : lost};
     };
     int cur = 0, count = 1, lost = 0;               // lost: rejected children of the current token
-    double c = 0.0, mass = 1.0;
+    Two c{0.f, 0.f}, mass{1.f, 0.f}, before;
     bool known = true;                              // whether mass is that of the present r
-    double before, own;
     if (tid == 0) taken[0] = 0;
     const unsigned long long okays = static_cast<unsigned long long>(okay[1]) << 32 | okay[0];
     const int par0 = par[lane], par1 = par[lane + 32];
@@ -333,38 +350,38 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
         const int t = __ffsll(left) - 1;
         left &= left - 1;
         bool accept;
-        double r = 0.0;
-        if (c == 0.0 && lost == 0) {
+        Two r{sp[t], 0.f};
+        if (c.h == 0.f && lost == 0) {
             accept = (okays >> t) & 1;
-            r = sp[t];
         } else {
             if (!known) {                           // a second child (trees): the first one's rejection is carried out
-                mass = pass(rest_of(cur, c, lost), before, own);
+                mass = pass(rest_of(cur, c, lost), before);
                 known = true;
                 __syncthreads();                    // seg has been read
             }
-            if (!(mass > 0.0)) continue;
-            const double p = sp[t], q = sq[t];
-            r = a.draft ? fmax(p - c * q, 0.0) : p;
-            if (!a.draft)
+            if (!(mass.h > 0.f)) continue;
+            if (a.draft) rest(sp[t], sq[t], c, r.h, r.l);
+            else
                 for (int i = 0; i < lost; ++i)
-                    if (gone[i] == tok[t]) r = 0.0;
-            accept = static_cast<double>(su[t]) * q * mass < r;
+                    if (gone[i] == tok[t]) r.h = 0.f;
+            // u q mass < r; u q in two words is exact
+            const float y = su[t] * sq[t];
+            accept = mass * y + mass * fmaf(su[t], sq[t], -y) < r;
         }
         if (accept) {
             cur = t;
             if (tid == 0) taken[count] = t;
             ++count;
             lost = 0;
-            c = 0.0;
-            mass = 1.0;
+            c = Two{0.f, 0.f};
+            mass = Two{1.f, 0.f};
             known = true;
             left = children(t);
         } else if (a.draft) {
-            c += mass;
+            c = c + mass;
             known = false;
         } else {
-            mass -= r;
+            mass = mass - r;
             __syncthreads();                        // gone has been read
             if (tid == 0) gone[lost] = tok[t];
             ++lost;
@@ -374,59 +391,54 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     __syncthreads();
     // ---- the next token
     Rest r = rest_of(cur, c, lost);
-    double all = pass(r, before, own);
-    if (!(all > 0.0)) {                             // the same in the whole cluster
+    Two all = pass(r, before);
+    if (!(all.h > 0.f)) {                           // the same in the whole cluster
         __syncthreads();
-        r = rest_of(cur, 0.0, 0);
-        all = pass(r, before, own);
+        r = rest_of(cur, Two{0.f, 0.f}, 0);
+        all = pass(r, before);
     }
-    const bool sound = all > 0.0 && all < INFINITY;
-    const double target = static_cast<double>(su[0]) * all;
+    const bool sound = all.h > 0.f && all.h < INFINITY;
+    const Two target = all * su[0];
     // The owner: the first CTA whose stretch takes the sum past the target; the last one with mass
     // where rounding (or a u of 1 or more) leaves none.
     int owner = -1;
     if (sound) {
-        double x = 0.0;
+        Two x{0.f, 0.f};
+#pragma unroll
+        for (int i = C - 1; i >= 0; --i)
+            if (owner < 0 && totals[turn ^ 1][i].h > 0.f) owner = i;
+        bool found = false;
+#pragma unroll
         for (int i = 0; i < C; ++i) {
-            const double y = totals[turn ^ 1][i];
-            x += y;
-            if (x > target && y > 0.0) {
+            const Two y = totals[turn ^ 1][i];
+            x = x + y;
+            if (!found && y.h > 0.f && target < x) {
                 owner = i;
-                break;
+                found = true;
             }
         }
-        if (owner < 0)
-            for (int i = 0; i < C; ++i)
-                if (totals[turn ^ 1][i] > 0.0) owner = i;
     }
     if (warp == 0 && (sound ? rank == owner : rank == 0)) {
         int v = -1;
         if (sound) {
             // the segment: a warp's scan of 32 at a time
-            double x = before;
+            Two x = before;
             int s_hit = -1, s_last = -1;
             for (int s0 = 0; s0 < a.segs && s_hit < 0; s0 += 32) {
                 const int s = s0 + lane;
-                const double y = s < a.segs ? seg[s] : 0.0;
-                double incl = y;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const double z = __shfl_up_sync(0xffffffffu, incl, off);
-                    if (lane >= off) incl += z;
-                }
-                const unsigned m = __ballot_sync(0xffffffffu, y > 0.0 && x + incl > target);
-                const unsigned some = __ballot_sync(0xffffffffu, y > 0.0);
+                const Two y = s < a.segs ? seg[s] : Two{0.f, 0.f}, incl = scan(y, lane);
+                const unsigned m = __ballot_sync(0xffffffffu, y.h > 0.f && target < x + incl);
+                const unsigned some = __ballot_sync(0xffffffffu, y.h > 0.f);
                 if (m) {
                     const int l = __ffs(m) - 1;
                     s_hit = s0 + l;
-                    x += __shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, y, l);
+                    x = x + shuffle(incl - y, l);
                 } else {
                     if (some) s_last = s0 + 31 - __clz(some);
-                    x += __shfl_sync(0xffffffffu, incl, 31);
+                    x = x + shuffle(incl, 31);
                 }
             }
-            v = s_hit >= 0 ? segment_find<VEC>(r, (first + s_hit) * kSeg, V, lane, target - x)
-                           : segment_find<VEC>(r, (first + s_last) * kSeg, V, lane, INFINITY);
+            v = segment_find<ROWS, VEC>(r, (first + (s_hit >= 0 ? s_hit : s_last)) * SEG, V, lane, target - x, s_hit < 0);
         }
         if (lane == 0) {
             a.next[b] = v;
@@ -440,15 +452,23 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     }
 }
 
-template <bool VEC>
+template <int ROWS, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1) draft_accept_kernel(const DraftArgs a)
 {
-    accept_body<kCluster, VEC>(a);
+    accept_body<kCluster, ROWS, VEC>(a);
 }
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) draft_accept_small_kernel(const DraftArgs a)
 {
-    accept_body<1, VEC>(a);
+    accept_body<1, 2, VEC>(a);
+}
+
+template <int ROWS>
+cudaError_t launch(const DraftArgs &a, bool vec, cudaStream_t s) {
+    const dim3 grid(kCluster, a.B);
+    const size_t smem = static_cast<size_t>(a.segs) * sizeof(Two);
+    return vec ? launch_pdl(draft_accept_kernel<ROWS, true>, grid, dim3(kThreads), smem, s, a)
+               : launch_pdl(draft_accept_kernel<ROWS, false>, grid, dim3(kThreads), smem, s, a);
 }
 
 }  // namespace
@@ -465,18 +485,22 @@ extern "C" int gdn_draft_accept(const gdn_draft_dims *d, const int32_t *tokens, 
     if (d->p_stride < d->V || (draft && d->q_stride < d->V)) return GDN_ERR_DIMS;
     if (d->B == 0) return GDN_OK;
     if (!tokens || !probs || !u || !accepted || !next || !status || (parent && !path)) return GDN_ERR_NULL;
+    // Terms of a segment: a CTA's 16 warps each get one as far as the vocabulary goes, 1024 at most (more in flight).
     const bool small = d->V <= kSmallV;
-    const int all = (d->V + kSeg - 1) / kSeg, segs = small ? all : (all + kCluster - 1) / kCluster;
-    const DraftArgs a{tokens, parent, probs, draft, u, draft_len, accepted, next, path, status, d->p_stride, d->q_stride,
-                      d->B, d->T, d->V, segs};
+    const int share = small ? d->V : (d->V + kCluster - 1) / kCluster;
+    const int rows = small || share <= 256 * kWarps ? 2 : share <= 512 * kWarps ? 4 : 8;
+    DraftArgs a{tokens, parent, probs, draft, u, draft_len, accepted, next, path, status, d->p_stride, d->q_stride,
+                d->B, d->T, d->V, (share + rows * 128 - 1) / (rows * 128)};
     // 16-byte loads where every row begins on such a boundary
     const bool vec = reinterpret_cast<uintptr_t>(probs) % 16 == 0 && d->p_stride % 4 == 0 &&
                      (!draft || (reinterpret_cast<uintptr_t>(draft) % 16 == 0 && d->q_stride % 4 == 0));
-    const size_t smem = static_cast<size_t>(segs) * sizeof(double);
-    const dim3 grid(small ? 1 : kCluster, d->B), block(kThreads);
-    const cudaError_t e = small ? (vec ? launch_pdl(draft_accept_small_kernel<true>, grid, block, smem, stream, a)
-                                       : launch_pdl(draft_accept_small_kernel<false>, grid, block, smem, stream, a))
-                                : (vec ? launch_pdl(draft_accept_kernel<true>, grid, block, smem, stream, a)
-                                       : launch_pdl(draft_accept_kernel<false>, grid, block, smem, stream, a));
+    cudaError_t e;
+    if (small) {
+        const size_t smem = static_cast<size_t>(a.segs) * sizeof(Two);
+        e = vec ? launch_pdl(draft_accept_small_kernel<true>, dim3(1, d->B), dim3(kThreads), smem, stream, a)
+                : launch_pdl(draft_accept_small_kernel<false>, dim3(1, d->B), dim3(kThreads), smem, stream, a);
+    } else {
+        e = rows == 2 ? launch<2>(a, vec, stream) : rows == 4 ? launch<4>(a, vec, stream) : launch<8>(a, vec, stream);
+    }
     return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
