@@ -22,6 +22,7 @@
 
 #include "gdnattn.h"
 #include "gdndraft.h"
+#include "pair_math.cuh"
 #include "replay_common.h"
 
 namespace gdn {
@@ -65,12 +66,6 @@ __device__ __forceinline__ bool operator<(Two a, Two b) {
     const Two d = sum_of(a.h, -b.h);
     return d.h + (d.l + (a.l - b.l)) < 0.f;
 }
-// (adding only, without bringing l back below h's last place)
-__device__ __forceinline__ void gather(Two &s, float h, float l) {
-    const Two t = sum_of(s.h, h);
-    s.h = t.h;
-    s.l += t.l + l;
-}
 __device__ __forceinline__ Two shuffle_xor(Two x, int off) {
     return Two{__shfl_xor_sync(0xffffffffu, x.h, off), __shfl_xor_sync(0xffffffffu, x.l, off)};
 }
@@ -79,7 +74,7 @@ __device__ __forceinline__ Two shuffle(Two x, int lane) {
 }
 // Sum over the lanes up to this one.
 __device__ __forceinline__ Two scan(Two x, int lane) {
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
         const Two y{__shfl_up_sync(0xffffffffu, x.h, off), __shfl_up_sync(0xffffffffu, x.l, off)};
         if (lane >= off) x = x + y;
@@ -87,15 +82,25 @@ __device__ __forceinline__ Two scan(Two x, int lane) {
     return x;
 }
 
-// max(p - c q, 0) in two words.
-__device__ __forceinline__ void rest(float p, float q, Two c, float &h, float &l) {
-    p = fmaxf(p, 0.f);                              // (NaN: 0)
-    const float t = c.h * q, e = fmaf(c.l, q, fmaf(c.h, q, -t));
-    const float d = p - t, bb = d - p;
-    const float err = (p - (d - bb)) - (t + bb) - e;
-    const bool some = !(d + err <= 0.f);            // (an infinity leaves NaN: the row has no sound sum)
-    h = some ? d : 0.f;
-    l = some ? err : 0.f;
+// max(p - c q, 0) in two words, for two tokens (two operations an instruction).  The sign is d's: where p and c q agree in
+// 24 bits the rest counts as 0.  A negative p or NaN gives 0, an infinity leaves NaN (the row has no sound sum).
+__device__ __forceinline__ void rest(float2 p, float2 q, Two c, float2 &h, float2 &l) {
+    const float2 minus = make_float2(-1.f, -1.f), t = mul2(make_float2(-c.h, -c.h), q);      // - c.h q
+    float2 e = fma2(make_float2(c.h, c.h), q, t);
+    e = fma2(make_float2(c.l, c.l), q, e);
+    const float2 d = add2(p, t), bp = fma2(p, minus, d);
+    const float2 err = fma2(e, minus, add2(fma2(fma2(bp, minus, d), minus, p), fma2(bp, minus, t)));
+    h = make_float2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f));
+    l = make_float2(d.x > 0.f ? err.x : 0.f, d.y > 0.f ? err.y : 0.f);
+}
+// Two sums side by side, without bringing l back below h's last place.
+struct Two2 {
+    float2 h, l;
+};
+__device__ __forceinline__ void gather(Two2 &s, float2 h, float2 l) {
+    const float2 minus = make_float2(-1.f, -1.f), t = add2(s.h, h), bp = fma2(s.h, minus, t);
+    s.l = add2(s.l, add2(l, add2(fma2(fma2(bp, minus, t), minus, s.h), fma2(bp, minus, h))));
+    s.h = t;
 }
 
 // What a row of r is made of.
@@ -104,14 +109,17 @@ struct Rest {
     Two c;
     const int *gone;                                // tokens that r has lost (draft NULL)
     int n_gone;
-    __device__ void term(int v, float pv, float qv, float &h, float &l) const {
+    // tokens v and v + 1
+    __device__ __forceinline__ void terms(int v, float2 pv, float2 qv, float2 &h, float2 &l) const {
         if (q) {
             rest(pv, qv, c, h, l);
         } else {
-            h = fmaxf(pv, 0.f);
-            l = 0.f;
-            for (int i = 0; i < n_gone; ++i)
-                if (v == gone[i]) h = 0.f;
+            h = make_float2(fmaxf(pv.x, 0.f), fmaxf(pv.y, 0.f));
+            l = make_float2(0.f, 0.f);
+            for (int i = 0; i < n_gone; ++i) {
+                if (v == gone[i]) h.x = 0.f;
+                if (v + 1 == gone[i]) h.y = 0.f;
+            }
         }
     }
 };
@@ -132,7 +140,7 @@ __device__ __forceinline__ void load4(const float *row, int v, int V, float (&x)
 template <int ROWS, bool VEC>
 __device__ __forceinline__ Two segment_sum(const Rest &r, int v0, int V, int lane) {
     constexpr int SOME = ROWS < 4 ? ROWS : 4;
-    Two s[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    Two2 s{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
     for (int at = v0 + lane * 4; at < v0 + ROWS * 128; at += SOME * 128) {
         float p[SOME][4], q[SOME][4];
@@ -144,84 +152,16 @@ __device__ __forceinline__ Two segment_sum(const Rest &r, int v0, int V, int lan
 #pragma unroll
         for (int i = 0; i < SOME; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float h, l;
-                r.term(at + i * 128 + j, p[i][j], r.q ? q[i][j] : 0.f, h, l);
-                gather(s[j & 1], h, l);
+            for (int j = 0; j < 4; j += 2) {
+                float2 h, l;
+                r.terms(at + i * 128 + j, make_float2(p[i][j], p[i][j + 1]), make_float2(q[i][j], q[i][j + 1]), h, l);
+                gather(s, h, l);
             }
     }
-    Two x = s[0] + s[1];
-#pragma unroll
+    Two x = Two{s.h.x, s.l.x} + Two{s.h.y, s.l.y};
+#pragma unroll 1
     for (int off = 16; off > 0; off >>= 1) x = x + shuffle_xor(x, off);
     return shuffle(x, 0);
-}
-
-// The first term of the segment at v0 at which the running sum passes `target`; the last term above 0 where none does (the
-// segment's sum was taken in another order) or `past` says so, -1 where there is none.
-template <int ROWS, bool VEC>
-__device__ __forceinline__ int segment_find(const Rest &r, int v0, int V, int lane, Two target, bool past) {
-    Two s[ROWS];                                    // of this lane's four terms in each row, then of whole rows
-    unsigned some = 0u;                             // rows with a term above 0 (this lane's, then all)
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int v = v0 + i * 128 + lane * 4;
-        float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
-        load4<VEC>(r.p, v, V, p);
-        if (r.q) load4<VEC>(r.q, v, V, q);
-        s[i] = Two{0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float h, l;
-            r.term(v + j, p[j], q[j], h, l);
-            gather(s[i], h, l);
-            if (h > 0.f) some |= 1u << i;
-        }
-    }
-    some = __reduce_or_sync(0xffffffffu, some);
-    if (!some) return -1;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) s[i] = s[i] + shuffle_xor(s[i], off);
-    // the row: every lane takes the same steps
-    Two before{0.f, 0.f}, sum{0.f, 0.f};
-    int row = -1;
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const Two next = sum + s[i];
-        if (!past && row < 0 && ((some >> i) & 1) && target < next) {
-            row = i;
-            before = sum;
-        }
-        sum = next;
-    }
-    past = row < 0;                                 // none: the last term of the last row with one
-    if (past) row = 31 - __clz(some);
-    row = __shfl_sync(0xffffffffu, row, 0);
-    const int v = v0 + row * 128 + lane * 4;
-    float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
-    load4<VEC>(r.p, v, V, p);
-    if (r.q) load4<VEC>(r.q, v, V, q);
-    Two x[4], mine{0.f, 0.f};
-    int last = -1;
-    bool over0[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float h, l;
-        r.term(v + j, p[j], q[j], h, l);
-        gather(mine, h, l);
-        x[j] = mine;
-        over0[j] = h > 0.f;
-        if (over0[j]) last = v + j;
-    }
-    const Two excl = before + (scan(mine, lane) - mine);
-    int hit = -1;
-#pragma unroll
-    for (int j = 3; j >= 0; --j)
-        if (!past && over0[j] && target < excl + x[j]) hit = v + j;
-    const unsigned m = __ballot_sync(0xffffffffu, hit >= 0);
-    if (m) return __shfl_sync(0xffffffffu, hit, __ffs(m) - 1);
-    return __shfl_sync(0xffffffffu, last, 31 - __clz(__ballot_sync(0xffffffffu, last >= 0)));
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -244,6 +184,7 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     __shared__ int tok[kMaxT], par[kMaxT], taken[kMaxT], gone[kMaxT];
     __shared__ float sp[kMaxT], sq[kMaxT], su[kMaxT];
     __shared__ unsigned okay[2];                    // tokens that would be accepted as first children
+    __shared__ __align__(8) Two rows[ROWS];         // sums of the chosen segment's rows
     __shared__ int bad;
     const int b = blockIdx.y, rank = C > 1 ? blockIdx.x : 0, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = a.T, V = a.V;
@@ -312,7 +253,7 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
         if (warp == 0) {                            // lane l adds segments l, l + 32, ..
             Two x{0.f, 0.f};
             for (int s = lane; s < a.segs; s += 32) x = x + seg[s];
-#pragma unroll
+#pragma unroll 1
             for (int off = 16; off > 0; off >>= 1) x = x + shuffle_xor(x, off);
             x = shuffle(x, 0);
             if (C == 1) {
@@ -325,7 +266,7 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
         else cluster_sync();
         Two all{0.f, 0.f};
         before = Two{0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < C; ++i) {
             if (i == rank) before = all;
             all = all + totals[turn][i];
@@ -346,7 +287,22 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     auto children = [&](int node) {
         return static_cast<unsigned long long>(__ballot_sync(0xffffffffu, par1 == node)) << 32 | __ballot_sync(0xffffffffu, par0 == node);
     };
-    for (unsigned long long left = children(0); left;) {
+    unsigned long long left = 0ull;
+    if (a.parent) {
+        left = children(0);
+    } else {                                        // a chain: its accepted tokens lie in a row, one rejection ends them
+        cur = min(__ffsll(~(okays >> 1)) - 1, n - 1);
+        count = cur + 1;
+        if (tid < count) taken[tid] = tid;
+        if (count < n && a.draft) {
+            c = mass;
+            known = false;
+        } else if (count < n) {
+            if (tid == 0) gone[0] = tok[count];
+            lost = 1;
+        }
+    }
+    while (left) {
         const int t = __ffsll(left) - 1;
         left &= left - 1;
         bool accept;
@@ -360,8 +316,11 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
                 __syncthreads();                    // seg has been read
             }
             if (!(mass.h > 0.f)) continue;
-            if (a.draft) rest(sp[t], sq[t], c, r.h, r.l);
-            else
+            if (a.draft) {
+                float2 h, l;
+                rest(make_float2(sp[t], 0.f), make_float2(sq[t], 0.f), c, h, l);
+                r = Two{h.x, l.x};
+            } else
                 for (int i = 0; i < lost; ++i)
                     if (gone[i] == tok[t]) r.h = 0.f;
             // u q mass < r; u q in two words is exact
@@ -401,29 +360,30 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     const Two target = all * su[0];
     // The owner: the first CTA whose stretch takes the sum past the target; the last one with mass
     // where rounding (or a u of 1 or more) leaves none.
-    int owner = -1;
+    int owner = sound ? -1 : 0;
+    bool found = false;
     if (sound) {
         Two x{0.f, 0.f};
-#pragma unroll
-        for (int i = C - 1; i >= 0; --i)
-            if (owner < 0 && totals[turn ^ 1][i].h > 0.f) owner = i;
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < C && !found; ++i) {
             const Two y = totals[turn ^ 1][i];
             x = x + y;
-            if (!found && y.h > 0.f && target < x) {
-                owner = i;
-                found = true;
-            }
+            if (y.h > 0.f) owner = i;
+            found = y.h > 0.f && target < x;
         }
     }
-    if (warp == 0 && (sound ? rank == owner : rank == 0)) {
-        int v = -1;
-        if (sound) {
-            // the segment: a warp's scan of 32 at a time
+    if (rank == owner) {                            // (the same in a CTA)
+        if (!sound) {
+            if (tid == 0) {
+                a.next[b] = -1;
+                atomicOr(a.status, GDN_STATUS_BAD_PROB);
+            }
+        } else {
+            // The segment, by a scan of 32 at a time (every warp for itself); then a warp per row of it, whose scan gives the
+            // row's sum and, in the row of the target, the place.  (One warp for all rows took four times as
+            // long: straight code that runs once waits for its instructions.)
             Two x = before;
-            int s_hit = -1, s_last = -1;
+            int s_hit = -1, s_last = 0;
             for (int s0 = 0; s0 < a.segs && s_hit < 0; s0 += 32) {
                 const int s = s0 + lane;
                 const Two y = s < a.segs ? seg[s] : Two{0.f, 0.f}, incl = scan(y, lane);
@@ -438,11 +398,51 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
                     x = x + shuffle(incl, 31);
                 }
             }
-            v = segment_find<ROWS, VEC>(r, (first + (s_hit >= 0 ? s_hit : s_last)) * SEG, V, lane, target - x, s_hit < 0);
-        }
-        if (lane == 0) {
-            a.next[b] = v;
-            if (v < 0) atomicOr(a.status, GDN_STATUS_BAD_PROB);
+            const Two goal = target - x;
+            const int v = (first + (s_hit >= 0 ? s_hit : s_last)) * SEG + warp * 128 + lane * 4;
+            Two2 h4[2];                             // this lane's four terms
+            Two mine{0.f, 0.f}, incl{0.f, 0.f};
+            if (warp < ROWS) {
+                float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
+                load4<VEC>(r.p, v, V, p);
+                if (r.q) load4<VEC>(r.q, v, V, q);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    r.terms(v + 2 * j, make_float2(p[2 * j], p[2 * j + 1]), make_float2(q[2 * j], q[2 * j + 1]), h4[j].h, h4[j].l);
+                mine = (Two{h4[0].h.x, h4[0].l.x} + Two{h4[0].h.y, h4[0].l.y}) + (Two{h4[1].h.x, h4[1].l.x} + Two{h4[1].h.y, h4[1].l.y});
+                incl = scan(mine, lane);
+                if (lane == 31) rows[warp] = incl;
+            }
+            __syncthreads();
+            if (warp < ROWS) {
+                Two sum{0.f, 0.f}, ahead{0.f, 0.f};
+                int row = -1, last = 0;
+#pragma unroll 1
+                for (int i = 0; i < ROWS; ++i) {
+                    const Two y = rows[i], next = sum + y;
+                    if (y.h > 0.f) last = i;
+                    if (row < 0 && s_hit >= 0 && y.h > 0.f && goal < next) {
+                        row = i;
+                        ahead = sum;
+                    }
+                    sum = next;
+                }
+                if (warp == (row >= 0 ? row : last)) {                // none past the goal: the last term with mass
+                    const Two excl = ahead + (incl - mine);
+                    const float h[4] = {h4[0].h.x, h4[0].h.y, h4[1].h.x, h4[1].h.y}, l[4] = {h4[0].l.x, h4[0].l.y, h4[1].l.x, h4[1].l.y};
+                    int hit = -1, end = -1;
+                    Two x4 = excl;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x4 = x4 + Two{h[j], l[j]};
+                        if (h[j] > 0.f) end = v + j;
+                        if (hit < 0 && row >= 0 && h[j] > 0.f && goal < x4) hit = v + j;
+                    }
+                    const unsigned m = __ballot_sync(0xffffffffu, hit >= 0), e = __ballot_sync(0xffffffffu, end >= 0);
+                    const int at = m ? __shfl_sync(0xffffffffu, hit, __ffs(m) - 1) : __shfl_sync(0xffffffffu, end, e ? 31 - __clz(e) : 0);
+                    if (lane == 0) a.next[b] = at;
+                }
+            }
         }
     }
     if (rank == 0) {
