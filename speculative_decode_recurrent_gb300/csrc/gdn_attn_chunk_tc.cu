@@ -8,14 +8,15 @@
 // them, would make the second product, half of all the work here, twice as long).  l is the sum of the weights in fp32.
 //
 // What bounds it: the MMAs.  A CTA has two tiles of 128 rows (row r = t G + g: tokens times the query heads of a key
-// head), so that one tile's softmax runs while the tensor cores work for the other: per tile of 128 keys
-// 2 x 1072 cycles of MMAs (d 128), against some 1000 of each group's softmax.
+// head) whose softmaxes and products overlap, and each tile has two score buffers, so that the next keys'
+// scores are there when a softmax ends (one buffer of twice the keys left the tensor cores waiting for a third of the
+// time: softmax, weights, scores one after the other in 3500 cycles for 2144 of MMAs).
 //
-// Roles.  Two groups of 128 threads, one per row (no exchange between lanes; the scores of a row are in registers); a
-// warp each loads keys and values (TMA through the block table); one warp issues, in the order P0 V, Q0 K', P1 V, Q1 K' (K' the
-// next tile).  The weights go over the scores in TMEM and are the A operand from there; scores of the next tile
-// follow the product that reads them in the order of issue.  d 256: the sums of 256 columns of two row
-// tiles leave no room for scores, so a CTA takes 128 columns of the values and both halves form the scores.
+// Roles.  Two groups of 128 threads, one per row (no exchange between lanes; the scores of a row are in registers), and
+// for each group a warp that issues: O += P_i V_i, then the scores of tile i + 2 into the buffer that held P_i (the weights go
+// over the scores in TMEM and are the A operand from there; the order of issue keeps the two apart).  A warp each loads
+// keys and values (TMA through the block table).  d 256: the sums of 256 columns of two row tiles leave no room for
+// scores, so a CTA takes 128 columns of the values and both halves form the scores.
 //
 // Work.  A CTA is (pair of row tiles, key head, sequence, part of the keys); the longest come first.  Keys are cut
 // into parts where the pairs alone would leave SMs without work (best_splits), joined by gdn_attn_chunk.cu.
@@ -36,14 +37,14 @@ constexpr int kMaxSplits = 64;
 
 template <int D> struct Plan {
     static constexpr int DV = D == 256 ? 128 : D;   // value columns of a CTA
-    static constexpr int KT = D == 256 ? 64 : 128;  // keys of a tile
-    static constexpr int NK = D == 64 ? 4 : D == 128 ? 3 : 2, NV = D == 64 ? 4 : 2;      // stages
+    static constexpr int KT = 64;                   // keys of a tile
+    static constexpr int NK = D == 64 ? 8 : D == 128 ? 5 : 2, NV = NK;                   // stages
     static constexpr int QA = D / 64, VA = DV / 64; // 64-column atoms of 128-byte rows
     static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = KT * D * 2, V_BYTES = KT * DV * 2;
     static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NK * K_BYTES, OFF_BAR = OFF_V + NV * V_BYTES;
-    static constexpr int BYTES = OFF_BAR + 256;
-    static constexpr int LOAD_WARP = 8, MMA_WARP = 10, THREADS = 11 * 32;
-    static constexpr int COL_S = 0, COL_O = 2 * KT; // TMEM: scores of the two tiles, then their sums
+    static constexpr int BYTES = OFF_BAR + 512;
+    static constexpr int LOAD_WARP = 8, MMA_WARP = 10, THREADS = 12 * 32;
+    static constexpr int COL_S = 0, COL_O = 4 * KT; // TMEM: two score buffers of each row tile, then their sums
     static_assert(COL_O + 2 * DV <= 512 && BYTES <= 227 * 1024, "plan");
 };
 
@@ -66,11 +67,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     id /= HALVES;
     const int part = id % a.splits, pairs = (a.row_tiles + 1) / 2, rt0 = (pairs - 1 - id / a.splits) * 2;      // long ones first
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *k_empty = k_full + P::NK, *v_full = k_empty + P::NK,
-             *v_empty = v_full + P::NV, *q_full = v_empty + P::NV, *s_full = q_full + 1, *p_full = s_full + 2, *o_done = p_full + 2,
-             *drain = o_done + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+             *v_empty = v_full + P::NV, *q_full = v_empty + P::NV, *s_full = q_full + 1, *p_full = s_full + 4, *o_done = p_full + 4,
+             *drain = o_done + 2;                   // s_full, p_full [group][buffer]; o_done, drain [group]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((2 * P::NK + 2 * P::NV + 8) * 8 + 8 <= 256, "barriers");
+    static_assert((2 * P::NK + 2 * P::NV + 13) * 8 + 8 <= 512, "barriers");
     if (saddr(smem) & 1023u) {
         if (tid == 0) atomicOr(a.s.status, kStatusTimeout);
         return;
@@ -78,19 +79,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (tid == 0) {
         for (int i = 0; i < P::NK; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
+            mbar_init(&k_empty[i], 2);              // the warps of both groups
         }
         for (int i = 0; i < P::NV; ++i) {
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&v_empty[i], 2);
         }
         mbar_init(q_full, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
-            mbar_init(&o_done[i], 1);
         }
-        mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&o_done[i], 1);
+            mbar_init(&drain[i], 1);
+        }
         *abort = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
         fence_mbar_init();
     }
@@ -202,77 +205,71 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int y = max(0, i - ns); y < i; ++y) done = done && mbar_wait(&full[y % ns], (y / ns) & 1);
             if (!done && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
-    } else if (warp == P::MMA_WARP) {
-        // ------------------------------------------------------ MMAs
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t dq = desc_sw128(saddr(smem)), dk0 = desc_sw128(saddr(smem) + P::OFF_K),
+    } else if (warp >= P::MMA_WARP) {
+        // ------------------------------------------------------ MMAs of a group
+        const int g = __shfl_sync(0xffffffffu, warp - P::MMA_WARP, 0), n = g ? n1 : n0;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), t_s = tm + P::COL_S + g * 2 * KT, t_o = tm + P::COL_O + g * DV;
+        const uint64_t dq = desc_sw128(saddr(smem) + g * P::Q_BYTES), dk0 = desc_sw128(saddr(smem) + P::OFF_K),
                        dv0 = desc_mn_sw128(saddr(smem) + P::OFF_V, KT * 128);
         constexpr uint32_t idS = idesc_mn(1, kRows, KT), idO = idesc_mn(1, kRows, DV) | kIdescMnMajorB;
-        auto scores = [&](int g, int ks) {          // Q_g K^T of the keys in stage ks
-            const uint64_t qd = desc_add(dq, g * P::Q_BYTES), kd = desc_add(dk0, ks * P::K_BYTES);
+        int ks = 0, kr = 0, vs = 0, vr = 0;         // stages of the next keys and values, and their rounds
+        bool issued = false;
+        auto scores = [&](int i) -> bool {          // Q K^T of tile i into buffer i % 2
+            if (!wait(&k_full[ks], kr & 1)) return false;
+            tc_fence_after();
+            const uint64_t kd = desc_add(dk0, ks * P::K_BYTES);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_bf16(tm + P::COL_S + g * KT, desc_add(qd, (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                    mma_bf16(t_s + (i & 1) * KT, desc_add(dq, (k >> 2) * (kRows * 128) + (k & 3) * 32),
                              desc_add(kd, (k >> 2) * (KT * 128) + (k & 3) * 32), idS, k > 0);
-                mma_commit(&s_full[g]);
+                mma_commit(&s_full[2 * g + (i & 1)]);
+                mma_commit(&k_empty[ks]);
             }
             __syncwarp();
+            issued = true;
+            if (++ks == P::NK) ks = 0, ++kr;
+            return true;
         };
-        auto sums = [&](int g, int vs, int i) {     // O_g += P_g V of the values in stage vs
+        bool ok = n == 0 || wait(q_full, 0);
+        for (int i = 0; ok && i < min(n, 2); ++i) ok = scores(i);
+        for (int i = 0; ok && i < n; ++i) {
+            ok = wait(&v_full[vs], vr & 1) && wait(&p_full[2 * g + (i & 1)], (i >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
             const uint64_t vd = desc_add(dv0, vs * P::V_BYTES);
             if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    mma_bf16_ts(tm + P::COL_O + g * DV, tm + P::COL_S + g * KT + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+                for (int k = 0; k < KT / 16; ++k)   // P_i V_i
+                    mma_bf16_ts(t_o, t_s + (i & 1) * KT + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
                 mma_commit(&o_done[g]);
+                mma_commit(&v_empty[vs]);
             }
             __syncwarp();
-        };
-        auto release = [&](uint64_t *bar) {
-            if (elect_one()) mma_commit(bar);
-            __syncwarp();
-        };
-        bool ok = count == 0 || (wait(q_full, 0) && wait(&k_full[0], 0));
-        const bool began = ok;
-        if (ok && count > 0) {
-            tc_fence_after();
-            if (n0 > 0) scores(0, 0);
-            if (n1 > 0) scores(1, 0);
-            release(&k_empty[0]);
-        }
-        int ks = 1 % P::NK, kr = 1 / P::NK, vs = 0, vr = 0;           // stages of the next keys and these values, and their rounds
-        for (int i = 0; ok && i < count; ++i) {
-            const bool more = i + 1 < count;
-            ok = wait(&v_full[vs], vr & 1) && (!more || wait(&k_full[ks], kr & 1));
-            if (!ok) break;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int n = g ? n1 : n0;
-                if (i < n) {
-                    if (!(ok = wait(&p_full[g], i & 1))) break;
-                    tc_fence_after();
-                    sums(g, vs, i);
-                    if (i + 1 < n) scores(g, ks);
-                }
-            }
-            if (!ok) break;
-            release(&v_empty[vs]);
-            if (more) release(&k_empty[ks]);
             if (++vs == P::NV) vs = 0, ++vr;
-            if (++ks == P::NK) ks = 0, ++kr;
+            if (i + 2 < n) ok = scores(i + 2);
         }
-        if (!ok && began) {                         // MMAs in flight end before their memory is given back
-            if (elect_one()) mma_commit(drain);
+        // tiles that only the other group sees: passed on once they are there (an arrival before that would count
+        // for the round before)
+        for (int i = n; ok && i < count; ++i) {
+            ok = wait(&k_full[ks], kr & 1);
+            if (ok && lane == 0) mbar_arrive(&k_empty[ks]);
+            if (++ks == P::NK) ks = 0, ++kr;
+            ok = ok && wait(&v_full[vs], vr & 1);
+            if (ok && lane == 0) mbar_arrive(&v_empty[vs]);
+            if (++vs == P::NV) vs = 0, ++vr;
+        }
+        if (!ok && issued) {                        // MMAs in flight end before their memory is given back
+            if (elect_one()) mma_commit(&drain[g]);
             __syncwarp();
-            if (!mbar_wait(drain, 0) && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
+            if (!mbar_wait(&drain[g], 0) && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
     } else {
         // ------------------------------------------------------ rows
         const int g = warp >> 2, r = tid & 127, n = g ? n1 : n0;
         const int tg = t0 + g * a.tpt;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lanes + P::COL_S + g * KT, t_o = tmem + lanes + P::COL_O + g * DV;
+        const uint32_t t_s0 = tmem + lanes + P::COL_S + g * 2 * KT, t_o = tmem + lanes + P::COL_O + g * DV;
         const bool used = r < (g ? live[1] : live[0]);
         const int lim = used ? sq.len + tg + r / G + 1 : 0;           // keys that this row sees
         const int free_to = sq.len + tg + 1;                          // keys that every row in use sees
@@ -294,7 +291,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 fence_proxy_async();
             }
-            if (!(ok = wait(&s_full[g], i & 1))) break;
+            const uint32_t t_s = t_s0 + (i & 1) * KT;
+            if (!(ok = wait(&s_full[2 * g + (i & 1)], (i >> 1) & 1))) break;
             tc_fence_after();
             uint32_t x[KT];
 #pragma unroll
@@ -319,7 +317,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     m = mt;
                     l *= fac;
                 }
-                if (i > 0) {                        // the sums so far: their last product must be done
+                if (i > 0) {                        // the sums so far: their last product must be done (the one before it
+                                                    // is, as its weights' buffer holds these scores)
                     if (!(ok = wait(&o_done[g], (i - 1) & 1))) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -336,27 +335,24 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const float ms = m == -INFINITY ? 0.f : m;
             const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-ms, -ms);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t p[KT / 2];
 #pragma unroll
-            for (int c = 0; c < KT; c += 64) {
-                uint32_t p[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float2 e = fma2(make_float2(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), sc, mm);
-                    e = make_float2(ex2(e.x), ex2(e.y));
-                    sum[k & 1] = add2(sum[k & 1], e);
-                    const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
-                    p[k] = *reinterpret_cast<const uint32_t *>(&w);
-                }
-                tmem_st32(t_s + c / 2, p);
+            for (int k = 0; k < KT / 2; ++k) {
+                float2 e = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc, mm);
+                e = make_float2(ex2(e.x), ex2(e.y));
+                sum[k & 1] = add2(sum[k & 1], e);
+                const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
+                p[k] = *reinterpret_cast<const uint32_t *>(&w);
             }
+            tmem_st32(t_s, p);
             l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[g]);
+            if (lane == 0) mbar_arrive(&p_full[2 * g + (i & 1)]);
         }
-        if (ok && n > 0) {
-            ok = wait(&o_done[g], (n - 1) & 1);
+        if (ok && n > 0) {                          // the last scores came after the product of n - 3: one phase after the other
+            ok = (n == 1 || wait(&o_done[g], n & 1)) && wait(&o_done[g], (n - 1) & 1);
             tc_fence_after();
         }
         if (ok && a.splits > 1) {
@@ -453,11 +449,11 @@ long long units(const gdn_page_cache *c, const gdn_attn_dims *d) {
     return static_cast<long long>(d->B) * c->Hkv * ((row_tiles(c, d) + 1) / 2) * (c->d == 256 ? 2 : 1);
 }
 // Parts of the key axis: the waves of CTAs times a part's share, plus a tenth of a unit for each part's beginning, end and
-// join; at least four tiles of keys each, as far as a sequence can be long.
+// join; at least 512 keys each, as far as a sequence can be long.
 int best_splits(const gdn_page_cache *c, const gdn_attn_dims *d) {
     const long long u = units(c, d), sms = sm_count();
     if (u >= 4 * sms || sms < 1) return 1;
-    const int keys = 4 * (c->d == 256 ? 64 : 128);
+    const int keys = 512;
     long long most = (static_cast<long long>(c->max_pages) * c->page + keys - 1) / keys;
     if (most > kMaxSplits) most = kMaxSplits;
     int best = 1;
