@@ -546,6 +546,7 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const uint64_t dS = desc_mn_sw128(saddr(smem) + P::OFF_S, P::S_BYTES), dX = desc_mn_sw128(saddr(smem) + P::OFF_X, P::X_BYTES);
         const uint64_t dA = desc_sw128(saddr(smem));
         constexpr uint32_t id = idesc_mn(1, 128, P::N) | kIdescMnMajorB;
+        const uint32_t one = elect_one();
         bool ok = true;
         int c = 0;
         for (; c < chunks; ++c) {
@@ -554,29 +555,23 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (!ok) break;
             tc_fence_after();
             const uint64_t kq = desc_add(dA, st * P::STAGE), e = desc_add(kq, P::KQ), mp = desc_add(e, 2 * Unit<DK>::E_BYTES - 8192);
-            if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_bf16(tm, desc_add(kq, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dS, ks * 2048), id, ks > 0);
-                mma_commit(d1);
-                mma_commit(&empty_k[st]);
-            }
-            __syncwarp();
+            for (int ks = 0; ks < DK / 16; ++ks)
+                mma_bf16_on(one, tm, desc_add(kq, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dS, ks * 2048), id, ks > 0);
+            mma_commit_on(one, d1);
+            mma_commit_on(one, &empty_k[st]);
             ok = wait(&full_e[st], (c >> 1) & 1) && wait(x_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)      // the first terms of E, then the second ones
-                    mma_bf16(tm + P::N, desc_add(e, (ks >> 2) * Unit<DK>::E_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
-                mma_commit(d2);
+            for (int ks = 0; ks < 8; ++ks)          // the first terms of E, then the second ones
+                mma_bf16_on(one, tm + P::N, desc_add(e, (ks >> 2) * Unit<DK>::E_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
+            mma_commit_on(one, d2);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_bf16(tm + 2 * P::N, desc_add(mp, (ks >> 2) * Unit<DK>::MP_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
-                mma_commit(d3);
-                mma_commit(&empty_e[st]);
-            }
-            __syncwarp();
+            for (int ks = 0; ks < 8; ++ks)
+                mma_bf16_on(one, tm + 2 * P::N, desc_add(mp, (ks >> 2) * Unit<DK>::MP_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
+            mma_commit_on(one, d3);
+            mma_commit_on(one, &empty_e[st]);
         }
         if (!ok && c > 0) {                         // MMAs in flight end before their memory is given back
             if (elect_one()) mma_commit(drain);

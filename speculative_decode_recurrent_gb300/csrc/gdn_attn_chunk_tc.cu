@@ -214,19 +214,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         constexpr uint32_t idS = idesc_mn(1, kRows, KT), idO = idesc_mn(1, kRows, DV) | kIdescMnMajorB;
         int ks = 0, kr = 0, vs = 0, vr = 0;         // stages of the next keys and values, and their rounds
         bool issued = false;
+        const uint32_t one = elect_one();
         auto scores = [&](int i) -> bool {          // Q K^T of tile i into buffer i % 2
             if (!wait(&k_full[ks], kr & 1)) return false;
             tc_fence_after();
             const uint64_t kd = desc_add(dk0, ks * P::K_BYTES);
-            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_bf16(t_s + (i & 1) * KT, desc_add(dq, (k >> 2) * (kRows * 128) + (k & 3) * 32),
-                             desc_add(kd, (k >> 2) * (KT * 128) + (k & 3) * 32), idS, k > 0);
-                mma_commit(&s_full[2 * g + (i & 1)]);
-                mma_commit(&k_empty[ks]);
-            }
-            __syncwarp();
+            for (int k = 0; k < D / 16; ++k)
+                mma_bf16_on(one, t_s + (i & 1) * KT, desc_add(dq, (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                            desc_add(kd, (k >> 2) * (KT * 128) + (k & 3) * 32), idS, k > 0);
+            mma_commit_on(one, &s_full[2 * g + (i & 1)]);
+            mma_commit_on(one, &k_empty[ks]);
             issued = true;
             if (++ks == P::NK) ks = 0, ++kr;
             return true;
@@ -238,14 +236,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
             tc_fence_after();
             const uint64_t vd = desc_add(dv0, vs * P::V_BYTES);
-            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < KT / 16; ++k)   // P_i V_i
-                    mma_bf16_ts(t_o, t_s + (i & 1) * KT + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
-                mma_commit(&o_done[g]);
-                mma_commit(&v_empty[vs]);
-            }
-            __syncwarp();
+            for (int k = 0; k < KT / 16; ++k)       // P_i V_i
+                mma_bf16_ts_on(one, t_o, t_s + (i & 1) * KT + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+            mma_commit_on(one, &o_done[g]);
+            mma_commit_on(one, &v_empty[vs]);
             if (++vs == P::NV) vs = 0, ++vr;
             if (i + 2 < n) ok = scores(i + 2);
         }
