@@ -7,16 +7,19 @@
 // which over a row's keys adds about as much as rounding the output does (two terms, as the verify of drafts takes
 // them, would make the second product, half of all the work here, twice as long).  l is the sum of the weights in fp32.
 //
-// What bounds it: the MMAs.  A CTA has two tiles of 128 rows (row r = t G + g: tokens times the query heads of a key
-// head) whose softmaxes and products overlap, and each tile has two score buffers, so that the next keys'
-// scores are there when a softmax ends (one buffer of twice the keys left the tensor cores waiting for a third of the
-// time: softmax, weights, scores one after the other in 3500 cycles for 2144 of MMAs).
+// What bounds it: the MMAs, and shared memory with them (an MMA of 128 rows by 128 keys takes 63 cycles with 64 of reads, one of
+// 64 keys 47 instead of 32).  A CTA has two tiles of 128 rows (row r = t G + g: tokens times the query heads of a key
+// head) whose softmaxes and products overlap.  Tiles of 128 keys leave TMEM for one score buffer of each row tile, so a
+// tile's softmax, its weights' product and the next scores follow one another: the weights go to their product in
+// halves, so that the first half's runs while the second is computed.  (Whole: 3500 cycles for the 2000 of a pair's
+// MMAs; tiles of 64 keys in two buffers: 2 x 1770.)
 //
-// Roles.  Two groups of 128 threads, one per row (no exchange between lanes; the scores of a row are in registers), and
-// for each group a warp that issues: O += P_i V_i, then the scores of tile i + 2 into the buffer that held P_i (the weights go
-// over the scores in TMEM and are the A operand from there; the order of issue keeps the two apart).  A warp each loads
-// keys and values (TMA through the block table).  d 256: the sums of 256 columns of two row tiles leave no room for
-// scores, so a CTA takes 128 columns of the values and both halves form the scores.
+// Roles.  Two groups of 128 threads, one per row (no exchange between lanes; the scores of a row are in registers); a
+// warp that issues, for each group in turn, O += P_i V_i, then the scores of the next tile into the buffer that held P_i (the
+// weights go over the scores in TMEM and are the A operand from there; the order of issue keeps the two apart); a warp each
+// that loads keys and values (TMA through the block table).  d 256: the sums of 256 columns of two row tiles leave no room for
+// scores, so a CTA takes 128 columns of the values and both halves form the scores; its tiles of 64 keys (shared
+// memory holds no larger ones) have two buffers.
 //
 // Work.  A CTA is (pair of row tiles, key head, sequence, part of the keys); the longest come first.  Keys are cut
 // into parts where the pairs alone would leave SMs without work (best_splits), joined by gdn_attn_chunk.cu.
@@ -37,14 +40,15 @@ constexpr int kMaxSplits = 64;
 
 template <int D> struct Plan {
     static constexpr int DV = D == 256 ? 128 : D;   // value columns of a CTA
-    static constexpr int KT = 64;                   // keys of a tile
-    static constexpr int NK = D == 64 ? 8 : D == 128 ? 5 : 2, NV = NK;                   // stages
+    static constexpr int KT = D == 256 ? 64 : 128, NB = D == 256 ? 2 : 1;      // keys of a tile, score buffers
+    static constexpr int PH = KT / 64;              // parts of a tile's weights
+    static constexpr int NK = D == 64 ? 5 : D == 128 ? 3 : 2, NV = D == 64 ? 4 : 2;      // stages
     static constexpr int QA = D / 64, VA = DV / 64; // 64-column atoms of 128-byte rows
     static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = KT * D * 2, V_BYTES = KT * DV * 2;
     static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NK * K_BYTES, OFF_BAR = OFF_V + NV * V_BYTES;
     static constexpr int BYTES = OFF_BAR + 512;
-    static constexpr int LOAD_WARP = 8, MMA_WARP = 10, THREADS = 12 * 32;
-    static constexpr int COL_S = 0, COL_O = 4 * KT; // TMEM: two score buffers of each row tile, then their sums
+    static constexpr int LOAD_WARP = 8, MMA_WARP = 10, THREADS = 11 * 32;
+    static constexpr int COL_S = 0, COL_O = 2 * NB * KT;       // TMEM: the score buffers of each row tile, then their sums
     static_assert(COL_O + 2 * DV <= 512 && BYTES <= 227 * 1024, "plan");
 };
 
@@ -68,8 +72,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const int part = id % a.splits, pairs = (a.row_tiles + 1) / 2, rt0 = (pairs - 1 - id / a.splits) * 2;      // long ones first
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *k_empty = k_full + P::NK, *v_full = k_empty + P::NK,
              *v_empty = v_full + P::NV, *q_full = v_empty + P::NV, *s_full = q_full + 1, *p_full = s_full + 4, *o_done = p_full + 4,
-             *drain = o_done + 2;                   // s_full, p_full [group][buffer]; o_done, drain [group]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
+             *drain = o_done + 2;                   // s_full [group][buffer], p_full [group][buffer or part]; o_done [group]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     static_assert((2 * P::NK + 2 * P::NV + 13) * 8 + 8 <= 512, "barriers");
     if (saddr(smem) & 1023u) {
@@ -79,21 +83,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (tid == 0) {
         for (int i = 0; i < P::NK; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 2);              // the warps of both groups
+            mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < P::NV; ++i) {
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 2);
+            mbar_init(&v_empty[i], 1);
         }
         mbar_init(q_full, 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&o_done[i], 1);
-            mbar_init(&drain[i], 1);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&o_done[i], 1);
+        mbar_init(drain, 1);
         *abort = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
         fence_mbar_init();
     }
@@ -205,66 +207,77 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int y = max(0, i - ns); y < i; ++y) done = done && mbar_wait(&full[y % ns], (y / ns) & 1);
             if (!done && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
-    } else if (warp >= P::MMA_WARP) {
-        // ------------------------------------------------------ MMAs of a group
-        const int g = __shfl_sync(0xffffffffu, warp - P::MMA_WARP, 0), n = g ? n1 : n0;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), t_s = tm + P::COL_S + g * 2 * KT, t_o = tm + P::COL_O + g * DV;
-        const uint64_t dq = desc_sw128(saddr(smem) + g * P::Q_BYTES), dk0 = desc_sw128(saddr(smem) + P::OFF_K),
+    } else if (warp == P::MMA_WARP) {
+        // ------------------------------------------------------ MMAs
+        // One warp for both groups, so that a group's products and its next scores run without the other's
+        // between them: the groups' softmaxes then fall into turns (issued by a warp each, they ran side by side, and
+        // the tensor cores waited).
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq = desc_sw128(saddr(smem)), dk0 = desc_sw128(saddr(smem) + P::OFF_K),
                        dv0 = desc_mn_sw128(saddr(smem) + P::OFF_V, KT * 128);
         constexpr uint32_t idS = idesc_mn(1, kRows, KT), idO = idesc_mn(1, kRows, DV) | kIdescMnMajorB;
-        int ks = 0, kr = 0, vs = 0, vr = 0;         // stages of the next keys and values, and their rounds
-        bool issued = false;
         const uint32_t one = elect_one();
-        auto scores = [&](int i) -> bool {          // Q K^T of tile i into buffer i % 2
-            if (!wait(&k_full[ks], kr & 1)) return false;
-            tc_fence_after();
-            const uint64_t kd = desc_add(dk0, ks * P::K_BYTES);
+        bool issued = false;
+        auto scores = [&](int g, int i, int ks) {   // Q_g K^T of tile i (stage ks) into buffer i % NB
+            const uint64_t qd = desc_add(dq, g * P::Q_BYTES), kd = desc_add(dk0, ks * P::K_BYTES);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                mma_bf16_on(one, t_s + (i & 1) * KT, desc_add(dq, (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                mma_bf16_on(one, tm + P::COL_S + (g * P::NB + i % P::NB) * KT, desc_add(qd, (k >> 2) * (kRows * 128) + (k & 3) * 32),
                             desc_add(kd, (k >> 2) * (KT * 128) + (k & 3) * 32), idS, k > 0);
-            mma_commit_on(one, &s_full[2 * g + (i & 1)]);
-            mma_commit_on(one, &k_empty[ks]);
+            mma_commit_on(one, &s_full[2 * g + i % P::NB]);
             issued = true;
-            if (++ks == P::NK) ks = 0, ++kr;
-            return true;
         };
-        bool ok = n == 0 || wait(q_full, 0);
-        for (int i = 0; ok && i < min(n, 2); ++i) ok = scores(i);
-        for (int i = 0; ok && i < n; ++i) {
-            ok = wait(&v_full[vs], vr & 1) && wait(&p_full[2 * g + (i & 1)], (i >> 1) & 1);
+        bool ok = count == 0 || wait(q_full, 0);
+        int ks = 0, kr = 0, vs = 0, vr = 0;         // stages of the next keys and values, and their rounds
+        auto next_keys = [&]() {
+            mma_commit_on(one, &k_empty[ks]);
+            if (++ks == P::NK) ks = 0, ++kr;
+        };
+        for (int i = 0; ok && i < min(count, P::NB); ++i) {
+            ok = wait(&k_full[ks], kr & 1);
             if (!ok) break;
             tc_fence_after();
+            if (i < n0) scores(0, i, ks);
+            if (i < n1) scores(1, i, ks);
+            next_keys();
+        }
+        for (int i = 0; ok && i < count; ++i) {
+            const int j = i + P::NB;                // the tile whose scores follow
+            ok = wait(&v_full[vs], vr & 1) && (j >= count || wait(&k_full[ks], kr & 1));
+            if (!ok) break;
             const uint64_t vd = desc_add(dv0, vs * P::V_BYTES);
 #pragma unroll
-            for (int k = 0; k < KT / 16; ++k)       // P_i V_i
-                mma_bf16_ts_on(one, t_o, t_s + (i & 1) * KT + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
-            mma_commit_on(one, &o_done[g]);
+            for (int g = 0; g < 2; ++g) {
+                if (i >= (g ? n1 : n0)) continue;
+#pragma unroll
+                for (int h2 = 0; h2 < P::PH; ++h2) {                  // O_g += P_i V_i
+                    ok = ok && wait(&p_full[2 * g + (P::NB == 2 ? i & 1 : h2)], (P::NB == 2 ? i >> 1 : i) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 4 * h2; k < 4 * h2 + 4; ++k)
+                        mma_bf16_ts_on(one, tm + P::COL_O + g * DV, tm + P::COL_S + (g * P::NB + i % P::NB) * KT + k * 8,
+                                       desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+                }
+                if (!ok) break;
+                mma_commit_on(one, &o_done[g]);
+                if (j < (g ? n1 : n0)) scores(g, j, ks);
+            }
+            if (!ok) break;
             mma_commit_on(one, &v_empty[vs]);
             if (++vs == P::NV) vs = 0, ++vr;
-            if (i + 2 < n) ok = scores(i + 2);
-        }
-        // tiles that only the other group sees: passed on once they are there (an arrival before that would count
-        // for the round before)
-        for (int i = n; ok && i < count; ++i) {
-            ok = wait(&k_full[ks], kr & 1);
-            if (ok && lane == 0) mbar_arrive(&k_empty[ks]);
-            if (++ks == P::NK) ks = 0, ++kr;
-            ok = ok && wait(&v_full[vs], vr & 1);
-            if (ok && lane == 0) mbar_arrive(&v_empty[vs]);
-            if (++vs == P::NV) vs = 0, ++vr;
+            if (j < count) next_keys();
         }
         if (!ok && issued) {                        // MMAs in flight end before their memory is given back
-            if (elect_one()) mma_commit(&drain[g]);
-            __syncwarp();
-            if (!mbar_wait(&drain[g], 0) && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
+            mma_commit_on(one, drain);
+            if (!mbar_wait(drain, 0) && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
     } else {
         // ------------------------------------------------------ rows
         const int g = warp >> 2, r = tid & 127, n = g ? n1 : n0;
         const int tg = t0 + g * a.tpt;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t t_s0 = tmem + lanes + P::COL_S + g * 2 * KT, t_o = tmem + lanes + P::COL_O + g * DV;
+        const uint32_t t_s0 = tmem + lanes + P::COL_S + g * (P::NB * KT), t_o = tmem + lanes + P::COL_O + g * DV;
         const bool used = r < (g ? live[1] : live[0]);
         const int lim = used ? sq.len + tg + r / G + 1 : 0;           // keys that this row sees
         const int free_to = sq.len + tg + 1;                          // keys that every row in use sees
@@ -286,8 +299,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 fence_proxy_async();
             }
-            const uint32_t t_s = t_s0 + (i & 1) * KT;
-            if (!(ok = wait(&s_full[2 * g + (i & 1)], (i >> 1) & 1))) break;
+            const uint32_t t_s = t_s0 + i % P::NB * KT;
+            if (!(ok = wait(&s_full[2 * g + i % P::NB], (i / P::NB) & 1))) break;
             tc_fence_after();
             uint32_t x[KT];
 #pragma unroll
@@ -330,24 +343,27 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const float ms = m == -INFINITY ? 0.f : m;
             const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-ms, -ms);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            uint32_t p[KT / 2];
 #pragma unroll
-            for (int k = 0; k < KT / 2; ++k) {
-                float2 e = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc, mm);
-                e = make_float2(ex2(e.x), ex2(e.y));
-                sum[k & 1] = add2(sum[k & 1], e);
-                const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
-                p[k] = *reinterpret_cast<const uint32_t *>(&w);
+            for (int h2 = 0; h2 < P::PH; ++h2) {
+                uint32_t p[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    float2 e = fma2(make_float2(__uint_as_float(x[64 * h2 + 2 * k]), __uint_as_float(x[64 * h2 + 2 * k + 1])), sc, mm);
+                    e = make_float2(ex2(e.x), ex2(e.y));
+                    sum[k & 1] = add2(sum[k & 1], e);
+                    const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
+                    p[k] = *reinterpret_cast<const uint32_t *>(&w);
+                }
+                tmem_st32(t_s + 32 * h2, p);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * g + (P::NB == 2 ? i & 1 : h2)]);
             }
-            tmem_st32(t_s, p);
             l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * g + (i & 1)]);
         }
-        if (ok && n > 0) {                          // the last scores came after the product of n - 3: one phase after the other
-            ok = (n == 1 || wait(&o_done[g], n & 1)) && wait(&o_done[g], (n - 1) & 1);
+        if (ok && n > 0) {                          // the last scores came after the product of NB + 1 tiles before: one phase after the other
+            ok = (P::NB == 1 || n == 1 || wait(&o_done[g], n & 1)) && wait(&o_done[g], (n - 1) & 1);
             tc_fence_after();
         }
         if (ok && a.splits > 1) {
