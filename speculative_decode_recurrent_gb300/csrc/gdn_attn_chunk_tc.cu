@@ -14,10 +14,10 @@
 // halves, so that the first half's runs while the second is computed.  (Whole: 3500 cycles for the 2000 of a pair's
 // MMAs; tiles of 64 keys in two buffers: 2 x 1770.)
 //
-// Roles.  Two groups of 128 threads, one per row (no exchange between lanes; the scores of a row are in registers); a
-// warp that issues, for each group in turn, O += P_i V_i, then the scores of the next tile into the buffer that held P_i (the
-// weights go over the scores in TMEM and are the A operand from there; the order of issue keeps the two apart); a warp each
-// that loads keys and values (TMA through the block table).  d 256: the sums of 256 columns of two row tiles leave no room for
+// Roles.  Two groups of 128 threads, one per row (no exchange between lanes; the scores of a row are in registers), and
+// for each group a warp that issues: O += P_i V_i, then the scores of the next tile into the buffer that held P_i (the weights
+// go over the scores in TMEM and are the A operand from there; the order of issue keeps the two apart).  A warp each loads
+// keys and values (TMA through the block table).  d 256: the sums of 256 columns of two row tiles leave no room for
 // scores, so a CTA takes 128 columns of the values and both halves form the scores; its tiles of 64 keys (shared
 // memory holds no larger ones) have two buffers.
 //
@@ -41,13 +41,12 @@ constexpr int kMaxSplits = 64;
 template <int D> struct Plan {
     static constexpr int DV = D == 256 ? 128 : D;   // value columns of a CTA
     static constexpr int KT = D == 256 ? 64 : 128, NB = D == 256 ? 2 : 1;      // keys of a tile, score buffers
-    static constexpr int PH = KT / 64;              // parts of a tile's weights
     static constexpr int NK = D == 64 ? 5 : D == 128 ? 3 : 2, NV = D == 64 ? 4 : 2;      // stages
     static constexpr int QA = D / 64, VA = DV / 64; // 64-column atoms of 128-byte rows
     static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = KT * D * 2, V_BYTES = KT * DV * 2;
-    static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NK * K_BYTES, OFF_BAR = OFF_V + NV * V_BYTES;
-    static constexpr int BYTES = OFF_BAR + 512;
-    static constexpr int LOAD_WARP = 8, MMA_WARP = 10, THREADS = 11 * 32;
+    static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NK * K_BYTES, OFF_XCH = OFF_V + NV * V_BYTES;
+    static constexpr int OFF_BAR = OFF_XCH + 512 * 4, BYTES = OFF_BAR + 512;
+    static constexpr int LOAD_WARP = 16, MMA_WARP = 18, THREADS = 20 * 32;
     static constexpr int COL_S = 0, COL_O = 2 * NB * KT;       // TMEM: the score buffers of each row tile, then their sums
     static_assert(COL_O + 2 * DV <= 512 && BYTES <= 227 * 1024, "plan");
 };
@@ -72,10 +71,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const int part = id % a.splits, pairs = (a.row_tiles + 1) / 2, rt0 = (pairs - 1 - id / a.splits) * 2;      // long ones first
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *k_empty = k_full + P::NK, *v_full = k_empty + P::NK,
              *v_empty = v_full + P::NV, *q_full = v_empty + P::NV, *s_full = q_full + 1, *p_full = s_full + 4, *o_done = p_full + 4,
-             *drain = o_done + 2;                   // s_full [group][buffer], p_full [group][buffer or part]; o_done [group]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+             *turn = o_done + 2, *drain = turn + 2;                 // s_full [group][buffer], p_full [group][buffer]; o_done, turn, drain [group]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((2 * P::NK + 2 * P::NV + 13) * 8 + 8 <= 512, "barriers");
+    static_assert((2 * P::NK + 2 * P::NV + 15) * 8 + 8 <= 512, "barriers");
     if (saddr(smem) & 1023u) {
         if (tid == 0) atomicOr(a.s.status, kStatusTimeout);
         return;
@@ -83,19 +82,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (tid == 0) {
         for (int i = 0; i < P::NK; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
+            mbar_init(&k_empty[i], 2);              // the warps of both groups
         }
         for (int i = 0; i < P::NV; ++i) {
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&v_empty[i], 2);
         }
         mbar_init(q_full, 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], 8);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&o_done[i], 1);
-        mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&o_done[i], 1);
+            mbar_init(&turn[i], 1);
+            mbar_init(&drain[i], 1);
+        }
         *abort = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
         fence_mbar_init();
     }
@@ -207,82 +209,88 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int y = max(0, i - ns); y < i; ++y) done = done && mbar_wait(&full[y % ns], (y / ns) & 1);
             if (!done && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
-    } else if (warp == P::MMA_WARP) {
-        // ------------------------------------------------------ MMAs
-        // One warp for both groups, so that a group's products and its next scores run without the other's
-        // between them: the groups' softmaxes then fall into turns (issued by a warp each, they ran side by side, and
-        // the tensor cores waited).
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t dq = desc_sw128(saddr(smem)), dk0 = desc_sw128(saddr(smem) + P::OFF_K),
+    } else if (warp >= P::MMA_WARP) {
+        // ------------------------------------------------------ MMAs of a group
+        // Issuing holds a warp up until its MMAs have nearly run, and each wait on a barrier costs it some 300 cycles, which
+        // one warp for both groups left the tensor cores idle.  Each group's warp waits while the other's MMAs
+        // run; a group's last product and its next scores go in one piece, in turns (`turn`), so that the groups' softmaxes
+        // stay half a period apart (without turns they fall into step, and both wait for the tensor cores at once).
+        const int g = __shfl_sync(0xffffffffu, warp - P::MMA_WARP, 0), n = g ? n1 : n0;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), t_s = tm + P::COL_S + g * (P::NB * KT), t_o = tm + P::COL_O + g * DV;
+        const uint64_t dq = desc_sw128(saddr(smem) + g * P::Q_BYTES), dk0 = desc_sw128(saddr(smem) + P::OFF_K),
                        dv0 = desc_mn_sw128(saddr(smem) + P::OFF_V, KT * 128);
         constexpr uint32_t idS = idesc_mn(1, kRows, KT), idO = idesc_mn(1, kRows, DV) | kIdescMnMajorB;
         const uint32_t one = elect_one();
+        int ks = 0, kr = 0, vs = 0, vr = 0;         // stages of the next keys and values, and their rounds
         bool issued = false;
-        auto scores = [&](int g, int i, int ks) {   // Q_g K^T of tile i (stage ks) into buffer i % NB
-            const uint64_t qd = desc_add(dq, g * P::Q_BYTES), kd = desc_add(dk0, ks * P::K_BYTES);
+        auto scores = [&](int i) {                  // Q K^T of tile i, whose keys are there, into buffer i % NB
+            const uint64_t kd = desc_add(dk0, ks * P::K_BYTES);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                mma_bf16_on(one, tm + P::COL_S + (g * P::NB + i % P::NB) * KT, desc_add(qd, (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                mma_bf16_on(one, t_s + i % P::NB * KT, desc_add(dq, (k >> 2) * (kRows * 128) + (k & 3) * 32),
                             desc_add(kd, (k >> 2) * (KT * 128) + (k & 3) * 32), idS, k > 0);
             mma_commit_on(one, &s_full[2 * g + i % P::NB]);
             issued = true;
         };
-        bool ok = count == 0 || wait(q_full, 0);
-        int ks = 0, kr = 0, vs = 0, vr = 0;         // stages of the next keys and values, and their rounds
-        auto next_keys = [&]() {
-            mma_commit_on(one, &k_empty[ks]);
+        // A tile that only the other group sees is passed on once it is there (an arrival before that would count for
+        // the round before).
+        auto free_keys = [&](int i) {
+            if (i < n) mma_commit_on(one, &k_empty[ks]);
+            else if (lane == 0) mbar_arrive(&k_empty[ks]);
             if (++ks == P::NK) ks = 0, ++kr;
         };
+        bool ok = count == 0 || wait(q_full, 0);
         for (int i = 0; ok && i < min(count, P::NB); ++i) {
             ok = wait(&k_full[ks], kr & 1);
             if (!ok) break;
             tc_fence_after();
-            if (i < n0) scores(0, i, ks);
-            if (i < n1) scores(1, i, ks);
-            next_keys();
+            if (i < n) scores(i);
+            free_keys(i);
         }
         for (int i = 0; ok && i < count; ++i) {
             const int j = i + P::NB;                // the tile whose scores follow
             ok = wait(&v_full[vs], vr & 1) && (j >= count || wait(&k_full[ks], kr & 1));
-            if (!ok) break;
             const uint64_t vd = desc_add(dv0, vs * P::V_BYTES);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (i >= (g ? n1 : n0)) continue;
-#pragma unroll
-                for (int h2 = 0; h2 < P::PH; ++h2) {                  // O_g += P_i V_i
-                    ok = ok && wait(&p_full[2 * g + (P::NB == 2 ? i & 1 : h2)], (P::NB == 2 ? i >> 1 : i) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 4 * h2; k < 4 * h2 + 4; ++k)
-                        mma_bf16_ts_on(one, tm + P::COL_O + g * DV, tm + P::COL_S + (g * P::NB + i % P::NB) * KT + k * 8,
-                                       desc_add(vd, k * 2048), idO, i > 0 || k > 0);
-                }
-                if (!ok) break;
-                mma_commit_on(one, &o_done[g]);
-                if (j < (g ? n1 : n0)) scores(g, j, ks);
-            }
+            if (i < n) ok = ok && wait(&p_full[2 * g + i % P::NB], (i / P::NB) & 1);
+            ok = ok && ((g == 0 && i == 0) || wait(&turn[g], (g ? i : i - 1) & 1));
             if (!ok) break;
-            mma_commit_on(one, &v_empty[vs]);
+            tc_fence_after();
+            if (i < n) {
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)   // O += P_i V_i
+                    mma_bf16_ts_on(one, t_o, t_s + i % P::NB * KT + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+            }
+            if (i < n) {
+                mma_commit_on(one, &o_done[g]);
+                mma_commit_on(one, &v_empty[vs]);
+            } else if (lane == 0) {
+                mbar_arrive(&v_empty[vs]);
+            }
             if (++vs == P::NV) vs = 0, ++vr;
-            if (j < count) next_keys();
+            if (j < n) scores(j);
+            if (lane == 0) mbar_arrive(&turn[g ^ 1]);
+            if (j < count) free_keys(j);
+            __syncwarp();
         }
         if (!ok && issued) {                        // MMAs in flight end before their memory is given back
-            mma_commit_on(one, drain);
-            if (!mbar_wait(drain, 0) && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
+            mma_commit_on(one, &drain[g]);
+            if (!mbar_wait(&drain[g], 0) && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
     } else {
         // ------------------------------------------------------ rows
-        const int g = warp >> 2, r = tid & 127, n = g ? n1 : n0;
+        // Thread (group, half of a tile's keys and of the output's columns, row).  An expired wait only stops the waiting
+        // (a thread that left would leave its pair at a barrier).
+        const int g = warp >> 3, kh = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, n = g ? n1 : n0, pair_id = 1 + g * 4 + (warp & 3);
+        constexpr int KH = KT / 2, DH = DV / 2;
         const int tg = t0 + g * a.tpt;
+        float *xch = reinterpret_cast<float *>(smem + P::OFF_XCH);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t t_s0 = tmem + lanes + P::COL_S + g * (P::NB * KT), t_o = tmem + lanes + P::COL_O + g * DV;
+        const uint32_t t_s0 = tmem + lanes + P::COL_S + g * (P::NB * KT), t_o = tmem + lanes + P::COL_O + g * DV + kh * DH;
         const bool used = r < (g ? live[1] : live[0]);
         const int lim = used ? sq.len + tg + r / G + 1 : 0;           // keys that this row sees
         const int free_to = sq.len + tg + 1;                          // keys that every row in use sees
         const bool whole = (g ? live[1] : live[0]) == kRows;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f;               // m: the same in both threads of a row; l: of this one's keys
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int j0 = (first + i) * KT;
@@ -290,9 +298,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 // values past the last token hold anything: zeros in their place (by both groups, each before its weights
                 // go to their product)
                 const int vst = i % P::NV;
-                if (!(ok = wait(&v_full[vst], (i / P::NV) & 1))) break;
+                ok = wait(&v_full[vst], (i / P::NV) & 1) && ok;
                 const int from = max(0, total - j0);
-                for (int e = r + from * (DV / 8); e < KT * (DV / 8); e += 128) {
+                for (int e = (tid & 255) + from * (DV / 8); e < KT * (DV / 8); e += 256) {
                     const int row = e / (DV / 8), c = e % (DV / 8);
                     *reinterpret_cast<uint4 *>(smem + P::OFF_V + vst * P::V_BYTES + (c >> 3) * (KT * 128) + sw128(row, c & 7)) =
                         make_uint4(0u, 0u, 0u, 0u);
@@ -300,43 +308,48 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 fence_proxy_async();
             }
             const uint32_t t_s = t_s0 + i % P::NB * KT;
-            if (!(ok = wait(&s_full[2 * g + i % P::NB], (i / P::NB) & 1))) break;
+            ok = wait(&s_full[2 * g + i % P::NB], (i / P::NB) & 1) && ok;
             tc_fence_after();
-            uint32_t x[KT];
+            uint32_t x[KH / 32][32];
 #pragma unroll
-            for (int c = 0; c < KT; c += 32) tmem_ld32(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
+            for (int c = 0; c < KH / 32; ++c) tmem_ld32(t_s + kh * KH + 32 * c, x[c]);
             tmem_wait_ld();
             if (!whole || j0 + KT > free_to) {
-                const int seen = lim - j0;
+                const int seen = lim - j0 - kh * KH;
 #pragma unroll
-                for (int k = 0; k < KT; ++k) x[k] = k < seen ? x[k] : 0xff800000u;
+                for (int k = 0; k < KH; ++k) x[k >> 5][k & 31] = k < seen ? x[k >> 5][k & 31] : 0xff800000u;
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int k = 0; k < KT; k += 8)
+            for (int k = 0; k < KH; k += 8)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    top[q] = fmaxf(top[q], fmaxf(__uint_as_float(x[k + 2 * q]), __uint_as_float(x[k + 2 * q + 1])));
+                    top[q] = fmaxf(top[q], fmaxf(__uint_as_float(x[k >> 5][(k & 31) + 2 * q]), __uint_as_float(x[k >> 5][(k & 31) + 2 * q + 1])));
             const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-            if (__any_sync(0xffffffffu, mt > m + 8.f)) {
+            // (also: both threads of each row have read their scores, which the weights go over)
+            if (pair_any(pair_id, mt > m + 8.f)) {
+                xch[tid] = mt;
+                bar_sync(pair_id, 64);
+                const float mp = fmaxf(mt, xch[tid ^ 128]);
+                bar_sync(pair_id, 64);              // read before it is written again
                 float fac = 1.f;
-                if (mt > m + 8.f) {
-                    fac = ex2(m - mt);              // 0 when nothing was summed
-                    m = mt;
+                if (mp > m + 8.f) {
+                    fac = ex2(m - mp);              // 0 when nothing was summed
+                    m = mp;
                     l *= fac;
                 }
                 if (i > 0) {                        // the sums so far: their last product must be done (the one before it
                                                     // is, as its weights' buffer holds these scores)
-                    if (!(ok = wait(&o_done[g], (i - 1) & 1))) break;
+                    ok = wait(&o_done[g], (i - 1) & 1) && ok;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < DV; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + c, o);
+                    for (int c = 0; c < DH; c += 8) {                 // (few at a time: the scores stay in registers)
+                        uint32_t o[8];
+                        tmem_load8(t_o + c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
-                        tmem_st32(t_o + c, o);
+                        for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
+                        tmem_store8(t_o + c, o);
                     }
                 }
             }
@@ -344,63 +357,57 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-ms, -ms);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int h2 = 0; h2 < P::PH; ++h2) {
-                uint32_t p[32];
+            for (int c = 0; c < KH / 32; ++c) {
+                uint32_t p[16];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float2 e = fma2(make_float2(__uint_as_float(x[64 * h2 + 2 * k]), __uint_as_float(x[64 * h2 + 2 * k + 1])), sc, mm);
+                for (int k = 0; k < 16; ++k) {
+                    float2 e = fma2(make_float2(__uint_as_float(x[c][2 * k]), __uint_as_float(x[c][2 * k + 1])), sc, mm);
                     e = make_float2(ex2(e.x), ex2(e.y));
                     sum[k & 1] = add2(sum[k & 1], e);
                     const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
                     p[k] = *reinterpret_cast<const uint32_t *>(&w);
                 }
-                tmem_st32(t_s + 32 * h2, p);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * g + (P::NB == 2 ? i & 1 : h2)]);
+                tmem_st16(t_s + kh * (KH / 2) + 16 * c, p);
             }
             l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * g + i % P::NB]);
         }
-        if (ok && n > 0) {                          // the last scores came after the product of NB + 1 tiles before: one phase after the other
-            ok = (P::NB == 1 || n == 1 || wait(&o_done[g], n & 1)) && wait(&o_done[g], (n - 1) & 1);
+        if (n > 0) {                                // the last scores came after the product of NB + 1 tiles before: one phase after the other
+            ok = (P::NB == 1 || n == 1 || wait(&o_done[g], n & 1)) && wait(&o_done[g], (n - 1) & 1) && ok;
             tc_fence_after();
         }
-        if (ok && a.splits > 1) {
+        xch[tid] = l;
+        bar_sync(pair_id, 64);
+        l += xch[tid ^ 128];
+        const int rows = min(a.tpt, a.s.T - tg) * G, c0 = half * DV + kh * DH;          // this thread's first output column
+        if (ok && a.splits > 1 && (g ? live[1] : live[0]) > 0) {
             const size_t unit = (static_cast<size_t>(b) * Hkv + h) * a.row_tiles + rt0 + g;
             float *w = a.ws + (unit * a.splits + part) * (static_cast<size_t>(kRows) * (D + 2));
-            if ((g ? live[1] : live[0]) > 0) {
-                if (n > 0)
+            if (n > 0)
 #pragma unroll 1
-                    for (int c = 0; c < DV; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + c, o);
-                        tmem_wait_ld();
-                        float4 *dst = reinterpret_cast<float4 *>(w + static_cast<size_t>(r) * D + half * DV + c);
+                for (int c = 0; c < DH; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + c, o);
+                    tmem_wait_ld();
+                    float4 *dst = reinterpret_cast<float4 *>(w + static_cast<size_t>(r) * D + c0 + c);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
-                                                 __uint_as_float(o[4 * k + 3]));
-                    }
-                if (half == 0) {
-                    w[static_cast<size_t>(kRows) * D + r] = m;
-                    w[static_cast<size_t>(kRows) * (D + 1) + r] = l;
+                    for (int k = 0; k < 8; ++k)
+                        dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                             __uint_as_float(o[4 * k + 3]));
                 }
-            } else if (part == 0) {                 // (the join passes over a tile without rows in use)
-                const int rows = min(a.tpt, a.s.T - tg) * G;
-                if (r < rows) {
-                    uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row_at(g, r) * D + half * DV);
-                    for (int c = 0; c < DV / 8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
-                    if (a.lse && half == 0) a.lse[row_at(g, r)] = -INFINITY;
-                }
+            if (half == 0 && kh == 0) {
+                w[static_cast<size_t>(kRows) * D + r] = m;
+                w[static_cast<size_t>(kRows) * (D + 1) + r] = l;
             }
-        } else if (ok) {
-            const int rows = min(a.tpt, a.s.T - tg) * G;
+        } else if (ok && (a.splits == 1 || part == 0)) {              // (the join passes over a tile without rows in use)
             const float inv = used ? 1.f / l : 0.f;
             const size_t at = r < rows ? row_at(g, r) : 0;
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + half * DV);
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + c0);
 #pragma unroll 1
-            for (int c = 0; c < DV; c += 32) {
+            for (int c = 0; c < DH; c += 32) {
                 uint32_t o[32];
                 if (n > 0) {
                     tmem_ld32(t_o + c, o);
@@ -419,7 +426,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
                 }
             }
-            if (a.lse && half == 0 && r < rows) a.lse[at] = used ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (a.lse && half == 0 && kh == 0 && r < rows) a.lse[at] = used ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         tc_fence_before();
     }

@@ -90,14 +90,6 @@ struct TcArgs {
 // often: no row warp leaves its loops early (an expired wait only stops the waiting), loop counts
 // and branches around a barrier follow from the share alone or, for a tile's non-finite values, from
 // one word in shared memory that all threads of the barrier read between the same two barriers.
-__device__ __forceinline__ bool pair_any(int id, bool x) {
-    uint32_t any;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(any) : "r"(id), "r"(static_cast<uint32_t>(x)) : "memory");
-    return any != 0;
-}
-
 // ------------------------------------------------------------- the work's layout
 // Units of one (sequence, key head): the row tiles that hold rows in use, in pairs where NQ is 2
 // (`pairs`, then `single`), take every tile of keys; each of the others is one tile without keys (its
