@@ -46,7 +46,7 @@ template <int D> struct Plan {
     static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = KT * D * 2, V_BYTES = KT * DV * 2;
     static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NK * K_BYTES, OFF_XCH = OFF_V + NV * V_BYTES;
     static constexpr int OFF_BAR = OFF_XCH + 512 * 4, BYTES = OFF_BAR + 512;
-    static constexpr int LOAD_WARP = 16, MMA_WARP = 18, THREADS = 20 * 32;
+    static constexpr int MMA_WARP = 0, LOAD_WARP = 2, ROW_WARP = 4, THREADS = 20 * 32;
     static constexpr int COL_S = 0, COL_O = 2 * NB * KT;       // TMEM: the score buffers of each row tile, then their sums
     static_assert(COL_O + 2 * DV <= 512 && BYTES <= 227 * 1024, "plan");
 };
@@ -209,7 +209,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int y = max(0, i - ns); y < i; ++y) done = done && mbar_wait(&full[y % ns], (y / ns) & 1);
             if (!done && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);
         }
-    } else if (warp >= P::MMA_WARP) {
+    } else if (warp < P::LOAD_WARP) {
         // ------------------------------------------------------ MMAs of a group
         // Issuing holds a warp up until its MMAs have nearly run, and each wait on a barrier costs it some 300 cycles, which
         // one warp for both groups left the tensor cores idle.  Each group's warp waits while the other's MMAs
@@ -280,7 +280,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         // ------------------------------------------------------ rows
         // Thread (group, half of a tile's keys and of the output's columns, row).  An expired wait only stops the waiting
         // (a thread that left would leave its pair at a barrier).
-        const int g = warp >> 3, kh = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, n = g ? n1 : n0, pair_id = 1 + g * 4 + (warp & 3);
+        const int rw = warp - P::ROW_WARP, rt = tid - P::ROW_WARP * 32;
+        const int g = rw >> 3, kh = (rw >> 2) & 1, r = (warp & 3) * 32 + lane, n = g ? n1 : n0, pair_id = 1 + g * 4 + (warp & 3);
         constexpr int KH = KT / 2, DH = DV / 2;
         const int tg = t0 + g * a.tpt;
         float *xch = reinterpret_cast<float *>(smem + P::OFF_XCH);
@@ -300,7 +301,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const int vst = i % P::NV;
                 ok = wait(&v_full[vst], (i / P::NV) & 1) && ok;
                 const int from = max(0, total - j0);
-                for (int e = (tid & 255) + from * (DV / 8); e < KT * (DV / 8); e += 256) {
+                for (int e = (rt & 255) + from * (DV / 8); e < KT * (DV / 8); e += 256) {
                     const int row = e / (DV / 8), c = e % (DV / 8);
                     *reinterpret_cast<uint4 *>(smem + P::OFF_V + vst * P::V_BYTES + (c >> 3) * (KT * 128) + sw128(row, c & 7)) =
                         make_uint4(0u, 0u, 0u, 0u);
@@ -328,9 +329,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
             // (also: both threads of each row have read their scores, which the weights go over)
             if (pair_any(pair_id, mt > m + 8.f)) {
-                xch[tid] = mt;
+                xch[rt] = mt;
                 bar_sync(pair_id, 64);
-                const float mp = fmaxf(mt, xch[tid ^ 128]);
+                const float mp = fmaxf(mt, xch[rt ^ 128]);
                 bar_sync(pair_id, 64);              // read before it is written again
                 float fac = 1.f;
                 if (mp > m + 8.f) {
@@ -379,9 +380,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             ok = (P::NB == 1 || n == 1 || wait(&o_done[g], n & 1)) && wait(&o_done[g], (n - 1) & 1) && ok;
             tc_fence_after();
         }
-        xch[tid] = l;
+        xch[rt] = l;
         bar_sync(pair_id, 64);
-        l += xch[tid ^ 128];
+        l += xch[rt ^ 128];
         const int rows = min(a.tpt, a.s.T - tg) * G, c0 = half * DV + kh * DH;          // this thread's first output column
         if (ok && a.splits > 1 && (g ? live[1] : live[0]) > 0) {
             const size_t unit = (static_cast<size_t>(b) * Hkv + h) * a.row_tiles + rt0 + g;
