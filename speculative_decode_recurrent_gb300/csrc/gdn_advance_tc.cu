@@ -491,17 +491,7 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {         // the same answer in a whole warp
-        bool ok = false;
-        for (uint32_t i = 0; i < kWaitLimit && !(ok = mbar_try_wait(bar, parity)); ++i)
-            if (*abort) break;
-        ok = __all_sync(0xffffffffu, ok) != 0;
-        if (!ok && lane == 0 && !*abort) {
-            *abort = 1;
-            atomicOr(a.status, kStatusTimeout);
-        }
-        return ok;
-    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.status); };
     const char *units = a.ws + (static_cast<size_t>(blockIdx.z) * ta.chunks * a.H + h) * Unit<DK>::BYTES;
     const size_t ustep = static_cast<size_t>(a.H) * Unit<DK>::BYTES;
     if (warp == P::LOAD_WARP) {

@@ -141,17 +141,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {         // the same answer in a whole warp
-        bool ok = false;
-        for (uint32_t i = 0; i < kWaitLimit && !(ok = mbar_try_wait(bar, parity)); ++i)
-            if (*abort) break;
-        ok = __all_sync(0xffffffffu, ok) != 0;
-        if (!ok && lane == 0 && !*abort) {
-            *abort = 1;
-            atomicOr(a.s.status, kStatusTimeout);
-        }
-        return ok;
-    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.s.status); };
     int first, end;                                 // this part's tiles of keys, and those that each row tile sees of them
     part_range(max(tiles[0], tiles[1]), part, a.splits, first, end);
     const int count = end - first, n0 = max(0, min(end, tiles[0]) - first), n1 = max(0, min(end, tiles[1]) - first);

@@ -3,6 +3,7 @@
 // dimensions and of plain memory, dozing waits, named barriers.
 #pragma once
 
+#include "gdnreplay.h"
 #include "tc_common.cuh"
 
 namespace gdn {
@@ -87,6 +88,24 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// A whole warp waits for a phase, a bounded time, and gets the same answer in every lane.  A wait that runs out sets *abort
+// and GDN_STATUS_TIMEOUT; from then on every wait that does not succeed at once gives up.  What has come already is
+// seen by the first look: 15 cycles, against 150 with the loop around it.
+static __device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort)) return false;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        *abort = 1;
+        atomicOr(status, GDN_STATUS_TIMEOUT);
+    }
+    __syncwarp();
+    return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_longer(bar, parity, abort, status);
 }
 // Whether x holds in any of the 64 threads of the barrier.
 __device__ __forceinline__ bool pair_any(int id, bool x) {
