@@ -8,14 +8,16 @@
 // the updates are u = P x, and so, with M[t][s] = scale e^{G_t - G_s} (q_t.k_s) (s <= t) and
 // D = diag(e^{G_63 - G_t}),
 //     o = scale gamma S q + (M P) x,    S' = gamma_63 S + E x,  E = K^T D P.
-// E (dk x 64) and M P (64 x 64) do not involve the state: the first kernel makes them for all chunks at once.  The
+// E (dk x 64) and M P (64 x 64) do not involve the state: the first kernel makes them for many chunks at once.  The
 // second walks the chunks of a head with the state at hand, two dependent products a chunk: [K;Q] S^T, then
-// E x (and (M P) x beside the next).  A slice of 32 value columns needs nothing of the others, so few heads still fill
-// many SMs.
+// E x (and (M P) x beside what follows).  Value columns need nothing of one another: few heads are cut into
+// slices of 32 columns, many are walked whole.
 //
-// Precision.  Keys and queries are exact in bf16.  S, x, E and M P enter as two bf16 terms each (relative 2^-17), with
-// one product less where both operands have two; the state itself stays in fp32 registers through the walk.  (One tf32
-// term would leave 2^-11 of S per chunk in the state.)  The inverse is formed in fp32 by 16 x 16 blocks.
+// Precision.  Outputs and states are fp32 and as exact as the token-by-token kernel's.  Keys and queries are exact in bf16;
+// S, x, E, M P and what these are made of enter as three bf16 terms each (all 24 bits), products of a pair of
+// them as the six of terms whose orders add up to two at most.  (Two terms and three products were 5e-6 off,
+// fifty times an fp32 sum's error, for some 30 % less time.)  The state itself stays in fp32 registers through the walk,
+// the inverse is formed in fp32 by blocks.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -33,11 +35,11 @@ constexpr int kSlice = 32;                          // value columns of a slice
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What the first kernel leaves of a chunk of a head, as the second one's operands lie in shared memory:
-// E as [dk][64 tokens] bf16 rows of 128 bytes (swizzled), first and second terms; M P as [64][64] likewise; gamma.
+// E as [dk][64 tokens] bf16 rows of 128 bytes (swizzled), its three terms; M P as [64][64] likewise; gamma.
 template <int DK> struct Unit {
-    static constexpr int E_BYTES = DK * 128, MP_BYTES = kC * 128;
-    static constexpr int TILES = 2 * E_BYTES + 2 * MP_BYTES;
-    static constexpr int BYTES = TILES + 512;       // gamma [64] fp32 at TILES
+    static constexpr int E_BYTES = DK * 128, MP_BYTES = kC * 128;      // of a term
+    static constexpr int OFF_MP = 3 * E_BYTES, OFF_GAMMA = OFF_MP + 3 * MP_BYTES;
+    static constexpr int BYTES = OFF_GAMMA + 512;   // gamma [64] fp32
 };
 
 struct TcAdvance {
@@ -45,47 +47,52 @@ struct TcAdvance {
     int b0;                                         // first sequence of the launch
     int c0, chunks;                                 // first chunk, chunks of the launch
     int dv;
+    int behind;                                     // the first kernel runs beside the walk over the chunks before (see launch)
 };
 
 // Tokens of the launch's chunks that are in use.
 __device__ __forceinline__ int tokens_here(const TcAdvance &ta, int n) { return max(0, min(n - ta.c0 * kC, ta.chunks * kC)); }
 
-// Two numbers as two packed bf16 terms each (the sum is the number to a relative 2^-17); NaN stays in both.
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t &h, uint32_t &l) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x, y);
-    h = *reinterpret_cast<const uint32_t *>(&a);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x - __uint_as_float(h << 16), y - __uint_as_float(h & 0xffff0000u));
-    l = *reinterpret_cast<const uint32_t *>(&b);
+// Two numbers as three packed bf16 terms each, 8 bits of the mantissa after the other (so their sum is the number; NaN stays).
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&t)[3]) {
+    const uint32_t mask = 0xffff0000u;
+    const float xm = x - __uint_as_float(__float_as_uint(x) & mask), ym = y - __uint_as_float(__float_as_uint(y) & mask);
+    t[0] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+    t[1] = __byte_perm(__float_as_uint(xm), __float_as_uint(ym), 0x7632);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(xm - __uint_as_float(__float_as_uint(xm) & mask), ym - __uint_as_float(__float_as_uint(ym) & mask));
+    t[2] = *reinterpret_cast<const uint32_t *>(&l);
 }
 // Eight of them as one 16-byte chunk of each term.
-__device__ __forceinline__ void split8(const float *y, uint4 &h, uint4 &l) {
-    split_pair(y[0], y[1], h.x, l.x);
-    split_pair(y[2], y[3], h.y, l.y);
-    split_pair(y[4], y[5], h.z, l.z);
-    split_pair(y[6], y[7], h.w, l.w);
+__device__ __forceinline__ void split8(const float *y, uint4 (&t)[3]) {
+    uint32_t p[4][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_pair(y[2 * i], y[2 * i + 1], p[i]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) t[k] = make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
 }
+// The products of two numbers of three terms: (term of A, term of B), the largest first.
+__device__ constexpr int kTermA[6] = {0, 0, 1, 0, 1, 2}, kTermB[6] = {0, 1, 0, 2, 1, 0};
 
 // ------------------------------------------------------------- E and M P of every chunk
 constexpr int kPrepThreads = 256;
 
-// Shared memory, 70 KB, so that three CTAs share an SM: [K;Q] as atoms of 64 columns, 128 rows of 128 bytes each (M's
-// terms go over the queries' rows of the two, E's over the whole at the end); A in fp32 (then F, then M P's terms); T in
-// fp32 (then P).
+// Shared memory, 73 KB, so that three CTAs share an SM: [K;Q] as atoms of 64 columns, 128 rows of 128 bytes each (M's
+// first two terms go over the queries' rows of the two, the third follows them); A in fp32, T over it, then the terms of F and
+// after them those of P; at the end those of E and M P over all of it.
 template <int DK> struct PrepPlan {
     static constexpr int LD = 68;                   // floats of a row of A and T: 16-byte rows, 4 banks apart
-    static constexpr int OFF_M = 8192, ATOM = 16384;
-    static constexpr int OFF_A = 32768, OFF_T = OFF_A + 18432;
-    static constexpr int OFF_G = OFF_T + kC * LD * 4;      // G (two words), gamma, beta, decay to the end
+    static constexpr int OFF_M = 8192, ATOM = 16384, OFF_M2 = 32768, OFF_T = OFF_M2 + 8192, TERM = kC * 128;
+    static constexpr int OFF_G = 3 * 128 * 128 + 3 * TERM;             // G (two words), gamma, beta, decay to the end
     static constexpr int OFF_BAR = OFF_G + 5 * kC * 4;
     static constexpr int BYTES = OFF_BAR + 64;
-    static_assert(kC * LD * 4 <= 18432 && OFF_T % 1024 == 0, "A's room");
+    static_assert(OFF_T % 1024 == 0 && kC * LD * 4 <= 3 * TERM && OFF_T + 3 * TERM <= OFF_G, "room");
 };
 
-// One level of the inverse: with the diagonal blocks of N rows of T = (I + A)^-1 in place, those of 2 N:
+// One level of the inverse, in A's place: with the diagonal blocks of N rows of T = (I + A)^-1 there, those of 2 N:
 // T21 = -T22 A21 T11.  X = A21 T11 lies in the block (1, 2) for the moment, so the loops stay clear of what
 // is above the diagonal blocks of 8.  A thread has N / 8 neighbouring elements.
 template <int N, int LD>
-__device__ __forceinline__ void inverse_level(const float *sA, float *sT, int tid) {
+__device__ __forceinline__ void inverse_level(float *sT, int tid) {
     constexpr int W = N / 8;
     const int c = (tid & 7) * W, r = (tid >> 3) % N, lo = tid / (8 * N) * 2 * N, hi = lo + N;
     float x[W];
@@ -110,7 +117,7 @@ __device__ __forceinline__ void inverse_level(const float *sA, float *sT, int ti
             }
         }
     };
-    product(sA + (hi + r) * LD + lo, sT + lo * LD + lo + c, c & ~7, N, 1.f);
+    product(sT + (hi + r) * LD + lo, sT + lo * LD + lo + c, c & ~7, N, 1.f);
 #pragma unroll
     for (int i = 0; i < W; ++i) sT[(lo + r) * LD + hi + c + i] = x[i];
     __syncthreads();
@@ -120,18 +127,18 @@ __device__ __forceinline__ void inverse_level(const float *sA, float *sT, int ti
     __syncthreads();
 }
 
-// 32 columns of this thread's lane from tcol on as two terms each, in columns 32 half .. of row `row` of the tiles hi and lo.
-__device__ __forceinline__ void stage_row(uint32_t tcol, uint8_t *hi, uint8_t *lo, int row, int half) {
+// 32 columns of this thread's lane from tcol on as three terms each, in columns 32 half .. of row `row` of the tiles, `step` bytes apart.
+__device__ __forceinline__ void stage_row(uint32_t tcol, uint8_t *tile, int step, int row, int half) {
     uint32_t r[32];
     tmem_ld32(tcol, r);
     tmem_wait_ld();
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        uint4 h, l;
-        split8(reinterpret_cast<const float *>(r) + 8 * c, h, l);
+        uint4 t[3];
+        split8(reinterpret_cast<const float *>(r) + 8 * c, t);
         const uint32_t at = sw128(row, 4 * half + c);
-        *reinterpret_cast<uint4 *>(hi + at) = h;
-        *reinterpret_cast<uint4 *>(lo + at) = l;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(tile + k * step + at) = t[k];
     }
 }
 
@@ -143,22 +150,23 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
     const AdvanceArgs &a = ta.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int h = blockIdx.x, c = blockIdx.y, b = ta.b0 + blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_wait();
-    pdl_release();
+    // Beside a walk, CTA 0 waits for it at its end instead (it also takes part in the launch when its own chunk is empty).
+    const bool waiter = ta.behind && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+    if (!ta.behind) pdl_wait();
     const AdvanceSeq sq = advance_seq(a, b);
     const int n = sq.bad ? 0 : tokens_here(ta, sq.n) - c * kC;          // tokens of this chunk in use
-    if (n <= 0) return;
-    if ((saddr(smem) & 1023u) || (a.flags & GDN_FLAG_TEST_EXPIRE)) {
-        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+    const bool expire = (saddr(smem) & 1023u) || (a.flags & GDN_FLAG_TEST_EXPIRE);
+    if (n <= 0 || expire) {
+        if (n > 0 && tid == 0) atomicOr(a.status, kStatusTimeout);
+        if (waiter) pdl_wait();
         return;
     }
-    float *sA = reinterpret_cast<float *>(smem + P::OFF_A), *sT = reinterpret_cast<float *>(smem + P::OFF_T);
+    float *sT = reinterpret_cast<float *>(smem + P::OFF_T);
     float *sGh = reinterpret_cast<float *>(smem + P::OFF_G), *sGl = sGh + kC, *sGam = sGl + kC, *sBeta = sGam + kC, *sEnd = sBeta + kC;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 4);
     if (tid == 0) {
-        mbar_init(&bar[0], 1);
-        mbar_init(&bar[1], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, 128);
@@ -248,7 +256,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
     }
     bool ok = mbar_wait(&bar[0], 0);
     tc_fence_after();
-    // ---- A in fp32 (rows of K), M as two bf16 terms (rows of Q)
+    // ---- A in fp32 (rows of K), M's terms (rows of Q)
     const int t = ((warp & 1) << 5) + lane;
     const bool keys = (warp & 3) < 2;
     if (__all_sync(0xffffffffu, ok)) {
@@ -272,15 +280,16 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
         if (keys) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<float4 *>(sA + t * P::LD + 32 * half + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                *reinterpret_cast<float4 *>(sT + t * P::LD + 32 * half + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
         } else {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                uint4 hh, ll;
-                split8(y + 8 * v, hh, ll);
-                const uint32_t at = P::OFF_M + sw128(t, 4 * half + v);
-                *reinterpret_cast<uint4 *>(smem + at) = hh;
-                *reinterpret_cast<uint4 *>(smem + P::ATOM + at) = ll;
+                uint4 m[3];
+                split8(y + 8 * v, m);
+                const uint32_t at = sw128(t, 4 * half + v);
+                *reinterpret_cast<uint4 *>(smem + P::OFF_M + at) = m[0];
+                *reinterpret_cast<uint4 *>(smem + P::OFF_M + P::ATOM + at) = m[1];
+                *reinterpret_cast<uint4 *>(smem + P::OFF_M2 + at) = m[2];
             }
         }
     }
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
     // ---- T = (I + A)^-1: diagonal blocks of 8 by substitution, a thread per column; then blocks of twice the size
     if (tid < kC) {
         const int bi = tid >> 3, j = tid & 7;
-        const float *Ab = sA + 8 * bi * P::LD + 8 * bi;
+        float *Ab = sT + 8 * bi * P::LD + 8 * bi;
         float x[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
@@ -302,187 +311,189 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
                 else s0 = fmaf(y[k], x[k], s0);
             }
             x[r] = r == j ? 1.f : r < j ? 0.f : -(s0 + s1);
-            sT[(8 * bi + r) * P::LD + 8 * bi + j] = x[r];
         }
+        __syncwarp();                               // a block's threads are in one warp
+#pragma unroll
+        for (int r = 0; r < 8; ++r) Ab[r * P::LD + j] = x[r];
     }
     __syncthreads();
-    inverse_level<8, P::LD>(sA, sT, tid);
-    inverse_level<16, P::LD>(sA, sT, tid);
-    inverse_level<32, P::LD>(sA, sT, tid);
-    // ---- P = T diag(beta) and F = D P as two bf16 terms each: a row's 16 columns, P over T and F over A
-    {
-        const int row = tid & (kC - 1), s0 = (tid >> 6) * 16;
-        const float end = sEnd[row];
-        float y[16], z[16];
+    inverse_level<8, P::LD>(sT, tid);
+    inverse_level<16, P::LD>(sT, tid);
+    inverse_level<32, P::LD>(sT, tid);
+    // ---- P = T diag(beta) and F = D P: a row's 16 columns; F's terms over T first, P's after the product with them
+    const int row = tid & (kC - 1), s0 = (tid >> 6) * 16;
+    const float end = sEnd[row];
+    float y[16];
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const float4 x4 = *reinterpret_cast<const float4 *>(sT + row * P::LD + s0 + j), b4 = *reinterpret_cast<const float4 *>(sBeta + s0 + j);
-            y[j] = x4.x * b4.x;
-            y[j + 1] = x4.y * b4.y;
-            y[j + 2] = x4.z * b4.z;
-            y[j + 3] = x4.w * b4.w;
-        }
+    for (int j = 0; j < 16; j += 4) {
+        const float4 x4 = *reinterpret_cast<const float4 *>(sT + row * P::LD + s0 + j), b4 = *reinterpret_cast<const float4 *>(sBeta + s0 + j);
+        y[j] = x4.x * b4.x;
+        y[j + 1] = x4.y * b4.y;
+        y[j + 2] = x4.z * b4.z;
+        y[j + 3] = x4.w * b4.w;
+    }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            y[j] = __uint_as_float(__float_as_uint(y[j]) & (s0 + j <= row ? 0xffffffffu : 0u));
-            z[j] = y[j] * end;
-        }
-        __syncthreads();
+    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(__float_as_uint(y[j]) & (s0 + j <= row ? 0xffffffffu : 0u));
+    auto put = [&](float f) {
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            uint4 hh, ll;
-            const uint32_t at = sw128(row, (s0 >> 3) + v);
-            split8(y + 8 * v, hh, ll);
-            *reinterpret_cast<uint4 *>(smem + P::OFF_T + at) = hh;
-            *reinterpret_cast<uint4 *>(smem + P::OFF_T + 8192 + at) = ll;
-            split8(z + 8 * v, hh, ll);
-            *reinterpret_cast<uint4 *>(smem + P::OFF_A + at) = hh;
-            *reinterpret_cast<uint4 *>(smem + P::OFF_A + 8192 + at) = ll;
+            float z[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = f * y[8 * v + j];
+            uint4 m[3];
+            split8(z, m);
+            const uint32_t at = P::OFF_T + sw128(row, (s0 >> 3) + v);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(smem + k * P::TERM + at) = m[k];
         }
-    }
-    fence_proxy_async();
+        fence_proxy_async();
+    };
+    __syncthreads();                                // T has been read
+    put(end);
     __syncthreads();
-    // ---- E = K^T F (rows dk: the keys read MN-major) and, over [K;Q] K^T, M P (lanes 64..127: M's rows follow the keys' in each
-    //      atom; where dk is 64 the rows before M's second term are no data, and lanes 0..63 are not read)
-    if (warp == 0) {
+    // ---- E = K^T F (rows dk: the keys read MN-major), then, over [K;Q] K^T, M P (lanes 64..127: each term of M begins 64 rows
+    //      into its operand; lanes 0..63 are not read)
+    const uint32_t one = elect_one();
+    const uint64_t dt = desc_mn_sw128(saddr(smem) + P::OFF_T, 8192);
+    if (warp == 0 && ok) {
         tc_fence_after();
-        const uint64_t dk = desc_mn_sw128(saddr(smem), P::ATOM), df = desc_mn_sw128(saddr(smem) + P::OFF_A, 8192);
-        const uint64_t dp = desc_mn_sw128(saddr(smem) + P::OFF_T, 8192), dm = desc_sw128(saddr(smem));
-        constexpr uint32_t idE = idesc_mn(1, 128, kC) | kIdescMnMajorA | kIdescMnMajorB, idM = idesc_mn(1, 128, kC) | kIdescMnMajorB;
-        if (elect_one() && ok) {
+        const uint64_t dk = desc_mn_sw128(saddr(smem), P::ATOM);
+        constexpr uint32_t idE = idesc_mn(1, 128, kC) | kIdescMnMajorA | kIdescMnMajorB;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                mma_bf16(tmem + 64, desc_add(dk, ks * 2048), desc_add(df, ks * 2048), idE, ks > 0);
-                mma_bf16(tmem + 64, desc_add(dk, ks * 2048), desc_add(df, 8192 + ks * 2048), idE, 1);
-            }
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                mma_bf16(tmem, desc_add(dm, ks * 32), desc_add(dp, ks * 2048), idM, ks > 0);
-                mma_bf16(tmem, desc_add(dm, ks * 32), desc_add(dp, 8192 + ks * 2048), idM, 1);
-                mma_bf16(tmem, desc_add(dm, P::ATOM + ks * 32), desc_add(dp, ks * 2048), idM, 1);
-            }
-            mma_commit(&bar[1]);
-        }
-        __syncwarp();
+        for (int k = 0; k < 12; ++k)
+            mma_bf16_on(one, tmem + 64, desc_add(dk, (k & 3) * 2048), desc_add(dt, (k >> 2) * P::TERM + (k & 3) * 2048), idE, k > 0);
+        mma_commit_on(one, &bar[1]);
     }
     ok = ok && mbar_wait(&bar[1], 0);
+    ok = __all_sync(0xffffffffu, ok);
+    put(1.f);
+    __syncthreads();
+    if (warp == 0 && ok) {
+        tc_fence_after();
+        constexpr uint32_t idM = idesc_mn(1, 128, kC) | kIdescMnMajorB;
+#pragma unroll
+        for (int k = 0; k < 24; ++k) {
+            const int ta3 = kTermA[k >> 2], m = ta3 == 2 ? P::OFF_M2 - 8192 : ta3 * P::ATOM;
+            mma_bf16_on(one, tmem, desc_add(desc_sw128(saddr(smem)), m + (k & 3) * 32),
+                        desc_add(dt, kTermB[k >> 2] * P::TERM + (k & 3) * 2048), idM, k > 0);
+        }
+        mma_commit_on(one, &bar[2]);
+    }
+    const bool began = ok;
+    ok = ok && mbar_wait(&bar[2], 0);
+    ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    // ---- the terms of both into shared memory as the walk wants them, and out in two copies
+    __syncthreads();                                // (a wait that ran out in another warp: its MMAs are drained below)
+    // ---- the terms of both into shared memory as the walk wants them, and out in one copy
     char *unit = a.ws + ((static_cast<size_t>(blockIdx.z) * ta.chunks + c) * a.H + h) * Unit<DK>::BYTES;
-    if (__all_sync(0xffffffffu, ok)) {
+    if (ok) {
         if ((warp & 3) * 32 < DK)
-            stage_row(tmem + lanes + 64 + 32 * half, smem, smem + Unit<DK>::E_BYTES, (warp & 3) * 32 + lane, half);
-        if (!keys)
-            stage_row(tmem + lanes + 32 * half, smem + P::OFF_A, smem + P::OFF_A + Unit<DK>::MP_BYTES, t, half);
-        if (tid < kC) reinterpret_cast<float *>(unit + Unit<DK>::TILES)[tid] = sGam[tid];
-    } else if (lane == 0) {                         // (nothing more was issued unless the second wait ran out: one more bounded wait)
+            stage_row(tmem + lanes + 64 + 32 * half, smem, Unit<DK>::E_BYTES, (warp & 3) * 32 + lane, half);
+        if (!keys) stage_row(tmem + lanes + 32 * half, smem + Unit<DK>::OFF_MP, Unit<DK>::MP_BYTES, t, half);
+        if (tid < kC) reinterpret_cast<float *>(unit + Unit<DK>::OFF_GAMMA)[tid] = sGam[tid];
+    } else if (lane == 0) {                         // one more bounded wait for what was issued
         atomicOr(a.status, kStatusTimeout);
-        if (!mbar_wait(&bar[1], 0)) atomicOr(a.status, GDN_STATUS_DRAIN);
+        if (began && !mbar_wait(&bar[2], 0)) atomicOr(a.status, GDN_STATUS_DRAIN);
+        if (!began && !mbar_wait(&bar[1], 0)) atomicOr(a.status, GDN_STATUS_DRAIN);
     }
     fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
-        bulk_store(unit, smem, 2 * Unit<DK>::E_BYTES);
-        bulk_store(unit + 2 * Unit<DK>::E_BYTES, smem + P::OFF_A, 2 * Unit<DK>::MP_BYTES);
+        bulk_store(unit, smem, Unit<DK>::OFF_GAMMA);
         bulk_store_wait();
     }
     if (warp == 1) tmem_dealloc(tmem, 128);
+    if (waiter) pdl_wait();
 }
 
-// ------------------------------------------------------------- the walk over the chunks
-template <int DK, int NS> struct ScanPlan {
-    static constexpr int KQ = DK * 256, STAGE = KQ + Unit<DK>::TILES, STAGES = 2;
-    static constexpr int S_BYTES = DK * 128, X_BYTES = kC * 128;      // rows of 32 first terms, 32 second ones
-    static constexpr int OFF_S = STAGES * STAGE, OFF_X = OFF_S + NS * S_BYTES, OFF_BAR = OFF_X + NS * X_BYTES;
-    static constexpr int BYTES = OFF_BAR + 256;
-    static constexpr int ROWS = NS * 256, LOAD_WARP = ROWS / 32, MMA_WARP = LOAD_WARP + 1, THREADS = ROWS + 64;
-    static constexpr int N = NS * 64, TMEM_COLS = NS == 1 ? 256 : 512;         // columns of a product; [K;Q] S^T, E x, M P x
-    static_assert(3 * N <= TMEM_COLS && BYTES <= 227 * 1024 && STAGE % 1024 == 0, "plan");
+// ------------------------------------------------------------- the walk over the chunks, by slices
+// One CTA per (slice of 32 value columns, head, sequence): the walk for few heads, whose chain of dependent steps bounds it
+// (about 2600 cycles a chunk).  S and x are the B operands: rows of 32 first, 32 second and 32 third terms, so one product of
+// 96 columns has all of them (55 cycles an MMA, against 39 for 32 columns).
+template <int DK> struct SlicePlan {
+    static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES, MP = 3 * Unit<DK>::MP_BYTES;
+    static constexpr int S_ATOM = DK * 128, X_ATOM = kC * 128;         // first and second terms, then the third in an atom of its own
+    static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + E, OFF_S = OFF_MP + 2 * MP, OFF_X = OFF_S + 2 * S_ATOM;
+    static constexpr int OFF_BAR = OFF_X + 2 * X_ATOM, BYTES = OFF_BAR + 256;
+    static constexpr int ROWS = 256, LOAD_WARP = 8, MMA_WARP = 9, THREADS = 320;
+    static constexpr int N = 96, TMEM_COLS = 512;                      // columns of a product: [K;Q] S^T, E x, M P x
+    static_assert(BYTES <= 227 * 1024 && OFF_E >= 8192, "plan");
 };
 
-// A thread's 16 numbers as two bf16 terms in row `row` of a tile of 128-byte rows: 32 first terms, then 32 second ones.
-__device__ __forceinline__ void put_row(uint8_t *tile, int row, int half, const float (&y)[16]) {
+// A thread's 16 numbers as three bf16 terms in row `row` of a tile: 32 first, 32 second ones, and 32 third ones an atom on.
+__device__ __forceinline__ void put_row(uint8_t *tile, int atom, int row, int half, const float (&y)[16]) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        uint4 h, l;
-        split8(y + 8 * c, h, l);
-        *reinterpret_cast<uint4 *>(tile + sw128(row, 2 * half + c)) = h;
-        *reinterpret_cast<uint4 *>(tile + sw128(row, 2 * half + c + 4)) = l;
+        uint4 t[3];
+        split8(y + 8 * c, t);
+        *reinterpret_cast<uint4 *>(tile + sw128(row, 2 * half + c)) = t[0];
+        *reinterpret_cast<uint4 *>(tile + sw128(row, 2 * half + c + 4)) = t[1];
+        *reinterpret_cast<uint4 *>(tile + atom + sw128(row, 2 * half + c)) = t[2];
     }
 }
-// The product's 16 columns: those with the first terms and those with the second ones added.
+// The product's 16 columns: those with the three terms added, the smallest first.
 __device__ __forceinline__ void get_row(uint32_t tcol, float (&y)[16]) {
-    uint32_t r[16], s[16];
+    uint32_t r[16], s[16], t[16];
     tmem_load16(tcol, r);
     tmem_load16(tcol + 32, s);
+    tmem_load16(tcol + 64, t);
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(r[j]) + __uint_as_float(s[j]);
+    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(r[j]) + (__uint_as_float(s[j]) + __uint_as_float(t[j]));
 }
 
-// One CTA per (NS slices of value columns, head, sequence).  A slice has eight row warps; one warp loads and one issues
-// the products of all slices together (a product's rows are read once for them: an MMA of 64 columns takes 50 cycles
-// for its 128 rows of 32 bytes, one of 128 columns 67).  Row r of a slice has token r (K's products, r < 64), token r - 64 (Q's) and key dimension r of the state, 16
-// columns in each of two warps (one per row: 800 cycles for x and as many for S instead of half).  Everything that a buffer's next use overwrites has been read by then: see each arrival.
-template <int DK, int NS>
-__global__ void __launch_bounds__(ScanPlan<DK, NS>::THREADS, 1)
-advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
-                    const __grid_constant__ TcAdvance ta)
+// What both walks begin with: the sequence, rows of out past it, a state without tokens.  False: nothing is left to do.
+__device__ __forceinline__ bool begin_walk(const TcAdvance &ta, const AdvanceSeq &sq, int n, int h, int b, int dv0, int cols, int dk, bool zero,
+                                           bool first, int threads) {
+    const AdvanceArgs &a = ta.a;
+    if (sq.bad) {
+        if (first && threadIdx.x == 0 && h == 0 && ta.c0 == 0) atomicOr(a.status, sq.bad);
+        return false;
+    }
+    const int t1 = min(a.T, (ta.c0 + ta.chunks) * kC);
+    float *out = a.out + (static_cast<size_t>(b) * a.T * a.H + h) * ta.dv + dv0;
+    for (int e = threadIdx.x;; e += threads) {
+        const int t = ta.c0 * kC + n + e / cols;
+        if (t >= t1) break;
+        out[static_cast<size_t>(t) * a.H * ta.dv + e % cols] = 0.f;
+    }
+    if (n == 0 && zero)
+        for (int e = threadIdx.x; e < cols * dk; e += threads)
+            a.state[((static_cast<size_t>(sq.slot) * a.H + h) * ta.dv + dv0) * dk + e] = 0.f;
+    return n > 0;
+}
+
+// Row r has token r (K's products, r < 64), token r - 64 (Q's) and key dimension r of the state, 16 columns in each of
+// two warps.  Everything that a buffer's next use overwrites has been read by then: see each arrival.
+template <int DK>
+__global__ void __launch_bounds__(SlicePlan<DK>::THREADS, 1)
+advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ TcAdvance ta)
 {
-    using P = ScanPlan<DK, NS>;
+    using P = SlicePlan<DK>;
     const AdvanceArgs &a = ta.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int h = blockIdx.y, b = ta.b0 + blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint64_t *full_k = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty_k = full_k + 2, *full_e = empty_k + 2,
-             *empty_e = full_e + 2, *d1 = empty_e + 2, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1, *x_ready = s_ready + 1, *drain = x_ready + 1;
+    uint64_t *full_k = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty_k = full_k + 2, *full_m = empty_k + 2, *empty_m = full_m + 2,
+             *full_e = empty_m + 2, *empty_e = full_e + 1, *d1 = empty_e + 1, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1,
+             *x_ready = s_ready + 1, *drain = x_ready + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     pdl_wait();
     pdl_release();
     const AdvanceSeq sq = advance_seq(a, b);
-    if (sq.bad) {
-        if (tid == 0 && blockIdx.x == 0 && h == 0 && ta.c0 == 0) atomicOr(a.status, sq.bad);
-        return;
-    }
-    const int n = tokens_here(ta, sq.n), chunks = (n + kC - 1) / kC;
-    const int dv0 = blockIdx.x * (NS * kSlice);
-    // rows of this launch past the sequence's last token
-    {
-        const int t1 = min(a.T, (ta.c0 + ta.chunks) * kC);
-        float *out = a.out + (static_cast<size_t>(b) * a.T * a.H + h) * ta.dv + dv0;
-        for (int e = tid; ; e += P::THREADS) {
-            const int t = ta.c0 * kC + n + e / (NS * kSlice);
-            if (t >= t1) break;
-            out[static_cast<size_t>(t) * a.H * ta.dv + e % (NS * kSlice)] = 0.f;
-        }
-    }
+    const int n = sq.bad ? 0 : tokens_here(ta, sq.n), chunks = (n + kC - 1) / kC, dv0 = blockIdx.x * kSlice;
     const bool zero = sq.fresh && ta.c0 == 0;       // starts from a zero state
-    if (n == 0) {
-        if (zero)
-            for (int e = tid; e < NS * kSlice * DK; e += P::THREADS)
-                a.state[((static_cast<size_t>(sq.slot) * a.H + h) * ta.dv + dv0) * DK + e] = 0.f;
-        return;
-    }
+    if (!begin_walk(ta, sq, n, h, b, dv0, kSlice, DK, zero, blockIdx.x == 0, P::THREADS)) return;
     if (saddr(smem) & 1023u) {
         if (tid == 0) atomicOr(a.status, kStatusTimeout);
         return;
     }
     if (tid == 0) {
         const bool expire = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&full_k[i], 1);
-            mbar_init(&empty_k[i], 1);
-            mbar_init(&full_e[i], 1);
-            mbar_init(&empty_e[i], 1);
-        }
-        mbar_init(d1, 1);
-        mbar_init(d2, 1);
-        mbar_init(d3, 1);
-        mbar_init(s_ready, P::ROWS / 32);           // a warp arrives once: 256 arrivals at one word take 500 cycles
-        mbar_init(x_ready, P::ROWS / 32);
-        mbar_init(drain, 1);
-        *abort = expire;
+        for (uint64_t *bar = full_k; bar <= drain; ++bar) mbar_init(bar, bar == s_ready || bar == x_ready ? P::ROWS / 32 : 1);
+        *abort = expire;                            // (a warp arrives once: 256 arrivals at one word take 500 cycles)
         if (expire) atomicOr(a.status, kStatusTimeout);
         fence_mbar_init();
     }
@@ -496,16 +507,18 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const size_t ustep = static_cast<size_t>(a.H) * Unit<DK>::BYTES;
     if (warp == P::LOAD_WARP) {
         // ------------------------------------------------------ loads
-        // Keys and queries go when the first product of two chunks before is done, E and M P after its last: with one
-        // barrier for both, a chunk's 80 KB came no sooner than it was needed (3000 cycles a chunk instead of 2400).
+        // Keys and queries go when the first product of two chunks before is done, E after its one use in the chunk before, M P
+        // after the last product of two before.  (With one barrier for all, a chunk's operands came no sooner
+        // than they were needed: 3000 cycles a chunk instead of 2400.)
         const int hk = h / (a.H / a.Hk);
-        int c = 0, half = 0;
+        int c = 0, part = 0;
         for (; c < chunks; ++c) {
             const int st = c & 1, before = ((c >> 1) - 1) & 1;
-            uint8_t *dst = smem + st * P::STAGE;
-            half = 0;
+            const char *unit = units + c * ustep;
+            part = 0;
             if (*abort || (c >= 2 && !wait(&empty_k[st], before))) break;
             if (elect_one()) {
+                uint8_t *dst = smem + st * P::KQ;
                 const int tok = b * a.T + (ta.c0 + c) * kC;           // (B T <= 2^28)
                 mbar_expect_tx(&full_k[st], P::KQ);
 #pragma unroll
@@ -515,28 +528,42 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 }
             }
             __syncwarp();
-            half = 1;
-            if (c >= 2 && !wait(&empty_e[st], before)) break;
+            part = 1;
+            if (c >= 1 && !wait(empty_e, (c - 1) & 1)) break;
             if (elect_one()) {
-                mbar_expect_tx(&full_e[st], Unit<DK>::TILES);
-                bulk_load(dst + P::KQ, units + c * ustep, Unit<DK>::TILES, &full_e[st]);
+                mbar_expect_tx(full_e, P::E);
+                bulk_load(smem + P::OFF_E, unit, P::E, full_e);
+            }
+            __syncwarp();
+            part = 2;
+            if (c >= 2 && !wait(&empty_m[st], before)) break;
+            if (elect_one()) {
+                mbar_expect_tx(&full_m[st], P::MP);
+                bulk_load(smem + P::OFF_MP + st * P::MP, unit + Unit<DK>::OFF_MP, P::MP, &full_m[st]);
             }
             __syncwarp();
         }
         if (*abort) {                               // copies in flight end before the CTA does
             bool done = true;
-            const int keys = c < chunks ? c + half : c;               // chunks whose keys, and whose E, have been requested
+            const int keys = c < chunks && part > 0 ? c + 1 : c, es = c < chunks && part > 1 ? c + 1 : c;   // chunks whose keys, whose E have been requested
             for (int i = max(0, keys - 2); i < keys; ++i) done = done && mbar_wait(&full_k[i & 1], (i >> 1) & 1);
-            for (int i = max(0, c - 2); i < c; ++i) done = done && mbar_wait(&full_e[i & 1], (i >> 1) & 1);
+            if (es > 0) done = done && mbar_wait(full_e, (es - 1) & 1);
+            for (int i = max(0, c - 2); i < c; ++i) done = done && mbar_wait(&full_m[i & 1], (i >> 1) & 1);
             if (!done && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
         }
     } else if (warp == P::MMA_WARP) {
         // ------------------------------------------------------ MMAs
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t dS = desc_mn_sw128(saddr(smem) + P::OFF_S, P::S_BYTES), dX = desc_mn_sw128(saddr(smem) + P::OFF_X, P::X_BYTES);
-        const uint64_t dA = desc_sw128(saddr(smem));
-        constexpr uint32_t id = idesc_mn(1, 128, P::N) | kIdescMnMajorB;
+        const uint64_t dS = desc_mn_sw128(saddr(smem) + P::OFF_S, P::S_ATOM), dX = desc_mn_sw128(saddr(smem) + P::OFF_X, P::X_ATOM);
+        const uint64_t dKQ = desc_sw128(saddr(smem)), dE = desc_sw128(saddr(smem) + P::OFF_E), dM = desc_sw128(saddr(smem) + P::OFF_MP - 8192);
         const uint32_t one = elect_one();
+        // A term of E or M P with as many terms of x as count: 3, 2 and 1 of 32 columns.
+        auto terms = [&](uint32_t acc, uint64_t left, int step) {
+#pragma unroll
+            for (int k = 0; k < 12; ++k)
+                mma_bf16_on(one, acc, desc_add(left, (k >> 2) * step + (k & 3) * 32), desc_add(dX, (k & 3) * 2048),
+                            idesc_mn(1, 128, 96 - 32 * (k >> 2)) | kIdescMnMajorB, k > 0);
+        };
         bool ok = true;
         int c = 0;
         for (; c < chunks; ++c) {
@@ -544,38 +571,35 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             ok = wait(&full_k[st], (c >> 1) & 1) && wait(s_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t kq = desc_add(dA, st * P::STAGE), e = desc_add(kq, P::KQ), mp = desc_add(e, 2 * Unit<DK>::E_BYTES - 8192);
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks)
-                mma_bf16_on(one, tm, desc_add(kq, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dS, ks * 2048), id, ks > 0);
+                mma_bf16_on(one, tm, desc_add(dKQ, st * P::KQ + (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dS, ks * 2048),
+                            idesc_mn(1, 128, P::N) | kIdescMnMajorB, ks > 0);
             mma_commit_on(one, d1);
             mma_commit_on(one, &empty_k[st]);
-            ok = wait(&full_e[st], (c >> 1) & 1) && wait(x_ready, c & 1);
+            ok = wait(full_e, c & 1) && wait(x_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)          // the first terms of E, then the second ones
-                mma_bf16_on(one, tm + P::N, desc_add(e, (ks >> 2) * Unit<DK>::E_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
+            terms(tm + P::N, dE, Unit<DK>::E_BYTES);
             mma_commit_on(one, d2);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_bf16_on(one, tm + 2 * P::N, desc_add(mp, (ks >> 2) * Unit<DK>::MP_BYTES + (ks & 3) * 32), desc_add(dX, (ks & 3) * 2048), id, ks > 0);
+            mma_commit_on(one, empty_e);
+            ok = wait(&full_m[st], (c >> 1) & 1);
+            if (!ok) break;
+            terms(tm + 2 * P::N, desc_add(dM, st * P::MP), Unit<DK>::MP_BYTES);
             mma_commit_on(one, d3);
-            mma_commit_on(one, &empty_e[st]);
+            mma_commit_on(one, &empty_m[st]);
         }
-        if (!ok && c > 0) {                         // MMAs in flight end before their memory is given back
-            if (elect_one()) mma_commit(drain);
-            __syncwarp();
+        if (!ok) {                                  // MMAs in flight end before their memory is given back
+            mma_commit_on(one, drain);
             if (!mbar_wait(drain, 0) && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
         }
     } else {
         // ------------------------------------------------------ rows
-        const int sl = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, t = row & (kC - 1);
-        const bool keys = row < kC;                 // (the same in a warp, as the next)
-        const bool has = row < DK;
-        const uint32_t tm = tmem + sl * 64 + 16 * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        uint8_t *sS = smem + P::OFF_S + sl * P::S_BYTES, *sX = smem + P::OFF_X + sl * P::X_BYTES;
-        const int col0 = dv0 + sl * kSlice + 16 * half;
+        const int half = warp >> 2, row = tid & 127, t = row & (kC - 1);
+        const bool keys = row < kC, has = row < DK;                   // (the same in a warp)
+        const uint32_t tm = tmem + 16 * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        uint8_t *sS = smem + P::OFF_S, *sX = smem + P::OFF_X;
+        const int col0 = dv0 + 16 * half;
         float *st = a.state + ((static_cast<size_t>(sq.slot) * a.H + h) * ta.dv + col0) * DK + row;
         float S[16];
 #pragma unroll
@@ -583,25 +607,29 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const size_t tok0 = static_cast<size_t>(b) * a.T + ta.c0 * kC + t;
         const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v) + tok0 * a.v_stride + h * ta.dv + col0;
         float *op = a.out + (tok0 * a.H + h) * ta.dv + col0;
-        uint4 v[2];
-        float gam = 0.f, gend = 0.f;
+        // values, gamma_t and gamma of the chunk's end, two chunks ahead
+        struct Ahead {
+            uint4 v[2];
+            float gam, gend;
+        } now, next;
+        auto fetch = [&](Ahead &f, int c) {
+            const float *gp = reinterpret_cast<const float *>(units + c * ustep + Unit<DK>::OFF_GAMMA);
+            f.v[0] = f.v[1] = make_uint4(0u, 0u, 0u, 0u);
+            f.gam = f.gend = 0.f;
+            if (c >= chunks) return;
+            f.gam = __ldcg(gp + t);
+            f.gend = __ldcg(gp + kC - 1);
+            if (keys && c * kC + t < n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) f.v[i] = __ldg(reinterpret_cast<const uint4 *>(vp + static_cast<size_t>(c) * kC * a.v_stride) + i);
+        };
         auto arrive = [&](uint64_t *bar) {          // for the warp, behind each lane's fences
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        auto fetch = [&](int c) {
-            const float *gp = reinterpret_cast<const float *>(units + c * ustep + Unit<DK>::TILES);
-            gam = __ldcg(gp + t);
-            gend = __ldcg(gp + kC - 1);
-            if (keys) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    v[i] = c * kC + t < n ? __ldg(reinterpret_cast<const uint4 *>(vp + static_cast<size_t>(c) * kC * a.v_stride) + i)
-                                          : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        fetch(0);
-        if (has) put_row(sS, row, half, S);
+        fetch(now, 0);
+        fetch(next, 1);
+        if (has) put_row(sS, P::S_ATOM, row, half, S);
         fence_proxy_async();
         arrive(s_ready);
         bool ok = true;
@@ -616,21 +644,22 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     float f[8];
-                    bf16x8_to_f32(v[i], f);
+                    bf16x8_to_f32(now.v[i], f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[8 * i + e] = live ? fmaf(-gam, y[8 * i + e], f[e]) : 0.f;
+                    for (int e = 0; e < 8; ++e) y[8 * i + e] = live ? fmaf(-now.gam, y[8 * i + e], f[e]) : 0.f;
                 }
-                put_row(sX, t, half, y);
+                put_row(sX, P::X_ATOM, t, half, y);
                 fence_proxy_async();
             } else {
-                const float f = gam * a.scale;
+                const float f = now.gam * a.scale;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) o[j] = f * y[j];
             }
-            const float ge = gend;
+            const float ge = now.gend;
             tc_fence_before();
             arrive(x_ready);                        // this row has read [K;Q] S^T (and, before it, the last M P x)
-            if (c + 1 < chunks) fetch(c + 1);
+            now = next;
+            fetch(next, c + 2);
             ok = wait(d2, c & 1);
             if (!ok) break;
             tc_fence_after();
@@ -638,7 +667,7 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 get_row(tm + P::N, y);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) S[j] = fmaf(ge, S[j], y[j]);
-                put_row(sS, row, half, S);
+                put_row(sS, P::S_ATOM, row, half, S);
                 fence_proxy_async();
             }
             tc_fence_before();
@@ -669,17 +698,288 @@ advance_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
 }
 
+// ------------------------------------------------------------- the walk over the chunks, by heads
+// One CTA per (head of 128 value columns, sequence): the walk for many heads, where the work on an SM counts and not the chain.
+// Here the state's columns are the rows (TMEM lanes): S and x are the A operands, straight from TMEM, and keys, queries, E and M P
+// the B operands as they lie.  A head costs an SM 240 KB of shared memory traffic a chunk instead of the 800 KB of
+// four slices, and nothing of S or x goes through it.
+//
+// TMEM columns: S (three terms, dk / 2 each), [K;Q] S^T and over it x (three terms of 32), E x, M P x.
+template <int DK> struct HeadPlan {
+    static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES, MP = 3 * Unit<DK>::MP_BYTES + 1024;       // M P, gamma
+    static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + 2 * E, OFF_BAR = OFF_MP + 2 * MP, BYTES = OFF_BAR + 256;
+    static constexpr int ROWS = 512, LOAD_WARP = 16, MMA_WARP = 17, THREADS = 576;
+    static constexpr int COL_D1 = 3 * DK / 2, COL_X = COL_D1, COL_D2 = COL_D1 + 128, COL_D3 = COL_D2 + DK, TMEM_COLS = 512;
+    static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4;    // copied: M P and gamma
+    static_assert(COL_D3 + kC <= TMEM_COLS && BYTES <= 227 * 1024 && MP % 1024 == 0, "plan");
+};
+
+// Row r is value column r, in four threads: each has 16 of the chunk's tokens and a quarter of the key dimensions.  An
+// expired wait only stops the waiting (a thread that left would leave others at a barrier).
+template <int DK>
+__global__ void __launch_bounds__(HeadPlan<DK>::THREADS, 1)
+advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ TcAdvance ta)
+{
+    using P = HeadPlan<DK>;
+    constexpr int DV = 128, DQ = DK / 4;            // key dimensions of a thread
+    const AdvanceArgs &a = ta.a;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int h = blockIdx.x, b = ta.b0 + blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t *full_k = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty_k = full_k + 2, *full_e = empty_k + 2, *empty_e = full_e + 2,
+             *full_m = empty_e + 2, *empty_m = full_m + 2, *d1 = empty_m + 2, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1,
+             *x_ready = s_ready + 1, *drain = x_ready + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    pdl_wait();
+    pdl_release();
+    const AdvanceSeq sq = advance_seq(a, b);
+    const int n = sq.bad ? 0 : tokens_here(ta, sq.n), chunks = (n + kC - 1) / kC;
+    const bool zero = sq.fresh && ta.c0 == 0;       // starts from a zero state
+    if (!begin_walk(ta, sq, n, h, b, 0, DV, DK, zero, true, P::THREADS)) return;
+    if (saddr(smem) & 1023u) {
+        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
+    if (tid == 0) {
+        const bool expire = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
+        for (uint64_t *bar = full_k; bar <= drain; ++bar) mbar_init(bar, bar == s_ready || bar == x_ready ? P::ROWS / 32 : 1);
+        *abort = expire;
+        if (expire) atomicOr(a.status, kStatusTimeout);
+        fence_mbar_init();
+    }
+    if (warp == P::LOAD_WARP) tmem_alloc(tmem_slot, P::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.status); };
+    if (warp == P::LOAD_WARP) {
+        // ------------------------------------------------------ loads
+        const char *units = a.ws + (static_cast<size_t>(blockIdx.y) * ta.chunks * a.H + h) * Unit<DK>::BYTES;
+        const size_t ustep = static_cast<size_t>(a.H) * Unit<DK>::BYTES;
+        const int hk = h / (a.H / a.Hk);
+        int c = 0, part = 0;
+        for (; c < chunks; ++c) {
+            const int st = c & 1, before = ((c >> 1) - 1) & 1;
+            const char *unit = units + c * ustep;
+            part = 0;
+            if (*abort || (c >= 2 && !wait(&empty_k[st], before))) break;
+            if (elect_one()) {
+                uint8_t *dst = smem + st * P::KQ;
+                const int tok = b * a.T + (ta.c0 + c) * kC;           // (B T <= 2^28)
+                mbar_expect_tx(&full_k[st], P::KQ);
+#pragma unroll
+                for (int at = 0; at < DK / 64; ++at) {
+                    tma_load_3d(dst + at * 16384, &tm_k, at * 64, hk, tok, &full_k[st]);
+                    tma_load_3d(dst + at * 16384 + 8192, &tm_q, at * 64, hk, tok, &full_k[st]);
+                }
+            }
+            __syncwarp();
+            part = 1;
+            if (c >= 2 && !wait(&empty_e[st], before)) break;
+            if (elect_one()) {
+                mbar_expect_tx(&full_e[st], P::E);
+                bulk_load(smem + P::OFF_E + st * P::E, unit, P::E, &full_e[st]);
+            }
+            __syncwarp();
+            part = 2;
+            if (c >= 2 && !wait(&empty_m[st], before)) break;
+            if (elect_one()) {
+                mbar_expect_tx(&full_m[st], P::M_BYTES);
+                bulk_load(smem + P::OFF_MP + st * P::MP, unit + Unit<DK>::OFF_MP, P::M_BYTES, &full_m[st]);
+            }
+            __syncwarp();
+        }
+        if (*abort) {                               // copies in flight end before the CTA does
+            bool done = true;
+            for (int p = 0; p < 3; ++p) {           // keys, E, M P: chunks that have been requested
+                uint64_t *full = p == 0 ? full_k : p == 1 ? full_e : full_m;
+                const int asked = c < chunks && part > p ? c + 1 : c;
+                for (int i = max(0, asked - 2); i < asked; ++i) done = done && mbar_wait(&full[i & 1], (i >> 1) & 1);
+            }
+            if (!done && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
+        }
+    } else if (warp == P::MMA_WARP) {
+        // ------------------------------------------------------ MMAs
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dKQ = desc_sw128(saddr(smem)), dE = desc_sw128(saddr(smem) + P::OFF_E), dM = desc_sw128(saddr(smem) + P::OFF_MP);
+        const uint32_t one = elect_one();
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1;
+            ok = wait(&full_k[st], (c >> 1) & 1) && wait(s_ready, c & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 3 * DK / 16; ++k) { // the terms of S
+                const int ks = k % (DK / 16);
+                mma_bf16_ts_on(one, tm + P::COL_D1, tm + k * 8, desc_add(dKQ, st * P::KQ + (ks >> 2) * 16384 + (ks & 3) * 32), idesc_mn(1, 128, 128), k > 0);
+            }
+            mma_commit_on(one, d1);
+            mma_commit_on(one, &empty_k[st]);
+            ok = wait(&full_e[st], (c >> 1) & 1) && wait(x_ready, c & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 24; ++k)
+                mma_bf16_ts_on(one, tm + P::COL_D2, tm + P::COL_X + kTermA[k >> 2] * 32 + (k & 3) * 8,
+                               desc_add(dE, st * P::E + kTermB[k >> 2] * Unit<DK>::E_BYTES + (k & 3) * 32), idesc_mn(1, 128, DK), k > 0);
+            mma_commit_on(one, d2);
+            mma_commit_on(one, &empty_e[st]);
+            ok = wait(&full_m[st], (c >> 1) & 1);
+            if (!ok) break;
+#pragma unroll
+            for (int k = 0; k < 24; ++k)            // (onto scale gamma S q, which the rows have put there)
+                mma_bf16_ts_on(one, tm + P::COL_D3, tm + P::COL_X + kTermA[k >> 2] * 32 + (k & 3) * 8,
+                               desc_add(dM, st * P::MP + kTermB[k >> 2] * Unit<DK>::MP_BYTES + (k & 3) * 32), idesc_mn(1, 128, kC), 1);
+            mma_commit_on(one, d3);
+            mma_commit_on(one, &empty_m[st]);
+        }
+        if (!ok) {                                  // MMAs in flight end before their memory is given back
+            mma_commit_on(one, drain);
+            if (!mbar_wait(drain, 0) && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
+        }
+    } else {
+        // ------------------------------------------------------ rows
+        const int q4 = warp >> 2, row = tid & 127, tq = 16 * q4;      // this thread's first token of a chunk
+        const uint32_t tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        float *st = a.state + ((static_cast<size_t>(sq.slot) * a.H + h) * DV + row) * DK + DQ * q4;
+        float S[DQ];
+#pragma unroll
+        for (int j = 0; j < DQ; j += 4) {
+            const float4 x = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4 *>(st + j);
+            S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+        }
+        const size_t tok0 = static_cast<size_t>(b) * a.T + ta.c0 * kC + tq;
+        const unsigned short *vp = static_cast<const unsigned short *>(a.v) + tok0 * a.v_stride + h * DV + row;
+        float *op = a.out + (tok0 * a.H + h) * DV + row;
+        const size_t ostep = static_cast<size_t>(a.H) * DV;
+        uint32_t v[8];                              // pairs of tokens' values of this column
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int t = c * kC + tq + 2 * j;
+                const unsigned short *p = vp + (static_cast<size_t>(c) * kC + 2 * j) * a.v_stride;
+                const uint32_t lo = t < n ? __ldg(p) : 0u, hi = t + 1 < n ? __ldg(p + a.v_stride) : 0u;
+                v[j] = lo | hi << 16;
+            }
+        };
+        auto put_state = [&]() {                    // S's terms: A operand, dk / 2 columns each
+#pragma unroll
+            for (int j = 0; j < DQ; j += 16) {
+                uint32_t w[3][8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t t[3];
+                    split_pair(S[j + 2 * i], S[j + 2 * i + 1], t);
+                    w[0][i] = t[0]; w[1][i] = t[1]; w[2][i] = t[2];
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) tmem_store8(tm + k * (DK / 2) + (DQ * q4 + j) / 2, w[k]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+        };
+        auto arrive = [&](uint64_t *bar) {          // for the warp, behind each lane's fences
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        fetch(0);
+        put_state();
+        arrive(s_ready);
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            const int sm = c & 1;
+            const float *gam = reinterpret_cast<const float *>(smem + P::OFF_MP + sm * P::MP + 3 * Unit<DK>::MP_BYTES);
+            ok = wait(&full_m[sm], (c >> 1) & 1) && ok;               // gamma
+            ok = wait(d1, c & 1) && ok;
+            tc_fence_after();
+            uint32_t y[16], z[16];
+            tmem_load16(tm + P::COL_D1 + tq, y);
+            tmem_load16(tm + P::COL_D1 + kC + tq, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                const float4 g = *reinterpret_cast<const float4 *>(gam + tq + j);
+                const float gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {       // x = v - gamma S k; nothing of tokens past the last
+                    const uint32_t w = v[(j + e) >> 1];
+                    const float f = __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+                    y[j + e] = __float_as_uint(fmaf(-gg[e], __uint_as_float(y[j + e]), f)) & (c * kC + tq + j + e < n ? 0xffffffffu : 0u);
+                    z[j + e] = __float_as_uint(gg[e] * a.scale * __uint_as_float(z[j + e]));
+                }
+            }
+            const float ge = gam[kC - 1];
+            tmem_st16(tm + P::COL_D3 + tq, z);      // (the last M P x has been read)
+            uint32_t w[3][8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t t[3];
+                split_pair(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]), t);
+                w[0][i] = t[0]; w[1][i] = t[1]; w[2][i] = t[2];
+            }
+            tc_fence_before();
+            bar_sync(1 + (warp & 3), 128);          // these lanes' [K;Q] S^T has been read: x goes over it
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 3; ++k) tmem_store8(tm + P::COL_X + 32 * k + 8 * q4, w[k]);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(x_ready);
+            if (c + 1 < chunks) fetch(c + 1);
+            ok = wait(d2, c & 1) && ok;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < DQ; j += 16) {
+                tmem_load16(tm + P::COL_D2 + DQ * q4 + j, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[j + i] = fmaf(ge, S[j + i], __uint_as_float(y[i]));
+            }
+            put_state();
+            arrive(s_ready);
+            ok = wait(d3, c & 1) && ok;
+            tc_fence_after();
+            tmem_load16(tm + P::COL_D3 + tq, z);
+            tmem_wait_ld();
+            if (ok)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (c * kC + tq + j < n) op[(static_cast<size_t>(c) * kC + j) * ostep] = __uint_as_float(z[j]);
+        }
+        if (ok)
+#pragma unroll
+            for (int j = 0; j < DQ; j += 4) *reinterpret_cast<float4 *>(st + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == P::LOAD_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, P::TMEM_COLS);
+    }
+}
+
 // ------------------------------------------------------------------ host side
-constexpr int64_t kBudget = 256ll << 20;            // of workspace: chunks beyond it follow in further launches
+constexpr int64_t kBudget = 192ll << 20;            // of workspace: chunks beyond it follow in further launches
 
 int64_t unit_bytes(const gdn_advance_dims *d) { return d->dk == 64 ? Unit<64>::BYTES : Unit<128>::BYTES; }
+int all_chunks(const gdn_advance_dims *d) { return (d->T + kC - 1) / kC; }
 int seqs_per_launch(const gdn_advance_dims *d) {
-    const int64_t n = kBudget / (unit_bytes(d) * d->H);
+    const int64_t n = kBudget / 2 / (unit_bytes(d) * d->H);
     return static_cast<int>(n < 1 ? 1 : n < d->B ? n : d->B);
 }
+// Chunks of a launch pair: a sixth of them, so that the first kernel's work for the next ones runs beside the walk; all where
+// there are few (a pair's beginning and end cost about as much as four chunks).
 int chunks_per_launch(const gdn_advance_dims *d) {
-    const int64_t all = (d->T + kC - 1) / kC, n = kBudget / (unit_bytes(d) * d->H * seqs_per_launch(d));
-    return static_cast<int>(n < 1 ? 1 : n < all ? n : all);
+    const int64_t all = all_chunks(d), most = kBudget / 2 / (unit_bytes(d) * d->H * seqs_per_launch(d));
+    int64_t n = all <= 16 ? all : (all + 5) / 6 < 8 ? 8 : (all + 5) / 6;
+    if (n > most) n = most < 1 ? 1 : most;
+    return static_cast<int>(n);
+}
+int buffers(const gdn_advance_dims *d) {
+    return chunks_per_launch(d) < all_chunks(d) || seqs_per_launch(d) < d->B ? 2 : 1;
 }
 
 // Keys or queries as [B T][Hk][dk]; boxes of 64 columns of one head, 64 tokens.
@@ -694,24 +994,33 @@ bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DK, int NS>
-int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
-    using P = ScanPlan<DK, NS>;
+// The launches alternate: prep 0, walk 0, prep 1, walk 1, ..  Prep k + 1 needs nothing of walk k and runs beside it: it does not wait
+// for the launch before it at its start (that launch's blocks have by then waited for prep k, so all that came before
+// is over), but one of its CTAs does at its end, so that walk k + 1, which waits for prep k + 1, also comes
+// after walk k.  Two workspaces: prep k + 1 begins when walk k has, and so after walk k - 1, the last reader of its own.
+template <int DK>
+int launch(const gdn_advance_dims *d, const AdvanceArgs &a, bool heads, cudaStream_t s) {
     CUtensorMap mk, mq;
     if (!token_map(&mk, a.k, d, d->k_stride) || !token_map(&mq, a.q, d, d->q_stride)) return GDN_ERR_LAUNCH;
     if (cudaFuncSetAttribute(advance_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepPlan<DK>::BYTES) != cudaSuccess ||
-        cudaFuncSetAttribute(advance_scan_kernel<DK, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES) != cudaSuccess)
+        cudaFuncSetAttribute(advance_slice_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, SlicePlan<DK>::BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(advance_head_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, HeadPlan<DK>::BYTES) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    const int all = (d->T + kC - 1) / kC, step = chunks_per_launch(d), seqs = seqs_per_launch(d);
-    TcAdvance ta{a, 0, 0, 0, d->dv};
+    const int all = all_chunks(d), step = chunks_per_launch(d), seqs = seqs_per_launch(d);
+    const int64_t half = unit_bytes(d) * d->H * seqs * step;
+    TcAdvance ta{a, 0, 0, 0, d->dv, 0};
     for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += seqs)
         for (ta.c0 = 0; ta.c0 < all; ta.c0 += step) {
             const int nb = d->B - ta.b0 < seqs ? d->B - ta.b0 : seqs;
             ta.chunks = all - ta.c0 < step ? all - ta.c0 : step;
-            if (launch_pdl(advance_prep_kernel<DK>, dim3(d->H, ta.chunks, nb), dim3(kPrepThreads), PrepPlan<DK>::BYTES, s, ta) != cudaSuccess ||
-                launch_pdl(advance_scan_kernel<DK, NS>, dim3(d->dv / (NS * kSlice), d->H, nb), dim3(P::THREADS), P::BYTES, s, mk, mq, ta) !=
-                    cudaSuccess)
-                return GDN_ERR_LAUNCH;
+            cudaError_t e = launch_pdl(advance_prep_kernel<DK>, dim3(d->H, ta.chunks, nb), dim3(kPrepThreads), PrepPlan<DK>::BYTES, s, ta);
+            if (e == cudaSuccess)
+                e = heads ? launch_pdl(advance_head_kernel<DK>, dim3(d->H, nb), dim3(HeadPlan<DK>::THREADS), HeadPlan<DK>::BYTES, s, mk, mq, ta)
+                          : launch_pdl(advance_slice_kernel<DK>, dim3(d->dv / kSlice, d->H, nb), dim3(SlicePlan<DK>::THREADS), SlicePlan<DK>::BYTES,
+                                       s, mk, mq, ta);
+            if (e != cudaSuccess) return GDN_ERR_LAUNCH;
+            ta.behind = 1;
+            ta.a.ws = ta.a.ws == a.ws ? a.ws + half : a.ws;
         }
     return GDN_OK;
 }
@@ -722,13 +1031,13 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
 bool advance_tc_shape(const gdn_advance_dims *d) { return d->in_dtype == GDN_DTYPE_BF16 && d->T > 32; }
 
 int64_t advance_tc_workspace(const gdn_advance_dims *d) {
-    return unit_bytes(d) * d->H * seqs_per_launch(d) * chunks_per_launch(d);
+    return unit_bytes(d) * d->H * seqs_per_launch(d) * chunks_per_launch(d) * buffers(d);
 }
 
 int advance_tc(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
-    // Slices of a CTA: one where that leaves SMs without work, else two.
-    const bool one = static_cast<long long>(d->B) * d->H * (d->dv / kSlice) <= sm_count();
-    return d->dk == 64 ? (one ? launch<64, 1>(d, a, s) : launch<64, 2>(d, a, s)) : one ? launch<128, 1>(d, a, s) : launch<128, 2>(d, a, s);
+    // By slices while each has an SM of its own; by heads beyond (which need 128 value columns).
+    const bool heads = d->dv == 128 && static_cast<long long>(d->B) * d->H * (d->dv / kSlice) > sm_count();
+    return d->dk == 64 ? launch<64>(d, a, heads, s) : launch<128>(d, a, heads, s);
 }
 
 }  // namespace gdn
