@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 
 #include "advance_common.h"
+#include "pair_math.cuh"
 #include "tc_async.cuh"
 
 namespace gdn {
@@ -54,19 +55,23 @@ struct TcAdvance {
 __device__ __forceinline__ int tokens_here(const TcAdvance &ta, int n) { return max(0, min(n - ta.c0 * kC, ta.chunks * kC)); }
 
 // Two numbers as three packed bf16 terms each, 8 bits of the mantissa after the other (so their sum is the number; NaN stays).
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&t)[3]) {
-    const uint32_t mask = 0xffff0000u;
-    const float xm = x - __uint_as_float(__float_as_uint(x) & mask), ym = y - __uint_as_float(__float_as_uint(y) & mask);
-    t[0] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-    t[1] = __byte_perm(__float_as_uint(xm), __float_as_uint(ym), 0x7632);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(xm - __uint_as_float(__float_as_uint(xm) & mask), ym - __uint_as_float(__float_as_uint(ym) & mask));
+__device__ __forceinline__ void split_pair(float2 x, uint32_t (&t)[3]) {
+    const float2 minus = make_float2(-1.f, -1.f);
+    auto high = [](float2 y) {
+        return make_float2(__uint_as_float(__float_as_uint(y.x) & 0xffff0000u), __uint_as_float(__float_as_uint(y.y) & 0xffff0000u));
+    };
+    const float2 m = fma2(high(x), minus, x);
+    t[0] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+    t[1] = __byte_perm(__float_as_uint(m.x), __float_as_uint(m.y), 0x7632);
+    const float2 r = fma2(high(m), minus, m);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(r.x, r.y);
     t[2] = *reinterpret_cast<const uint32_t *>(&l);
 }
 // Eight of them as one 16-byte chunk of each term.
 __device__ __forceinline__ void split8(const float *y, uint4 (&t)[3]) {
     uint32_t p[4][3];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split_pair(y[2 * i], y[2 * i + 1], p[i]);
+    for (int i = 0; i < 4; ++i) split_pair(make_float2(y[2 * i], y[2 * i + 1]), p[i]);
 #pragma unroll
     for (int k = 0; k < 3; ++k) t[k] = make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
 }
@@ -412,13 +417,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
 // (about 2600 cycles a chunk).  S and x are the B operands: rows of 32 first, 32 second and 32 third terms, so one product of
 // 96 columns has all of them (55 cycles an MMA, against 39 for 32 columns).
 template <int DK> struct SlicePlan {
-    static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES, MP = 3 * Unit<DK>::MP_BYTES;
+    static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES;
+    static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4, V_AT = 3 * Unit<DK>::MP_BYTES + 1024, MP = V_AT + kC * kSlice * 2;   // M P and gamma, values
     static constexpr int S_ATOM = DK * 128, X_ATOM = kC * 128;         // first and second terms, then the third in an atom of its own
     static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + E, OFF_S = OFF_MP + 2 * MP, OFF_X = OFF_S + 2 * S_ATOM;
     static constexpr int OFF_BAR = OFF_X + 2 * X_ATOM, BYTES = OFF_BAR + 256;
     static constexpr int ROWS = 256, LOAD_WARP = 8, MMA_WARP = 9, THREADS = 320;
     static constexpr int N = 96, TMEM_COLS = 512;                      // columns of a product: [K;Q] S^T, E x, M P x
-    static_assert(BYTES <= 227 * 1024 && OFF_E >= 8192, "plan");
+    static_assert(BYTES <= 227 * 1024 && OFF_E >= 8192 && MP % 1024 == 0, "plan");
 };
 
 // A thread's 16 numbers as three bf16 terms in row `row` of a tile: 32 first, 32 second ones, and 32 third ones an atom on.
@@ -469,7 +475,7 @@ __device__ __forceinline__ bool begin_walk(const TcAdvance &ta, const AdvanceSeq
 template <int DK>
 __global__ void __launch_bounds__(SlicePlan<DK>::THREADS, 1)
 advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
-                     const __grid_constant__ TcAdvance ta)
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcAdvance ta)
 {
     using P = SlicePlan<DK>;
     const AdvanceArgs &a = ta.a;
@@ -507,8 +513,8 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const size_t ustep = static_cast<size_t>(a.H) * Unit<DK>::BYTES;
     if (warp == P::LOAD_WARP) {
         // ------------------------------------------------------ loads
-        // Keys and queries go when the first product of two chunks before is done, E after its one use in the chunk before, M P
-        // after the last product of two before.  (With one barrier for all, a chunk's operands came no sooner
+        // Keys and queries go when the first product of two chunks before is done, M P (with gamma and the values) after the last
+        // product of two before, and E, the last to be free, after its one use in the chunk before.  (With one barrier for all, a chunk's operands came no sooner
         // than they were needed: 3000 cycles a chunk instead of 2400.)
         const int hk = h / (a.H / a.Hk);
         int c = 0, part = 0;
@@ -529,26 +535,28 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
             __syncwarp();
             part = 1;
+            if (c >= 2 && !wait(&empty_m[st], before)) break;
+            if (elect_one()) {
+                uint8_t *dst = smem + P::OFF_MP + st * P::MP;
+                mbar_expect_tx(&full_m[st], P::M_BYTES + kC * kSlice * 2);
+                bulk_load(dst, unit + Unit<DK>::OFF_MP, P::M_BYTES, &full_m[st]);
+                tma_load_3d(dst + P::V_AT, &tm_v, dv0, h, b * a.T + (ta.c0 + c) * kC, &full_m[st]);
+            }
+            __syncwarp();
+            part = 2;
             if (c >= 1 && !wait(empty_e, (c - 1) & 1)) break;
             if (elect_one()) {
                 mbar_expect_tx(full_e, P::E);
                 bulk_load(smem + P::OFF_E, unit, P::E, full_e);
             }
             __syncwarp();
-            part = 2;
-            if (c >= 2 && !wait(&empty_m[st], before)) break;
-            if (elect_one()) {
-                mbar_expect_tx(&full_m[st], P::MP);
-                bulk_load(smem + P::OFF_MP + st * P::MP, unit + Unit<DK>::OFF_MP, P::MP, &full_m[st]);
-            }
-            __syncwarp();
         }
         if (*abort) {                               // copies in flight end before the CTA does
             bool done = true;
-            const int keys = c < chunks && part > 0 ? c + 1 : c, es = c < chunks && part > 1 ? c + 1 : c;   // chunks whose keys, whose E have been requested
+            const int keys = c < chunks && part > 0 ? c + 1 : c, ms = c < chunks && part > 1 ? c + 1 : c;   // chunks whose keys, whose M P have been requested
             for (int i = max(0, keys - 2); i < keys; ++i) done = done && mbar_wait(&full_k[i & 1], (i >> 1) & 1);
-            if (es > 0) done = done && mbar_wait(full_e, (es - 1) & 1);
-            for (int i = max(0, c - 2); i < c; ++i) done = done && mbar_wait(&full_m[i & 1], (i >> 1) & 1);
+            for (int i = max(0, ms - 2); i < ms; ++i) done = done && mbar_wait(&full_m[i & 1], (i >> 1) & 1);
+            if (c > 0) done = done && mbar_wait(full_e, (c - 1) & 1);
             if (!done && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
         }
     } else if (warp == P::MMA_WARP) {
@@ -605,61 +613,43 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
         for (int j = 0; j < 16; ++j) S[j] = has && !zero ? st[j * DK] : 0.f;
         const size_t tok0 = static_cast<size_t>(b) * a.T + ta.c0 * kC + t;
-        const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v) + tok0 * a.v_stride + h * ta.dv + col0;
         float *op = a.out + (tok0 * a.H + h) * ta.dv + col0;
-        // values, gamma_t and gamma of the chunk's end, two chunks ahead
-        struct Ahead {
-            uint4 v[2];
-            float gam, gend;
-        } now, next;
-        auto fetch = [&](Ahead &f, int c) {
-            const float *gp = reinterpret_cast<const float *>(units + c * ustep + Unit<DK>::OFF_GAMMA);
-            f.v[0] = f.v[1] = make_uint4(0u, 0u, 0u, 0u);
-            f.gam = f.gend = 0.f;
-            if (c >= chunks) return;
-            f.gam = __ldcg(gp + t);
-            f.gend = __ldcg(gp + kC - 1);
-            if (keys && c * kC + t < n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) f.v[i] = __ldg(reinterpret_cast<const uint4 *>(vp + static_cast<size_t>(c) * kC * a.v_stride) + i);
-        };
         auto arrive = [&](uint64_t *bar) {          // for the warp, behind each lane's fences
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        fetch(now, 0);
-        fetch(next, 1);
         if (has) put_row(sS, P::S_ATOM, row, half, S);
         fence_proxy_async();
         arrive(s_ready);
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
             float y[16], o[16];
-            ok = wait(d1, c & 1);
+            const uint8_t *slot = smem + P::OFF_MP + (c & 1) * P::MP;
+            const float *gam = reinterpret_cast<const float *>(slot + 3 * Unit<DK>::MP_BYTES);
+            ok = wait(&full_m[c & 1], (c >> 1) & 1) && wait(d1, c & 1);
             if (!ok) break;
             tc_fence_after();
             get_row(tm, y);
             if (keys) {                             // x = v - gamma S k; nothing of rows past the last token
                 const bool live = c * kC + t < n;
+                const float f = -gam[t];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float f[8];
-                    bf16x8_to_f32(now.v[i], f);
+                    float v[8];
+                    bf16x8_to_f32(*reinterpret_cast<const uint4 *>(slot + P::V_AT + t * (kSlice * 2) + 32 * half + 16 * i), v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[8 * i + e] = live ? fmaf(-now.gam, y[8 * i + e], f[e]) : 0.f;
+                    for (int e = 0; e < 8; ++e) y[8 * i + e] = live ? fmaf(f, y[8 * i + e], v[e]) : 0.f;
                 }
                 put_row(sX, P::X_ATOM, t, half, y);
                 fence_proxy_async();
             } else {
-                const float f = now.gam * a.scale;
+                const float f = gam[t] * a.scale;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) o[j] = f * y[j];
             }
-            const float ge = now.gend;
+            const float ge = gam[kC - 1];
             tc_fence_before();
             arrive(x_ready);                        // this row has read [K;Q] S^T (and, before it, the last M P x)
-            now = next;
-            fetch(next, c + 2);
             ok = wait(d2, c & 1);
             if (!ok) break;
             tc_fence_after();
@@ -706,11 +696,11 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 //
 // TMEM columns: S (three terms, dk / 2 each), [K;Q] S^T and over it x (three terms of 32), E x, M P x.
 template <int DK> struct HeadPlan {
-    static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES, MP = 3 * Unit<DK>::MP_BYTES + 1024;       // M P, gamma
-    static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + 2 * E, OFF_BAR = OFF_MP + 2 * MP, BYTES = OFF_BAR + 256;
+    static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES;
+    static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4, V_AT = 3 * Unit<DK>::MP_BYTES + 1024, MP = V_AT + kC * 256;   // M P and gamma, values
+    static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + E, OFF_BAR = OFF_MP + 2 * MP, BYTES = OFF_BAR + 256;
     static constexpr int ROWS = 512, LOAD_WARP = 16, MMA_WARP = 17, THREADS = 576;
     static constexpr int COL_D1 = 3 * DK / 2, COL_X = COL_D1, COL_D2 = COL_D1 + 128, COL_D3 = COL_D2 + DK, TMEM_COLS = 512;
-    static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4;    // copied: M P and gamma
     static_assert(COL_D3 + kC <= TMEM_COLS && BYTES <= 227 * 1024 && MP % 1024 == 0, "plan");
 };
 
@@ -719,15 +709,15 @@ template <int DK> struct HeadPlan {
 template <int DK>
 __global__ void __launch_bounds__(HeadPlan<DK>::THREADS, 1)
 advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
-                    const __grid_constant__ TcAdvance ta)
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcAdvance ta)
 {
     using P = HeadPlan<DK>;
     constexpr int DV = 128, DQ = DK / 4;            // key dimensions of a thread
     const AdvanceArgs &a = ta.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int h = blockIdx.x, b = ta.b0 + blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint64_t *full_k = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty_k = full_k + 2, *full_e = empty_k + 2, *empty_e = full_e + 2,
-             *full_m = empty_e + 2, *empty_m = full_m + 2, *d1 = empty_m + 2, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1,
+    uint64_t *full_k = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty_k = full_k + 2, *full_m = empty_k + 2, *empty_m = full_m + 2,
+             *full_e = empty_m + 2, *empty_e = full_e + 1, *d1 = empty_e + 1, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1,
              *x_ready = s_ready + 1, *drain = x_ready + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -777,27 +767,28 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             __syncwarp();
             part = 1;
-            if (c >= 2 && !wait(&empty_e[st], before)) break;
+            if (c >= 2 && !wait(&empty_m[st], before)) break;
             if (elect_one()) {
-                mbar_expect_tx(&full_e[st], P::E);
-                bulk_load(smem + P::OFF_E + st * P::E, unit, P::E, &full_e[st]);
+                uint8_t *dst = smem + P::OFF_MP + st * P::MP;
+                mbar_expect_tx(&full_m[st], P::M_BYTES + kC * 256);
+                bulk_load(dst, unit + Unit<DK>::OFF_MP, P::M_BYTES, &full_m[st]);
+                tma_load_3d(dst + P::V_AT, &tm_v, 0, h, b * a.T + (ta.c0 + c) * kC, &full_m[st]);
             }
             __syncwarp();
             part = 2;
-            if (c >= 2 && !wait(&empty_m[st], before)) break;
+            if (c >= 1 && !wait(empty_e, (c - 1) & 1)) break;
             if (elect_one()) {
-                mbar_expect_tx(&full_m[st], P::M_BYTES);
-                bulk_load(smem + P::OFF_MP + st * P::MP, unit + Unit<DK>::OFF_MP, P::M_BYTES, &full_m[st]);
+                mbar_expect_tx(full_e, P::E);
+                bulk_load(smem + P::OFF_E, unit, P::E, full_e);
             }
             __syncwarp();
         }
         if (*abort) {                               // copies in flight end before the CTA does
             bool done = true;
-            for (int p = 0; p < 3; ++p) {           // keys, E, M P: chunks that have been requested
-                uint64_t *full = p == 0 ? full_k : p == 1 ? full_e : full_m;
-                const int asked = c < chunks && part > p ? c + 1 : c;
-                for (int i = max(0, asked - 2); i < asked; ++i) done = done && mbar_wait(&full[i & 1], (i >> 1) & 1);
-            }
+            const int keys = c < chunks && part > 0 ? c + 1 : c, ms = c < chunks && part > 1 ? c + 1 : c;   // chunks whose keys, whose M P have been requested
+            for (int i = max(0, keys - 2); i < keys; ++i) done = done && mbar_wait(&full_k[i & 1], (i >> 1) & 1);
+            for (int i = max(0, ms - 2); i < ms; ++i) done = done && mbar_wait(&full_m[i & 1], (i >> 1) & 1);
+            if (c > 0) done = done && mbar_wait(full_e, (c - 1) & 1);
             if (!done && lane == 0) atomicOr(a.status, GDN_STATUS_DRAIN);
         }
     } else if (warp == P::MMA_WARP) {
@@ -818,15 +809,15 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             mma_commit_on(one, d1);
             mma_commit_on(one, &empty_k[st]);
-            ok = wait(&full_e[st], (c >> 1) & 1) && wait(x_ready, c & 1);
+            ok = wait(full_e, c & 1) && wait(x_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 24; ++k)
                 mma_bf16_ts_on(one, tm + P::COL_D2, tm + P::COL_X + kTermA[k >> 2] * 32 + (k & 3) * 8,
-                               desc_add(dE, st * P::E + kTermB[k >> 2] * Unit<DK>::E_BYTES + (k & 3) * 32), idesc_mn(1, 128, DK), k > 0);
+                               desc_add(dE, kTermB[k >> 2] * Unit<DK>::E_BYTES + (k & 3) * 32), idesc_mn(1, 128, DK), k > 0);
             mma_commit_on(one, d2);
-            mma_commit_on(one, &empty_e[st]);
+            mma_commit_on(one, empty_e);
             ok = wait(&full_m[st], (c >> 1) & 1);
             if (!ok) break;
 #pragma unroll
@@ -845,26 +836,16 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const int q4 = warp >> 2, row = tid & 127, tq = 16 * q4;      // this thread's first token of a chunk
         const uint32_t tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         float *st = a.state + ((static_cast<size_t>(sq.slot) * a.H + h) * DV + row) * DK + DQ * q4;
-        float S[DQ];
+        float2 S[DQ / 2];
 #pragma unroll
         for (int j = 0; j < DQ; j += 4) {
             const float4 x = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4 *>(st + j);
-            S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+            S[j / 2] = make_float2(x.x, x.y);
+            S[j / 2 + 1] = make_float2(x.z, x.w);
         }
         const size_t tok0 = static_cast<size_t>(b) * a.T + ta.c0 * kC + tq;
-        const unsigned short *vp = static_cast<const unsigned short *>(a.v) + tok0 * a.v_stride + h * DV + row;
         float *op = a.out + (tok0 * a.H + h) * DV + row;
         const size_t ostep = static_cast<size_t>(a.H) * DV;
-        uint32_t v[8];                              // pairs of tokens' values of this column
-        auto fetch = [&](int c) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int t = c * kC + tq + 2 * j;
-                const unsigned short *p = vp + (static_cast<size_t>(c) * kC + 2 * j) * a.v_stride;
-                const uint32_t lo = t < n ? __ldg(p) : 0u, hi = t + 1 < n ? __ldg(p + a.v_stride) : 0u;
-                v[j] = lo | hi << 16;
-            }
-        };
         auto put_state = [&]() {                    // S's terms: A operand, dk / 2 columns each
 #pragma unroll
             for (int j = 0; j < DQ; j += 16) {
@@ -872,7 +853,7 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint32_t t[3];
-                    split_pair(S[j + 2 * i], S[j + 2 * i + 1], t);
+                    split_pair(S[j / 2 + i], t);
                     w[0][i] = t[0]; w[1][i] = t[1]; w[2][i] = t[2];
                 }
 #pragma unroll
@@ -885,41 +866,44 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        fetch(0);
         put_state();
         arrive(s_ready);
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
             const int sm = c & 1;
             const float *gam = reinterpret_cast<const float *>(smem + P::OFF_MP + sm * P::MP + 3 * Unit<DK>::MP_BYTES);
-            ok = wait(&full_m[sm], (c >> 1) & 1) && ok;               // gamma
+            const unsigned short *val = reinterpret_cast<const unsigned short *>(smem + P::OFF_MP + sm * P::MP + P::V_AT) + tq * DV + row;
+            ok = wait(&full_m[sm], (c >> 1) & 1) && ok;               // gamma and the values
             ok = wait(d1, c & 1) && ok;
             tc_fence_after();
-            uint32_t y[16], z[16];
+            uint32_t y[16], z[16], w[3][8];
             tmem_load16(tm + P::COL_D1 + tq, y);
             tmem_load16(tm + P::COL_D1 + kC + tq, z);
             tmem_wait_ld();
+            const bool whole = (c + 1) * kC <= n;
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
-                const float4 g = *reinterpret_cast<const float4 *>(gam + tq + j);
-                const float gg[4] = {g.x, g.y, g.z, g.w};
+                const float4 g4 = *reinterpret_cast<const float4 *>(gam + tq + j);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {       // x = v - gamma S k; nothing of tokens past the last
-                    const uint32_t w = v[(j + e) >> 1];
-                    const float f = __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
-                    y[j + e] = __float_as_uint(fmaf(-gg[e], __uint_as_float(y[j + e]), f)) & (c * kC + tq + j + e < n ? 0xffffffffu : 0u);
-                    z[j + e] = __float_as_uint(gg[e] * a.scale * __uint_as_float(z[j + e]));
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 g = e ? make_float2(g4.z, g4.w) : make_float2(g4.x, g4.y);
+                    // x = v - gamma S k; nothing of tokens past the last
+                    float2 x = fma2(make_float2(-g.x, -g.y), make_float2(__uint_as_float(y[j + e]), __uint_as_float(y[j + e + 1])),
+                                    make_float2(__uint_as_float(val[(j + e) * DV] << 16), __uint_as_float(val[(j + e + 1) * DV] << 16)));
+                    if (!whole) {
+                        x.x = c * kC + tq + j + e < n ? x.x : 0.f;
+                        x.y = c * kC + tq + j + e + 1 < n ? x.y : 0.f;
+                    }
+                    uint32_t t[3];
+                    split_pair(x, t);
+                    w[0][(j + e) / 2] = t[0]; w[1][(j + e) / 2] = t[1]; w[2][(j + e) / 2] = t[2];
+                    const float2 o = mul2(mul2(g, make_float2(a.scale, a.scale)), make_float2(__uint_as_float(z[j + e]), __uint_as_float(z[j + e + 1])));
+                    z[j + e] = __float_as_uint(o.x);
+                    z[j + e + 1] = __float_as_uint(o.y);
                 }
             }
             const float ge = gam[kC - 1];
             tmem_st16(tm + P::COL_D3 + tq, z);      // (the last M P x has been read)
-            uint32_t w[3][8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t t[3];
-                split_pair(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]), t);
-                w[0][i] = t[0]; w[1][i] = t[1]; w[2][i] = t[2];
-            }
             tc_fence_before();
             bar_sync(1 + (warp & 3), 128);          // these lanes' [K;Q] S^T has been read: x goes over it
             tc_fence_after();
@@ -928,7 +912,6 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             tmem_wait_st();
             tc_fence_before();
             arrive(x_ready);
-            if (c + 1 < chunks) fetch(c + 1);
             ok = wait(d2, c & 1) && ok;
             tc_fence_after();
 #pragma unroll
@@ -936,7 +919,8 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 tmem_load16(tm + P::COL_D2 + DQ * q4 + j, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[j + i] = fmaf(ge, S[j + i], __uint_as_float(y[i]));
+                for (int i = 0; i < 16; i += 2)
+                    S[(j + i) / 2] = fma2(make_float2(ge, ge), S[(j + i) / 2], make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
             }
             put_state();
             arrive(s_ready);
@@ -951,7 +935,7 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
         if (ok)
 #pragma unroll
-            for (int j = 0; j < DQ; j += 4) *reinterpret_cast<float4 *>(st + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+            for (int j = 0; j < DQ; j += 4) *reinterpret_cast<float4 *>(st + j) = make_float4(S[j / 2].x, S[j / 2].y, S[j / 2 + 1].x, S[j / 2 + 1].y);
         tc_fence_before();
     }
     __syncthreads();
@@ -982,16 +966,16 @@ int buffers(const gdn_advance_dims *d) {
     return chunks_per_launch(d) < all_chunks(d) || seqs_per_launch(d) < d->B ? 2 : 1;
 }
 
-// Keys or queries as [B T][Hk][dk]; boxes of 64 columns of one head, 64 tokens.
-bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int64_t stride) {
+// Keys, queries or values as [B T][heads][dim]; boxes of `cols` columns of one head, 64 tokens.
+bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int heads, int dim, int64_t stride, int cols, bool swizzle) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d->dk), static_cast<cuuint64_t>(d->Hk), static_cast<cuuint64_t>(d->B) * d->T};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d->dk) * 2, static_cast<cuuint64_t>(stride) * 2};
-    cuuint32_t box[3] = {64, 1, kC}, estr[3] = {1, 1, 1};
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(d->B) * d->T};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(dim) * 2, static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), 1, kC}, estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The launches alternate: prep 0, walk 0, prep 1, walk 1, ..  Prep k + 1 needs nothing of walk k and runs beside it: it does not wait
@@ -1000,8 +984,10 @@ bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int6
 // after walk k.  Two workspaces: prep k + 1 begins when walk k has, and so after walk k - 1, the last reader of its own.
 template <int DK>
 int launch(const gdn_advance_dims *d, const AdvanceArgs &a, bool heads, cudaStream_t s) {
-    CUtensorMap mk, mq;
-    if (!token_map(&mk, a.k, d, d->k_stride) || !token_map(&mq, a.q, d, d->q_stride)) return GDN_ERR_LAUNCH;
+    CUtensorMap mk, mq, mv;
+    if (!token_map(&mk, a.k, d, d->Hk, d->dk, d->k_stride, 64, true) || !token_map(&mq, a.q, d, d->Hk, d->dk, d->q_stride, 64, true) ||
+        !token_map(&mv, a.v, d, d->H, d->dv, d->v_stride, heads ? 128 : kSlice, false))
+        return GDN_ERR_LAUNCH;
     if (cudaFuncSetAttribute(advance_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepPlan<DK>::BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(advance_slice_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, SlicePlan<DK>::BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(advance_head_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, HeadPlan<DK>::BYTES) != cudaSuccess)
@@ -1015,9 +1001,9 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, bool heads, cudaStre
             ta.chunks = all - ta.c0 < step ? all - ta.c0 : step;
             cudaError_t e = launch_pdl(advance_prep_kernel<DK>, dim3(d->H, ta.chunks, nb), dim3(kPrepThreads), PrepPlan<DK>::BYTES, s, ta);
             if (e == cudaSuccess)
-                e = heads ? launch_pdl(advance_head_kernel<DK>, dim3(d->H, nb), dim3(HeadPlan<DK>::THREADS), HeadPlan<DK>::BYTES, s, mk, mq, ta)
+                e = heads ? launch_pdl(advance_head_kernel<DK>, dim3(d->H, nb), dim3(HeadPlan<DK>::THREADS), HeadPlan<DK>::BYTES, s, mk, mq, mv, ta)
                           : launch_pdl(advance_slice_kernel<DK>, dim3(d->dv / kSlice, d->H, nb), dim3(SlicePlan<DK>::THREADS), SlicePlan<DK>::BYTES,
-                                       s, mk, mq, ta);
+                                       s, mk, mq, mv, ta);
             if (e != cudaSuccess) return GDN_ERR_LAUNCH;
             ta.behind = 1;
             ta.a.ws = ta.a.ws == a.ws ? a.ws + half : a.ws;
