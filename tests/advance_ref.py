@@ -32,10 +32,11 @@ def advance_bound(norm, eff, dk, chunked):
     A step alpha S (I - beta k k^T) + beta v k^T does not lengthen a difference by more than alpha (|k| = 1 up to
     its rounding), so errors of steps add up to eff times the largest.  Token by token, a step's is that of two sums of dk
     products and a few roundings, each 2^-24 of the norms: (dk + 8) 2^-24 norm.  Chunked: the products of 64 tokens with
-    S, with x and of E and MP take operands of two bf16 terms each (2^-17 of an operand is left out, and the
-    product of the two second terms, 2^-18); three such products in a row on S's path and on the update's, rows of up to
-    dk + 64 summands in fp32: 2^-14 + (dk + 64) 2^-23 of the norms, once per chunk and so at most once per step."""
-    step = 2.0 ** -14 + (dk + 64) * 2.0 ** -23 if chunked else (dk + 8) * 2.0 ** -24
+    S, with x and of E and MP take operands of three bf16 terms each, which are exact; left out of a product of two such
+    operands are its parts of the third order, 2 * 2^-7 * 2^-14 of the norms, in E x, in (MP) x and in MP itself; the
+    sums, rows of up to dk + 64 summands in fp32 (2^-23: added without rounding to nearest), lie on S's path and on
+    the update's: 2^-18 + (dk + 64) 2^-22 of the norms, once per chunk and so at most once per step."""
+    step = 2.0 ** -18 + (dk + 64) * 2.0 ** -22 if chunked else (dk + 8) * 2.0 ** -24
     return 1.01 * eff * step * norm + 1e-30
 
 

@@ -119,6 +119,37 @@ def test_advance_gates(gates, dk, dv):
     c.check(True)
 
 
+def ragged(B, T, seed):
+    """Lengths of B sequences in chunks of T, among them T, 0 and what lies around a tile's end."""
+    g = np.random.default_rng(seed)
+    lens = g.integers(0, T + 1, B)
+    edge = [x for x in (T, 0, 1, 32, 33, 63, 64, 65, T - 1) if x <= T][:B]
+    lens[g.permutation(B)[:len(edge)]] = edge
+    return [int(x) for x in lens]
+
+
+@pytest.mark.parametrize("B,T,H,Hk,dk,dv", [
+    (20, 140, 2, 1, 128, 128),               # heads walked whole
+    (20, 150, 2, 2, 64, 128),
+    (3, 1100, 2, 1, 128, 128),               # a long prompt's further launches, by slices
+    (2, 1300, 3, 3, 64, 64),
+    (3, 1100, 14, 7, 128, 128),              # and by heads
+    (4, 1090, 10, 10, 64, 128),
+    (110, 40, 16, 4, 128, 128),              # more sequences than a launch's workspace holds
+])
+def test_advance_many_heads_and_long_prompts(B, T, H, Hk, dk, dv):
+    lens = ragged(B, T, T)
+    c = Case(lens, T, H, Hk, dk, dv, BF, seed=19, fresh=[b % 3 == 1 for b in range(B)])
+    c.run()
+    first = c.out.clone(), c.layer.t["state"].clone()
+    c.check(True)
+    c.layer.t["state"].copy_(c.state)
+    c.out.fill_(5)
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, first[0]) and torch.equal(c.layer.t["state"], first[1])
+
+
 def test_advance_in_pieces_is_the_whole():
     """A prompt in chunks of odd lengths, then single tokens: the state is that of one call, within the bound."""
     c = Case([256], 256, 4, 4, 128, 128, BF, seed=13)
