@@ -765,6 +765,8 @@ class AttnLayer:
         _check("gdn_attn_chunk_workspace", min(need, 0))
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        # (a layer of more tokens than a verify takes may be there for stage alone: chunk refuses what is too small)
+        self._chunk_need, need = need, need if dims.T <= 64 else 0
         self.workspace, self.state_idx = workspace, state_idx
         self._keep = (q_weight, k_weight, cos_sin, state_idx, workspace)     # the calls use their addresses
         self._index = at = cache._index
@@ -853,6 +855,8 @@ class AttnLayer:
         over the committed tokens and the chunk's own into ``out`` (and ``lse`` fp32 [B, T, Hq]).  chunk_len
         int32 [B]: tokens in use (None: T, any number that the layer was made for).  seq_len does not move:
         accept the chunk, or write the new lengths, afterwards."""
+        if self._ws_bytes < self._chunk_need:
+            raise ValueError(f"chunk: needs a workspace of at least {self._chunk_need} bytes, got {self._ws_bytes}")
         t, e, cache, at = self._dtype, self._elems, self.cache, self._index
         rc = self._lib.gdn_attn_chunk(
             cache._c, self.layer, self._ref, self._idx,

@@ -197,3 +197,33 @@ def test_expired_wait_writes_nothing(d):
     c.cache.status.zero_()
     c.run()                                                  # and the next call is sound
     c.check()
+
+
+def test_a_layer_for_staging_takes_a_smaller_workspace():
+    """A layer of more tokens than a verify takes may share a verify's workspace; chunk refuses one that it needs more of."""
+    import speculative_decode_recurrent_gb300 as lib
+    c = Case([500], [100], 100, 4, 2, 128, 16, BF, seed=39)
+    idx = c.layer.state_idx
+    dims = lib.AttnDims(B=1, T=100, Hq=4, scale=c.scale)
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    layer = lib.AttnLayer(dims, c.cache, 1, state_idx=idx, workspace=small)
+    assert c.layer.workspace.numel() > 16
+    with pytest.raises(ValueError, match="chunk: needs a workspace"):
+        layer.chunk(c.qd, c.out)
+    with pytest.raises(ValueError, match="workspace"):
+        lib.AttnLayer(lib.AttnDims(B=1, T=64, Hq=4, scale=c.scale), c.cache, 1, state_idx=idx, workspace=small)
+    other = lib.AttnLayer(dims, c.cache, 1, state_idx=idx, workspace=c.layer.workspace)
+    other.chunk(c.qd, c.out, lse=c.lse, chunk_len=i32(c.lens))
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_no_sequences_and_wrong_tensors(dtype):
+    import speculative_decode_recurrent_gb300 as lib
+    c = Case([30], [70], 70, 4, 2, 128, 16, dtype, seed=40)
+    none = lib.AttnLayer(lib.AttnDims(B=0, T=70, Hq=4, scale=c.scale), c.cache, 0)
+    none.chunk(c.qd[:0], c.out[:0])
+    for bad in (c.qd[:, :69].contiguous(), c.qd.float() if dtype == BF else c.qd.bfloat16(), c.qd.cpu(), c.qd.transpose(1, 2)):
+        with pytest.raises((ValueError, TypeError)):
+            c.layer.chunk(bad, c.out)
+    assert (c.out == 7).all()
