@@ -5,7 +5,8 @@ Each step drafts a chain of T tokens per sequence.  A recurrent layer verifies i
 checkpoint and buffer; the attention layer stages the chain's keys and values in its pages and
 attends over them and the context.  Accepting p tokens moves two lengths.  Between the steps a
 sequence is forked and one is released.  A second attention cache then verifies a token tree and
-commits one of its paths.
+commits one of its paths.  At last a stack of a convolution, a recurrent and an attention layer takes
+prompts in chunks, then decodes: drafts of a bigram table, verified, accepted by speculative sampling.
 
     python examples/hybrid_decode.py            # needs a GB300
 """
@@ -42,9 +43,13 @@ def recurrent_layer(g):
     return lib.ReplayLayer(dims, init)
 
 
-def attention(cache, g, tokens):
+def norm_weights(g):
+    return (1 + 0.1 * torch.randn(2, D, generator=g)).cuda()
+
+
+def attention(cache, g, tokens, w=None):
     rope = lib.RopeDims(rot=64, style=lib.ROPE_HALF, max_pos=512, eps=1e-6)
-    w = (1 + 0.1 * torch.randn(2, D, generator=g)).cuda()
+    w = norm_weights(g) if w is None else w
     return lib.AttnLayer(lib.AttnDims(B=B, T=tokens, Hq=H, scale=D ** -0.5), cache, 0, rope, w[0], w[1],
                          angles(512, 64), state_idx=torch.arange(B, dtype=torch.int32, device="cuda"))
 
@@ -127,8 +132,120 @@ def run_tree(seed=2):
                 status=int(cache.status.item()))
 
 
+V, W, PART, C = 97, 4, 100, 3 * H * D                       # vocabulary, convolution width, tokens of a prompt's chunk, channels
+
+
+class Stack:
+    """A convolution over the channels of q, k and v, a recurrent layer, an attention layer and a head, with random weights."""
+
+    def __init__(self, g):
+        def weight(n, m):
+            return (torch.randn(n, m, generator=g) * n ** -0.5).bfloat16().cuda()
+
+        self.embed = torch.randn(V, C, generator=g).bfloat16().cuda()
+        self.gate = (-torch.rand(V, H, generator=g)).cuda()
+        self.beta = torch.rand(V, H, generator=g).cuda()
+        self.w_qkv, self.w_out = weight(H * D, (H + 2 * HKV) * D), weight(H * D, V)
+        self.drafter = torch.randn(V, V, generator=g).softmax(-1).cuda()
+        dims = lib.ConvDims(B=B, D=C, W=W, T=T, cap=W - 1 + T, n_slot=SLOTS, act=lib.CONV_ACT_SILU, in_dtype=lib.DTYPE_BF16,
+                            out_dtype=lib.DTYPE_BF16)
+        self.conv = lib.ConvLayer(dims, dict(ring=torch.zeros(SLOTS, dims.cap, C, dtype=torch.bfloat16),
+                                             pos=torch.zeros(SLOTS, dtype=torch.int32),
+                                             state_idx=torch.arange(B, dtype=torch.int32),
+                                             weight=0.5 * torch.randn(C, W, generator=g)))
+        self.gdn, self.cache = recurrent_layer(g), page_cache()
+        w = norm_weights(g)                                 # one layer, for chunks of a prompt and for drafts
+        self.part, self.block = (attention(self.cache, g, n, w) for n in (PART, T))
+
+    def mixed(self, tokens, y):
+        """q, k, v, log-decays and update rates from the convolution's outputs."""
+        q, k, v = (x.unflatten(-1, (H, D)) for x in y.split(H * D, -1))
+        return unit(q.float()).bfloat16(), unit(k.float()).bfloat16(), v, self.gate[tokens], self.beta[tokens]
+
+    def projected(self, out):
+        qkv = (out.bfloat16().flatten(2) @ self.w_qkv).split([H * D, HKV * D, HKV * D], -1)
+        return [p.unflatten(-1, (-1, D)) for p in qkv]
+
+    def probs(self, att):
+        return (att.flatten(2) @ self.w_out).float().softmax(-1)
+
+    def prompt(self, tokens, n, fresh):
+        """A chunk of n[b] committed tokens; the target's distribution after the last of them."""
+        y = torch.empty(B, PART, C, dtype=torch.bfloat16, device="cuda")
+        self.conv.advance(self.embed[tokens], y, chunk_len=n, fresh=fresh)
+        out = torch.empty(B, PART, H, D, device="cuda")
+        self.gdn.advance(*self.mixed(tokens, y), out, chunk_len=n, fresh=fresh)
+        q, att = (torch.empty(B, PART, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        self.cache.reserve(i32(range(B)), PART)
+        self.part.stage(*self.projected(out), q, draft_len=n)
+        self.part.chunk(q, att, chunk_len=n)
+        self.cache.seq_len[:B] += n
+        return self.probs(att)[torch.arange(B, device="cuda"), (n - 1).clamp(min=0).long()]
+
+    def verify(self, tokens):
+        """The target's distributions after each token of a block."""
+        y = torch.empty(B, T, C, dtype=torch.bfloat16, device="cuda")
+        self.conv.verify(self.embed[tokens], y)
+        out = torch.empty(B, T, H, D, device="cuda")
+        self.gdn.verify(*(x.contiguous() for x in self.mixed(tokens, y)), out)
+        q, att = (torch.empty(B, T, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        self.cache.reserve(i32(range(B)), T)
+        self.block.stage(*self.projected(out), q)
+        self.block.verify(q, att)
+        return self.probs(att), q, att
+
+    def accept(self, p):
+        self.conv.accept(p)
+        self.gdn.accept(p)
+        self.gdn.flush()
+        self.cache.accept(p, state_idx=i32(range(B)), T=T)
+
+
+def run_prompt(lens=(150, 70, 1), rounds=5, seed=3):
+    """Prompts of the given lengths in chunks, then rounds of speculative decoding.  Returns the stack, each sequence's
+    committed tokens and what each round's sampling took and gave (for the tests)."""
+    g = torch.Generator().manual_seed(seed)
+    s = Stack(g)
+    prompts = torch.randint(0, V, (B, -(-max(lens) // PART) * PART), generator=g)
+    first = torch.empty(B, V, device="cuda")
+    for at in range(0, max(lens), PART):
+        n = i32([min(max(x - at, 0), PART) for x in lens])
+        p = s.prompt(prompts[:, at:at + PART].cuda(), n, fresh=i32([at == 0] * B))
+        first = torch.where((n > 0)[:, None], p, first)
+    # the first token after the prompt: a block of one, nothing to accept
+    one = lib.DraftSampler(lib.DraftDims(B=B, T=1, V=V))
+    sampler = lib.DraftSampler(lib.DraftDims(B=B, T=T, V=V))
+    taken, cur = torch.empty(B, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    one.accept(torch.zeros(B, 1, dtype=torch.int32, device="cuda"), first[:, None].contiguous(), torch.rand(B, 1, generator=g).cuda(),
+               taken, cur)
+    committed = [prompts[b, :n].tolist() for b, n in enumerate(lens)]
+    log = []
+    for _ in range(rounds):
+        tokens = cur[:, None]
+        for _ in range(T - 1):                              # the drafter's chain
+            q = s.drafter[tokens[:, -1].long()].cpu()
+            tokens = torch.cat([tokens, torch.multinomial(q, 1, generator=g).int().cuda()], 1)
+        draft = s.drafter[tokens.long()]                    # row t: what token t + 1 was drawn from
+        probs, q_rot, att = s.verify(tokens)
+        u = torch.rand(B, T, generator=g).cuda()
+        cur = torch.empty_like(cur)
+        before = s.cache.seq_len.tolist()
+        sampler.accept(tokens, probs, u, taken, cur, draft=draft)
+        s.accept(taken)
+        log.append(dict(tokens=tokens, probs=probs, draft=draft, u=u, taken=taken.tolist(), next=cur.tolist(), q=q_rot, att=att,
+                        lengths=before))
+        for b, n in enumerate(log[-1]["taken"]):
+            committed[b] += tokens[b, :n].tolist()
+    s.gdn.flush(force=True)
+    torch.cuda.synchronize()
+    status = [x.status.item() for x in (s.conv, s.gdn, s.cache, one, sampler)]
+    return dict(stack=s, committed=committed, log=log, status=max(status))
+
+
 if __name__ == "__main__":
     r = run()
     print("lengths", r["lengths"], "committed", r["committed"], "status", r["status"])
     t = run_tree()
     print("tree: lengths", t["cache"].seq_len[:B].tolist(), "status", t["status"])
+    p = run_prompt()
+    print("prompts: lengths", [len(x) for x in p["committed"]], "accepted", [x["taken"] for x in p["log"]], "status", p["status"])
