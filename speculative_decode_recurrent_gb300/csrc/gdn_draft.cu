@@ -164,8 +164,11 @@ __device__ __forceinline__ Two segment_sum(const Rest &r, int v0, int V, int lan
     return shuffle(x, 0);
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // `x` to the same place of the CTA of rank `to`.
 __device__ __forceinline__ void put_remote(Two *at, int to, Two x) {
@@ -188,6 +191,7 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
     __shared__ int bad;
     const int b = blockIdx.y, rank = C > 1 ? blockIdx.x : 0, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = a.T, V = a.V;
+    if (C > 1) cluster_arrive();                    // waited for below: no CTA writes to one that has not begun
     if (tid == 0) bad = 0;
     pdl_wait();
     pdl_release();
@@ -227,6 +231,7 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
         if (lane == 0) okay[warp] = m;
     }
     __syncthreads();
+    if (C > 1) cluster_wait();
     if (bad || n == 0) {
         if (rank == 0) {
             if (a.path)

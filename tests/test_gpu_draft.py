@@ -154,3 +154,62 @@ def test_graph_replay_follows_its_inputs():
         for b in range(B):
             ref, v, _ = R.sample(x[0][b].tolist(), x[1][b].tolist(), x[2][b].double().numpy(), x[3][b].double().numpy(), x[4][b].double().numpy(), T)
             assert acc.tolist()[b] == len(ref) and nxt.tolist()[b] == v and path.tolist()[b][:len(ref)] == ref
+
+
+@pytest.mark.parametrize("drafter", ["dist", "point"])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("B,T,V,pad", [(3, 5, 150001, 0), (1, 2, 1 << 24, 0), (4, 3, 4096, 2), (1, 64, 70000, 0)])
+def test_large_vocabularies(B, T, V, pad, tree, drafter):
+    g = torch.Generator().manual_seed(7 + T)
+    z = torch.randn(B, T, V, generator=g)
+    p = torch.softmax(z, -1)
+    q = torch.softmax(z + 0.7 * torch.randn(B, T, V, generator=g), -1)
+    parent = torch.arange(-1, T - 1, dtype=torch.int32).expand(B, T).contiguous()
+    if tree:
+        parent[:, 1:] = (torch.arange(T - 1, dtype=torch.int32) // 3)[None]
+    tokens = torch.empty(B, T, dtype=torch.int32)
+    for b in range(B):
+        for t in range(T):
+            tokens[b, t] = (q if t % 2 else p)[b, max(int(parent[b, t]), 0)].argmax()
+    u = torch.rand(B, T, generator=g)
+    u[:, 1:] *= 0.9                                # (the likeliest token of a row: often accepted, siblings alike)
+    acc, nxt, path, status = run(tokens, parent, p, q if drafter == "dist" else None, u, [T] * B, tree, pad)
+    assert status == 0
+    for b in range(B):
+        ref, v, near = R.sample(tokens[b].tolist(), parent[b].tolist(), p[b].double().numpy(),
+                                q[b].double().numpy() if drafter == "dist" else None, u[b].double().numpy(), T)
+        assert near > 2.0 ** -40
+        assert acc[b] == len(ref) and path[b] == ref + [-1] * (T - len(ref)) and nxt[b] == v, b
+
+
+@pytest.mark.parametrize("V", [3, 4099, 140000])
+def test_random_numbers_at_and_past_the_ends(V):
+    """u of 0 takes the first token with mass, one just below 1 (or, outside what the header asks for, 1 and more) the last;
+    NaN and negative numbers still give a token with mass."""
+    p = torch.zeros(6, 1, V)
+    p[..., 1], p[..., V - 2] = 0.5, 0.5
+    u = torch.tensor([0.0, 1 - 2.0 ** -24, 1.0, 3.0, float("nan"), -1.0])[:, None]
+    acc, nxt, _, status = run(torch.zeros(6, 1, dtype=torch.int32), None, p, None, u, [1] * 6, False)
+    assert status == 0 and acc == [1] * 6
+    assert nxt[0] == 1 and nxt[1:4] == [V - 2] * 3 and all(x in (1, V - 2) for x in nxt[4:])
+
+
+def test_another_stream_and_no_sequences():
+    import speculative_decode_recurrent_gb300 as lib
+    tokens, _, p, q, u = inputs(3, 4, 9000, torch.Generator().manual_seed(8), False)
+    want = run(tokens, None, p, q, u, [4] * 3, False)[:2]
+    s, side = lib.DraftSampler(lib.DraftDims(B=3, T=4, V=9000)), torch.cuda.Stream()
+    x = [t.cuda() for t in (tokens, p, u, q)]
+    acc, nxt = (torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(2))
+    side.wait_stream(torch.cuda.current_stream())
+    s.accept(*x[:3], acc, nxt, draft=x[3], stream=side)
+    side.synchronize()
+    assert (acc.tolist(), nxt.tolist()) == want
+    none = lib.DraftSampler(lib.DraftDims(B=0, T=4, V=9000))
+    none.accept(*(t[:0] for t in x[:3]), acc[:0], nxt[:0])
+    with pytest.raises(ValueError, match="u: needs"):
+        s.accept(*x[:2], x[2][:, :3].contiguous(), acc, nxt)
+    with pytest.raises((ValueError, TypeError)):
+        s.accept(x[0].long(), *x[1:3], acc, nxt)
+    with pytest.raises(lib.GdnError):              # a tree needs a path
+        s.accept(*x[:3], acc, nxt, parent=x[0])
