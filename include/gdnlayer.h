@@ -79,7 +79,7 @@ int gdn_conv_accept(const gdn_conv_dims *dims, int32_t *ring_pos, const int32_t 
  * gdn_conv_advance -- the same convolution over committed tokens: a prompt, a chunk of one or single
  * tokens.  y for x_0 .. x_{n-1} (n = chunk_len[b], NULL: T) after the ring's window, or after zeros where
  * fresh[b] is not 0 (NULL: none; the ring is then not read); the last W-1 inputs go to the ring and ring_pos moves on
- * by n (mod cap).  Rows t >= n of y get 0.  dims as above, but T is 1..2^20 (B * T <= 2^28, B <= 65535, T * D <= 2^40) and cap >= W - 1,
+ * by n (mod cap).  Rows t >= n of y get 0; y does not overlap x.  dims as above, but T is 1..2^20 (B * T <= 2^28, B <= 65535, T * D <= 2^40) and cap >= W - 1,
  * cap >= 1 is enough.  Status bits as for gdn_conv_verify, _BAD_LEN also for chunk_len
  * outside [0, T]; the sequence is skipped.
  */

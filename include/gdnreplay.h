@@ -206,10 +206,13 @@ int gdn_replay_accept_fold(const gdn_replay_dims *dims, int32_t *buf_len,
  * and state[s,h] = S after the last token.  Rows t >= chunk_len[b] of out get 0.  The buffer has to be empty
  * (buf_len[s] == 0; NULL: there is none): a sequence with buffered tokens is flushed first (force).
  *   q, k  in_dtype [B, T, Hk, dk], v in_dtype [B, T, H, dv]: heads of a token dense, tokens a stride
- *   apart (views of one projection's output), 16-byte aligned;  g, beta fp32 [B, T, H] (g <= 0, as above);
+ *   apart (views of one projection's output), 16-byte aligned;  g, beta fp32 [B, T, H] (g <= 0, as above; -infinity
+ *   forgets the state);
  *   out fp32 [B, T, H, dv];  chunk_len int32 [B], NULL: T;  fresh int32 [B], NULL: none;
  *   workspace: workspace_bytes >= gdn_replay_advance_workspace() bytes, 16-byte aligned, no initial
  *   content; calls that overlap on the GPU need one each.
+ * Rows past chunk_len may hold anything. An infinite or NaN input of a token in use goes on into its head's outputs and
+ * state, and may leave NaN in up to 63 rows of the head's outputs before it.
  * GDN_STATUS_BAD_SLOT; _BAD_LEN (chunk_len outside [0, T], or a buffer that is not empty): the sequence is
  * skipped, out and state unwritten.  _TIMEOUT, _DRAIN: no output or state of the call may be trusted.
  */

@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
             for (int i = 0; i < 2; ++i) {
                 const int t = lane + 32 * i;
                 const size_t at = (tok0 + t) * a.H + h;
-                hi[i] = t < n ? a.g[at] : 0.f;
+                const float g = t < n ? a.g[at] : 0.f;
+                hi[i] = g < -1000.f ? -1000.f : g;  // (e^-1000 is 0 as well; of -infinity there is no difference. NaN stays)
                 be[i] = t < n ? a.beta[at] : 0.f;
                 lo[i] = 0.f;
             }
@@ -551,7 +552,7 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
             __syncwarp();
         }
-        if (*abort) {                               // copies in flight end before the CTA does
+        {                                           // copies in flight end before the CTA does (their users may have given up)
             bool done = true;
             const int keys = c < chunks && part > 0 ? c + 1 : c, ms = c < chunks && part > 1 ? c + 1 : c;   // chunks whose keys, whose M P have been requested
             for (int i = max(0, keys - 2); i < keys; ++i) done = done && mbar_wait(&full_k[i & 1], (i >> 1) & 1);
@@ -783,7 +784,7 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             __syncwarp();
         }
-        if (*abort) {                               // copies in flight end before the CTA does
+        {                                           // copies in flight end before the CTA does (their users may have given up)
             bool done = true;
             const int keys = c < chunks && part > 0 ? c + 1 : c, ms = c < chunks && part > 1 ? c + 1 : c;   // chunks whose keys, whose M P have been requested
             for (int i = max(0, keys - 2); i < keys; ++i) done = done && mbar_wait(&full_k[i & 1], (i >> 1) & 1);

@@ -194,7 +194,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             if (++st == ns) st = 0, ++round;
         }
-        if (*abort) {                               // copies in flight end before the CTA does
+        {                                           // copies in flight end before the CTA does (their users may have given up)
             bool done = vals || !asked || mbar_wait(q_full, 0);
             for (int y = max(0, i - ns); y < i; ++y) done = done && mbar_wait(&full[y % ns], (y / ns) & 1);
             if (!done && lane == 0) atomicOr(a.s.status, GDN_STATUS_DRAIN);

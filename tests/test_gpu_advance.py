@@ -150,6 +150,39 @@ def test_advance_many_heads_and_long_prompts(B, T, H, Hk, dk, dv):
     assert torch.equal(c.out, first[0]) and torch.equal(c.layer.t["state"], first[1])
 
 
+@pytest.mark.parametrize("T,dtype", [(300, BF), (20, BF), (70, F32)])
+def test_advance_decays_that_forget_the_state(T, dtype):
+    """A log-decay of -infinity or far below what fp32 holds is a decay of 0: nothing of the state before it is left."""
+    c = Case([T, T - 3], T, 2, 1, 128, 64, dtype, seed=20)
+    g = torch.Generator().manual_seed(21)
+    pick = torch.rand(c.g.shape, generator=g).cuda()
+    for b, n in enumerate(c.lens):
+        for lo, x in ((0.0, -float("inf")), (0.03, -1e30), (0.06, -150.0), (0.09, -1e-30), (0.12, 0.0)):
+            hit = (pick[b, :n] >= lo) & (pick[b, :n] < lo + 0.03)
+            c.g[b, :n][hit] = x
+    c.g[0, 0] = -float("inf")
+    c.run()
+    c.check(is_chunked(dtype, T))
+
+
+def test_advance_keeps_a_bad_head_to_itself():
+    """NaN in a token of one head: the other heads and sequences are as if it were not there."""
+    c = Case([130, 130], 130, 4, 4, 128, 128, BF, seed=22)
+    c.run()
+    out, state = c.out.clone(), c.layer.t["state"].clone()
+    c.layer.t["state"].copy_(c.state)
+    c.v[0, 70, 1, 5] = float("nan")
+    c.q[1, 100, 3, 7] = float("inf")
+    c.run()
+    torch.cuda.synchronize()
+    s0, s1 = (int(x) for x in c.slots)
+    same = c.out == out
+    assert same[0, :, [0, 2, 3]].all() and same[1, :, :3].all() and same[0, :64, 1].all() and same[1, :64, 3].all()
+    assert not torch.isfinite(c.out[1, 100, 3]).all() and torch.isnan(c.out[0, 70:, 1, 5]).all()
+    now = c.layer.t["state"]
+    assert torch.equal(now[s1], state[s1]) and torch.equal(now[s0, [0, 2, 3]], state[s0, [0, 2, 3]])
+
+
 def test_advance_in_pieces_is_the_whole():
     """A prompt in chunks of odd lengths, then single tokens: the state is that of one call, within the bound."""
     c = Case([256], 256, 4, 4, 128, 128, BF, seed=13)
