@@ -351,6 +351,7 @@ class ReplayLayer:
         self.t = {n: None if init[n] is None else init[n].to(device).contiguous() for n in
                   ("state", "state_idx", "buf_k", "buf_v", "buf_g", "buf_beta", "buf_len")}
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._advances = {}
 
     def verify(self, q, k, v, g, beta, out, stream=None):
         t = self.t
@@ -377,15 +378,24 @@ class ReplayLayer:
                                self.status, stream)
 
     def _advance_dims(self, T, Hk):
-        d = self.d
-        e = 16 // (2 if d.in_dtype == DTYPE_BF16 else 4)
-        return AdvanceDims(B=d.B, T=T, H=d.H, Hk=Hk, dk=d.dk, dv=d.dv, n_slot=d.n_slot, in_dtype=d.in_dtype, scale=d.scale,
-                           flags=d.flags, q_stride=Hk * d.dk // e * e, k_stride=Hk * d.dk // e * e, v_stride=d.H * d.dv)
+        """The dims of an advance (strides of dense tensors) and its workspace's bytes; kept by the numbers they follow
+        from, as a single token's call is mostly host work."""
+        key = (T, Hk, bytes(self.d))
+        got = self._advances.get(key)
+        if got is None:
+            d = self.d
+            e = 16 // (2 if d.in_dtype == DTYPE_BF16 else 4)
+            a = AdvanceDims(B=d.B, T=T, H=d.H, Hk=Hk, dk=d.dk, dv=d.dv, n_slot=d.n_slot, in_dtype=d.in_dtype, scale=d.scale,
+                            flags=d.flags, q_stride=Hk * d.dk // e * e, k_stride=Hk * d.dk // e * e, v_stride=d.H * d.dv)
+            if len(self._advances) >= 64:
+                self._advances.clear()
+            got = self._advances[key] = a, gdn_replay_advance_workspace(a)
+        return got
 
     def advance_workspace(self, T, Hk=None):
         """A workspace for ``advance`` with T tokens per sequence and Hk key heads (None: as many as value
         heads), or None where none is needed.  Layers that run one after the other may share one."""
-        n = gdn_replay_advance_workspace(self._advance_dims(T, self.d.H if Hk is None else Hk))
+        _, n = self._advance_dims(T, self.d.H if Hk is None else Hk)
         return torch.empty(n, dtype=torch.uint8, device=self.status.device) if n else None
 
     def advance(self, q, k, v, g, beta, out, chunk_len=None, fresh=None, workspace=None, stream=None):
@@ -396,12 +406,10 @@ class ReplayLayer:
         ``workspace`` (advance_workspace) one is allocated for the call."""
         if q.dim() != 4 or k.dim() != 4:
             raise ValueError("q, k: expected [B, T, Hk, dk]")
-        d = self._advance_dims(q.shape[1], k.shape[2])
-        if workspace is None:
-            n = gdn_replay_advance_workspace(d)
-            if n:
-                with torch.cuda.stream(stream):
-                    workspace = torch.empty(n, dtype=torch.uint8, device=self.status.device)
+        d, n = self._advance_dims(q.shape[1], k.shape[2])
+        if n and workspace is None:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=torch.uint8, device=self.status.device)
         t = self.t
         gdn_replay_advance(d, t["state"], t["state_idx"], t["buf_len"], chunk_len, fresh, q, k, v, g, beta, out, workspace,
                            self.status, stream)

@@ -32,7 +32,6 @@ namespace {
 using namespace tc;
 
 constexpr int kC = 64;                              // tokens of a chunk
-constexpr int kSlice = 32;                          // value columns of a slice
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What the first kernel leaves of a chunk of a head, as the second one's operands lie in shared memory:
@@ -417,37 +416,47 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
 // One CTA per (slice of 32 value columns, head, sequence): the walk for few heads, whose chain of dependent steps bounds it
 // (about 2600 cycles a chunk).  S and x are the B operands: rows of 32 first, 32 second and 32 third terms, so one product of
 // 96 columns has all of them (55 cycles an MMA, against 39 for 32 columns).
-template <int DK> struct SlicePlan {
+template <int DK, int SL> struct SlicePlan {
     static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES;
-    static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4, V_AT = 3 * Unit<DK>::MP_BYTES + 1024, MP = V_AT + kC * kSlice * 2;   // M P and gamma, values
-    static constexpr int S_ATOM = DK * 128, X_ATOM = kC * 128;         // first and second terms, then the third in an atom of its own
-    static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + E, OFF_S = OFF_MP + 2 * MP, OFF_X = OFF_S + 2 * S_ATOM;
-    static constexpr int OFF_BAR = OFF_X + 2 * X_ATOM, BYTES = OFF_BAR + 256;
+    static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4, V_AT = 3 * Unit<DK>::MP_BYTES + 1024, MP = V_AT + (kC * SL * 2 + 1023) / 1024 * 1024;   // M P and gamma, values
+    static constexpr int S_ATOM = DK * 128, X_ATOM = kC * 128, ATOMS = SL == 32 ? 2 : 1;      // rows of 64 columns: the third terms of 32 take a second one
+    static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + E, OFF_S = OFF_MP + 2 * MP, OFF_X = OFF_S + ATOMS * S_ATOM;
+    static constexpr int OFF_BAR = OFF_X + ATOMS * X_ATOM, BYTES = OFF_BAR + 256;
     static constexpr int ROWS = 256, LOAD_WARP = 8, MMA_WARP = 9, THREADS = 320;
-    static constexpr int N = 96, TMEM_COLS = 512;                      // columns of a product: [K;Q] S^T, E x, M P x
+    static constexpr int N = 3 * SL, AT = SL == 32 ? 96 : 64, TMEM_COLS = SL == 32 ? 512 : 256;       // a product's columns, and from one to the next: [K;Q] S^T, E x, M P x
     static_assert(BYTES <= 227 * 1024 && OFF_E >= 8192 && MP % 1024 == 0, "plan");
 };
 
-// A thread's 16 numbers as three bf16 terms in row `row` of a tile: 32 first, 32 second ones, and 32 third ones an atom on.
-__device__ __forceinline__ void put_row(uint8_t *tile, int atom, int row, int half, const float (&y)[16]) {
+// A thread's C numbers, the `half`-th of a slice's row, as three bf16 terms in row `row` of a tile: the first terms of 2 C, the
+// second, the third (of 32 columns an atom on).
+template <int C>
+__device__ __forceinline__ void put_row(uint8_t *tile, int atom, int row, int half, const float (&y)[C]) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < C / 8; ++c) {
         uint4 t[3];
         split8(y + 8 * c, t);
-        *reinterpret_cast<uint4 *>(tile + sw128(row, 2 * half + c)) = t[0];
-        *reinterpret_cast<uint4 *>(tile + sw128(row, 2 * half + c + 4)) = t[1];
-        *reinterpret_cast<uint4 *>(tile + atom + sw128(row, 2 * half + c)) = t[2];
+        const int at = C / 8 * half + c;
+        *reinterpret_cast<uint4 *>(tile + sw128(row, at)) = t[0];
+        *reinterpret_cast<uint4 *>(tile + sw128(row, at + C / 4)) = t[1];
+        *reinterpret_cast<uint4 *>(C == 16 ? tile + atom + sw128(row, at) : tile + sw128(row, at + C / 2)) = t[2];
     }
 }
-// The product's 16 columns: those with the three terms added, the smallest first.
-__device__ __forceinline__ void get_row(uint32_t tcol, float (&y)[16]) {
-    uint32_t r[16], s[16], t[16];
-    tmem_load16(tcol, r);
-    tmem_load16(tcol + 32, s);
-    tmem_load16(tcol + 64, t);
+// The product's C columns: those with the three terms added, the smallest first.
+template <int C>
+__device__ __forceinline__ void get_row(uint32_t tcol, float (&y)[C]) {
+    uint32_t r[C], s[C], t[C];
+    if constexpr (C == 16) {
+        tmem_load16(tcol, r);
+        tmem_load16(tcol + 32, s);
+        tmem_load16(tcol + 64, t);
+    } else {
+        tmem_load8(tcol, r);
+        tmem_load8(tcol + 16, s);
+        tmem_load8(tcol + 32, t);
+    }
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(r[j]) + (__uint_as_float(s[j]) + __uint_as_float(t[j]));
+    for (int j = 0; j < C; ++j) y[j] = __uint_as_float(r[j]) + (__uint_as_float(s[j]) + __uint_as_float(t[j]));
 }
 
 // What both walks begin with: the sequence, rows of out past it, a state without tokens.  False: nothing is left to do.
@@ -473,12 +482,13 @@ __device__ __forceinline__ bool begin_walk(const TcAdvance &ta, const AdvanceSeq
 
 // Row r has token r (K's products, r < 64), token r - 64 (Q's) and key dimension r of the state, 16 columns in each of
 // two warps.  Everything that a buffer's next use overwrites has been read by then: see each arrival.
-template <int DK>
-__global__ void __launch_bounds__(SlicePlan<DK>::THREADS, 1)
+template <int DK, int SL>
+__global__ void __launch_bounds__(SlicePlan<DK, SL>::THREADS, 1)
 advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcAdvance ta)
 {
-    using P = SlicePlan<DK>;
+    using P = SlicePlan<DK, SL>;
+    constexpr int C = SL / 2;                       // columns of a thread
     const AdvanceArgs &a = ta.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int h = blockIdx.y, b = ta.b0 + blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -490,9 +500,9 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     pdl_wait();
     pdl_release();
     const AdvanceSeq sq = advance_seq(a, b);
-    const int n = sq.bad ? 0 : tokens_here(ta, sq.n), chunks = (n + kC - 1) / kC, dv0 = blockIdx.x * kSlice;
+    const int n = sq.bad ? 0 : tokens_here(ta, sq.n), chunks = (n + kC - 1) / kC, dv0 = blockIdx.x * SL;
     const bool zero = sq.fresh && ta.c0 == 0;       // starts from a zero state
-    if (!begin_walk(ta, sq, n, h, b, dv0, kSlice, DK, zero, blockIdx.x == 0, P::THREADS)) return;
+    if (!begin_walk(ta, sq, n, h, b, dv0, SL, DK, zero, blockIdx.x == 0, P::THREADS)) return;
     if (saddr(smem) & 1023u) {
         if (tid == 0) atomicOr(a.status, kStatusTimeout);
         return;
@@ -539,7 +549,7 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (c >= 2 && !wait(&empty_m[st], before)) break;
             if (elect_one()) {
                 uint8_t *dst = smem + P::OFF_MP + st * P::MP;
-                mbar_expect_tx(&full_m[st], P::M_BYTES + kC * kSlice * 2);
+                mbar_expect_tx(&full_m[st], P::M_BYTES + kC * SL * 2);
                 bulk_load(dst, unit + Unit<DK>::OFF_MP, P::M_BYTES, &full_m[st]);
                 tma_load_3d(dst + P::V_AT, &tm_v, dv0, h, b * a.T + (ta.c0 + c) * kC, &full_m[st]);
             }
@@ -566,12 +576,12 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const uint64_t dS = desc_mn_sw128(saddr(smem) + P::OFF_S, P::S_ATOM), dX = desc_mn_sw128(saddr(smem) + P::OFF_X, P::X_ATOM);
         const uint64_t dKQ = desc_sw128(saddr(smem)), dE = desc_sw128(saddr(smem) + P::OFF_E), dM = desc_sw128(saddr(smem) + P::OFF_MP - 8192);
         const uint32_t one = elect_one();
-        // A term of E or M P with as many terms of x as count: 3, 2 and 1 of 32 columns.
+        // A term of E or M P with as many terms of x as count: 3, 2 and 1 of a slice's columns.
         auto terms = [&](uint32_t acc, uint64_t left, int step) {
 #pragma unroll
             for (int k = 0; k < 12; ++k)
                 mma_bf16_on(one, acc, desc_add(left, (k >> 2) * step + (k & 3) * 32), desc_add(dX, (k & 3) * 2048),
-                            idesc_mn(1, 128, 96 - 32 * (k >> 2)) | kIdescMnMajorB, k > 0);
+                            idesc_mn(1, 128, P::N - SL * (k >> 2)) | kIdescMnMajorB, k > 0);
         };
         bool ok = true;
         int c = 0;
@@ -589,12 +599,12 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             ok = wait(full_e, c & 1) && wait(x_ready, c & 1);
             if (!ok) break;
             tc_fence_after();
-            terms(tm + P::N, dE, Unit<DK>::E_BYTES);
+            terms(tm + P::AT, dE, Unit<DK>::E_BYTES);
             mma_commit_on(one, d2);
             mma_commit_on(one, empty_e);
             ok = wait(&full_m[st], (c >> 1) & 1);
             if (!ok) break;
-            terms(tm + 2 * P::N, desc_add(dM, st * P::MP), Unit<DK>::MP_BYTES);
+            terms(tm + 2 * P::AT, desc_add(dM, st * P::MP), Unit<DK>::MP_BYTES);
             mma_commit_on(one, d3);
             mma_commit_on(one, &empty_m[st]);
         }
@@ -606,13 +616,13 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         // ------------------------------------------------------ rows
         const int half = warp >> 2, row = tid & 127, t = row & (kC - 1);
         const bool keys = row < kC, has = row < DK;                   // (the same in a warp)
-        const uint32_t tm = tmem + 16 * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t tm = tmem + C * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         uint8_t *sS = smem + P::OFF_S, *sX = smem + P::OFF_X;
-        const int col0 = dv0 + 16 * half;
+        const int col0 = dv0 + C * half;
         float *st = a.state + ((static_cast<size_t>(sq.slot) * a.H + h) * ta.dv + col0) * DK + row;
-        float S[16];
+        float S[C];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) S[j] = has && !zero ? st[j * DK] : 0.f;
+        for (int j = 0; j < C; ++j) S[j] = has && !zero ? st[j * DK] : 0.f;
         const size_t tok0 = static_cast<size_t>(b) * a.T + ta.c0 * kC + t;
         float *op = a.out + (tok0 * a.H + h) * ta.dv + col0;
         auto arrive = [&](uint64_t *bar) {          // for the warp, behind each lane's fences
@@ -624,7 +634,7 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         arrive(s_ready);
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
-            float y[16], o[16];
+            float y[C], o[C];
             const uint8_t *slot = smem + P::OFF_MP + (c & 1) * P::MP;
             const float *gam = reinterpret_cast<const float *>(slot + 3 * Unit<DK>::MP_BYTES);
             ok = wait(&full_m[c & 1], (c >> 1) & 1) && wait(d1, c & 1);
@@ -635,9 +645,9 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 const bool live = c * kC + t < n;
                 const float f = -gam[t];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < C / 8; ++i) {
                     float v[8];
-                    bf16x8_to_f32(*reinterpret_cast<const uint4 *>(slot + P::V_AT + t * (kSlice * 2) + 32 * half + 16 * i), v);
+                    bf16x8_to_f32(*reinterpret_cast<const uint4 *>(slot + P::V_AT + t * (SL * 2) + C * 2 * half + 16 * i), v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[8 * i + e] = live ? fmaf(f, y[8 * i + e], v[e]) : 0.f;
                 }
@@ -646,7 +656,7 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             } else {
                 const float f = gam[t] * a.scale;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = f * y[j];
+                for (int j = 0; j < C; ++j) o[j] = f * y[j];
             }
             const float ge = gam[kC - 1];
             tc_fence_before();
@@ -655,9 +665,9 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (!ok) break;
             tc_fence_after();
             if (has) {
-                get_row(tm + P::N, y);
+                get_row(tm + P::AT, y);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) S[j] = fmaf(ge, S[j], y[j]);
+                for (int j = 0; j < C; ++j) S[j] = fmaf(ge, S[j], y[j]);
                 put_row(sS, P::S_ATOM, row, half, S);
                 fence_proxy_async();
             }
@@ -667,11 +677,11 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 ok = wait(d3, c & 1);
                 if (!ok) break;
                 tc_fence_after();
-                get_row(tm + 2 * P::N, y);
+                get_row(tm + 2 * P::AT, y);
                 if (c * kC + t < n) {
                     float4 *dst = reinterpret_cast<float4 *>(op + static_cast<size_t>(c) * kC * a.H * ta.dv);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < C / 4; ++j)
                         dst[j] = make_float4(o[4 * j] + y[4 * j], o[4 * j + 1] + y[4 * j + 1], o[4 * j + 2] + y[4 * j + 2],
                                              o[4 * j + 3] + y[4 * j + 3]);
                 }
@@ -679,7 +689,7 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         if (ok && has)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) st[j * DK] = S[j];
+            for (int j = 0; j < C; ++j) st[j * DK] = S[j];
         tc_fence_before();
     }
     __syncthreads();
@@ -716,7 +726,7 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     constexpr int DV = 128, DQ = DK / 4;            // key dimensions of a thread
     const AdvanceArgs &a = ta.a;
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int h = blockIdx.x, b = ta.b0 + blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.y, b = ta.b0 + blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t *full_k = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR), *empty_k = full_k + 2, *full_m = empty_k + 2, *empty_m = full_m + 2,
              *full_e = empty_m + 2, *empty_e = full_e + 1, *d1 = empty_e + 1, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1,
              *x_ready = s_ready + 1, *drain = x_ready + 1;
@@ -747,7 +757,7 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.status); };
     if (warp == P::LOAD_WARP) {
         // ------------------------------------------------------ loads
-        const char *units = a.ws + (static_cast<size_t>(blockIdx.y) * ta.chunks * a.H + h) * Unit<DK>::BYTES;
+        const char *units = a.ws + (static_cast<size_t>(blockIdx.z) * ta.chunks * a.H + h) * Unit<DK>::BYTES;
         const size_t ustep = static_cast<size_t>(a.H) * Unit<DK>::BYTES;
         const int hk = h / (a.H / a.Hk);
         int c = 0, part = 0;
@@ -947,7 +957,7 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int64_t kBudget = 192ll << 20;            // of workspace: chunks beyond it follow in further launches
+constexpr int64_t kBudget = 768ll << 20;            // of workspace: what is beyond it follows in further launches
 
 int64_t unit_bytes(const gdn_advance_dims *d) { return d->dk == 64 ? Unit<64>::BYTES : Unit<128>::BYTES; }
 int all_chunks(const gdn_advance_dims *d) { return (d->T + kC - 1) / kC; }
@@ -955,17 +965,57 @@ int seqs_per_launch(const gdn_advance_dims *d) {
     const int64_t n = kBudget / 2 / (unit_bytes(d) * d->H);
     return static_cast<int>(n < 1 ? 1 : n < d->B ? n : d->B);
 }
-// Chunks of a launch pair: a sixth of them, so that the first kernel's work for the next ones runs beside the walk; all where
-// there are few (a pair's beginning and end cost about as much as four chunks).
-int chunks_per_launch(const gdn_advance_dims *d) {
-    const int64_t all = all_chunks(d), most = kBudget / 2 / (unit_bytes(d) * d->H * seqs_per_launch(d));
-    int64_t n = all <= 16 ? all : (all + 5) / 6 < 8 ? 8 : (all + 5) / 6;
-    if (n > most) n = most < 1 ? 1 : most;
-    return static_cast<int>(n);
+// Value columns of a walk's CTA: slices of 32 while each has an SM of its own, heads beyond (which need 128 value columns);
+// slices of 16 where even those have (8192 tokens of 16 heads: 172 us of walking, against 205 with 32) and no first kernel is to run beside
+// them, for which they leave no SMs.
+int walk_columns(const gdn_advance_dims *d, bool last) {
+    const long long heads = static_cast<long long>(seqs_per_launch(d)) * d->H, sms = sm_count();
+    return last && heads * (d->dv / 16) <= sms ? 16 : d->dv == 128 && heads * (d->dv / 32) > sms ? 128 : 32;
 }
-int buffers(const gdn_advance_dims *d) {
-    return chunks_per_launch(d) < all_chunks(d) || seqs_per_launch(d) < d->B ? 2 : 1;
+
+// The chunks come in launches of the two kernels, so that the first one's work for the next chunks runs beside the walk,
+// on SMs that the walk leaves free: beside c chunks of it there is time for r c.  The first launch's own work runs alone (16 us for
+// three CTAs on an SM), and each launch costs some 12 us (by heads 20: more state comes in and goes out); their number and the
+// first one's size follow from that.  8192 tokens of 16 heads: 224 us in three launches, 252 in one, 250 in six; 8 prompts of 16
+// heads, whose walk leaves few SMs: 218 in one, 225 in two.
+struct Segments {
+    int first, most, n;
+    double r;
+    int next(int i, int size, int rest) const {     // of launch i, after one of `size`
+        double c = i == 0 ? first : size * r;
+        if (i == n - 1 || c >= rest) c = rest;
+        return c < 1 ? 1 : c > most ? most : static_cast<int>(c);
+    }
+};
+Segments segments(const gdn_advance_dims *d) {
+    const int all = all_chunks(d), seqs = seqs_per_launch(d), cols = walk_columns(d, false);
+    const double sms = sm_count() < 1 ? 1 : sm_count(), units = static_cast<double>(seqs) * d->H, ctas = units * (d->dv / cols);
+    const double prep = 16.0 / 3 * units / sms, walk = cols == 128 ? 3.4 : 1.6, free = ctas < sms ? 1 - ctas / sms : 0;   // us a chunk
+    const int64_t most = kBudget / 2 / (unit_bytes(d) * d->H * seqs);
+    Segments s{all, static_cast<int>(most < 1 ? 1 : most < all ? most : all), 1, walk * free / prep};
+    double best = 1e30, sum = 0, pow = 1;
+    for (int n = 1; n <= 6; ++n, pow *= s.r) {
+        sum += pow;
+        const double cost = prep * all / sum + (cols == 128 ? 20.0 : 12.0) * n;
+        if (cost < best) {
+            best = cost;
+            s.n = n;
+            s.first = static_cast<int>(all / sum + 0.999);
+        }
+    }
+    return s;
 }
+// Chunks of the largest launch.
+int largest_launch(const gdn_advance_dims *d) {
+    const Segments g = segments(d);
+    int largest = 0, size = 0;
+    for (int i = 0, rest = all_chunks(d); rest > 0; ++i, rest -= size) {
+        size = g.next(i, size, rest);
+        if (size > largest) largest = size;
+    }
+    return largest;
+}
+int buffers(const gdn_advance_dims *d) { return largest_launch(d) < all_chunks(d) || seqs_per_launch(d) < d->B ? 2 : 1; }
 
 // Keys, queries or values as [B T][heads][dim]; boxes of `cols` columns of one head, 64 tokens.
 bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int heads, int dim, int64_t stride, int cols, bool swizzle) {
@@ -984,31 +1034,40 @@ bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int 
 // is over), but one of its CTAs does at its end, so that walk k + 1, which waits for prep k + 1, also comes
 // after walk k.  Two workspaces: prep k + 1 begins when walk k has, and so after walk k - 1, the last reader of its own.
 template <int DK>
-int launch(const gdn_advance_dims *d, const AdvanceArgs &a, bool heads, cudaStream_t s) {
-    CUtensorMap mk, mq, mv;
+int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
+    CUtensorMap mk, mq, mv[2];
+    const int columns[2] = {walk_columns(d, false), walk_columns(d, true)};
     if (!token_map(&mk, a.k, d, d->Hk, d->dk, d->k_stride, 64, true) || !token_map(&mq, a.q, d, d->Hk, d->dk, d->q_stride, 64, true) ||
-        !token_map(&mv, a.v, d, d->H, d->dv, d->v_stride, heads ? 128 : kSlice, false))
+        !token_map(&mv[0], a.v, d, d->H, d->dv, d->v_stride, columns[0], false) ||
+        !token_map(&mv[1], a.v, d, d->H, d->dv, d->v_stride, columns[1], false))
         return GDN_ERR_LAUNCH;
-    if (cudaFuncSetAttribute(advance_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepPlan<DK>::BYTES) != cudaSuccess ||
-        cudaFuncSetAttribute(advance_slice_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, SlicePlan<DK>::BYTES) != cudaSuccess ||
-        cudaFuncSetAttribute(advance_head_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, HeadPlan<DK>::BYTES) != cudaSuccess)
+    if (cudaFuncSetAttribute(advance_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepPlan<DK>::BYTES) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    const int all = all_chunks(d), step = chunks_per_launch(d), seqs = seqs_per_launch(d);
-    const int64_t half = unit_bytes(d) * d->H * seqs * step;
+    auto walk = [&](int cols, int nb, const CUtensorMap &m, const TcAdvance &ta) {
+        const int bytes = cols == 128 ? HeadPlan<DK>::BYTES : cols == 32 ? SlicePlan<DK, 32>::BYTES : SlicePlan<DK, 16>::BYTES;
+        const int threads = cols == 128 ? HeadPlan<DK>::THREADS : SlicePlan<DK, 32>::THREADS;
+        auto *kern = cols == 128 ? advance_head_kernel<DK> : cols == 32 ? advance_slice_kernel<DK, 32> : advance_slice_kernel<DK, 16>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        return e != cudaSuccess ? e : launch_pdl(kern, dim3(d->dv / cols, d->H, nb), dim3(threads), bytes, s, mk, mq, m, ta);
+    };
+    const int all = all_chunks(d), seqs = seqs_per_launch(d);
+    const Segments g = segments(d);
+    const int64_t half = unit_bytes(d) * d->H * seqs * largest_launch(d);
     TcAdvance ta{a, 0, 0, 0, d->dv, 0};
-    for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += seqs)
-        for (ta.c0 = 0; ta.c0 < all; ta.c0 += step) {
-            const int nb = d->B - ta.b0 < seqs ? d->B - ta.b0 : seqs;
-            ta.chunks = all - ta.c0 < step ? all - ta.c0 : step;
+    for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += seqs) {
+        const int nb = d->B - ta.b0 < seqs ? d->B - ta.b0 : seqs;
+        ta.chunks = 0;
+        for (int i = 0, c0 = 0; c0 < all; ++i, c0 += ta.chunks) {
+            ta.c0 = c0;
+            ta.chunks = g.next(i, ta.chunks, all - c0);
+            const bool last = c0 + ta.chunks == all && ta.b0 + nb == d->B;
             cudaError_t e = launch_pdl(advance_prep_kernel<DK>, dim3(d->H, ta.chunks, nb), dim3(kPrepThreads), PrepPlan<DK>::BYTES, s, ta);
-            if (e == cudaSuccess)
-                e = heads ? launch_pdl(advance_head_kernel<DK>, dim3(d->H, nb), dim3(HeadPlan<DK>::THREADS), HeadPlan<DK>::BYTES, s, mk, mq, mv, ta)
-                          : launch_pdl(advance_slice_kernel<DK>, dim3(d->dv / kSlice, d->H, nb), dim3(SlicePlan<DK>::THREADS), SlicePlan<DK>::BYTES,
-                                       s, mk, mq, mv, ta);
+            if (e == cudaSuccess) e = walk(columns[last], nb, mv[last], ta);
             if (e != cudaSuccess) return GDN_ERR_LAUNCH;
             ta.behind = 1;
             ta.a.ws = ta.a.ws == a.ws ? a.ws + half : a.ws;
         }
+    }
     return GDN_OK;
 }
 
@@ -1018,13 +1077,11 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, bool heads, cudaStre
 bool advance_tc_shape(const gdn_advance_dims *d) { return d->in_dtype == GDN_DTYPE_BF16 && d->T > 32; }
 
 int64_t advance_tc_workspace(const gdn_advance_dims *d) {
-    return unit_bytes(d) * d->H * seqs_per_launch(d) * chunks_per_launch(d) * buffers(d);
+    return unit_bytes(d) * d->H * seqs_per_launch(d) * largest_launch(d) * buffers(d);
 }
 
 int advance_tc(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
-    // By slices while each has an SM of its own; by heads beyond (which need 128 value columns).
-    const bool heads = d->dv == 128 && static_cast<long long>(d->B) * d->H * (d->dv / kSlice) > sm_count();
-    return d->dk == 64 ? launch<64>(d, a, heads, s) : launch<128>(d, a, heads, s);
+    return d->dk == 64 ? launch<64>(d, a, s) : launch<128>(d, a, s);
 }
 
 }  // namespace gdn

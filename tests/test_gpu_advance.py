@@ -131,7 +131,11 @@ def ragged(B, T, seed):
 @pytest.mark.parametrize("B,T,H,Hk,dk,dv", [
     (20, 140, 2, 1, 128, 128),               # heads walked whole
     (20, 150, 2, 2, 64, 128),
-    (3, 1100, 2, 1, 128, 128),               # a long prompt's further launches, by slices
+    (6, 140, 4, 2, 128, 128),                # slices of 32 columns
+    (10, 150, 5, 5, 64, 64),
+    (11, 90, 4, 1, 128, 64),
+    (2, 1100, 12, 12, 64, 128),
+    (3, 1100, 2, 1, 128, 128),               # a long prompt's further launches, by slices of 16
     (2, 1300, 3, 3, 64, 64),
     (3, 1100, 14, 7, 128, 128),              # and by heads
     (4, 1090, 10, 10, 64, 128),
