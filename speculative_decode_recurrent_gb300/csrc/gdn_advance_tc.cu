@@ -80,54 +80,76 @@ __device__ constexpr int kTermA[6] = {0, 0, 1, 0, 1, 2}, kTermB[6] = {0, 1, 0, 2
 // ------------------------------------------------------------- E and M P of every chunk
 constexpr int kPrepThreads = 256;
 
-// Shared memory, 73 KB, so that three CTAs share an SM: [K;Q] as atoms of 64 columns, 128 rows of 128 bytes each (M's
-// first two terms go over the queries' rows of the two, the third follows them); A in fp32, T over it, then the terms of F and
-// after them those of P; at the end those of E and M P over all of it.
+// What bounds it: shared memory's bandwidth (six thousand cycles of loads and stores a chunk, two thousand of operands, of some
+// ten thousand that an SM takes; 98 us for the 2800 chunks of 8 prompts of 16 heads, 200 MB of operators).
+// Its size here, 50 KB, lets four CTAs share an SM: [K;Q] as
+// atoms of 64 columns, 128 rows of 128 bytes each; A in fp32, T over it.  What is no longer needed makes room: the first two terms of M
+// lie over the queries, the third (in registers until then) over the second half of the keys once E is there; F's terms over T (the third
+// after the others' product), P's after them, its third over the first half of the keys; at the end E's and M P's over all of it.
 template <int DK> struct PrepPlan {
     static constexpr int LD = 68;                   // floats of a row of A and T: 16-byte rows, 4 banks apart
-    static constexpr int OFF_M = 8192, ATOM = 16384, OFF_M2 = 32768, OFF_T = OFF_M2 + 8192, TERM = kC * 128;
-    static constexpr int OFF_G = 3 * 128 * 128 + 3 * TERM;             // G (two words), gamma, beta, decay to the end
+    static constexpr int ATOM = 16384, TERM = kC * 128, OFF_M0 = 8192, OFF_M1 = 24576, OFF_M2 = 16384, OFF_P2 = 0;
+    static constexpr int OFF_T = 32768, OFF_G = OFF_T + kC * LD * 4;   // then G (two words), gamma, beta, decay to the end
     static constexpr int OFF_BAR = OFF_G + 5 * kC * 4;
     static constexpr int BYTES = OFF_BAR + 64;
-    static_assert(OFF_T % 1024 == 0 && kC * LD * 4 <= 3 * TERM && OFF_T + 3 * TERM <= OFF_G, "room");
+    static_assert(OFF_T % 1024 == 0 && 2 * TERM <= kC * LD * 4 && 3 * Unit<DK>::E_BYTES <= OFF_G, "room");
 };
 
 // One level of the inverse, in A's place: with the diagonal blocks of N rows of T = (I + A)^-1 there, those of 2 N:
 // T21 = -T22 A21 T11.  X = A21 T11 lies in the block (1, 2) for the moment, so the loops stay clear of what
-// is above the diagonal blocks of 8.  A thread has N / 8 neighbouring elements.
+// is above the diagonal blocks of 8.  A thread has N / 8 neighbouring elements of a row, or of two.
 template <int N, int LD>
 __device__ __forceinline__ void inverse_level(float *sT, int tid) {
-    constexpr int W = N / 8;
-    const int c = (tid & 7) * W, r = (tid >> 3) % N, lo = tid / (8 * N) * 2 * N, hi = lo + N;
-    float x[W];
+    constexpr int W = N / 8, R = N == 32 ? 2 : 1;   // columns and rows of a thread (two of 32: fewer loads, which shared memory bounds)
+    const int c = (tid & 7) * W, r = (tid >> 3) * R % N, lo = tid * R / (8 * N) * 2 * N, hi = lo + N;
+    const bool on = tid < kPrepThreads / R;
+    float x[R][W];
     auto product = [&](const float *row, const float *cols, int k0, int k1, float sign) {      // sums over [k0, k1), multiples of 4
 #pragma unroll
-        for (int i = 0; i < W; ++i) x[i] = 0.f;
+        for (int e = 0; e < R; ++e)
+#pragma unroll
+            for (int i = 0; i < W; ++i) x[e][i] = 0.f;
 #pragma unroll 2
         for (int k = k0; k < k1; k += 4) {
-            const float4 y = *reinterpret_cast<const float4 *>(row + k);
-            const float yy[4] = {sign * y.x, sign * y.y, sign * y.z, sign * y.w};
+            float yy[R][4];
+#pragma unroll
+            for (int e = 0; e < R; ++e) {
+                const float4 y = *reinterpret_cast<const float4 *>(row + e * LD + k);
+                yy[e][0] = sign * y.x; yy[e][1] = sign * y.y; yy[e][2] = sign * y.z; yy[e][3] = sign * y.w;
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float *z = cols + (k + q) * LD;
+                float zz[W];
                 if constexpr (W == 4) {
-                    const float4 zz = *reinterpret_cast<const float4 *>(z);
-                    x[0] = fmaf(yy[q], zz.x, x[0]); x[1] = fmaf(yy[q], zz.y, x[1]);
-                    x[2] = fmaf(yy[q], zz.z, x[2]); x[3] = fmaf(yy[q], zz.w, x[3]);
+                    const float4 z4 = *reinterpret_cast<const float4 *>(z);
+                    zz[0] = z4.x; zz[1] = z4.y; zz[2] = z4.z; zz[3] = z4.w;
                 } else {
 #pragma unroll
-                    for (int i = 0; i < W; ++i) x[i] = fmaf(yy[q], z[i], x[i]);
+                    for (int i = 0; i < W; ++i) zz[i] = z[i];
                 }
+#pragma unroll
+                for (int e = 0; e < R; ++e)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) x[e][i] = fmaf(yy[e][q], zz[i], x[e][i]);
             }
         }
     };
-    product(sT + (hi + r) * LD + lo, sT + lo * LD + lo + c, c & ~7, N, 1.f);
+    auto put = [&](float *at) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) sT[(lo + r) * LD + hi + c + i] = x[i];
+        for (int e = 0; e < R; ++e)
+#pragma unroll
+            for (int i = 0; i < W; ++i) at[e * LD + i] = x[e][i];
+    };
+    if (on) {
+        product(sT + (hi + r) * LD + lo, sT + lo * LD + lo + c, c & ~7, N, 1.f);
+        put(sT + (lo + r) * LD + hi + c);
+    }
     __syncthreads();
-    product(sT + (hi + r) * LD + hi, sT + lo * LD + hi + c, 0, (r | 7) + 1, -1.f);
-#pragma unroll
-    for (int i = 0; i < W; ++i) sT[(hi + r) * LD + lo + c + i] = x[i];
+    if (on) {
+        product(sT + (hi + r) * LD + hi, sT + lo * LD + hi + c, 0, (r | 7) + 1, -1.f);
+        put(sT + (hi + r) * LD + lo + c);
+    }
     __syncthreads();
 }
 
@@ -148,7 +170,7 @@ __device__ __forceinline__ void stage_row(uint32_t tcol, uint8_t *tile, int step
 
 // One CTA per (head, chunk, sequence).  Warps w and w + 4 share TMEM lanes 32 (w % 4) .. and halve the columns.
 template <int DK>
-__global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcAdvance ta)
+__global__ void __launch_bounds__(kPrepThreads, 4) advance_prep_kernel(const TcAdvance ta)
 {
     using P = PrepPlan<DK>;
     const AdvanceArgs &a = ta.a;
@@ -170,7 +192,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 4);
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bar[i], 1);
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, 128);
@@ -261,40 +283,47 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
     }
     bool ok = mbar_wait(&bar[0], 0);
     tc_fence_after();
+    ok = __all_sync(0xffffffffu, ok);
+    int issued = 0;                                 // the last barrier that MMAs may have been committed to
     // ---- A in fp32 (rows of K), M's terms (rows of Q)
     const int t = ((warp & 1) << 5) + lane;
     const bool keys = (warp & 3) < 2;
-    if (__all_sync(0xffffffffu, ok)) {
+    uint4 m2[4];                                    // M's third terms
+    if (ok) {
         const float gh = sGh[t], gl = sGl[t], f = keys ? sBeta[t] : a.scale;
-        uint32_t r[32];
-        tmem_ld32(tmem + lanes + 32 * half, r);
-        tmem_wait_ld();
-        float y[32];
-        const int seen = t - 32 * half + (keys ? 0 : 1);          // columns j < seen count
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 h4 = *reinterpret_cast<const float4 *>(sGh + 32 * half + j), l4 = *reinterpret_cast<const float4 *>(sGl + 32 * half + j);
-            y[j] = ex2(((gh - h4.x) + (gl - l4.x)) * kLog2e);
-            y[j + 1] = ex2(((gh - h4.y) + (gl - l4.y)) * kLog2e);
-            y[j + 2] = ex2(((gh - h4.z) + (gl - l4.z)) * kLog2e);
-            y[j + 3] = ex2(((gh - h4.w) + (gl - l4.w)) * kLog2e);
-        }
+        for (int v = 0; v < 2; ++v) {
+            const int j0 = 32 * half + 16 * v;
+            uint32_t r[16];
+            tmem_load16(tmem + lanes + j0, r);
+            tmem_wait_ld();
+            float y[16];
+            const int seen = t - j0 + (keys ? 0 : 1);             // columns j < seen count
 #pragma unroll
-        for (int j = 0; j < 32; ++j)                              // (as bits: a select here became 32 branches)
-            y[j] = __uint_as_float(__float_as_uint(__uint_as_float(r[j]) * y[j] * f) & (j < seen ? 0xffffffffu : 0u));
-        if (keys) {
+            for (int j = 0; j < 16; j += 4) {
+                const float4 h4 = *reinterpret_cast<const float4 *>(sGh + j0 + j), l4 = *reinterpret_cast<const float4 *>(sGl + j0 + j);
+                y[j] = ex2(((gh - h4.x) + (gl - l4.x)) * kLog2e);
+                y[j + 1] = ex2(((gh - h4.y) + (gl - l4.y)) * kLog2e);
+                y[j + 2] = ex2(((gh - h4.z) + (gl - l4.z)) * kLog2e);
+                y[j + 3] = ex2(((gh - h4.w) + (gl - l4.w)) * kLog2e);
+            }
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<float4 *>(sT + t * P::LD + 32 * half + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-        } else {
+            for (int j = 0; j < 16; ++j)                          // (as bits: a select here became 32 branches)
+                y[j] = __uint_as_float(__float_as_uint(__uint_as_float(r[j]) * y[j] * f) & (j < seen ? 0xffffffffu : 0u));
+            if (keys) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                uint4 m[3];
-                split8(y + 8 * v, m);
-                const uint32_t at = sw128(t, 4 * half + v);
-                *reinterpret_cast<uint4 *>(smem + P::OFF_M + at) = m[0];
-                *reinterpret_cast<uint4 *>(smem + P::OFF_M + P::ATOM + at) = m[1];
-                *reinterpret_cast<uint4 *>(smem + P::OFF_M2 + at) = m[2];
+                for (int j = 0; j < 16; j += 4)
+                    *reinterpret_cast<float4 *>(sT + t * P::LD + j0 + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint4 m[3];
+                    split8(y + 8 * c, m);
+                    const uint32_t at = sw128(t, 4 * half + 2 * v + c);
+                    *reinterpret_cast<uint4 *>(smem + P::OFF_M0 + at) = m[0];
+                    *reinterpret_cast<uint4 *>(smem + P::OFF_M1 + at) = m[1];
+                    m2[2 * v + c] = m[2];
+                }
             }
         }
     }
@@ -339,7 +368,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(__float_as_uint(y[j]) & (s0 + j <= row ? 0xffffffffu : 0u));
-    auto put = [&](float f) {
+    // Their terms: the first two in T's place; the third is returned.
+    auto put = [&](float f, uint4 (&third)[2]) {
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
             float z[8];
@@ -348,64 +378,92 @@ __global__ void __launch_bounds__(kPrepThreads, 3) advance_prep_kernel(const TcA
             uint4 m[3];
             split8(z, m);
             const uint32_t at = P::OFF_T + sw128(row, (s0 >> 3) + v);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(smem + k * P::TERM + at) = m[k];
+            *reinterpret_cast<uint4 *>(smem + at) = m[0];
+            *reinterpret_cast<uint4 *>(smem + P::TERM + at) = m[1];
+            third[v] = m[2];
         }
+    };
+    auto put_third = [&](int off, const uint4 (&third)[2]) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) *reinterpret_cast<uint4 *>(smem + off + sw128(row, (s0 >> 3) + v)) = third[v];
         fence_proxy_async();
     };
+    auto wait = [&](int i) {                        // for barrier i, to which this warp takes MMAs to have been committed
+        if (ok) {
+            issued = i;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar[i], 0));
+        }
+        tc_fence_after();
+    };
     __syncthreads();                                // T has been read
-    put(end);
+    uint4 third[2];
+    put(end, third);
+    fence_proxy_async();
     __syncthreads();
     // ---- E = K^T F (rows dk: the keys read MN-major), then, over [K;Q] K^T, M P (lanes 64..127: each term of M begins 64 rows
     //      into its operand; lanes 0..63 are not read)
     const uint32_t one = elect_one();
     const uint64_t dt = desc_mn_sw128(saddr(smem) + P::OFF_T, 8192);
+    const uint64_t dk = desc_mn_sw128(saddr(smem), P::ATOM);
+    constexpr uint32_t idE = idesc_mn(1, 128, kC) | kIdescMnMajorA | kIdescMnMajorB;
     if (warp == 0 && ok) {
         tc_fence_after();
-        const uint64_t dk = desc_mn_sw128(saddr(smem), P::ATOM);
-        constexpr uint32_t idE = idesc_mn(1, 128, kC) | kIdescMnMajorA | kIdescMnMajorB;
 #pragma unroll
-        for (int k = 0; k < 12; ++k)
+        for (int k = 0; k < 8; ++k)
             mma_bf16_on(one, tmem + 64, desc_add(dk, (k & 3) * 2048), desc_add(dt, (k >> 2) * P::TERM + (k & 3) * 2048), idE, k > 0);
         mma_commit_on(one, &bar[1]);
     }
-    ok = ok && mbar_wait(&bar[1], 0);
-    ok = __all_sync(0xffffffffu, ok);
-    put(1.f);
+    wait(1);
+    put_third(P::OFF_T, third);                     // F's
+    __syncthreads();
+    if (warp == 0 && ok) {
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_bf16_on(one, tmem + 64, desc_add(dk, k * 2048), desc_add(dt, k * 2048), idE, 1);
+        mma_commit_on(one, &bar[2]);
+    }
+    wait(2);
+    put(1.f, third);
+    if (!keys && ok)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4 *>(smem + P::OFF_M2 + sw128(t, 4 * half + v)) = m2[v];
+    put_third(P::OFF_P2, third);
     __syncthreads();
     if (warp == 0 && ok) {
         tc_fence_after();
         constexpr uint32_t idM = idesc_mn(1, 128, kC) | kIdescMnMajorB;
+        constexpr int off_m[3] = {P::OFF_M0 - 8192, P::OFF_M1 - 8192, P::OFF_M2 - 8192}, off_p[3] = {P::OFF_T, P::OFF_T + P::TERM, P::OFF_P2};
+        const uint64_t dm = desc_sw128(saddr(smem)), dp = desc_mn_sw128(saddr(smem), 8192);
 #pragma unroll
-        for (int k = 0; k < 24; ++k) {
-            const int ta3 = kTermA[k >> 2], m = ta3 == 2 ? P::OFF_M2 - 8192 : ta3 * P::ATOM;
-            mma_bf16_on(one, tmem, desc_add(desc_sw128(saddr(smem)), m + (k & 3) * 32),
-                        desc_add(dt, kTermB[k >> 2] * P::TERM + (k & 3) * 2048), idM, k > 0);
-        }
-        mma_commit_on(one, &bar[2]);
+        for (int k = 0; k < 24; ++k)
+            mma_bf16_on(one, tmem, desc_add(dm, off_m[kTermA[k >> 2]] + (k & 3) * 32), desc_add(dp, off_p[kTermB[k >> 2]] + (k & 3) * 2048), idM, k > 0);
+        mma_commit_on(one, &bar[3]);
     }
-    const bool began = ok;
-    ok = ok && mbar_wait(&bar[2], 0);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
+    wait(3);
     __syncthreads();                                // (a wait that ran out in another warp: its MMAs are drained below)
-    // ---- the terms of both into shared memory as the walk wants them, and out in one copy
+    // ---- the terms of both into shared memory as the walk wants them, and out
     char *unit = a.ws + ((static_cast<size_t>(blockIdx.z) * ta.chunks + c) * a.H + h) * Unit<DK>::BYTES;
     if (ok) {
         if ((warp & 3) * 32 < DK)
             stage_row(tmem + lanes + 64 + 32 * half, smem, Unit<DK>::E_BYTES, (warp & 3) * 32 + lane, half);
-        if (!keys) stage_row(tmem + lanes + 32 * half, smem + Unit<DK>::OFF_MP, Unit<DK>::MP_BYTES, t, half);
         if (tid < kC) reinterpret_cast<float *>(unit + Unit<DK>::OFF_GAMMA)[tid] = sGam[tid];
     } else if (lane == 0) {                         // one more bounded wait for what was issued
         atomicOr(a.status, kStatusTimeout);
-        if (began && !mbar_wait(&bar[2], 0)) atomicOr(a.status, GDN_STATUS_DRAIN);
-        if (!began && !mbar_wait(&bar[1], 0)) atomicOr(a.status, GDN_STATUS_DRAIN);
+        if (!mbar_wait(&bar[issued], 0)) atomicOr(a.status, GDN_STATUS_DRAIN);
     }
+    fence_proxy_async();
+    __syncthreads();
+    if (tid == 0) {
+        bulk_store(unit, smem, 3 * Unit<DK>::E_BYTES);
+        bulk_store_wait();
+    }
+    __syncthreads();
+    if (ok && !keys) stage_row(tmem + lanes + 32 * half, smem, Unit<DK>::MP_BYTES, t, half);
     fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
-        bulk_store(unit, smem, Unit<DK>::OFF_GAMMA);
+        bulk_store(unit + Unit<DK>::OFF_MP, smem, 3 * Unit<DK>::MP_BYTES);
         bulk_store_wait();
     }
     if (warp == 1) tmem_dealloc(tmem, 128);
@@ -974,8 +1032,8 @@ int walk_columns(const gdn_advance_dims *d, bool last) {
 }
 
 // The chunks come in launches of the two kernels, so that the first one's work for the next chunks runs beside the walk,
-// on SMs that the walk leaves free: beside c chunks of it there is time for r c.  The first launch's own work runs alone (16 us for
-// three CTAs on an SM), and each launch costs some 12 us (by heads 20: more state comes in and goes out); their number and the
+// on SMs that the walk leaves free: beside c chunks of it there is time for r c.  The first launch's own work runs alone (5.3 us a
+// chunk and SM), and each launch costs some 12 us (by heads 20: more state comes in and goes out); their number and the
 // first one's size follow from that.  8192 tokens of 16 heads: 224 us in three launches, 252 in one, 250 in six; 8 prompts of 16
 // heads, whose walk leaves few SMs: 218 in one, 225 in two.
 struct Segments {
