@@ -1131,8 +1131,13 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-// Up to 32 tokens the token-by-token kernel is faster.
-bool advance_tc_shape(const gdn_advance_dims *d) { return d->in_dtype == GDN_DTYPE_BF16 && d->T > 32; }
+// Short chunks go token by token, whose time grows with them, where the chunked form's is that of a whole chunk (heads of 128 and
+// 128): 16 heads 11.3 us for 32 tokens and 13.9 for 40, chunked 13.6; where its CTAs (32 value columns each) share the SMs,
+// 128 heads 14.2 for 16 and 20.7 for 24, chunked 20.9; 512 heads 46 and 68, chunked 63.
+bool advance_tc_shape(const gdn_advance_dims *d) {
+    const bool share = static_cast<long long>(d->B) * d->H * (d->dv / 32) > sm_count();
+    return d->in_dtype == GDN_DTYPE_BF16 && d->T > (share ? 23 : 38);
+}
 
 int64_t advance_tc_workspace(const gdn_advance_dims *d) {
     return unit_bytes(d) * d->H * seqs_per_launch(d) * largest_launch(d) * buffers(d);

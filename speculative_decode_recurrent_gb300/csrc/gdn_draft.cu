@@ -24,14 +24,16 @@
 #include "gdndraft.h"
 #include "pair_math.cuh"
 #include "replay_common.h"
+#include "tc_common.cuh"
 
 namespace gdn {
 namespace {
 
+using tc::sm_count;
+
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kMaxT = 64;
-constexpr int kSmallV = 4096;                       // vocabularies that one CTA takes alone
 
 struct DraftArgs {
     const int32_t *tokens, *parent;
@@ -462,16 +464,19 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1) 
 {
     accept_body<kCluster, ROWS, VEC>(a);
 }
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) draft_accept_small_kernel(const DraftArgs a)
+template <int ROWS, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) draft_accept_one_kernel(const DraftArgs a)
 {
-    accept_body<1, 2, VEC>(a);
+    accept_body<1, ROWS, VEC>(a);
 }
 
 template <int ROWS>
-cudaError_t launch(const DraftArgs &a, bool vec, cudaStream_t s) {
-    const dim3 grid(kCluster, a.B);
+cudaError_t launch(const DraftArgs &a, bool one, bool vec, cudaStream_t s) {
     const size_t smem = static_cast<size_t>(a.segs) * sizeof(Two);
+    if (one)
+        return vec ? launch_pdl(draft_accept_one_kernel<ROWS, true>, dim3(1, a.B), dim3(kThreads), smem, s, a)
+                   : launch_pdl(draft_accept_one_kernel<ROWS, false>, dim3(1, a.B), dim3(kThreads), smem, s, a);
+    const dim3 grid(kCluster, a.B);
     return vec ? launch_pdl(draft_accept_kernel<ROWS, true>, grid, dim3(kThreads), smem, s, a)
                : launch_pdl(draft_accept_kernel<ROWS, false>, grid, dim3(kThreads), smem, s, a);
 }
@@ -490,22 +495,20 @@ extern "C" int gdn_draft_accept(const gdn_draft_dims *d, const int32_t *tokens, 
     if (d->p_stride < d->V || (draft && d->q_stride < d->V)) return GDN_ERR_DIMS;
     if (d->B == 0) return GDN_OK;
     if (!tokens || !probs || !u || !accepted || !next || !status || (parent && !path)) return GDN_ERR_NULL;
-    // Terms of a segment: a CTA's 16 warps each get one as far as the vocabulary goes, 1024 at most (more in flight).
-    const bool small = d->V <= kSmallV;
-    const int share = small ? d->V : (d->V + kCluster - 1) / kCluster;
-    const int rows = small || share <= 256 * kWarps ? 2 : share <= 512 * kWarps ? 4 : 8;
+    // One CTA for a sequence where the vocabulary is small (chains of 3, device time: 4096 probabilities 5.0 us, by clusters 5.3; 16384
+    // 8.3 and 5.2), or where the clusters of so many sequences would come in several waves (two CTAs share an SM): 64 sequences of
+    // 32768 10.1 us and 13.6, of 65536 15.3 and 15.5; 256 of 131072 46 and 72.
+    const long long slots = 2ll * sm_count();
+    const bool one = d->V <= 4096 || (kCluster * static_cast<long long>(d->B) > slots && d->V <= 131072 && d->V <= 512ll * d->B);
+    // Terms of a segment: a CTA's 16 warps each get one as far as the vocabulary goes, 1024 at most (more in flight: 64 chains over
+    // 262144 take 32.6 us, in segments of 256 terms 38.5; one over 32768 5.6, in segments of 512 6.0).
+    const int share = one ? d->V : (d->V + kCluster - 1) / kCluster;
+    const int rows = share <= 256 * kWarps ? 2 : share <= 512 * kWarps ? 4 : 8;
     DraftArgs a{tokens, parent, probs, draft, u, draft_len, accepted, next, path, status, d->p_stride, d->q_stride,
                 d->B, d->T, d->V, (share + rows * 128 - 1) / (rows * 128)};
     // 16-byte loads where every row begins on such a boundary
     const bool vec = reinterpret_cast<uintptr_t>(probs) % 16 == 0 && d->p_stride % 4 == 0 &&
                      (!draft || (reinterpret_cast<uintptr_t>(draft) % 16 == 0 && d->q_stride % 4 == 0));
-    cudaError_t e;
-    if (small) {
-        const size_t smem = static_cast<size_t>(a.segs) * sizeof(Two);
-        e = vec ? launch_pdl(draft_accept_small_kernel<true>, dim3(1, d->B), dim3(kThreads), smem, stream, a)
-                : launch_pdl(draft_accept_small_kernel<false>, dim3(1, d->B), dim3(kThreads), smem, stream, a);
-    } else {
-        e = rows == 2 ? launch<2>(a, vec, stream) : rows == 4 ? launch<4>(a, vec, stream) : launch<8>(a, vec, stream);
-    }
+    const cudaError_t e = rows == 2 ? launch<2>(a, one, vec, stream) : rows == 4 ? launch<4>(a, one, vec, stream) : launch<8>(a, one, vec, stream);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
