@@ -23,10 +23,8 @@ __device__ __forceinline__ void part_range(int tiles, int i, int parts, int &fir
     end = static_cast<int>(static_cast<long long>(tiles) * (i + 1) / parts);
 }
 
-// Partial results of a unit's part: o [rows][D], m [rows], l [rows] in fp32; m in powers of two.
-inline size_t part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
-
-int chunk_join(const ChunkArgs &a, int rows, int d, bool bf16, cudaStream_t s);
+// Partial results of a unit's part: o [rows][D] ([D][rows] of the bf16 kernel), m [rows], l [rows] in fp32; m in powers of two.
+__host__ __device__ inline size_t part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
 
 // The bf16 kernel (gdn_attn_chunk_tc.cu).
 int64_t chunk_tc_workspace(const gdn_page_cache *c, const gdn_attn_dims *d);

@@ -203,9 +203,10 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
 
 // A warp per row: the parts of its unit, in their order.  Rows not in use have been written already where their whole tile
 // is not; the others get 0 here.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkArgs a, int tile_rows)
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkArgs a)
 {
+    constexpr int tile_rows = kRT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.x % (tile_rows / 8) * 8 + warp, rt = blockIdx.x / (tile_rows / 8), h = blockIdx.y, b = blockIdx.z;
     pdl_wait();
@@ -240,8 +241,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkArgs a, int 
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
         const float y = r < live ? o[c] * inv : 0.f;
-        if (BF16) static_cast<__nv_bfloat16 *>(a.out)[row * D + lane + 32 * c] = __float2bfloat16_rn(y);
-        else static_cast<float *>(a.out)[row * D + lane + 32 * c] = y;
+        static_cast<float *>(a.out)[row * D + lane + 32 * c] = y;
     }
     if (a.lse && lane == 0) a.lse[row] = r < live ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
@@ -267,7 +267,10 @@ int launch_core(const gdn_page_cache *c, const gdn_attn_dims *d, ChunkArgs a, cu
         return GDN_ERR_LAUNCH;
     const dim3 grid(static_cast<unsigned>(a.row_tiles) * a.splits, c->Hkv, d->B);
     if (launch_pdl(chunk_core_kernel<D>, grid, dim3(kThreads), P::BYTES, s, a) != cudaSuccess) return GDN_ERR_LAUNCH;
-    return a.splits == 1 ? GDN_OK : chunk_join(a, kRT, D, false, s);
+    if (a.splits > 1 &&
+        launch_pdl(chunk_join_kernel<D>, dim3(static_cast<unsigned>(a.row_tiles) * (kRT / 8), c->Hkv, d->B), dim3(256), 0, s, a) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    return GDN_OK;
 }
 
 int check_chunk(const gdn_page_cache *c, const gdn_attn_dims *d) {
@@ -277,20 +280,6 @@ int check_chunk(const gdn_page_cache *c, const gdn_attn_dims *d) {
 }
 
 }  // namespace
-
-int chunk_join(const ChunkArgs &a, int rows, int d, bool bf16, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.row_tiles) * (rows / 8), a.s.Hkv, a.s.B), block(256);
-    cudaError_t e;
-    if (bf16)
-        e = d == 64 ? launch_pdl(chunk_join_kernel<64, true>, grid, block, 0, s, a, rows)
-            : d == 128 ? launch_pdl(chunk_join_kernel<128, true>, grid, block, 0, s, a, rows)
-                       : launch_pdl(chunk_join_kernel<256, true>, grid, block, 0, s, a, rows);
-    else
-        e = d == 64 ? launch_pdl(chunk_join_kernel<64, false>, grid, block, 0, s, a, rows)
-            : d == 128 ? launch_pdl(chunk_join_kernel<128, false>, grid, block, 0, s, a, rows)
-                       : launch_pdl(chunk_join_kernel<256, false>, grid, block, 0, s, a, rows);
-    return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
-}
 
 }  // namespace gdn
 

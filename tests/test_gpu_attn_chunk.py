@@ -202,7 +202,7 @@ def test_expired_wait_writes_nothing(d):
 def test_a_layer_for_staging_takes_a_smaller_workspace():
     """A layer of more tokens than a verify takes may share a verify's workspace; chunk refuses one that it needs more of."""
     import speculative_decode_recurrent_gb300 as lib
-    c = Case([500], [100], 100, 4, 2, 128, 16, BF, seed=39)
+    c = Case([5000], [100], 100, 4, 2, 128, 16, BF, seed=39)     # (long enough for parts of the keys)
     idx = c.layer.state_idx
     dims = lib.AttnDims(B=1, T=100, Hq=4, scale=c.scale)
     small = torch.empty(16, dtype=torch.uint8, device="cuda")
@@ -227,3 +227,30 @@ def test_no_sequences_and_wrong_tensors(dtype):
         with pytest.raises((ValueError, TypeError)):
             c.layer.chunk(bad, c.out)
     assert (c.out == 7).all()
+
+
+@pytest.mark.parametrize("past,T", [(0, 130), (1500, 80)])
+def test_outputs_on_any_16_byte_boundary(past, T):
+    c = Case([past], [T - 3], T, 6, 2, 128, 16, BF, seed=41)
+    room = torch.full((c.out.numel() + 16,), 7.0, dtype=BF, device="cuda")
+    c.out = room[8:-8].view(c.out.shape)
+    assert c.out.data_ptr() % 32 == 16
+    c.run()
+    c.check()
+    assert (room[:8] == 7).all() and (room[-8:] == 7).all()
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(256, 8, 2), (128, 16, 2), (64, 16, 2)])
+def test_many_short_units_and_calls(d, Hq, Hkv):
+    """Prompts of a few tiles, so that a CTA takes many units one after the other, and many calls in a row: every one gives
+    the first one's bits."""
+    c = Case([0, 3, 300, 64] * 4, [130, 80, 1, 0, 65, 127, 128, 129, 66, 130, 9, 100, 130, 2, 78, 130], 130, Hq, Hkv, d, 16, BF, seed=42)
+    lens = i32(c.lens)
+    c.layer.chunk(c.qd, c.out, lse=c.lse, chunk_len=lens)
+    first = c.out.clone(), c.lse.clone()
+    c.check()
+    for _ in range(200):
+        c.layer.chunk(c.qd, c.out, lse=c.lse, chunk_len=lens)
+    torch.cuda.synchronize()
+    assert int(c.cache.status.item()) == 0
+    assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
