@@ -2,7 +2,8 @@
 DeltaNet state on sm_103a).
 
 Argument marshalling only: every step of the path runs in the CUDA kernels of
-``csrc/gdn_replay.cu`` behind the C ABI declared in ``include/gdnreplay.h``.
+``csrc/`` behind the C ABI declared in ``include/`` (``gdnreplay.h``: the recurrence;
+``gdnlayer.h``, ``gdnattn.h``, ``gdndraft.h``: what stands beside it).
 PyTorch supplies device memory and the current stream.  There is no CPU
 fallback: if the shared library cannot be built or loaded, every call raises.
 """

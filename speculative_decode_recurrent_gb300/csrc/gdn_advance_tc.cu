@@ -471,9 +471,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) advance_prep_kernel(const TcA
 }
 
 // ------------------------------------------------------------- the walk over the chunks, by slices
-// One CTA per (slice of 32 value columns, head, sequence): the walk for few heads, whose chain of dependent steps bounds it
-// (about 2600 cycles a chunk).  S and x are the B operands: rows of 32 first, 32 second and 32 third terms, so one product of
-// 96 columns has all of them (55 cycles an MMA, against 39 for 32 columns).
+// One CTA per (slice of 32 or 16 value columns, head, sequence): the walk for few heads, whose chain of dependent steps bounds it
+// (3100 cycles a chunk, with 16 columns 2580: 800 to [K;Q] S^T, 900 to x, 800 to E x, 600 to the new S).  S and x are the B operands:
+// rows of a slice's first, second and third terms, so one product has all of them (55 cycles an MMA of 96 columns, against 39
+// for 32).
 template <int DK, int SL> struct SlicePlan {
     static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES;
     static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4, V_AT = 3 * Unit<DK>::MP_BYTES + 1024, MP = V_AT + (kC * SL * 2 + 1023) / 1024 * 1024;   // M P and gamma, values
@@ -584,7 +585,7 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         // ------------------------------------------------------ loads
         // Keys and queries go when the first product of two chunks before is done, M P (with gamma and the values) after the last
         // product of two before, and E, the last to be free, after its one use in the chunk before.  (With one barrier for all, a chunk's operands came no sooner
-        // than they were needed: 3000 cycles a chunk instead of 2400.)
+        // than they were needed: 600 cycles a chunk more.)
         const int hk = h / (a.H / a.Hk);
         int c = 0, part = 0;
         for (; c < chunks; ++c) {
@@ -761,7 +762,8 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 // One CTA per (head of 128 value columns, sequence): the walk for many heads, where the work on an SM counts and not the chain.
 // Here the state's columns are the rows (TMEM lanes): S and x are the A operands, straight from TMEM, and keys, queries, E and M P
 // the B operands as they lie.  A head costs an SM 240 KB of shared memory traffic a chunk instead of the 800 KB of
-// four slices, and nothing of S or x goes through it.
+// four slices, and nothing of S or x goes through it: 6500 cycles a chunk, of which the MMAs are 3900 (8 prompts of 16 heads, up to
+// 32 chunks: 115 us).
 //
 // TMEM columns: S (three terms, dk / 2 each), [K;Q] S^T and over it x (three terms of 32), E x, M P x.
 template <int DK> struct HeadPlan {

@@ -28,7 +28,7 @@ __device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpr
 
 // 64 rows x 64 keys a tile, 16 x 16 threads with 4 x 4 scores and 4 x D / 16 sums each.  A tile's 16 reads of 16
 // bytes serve 64 products in 32 two-wide instructions, so the products bound it, then the tile's
-// loads, which nothing hides within a CTA.
+// loads, which nothing hides within a CTA (29 TFLOP/s over long contexts; 3 of 67 to 150 tokens after 5 to 700 38 us).
 template <int D>
 __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
 {
@@ -248,9 +248,10 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkArgs a)
 
 int core_tokens(const gdn_page_cache *c, const gdn_attn_dims *d) { return kRT / (d->Hq / c->Hkv); }
 int core_tiles(const gdn_page_cache *c, const gdn_attn_dims *d) { return (d->T + core_tokens(c, d) - 1) / core_tokens(c, d); }
-// Parts of the key axis: enough CTAs for two waves, as far as one row tile has keys for them.
+// Parts of the key axis: four CTAs for each SM, as far as one row tile has keys for them: 256 tokens after 20000
+// (16 and 2 heads of 128) 1459 us, with two CTAs for each 1705, with one 1892; 3 of 150 after 400 (12 and 3 of 64) 35, 35, 49.
 int core_splits(const gdn_page_cache *c, const gdn_attn_dims *d) {
-    const long long units = static_cast<long long>(d->B) * c->Hkv * core_tiles(c, d), want = 2 * sm_count();
+    const long long units = static_cast<long long>(d->B) * c->Hkv * core_tiles(c, d), want = 4 * sm_count();
     const long long most = (static_cast<long long>(c->max_pages) * c->page + 4 * kKT - 1) / (4 * kKT);
     long long n = units >= want ? 1 : (want + units - 1) / units;
     if (n > most) n = most;

@@ -12,7 +12,7 @@
 // head) whose softmaxes and products overlap.  Tiles of 128 keys leave TMEM for one score buffer of each row tile, so a
 // tile's softmax, its weights' product and the next scores follow one another: a pair's tiles take some 2500 cycles, their MMAs
 // 2000.  (Tiles of 64 keys in two buffers: 2 x 1770.)  4 sequences of 4096 tokens after 16384: 1.5 ms, 1640 TFLOP/s; 4 prompts of up
-// to 4096 tokens 168 us; 256 tokens after 60001 (16 query heads, 2 key heads of 128) 102 us.
+// to 4096 tokens 168 us; 256 tokens after 60001 (16 query heads, 2 key heads of 128) 98 us.
 //
 // Roles.  Two groups of 256 threads, two per row (each half of a tile's keys; the scores of a row are in registers), and
 // for each group a warp that issues: O += P_i V_i, then the scores of the next tile into the buffer that held P_i (the weights
@@ -595,12 +595,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
 }
 
-// The parts of a unit of 128 rows, joined: o [d][128 rows], m [128], l [128] each.  A thread has a row's 16 columns.
+// The parts of a unit of 128 rows, joined: o [d][128 rows], m [128], l [128] each.  A thread has a row's 8 columns, of four parts at
+// a time: what bounds it is the way to L2 (19 MB of 9 parts for 256 tokens of 16 heads of 128).
 template <int D>
-__global__ void __launch_bounds__(D * 2) chunk_tc_join_kernel(const ChunkArgs a)
+__global__ void __launch_bounds__(D * 4) chunk_tc_join_kernel(const ChunkArgs a)
 {
-    constexpr int Q = kRows / 32;
-    const int lane = threadIdx.x & 31, c0 = threadIdx.x / 32 * 16, r = blockIdx.x % Q * 32 + lane, rt = blockIdx.x / Q, h = blockIdx.y, b = blockIdx.z;
+    constexpr int Q = kRows / 32, C = 8, SOME = 4;
+    const int lane = threadIdx.x & 31, c0 = threadIdx.x / 32 * C, r = blockIdx.x % Q * 32 + lane, rt = blockIdx.x / Q, h = blockIdx.y, b = blockIdx.z;
     pdl_wait();
     pdl_release();
     const Seq sq = load_seq<true>(a.s, b);
@@ -608,33 +609,50 @@ __global__ void __launch_bounds__(D * 2) chunk_tc_join_kernel(const ChunkArgs a)
     if (sq.bad || live <= 0) return;                // (a tile without rows in use has been written already)
     const size_t unit = (static_cast<size_t>(b) * a.s.Hkv + h) * a.row_tiles + rt, step = part_floats(kRows, D);
     const float *w = a.ws + unit * a.splits * step + r;
-    float m = -INFINITY, l = 0.f, o[16];
-#pragma unroll 4
-    for (int i = 0; i < a.splits; ++i) m = fmaxf(m, w[i * step + D * kRows]);
-    const float ref = r < live && m != -INFINITY ? m : 0.f;
+    float m = -INFINITY, l = 0.f, o[C];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) o[c] = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < a.splits; ++i) {
-        const float *p = w + i * step;
-        const float li = p[(D + 1) * kRows], f = ex2(p[D * kRows] - ref);
-        l = fmaf(f, li, l);
+    for (int c = 0; c < C; ++c) o[c] = 0.f;
+    for (int i0 = 0; i0 < a.splits; i0 += SOME) {
+        float x[SOME][C], mi[SOME], li[SOME];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const float x = p[(c0 + c) * kRows];    // (not written by a part without keys of this row's tile)
-            o[c] = li == 0.f ? o[c] : fmaf(f, x, o[c]);
+        for (int i = 0; i < SOME; ++i) {            // (past the last part: the last one again, without weight)
+            const float *p = w + min(i0 + i, a.splits - 1) * step;
+            mi[i] = p[D * kRows];
+            li[i] = p[(D + 1) * kRows];
+#pragma unroll
+            for (int c = 0; c < C; ++c) x[i][c] = p[(c0 + c) * kRows];         // (not written by a part without keys of this row's tile)
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < SOME; ++i) {
+            if (i0 + i >= a.splits) li[i] = 0.f;
+            if (li[i] != 0.f) top = fmaxf(top, mi[i]);
+        }
+        const float ref = top == -INFINITY ? 0.f : top, fix = ex2(m - ref);
+        m = top;
+        l *= fix;
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] *= fix;
+#pragma unroll
+        for (int i = 0; i < SOME; ++i) {
+            const float f = ex2(mi[i] - ref);
+            if (li[i] != 0.f) {
+                l = fmaf(f, li[i], l);
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[c] = fmaf(f, x[i][c], o[c]);
+            }
         }
     }
     if (r >= rows) return;
     const size_t row = (static_cast<size_t>(b) * a.s.T + t0 + r / a.G) * a.Hq + h * a.G + r % a.G;
     const float inv = 1.f / l;
-    uint32_t y[8];
+    uint32_t y[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 4; ++k) {
         const __nv_bfloat162 z = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
         y[k] = r < live ? *reinterpret_cast<const uint32_t *>(&z) : 0u;
     }
-    store_32(static_cast<__nv_bfloat16 *>(a.out) + row * D + c0, y, (reinterpret_cast<uintptr_t>(a.out) & 31) == 0);
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + c0) = make_uint4(y[0], y[1], y[2], y[3]);
     if (a.lse && c0 == 0) a.lse[row] = r < live ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -705,7 +723,7 @@ int launch(const gdn_page_cache *c, const gdn_attn_dims *d, ChunkArgs a, cudaStr
     if (grid > 0x7fffffffLL) return GDN_ERR_DIMS;
     if (launch_pdl(chunk_tc_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(P::THREADS), P::BYTES, s, mq, mk, mv, a) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    if (a.splits > 1 && launch_pdl(chunk_tc_join_kernel<D>, dim3(static_cast<unsigned>(a.row_tiles) * (kRows / 32), c->Hkv, d->B), dim3(D * 2), 0, s,
+    if (a.splits > 1 && launch_pdl(chunk_tc_join_kernel<D>, dim3(static_cast<unsigned>(a.row_tiles) * (kRows / 32), c->Hkv, d->B), dim3(D * 4), 0, s,
                                    a) != cudaSuccess)
         return GDN_ERR_LAUNCH;
     return GDN_OK;

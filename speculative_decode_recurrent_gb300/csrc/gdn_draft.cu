@@ -16,7 +16,8 @@
 // What bounds it: a few rows of V numbers per sequence, and a chain of dependent steps (tokens, their probabilities,
 // the walk, the pass, its sum across the cluster, the search).  A cluster of eight CTAs takes a sequence, each a
 // stretch of the vocabulary, in segments of 1024 terms per warp (256 or 512 where those would leave warps without one); two
-// CTAs share an SM.
+// CTAs share an SM.  On the device: a chain of 8 over 32768 probabilities 5.6 us, 32 chains of 16 over 131072 12 (half of the copy
+// bandwidth for the rows that have to be read).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
