@@ -236,8 +236,8 @@ int gdn_replay_advance(const gdn_advance_dims *dims, float *state, const int32_t
                        float *out, void *workspace, int64_t workspace_bytes, int32_t *status,
                        cudaStream_t stream);
 
-/* Bytes of workspace that gdn_replay_advance needs for these dims on the current device, or a
- * negative GDN_ERR_* code. */
+/* Bytes of workspace that gdn_replay_advance needs for these dims on the current device (enough for a smaller T
+ * too), or a negative GDN_ERR_* code. */
 int64_t gdn_replay_advance_workspace(const gdn_advance_dims *dims);
 
 /*

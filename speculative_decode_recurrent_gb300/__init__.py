@@ -394,7 +394,7 @@ class ReplayLayer:
         return got
 
     def advance_workspace(self, T, Hk=None):
-        """A workspace for ``advance`` with T tokens per sequence and Hk key heads (None: as many as value
+        """A workspace for ``advance`` with up to T tokens per sequence and Hk key heads (None: as many as value
         heads), or None where none is needed.  Layers that run one after the other may share one."""
         _, n = self._advance_dims(T, self.d.H if Hk is None else Hk)
         return torch.empty(n, dtype=torch.uint8, device=self.status.device) if n else None

@@ -1065,17 +1065,22 @@ Segments segments(const gdn_advance_dims *d) {
     }
     return s;
 }
-// Chunks of the largest launch.
-int largest_launch(const gdn_advance_dims *d) {
+// Two workspaces take turns, the first of as many chunks as its largest launch has; both together have no more than all chunks, nor
+// than twice the most of a launch.  (Where sequences come in several groups the turns go on, so each has room for any launch.)
+int first_room(const gdn_advance_dims *d) {
     const Segments g = segments(d);
-    int largest = 0, size = 0;
+    const bool groups = seqs_per_launch(d) < d->B;
+    int room = 0, size = 0;
     for (int i = 0, rest = all_chunks(d); rest > 0; ++i, rest -= size) {
         size = g.next(i, size, rest);
-        if (size > largest) largest = size;
+        if ((groups || i % 2 == 0) && size > room) room = size;
     }
-    return largest;
+    return room;
 }
-int buffers(const gdn_advance_dims *d) { return largest_launch(d) < all_chunks(d) || seqs_per_launch(d) < d->B ? 2 : 1; }
+int64_t room(const gdn_advance_dims *d) {           // of both; does not fall where T grows
+    const int64_t all = all_chunks(d), most = segments(d).most, both = 2 * (seqs_per_launch(d) < d->B ? (all < most ? all : most) : most);
+    return seqs_per_launch(d) < d->B || both < all ? both : all;
+}
 
 // Keys, queries or values as [B T][heads][dim]; boxes of `cols` columns of one head, 64 tokens.
 bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int heads, int dim, int64_t stride, int cols, bool swizzle) {
@@ -1112,7 +1117,7 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
     };
     const int all = all_chunks(d), seqs = seqs_per_launch(d);
     const Segments g = segments(d);
-    const int64_t half = unit_bytes(d) * d->H * seqs * largest_launch(d);
+    const int64_t second = unit_bytes(d) * d->H * seqs * first_room(d);
     TcAdvance ta{a, 0, 0, 0, d->dv, 0};
     for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += seqs) {
         const int nb = d->B - ta.b0 < seqs ? d->B - ta.b0 : seqs;
@@ -1125,7 +1130,7 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
             if (e == cudaSuccess) e = walk(columns[last], nb, mv[last], ta);
             if (e != cudaSuccess) return GDN_ERR_LAUNCH;
             ta.behind = 1;
-            ta.a.ws = ta.a.ws == a.ws ? a.ws + half : a.ws;
+            ta.a.ws = ta.a.ws == a.ws ? a.ws + second : a.ws;
         }
     }
     return GDN_OK;
@@ -1142,7 +1147,7 @@ bool advance_tc_shape(const gdn_advance_dims *d) {
 }
 
 int64_t advance_tc_workspace(const gdn_advance_dims *d) {
-    return unit_bytes(d) * d->H * seqs_per_launch(d) * largest_launch(d) * buffers(d);
+    return unit_bytes(d) * d->H * seqs_per_launch(d) * room(d);
 }
 
 int advance_tc(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {

@@ -360,3 +360,24 @@ def test_advance_expired_wait_writes_nothing():
     c.layer.d.flags = 0
     c.run()
     c.check(True)
+
+
+@pytest.mark.parametrize("B,H,dk,dv", [(1, 16, 128, 128), (2, 4, 64, 64), (8, 16, 128, 128), (1, 64, 128, 64), (40, 40, 64, 128)])
+def test_a_workspace_is_enough_for_fewer_tokens(B, H, dk, dv):
+    import speculative_decode_recurrent_gb300 as lib
+    need = [lib.gdn_replay_advance_workspace(lib.AdvanceDims(B=B, T=T, H=H, Hk=H, dk=dk, dv=dv, n_slot=B, in_dtype=lib.DTYPE_BF16, scale=1.0,
+                                                             q_stride=H * dk, k_stride=H * dk, v_stride=H * dv))
+            for T in list(range(1, 3000, 37)) + [4096, 8192, 10000, 30000, 100000]]
+    assert all(a <= b for a, b in zip(need, need[1:])) and need[-1] <= 768 << 20
+
+
+@pytest.mark.parametrize("lens,T,H,dv", [([2500], 2500, 2, 128), ([1500, 700, 1400], 1500, 14, 128), ([40, 1, 64], 70, 3, 64)])
+def test_advance_stays_in_its_workspace(lens, T, H, dv):
+    c = Case(lens, T, H, H, 128, dv, BF, seed=23)
+    n = c.layer.advance_workspace(T, H).numel()
+    room = torch.full((n + 8192,), 171, dtype=torch.uint8, device="cuda")
+    c.run(workspace=room[4096:4096 + n])
+    c.check(True)
+    assert (room[:4096] == 171).all() and (room[4096 + n:] == 171).all()
+    with pytest.raises(Exception, match="-2|dims|DIMS|workspace"):
+        c.run(workspace=room[4096:4096 + n - 16])
