@@ -4,17 +4,19 @@
 // Token by token, a row i of the state (one value column) is independent of the others:
 //     w = beta (v_i - alpha S_i.k),   S_i <- alpha S_i + w k,   o_i = S_i.(scale q).
 // Eight lanes hold a row in registers, so a token costs a row two dot products over them.  A short call
-// (single tokens without a draft: 16 heads 4.6 us) is bound by its chain of loads and launch; a long one by that of
-// dependent instructions from token to token, some 400 cycles (fp32 keys and values have no tensor-core product; 333 tokens of
-// 30 heads 69 us.  Four tokens at a time, with their products among themselves made ahead, were no faster: 75.)
+// (single tokens without a draft: 16 heads 4 us) is bound by its chain of loads and launch; a long one by that of
+// dependent instructions from token to token, some 360 cycles (fp32 keys and values have no tensor-core product; 333 tokens of
+// 30 heads 64 us.  Four tokens at a time, with their products among themselves made ahead, took 75 where one at a time took 70; the last
+// output's sum beside the next token's 63, but a sixth longer where heads share the SMs.)
 #include <cuda_bf16.h>
 
 #include "advance_common.h"
+#include "tc_common.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kRows = 32, kLanes = 8, kThreads = kRows * kLanes;      // state rows of a CTA, lanes of a row
+constexpr int kLanes = 8;                                             // of a state row
 constexpr int kTile = 16;                                             // tokens staged at a time
 
 __device__ __forceinline__ void widen(const uint4 &r, float (&f)[8]) {
@@ -29,7 +31,7 @@ __device__ __forceinline__ void widen(const uint4 &r, float (&f)[8]) {
 
 // Rows of DK numbers of the tile's tokens, kept as they are in memory until they go to shared memory: a thread has
 // 8 numbers of each of PER rows.
-template <int DK, typename TIn> struct RowTile {
+template <int DK, typename TIn, int kThreads> struct RowTile {
     static constexpr int VECS = DK / 8, PER = (kTile * VECS + kThreads - 1) / kThreads;
     static constexpr int W = sizeof(TIn) == 2 ? 1 : 2;                // 16-byte words of 8 numbers
     uint4 raw[PER][W];
@@ -68,15 +70,15 @@ template <int DK, typename TIn> struct RowTile {
 __device__ __forceinline__ float wide(float x) { return x; }
 __device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// One CTA per (32 state rows, head, sequence).  Lane l of a row owns the columns 32 i + 4 l .. + 3, so that a row's
+// One CTA per (ROWS state rows, head, sequence).  Lane l of a row owns the columns 32 i + 4 l .. + 3, so that a row's
 // lanes move 128 contiguous bytes of the state at a time.  The next tile of tokens is on its way to
 // registers while the present one is in use.
-template <int DK, typename TIn>
-__global__ void __launch_bounds__(kThreads) advance_tokens_kernel(const AdvanceArgs a, int dv)
+template <int DK, typename TIn, int ROWS>
+__global__ void __launch_bounds__(ROWS * kLanes) advance_tokens_kernel(const AdvanceArgs a, int dv)
 {
-    constexpr int NC = DK / kLanes;
-    __shared__ float sK[2][kTile * DK], sQ[2][kTile * DK], sV[2][kTile * kRows], sA[2][kTile], sB[2][kTile];
-    const int row0 = blockIdx.x * kRows, h = blockIdx.y, b = blockIdx.z, H = a.H;
+    constexpr int NC = DK / kLanes, kThreads = ROWS * kLanes;
+    __shared__ float sK[2][kTile * DK], sQ[2][kTile * DK], sV[2][kTile * ROWS], sA[2][kTile], sB[2][kTile];
+    const int row0 = blockIdx.x * ROWS, h = blockIdx.y, b = blockIdx.z, H = a.H;
     const int tid = threadIdx.x, r = tid / kLanes, l = tid % kLanes, c0 = l * 4;
     pdl_wait();
     pdl_release();
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) advance_tokens_kernel(const AdvanceA
     const TIn *ki = static_cast<const TIn *>(a.k) + tok0 * a.k_stride + hk * DK;
     const TIn *vi = static_cast<const TIn *>(a.v) + tok0 * a.v_stride + h * dv + row0;
     const float *gi = a.g + tok0 * H + h, *bi = a.beta + tok0 * H + h;
-    RowTile<DK, TIn> tk, tq;
+    RowTile<DK, TIn, kThreads> tk, tq;
     float tv[2], tg = 0.f, tb = 0.f;
     auto load = [&](int t0) {
         const int m = min(kTile, n - t0);
@@ -99,8 +101,8 @@ __global__ void __launch_bounds__(kThreads) advance_tokens_kernel(const AdvanceA
         tq.load(qi + t0 * a.q_stride, a.q_stride, m, tid);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int t = (tid >> 5) + 8 * i;
-            tv[i] = t < m ? wide(vi[(t0 + t) * a.v_stride + (tid & 31)]) : 0.f;
+            const int t = tid / ROWS + 8 * i;
+            tv[i] = t < m ? wide(vi[(t0 + t) * a.v_stride + tid % ROWS]) : 0.f;
         }
         if (tid < m) {
             tg = gi[static_cast<size_t>(t0 + tid) * H];
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) advance_tokens_kernel(const AdvanceA
 #pragma unroll
             for (int m2 = 1; m2 < kLanes; m2 <<= 1) sk += __shfl_xor_sync(0xffffffffu, sk, m2);
             const float alpha = sA[buf][t];
-            const float w = sB[buf][t] * (sV[buf][t * kRows + r] - alpha * sk);
+            const float w = sB[buf][t] * (sV[buf][t * ROWS + r] - alpha * sk);
             float o = 0.f;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -161,8 +163,8 @@ __global__ void __launch_bounds__(kThreads) advance_tokens_kernel(const AdvanceA
 #pragma unroll
     for (int i = 0; i < NC / 4; ++i)
         *reinterpret_cast<float4 *>(st + 32 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-    for (int t = n + (tid >> 5); t < a.T; t += kThreads / 32)         // rows past the chunk
-        a.out[((tok0 + t) * H + h) * dv + row0 + (tid & 31)] = 0.f;
+    for (int t = n + tid / ROWS; t < a.T; t += kLanes)               // rows past the chunk
+        a.out[((tok0 + t) * H + h) * dv + row0 + tid % ROWS] = 0.f;
 }
 
 int check_advance(const gdn_advance_dims *d) {
@@ -182,11 +184,18 @@ int check_advance(const gdn_advance_dims *d) {
 }
 bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+template <typename TIn, int ROWS>
+cudaError_t launch_rows(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
+    const dim3 grid(d->dv / ROWS, d->H, d->B), block(ROWS * kLanes);
+    return d->dk == 64 ? launch_pdl(advance_tokens_kernel<64, TIn, ROWS>, grid, block, 0, s, a, d->dv)
+                       : launch_pdl(advance_tokens_kernel<128, TIn, ROWS>, grid, block, 0, s, a, d->dv);
+}
 template <typename TIn>
 cudaError_t launch_tokens(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
-    const dim3 grid(d->dv / kRows, d->H, d->B);
-    return d->dk == 64 ? launch_pdl(advance_tokens_kernel<64, TIn>, grid, dim3(kThreads), 0, s, a, d->dv)
-                       : launch_pdl(advance_tokens_kernel<128, TIn>, grid, dim3(kThreads), 0, s, a, d->dv);
+    // Fewer rows a CTA while each then has an SM of its own: its warps share the SM's way to shared memory (16 heads of 128 x 128, 32
+    // tokens: 16 rows 9.0 us, 32 rows 11.3; a token alone 3.6 and 4.3).
+    const long long rows = static_cast<long long>(d->B) * d->H * d->dv, sms = tc::sm_count();
+    return rows <= 8 * sms ? launch_rows<TIn, 8>(d, a, s) : rows <= 16 * sms ? launch_rows<TIn, 16>(d, a, s) : launch_rows<TIn, 32>(d, a, s);
 }
 
 }  // namespace

@@ -1139,11 +1139,11 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
 }  // namespace
 
 // Short chunks go token by token, whose time grows with them, where the chunked form's is that of a whole chunk (heads of 128 and
-// 128): 16 heads 11.3 us for 32 tokens and 13.9 for 40, chunked 13.6; where its CTAs (32 value columns each) share the SMs,
-// 128 heads 14.2 for 16 and 20.7 for 24, chunked 20.9; 512 heads 46 and 68, chunked 63.
+// 128): 16 heads, whose rows spread over the SMs, 9.0 us for 32 tokens and 11.3 for 40, chunked 13.6; with 32 rows a CTA 13.9 for 40;
+// where the CTAs share the SMs, 128 heads 14.2 for 16 and 20.7 for 24, chunked 20.9; 512 heads 46 and 68, chunked 63.
 bool advance_tc_shape(const gdn_advance_dims *d) {
-    const bool share = static_cast<long long>(d->B) * d->H * (d->dv / 32) > sm_count();
-    return d->in_dtype == GDN_DTYPE_BF16 && d->T > (share ? 23 : 38);
+    const long long rows = static_cast<long long>(d->B) * d->H * d->dv, sms = sm_count();
+    return d->in_dtype == GDN_DTYPE_BF16 && d->T > (rows <= 16 * sms ? 50 : rows <= 32 * sms ? 38 : 23);
 }
 
 int64_t advance_tc_workspace(const gdn_advance_dims *d) {

@@ -154,6 +154,14 @@ def test_advance_many_heads_and_long_prompts(B, T, H, Hk, dk, dv):
     assert torch.equal(c.out, first[0]) and torch.equal(c.layer.t["state"], first[1])
 
 
+@pytest.mark.parametrize("B,H,dk,dv", [(1, 4, 128, 128), (2, 9, 128, 128), (5, 6, 64, 64), (3, 13, 64, 128), (12, 16, 128, 64)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_advance_token_by_token_at_every_share_of_the_sms(B, H, dk, dv, dtype):
+    c = Case(ragged(B, 19, 3 * B), 19, H, H, dk, dv, dtype, seed=24, fresh=[b % 2 for b in range(B)])
+    c.run()
+    c.check(False)
+
+
 @pytest.mark.parametrize("T,dtype", [(300, BF), (20, BF), (70, F32)])
 def test_advance_decays_that_forget_the_state(T, dtype):
     """A log-decay of -infinity or far below what fp32 holds is a decay of 0: nothing of the state before it is left."""
