@@ -1142,8 +1142,9 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
 // 128): 16 heads, whose rows spread over the SMs, 9.0 us for 32 tokens and 11.3 for 40, chunked 13.6; with 32 rows a CTA 13.9 for 40;
 // where the CTAs share the SMs, 128 heads 14.2 for 16 and 20.7 for 24, chunked 20.9; 512 heads 46 and 68, chunked 63.
 bool advance_tc_shape(const gdn_advance_dims *d) {
+    if (d->in_dtype != GDN_DTYPE_BF16 || d->T <= 23) return false;
     const long long rows = static_cast<long long>(d->B) * d->H * d->dv, sms = sm_count();
-    return d->in_dtype == GDN_DTYPE_BF16 && d->T > (rows <= 16 * sms ? 50 : rows <= 32 * sms ? 38 : 23);
+    return d->T > (rows <= 16 * sms ? 50 : rows <= 32 * sms ? 38 : 23);
 }
 
 int64_t advance_tc_workspace(const gdn_advance_dims *d) {
