@@ -15,8 +15,11 @@
 #include "gdnlayer.h"
 #include "pair_math.cuh"
 #include "replay_common.h"
+#include "tc_common.cuh"
 
 namespace {
+
+using gdn::tc::sm_count;
 
 using gdn::launch_pdl;
 using gdn::pdl_release;
@@ -180,8 +183,10 @@ __global__ void conv_accept_kernel(int32_t *ring_pos, const int32_t *state_idx, 
 // ring's window for the first run) and the run's own, eight positions ahead of their use.  Long runs read the taps and
 // the window less often (8 prompts of 700 to 2048 tokens, 6144 channels: 67 us, 0.64 of the copy bandwidth; 79 with runs of 8),
 // short ones fill the GPU where there is little to do.  The first run's thread is the only one that reads its channels of the ring, so it also
-// puts the last W - 1 inputs there; the position moves one launch on, when every CTA has read it.
-constexpr int kStep = 8;
+// puts the last W - 1 inputs there; the position moves one launch on, when every CTA has read it, or at once where a sequence's
+// CTAs are a cluster: one launch instead of two, which is what short calls cost.
+constexpr int kStep = 8, kConvCluster = 16;
+__host__ __device__ constexpr int conv_threads(bool cluster) { return cluster ? 2 * kConvThreads : kConvThreads; }
 
 struct ConvAdvanceArgs {
     void *ring;
@@ -213,18 +218,19 @@ __device__ __forceinline__ ConvSeq conv_seq(const ConvAdvanceArgs &a, int b) {
     return s;
 }
 
-template <typename TIn, typename TOut, int W, int BLOCKS>
-__global__ void __launch_bounds__(kConvThreads) conv_advance_kernel(const ConvAdvanceArgs a, int chan_blocks)
+template <typename TIn, typename TOut, int W, int BLOCKS, bool CLUSTER>
+__global__ void __launch_bounds__(conv_threads(CLUSTER)) conv_advance_kernel(const ConvAdvanceArgs a, int chan_blocks)
 {
     using Raw = typename In4<TIn>::Raw;
     constexpr int RUN = kStep * BLOCKS;
     const int b = blockIdx.y, t0 = blockIdx.x / chan_blocks * RUN;
-    const int c0 = (blockIdx.x % chan_blocks * kConvThreads + threadIdx.x) * 4;
+    const int c0 = (blockIdx.x % chan_blocks * conv_threads(CLUSTER) + threadIdx.x) * 4;
     pdl_wait();
     pdl_release();
-    if (c0 >= a.D) return;
+    if (c0 >= a.D) return;                               // (a thread that has left is not waited for)
     const int D = a.D;
     const ConvSeq sq = conv_seq(a, b);
+    if (CLUSTER) asm volatile("barrier.cluster.arrive.release;" ::: "memory");        // the position has been read
     if (sq.bad) {
         if (c0 == 0 && t0 == 0) atomicOr(a.status, sq.bad);
         return;
@@ -332,6 +338,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_advance_kernel(const ConvAd
 #pragma unroll
                 for (int i = 0; i < 2; ++i) h[j][i] = z[j][i];
         }
+    }
+    if (CLUSTER) {
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (t0 == 0 && c0 == 0) a.ring_pos[sq.slot] = (sq.pos + n) % a.cap;
     }
 }
 
@@ -461,22 +471,44 @@ int launch_conv(const gdn_conv_dims *d, const ConvArgs &a, cudaStream_t s) {
     }
 }
 
-template <typename TIn, typename TOut, int BLOCKS>
+template <typename TIn, typename TOut, int BLOCKS, bool CLUSTER>
 cudaError_t launch_conv_runs(const gdn_conv_dims *d, const ConvAdvanceArgs &a, cudaStream_t s) {
-    const int cb = (d->D / 4 + kConvThreads - 1) / kConvThreads, run = kStep * BLOCKS;      // (runs x cb < 2^31: check_conv)
-    const dim3 grid(static_cast<unsigned>((d->T + run - 1) / run) * cb, d->B), block(kConvThreads);
-    return d->W == 1   ? launch_pdl(conv_advance_kernel<TIn, TOut, 1, BLOCKS>, grid, block, 0, s, a, cb)
-           : d->W == 2 ? launch_pdl(conv_advance_kernel<TIn, TOut, 2, BLOCKS>, grid, block, 0, s, a, cb)
-           : d->W == 3 ? launch_pdl(conv_advance_kernel<TIn, TOut, 3, BLOCKS>, grid, block, 0, s, a, cb)
-                       : launch_pdl(conv_advance_kernel<TIn, TOut, 4, BLOCKS>, grid, block, 0, s, a, cb);
+    const int threads = conv_threads(CLUSTER), cb = (d->D / 4 + threads - 1) / threads, run = kStep * BLOCKS;      // (runs x cb < 2^31: check_conv)
+    auto *kern = d->W == 1   ? conv_advance_kernel<TIn, TOut, 1, BLOCKS, CLUSTER>
+                 : d->W == 2 ? conv_advance_kernel<TIn, TOut, 2, BLOCKS, CLUSTER>
+                 : d->W == 3 ? conv_advance_kernel<TIn, TOut, 3, BLOCKS, CLUSTER>
+                             : conv_advance_kernel<TIn, TOut, 4, BLOCKS, CLUSTER>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((d->T + run - 1) / run) * cb, d->B);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cfg.gridDim.x;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    if (CLUSTER && cfg.gridDim.x > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, a, cb);
 }
 
 template <typename TIn, typename TOut>
 cudaError_t launch_conv_advance(const gdn_conv_dims *d, const ConvAdvanceArgs &a, cudaStream_t s) {
+    const int threads = conv_threads(true), cb = (d->D / 4 + threads - 1) / threads;
+    // A sequence's CTAs as a cluster where they all have an SM of their own: one token over 6144 channels 3.4 us, in two launches 3.9, and 2 us
+    // less on the host; 2 of 65 tokens over 200 channels 4.0 both.  64 single tokens over 6144 channels would take 7.4 instead of 5.0, the
+    // 65 tokens in runs of 32 5.8.
+    const long long ctas = static_cast<long long>((d->T + kStep - 1) / kStep) * cb;
+    if (ctas <= kConvCluster && ctas * d->B <= sm_count()) return launch_conv_runs<TIn, TOut, 1, true>(d, a, s);
     // Runs of 32 where there is enough to do for them (bf16, 6144 channels: 4096 tokens 22.9 us, with runs of 8 27.7; 2048 tokens
     // 13.7 and 13.9; 512 tokens 7.3 and 5.8).
     const bool many = static_cast<long long>(d->B) * d->T * (d->D / 4) >= 6ll << 19;
-    const cudaError_t e = many ? launch_conv_runs<TIn, TOut, 4>(d, a, s) : launch_conv_runs<TIn, TOut, 1>(d, a, s);
+    const cudaError_t e = many ? launch_conv_runs<TIn, TOut, 4, false>(d, a, s) : launch_conv_runs<TIn, TOut, 1, false>(d, a, s);
     return e != cudaSuccess ? e : launch_pdl(conv_position_kernel, dim3((d->B + 127) / 128), dim3(128), 0, s, a);
 }
 

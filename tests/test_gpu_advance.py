@@ -285,6 +285,9 @@ def test_advance_graph_and_stream_give_the_same_bits():
     (3, 7, 520, 65, [65, 1], [1, 1], True, False),
     (2, 1, 16, 1, [1, 0], [0, 1], False, True),
     (1, 1, 24, 130, [129, 8], [0, 1], True, True),
+    (4, 8, 6144, 1, [1, 0, 1], [0, 0, 1], True, True),       # a cluster's CTAs beside one another
+    (4, 3, 2056, 16, [16, 2, 15], [0, 1, 0], True, False),
+    (3, 4, 1032, 129, [129, 1, 64], [1, 0, 0], True, True),  # two CTAs of channels, more runs than a cluster has
 ])
 def test_conv_advance_matches_the_formula(W, cap, D, T, lens, fresh, silu, bias, din, dout):
     import speculative_decode_recurrent_gb300 as lib
