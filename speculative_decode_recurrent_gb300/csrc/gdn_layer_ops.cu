@@ -500,9 +500,9 @@ cudaError_t launch_conv_runs(const gdn_conv_dims *d, const ConvAdvanceArgs &a, c
 template <typename TIn, typename TOut>
 cudaError_t launch_conv_advance(const gdn_conv_dims *d, const ConvAdvanceArgs &a, cudaStream_t s) {
     const int threads = conv_threads(true), cb = (d->D / 4 + threads - 1) / threads;
-    // A sequence's CTAs as a cluster where they all have an SM of their own: one token over 6144 channels 3.4 us, in two launches 3.9, and 2 us
-    // less on the host; 2 of 65 tokens over 200 channels 4.0 both.  64 single tokens over 6144 channels would take 7.4 instead of 5.0, the
-    // 65 tokens in runs of 32 5.8.
+    // A sequence's CTAs as a cluster where they all have an SM of their own: 2 of 65 tokens over 200 channels 4.0 us on the device and 9.2 a
+    // call, in two launches 4.7 and 10.6; one token over 6144 channels 3.7 both.  64 single tokens would take 7.4 instead of 5.0, the 65
+    // tokens in runs of 32 5.8.
     const long long ctas = static_cast<long long>((d->T + kStep - 1) / kStep) * cb;
     if (ctas <= kConvCluster && ctas * d->B <= sm_count()) return launch_conv_runs<TIn, TOut, 1, true>(d, a, s);
     // Runs of 32 where there is enough to do for them (bf16, 6144 channels: 4096 tokens 22.9 us, with runs of 8 27.7; 2048 tokens
