@@ -1,6 +1,6 @@
 // gdn_attn_chunk.cu -- attention of a chunk of new tokens over the paged cache, for sm_103a: the C ABI entry
 // points (include/gdnattn.h), the kernel on the CUDA cores (fp32 caches: there is no fp32 tensor-core
-// product) and the join of split keys.  bf16 caches take gdn_attn_chunk_tc.cu.
+// product) and the join of its split keys.  bf16 caches take gdn_attn_chunk_tc.cu.
 //
 // Mathematics.  One pass over a row's keys with the running maximum m and sum l of its softmax in powers
 // of two: for each tile of keys m' = max(m, max s), o <- 2^(m - m') o + sum_j 2^(s_j - m') v_j, l likewise; out = o / l,

@@ -392,3 +392,27 @@ def test_advance_stays_in_its_workspace(lens, T, H, dv):
     assert (room[:4096] == 171).all() and (room[4096 + n:] == 171).all()
     with pytest.raises(Exception, match="-2|dims|DIMS|workspace"):
         c.run(workspace=room[4096:4096 + n - 16])
+
+
+def test_calls_on_two_streams_at_once():
+    """Prompts of several launches on two streams, each with its own workspace: the bits of one after the other."""
+    cases = [Case([2100, 1900], 2100, 3, 3, 128, 128, BF, seed=25), Case(ragged(9, 1100, 26), 1100, 8, 8, 128, 128, BF, seed=26)]
+    ws = [c.layer.advance_workspace(c.T, c.Hk) for c in cases]
+    want = []
+    for c, w in zip(cases, ws):
+        c.run(workspace=w)
+        torch.cuda.synchronize()
+        want.append((c.out.clone(), c.layer.t["state"].clone()))
+    lens, fresh = [i32(c.lens) for c in cases], [i32(c.fresh) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    start = [c.state.cuda() for c in cases]
+    for _ in range(5):
+        for c, s in zip(cases, start):
+            c.layer.t["state"].copy_(s)
+            c.out.fill_(3)
+        torch.cuda.synchronize()
+        for c, w, n, f, stream in zip(cases, ws, lens, fresh, streams):
+            c.layer.advance(c.q, c.k, c.v, c.g, c.beta, c.out, chunk_len=n, fresh=f, workspace=w, stream=stream)
+        torch.cuda.synchronize()
+        for c, (out, state) in zip(cases, want):
+            assert torch.equal(c.out, out) and torch.equal(c.layer.t["state"], state) and int(c.layer.status.item()) == 0

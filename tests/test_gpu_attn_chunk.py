@@ -254,3 +254,25 @@ def test_many_short_units_and_calls(d, Hq, Hkv):
     torch.cuda.synchronize()
     assert int(c.cache.status.item()) == 0
     assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+
+
+def test_calls_on_two_streams_at_once():
+    """Two layers' chunks, one whose keys are cut and one of many units, on two streams: the bits of one after the other."""
+    cases = [Case([6000], [120], 120, 16, 2, 128, 16, BF, seed=43), Case([0] * 12, [200, 130, 5, 0] * 3, 200, 16, 2, 128, 16, BF, seed=44),
+             Case([900, 0], [140, 77], 140, 8, 2, 256, 16, BF, seed=45)]
+    lens, want = [i32(c.lens) for c in cases], []
+    for c in cases:
+        c.run()
+        torch.cuda.synchronize()
+        want.append((c.out.clone(), c.lse.clone()))
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(10):
+        for c in cases:
+            c.out.fill_(3)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for c, n, stream in zip(cases, lens, streams):
+                c.layer.chunk(c.qd, c.out, lse=c.lse, chunk_len=n, stream=stream)
+        torch.cuda.synchronize()
+        for c, (out, lse) in zip(cases, want):
+            assert torch.equal(c.out, out) and torch.equal(c.lse, lse) and int(c.cache.status.item()) == 0
