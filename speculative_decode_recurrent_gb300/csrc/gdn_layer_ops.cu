@@ -181,10 +181,12 @@ __global__ void conv_accept_kernel(int32_t *ring_pos, const int32_t *state_idx, 
 // ------------------------------------------------- the convolution over committed tokens
 // A thread owns four channels of one sequence for a run of 8 BLOCKS positions: it reads the W - 1 inputs before the run (the
 // ring's window for the first run) and the run's own, eight positions ahead of their use.  Long runs read the taps and
-// the window less often (8 prompts of 700 to 2048 tokens, 6144 channels: 67 us, 0.64 of the copy bandwidth; 79 with runs of 8),
+// the window less often (8 prompts of 700 to 2048 tokens, 6144 channels: 62 us, 0.69 of the copy bandwidth; runs of 8 took 79
+// where these took 67),
 // short ones fill the GPU where there is little to do.  The first run's thread is the only one that reads its channels of the ring, so it also
 // puts the last W - 1 inputs there; the position moves one launch on, when every CTA has read it, or at once where a sequence's
-// CTAs are a cluster: one launch instead of two, which is what short calls cost.
+// CTAs are a cluster: one launch instead of two, which is what short calls cost.  Six CTAs share an SM (80 registers; with 96 five did: 67 us,
+// with 72, which spill, 66; fp32 inputs take more).
 constexpr int kStep = 8, kConvCluster = 16;
 __host__ __device__ constexpr int conv_threads(bool cluster) { return cluster ? 2 * kConvThreads : kConvThreads; }
 
@@ -219,7 +221,7 @@ __device__ __forceinline__ ConvSeq conv_seq(const ConvAdvanceArgs &a, int b) {
 }
 
 template <typename TIn, typename TOut, int W, int BLOCKS, bool CLUSTER>
-__global__ void __launch_bounds__(conv_threads(CLUSTER)) conv_advance_kernel(const ConvAdvanceArgs a, int chan_blocks)
+__global__ void __launch_bounds__(conv_threads(CLUSTER), CLUSTER || sizeof(TIn) == 4 ? 1 : 6) conv_advance_kernel(const ConvAdvanceArgs a, int chan_blocks)
 {
     using Raw = typename In4<TIn>::Raw;
     constexpr int RUN = kStep * BLOCKS;
@@ -505,8 +507,8 @@ cudaError_t launch_conv_advance(const gdn_conv_dims *d, const ConvAdvanceArgs &a
     // tokens in runs of 32 5.8.
     const long long ctas = static_cast<long long>((d->T + kStep - 1) / kStep) * cb;
     if (ctas <= kConvCluster && ctas * d->B <= sm_count()) return launch_conv_runs<TIn, TOut, 1, true>(d, a, s);
-    // Runs of 32 where there is enough to do for them (bf16, 6144 channels: 4096 tokens 22.9 us, with runs of 8 27.7; 2048 tokens
-    // 13.7 and 13.9; 512 tokens 7.3 and 5.8).
+    // Runs of 32 where there is enough to do for them (bf16, 6144 channels, with five CTAs an SM: 4096 tokens 22.9 us, with runs of 8
+    // 27.7; 2048 tokens 13.7 and 13.9; 512 tokens 7.3 and 5.8).
     const bool many = static_cast<long long>(d->B) * d->T * (d->D / 4) >= 6ll << 19;
     const cudaError_t e = many ? launch_conv_runs<TIn, TOut, 4, false>(d, a, s) : launch_conv_runs<TIn, TOut, 1, false>(d, a, s);
     return e != cudaSuccess ? e : launch_pdl(conv_position_kernel, dim3((d->B + 127) / 128), dim3(128), 0, s, a);
