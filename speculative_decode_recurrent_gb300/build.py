@@ -20,7 +20,8 @@ HEADERS = [os.path.join(ROOT, "include", "gdnreplay.h"), os.path.join(ROOT, "inc
            os.path.join(ROOT, "include", "gdnnonreplay.h"), os.path.join(ROOT, "include", "gdnattn.h"),
            os.path.join(PKG, "csrc", "replay_common.h"), os.path.join(PKG, "csrc", "tc_common.cuh"),
            os.path.join(ROOT, "include", "gdndraft.h"),
-           *(os.path.join(PKG, "csrc", f) for f in ("attn_common.h", "advance_common.h", "chunk_common.h", "tc_async.cuh", "pair_math.cuh"))]
+           *(os.path.join(PKG, "csrc", f) for f in ("attn_common.h", "advance_common.h", "advance_plan.h", "chunk_common.h", "tc_async.cuh",
+                                                  "pair_math.cuh"))]
 LIB = os.path.join(PKG, "_build", "libgdnreplay.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 
 #include "advance_common.h"
+#include "advance_plan.h"
 #include "pair_math.cuh"
 #include "tc_async.cuh"
 
@@ -31,7 +32,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kC = 64;                              // tokens of a chunk
+constexpr int kC = kChunkTokens;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What the first kernel leaves of a chunk of a head, as the second one's operands lie in shared memory:
@@ -1017,70 +1018,8 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int64_t kBudget = 768ll << 20;            // of workspace: what is beyond it follows in further launches
-
 int64_t unit_bytes(const gdn_advance_dims *d) { return d->dk == 64 ? Unit<64>::BYTES : Unit<128>::BYTES; }
-int all_chunks(const gdn_advance_dims *d) { return (d->T + kC - 1) / kC; }
-int seqs_per_launch(const gdn_advance_dims *d) {
-    const int64_t n = kBudget / 2 / (unit_bytes(d) * d->H);
-    return static_cast<int>(n < 1 ? 1 : n < d->B ? n : d->B);
-}
-// Value columns of a walk's CTA: slices of 32 while each has an SM of its own, heads beyond (which need 128 value columns);
-// slices of 16 where even those have (8192 tokens of 16 heads: 172 us of walking, against 205 with 32) and no first kernel is to run beside
-// them, for which they leave no SMs.
-int walk_columns(const gdn_advance_dims *d, bool last) {
-    const long long heads = static_cast<long long>(seqs_per_launch(d)) * d->H, sms = sm_count();
-    return last && heads * (d->dv / 16) <= sms ? 16 : d->dv == 128 && heads * (d->dv / 32) > sms ? 128 : 32;
-}
-
-// The chunks come in launches of the two kernels, so that the first one's work for the next chunks runs beside the walk,
-// on SMs that the walk leaves free: beside c chunks of it there is time for r c.  The first launch's own work runs alone (5.3 us a
-// chunk and SM), and each launch costs some 12 us (by heads 20: more state comes in and goes out); their number and the
-// first one's size follow from that.  8192 tokens of 16 heads: 224 us in three launches, 252 in one, 250 in six; 8 prompts of 16
-// heads, whose walk leaves few SMs: 218 in one, 225 in two.
-struct Segments {
-    int first, most, n;
-    double r;
-    int next(int i, int size, int rest) const {     // of launch i, after one of `size`
-        double c = i == 0 ? first : size * r;
-        if (i == n - 1 || c >= rest) c = rest;
-        return c < 1 ? 1 : c > most ? most : static_cast<int>(c);
-    }
-};
-Segments segments(const gdn_advance_dims *d) {
-    const int all = all_chunks(d), seqs = seqs_per_launch(d), cols = walk_columns(d, false);
-    const double sms = sm_count() < 1 ? 1 : sm_count(), units = static_cast<double>(seqs) * d->H, ctas = units * (d->dv / cols);
-    const double prep = 16.0 / 3 * units / sms, walk = cols == 128 ? 3.4 : 1.6, free = ctas < sms ? 1 - ctas / sms : 0;   // us a chunk
-    const int64_t most = kBudget / 2 / (unit_bytes(d) * d->H * seqs);
-    Segments s{all, static_cast<int>(most < 1 ? 1 : most < all ? most : all), 1, walk * free / prep};
-    double best = 1e30, sum = 0, pow = 1;
-    for (int n = 1; n <= 6; ++n, pow *= s.r) {
-        sum += pow;
-        const double cost = prep * all / sum + (cols == 128 ? 20.0 : 12.0) * n;
-        if (cost < best) {
-            best = cost;
-            s.n = n;
-            s.first = static_cast<int>(all / sum + 0.999);
-        }
-    }
-    return s;
-}
-// Two workspaces take turns, the first of as many chunks as its largest launch has; both together have no more than all chunks, nor
-// than twice the most of a launch.  (Where sequences come in several groups the turns go on, so each has room for any launch.)
-int first_room(const gdn_advance_dims *d) {
-    const Segments g = segments(d);
-    const bool groups = seqs_per_launch(d) < d->B;
-    int room = 0, size = 0;
-    for (int i = 0, rest = all_chunks(d); rest > 0; ++i, rest -= size) {
-        size = g.next(i, size, rest);
-        if ((groups || i % 2 == 0) && size > room) room = size;
-    }
-    return room;
-}
-int64_t room(const gdn_advance_dims *d) {           // of both; does not fall where T grows
-    const int64_t all = all_chunks(d), most = segments(d).most, both = 2 * (seqs_per_launch(d) < d->B ? (all < most ? all : most) : most);
-    return seqs_per_launch(d) < d->B || both < all ? both : all;
-}
+AdvancePlan plan_of(const gdn_advance_dims *d) { return advance_plan(d->B, d->T, d->H, d->dv, unit_bytes(d), sm_count()); }
 
 // Keys, queries or values as [B T][heads][dim]; boxes of `cols` columns of one head, 64 tokens.
 bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int heads, int dim, int64_t stride, int cols, bool swizzle) {
@@ -1101,7 +1040,8 @@ bool token_map(CUtensorMap *m, const void *base, const gdn_advance_dims *d, int 
 template <int DK>
 int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
     CUtensorMap mk, mq, mv[2];
-    const int columns[2] = {walk_columns(d, false), walk_columns(d, true)};
+    const AdvancePlan p = plan_of(d);
+    const int columns[2] = {p.walk_columns(false), p.walk_columns(true)};
     if (!token_map(&mk, a.k, d, d->Hk, d->dk, d->k_stride, 64, true) || !token_map(&mq, a.q, d, d->Hk, d->dk, d->q_stride, 64, true) ||
         !token_map(&mv[0], a.v, d, d->H, d->dv, d->v_stride, columns[0], false) ||
         !token_map(&mv[1], a.v, d, d->H, d->dv, d->v_stride, columns[1], false))
@@ -1115,17 +1055,15 @@ int launch(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         return e != cudaSuccess ? e : launch_pdl(kern, dim3(d->dv / cols, d->H, nb), dim3(threads), bytes, s, mk, mq, m, ta);
     };
-    const int all = all_chunks(d), seqs = seqs_per_launch(d);
-    const Segments g = segments(d);
-    const int64_t second = unit_bytes(d) * d->H * seqs * first_room(d);
+    const int64_t second = p.unit * d->H * p.seqs * p.first_room();
     TcAdvance ta{a, 0, 0, 0, d->dv, 0};
-    for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += seqs) {
-        const int nb = d->B - ta.b0 < seqs ? d->B - ta.b0 : seqs;
+    for (ta.b0 = 0; ta.b0 < d->B; ta.b0 += p.seqs) {
+        const int nb = d->B - ta.b0 < p.seqs ? d->B - ta.b0 : p.seqs;
         ta.chunks = 0;
-        for (int i = 0, c0 = 0; c0 < all; ++i, c0 += ta.chunks) {
+        for (int i = 0, c0 = 0; c0 < p.all; ++i, c0 += ta.chunks) {
             ta.c0 = c0;
-            ta.chunks = g.next(i, ta.chunks, all - c0);
-            const bool last = c0 + ta.chunks == all && ta.b0 + nb == d->B;
+            ta.chunks = p.next(i, ta.chunks, p.all - c0);
+            const bool last = c0 + ta.chunks == p.all && ta.b0 + nb == d->B;
             cudaError_t e = launch_pdl(advance_prep_kernel<DK>, dim3(d->H, ta.chunks, nb), dim3(kPrepThreads), PrepPlan<DK>::BYTES, s, ta);
             if (e == cudaSuccess) e = walk(columns[last], nb, mv[last], ta);
             if (e != cudaSuccess) return GDN_ERR_LAUNCH;
@@ -1148,7 +1086,7 @@ bool advance_tc_shape(const gdn_advance_dims *d) {
 }
 
 int64_t advance_tc_workspace(const gdn_advance_dims *d) {
-    return unit_bytes(d) * d->H * seqs_per_launch(d) * room(d);
+    return plan_of(d).workspace();
 }
 
 int advance_tc(const gdn_advance_dims *d, const AdvanceArgs &a, cudaStream_t s) {
