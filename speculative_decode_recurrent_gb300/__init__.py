@@ -753,9 +753,10 @@ class AttnLayer:
     """One attention layer over a PagedCache: the staging of a draft block and its verify.
 
     ``rope``, ``q_weight``, ``k_weight`` (fp32 [d]) and ``cos_sin`` (fp32 [max_pos, rot]) serve
-    ``stage`` alone.  state_idx (int32 [B]) maps rows to slots; None is the identity.  The
-    workspace is allocated here unless one is passed (layers that run one after the other may
-    share one: ``other.workspace``); ``status`` is the cache's.
+    ``stage`` alone.  state_idx (int32 [B]) maps rows to slots; None is the identity.  Unless a
+    workspace is passed (layers that run one after the other may share one: ``other.workspace``), a verify's
+    is allocated here, that of a chunk of more than 64 tokens with the first ``chunk`` or look at
+    ``workspace``: a layer that only stages needs none.  ``status`` is the cache's.
     """
 
     def __init__(self, dims: AttnDims, cache: PagedCache, layer: int, rope: RopeDims | None = None,
@@ -769,17 +770,18 @@ class AttnLayer:
         self._tok, self._row = (dims.B, dims.T), (dims.B, dims.T, dims.Hq)
         self._vec, self._kv = self._row + (c.d,), self._tok + (c.Hkv, c.d)
         dev = cache.status.device
-        # (a chunk of up to 64 tokens is a verify, and needs its workspace; stage takes more rows than a chunk may have)
-        need = cache._lib.gdn_attn_chunk_workspace(cache._c, self._ref) if dims.B * dims.T <= 1 << 28 else 0
-        _check("gdn_attn_chunk_workspace", min(need, 0))
+        need, later = 0, dims.T > 64
+        if not later:
+            need = cache._lib.gdn_attn_workspace(cache._c, self._ref)
+            _check("gdn_attn_workspace", min(need, 0))
+        self._chunk_need = None if later else need               # (a chunk of up to 64 tokens is a verify)
+        self._index = at = cache._index
+        self._to_allocate = workspace is None and later
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        # (a layer of more tokens than a verify takes may be there for stage alone: chunk refuses what is too small)
-        self._chunk_need, need = need, need if dims.T <= 64 else 0
-        self.workspace, self.state_idx = workspace, state_idx
-        self._keep = (q_weight, k_weight, cos_sin, state_idx, workspace)     # the calls use their addresses
-        self._index = at = cache._index
-        self._ws, self._ws_bytes = _in(workspace, torch.uint8, need, "workspace", at) or None, workspace.numel()
+        self.state_idx = state_idx
+        self._keep = (q_weight, k_weight, cos_sin, state_idx)    # the calls use their addresses
+        self._take(workspace, need)
         self._idx = None if state_idx is None else _in(state_idx, _I32, dims.B, "state_idx", at)
         if rope is not None:
             self._w = (_in(q_weight, _F32, c.d, "q_weight", at), _in(k_weight, _F32, c.d, "k_weight", at),
@@ -790,6 +792,34 @@ class AttnLayer:
     def d(self):
         """A copy of the layer's dims."""
         return AttnDims.from_buffer_copy(self._d)
+
+    def _take(self, workspace, need):
+        self._ws, self._ws_bytes = _in(workspace, torch.uint8, need, "workspace", self._index) or None, workspace.numel()
+        self._workspace = self._kept_workspace = workspace       # (the second holds on to it, whatever becomes of the first)
+
+    def _chunk_workspace(self, stream=None):
+        """Bytes that a chunk needs; allocates them, once, for a layer that was given no workspace."""
+        need = self._chunk_need
+        if need is None:
+            need = self._lib.gdn_attn_chunk_workspace(self.cache._c, self._ref)
+            _check("gdn_attn_chunk", min(need, 0))
+            self._chunk_need = need
+        if self._to_allocate:
+            with torch.cuda.stream(stream):
+                self._take(torch.empty(need, dtype=torch.uint8, device=self.status.device), need)
+            self._to_allocate = False
+        return need
+
+    @property
+    def workspace(self):
+        """The layer's workspace; that of a chunk is allocated when it is first needed."""
+        if self._to_allocate:
+            self._chunk_workspace()
+        return self._workspace
+
+    @workspace.setter
+    def workspace(self, value):
+        self._workspace = value
 
     def _block(self, t, shape, name):
         """Address and token stride of q, k or v: [B, T, heads, d], dense within a token, the
@@ -864,8 +894,10 @@ class AttnLayer:
         over the committed tokens and the chunk's own into ``out`` (and ``lse`` fp32 [B, T, Hq]).  chunk_len
         int32 [B]: tokens in use (None: T, any number that the layer was made for).  seq_len does not move:
         accept the chunk, or write the new lengths, afterwards."""
-        if self._ws_bytes < self._chunk_need:
-            raise ValueError(f"chunk: needs a workspace of at least {self._chunk_need} bytes, got {self._ws_bytes}")
+        if self._chunk_need is None or self._to_allocate or self._ws_bytes < self._chunk_need:
+            need = self._chunk_workspace(stream)
+            if self._ws_bytes < need:
+                raise ValueError(f"chunk: needs a workspace of at least {need} bytes, got {self._ws_bytes}")
         t, e, cache, at = self._dtype, self._elems, self.cache, self._index
         rc = self._lib.gdn_attn_chunk(
             cache._c, self.layer, self._ref, self._idx,
