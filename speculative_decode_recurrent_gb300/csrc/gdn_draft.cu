@@ -16,7 +16,7 @@
 // What bounds it: a few rows of V numbers per sequence, and a chain of dependent steps (tokens, their probabilities,
 // the walk, the pass, its sum across the cluster, the search).  A cluster of eight CTAs takes a sequence, each a
 // stretch of the vocabulary, in segments of 1024 terms per warp (256 or 512 where those would leave warps without one); two
-// CTAs share an SM.  On the device: a chain of 8 over 32768 probabilities 5.6 us, 32 chains of 16 over 131072 12 (half of the copy
+// CTAs share an SM.  On the device: a chain of 8 over 32768 probabilities 5.8 us, 32 chains of 16 over 131072 12.3 (half of the copy
 // bandwidth for the rows that have to be read).
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -85,16 +85,19 @@ __device__ __forceinline__ Two scan(Two x, int lane) {
     return x;
 }
 
-// max(p - c q, 0) in two words, for two tokens (two operations an instruction).  The sign is d's: where p and c q agree in
-// 24 bits the rest counts as 0.  A negative p or NaN gives 0, an infinity leaves NaN (the row has no sound sum).
+// max(p - c q, 0) in two words, for two tokens (two operations an instruction).  The sign is that of both words: where p and c q agree in
+// 24 bits, h is 0 or a last place or two and l decides (so l may be as large as h, and h 0 with l above it).  A negative p or
+// NaN gives 0, an infinity leaves NaN (the row has no sound sum).
 __device__ __forceinline__ void rest(float2 p, float2 q, Two c, float2 &h, float2 &l) {
     const float2 minus = make_float2(-1.f, -1.f), t = mul2(make_float2(-c.h, -c.h), q);      // - c.h q
+    p = make_float2(fmaxf(p.x, 0.f), fmaxf(p.y, 0.f));
     float2 e = fma2(make_float2(c.h, c.h), q, t);
     e = fma2(make_float2(c.l, c.l), q, e);
     const float2 d = add2(p, t), bp = fma2(p, minus, d);
     const float2 err = fma2(e, minus, add2(fma2(fma2(bp, minus, d), minus, p), fma2(bp, minus, t)));
-    h = make_float2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f));
-    l = make_float2(d.x > 0.f ? err.x : 0.f, d.y > 0.f ? err.y : 0.f);
+    const float2 s = add2(d, err);                  // (NaN of an infinity passes)
+    h = make_float2(s.x <= 0.f ? 0.f : d.x, s.y <= 0.f ? 0.f : d.y);
+    l = make_float2(s.x <= 0.f ? 0.f : err.x, s.y <= 0.f ? 0.f : err.y);
 }
 // Two sums side by side, without bringing l back below h's last place.
 struct Two2 {
@@ -443,8 +446,8 @@ __device__ __forceinline__ void accept_body(const DraftArgs &a)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         x4 = x4 + Two{h[j], l[j]};
-                        if (h[j] > 0.f) end = v + j;
-                        if (hit < 0 && row >= 0 && h[j] > 0.f && goal < x4) hit = v + j;
+                        if (h[j] + l[j] > 0.f) end = v + j;
+                        if (hit < 0 && row >= 0 && h[j] + l[j] > 0.f && goal < x4) hit = v + j;
                     }
                     const unsigned m = __ballot_sync(0xffffffffu, hit >= 0), e = __ballot_sync(0xffffffffu, end >= 0);
                     const int at = m ? __shfl_sync(0xffffffffu, hit, __ffs(m) - 1) : __shfl_sync(0xffffffffu, end, e ? 31 - __clz(e) : 0);
