@@ -160,7 +160,8 @@ int64_t gdn_attn_workspace(const gdn_page_cache *cache, const gdn_attn_dims *dim
  * head h, over the tokens j <= seq_len + t, as in gdn_attn_verify:
  *     s_j = scale q_t . k_j,   out = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}.
  * Rows t >= n get out 0 and lse -inf.  Keys and values of tokens past the chunk's end may hold anything (NaN and
- * infinity included); an infinite or NaN value of a token within it may leave NaN in its column of rows before it.
+ * infinity included); an infinite or NaN value of a token leaves infinity or NaN in its column of the rows that see it, and
+ * nothing in those before it.
  * T is 1..2^20, B * T <= 2^28; chunks of up to 64 tokens are a chain to gdn_attn_verify and go there.
  *   q, out dtype [B, T, Hq, d] (16-byte aligned);  lse fp32 [B, T, Hq] or NULL;  workspace:
  *   workspace_bytes >= gdn_attn_chunk_workspace() bytes, 16-byte aligned, no initial content; calls that

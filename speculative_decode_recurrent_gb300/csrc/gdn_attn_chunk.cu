@@ -83,8 +83,10 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
         lim[i] = r < live ? sq.len + t0 + r / G + 1 : 0;
     }
     const int32_t *tab = a.s.table + static_cast<size_t>(sq.slot) * a.s.max_pages;
+    const int unseen = sq.len + t0 + 1;                               // tokens from here on are not seen by every row
     for (int kt = first; kt < end; ++kt) {
         __syncthreads();                                              // the tile before has been read
+        bool odd = false;                                             // an infinite or NaN value of such a token
         for (int e = tid; e < kKT * (D / 4); e += kThreads) {
             const int r = e / (D / 4), c = e % (D / 4) * 4, j = kt * kKT + r;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
@@ -96,12 +98,13 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
                     const size_t off = (((static_cast<size_t>(id) * Hkv + h) << a.s.page_shift) + (j & ((1 << a.s.page_shift) - 1))) * D + c;
                     x = load4(static_cast<const float *>(a.k) + off);
                     y = load4(static_cast<const float *>(a.v) + off);
+                    odd |= j >= unseen && !(fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY);
                 }
             }
             *reinterpret_cast<float4 *>(sK + r * P::LD + c) = x;
             *reinterpret_cast<float4 *>(sV + r * D + c) = y;
         }
-        __syncthreads();
+        odd = __syncthreads_or(odd);
         float2 s[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -149,21 +152,39 @@ __global__ void __launch_bounds__(kThreads) chunk_core_kernel(const ChunkArgs a)
             for (int c = 0; c < D / 32; ++c) o[i][c] = mul2(o[i][c], f2);
         }
         __syncwarp();                                                 // a row's weights are its half-warp's own
-        for (int j = 0; j < kKT; j += 4) {
-            float4 p[4];
+        if (!odd) {
+            for (int j = 0; j < kKT; j += 4) {
+                float4 p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + i) * P::LP + j);
+                for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + i) * P::LP + j);
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
+                for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const float4 y = *reinterpret_cast<const float4 *>(sV + (j + jj) * D + tx * 4 + 64 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
+                            const float2 w2 = make_float2(w, w);
+                            o[i][2 * c] = fma2(w2, make_float2(y.x, y.y), o[i][2 * c]);
+                            o[i][2 * c + 1] = fma2(w2, make_float2(y.z, y.w), o[i][2 * c + 1]);
+                        }
+                    }
+            }
+        } else {                                                      // a weight of 0 must not meet an infinity or NaN
+#pragma unroll 1
+            for (int j = 0; j < kKT; ++j)
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    const float4 y = *reinterpret_cast<const float4 *>(sV + (j + jj) * D + tx * 4 + 64 * c);
+                    const float4 y = *reinterpret_cast<const float4 *>(sV + j * D + tx * 4 + 64 * c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
+                        const float w = sP[(ty * 4 + i) * P::LP + j];
                         const float2 w2 = make_float2(w, w);
-                        o[i][2 * c] = fma2(w2, make_float2(y.x, y.y), o[i][2 * c]);
-                        o[i][2 * c + 1] = fma2(w2, make_float2(y.z, y.w), o[i][2 * c + 1]);
+                        if (kt * kKT + j < lim[i]) {
+                            o[i][2 * c] = fma2(w2, make_float2(y.x, y.y), o[i][2 * c]);
+                            o[i][2 * c + 1] = fma2(w2, make_float2(y.z, y.w), o[i][2 * c + 1]);
+                        }
                     }
                 }
         }

@@ -48,7 +48,7 @@ template <int D> struct Plan {
     static constexpr int QA = D / 64, VA = DV / 64; // 64-column atoms of 128-byte rows
     static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = KT * D * 2, V_BYTES = KT * DV * 2;
     static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NK * K_BYTES, OFF_XCH = OFF_V + NV * V_BYTES;
-    static constexpr int OFF_BAR = OFF_XCH + 512 * 4, BYTES = OFF_BAR + 384 + 160;
+    static constexpr int OFF_BAR = OFF_XCH + 512 * 4, BYTES = OFF_BAR + 384 + 176;
     static constexpr int MMA_WARP = 0, LOAD_WARP = 2, ROW_WARP = 4, WARPS = 20, THREADS = WARPS * 32;
     static constexpr int OFF_SLOT = OFF_BAR + 352, OFF_NEXT = OFF_SLOT + 16, OFF_UNIT = OFF_BAR + 384;      // TMEM address and abort; the next CTA's index; units
     static constexpr int COL_S = 0, COL_O = 2 * NB * KT;       // TMEM: the score buffers of each row tile, then their sums
@@ -66,6 +66,13 @@ __device__ __forceinline__ void store_32(void *dst, const uint32_t (&x)[8], bool
     }
 }
 
+// Bit 15 or 31 where a half of x is an infinite or NaN bf16 number (all bits of its exponent); those halves as a mask.
+__device__ __forceinline__ uint32_t odd_bits(uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; }
+__device__ __forceinline__ uint32_t odd_halves(uint32_t x) {
+    const uint32_t e = x & 0x7f807f80u;
+    return ((e & 0xffffu) == 0x7f80u ? 0xffffu : 0u) | (e >= 0x7f800000u ? 0xffff0000u : 0u);
+}
+
 template <bool X> struct Flag {
     static constexpr bool value = X;
 };
@@ -73,12 +80,43 @@ template <bool X> struct Flag {
 struct Unit {
     int h, b, half, part, rt0, slot, len, n;
     int live[2], tiles[2];                          // of each row tile: rows in use; tiles of keys that this part has of it
+    int keys[2];                                    // and its last row's keys from this part's first on
     int first, count;                               // this part's tiles of keys
     int before[2], all;                             // tiles of the CTA's units before: each group's, both groups' (so, of values)
     int sums[2];                                    // of those units, how many had tiles of each group
     int stop;
 };
-static_assert(sizeof(Unit) == 80, "unit");
+static_assert(sizeof(Unit) == 88, "unit");
+
+// NaN in the sums (N columns from t_o and column c0 on) of a row where it sees an infinite or NaN value of the tokens [j0, j1), which its
+// products have met as 0.  A rare path: the values are read from memory again.
+template <int N>
+__device__ __noinline__ void spoil_sums(const ChunkArgs &a, int slot, int h, int c0, int d, int j0, int j1, uint32_t t_o) {
+    unsigned long long odd = 0ull;
+    const int32_t *tab = a.s.table + static_cast<size_t>(slot) * a.s.max_pages;
+    for (int j = j0; j < j1; ++j) {
+        const int id = __ldg(tab + (j >> a.s.page_shift));
+        if (id < 0 || id >= a.s.n_page) continue;
+        const size_t row = ((static_cast<size_t>(id) * a.s.Hkv + h) << a.s.page_shift) + (j & ((1 << a.s.page_shift) - 1));
+        const uint32_t *v = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.v) + row * d + c0);
+        for (int c = 0; c < N / 2; ++c) {
+            const uint32_t m = odd_halves(__ldg(v + c));
+            odd |= static_cast<unsigned long long>((m & 1u) | (m >> 30 & 2u)) << 2 * c;
+        }
+    }
+    for (int c = 0; c < N; c += 8) {
+        const uint32_t m = static_cast<uint32_t>(odd >> c) & 0xffu;
+        if (!__any_sync(0xffffffffu, m != 0)) continue;
+        uint32_t o[8];
+        tmem_load8(t_o + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (m >> k & 1u) o[k] = 0x7fffffffu;
+        tmem_store8(t_o + c, o);
+    }
+    tmem_wait_st();
+}
 
 // The index of a CTA of the grid that has not begun, which this one takes over: asked for, and read.
 __device__ __forceinline__ void ask_next(uint32_t at, uint64_t *bar) {
@@ -110,6 +148,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
              *u_full = drain + 2, *u_empty = u_full + 2, *asked_next = u_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + P::OFF_SLOT);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *odd_values = abort + 1;           // infinities or NaN have been zeroed among the values
     Unit *units = reinterpret_cast<Unit *>(smem + P::OFF_UNIT);
     static_assert((2 * P::NK + 2 * P::NV + 25) * 8 <= 352, "barriers");
     if (saddr(smem) & 1023u) {
@@ -142,6 +181,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
         mbar_init(asked_next, 1);
         *abort = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
+        *odd_values = 0;
         fence_mbar_init();
     }
     if (warp == P::MMA_WARP) tmem_alloc(tmem_slot, 512);
@@ -196,12 +236,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int g = 0; g < 2; ++g) {
                 const int tg = (x.rt0 + g) * a.tpt, n = min(a.tpt, sq.n - tg);
                 x.live[g] = max(n, 0) * G;
-                tiles[g] = n > 0 ? (sq.len + tg + n + KT - 1) / KT : 0;
+                x.keys[g] = sq.len + tg + n;
+                tiles[g] = n > 0 ? (x.keys[g] + KT - 1) / KT : 0;
             }
             part_range(max(tiles[0], tiles[1]), x.part, a.splits, x.first, end);
             x.count = end - x.first;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) x.tiles[g] = max(0, min(end, tiles[g]) - x.first);
+            for (int g = 0; g < 2; ++g) {
+                x.tiles[g] = max(0, min(end, tiles[g]) - x.first);
+                x.keys[g] -= x.first * KT;
+            }
             x.stop = 0;
             return true;
         };
@@ -338,7 +382,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         bool ok = true, ended = false;
         for (int u = 0; ok && next_unit(u); ++u) {
             const int stop = __shfl_sync(0xffffffffu, units[u & 1].stop, 0), count = __shfl_sync(0xffffffffu, units[u & 1].count, 0),
-                      n = __shfl_sync(0xffffffffu, units[u & 1].tiles[g], 0);
+                      n = __shfl_sync(0xffffffffu, units[u & 1].tiles[g], 0), keys = __shfl_sync(0xffffffffu, units[u & 1].keys[g], 0);
             if (stop) {
                 ended = true;
                 break;
@@ -373,9 +417,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (!ok) break;
                 tc_fence_after();
                 if (i < n) {
+                    const uint32_t t_p = t_s + at % P::NB * KT;       // O += P_i V_i
+                    if (P::NB > 1 || keys >= (i + 1) * KT) {
 #pragma unroll
-                    for (int k = 0; k < KT / 16; ++k)                 // O += P_i V_i
-                        mma_bf16_ts_on(one, t_o, t_s + at % P::NB * KT + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+                        for (int k = 0; k < KT / 16; ++k) mma_bf16_ts_on(one, t_o, t_p + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+                    } else {                        // no further than the group's last row sees
+                        const int some = __shfl_sync(0xffffffffu, (keys - i * KT + 15) / 16, 0);
+#pragma unroll 1
+                        for (int k = 0; k < some; ++k) mma_bf16_ts_on(one, t_o, t_p + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+                    }
                 }
                 if (i < n) {
                     mma_commit_on(one, &o_done[g]);
@@ -417,24 +467,52 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (w.stop) break;
         // Tiles of this group since the beginning, of which those below `plain` are seen by every row, all of them in use.
         const int end = w.before[g] + w.tiles[g];
-        const int plain = w.live[g] == kRows ? (w.len + (w.rt0 + g) * a.tpt + 1) / KT - w.first + w.before[g] : 0;
+        const int whole = (w.len + (w.rt0 + g) * a.tpt + 1) / KT - w.first + w.before[g];       // (tiles of tokens that they all see)
+        const int plain = w.live[g] == kRows ? whole : 0;
         float m = -INFINITY, l = 0.f;               // m: the same in both threads of a row; l: of this one's keys
         bool ok = true;
+        // (before the scores, while the warps would wait for them; for tiles in two buffers, whose scores are there, behind them)
+        constexpr bool LATE = P::NB > 1;
+        auto clean = [&](auto edge, int at) {
+            if (!edge.value || at < whole) return;
+            // A weight of 0 must not meet an infinity or NaN.  The product of this group takes the tile's keys up to its last row's, in
+            // sixteens; of those, values past the last token, which hold anything, become 0, and so do infinite and NaN ones of tokens that
+            // some of its rows do not see.  The rows that do, of either group, get NaN at the unit's end: the second group's product of a tile
+            // comes after the first one's, so it meets the same zeros each time.  (Both: 1 % of the prompts' time, 4 % of 256 tokens'.)
+            const int i = at - w.before[g], j0 = (w.first + i) * KT, tile = w.all + i, vst = tile % P::NV;
+            const int lo = max(0, w.len + (w.rt0 + g) * a.tpt + 1 - j0), vecs = ((LATE ? KT : min(KT, (w.keys[g] - i * KT + 15) & ~15)) - lo) * (DV / 8);
+            if (vecs > 0) {
+                const int used = w.len + w.n - j0;
+                ok = wait(&v_full[vst], (tile / P::NV) & 1) && ok;
+                for (int e0 = rt & 255; e0 < vecs; e0 += 512) {
+                    uint4 y[2], *at_v[2];
+                    bool past = false;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int e = min(e0 + 256 * k, vecs - 1), row = lo + e / (DV / 8), c = e % (DV / 8);
+                        at_v[k] = reinterpret_cast<uint4 *>(smem + P::OFF_V + vst * P::V_BYTES + (c >> 3) * (KT * 128) + sw128(row, c & 7));
+                        y[k] = *at_v[k];
+                        if (row >= used) {
+                            past = true;
+                            y[k] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    const uint32_t odd = (odd_bits(y[0].x) | odd_bits(y[0].y) | odd_bits(y[0].z) | odd_bits(y[0].w) | odd_bits(y[1].x) |
+                                          odd_bits(y[1].y) | odd_bits(y[1].z) | odd_bits(y[1].w)) & 0x80008000u;
+                    if (past || odd) {
+                        if (odd) *odd_values = 1;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            *at_v[k] = make_uint4(y[k].x & ~odd_halves(y[k].x), y[k].y & ~odd_halves(y[k].y), y[k].z & ~odd_halves(y[k].z),
+                                                  y[k].w & ~odd_halves(y[k].w));
+                        fence_proxy_async();
+                    }
+                }
+            }
+        };
         // (in two copies: the tiles that every row sees have nothing of the others' masks)
         auto tile_of = [&](auto edge, int at) {
-            if (edge.value && (w.first + at - w.before[g] + 1) * KT > w.len + w.n) {
-                // values past the last token hold anything: zeros in their place (by both groups, each before its weights
-                // go to their product)
-                const int total = w.len + w.n, j0 = (w.first + at - w.before[g]) * KT, tile = w.all + at - w.before[g], vst = tile % P::NV;
-                ok = wait(&v_full[vst], (tile / P::NV) & 1) && ok;
-                const int from = max(0, total - j0);
-                for (int e = (rt & 255) + from * (DV / 8); e < KT * (DV / 8); e += 256) {
-                    const int row = e / (DV / 8), c = e % (DV / 8);
-                    *reinterpret_cast<uint4 *>(smem + P::OFF_V + vst * P::V_BYTES + (c >> 3) * (KT * 128) + sw128(row, c & 7)) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async();
-            }
+            if constexpr (!LATE) clean(edge, at);
             const uint32_t t_s = t_s0 + at % P::NB * KT;
             ok = wait(&s_full[2 * g + at % P::NB], (at / P::NB) & 1) && ok;
             tc_fence_after();
@@ -500,6 +578,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 tmem_st16(t_s + kh * (KH / 2) + 16 * c, p);
             }
             l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+            if constexpr (LATE) clean(edge, at);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -513,6 +592,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (n > 0) {                                // (by a barrier of its own: o_done may be a phase or two behind)
             ok = wait(&o_last[g], w.sums[g] & 1) && ok;
             tc_fence_after();
+            if (__any_sync(0xffffffffu, *odd_values) && ok)
+                spoil_sums<DH>(a, w.slot, w.h, w.half * DV + kh * DH, D, max(w.first * KT, w.len + w.rt0 * a.tpt + 1),
+                               r < w.live[g] ? min((w.first + n) * KT, w.len + (w.rt0 + g) * a.tpt + r / G + 1) : 0, t_o);
         }
         xch[rt] = l;
         bar_sync(pair_id, 64);
