@@ -211,8 +211,8 @@ int gdn_replay_accept_fold(const gdn_replay_dims *dims, int32_t *buf_len,
  *   out fp32 [B, T, H, dv];  chunk_len int32 [B], NULL: T;  fresh int32 [B], NULL: none;
  *   workspace: workspace_bytes >= gdn_replay_advance_workspace() bytes, 16-byte aligned, no initial
  *   content; calls that overlap on the GPU need one each.
- * Rows past chunk_len may hold anything. An infinite or NaN input of a token in use goes on into its head's outputs and
- * state, and may leave NaN in up to 63 rows of the head's outputs before it.
+ * Rows past chunk_len may hold anything. An infinite or NaN input of a token in use goes on into its head's outputs (a value's: into its
+ * column) from that token on and into the state, and nowhere else.
  * GDN_STATUS_BAD_SLOT; _BAD_LEN (chunk_len outside [0, T], or a buffer that is not empty): the sequence is
  * skipped, out and state unwritten.  _TIMEOUT, _DRAIN: no output or state of the call may be trusted.
  */

@@ -67,6 +67,8 @@ __device__ __forceinline__ void split_pair(float2 x, uint32_t (&t)[3]) {
     const __nv_bfloat162 l = __floats2bfloat162_rn(r.x, r.y);
     t[2] = *reinterpret_cast<const uint32_t *>(&l);
 }
+// Bit 15 or 31 where a half of x is an infinite or NaN bf16 number.
+__device__ __forceinline__ uint32_t odd_bits(uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; }
 // Eight of them as one 16-byte chunk of each term.
 __device__ __forceinline__ void split8(const float *y, uint4 (&t)[3]) {
     uint32_t p[4][3];
@@ -77,6 +79,7 @@ __device__ __forceinline__ void split8(const float *y, uint4 (&t)[3]) {
 }
 // The products of two numbers of three terms: (term of A, term of B), the largest first.
 __device__ constexpr int kTermA[6] = {0, 0, 1, 0, 1, 2}, kTermB[6] = {0, 1, 0, 2, 1, 0};
+constexpr int kNever = 0x7fffffff;
 
 // ------------------------------------------------------------- E and M P of every chunk
 constexpr int kPrepThreads = 256;
@@ -286,89 +289,118 @@ __global__ void __launch_bounds__(kPrepThreads, 4) advance_prep_kernel(const TcA
     tc_fence_after();
     ok = __all_sync(0xffffffffu, ok);
     int issued = 0;                                 // the last barrier that MMAs may have been committed to
-    // ---- A in fp32 (rows of K), M's terms (rows of Q)
     const int t = ((warp & 1) << 5) + lane;
     const bool keys = (warp & 3) < 2;
     uint4 m2[4];                                    // M's third terms
-    if (ok) {
-        const float gh = sGh[t], gl = sGl[t], f = keys ? sBeta[t] : a.scale;
+    const int row = tid & (kC - 1), s0 = (tid >> 6) * 16;
+    float y[16];
+    // From the first token on whose key, decay or beta is not finite, all outputs and the state are NaN: the walk learns of it by a gamma of
+    // NaN.  The rows before it must not meet it (they have zeros for it, which make NaN of it).  Such a token shows in P; then A, M
+    // and P are made again as if it and those behind it had keys and betas of 0.
+    int sound = kC;                                 // tokens before it
+    for (bool again = false;; again = true) {
+        // ---- A in fp32 (rows of K), M's terms (rows of Q)
+        if (ok) {
+            const float gh = sGh[t], gl = sGl[t], f = keys ? sBeta[t] : a.scale;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const int j0 = 32 * half + 16 * v;
-            uint32_t r[16];
-            tmem_load16(tmem + lanes + j0, r);
-            tmem_wait_ld();
-            float y[16];
-            const int seen = t - j0 + (keys ? 0 : 1);             // columns j < seen count
+            for (int v = 0; v < 2; ++v) {
+                const int j0 = 32 * half + 16 * v;
+                uint32_t r[16];
+                tmem_load16(tmem + lanes + j0, r);
+                tmem_wait_ld();
+                float y[16];
+                const int seen = t < sound ? t - j0 + (keys ? 0 : 1) : 0;               // columns j < seen count
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-                const float4 h4 = *reinterpret_cast<const float4 *>(sGh + j0 + j), l4 = *reinterpret_cast<const float4 *>(sGl + j0 + j);
-                y[j] = ex2(((gh - h4.x) + (gl - l4.x)) * kLog2e);
-                y[j + 1] = ex2(((gh - h4.y) + (gl - l4.y)) * kLog2e);
-                y[j + 2] = ex2(((gh - h4.z) + (gl - l4.z)) * kLog2e);
-                y[j + 3] = ex2(((gh - h4.w) + (gl - l4.w)) * kLog2e);
-            }
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 h4 = *reinterpret_cast<const float4 *>(sGh + j0 + j), l4 = *reinterpret_cast<const float4 *>(sGl + j0 + j);
+                    y[j] = ex2(((gh - h4.x) + (gl - l4.x)) * kLog2e);
+                    y[j + 1] = ex2(((gh - h4.y) + (gl - l4.y)) * kLog2e);
+                    y[j + 2] = ex2(((gh - h4.z) + (gl - l4.z)) * kLog2e);
+                    y[j + 3] = ex2(((gh - h4.w) + (gl - l4.w)) * kLog2e);
+                }
 #pragma unroll
-            for (int j = 0; j < 16; ++j)                          // (as bits: a select here became 32 branches)
-                y[j] = __uint_as_float(__float_as_uint(__uint_as_float(r[j]) * y[j] * f) & (j < seen ? 0xffffffffu : 0u));
-            if (keys) {
+                for (int j = 0; j < 16; ++j)                          // (as bits: a select here became 32 branches)
+                    y[j] = __uint_as_float(__float_as_uint(__uint_as_float(r[j]) * y[j] * f) & (j < seen ? 0xffffffffu : 0u));
+                if (keys) {
 #pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                    *reinterpret_cast<float4 *>(sT + t * P::LD + j0 + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-            } else {
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4 *>(sT + t * P::LD + j0 + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                } else {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint4 m[3];
-                    split8(y + 8 * c, m);
-                    const uint32_t at = sw128(t, 4 * half + 2 * v + c);
-                    *reinterpret_cast<uint4 *>(smem + P::OFF_M0 + at) = m[0];
-                    *reinterpret_cast<uint4 *>(smem + P::OFF_M1 + at) = m[1];
-                    m2[2 * v + c] = m[2];
+                    for (int c = 0; c < 2; ++c) {
+                        uint4 m[3];
+                        split8(y + 8 * c, m);
+                        const uint32_t at = sw128(t, 4 * half + 2 * v + c);
+                        *reinterpret_cast<uint4 *>(smem + P::OFF_M0 + at) = m[0];
+                        *reinterpret_cast<uint4 *>(smem + P::OFF_M1 + at) = m[1];
+                        m2[2 * v + c] = m[2];
+                    }
                 }
             }
         }
-    }
-    tc_fence_before();
-    __syncthreads();
-    // ---- T = (I + A)^-1: diagonal blocks of 8 by substitution, a thread per column; then blocks of twice the size
-    if (tid < kC) {
-        const int bi = tid >> 3, j = tid & 7;
-        float *Ab = sT + 8 * bi * P::LD + 8 * bi;
-        float x[8];
+        tc_fence_before();
+        __syncthreads();
+        // ---- T = (I + A)^-1: diagonal blocks of 8 by substitution, a thread per column; then blocks of twice the size
+        if (tid < kC) {
+            const int bi = tid >> 3, j = tid & 7;
+            float *Ab = sT + 8 * bi * P::LD + 8 * bi;
+            float x[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const float4 y0 = *reinterpret_cast<const float4 *>(Ab + r * P::LD), y1 = *reinterpret_cast<const float4 *>(Ab + r * P::LD + 4);
-            const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-            float s0 = 0.f, s1 = 0.f;
+            for (int r = 0; r < 8; ++r) {
+                const float4 y0 = *reinterpret_cast<const float4 *>(Ab + r * P::LD), y1 = *reinterpret_cast<const float4 *>(Ab + r * P::LD + 4);
+                const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int k = 0; k < r; ++k) {
-                if (k & 1) s1 = fmaf(y[k], x[k], s1);
-                else s0 = fmaf(y[k], x[k], s0);
+                for (int k = 0; k < r; ++k) {
+                    if (k & 1) s1 = fmaf(y[k], x[k], s1);
+                    else s0 = fmaf(y[k], x[k], s0);
+                }
+                x[r] = r == j ? 1.f : r < j ? 0.f : -(s0 + s1);
             }
-            x[r] = r == j ? 1.f : r < j ? 0.f : -(s0 + s1);
+            __syncwarp();                               // a block's threads are in one warp
+#pragma unroll
+            for (int r = 0; r < 8; ++r) Ab[r * P::LD + j] = x[r];
         }
-        __syncwarp();                               // a block's threads are in one warp
+        __syncthreads();
+        inverse_level<8, P::LD>(sT, tid);
+        inverse_level<16, P::LD>(sT, tid);
+        inverse_level<32, P::LD>(sT, tid);
+        // ---- P = T diag(beta) and F = D P: a row's 16 columns; F's terms over T first, P's after the product with them
 #pragma unroll
-        for (int r = 0; r < 8; ++r) Ab[r * P::LD + j] = x[r];
+        for (int j = 0; j < 16; j += 4) {
+            const float4 x4 = *reinterpret_cast<const float4 *>(sT + row * P::LD + s0 + j), b4 = *reinterpret_cast<const float4 *>(sBeta + s0 + j);
+            y[j] = x4.x * b4.x;
+            y[j + 1] = x4.y * b4.y;
+            y[j + 2] = x4.z * b4.z;
+            y[j + 3] = x4.w * b4.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(__float_as_uint(y[j]) & (s0 + j <= row ? 0xffffffffu : 0u));
+        float2 probe = make_float2(0.f, 0.f);           // (0 times a finite number adds nothing)
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) probe = fma2(make_float2(y[j], y[j + 1]), make_float2(0.f, 0.f), probe);
+        const bool odd = !(probe.x + probe.y == 0.f);
+        if (!__syncthreads_or(odd) || again) break;     // (T has been read)
+        int *first = reinterpret_cast<int *>(tmem_slot + 1);
+        if (tid == 0) *first = kC;
+        __syncthreads();
+        if (tid < kC) {
+            bool bad = !(fabsf(sGh[tid]) < INFINITY && fabsf(sBeta[tid]) < INFINITY);
+            for (int v = 0; v < VR; ++v) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(smem + (v >> 3) * P::ATOM + sw128(tid, v & 7));
+                bad |= ((odd_bits(x.x) | odd_bits(x.y) | odd_bits(x.z) | odd_bits(x.w)) & 0x80008000u) != 0;
+            }
+            if (bad) atomicMin(first, tid);
+        }
+        __syncthreads();
+        sound = *first;
+        if (tid < kC && tid >= sound) {
+            sGam[tid] = __uint_as_float(0x7fffffffu);
+            sBeta[tid] = 0.f;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    inverse_level<8, P::LD>(sT, tid);
-    inverse_level<16, P::LD>(sT, tid);
-    inverse_level<32, P::LD>(sT, tid);
-    // ---- P = T diag(beta) and F = D P: a row's 16 columns; F's terms over T first, P's after the product with them
-    const int row = tid & (kC - 1), s0 = (tid >> 6) * 16;
     const float end = sEnd[row];
-    float y[16];
-#pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-        const float4 x4 = *reinterpret_cast<const float4 *>(sT + row * P::LD + s0 + j), b4 = *reinterpret_cast<const float4 *>(sBeta + s0 + j);
-        y[j] = x4.x * b4.x;
-        y[j + 1] = x4.y * b4.y;
-        y[j + 2] = x4.z * b4.z;
-        y[j + 3] = x4.w * b4.w;
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(__float_as_uint(y[j]) & (s0 + j <= row ? 0xffffffffu : 0u));
     // Their terms: the first two in T's place; the third is returned.
     auto put = [&](float f, uint4 (&third)[2]) {
 #pragma unroll
@@ -396,7 +428,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4) advance_prep_kernel(const TcA
         }
         tc_fence_after();
     };
-    __syncthreads();                                // T has been read
     uint4 third[2];
     put(end, third);
     fence_proxy_async();
@@ -481,7 +512,7 @@ template <int DK, int SL> struct SlicePlan {
     static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4, V_AT = 3 * Unit<DK>::MP_BYTES + 1024, MP = V_AT + (kC * SL * 2 + 1023) / 1024 * 1024;   // M P and gamma, values
     static constexpr int S_ATOM = DK * 128, X_ATOM = kC * 128, ATOMS = SL == 32 ? 2 : 1;      // rows of 64 columns: the third terms of 32 take a second one
     static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + E, OFF_S = OFF_MP + 2 * MP, OFF_X = OFF_S + ATOMS * S_ATOM;
-    static constexpr int OFF_BAR = OFF_X + ATOMS * X_ATOM, BYTES = OFF_BAR + 256;
+    static constexpr int OFF_BAR = OFF_X + ATOMS * X_ATOM, OFF_BAD = OFF_BAR + 256, BYTES = OFF_BAD + SL * 4;      // barriers; the first bad token by column
     static constexpr int ROWS = 256, LOAD_WARP = 8, MMA_WARP = 9, THREADS = 320;
     static constexpr int N = 3 * SL, AT = SL == 32 ? 96 : 64, TMEM_COLS = SL == 32 ? 512 : 256;       // a product's columns, and from one to the next: [K;Q] S^T, E x, M P x
     static_assert(BYTES <= 227 * 1024 && OFF_E >= 8192 && MP % 1024 == 0, "plan");
@@ -556,7 +587,8 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
              *full_e = empty_m + 2, *empty_e = full_e + 1, *d1 = empty_e + 1, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1,
              *x_ready = s_ready + 1, *drain = x_ready + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1), *any_bad = abort + 1;
+    int *bad = reinterpret_cast<int *>(smem + P::OFF_BAD);
     pdl_wait();
     pdl_release();
     const AdvanceSeq sq = advance_seq(a, b);
@@ -571,9 +603,11 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const bool expire = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
         for (uint64_t *bar = full_k; bar <= drain; ++bar) mbar_init(bar, bar == s_ready || bar == x_ready ? P::ROWS / 32 : 1);
         *abort = expire;                            // (a warp arrives once: 256 arrivals at one word take 500 cycles)
+        *any_bad = 0;
         if (expire) atomicOr(a.status, kStatusTimeout);
         fence_mbar_init();
     }
+    if (tid < SL) bad[tid] = kNever;
     if (warp == P::LOAD_WARP) tmem_alloc(tmem_slot, P::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -712,6 +746,21 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     for (int e = 0; e < 8; ++e) y[8 * i + e] = live ? fmaf(f, y[8 * i + e], v[e]) : 0.f;
                 }
                 put_row(sX, P::X_ATOM, t, half, y);
+                // An infinity or NaN enters the products as 0 (a row before it has a 0 for it there); its column is NaN from this token on.
+                float2 probe[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int j = 0; j < C; j += 2) probe[j / 2 & 1] = fma2(make_float2(y[j], y[j + 1]), make_float2(0.f, 0.f), probe[j / 2 & 1]);
+                probe[0] = add2(probe[0], probe[1]);
+                if (!(probe[0].x + probe[0].y == 0.f)) {
+                    *any_bad = 1;
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        if (!(fabsf(y[j]) < INFINITY)) {
+                            y[j] = 0.f;
+                            atomicMin(bad + C * half + j, c * kC + t);
+                        }
+                    put_row(sX, P::X_ATOM, t, half, y);
+                }
                 fence_proxy_async();
             } else {
                 const float f = gam[t] * a.scale;
@@ -724,10 +773,15 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             ok = wait(d2, c & 1);
             if (!ok) break;
             tc_fence_after();
+            const bool spoilt = *any_bad != 0;
             if (has) {
                 get_row(tm + P::AT, y);
 #pragma unroll
                 for (int j = 0; j < C; ++j) S[j] = fmaf(ge, S[j], y[j]);
+                if (spoilt)
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        if (bad[C * half + j] != kNever) S[j] = __uint_as_float(0x7fffffffu);
                 put_row(sS, P::S_ATOM, row, half, S);
                 fence_proxy_async();
             }
@@ -738,6 +792,10 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (!ok) break;
                 tc_fence_after();
                 get_row(tm + 2 * P::AT, y);
+                if (spoilt)
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        if (bad[C * half + j] <= c * kC + t) y[j] = __uint_as_float(0x7fffffffu);
                 if (c * kC + t < n) {
                     float4 *dst = reinterpret_cast<float4 *>(op + static_cast<size_t>(c) * kC * a.H * ta.dv);
 #pragma unroll
@@ -770,7 +828,7 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 template <int DK> struct HeadPlan {
     static constexpr int KQ = DK * 256, E = 3 * Unit<DK>::E_BYTES;
     static constexpr int M_BYTES = 3 * Unit<DK>::MP_BYTES + kC * 4, V_AT = 3 * Unit<DK>::MP_BYTES + 1024, MP = V_AT + kC * 256;   // M P and gamma, values
-    static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + E, OFF_BAR = OFF_MP + 2 * MP, BYTES = OFF_BAR + 256;
+    static constexpr int OFF_E = 2 * KQ, OFF_MP = OFF_E + E, OFF_BAR = OFF_MP + 2 * MP, OFF_BAD = OFF_BAR + 256, BYTES = OFF_BAD + 128 * 4;
     static constexpr int ROWS = 512, LOAD_WARP = 16, MMA_WARP = 17, THREADS = 576;
     static constexpr int COL_D1 = 3 * DK / 2, COL_X = COL_D1, COL_D2 = COL_D1 + 128, COL_D3 = COL_D2 + DK, TMEM_COLS = 512;
     static_assert(COL_D3 + kC <= TMEM_COLS && BYTES <= 227 * 1024 && MP % 1024 == 0, "plan");
@@ -792,7 +850,8 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
              *full_e = empty_m + 2, *empty_e = full_e + 1, *d1 = empty_e + 1, *d2 = d1 + 1, *d3 = d2 + 1, *s_ready = d3 + 1,
              *x_ready = s_ready + 1, *drain = x_ready + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1), *any_bad = abort + 1;
+    int *bad = reinterpret_cast<int *>(smem + P::OFF_BAD);
     pdl_wait();
     pdl_release();
     const AdvanceSeq sq = advance_seq(a, b);
@@ -807,9 +866,11 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const bool expire = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
         for (uint64_t *bar = full_k; bar <= drain; ++bar) mbar_init(bar, bar == s_ready || bar == x_ready ? P::ROWS / 32 : 1);
         *abort = expire;
+        *any_bad = 0;
         if (expire) atomicOr(a.status, kStatusTimeout);
         fence_mbar_init();
     }
+    if (tid < DV) bad[tid] = kNever;
     if (warp == P::LOAD_WARP) tmem_alloc(tmem_slot, P::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -981,11 +1042,29 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 3; ++k) tmem_store8(tm + P::COL_X + 32 * k + 8 * q4, w[k]);
+            // An infinity or NaN, whose second and third terms are NaN, enters the products as 0 (a token before it has a 0 for it there); its row is
+            // NaN from this token on.
+            uint32_t odd = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) odd |= odd_bits(w[2][j]);
+            if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0)) {
+                *any_bad = 1;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if ((w[2][j / 2] >> (j % 2 * 16) & 0x7f80u) == 0x7f80u) {
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) w[k][j / 2] &= j % 2 ? 0xffffu : 0xffff0000u;
+                        atomicMin(bad + row, c * kC + tq + j);
+                    }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) tmem_store8(tm + P::COL_X + 32 * k + 8 * q4, w[k]);
+            }
             tmem_wait_st();
             tc_fence_before();
             arrive(x_ready);
             ok = wait(d2, c & 1) && ok;
             tc_fence_after();
+            const int from = *any_bad ? bad[row] : kNever;            // the first bad token of this row
 #pragma unroll
             for (int j = 0; j < DQ; j += 16) {
                 tmem_load16(tm + P::COL_D2 + DQ * q4 + j, y);
@@ -994,12 +1073,19 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 for (int i = 0; i < 16; i += 2)
                     S[(j + i) / 2] = fma2(make_float2(ge, ge), S[(j + i) / 2], make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
             }
+            if (from != kNever)
+#pragma unroll
+                for (int j = 0; j < DQ / 2; ++j) S[j] = make_float2(__uint_as_float(0x7fffffffu), __uint_as_float(0x7fffffffu));
             put_state();
             arrive(s_ready);
             ok = wait(d3, c & 1) && ok;
             tc_fence_after();
             tmem_load16(tm + P::COL_D3 + tq, z);
             tmem_wait_ld();
+            if (from != kNever)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (c * kC + tq + j >= from) z[j] = 0x7fffffffu;
             if (ok)
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
