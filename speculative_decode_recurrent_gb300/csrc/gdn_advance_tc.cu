@@ -13,11 +13,13 @@
 // E x (and (M P) x beside what follows).  Value columns need nothing of one another: few heads are cut into
 // slices of 32 columns, many are walked whole.
 //
-// Precision.  Outputs and states are fp32 and as exact as the token-by-token kernel's.  Keys and queries are exact in bf16;
-// S, x, E, M P and what these are made of enter as three bf16 terms each (all 24 bits), products of a pair of
-// them as the six of terms whose orders add up to two at most.  (Two terms and three products were 5e-6 off,
-// fifty times an fp32 sum's error, for some 30 % less time.)  The state itself stays in fp32 registers through the walk,
-// the inverse is formed in fp32 by blocks.
+// Precision.  Keys and queries are exact in bf16; S, x, E, M P and what these are made of enter as three bf16 terms each (all 24 bits),
+// products of a pair of them as the six of terms whose orders add up to two at most, the smallest first: additions in the tensor
+// cores do not round to nearest, and few of them act on a full-size sum so (largest first, heads were off by two to three times as
+// much).  Against 64 bits (root mean squares): outputs 3 to 4e-7 and states 1 to 2.5e-7, where a token at a time in fp32 gives 1.1e-7 and
+// 0.6e-7; of decays of 0.999 a token, whose errors add up, 6 to 8e-7 and 4 to 8e-7 against 2 to 3e-6.  (Two terms and three products
+// were 5e-6 off for some 30 % less time.)  The state itself stays in fp32 registers through the walk, the inverse is formed in fp32 by
+// blocks.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -77,8 +79,9 @@ __device__ __forceinline__ void split8(const float *y, uint4 (&t)[3]) {
 #pragma unroll
     for (int k = 0; k < 3; ++k) t[k] = make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
 }
-// The products of two numbers of three terms: (term of A, term of B), the largest first.
-__device__ constexpr int kTermA[6] = {0, 0, 1, 0, 1, 2}, kTermB[6] = {0, 1, 0, 2, 1, 0};
+// The products of two numbers of three terms: (term of A, term of B), the smallest first: an addition to a sum does not round to
+// nearest, so the fewer come once it is large, the better.
+__device__ constexpr int kTermA[6] = {2, 1, 0, 1, 0, 0}, kTermB[6] = {0, 1, 2, 0, 1, 0};
 constexpr int kNever = 0x7fffffff;
 
 // ------------------------------------------------------------- E and M P of every chunk
@@ -936,9 +939,9 @@ advance_head_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 3 * DK / 16; ++k) { // the terms of S
+            for (int k = 0; k < 3 * DK / 16; ++k) { // the terms of S, the smallest first
                 const int ks = k % (DK / 16);
-                mma_bf16_ts_on(one, tm + P::COL_D1, tm + k * 8, desc_add(dKQ, st * P::KQ + (ks >> 2) * 16384 + (ks & 3) * 32), idesc_mn(1, 128, 128), k > 0);
+                mma_bf16_ts_on(one, tm + P::COL_D1, tm + (2 - k / (DK / 16)) * (DK / 2) + ks * 8, desc_add(dKQ, st * P::KQ + (ks >> 2) * 16384 + (ks & 3) * 32), idesc_mn(1, 128, 128), k > 0);
             }
             mma_commit_on(one, d1);
             mma_commit_on(one, &empty_k[st]);
