@@ -162,10 +162,11 @@ int64_t gdn_attn_workspace(const gdn_page_cache *cache, const gdn_attn_dims *dim
  * Rows t >= n get out 0 and lse -inf.  Keys and values of tokens past the chunk's end may hold anything (NaN and
  * infinity included); an infinite or NaN value of a token leaves infinity or NaN in its column of the rows that see it, and
  * nothing in those before it.
- * T is 1..2^20, B * T <= 2^28; chunks of up to 64 tokens are a chain to gdn_attn_verify and go there.
+ * T is 1..2^20, B * T <= 2^28; chunks of up to 64 tokens are a chain to gdn_attn_verify and go there (its weights are two bf16
+ * terms each; here, in bf16, one: at most 2^-8 of a weight off, 2.2e-3 of the outputs where their own rounding is 1.7e-3).
  *   q, out dtype [B, T, Hq, d] (16-byte aligned);  lse fp32 [B, T, Hq] or NULL;  workspace:
  *   workspace_bytes >= gdn_attn_chunk_workspace() bytes, 16-byte aligned, no initial content; calls that
- *   overlap on the GPU need one each.
+ *   overlap on the GPU need one each.  out does not overlap q.
  * GDN_STATUS_* as for gdn_attn_verify.
  */
 int gdn_attn_chunk(const gdn_page_cache *cache, int32_t layer, const gdn_attn_dims *dims,

@@ -31,7 +31,7 @@ extern "C" {
  * and m anew.  When no child is left, the next token is drawn from r: the smallest v with sum_{w <= v} r(w) > u[b][0]
  * sum_w r(w); from p where r has no mass.  draft NULL: a drafter that is certain of each child (q is 1 at it):
  * r loses the rejected tokens, and m is 1 less their p.  The accepted tokens and the next one are then distributed as
- * the target's (the random numbers u uniform in [0, 1)).  Everything is decided in 46 bits or more.
+ * the target's (the random numbers u uniform in [0, 1)).  Terms and sums are held to 2^-46 of the probabilities or better.
  *   tokens   int32 [B, T]     the block's tokens (token 0 is not looked at)
  *   parent   int32 [B, T]     as in gdn_tree_build (gdnattn.h): parent[t] < t; -1 past token 0: never reached;
  *                             NULL: a chain

@@ -208,7 +208,7 @@ int gdn_replay_accept_fold(const gdn_replay_dims *dims, int32_t *buf_len,
  *   q, k  in_dtype [B, T, Hk, dk], v in_dtype [B, T, H, dv]: heads of a token dense, tokens a stride
  *   apart (views of one projection's output), 16-byte aligned;  g, beta fp32 [B, T, H] (g <= 0, as above; -infinity
  *   forgets the state);
- *   out fp32 [B, T, H, dv];  chunk_len int32 [B], NULL: T;  fresh int32 [B], NULL: none;
+ *   out fp32 [B, T, H, dv], overlapping no input;  chunk_len int32 [B], NULL: T;  fresh int32 [B], NULL: none;
  *   workspace: workspace_bytes >= gdn_replay_advance_workspace() bytes, 16-byte aligned, no initial
  *   content; calls that overlap on the GPU need one each.
  * Rows past chunk_len may hold anything. An infinite or NaN input of a token in use goes on into its head's outputs (a value's: into its

@@ -549,7 +549,7 @@ class ConvLayer:
         gdn_conv_accept(self.d, self.t["pos"], self.t["state_idx"], accepted, self.status, stream)
 
     def advance(self, x, y, chunk_len=None, fresh=None, stream=None):
-        """Committed tokens (a prompt, a chunk of one, a single token): x, y [B, T, D]; chunk_len int32 [B]
+        """Committed tokens (a prompt, a chunk of one, a single token): x, y [B, T, D], not overlapping; chunk_len int32 [B]
         tokens in use (None: T); fresh int32 [B], not 0: the sequence starts from a window of zeros."""
         if x.dim() != 3:
             raise ValueError(f"x: expected [B, T, D], got {tuple(x.shape)}")
@@ -814,7 +814,10 @@ class AttnLayer:
     def workspace(self):
         """The layer's workspace; that of a chunk is allocated when it is first needed."""
         if self._to_allocate:
-            self._chunk_workspace()
+            try:
+                self._chunk_workspace()
+            except GdnError:                                     # (dims that stage takes and chunk does not: it has none)
+                pass
         return self._workspace
 
     @workspace.setter
@@ -893,7 +896,8 @@ class AttnLayer:
         """Causal attention of a chunk of new tokens (a prompt, a part of one), staged already: q [B, T, Hq, d]
         over the committed tokens and the chunk's own into ``out`` (and ``lse`` fp32 [B, T, Hq]).  chunk_len
         int32 [B]: tokens in use (None: T, any number that the layer was made for).  seq_len does not move:
-        accept the chunk, or write the new lengths, afterwards."""
+        accept the chunk, or write the new lengths, afterwards.  bf16 chunks of more than 64 tokens round each softmax weight to bf16
+        before the product with the values; up to 64 are a verify, which keeps two terms."""
         if self._chunk_need is None or self._to_allocate or self._ws_bytes < self._chunk_need:
             need = self._chunk_workspace(stream)
             if self._ws_bytes < need:

@@ -57,6 +57,8 @@ struct AdvancePlan {
 // chunk and SM), as does what of a later one's the walk before it leaves no time for, and each launch costs some 12 us (by heads
 // 20: more state comes in and goes out); their number and the first one's size follow from that.  8192 tokens of 16 heads:
 // 224 us in three launches, 252 in one, 250 in six; 8 prompts of 16 heads, whose walk leaves few SMs: 218 in one, 225 in two.
+// These times are of 16 heads of 128 x 128 and stand for the other sizes too.  (With 64 key dims a walk's CTA leaves shared memory for one of the
+// first kernel on its SM, but no TMEM: one of the two then waits for the other's columns, and less runs beside.)
 // Where the workspace holds fewer chunks than a plan wants, its launches are as large as that lets them be (16 prompts of 4096
 // tokens, 16 heads: 966 us in four; in 44, all but the first of one chunk, 1811).
 inline AdvancePlan advance_plan(int B, int T, int H, int dv, int64_t unit, int sms) {

@@ -5,8 +5,8 @@
 //     w = beta (v_i - alpha S_i.k),   S_i <- alpha S_i + w k,   o_i = S_i.(scale q).
 // Eight lanes hold a row in registers, so a token costs a row two dot products over them.  A short call
 // (single tokens without a draft: 16 heads 4 us) is bound by its chain of loads and launch; a long one by that of
-// dependent instructions from token to token, some 360 cycles (fp32 keys and values have no tensor-core product; 333 tokens of
-// 30 heads 64 us.  Four tokens at a time, with their products among themselves made ahead, took 75 where one at a time took 70; the last
+// dependent instructions from token to token, some 360 cycles (fp32 keys and values, whose products would be six of bf16
+// terms in the chunked form, which is not built for them; 333 tokens of 30 heads 64 us, 8192 of 16 heads of 128 x 128 1.75 ms.  Four tokens at a time, with their products among themselves made ahead, took 75 where one at a time took 70; the last
 // output's sum beside the next token's 63, but a sixth longer where heads share the SMs.)
 #include <cuda_bf16.h>
 

@@ -825,7 +825,7 @@ advance_slice_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 // Here the state's columns are the rows (TMEM lanes): S and x are the A operands, straight from TMEM, and keys, queries, E and M P
 // the B operands as they lie.  A head costs an SM 240 KB of shared memory traffic a chunk instead of the 800 KB of
 // four slices, and nothing of S or x goes through it: 6500 cycles a chunk, of which the MMAs are 3900 (8 prompts of 16 heads, up to
-// 32 chunks: 115 us).
+// 32 chunks: 118 us).
 //
 // TMEM columns: S (three terms, dk / 2 each), [K;Q] S^T and over it x (three terms of 32), E x, M P x.
 template <int DK> struct HeadPlan {

@@ -1,6 +1,6 @@
 // gdn_attn_chunk.cu -- attention of a chunk of new tokens over the paged cache, for sm_103a: the C ABI entry
-// points (include/gdnattn.h), the kernel on the CUDA cores (fp32 caches: there is no fp32 tensor-core
-// product) and the join of its split keys.  bf16 caches take gdn_attn_chunk_tc.cu.
+// points (include/gdnattn.h), the kernel on the CUDA cores (fp32 caches: the tensor cores have no fp32 product, and fp32 out
+// of products of bf16 terms, six for each, is not built) and the join of its split keys.  bf16 caches take gdn_attn_chunk_tc.cu.
 //
 // Mathematics.  One pass over a row's keys with the running maximum m and sum l of its softmax in powers
 // of two: for each tile of keys m' = max(m, max s), o <- 2^(m - m') o + sum_j 2^(s_j - m') v_j, l likewise; out = o / l,
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkArgs a)
 int core_tokens(const gdn_page_cache *c, const gdn_attn_dims *d) { return kRT / (d->Hq / c->Hkv); }
 int core_tiles(const gdn_page_cache *c, const gdn_attn_dims *d) { return (d->T + core_tokens(c, d) - 1) / core_tokens(c, d); }
 // Parts of the key axis: four CTAs for each SM, as far as one row tile has keys for them: 256 tokens after 20000
-// (16 and 2 heads of 128) 1459 us, with two CTAs for each 1705, with one 1892; 3 of 150 after 400 (12 and 3 of 64) 35, 35, 49.
+// (16 and 2 heads of 128) 1470 us, with two CTAs for each 1705, with one 1892; 3 of 150 after 400 (12 and 3 of 64) 35, 35, 49.
 int core_splits(const gdn_page_cache *c, const gdn_attn_dims *d) {
     const long long units = static_cast<long long>(d->B) * c->Hkv * core_tiles(c, d), want = 4 * sm_count();
     const long long most = (static_cast<long long>(c->max_pages) * c->page + 4 * kKT - 1) / (4 * kKT);

@@ -11,8 +11,9 @@
 // 64 keys 47 instead of 32).  A CTA has two tiles of 128 rows (row r = t G + g: tokens times the query heads of a key
 // head) whose softmaxes and products overlap.  Tiles of 128 keys leave TMEM for one score buffer of each row tile, so a
 // tile's softmax, its weights' product and the next scores follow one another: a pair's tiles take some 2500 cycles, their MMAs
-// 2000.  (Tiles of 64 keys in two buffers: 2 x 1770.)  4 sequences of 4096 tokens after 16384: 1.5 ms, 1640 TFLOP/s; 4 prompts of up
-// to 4096 tokens 168 us; 256 tokens after 60001 (16 query heads, 2 key heads of 128) 98 us.
+// 2000.  (Tiles of 64 keys in two buffers: 2 x 1770.)  4 sequences of 4096 tokens after 16384: 1.46 ms, 1690 TFLOP/s; 4 prompts of up
+// to 4096 tokens 171 us; 256 tokens after 60001 (16 query heads, 2 key heads of 128) 97 us.  Head dims of 64: 133 and 77 us (0.43 of the
+// peak: half the products a score, for the same softmax), of 256: 459 and 268 us (0.5: scores formed twice, once for each half of the values).
 //
 // Roles.  Two groups of 256 threads, two per row (each half of a tile's keys; the scores of a row are in registers), and
 // for each group a warp that issues: O += P_i V_i, then the scores of the next tile into the buffer that held P_i (the weights
@@ -24,7 +25,7 @@
 // Work.  A unit is (pair of row tiles, key head, sequence, part of the keys); the longest come first.  A CTA takes over the
 // units of CTAs of the grid that have not begun (cluster launch control), so that a unit's keys, values and queries are loaded and
 // its first scores formed while the rows of the one before are scaled and written: with a CTA for each unit its beginning and
-// end cost 8 us each time (64 prompts of 256 tokens 73 us, now 46; 4 of 4096 211, now 187).  Keys are cut
+// end cost 8 us each time (64 prompts of 256 tokens 73 us, without 46, which is 49 with the look at the values; 4 of 4096 211 and 187).  Keys are cut
 // into parts where the pairs alone would leave SMs without work (best_splits), joined by chunk_tc_join_kernel.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -770,7 +771,9 @@ long long units(const gdn_page_cache *c, const gdn_attn_dims *d) {
 // Parts of the key axis, at least 512 keys each, as far as a sequence can be long: the fewest tiles' times (of 128 keys, about
 // 2400 cycles) until the last CTA is through.  A unit costs 2.5 of them beside its own tiles, a part's way through memory and the
 // join 0.064 (divided among the SMs already) and the join's launch 3.  Units of nearly one length come in waves; those of a prompt,
-// whose length falls from the longest to nothing, fill the SMs, with half a unit at the end.
+// whose length falls from the longest to nothing, fill the SMs, with half a unit at the end.  The lengths are on the device: the cache's
+// capacity stands for them here, so where sequences are far shorter there are parts without keys, which cost their CTA a unit's
+// 2.5 tiles and the join its loads.  The figures are of head dims of 128.
 int best_splits(const gdn_page_cache *c, const gdn_attn_dims *d) {
     const long long sms = sm_count(), u = units(c, d);
     if (sms < 1 || u >= 4 * sms) return 1;

@@ -9,8 +9,8 @@
 //
 // Precision.  The next token is where a running sum of up to 2^24 terms passes a threshold: in 32 bits the
 // sums of 10^5 terms are off by more than many a term.  A term is p - c q in two fp32 words (exact for c = 1), and sums,
-// masses and thresholds are two words throughout (46 bits and more), so a token differs from the 64-bit one's
-// only where the threshold lies within some 2^-44 of a border.  Two words, because fp64 is slow on this chip: with 64-bit
+// masses and thresholds are two words throughout (46 bits and more of p), so a token differs from the 64-bit one's
+// only where the threshold lies within some 2^-44 of a border (where rejections leave little of p, as much more of that rest).  Two words, because fp64 is slow on this chip: with 64-bit
 // sums above the lanes' the search alone took 12 us, a whole call over 32768 probabilities 23.
 //
 // What bounds it: a few rows of V numbers per sequence, and a chain of dependent steps (tokens, their probabilities,
