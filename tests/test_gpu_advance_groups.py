@@ -1,5 +1,5 @@
-"""gdn_replay_advance where its workspace holds only some of the sequences or of their chunks at a time: groups of
-sequences, launches that the workspace cuts short, and both; tokens in every launch."""
+"""gdn_replay_advance in more than one launch: where its workspace holds only some of the sequences or of their chunks at a time (groups of
+sequences, launches cut short, both), and where the chunks' operators are made beside the walk; tokens in every launch."""
 import numpy as np
 import pytest
 import torch
@@ -43,8 +43,11 @@ def reference(S, q, k, v, g, beta, lens, scale):
     return out, S, max(norm.sqrt().item(), v[live].abs().max().item()), eff
 
 
-# (what the shape is there for: groups of sequences, launches cut short)
+# (what the shape is there for: groups of sequences, launches cut short; neither: several launches beside one another)
 @pytest.mark.parametrize("B,T,H,Hk,dk,dv,groups,cut", [
+    (1, 8192, 16, 16, 128, 128, False, False),       # three launches, the last by slices of 16
+    (1, 1500, 30, 15, 64, 64, False, False),
+    (2, 1500, 16, 16, 128, 64, False, False),
     (90, 70, 64, 16, 128, 128, True, True),          # heads walked whole, a last group of six sequences, a chunk a launch
     (360, 64, 16, 16, 128, 128, True, False),        # a group of 338 and one of 22
     (350, 60, 32, 32, 64, 64, True, False),          # slices
@@ -52,10 +55,10 @@ def reference(S, q, k, v, g, beta, lens, scale):
     (3, 3000, 96, 96, 128, 64, False, True),         # by slices, three launches over two workspaces
     (4, 900, 160, 160, 64, 128, False, True),
 ])
-def test_advance_beyond_a_workspace(B, T, H, Hk, dk, dv, groups, cut):
+def test_advance_in_more_than_one_launch(B, T, H, Hk, dk, dv, groups, cut):
     import speculative_decode_recurrent_gb300 as lib
     p = plan(B, T, H, dk, dv, torch.cuda.get_device_properties(0).multi_processor_count)
-    assert (p["seqs"] < B) == groups and (len(p["sizes"]) > 1 and p["most"] < p["all"]) == cut, p
+    assert (p["seqs"] < B) == groups and (p["most"] < p["all"]) == cut and (groups or len(p["sizes"]) > 1), p
     gen = torch.Generator(device="cuda").manual_seed(B + T)
     unit = torch.nn.functional.normalize
 
@@ -104,3 +107,27 @@ def test_advance_beyond_a_workspace(B, T, H, Hk, dk, dv, groups, cut):
         assert (out[b, m:] == 0).all(), (b, m)
     left = [s for s in range(B + 1) if s not in set(slots.tolist())]
     assert torch.equal(layer.t["state"][left], state[left])
+
+
+def test_calls_of_several_launches_on_two_streams_at_once():
+    """Each with its own workspace: the bits of one after the other."""
+    from test_gpu_advance import Case
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    cases = [Case([4096], 4096, 16, 16, 128, 128, BF, seed=91), Case([1500], 1500, 30, 30, 64, 64, BF, seed=92)]
+    assert all(len(plan(1, c.T, c.H, c.dk, c.dv, sms)["sizes"]) > 1 for c in cases)
+    ws = [c.layer.advance_workspace(c.T, c.Hk) for c in cases]
+    lens, start, streams, want = [i32(c.lens) for c in cases], [c.state.cuda() for c in cases], [torch.cuda.Stream() for _ in cases], []
+    for c, w in zip(cases, ws):
+        c.run(workspace=w)
+        torch.cuda.synchronize()
+        want.append((c.out.clone(), c.layer.t["state"].clone()))
+    for _ in range(5):
+        for c, s in zip(cases, start):
+            c.layer.t["state"].copy_(s)
+            c.out.fill_(3)
+        torch.cuda.synchronize()
+        for c, w, n, stream in zip(cases, ws, lens, streams):
+            c.layer.advance(c.q, c.k, c.v, c.g, c.beta, c.out, chunk_len=n, workspace=w, stream=stream)
+        torch.cuda.synchronize()
+        for c, (out, state) in zip(cases, want):
+            assert torch.equal(c.out, out) and torch.equal(c.layer.t["state"], state) and int(c.layer.status.item()) == 0

@@ -3,6 +3,7 @@ other column keeps its bits; what the recurrence takes them into is not finite."
 import pytest
 import torch
 
+from advance_plan import plan
 from test_gpu_advance import BF, F32, Case
 
 pytestmark = pytest.mark.gpu
@@ -21,7 +22,7 @@ SHAPES = {
     "slices of 64 rows": ([150] * 9, 150, 5, 5, 64, 64, BF),
     "heads": ([200, 150] * 5, 200, 8, 4, 128, 128, BF),
     "heads of 64 key dims": ([140] * 20, 140, 4, 4, 64, 128, BF),
-    "several launches": ([2100], 2100, 3, 3, 128, 128, BF),
+    "two launches": ([1500], 1500, 30, 30, 64, 64, BF),
     "token by token": ([19, 17], 19, 4, 2, 128, 64, BF),
     "fp32": ([90, 75], 90, 3, 3, 64, 64, F32),
 }
@@ -31,6 +32,8 @@ SHAPES = {
 @pytest.mark.parametrize("name", SHAPES)
 def test_bad_inputs_go_forward_alone(name, at):
     lens, T, H, Hk, dk, dv, dtype = SHAPES[name]
+    if name == "two launches":
+        assert len(plan(1, T, H, dk, dv, torch.cuda.get_device_properties(0).multi_processor_count)["sizes"]) == 2
     c = Case(lens, T, H, Hk, dk, dv, dtype, seed=31)
     c.run()
     torch.cuda.synchronize()

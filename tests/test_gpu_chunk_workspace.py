@@ -75,3 +75,4 @@ def test_a_layer_of_dims_that_chunk_refuses_still_stages():
     many = lib.AttnLayer(lib.AttnDims(B=300, T=1 << 20, Hq=4, scale=c.scale), c.cache, 0)
     with pytest.raises(lib.GdnError):
         many.chunk(c.qd, c.out)
+    assert many.workspace.numel() == 0
