@@ -71,6 +71,8 @@ typedef struct {
     int32_t *block_table, *seq_len, *n_owned, *ref, *free_list, *free_count;
 } gdn_page_cache;
 
+#define GDN_FLAG_TWO_TERMS 4  /* gdn_attn_chunk in bf16: softmax weights in two bf16 terms (see there) */
+
 /* One block of drafted tokens.  Row t of sequence b is in use when t < draft_len[b]
  * (draft_len NULL: every row). */
 typedef struct {
@@ -80,7 +82,7 @@ typedef struct {
     int32_t Hq;         /* query heads, a multiple of Hkv, Hq / Hkv <= 64; head h reads key head
                            h / (Hq / Hkv) */
     float   scale;      /* score scale, normally 1/sqrt(d) */
-    int32_t flags;      /* GDN_FLAG_TEST_EXPIRE or 0 */
+    int32_t flags;      /* GDN_FLAG_TEST_EXPIRE, GDN_FLAG_TWO_TERMS or 0 */
 } gdn_attn_dims;
 
 #define GDN_ROPE_HALF  0    /* pairs (i, i + rot/2) */
@@ -162,8 +164,9 @@ int64_t gdn_attn_workspace(const gdn_page_cache *cache, const gdn_attn_dims *dim
  * Rows t >= n get out 0 and lse -inf.  Keys and values of tokens past the chunk's end may hold anything (NaN and
  * infinity included); an infinite or NaN value of a token leaves infinity or NaN in its column of the rows that see it, and
  * nothing in those before it.
- * T is 1..2^20, B * T <= 2^28; chunks of up to 64 tokens are a chain to gdn_attn_verify and go there (its weights are two bf16
- * terms each; here, in bf16, one: at most 2^-8 of a weight off, 2.2e-3 of the outputs where their own rounding is 1.7e-3).
+ * T is 1..2^20, B * T <= 2^28; chunks of up to 64 tokens are a chain to gdn_attn_verify and go there.  Its weights enter the product
+ * with bf16 values as two bf16 terms each.  Here that takes GDN_FLAG_TWO_TERMS; without it they are one, at most 2^-8 of a weight off
+ * (2.2e-3 of the outputs, where their own rounding is 1.7e-3), in three quarters of the time.
  *   q, out dtype [B, T, Hq, d] (16-byte aligned);  lse fp32 [B, T, Hq] or NULL;  workspace:
  *   workspace_bytes >= gdn_attn_chunk_workspace() bytes, 16-byte aligned, no initial content; calls that
  *   overlap on the GPU need one each.  out does not overlap q.

@@ -20,7 +20,7 @@ __all__ = ["Dims", "GdnError", "load", "gdn_replay_verify", "gdn_replay_accept",
            "gdn_replay_flush", "gdn_replay_verify_fold", "gdn_replay_accept_fold",
            "gdn_replay_kernel_family", "gdn_replay_strerror", "STATUS_BAD_ACCEPT",
            "STATUS_NO_ROOM", "STATUS_BAD_LEN", "STATUS_BAD_SLOT", "STATUS_TIMEOUT",
-           "STATUS_DRAIN", "FLAG_TEST_EXPIRE", "FAMILY_TCGEN05", "FAMILY_PERTOKEN", "DTYPE_BF16",
+           "STATUS_DRAIN", "FLAG_TEST_EXPIRE", "FLAG_TWO_TERMS", "FAMILY_TCGEN05", "FAMILY_PERTOKEN", "DTYPE_BF16",
            "DTYPE_F32", "ReplayLayer", "ConvDims", "gdn_conv_verify", "gdn_conv_accept",
            "gdn_gated_rmsnorm_fp8", "ConvLayer", "CONV_ACT_NONE", "CONV_ACT_SILU",
            "gdn_nonreplay_verify", "gdn_nonreplay_accept", "NonReplayLayer",
@@ -35,6 +35,7 @@ STATUS_DRAIN = 32
 STATUS_BAD_PAGE, STATUS_BAD_POS, STATUS_BAD_TREE, STATUS_NO_PAGES = 64, 128, 256, 512
 STATUS_BAD_TOKEN, STATUS_BAD_PROB = 1024, 2048
 FLAG_TEST_EXPIRE = 1
+FLAG_TWO_TERMS = 4                   # AttnDims: AttnLayer.chunk in bf16 keeps two terms of a softmax weight
 FAMILY_TCGEN05, FAMILY_PERTOKEN = 1, 2
 FAMILY_NAMES = {FAMILY_TCGEN05: "tcgen05", FAMILY_PERTOKEN: "per-token"}
 CONV_ACT_NONE, CONV_ACT_SILU = 0, 1
@@ -897,7 +898,7 @@ class AttnLayer:
         over the committed tokens and the chunk's own into ``out`` (and ``lse`` fp32 [B, T, Hq]).  chunk_len
         int32 [B]: tokens in use (None: T, any number that the layer was made for).  seq_len does not move:
         accept the chunk, or write the new lengths, afterwards.  bf16 chunks of more than 64 tokens round each softmax weight to bf16
-        before the product with the values; up to 64 are a verify, which keeps two terms."""
+        before the product with the values, unless the layer's dims have FLAG_TWO_TERMS; up to 64 are a verify, which keeps two terms."""
         if self._chunk_need is None or self._to_allocate or self._ws_bytes < self._chunk_need:
             need = self._chunk_workspace(stream)
             if self._ws_bytes < need:

@@ -93,7 +93,7 @@ inline int check_cache(const gdn_page_cache *c) {
 inline int check_attn(const gdn_page_cache *c, const gdn_attn_dims *a, int max_T) {
     if (const int rc = check_cache(c)) return rc;
     if (!a) return GDN_ERR_NULL;
-    if (a->B < 0 || a->B > 65535 || a->T < 1 || a->T > max_T || (a->flags & ~GDN_FLAG_TEST_EXPIRE)) return GDN_ERR_DIMS;
+    if (a->B < 0 || a->B > 65535 || a->T < 1 || a->T > max_T || (a->flags & ~(GDN_FLAG_TEST_EXPIRE | GDN_FLAG_TWO_TERMS))) return GDN_ERR_DIMS;
     if (static_cast<long long>(a->B) * a->T > (1ll << 30)) return GDN_ERR_DIMS;
     if (a->Hq < 1 || a->Hq % c->Hkv != 0 || a->Hq / c->Hkv > 64) return GDN_ERR_DIMS;
     if (!(a->scale > 0.f) || !(a->scale < 1e30f)) return GDN_ERR_DIMS;

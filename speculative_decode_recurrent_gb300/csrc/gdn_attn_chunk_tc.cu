@@ -4,8 +4,10 @@
 // Mathematics.  As in gdn_attn_chunk.cu, with a reference m in the maximum's place: it is raised (o and l rescaled)
 // only when a tile's maximum exceeds it by more than 8 in powers of two, so weights stay below 2^8 and most tiles
 // rescale nothing.  Weights enter the second product as one bf16 term: each is off by 2^-8 of itself at most, unbiased,
-// which over a row's keys adds about as much as rounding the output does (two terms, as the verify of drafts takes
-// them, would make the second product, half of all the work here, twice as long).  l is the sum of the weights in fp32.
+// which over a row's keys adds about as much as rounding the output does: 2.1e-3 to 2.3e-3 of the outputs, of which their own rounding is 1.7e-3.
+// With GDN_FLAG_TWO_TERMS it is two terms (2^-17), as in the verify of drafts, and what is left is the outputs' rounding; the second
+// product, half of all the work here, is then twice as long (prompts 215 us on the device instead of 161, 256 tokens after 60001 122
+// instead of 93, 64 prompts of 256 tokens 60 instead of 49).  l is the sum of the weights in fp32.
 //
 // What bounds it: the MMAs, and shared memory with them (an MMA of 128 rows by 128 keys takes 63 cycles with 64 of reads, one of
 // 64 keys 47 instead of 32).  A CTA has two tiles of 128 rows (row r = t G + g: tokens times the query heads of a key
@@ -133,7 +135,7 @@ __device__ __forceinline__ int read_next(uint32_t at) {
     return x;
 }
 
-template <int D>
+template <int D, bool TWO>                          // TWO: weights in two bf16 terms
 __global__ void __launch_bounds__(Plan<D>::THREADS, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkArgs a)
@@ -418,14 +420,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (!ok) break;
                 tc_fence_after();
                 if (i < n) {
-                    const uint32_t t_p = t_s + at % P::NB * KT;       // O += P_i V_i
+                    const uint32_t t_p = t_s + at % P::NB * KT;       // O += P_i V_i, the second terms (KT / 2 columns on) first
                     if (P::NB > 1 || keys >= (i + 1) * KT) {
 #pragma unroll
-                        for (int k = 0; k < KT / 16; ++k) mma_bf16_ts_on(one, t_o, t_p + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+                        for (int k = TWO ? -KT / 16 : 0; k < KT / 16; ++k) {
+                            const int at_k = k & (KT / 16 - 1);
+                            mma_bf16_ts_on(one, t_o, t_p + (k < 0 ? KT / 2 : 0) + at_k * 8, desc_add(vd, at_k * 2048), idO, i > 0 || k != (TWO ? -KT / 16 : 0));
+                        }
                     } else {                        // no further than the group's last row sees
                         const int some = __shfl_sync(0xffffffffu, (keys - i * KT + 15) / 16, 0);
 #pragma unroll 1
-                        for (int k = 0; k < some; ++k) mma_bf16_ts_on(one, t_o, t_p + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+                        for (int k = 0; k < some; ++k) {
+                            if (TWO) mma_bf16_ts_on(one, t_o, t_p + KT / 2 + k * 8, desc_add(vd, k * 2048), idO, i > 0 || k > 0);
+                            mma_bf16_ts_on(one, t_o, t_p + k * 8, desc_add(vd, k * 2048), idO, TWO || i > 0 || k > 0);
+                        }
                     }
                 }
                 if (i < n) {
@@ -568,6 +576,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
             for (int c = 0; c < KH / 32; ++c) {
                 uint32_t p[16];
+                [[maybe_unused]] uint32_t rest[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     float2 e = fma2(make_float2(__uint_as_float(x[c][2 * k]), __uint_as_float(x[c][2 * k + 1])), sc, mm);
@@ -575,8 +584,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     sum[k & 1] = add2(sum[k & 1], e);
                     const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
                     p[k] = *reinterpret_cast<const uint32_t *>(&w);
+                    if constexpr (TWO) {
+                        const float2 r = fma2(make_float2(__uint_as_float(p[k] << 16), __uint_as_float(p[k] & 0xffff0000u)), make_float2(-1.f, -1.f), e);
+                        const __nv_bfloat162 second = __floats2bfloat162_rn(r.x, r.y);
+                        rest[k] = *reinterpret_cast<const uint32_t *>(&second);
+                    }
                 }
                 tmem_st16(t_s + kh * (KH / 2) + 16 * c, p);
+                if constexpr (TWO) tmem_st16(t_s + KT / 2 + kh * (KH / 2) + 16 * c, rest);
             }
             l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
             if constexpr (LATE) clean(edge, at);
@@ -794,19 +809,20 @@ int best_splits(const gdn_page_cache *c, const gdn_attn_dims *d) {
     return best;
 }
 
-template <int D>
+template <int D, bool TWO>
 int launch(const gdn_page_cache *c, const gdn_attn_dims *d, ChunkArgs a, cudaStream_t s) {
     using P = Plan<D>;
+    constexpr auto kern = chunk_tc_kernel<D, TWO>;
     a.tpt = tile_tokens(c, d);
     a.row_tiles = row_tiles(c, d);
     a.splits = best_splits(c, d);
     CUtensorMap mq, mk, mv;
     if (!query_map(&mq, a.q, c, d, a.tpt) || !rows_map(&mk, a.k, c, P::KT) || !rows_map(&mv, a.v, c, P::KT)) return GDN_ERR_LAUNCH;
-    if (cudaFuncSetAttribute(chunk_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES) != cudaSuccess)
         return GDN_ERR_LAUNCH;
     const long long grid = units(c, d) * a.splits;
     if (grid > 0x7fffffffLL) return GDN_ERR_DIMS;
-    if (launch_pdl(chunk_tc_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(P::THREADS), P::BYTES, s, mq, mk, mv, a) != cudaSuccess)
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(P::THREADS), P::BYTES, s, mq, mk, mv, a) != cudaSuccess)
         return GDN_ERR_LAUNCH;
     if (a.splits > 1 && launch_pdl(chunk_tc_join_kernel<D>, dim3(static_cast<unsigned>(a.row_tiles) * (kRows / 32), c->Hkv, d->B), dim3(D * 4), 0, s,
                                    a) != cudaSuccess)
@@ -822,7 +838,9 @@ int64_t chunk_tc_workspace(const gdn_page_cache *c, const gdn_attn_dims *d) {
 }
 
 int chunk_tc(const gdn_page_cache *c, const gdn_attn_dims *d, ChunkArgs a, cudaStream_t s) {
-    return c->d == 64 ? launch<64>(c, d, a, s) : c->d == 128 ? launch<128>(c, d, a, s) : launch<256>(c, d, a, s);
+    if (d->flags & GDN_FLAG_TWO_TERMS)
+        return c->d == 64 ? launch<64, true>(c, d, a, s) : c->d == 128 ? launch<128, true>(c, d, a, s) : launch<256, true>(c, d, a, s);
+    return c->d == 64 ? launch<64, false>(c, d, a, s) : c->d == 128 ? launch<128, false>(c, d, a, s) : launch<256, false>(c, d, a, s);
 }
 
 }  // namespace gdn

@@ -16,7 +16,16 @@ def _gpu(cuda_ok):
 
 
 class Odd(Case):
-    """``values``: (sequence, token of the whole context, key head, column, number); ``keys``: (sequence, token, key head)."""
+    """(``flags``: of the layer's dims.)  ``values``: (sequence, token of the whole context, key head, column, number); ``keys``: (sequence, token, key head)."""
+
+    def __init__(self, *a, flags=0, **kw):
+        import speculative_decode_recurrent_gb300 as lib
+        super().__init__(*a, **kw)
+        self.one_term = self.c.dtype == BF and not flags
+        if flags:
+            d = self.layer.d
+            self.layer = lib.AttnLayer(lib.AttnDims(B=d.B, T=d.T, Hq=d.Hq, scale=d.scale, flags=flags), self.cache, self.c.layers - 1,
+                                       state_idx=self.layer.state_idx)
 
     def spoil(self, values, keys=()):
         c = self.c
@@ -47,7 +56,7 @@ class Odd(Case):
                     nan_from[h] = min(nan_from[h], t)
                     k[t, h] = 0.0
             ref, _, A, S = reference(R.f64(self.q[b, :n]), k, v, past, self.scale)
-            tol = attn_bounds.verify_bounds(ref, A, S, m, c.d, bf) + (1.01 * 2.0 ** -8 * A if bf else 0)
+            tol = attn_bounds.verify_bounds(ref, A, S, m, c.d, bf) + (1.01 * 2.0 ** -8 * A if self.one_term else 0)
             seen = np.cumsum(self.odd[b], 0)[past:] > 0       # [n, Hkv, d]
             seen = seen | (np.arange(past, m)[:, None] >= nan_from)[:, :, None]
             seen = np.repeat(seen, G, 1)
@@ -69,10 +78,10 @@ SHAPES = [
 ]
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dtype,flags", [(BF, 0), (F32, 0), (BF, 4)])          # (4: FLAG_TWO_TERMS)
 @pytest.mark.parametrize("i", range(len(SHAPES)))
-def test_values_reach_the_rows_that_see_them(i, dtype):
-    c = Odd(*SHAPES[i], dtype, seed=71)
+def test_values_reach_the_rows_that_see_them(i, dtype, flags):
+    c = Odd(*SHAPES[i], dtype, seed=71, flags=flags)
     d, Hkv, inf, values = c.c.d, c.c.Hkv, float("inf"), []
     for b, n in enumerate(c.lens):
         at = sorted({n - 1, n // 2, n // 3, min(n - 1, 1), min(n - 1, 15), min(n - 1, 16), min(n - 1, 47), min(n - 1, 64), 3 * n // 4})
