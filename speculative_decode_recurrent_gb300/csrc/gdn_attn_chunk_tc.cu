@@ -101,10 +101,18 @@ __device__ __noinline__ void spoil_sums(const ChunkArgs &a, int slot, int h, int
         const int id = __ldg(tab + (j >> a.s.page_shift));
         if (id < 0 || id >= a.s.n_page) continue;
         const size_t row = ((static_cast<size_t>(id) * a.s.Hkv + h) << a.s.page_shift) + (j & ((1 << a.s.page_shift) - 1));
-        const uint32_t *v = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.v) + row * d + c0);
-        for (int c = 0; c < N / 2; ++c) {
-            const uint32_t m = odd_halves(__ldg(v + c));
-            odd |= static_cast<unsigned long long>((m & 1u) | (m >> 30 & 2u)) << 2 * c;
+        const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) + row * d + c0);
+#pragma unroll 4
+        for (int c = 0; c < N / 8; ++c) {
+            const uint4 x = __ldg(v + c);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t y = odd_halves(w[k]);
+                m |= ((y & 1u) | (y >> 30 & 2u)) << 2 * k;
+            }
+            odd |= static_cast<unsigned long long>(m) << 8 * c;
         }
     }
     for (int c = 0; c < N; c += 8) {
@@ -151,7 +159,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
              *u_full = drain + 2, *u_empty = u_full + 2, *asked_next = u_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + P::OFF_SLOT);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile int *odd_values = abort + 1;           // infinities or NaN have been zeroed among the values
+    volatile int *odd_values = abort + 1;           // [2]: the last unit in the slot (its number plus 1) of whose values infinities or NaN have been zeroed
     Unit *units = reinterpret_cast<Unit *>(smem + P::OFF_UNIT);
     static_assert((2 * P::NK + 2 * P::NV + 25) * 8 <= 352, "barriers");
     if (saddr(smem) & 1023u) {
@@ -184,7 +192,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
         mbar_init(asked_next, 1);
         *abort = (a.flags & GDN_FLAG_TEST_EXPIRE) != 0;
-        *odd_values = 0;
+        odd_values[0] = odd_values[1] = 0;
         fence_mbar_init();
     }
     if (warp == P::MMA_WARP) tmem_alloc(tmem_slot, 512);
@@ -509,7 +517,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     const uint32_t odd = (odd_bits(y[0].x) | odd_bits(y[0].y) | odd_bits(y[0].z) | odd_bits(y[0].w) | odd_bits(y[1].x) |
                                           odd_bits(y[1].y) | odd_bits(y[1].z) | odd_bits(y[1].w)) & 0x80008000u;
                     if (past || odd) {
-                        if (odd) *odd_values = 1;
+                        if (odd) odd_values[u & 1] = u + 1;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             *at_v[k] = make_uint4(y[k].x & ~odd_halves(y[k].x), y[k].y & ~odd_halves(y[k].y), y[k].z & ~odd_halves(y[k].z),
@@ -608,7 +616,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (n > 0) {                                // (by a barrier of its own: o_done may be a phase or two behind)
             ok = wait(&o_last[g], w.sums[g] & 1) && ok;
             tc_fence_after();
-            if (__any_sync(0xffffffffu, *odd_values) && ok)
+            if (__any_sync(0xffffffffu, odd_values[u & 1] == u + 1) && ok)
                 spoil_sums<DH>(a, w.slot, w.h, w.half * DV + kh * DH, D, max(w.first * KT, w.len + w.rt0 * a.tpt + 1),
                                r < w.live[g] ? min((w.first + n) * KT, w.len + (w.rt0 + g) * a.tpt + r / G + 1) : 0, t_o);
         }
